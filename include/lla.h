@@ -306,6 +306,98 @@ int lla_gdn_forward_profile(const void* q, const void* k, const void* v, const f
                             void* stream, int dtype, float* kernel_ms, const char** kernel_names, int cap);
 
 /*
+ * Linear attention with one decay per head: the recurrence that the Fenwick hierarchy of
+ * lla_forward is laid over, with one state and one constant decay for each head ("Log-Linear
+ * Attention", pt section 2 / fr section 2 take gated linear attention as the base of the hierarchy):
+ *
+ *     S_t = g_h S_{t-1} + k_t v_t^T,   o_t = S_t^T q_t,   g_h = exp(log_a_h),
+ *
+ * i.e. o_t = sum_{s<=t} g^(t-s) (q_t . k_s) v_s + g^(t+1) S_{-1}^T q_t. No scale, no normalisation.
+ * With lambda = 1 at every level and log_a the same at every token, lla_forward computes the same.
+ *
+ *   log_a     [H]            fp32   log of each head's decay (<= 0 expected; -inf, a decay of 0, is
+ *                                   valid; positive values are computed as given). A constant of the
+ *                                   model: lla_linear_backward forms no gradient of it (for learned or
+ *                                   per-token decays see lla_backward).
+ *   state0    [B0,H,dk,dv]   fp32   S_{-1}, the state that the sequences go on from: B0 = 0 (state0
+ *                                   NULL: zeros), 1 (one state for the whole batch, e.g. of a common
+ *                                   prefix that was computed once) or B (one each).
+ *   state_out [B,H,dk,dv]    fp32   written: S_{T-1}. NULL: not wanted. Must not overlap state0.
+ *   q, k [B,H,T,dk], v, out [B,H,T,dv]  dtype, as lla_forward; any T >= 1 (no chunk argument).
+ *   dk, dv 1..128. bf16 with dk and dv multiples of 8 runs on tensor cores (128-token chunks, bf16
+ *   operands, fp32 accumulation, states in fp32); every other shape runs fp32 arithmetic on CUDA
+ *   cores. Sums are formed in a fixed order: repeated calls give identical bits.
+ * Tokens are mixed in chunks of 128 (64 on CUDA cores), so an infinity or NaN in v may reach the
+ * other rows of its own chunk, as well as every later row; one in k or q obeys causality. Rows of
+ * other sequences (and, packed, rows of no sequence) are never mixed in.
+ *
+ * lla_linear_forward: prompts of one length.
+ *
+ * lla_linear_forward_varlen: packed sequences, layout and cu_seqlens rules as lla_forward_varlen:
+ *   q, k [H,total_T,dk]; v, out [H,total_T,dv]; state0 [n0,H,dk,dv], n0 in {0, 1, n_seq};
+ *   state_out [n_seq,H,dk,dv]. A sequence may be empty: its state_out is its state0 (or zeros).
+ *   Rows of out that belong to no sequence are left as they were. A sequence whose bounds break the
+ *   rules (cu_seqlens not rising, rows past total_T, more than max_T of them) is skipped, its rows and
+ *   state_out left as they were, and lla_device_error reports LLA_ERR_DEVICE.
+ *
+ * lla_linear_backward: gradients of sum(dout . out) + sum(dstate_out . state_out).
+ *   dout       [B,H,T,dv]   dtype   upstream gradient of out
+ *   dstate_out [B,H,dk,dv]  fp32    upstream gradient of state_out; NULL: zeros
+ *   dq, dk [B,H,T,dk], dv [B,H,T,dv]  dtype, written
+ *   dstate0    [B0,H,dk,dv] fp32    written (B0 = 1: summed over the batch in order); NULL: not wanted
+ *   The outputs must not overlap any input or each other. Nothing of the forward is kept: its states
+ *   are formed again from k, v and state0.
+ *
+ * lla_linear_decode_step: one token of every sequence; state [B,H,dk,dv] fp32 is read and written in
+ *   place (S_{t-1} on entry, S_t on return; what lla_linear_forward leaves in state_out). q, k
+ *   [B,H,dk], v, out [B,H,dv] dtype.
+ *
+ * Workspace comes from the library's stream-ordered pool. Errors: LLA_ERR_INVALID_ARG /
+ * LLA_ERR_UNSUPPORTED before any launch, LLA_ERR_NOMEM if the pool cannot grow, LLA_ERR_CUDA on a
+ * launch failure; a bounded wait that runs out is reported by lla_device_error as LLA_ERR_TIMEOUT.
+ */
+int lla_linear_forward(const void* q, const void* k, const void* v, const float* log_a, const float* state0, void* out,
+                       float* state_out, int B, int B0, int H, int T, int dk, int dv, void* stream, int dtype);
+int lla_linear_forward_varlen(const void* q, const void* k, const void* v, const float* log_a, const float* state0,
+                              void* out, float* state_out, const int32_t* cu_seqlens, int n_seq, int n0, int H,
+                              int total_T, int max_T, int dk, int dv, void* stream, int dtype);
+int lla_linear_backward(const void* q, const void* k, const void* v, const float* log_a, const float* state0,
+                        const void* dout, const float* dstate_out, void* dq, void* dk, void* dv, float* dstate0, int B,
+                        int B0, int H, int T, int dk_, int dv_, void* stream, int dtype);
+int lla_linear_decode_step(const void* q, const void* k, const void* v, const float* log_a, float* state, void* out,
+                           void* stream, int B, int H, int dk, int dv, int dtype);
+
+/*
+ * lla_decode_step for a batch whose sequences all start with the same prefix_len tokens (a system
+ * prompt), whose Fenwick states are kept once per head instead of once per sequence. Every aligned
+ * block of the prefix's Fenwick walk lies inside one bucket of any later position, so a step is
+ *
+ *     o_t = sum_l lambda_t^(l) (own^(l))^T q_t + exp(D_t) sum_j lambda_t^(l(t,j)) (prefix^(j))^T q_t
+ *
+ * with own^(l) the part of bucket l at positions >= prefix_len, j the walk's blocks, and D_t the sum
+ * of log_a over the tokens prefix_len..t. The result is lla_decode_step's on the whole states.
+ *
+ *   q, k, v, log_a, lambda, t, out   as lla_decode_step; t[b] counts from the start of the prefix
+ *   prefix_states [H,Lp,dk,dv] fp32  read only: what lla_prefill_state writes for the prefix (B = 1).
+ *          Needs Lp >= lla_num_levels(prefix_len); slots that the prefix does not hold are not read.
+ *   prefix_len    >= 1               tokens of the prefix (P)
+ *   prefix_decay  [B,H]        fp32  D, read (not at t[b] = P, where it counts from 0) and written
+ *   fenwick_states [B,H,Lmax,dk,dv] fp32, read and written in place: each sequence's own buckets. Slot
+ *          l holds the part of bucket l at positions >= P. Slots without such positions are never read
+ *          and may hold anything (so nothing is read at t[b] = P, and no initialisation is needed); a
+ *          slot that the carry empties is left as it was.
+ *   Needs prefix_len <= t < 2^(Lmax-1); a sequence outside that range is skipped (its states, decay
+ *   and output untouched) and LLA_ERR_DEVICE is recorded in the device error word.
+ *   After a prompt of n own tokens handled by lla_prefill_state on its own, the states are valid here
+ *   where P is a multiple of a power of two >= n (then own levels do not depend on P).
+ *   dk 1..256; dv in {16, 32, 64, 128}; Lmax in 1..40. Workspace from the library's pool.
+ */
+int lla_decode_step_shared(const void* q, const void* k, const void* v, const float* log_a, const float* lambda,
+                           const float* prefix_states, int64_t prefix_len, int Lp, float* prefix_decay,
+                           float* fenwick_states, const int64_t* t, void* out, void* stream, int B, int H, int dk,
+                           int dv, int Lmax, int dtype);
+
+/*
  * Test hook for the failure path of the bounded waits (no counterpart on the
  * pages; not for production use). On the current device, for the tensor-core
  * prefill output kernel of dv = 64: limit_cycles > 0 bounds each of its pipeline

@@ -79,6 +79,17 @@ def load() -> ctypes.CDLL:
             lib.lla_forward_varlen.restype = i
             lib.lla_prefill_state_varlen.argtypes = [vp, vp, fp, vp, fp] + [i] * 7 + [vp, i]
             lib.lla_prefill_state_varlen.restype = i
+            lib.lla_linear_forward.argtypes = [vp, vp, vp, fp, fp, vp, fp] + [i] * 6 + [vp, i]
+            lib.lla_linear_forward.restype = i
+            lib.lla_linear_forward_varlen.argtypes = [vp, vp, vp, fp, fp, vp, fp, vp] + [i] * 7 + [vp, i]
+            lib.lla_linear_forward_varlen.restype = i
+            lib.lla_linear_backward.argtypes = [vp, vp, vp, fp, fp, vp, fp, vp, vp, vp, fp] + [i] * 6 + [vp, i]
+            lib.lla_linear_backward.restype = i
+            lib.lla_linear_decode_step.argtypes = [vp, vp, vp, fp, fp, vp, vp] + [i] * 5
+            lib.lla_linear_decode_step.restype = i
+            lib.lla_decode_step_shared.argtypes = ([vp, vp, vp, fp, fp, fp, ctypes.c_int64, i, fp, fp, vp, vp, vp]
+                                                   + [i] * 6)
+            lib.lla_decode_step_shared.restype = i
             _lib = lib
     return _lib
 
@@ -402,3 +413,179 @@ def prefill_state_varlen(k, v, log_a, cu_seqlens, max_T: int, states, stream=Non
 def device_error(stream=None) -> int:
     """Synchronise ``stream``, then read and clear the device error word (an lla status)."""
     return int(load().lla_device_error(_stream_handle(stream)))
+
+
+def _linear_inputs(named, log_a, H):
+    """Checks of the linear-attention calls: ``named`` {name: tensor} of one dtype, log_a [H] fp32."""
+    torch = _torch()
+    q = next(iter(named.values()))
+    for n, t_ in named.items():
+        _check(t_, n, q.device)
+        if t_.dtype != q.dtype:
+            raise TypeError(f"{', '.join(named)} must share one dtype")
+    _check(log_a, "log_a", q.device)
+    if log_a.dtype != torch.float32 or log_a.shape != (H,):
+        raise ValueError(f"log_a must be float32 [{H}] (one decay per head)")
+
+
+def _state(t_, name, shape, device):
+    """Address of an optional fp32 state tensor of the given shape (None: NULL)."""
+    torch = _torch()
+    if t_ is None:
+        return None
+    _check(t_, name, device)
+    if t_.dtype != torch.float32 or tuple(t_.shape) != tuple(shape):
+        raise ValueError(f"{name} must be float32 {list(shape)}, got {t_.dtype} {list(t_.shape)}")
+    return t_.data_ptr()
+
+
+def _on(device, stream):
+    """Contexts that make ``device`` and the launch stream current, so that what a call allocates
+    belongs to the stream that writes it."""
+    torch = _torch()
+    import contextlib
+    ctx = contextlib.ExitStack()
+    ctx.enter_context(torch.cuda.device(device))
+    if stream is not None:
+        if stream.device != device:
+            raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
+        ctx.enter_context(torch.cuda.stream(stream))
+    return ctx
+
+
+def _given(out, shape, like):
+    """The caller's output tensor, checked, or a new one."""
+    torch = _torch()
+    if out is None:
+        return torch.empty(shape, dtype=like.dtype, device=like.device)
+    _check(out, "out", like.device)
+    if out.dtype != like.dtype or tuple(out.shape) != tuple(shape):
+        raise ValueError(f"out must be {like.dtype} {list(shape)}, got {out.dtype} {list(out.shape)}")
+    return out
+
+
+def linear_forward(q, k, v, log_a, state0=None, state_out=None, out=None, stream=None):
+    """Linear attention with one decay per head, lla_linear_forward: S_t = exp(log_a_h) S_{t-1} + k_t v_t^T,
+    o_t = S_t^T q_t. Returns out [B,H,T,dv].
+
+    q, k [B,H,T,dk]; v [B,H,T,dv] (bf16 or fp32, one dtype, any T >= 1); log_a [H] fp32. ``state0`` fp32
+    [B,H,dk,dv], or [1,H,dk,dv] for one state shared by the batch, is the state the sequences go on from;
+    ``state_out`` fp32 [B,H,dk,dv] is written with the state after the last token (see linear_decode_step)."""
+    B, H, T, dk = q.shape
+    dv = v.shape[-1]
+    _linear_inputs({"q": q, "k": k, "v": v}, log_a, H)
+    if k.shape != q.shape or v.shape != (B, H, T, dv):
+        raise ValueError("shape mismatch between q, k and v")
+    B0 = 0 if state0 is None else int(state0.shape[0])
+    s0 = _state(state0, "state0", (1 if B0 == 1 else B, H, dk, dv), q.device)
+    s1 = _state(state_out, "state_out", (B, H, dk, dv), q.device)
+    with _on(q.device, stream):
+        out = _given(out, (B, H, T, dv), q)
+        _call(load().lla_linear_forward(q.data_ptr(), k.data_ptr(), v.data_ptr(), log_a.data_ptr(), s0,
+                                        out.data_ptr(), s1, B, B0, H, T, dk, dv, _stream_handle(stream),
+                                        _dtype_code(q)), "lla_linear_forward")
+    return out
+
+
+def linear_forward_varlen(q, k, v, log_a, cu_seqlens, max_T: int, state0=None, state_out=None, out=None, stream=None):
+    """lla_linear_forward_varlen: packed sequences. q, k [H,total,dk]; v [H,total,dv]; log_a [H]; cu_seqlens
+    int32 [n+1] on the device; state0 [n,H,dk,dv] or [1,H,dk,dv] (shared); state_out [n,H,dk,dv]. Rows of
+    ``out`` that belong to no sequence are left as they were (uninitialised in a new ``out``)."""
+    torch = _torch()
+    H, total, dk = q.shape
+    dv = v.shape[-1]
+    _linear_inputs({"q": q, "k": k, "v": v}, log_a, H)
+    _check(cu_seqlens, "cu_seqlens", q.device)
+    if cu_seqlens.dtype != torch.int32 or cu_seqlens.dim() != 1:
+        raise TypeError("cu_seqlens must be int32 [n+1]")
+    n = cu_seqlens.numel() - 1
+    if k.shape != q.shape or v.shape != (H, total, dv):
+        raise ValueError("shape mismatch between packed q, k and v")
+    n0 = 0 if state0 is None else int(state0.shape[0])
+    s0 = _state(state0, "state0", (1 if n0 == 1 else n, H, dk, dv), q.device)
+    s1 = _state(state_out, "state_out", (n, H, dk, dv), q.device)
+    with _on(q.device, stream):
+        out = _given(out, (H, total, dv), q)
+        _call(load().lla_linear_forward_varlen(q.data_ptr(), k.data_ptr(), v.data_ptr(), log_a.data_ptr(), s0,
+                                               out.data_ptr(), s1, cu_seqlens.data_ptr(), n, n0, H, total,
+                                               int(max_T), dk, dv, _stream_handle(stream), _dtype_code(q)),
+              "lla_linear_forward_varlen")
+    return out
+
+
+def linear_backward(q, k, v, log_a, dout, state0=None, dstate_out=None, stream=None):
+    """lla_linear_backward: gradients of sum(dout * out) + sum(dstate_out * state_out) of linear_forward.
+
+    Returns (dq, dk, dv, dstate0): dq/dk/dv in q's dtype, dstate0 fp32 like state0 (None without one; summed
+    over the batch where state0 is shared). log_a is a constant and has no gradient."""
+    torch = _torch()
+    B, H, T, dk = q.shape
+    dv = v.shape[-1]
+    _linear_inputs({"q": q, "k": k, "v": v, "dout": dout}, log_a, H)
+    if k.shape != q.shape or v.shape != (B, H, T, dv) or dout.shape != v.shape:
+        raise ValueError("shape mismatch between q, k, v and dout")
+    B0 = 0 if state0 is None else int(state0.shape[0])
+    s0 = _state(state0, "state0", (1 if B0 == 1 else B, H, dk, dv), q.device)
+    s1 = _state(dstate_out, "dstate_out", (B, H, dk, dv), q.device)
+    with _on(q.device, stream):
+        dq, dk_, dv_ = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
+        ds = None if state0 is None else torch.empty_like(state0)
+        _call(load().lla_linear_backward(q.data_ptr(), k.data_ptr(), v.data_ptr(), log_a.data_ptr(), s0,
+                                         dout.data_ptr(), s1, dq.data_ptr(), dk_.data_ptr(), dv_.data_ptr(),
+                                         None if ds is None else ds.data_ptr(), B, B0, H, T, dk, dv,
+                                         _stream_handle(stream), _dtype_code(q)), "lla_linear_backward")
+    return dq, dk_, dv_, ds
+
+
+def linear_decode_step(q, k, v, log_a, state, out=None, stream=None):
+    """One token of every sequence, lla_linear_decode_step. q, k [B,H,dk]; v [B,H,dv]; log_a [H] fp32;
+    ``state`` [B,H,dk,dv] fp32 is updated in place. Returns out [B,H,dv]."""
+    B, H, dk = q.shape
+    dv = v.shape[-1]
+    _linear_inputs({"q": q, "k": k, "v": v}, log_a, H)
+    if k.shape != q.shape or v.shape != (B, H, dv):
+        raise ValueError("shape mismatch between q, k and v")
+    if state is None:
+        raise ValueError("state is needed")
+    sp = _state(state, "state", (B, H, dk, dv), q.device)
+    with _on(q.device, stream):
+        out = _given(out, (B, H, dv), q)
+        _call(load().lla_linear_decode_step(q.data_ptr(), k.data_ptr(), v.data_ptr(), log_a.data_ptr(), sp,
+                                            out.data_ptr(), _stream_handle(stream), B, H, dk, dv, _dtype_code(q)),
+              "lla_linear_decode_step")
+    return out
+
+
+def decode_step_shared(q, k, v, log_a, lam, prefix_states, prefix_len: int, prefix_decay, states, t, out=None,
+                       stream=None):
+    """decode_step of a batch whose sequences share their first ``prefix_len`` tokens, lla_decode_step_shared.
+
+    ``prefix_states`` [H,Lp,dk,dv] fp32 (read only): prefill_state of the prefix, kept once. ``prefix_decay``
+    [B,H] fp32 and ``states`` [B,H,Lmax,dk,dv] fp32 (each sequence's own buckets) are updated in place and need
+    no initialisation. ``t`` int64 [B] on the device, prefix_len <= t. Returns out [B,H,dv]."""
+    torch = _torch()
+    B, H, dk = q.shape
+    dv = v.shape[-1]
+    for t_, n in ((q, "q"), (k, "k"), (v, "v"), (log_a, "log_a"), (lam, "lambda"), (t, "t")):
+        _check(t_, n, q.device)
+    if k.dtype != q.dtype or v.dtype != q.dtype:
+        raise TypeError("q, k and v must share one dtype")
+    if log_a.dtype != torch.float32 or lam.dtype != torch.float32:
+        raise TypeError("log_a and lambda must be float32")
+    if t.dtype != torch.int64 or t.shape != (B,):
+        raise ValueError("t must be int64 [B]")
+    if prefix_states is None or prefix_decay is None or states is None or prefix_states.dim() != 4 or states.dim() != 5:
+        raise ValueError("prefix_states [H,Lp,dk,dv], prefix_decay [B,H] and states [B,H,Lmax,dk,dv] are needed")
+    Lp, Lmax = int(prefix_states.shape[1]), int(states.shape[2])
+    pp = _state(prefix_states, "prefix_states", (H, Lp, dk, dv), q.device)
+    dp = _state(prefix_decay, "prefix_decay", (B, H), q.device)
+    sp = _state(states, "states", (B, H, Lmax, dk, dv), q.device)
+    if lam.shape != (B, H, Lmax) or log_a.shape != (B, H) or k.shape != q.shape or v.shape != (B, H, dv):
+        raise ValueError("shape mismatch in decode inputs")
+    with _on(q.device, stream):
+        out = _given(out, (B, H, dv), q)
+        _call(load().lla_decode_step_shared(q.data_ptr(), k.data_ptr(), v.data_ptr(), log_a.data_ptr(),
+                                            lam.data_ptr(), pp, int(prefix_len), Lp, dp, sp, t.data_ptr(),
+                                            out.data_ptr(), _stream_handle(stream), B, H, dk, dv, Lmax,
+                                            _dtype_code(q)), "lla_decode_step_shared")
+    return out

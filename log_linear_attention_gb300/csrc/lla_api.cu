@@ -5,6 +5,7 @@
 
 #include "../../include/lla.h"
 #include "lla_internal.cuh"
+#include "lla_linear.cuh"
 
 // One error word per device (each device holds its own copy of this variable).
 __device__ int lla_device_error_word;
@@ -617,6 +618,204 @@ int lla_device_error(void* stream) {
     if (word == lla::kDevBadInput) return LLA_ERR_DEVICE;
     if (word == lla::kDevTimeout) return LLA_ERR_TIMEOUT;
     return word == 0 ? LLA_OK : LLA_ERR_DEVICE;
+}
+
+}  // extern "C"
+
+// ---- linear attention with one decay per head
+
+namespace {
+
+bool overlap(const void* a, size_t na, const void* b, size_t nb) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return a && b && x < y + nb && y < x + na;
+}
+
+// Checks shared by the linear prefill, packed prefill and backward: `rows` = rows of one tensor,
+// batch = sequences, b0 = entering states.
+int validate_linear(const void* q, const void* k, const void* v, const float* log_a, const float* state0, int batch,
+                    int b0, int H, int64_t rows, int T, int dk, int dv, int dtype) {
+    if (!q || !k || !v || !log_a) return LLA_ERR_INVALID_ARG;
+    if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(log_a) || !aligned16(state0))
+        return LLA_ERR_INVALID_ARG;
+    if (dtype != LLA_BF16 && dtype != LLA_F32) return LLA_ERR_INVALID_ARG;
+    if (batch < 1 || H < 1 || T < 1 || dk < 1 || dv < 1) return LLA_ERR_INVALID_ARG;
+    if ((b0 != 0 && b0 != 1 && b0 != batch) || (b0 == 0) != (state0 == nullptr)) return LLA_ERR_INVALID_ARG;
+    if (dk > 128 || dv > 128) return LLA_ERR_UNSUPPORTED;
+    if ((int64_t)batch * H > 65535) return LLA_ERR_UNSUPPORTED;
+    if (rows * (dk > dv ? dk : dv) > ((int64_t)1 << 40)) return LLA_ERR_UNSUPPORTED;
+    if ((int64_t)batch * ((T - 1) / 64 + 1) > 0x7fffffff) return LLA_ERR_UNSUPPORTED;
+    return LLA_OK;
+}
+
+struct PoolBuffer {  // workspace from the library pool on one stream, returned there
+    cudaStream_t s;
+    char* p = nullptr;
+    explicit PoolBuffer(cudaStream_t stream) : s(stream) {}
+    int take(int dev, size_t bytes) {
+        if (bytes == 0) return LLA_OK;
+        cudaMemPool_t pool = workspace_pool(dev);
+        if (!pool) return LLA_ERR_CUDA;
+        if (cudaMallocFromPoolAsync(reinterpret_cast<void**>(&p), bytes, pool, s) != cudaSuccess) {
+            cudaGetLastError();
+            return LLA_ERR_NOMEM;
+        }
+        return LLA_OK;
+    }
+    int give(cudaError_t e) {
+        const cudaError_t f = p ? cudaFreeAsync(p, s) : cudaSuccess;
+        return (e == cudaSuccess && f == cudaSuccess) ? LLA_OK : LLA_ERR_CUDA;
+    }
+};
+
+size_t up256(size_t x) { return (x + 255) / 256 * 256; }
+
+lla::LinSeqs dense_seqs(int B, int H, int T) {
+    lla::LinSeqs sq = {};
+    sq.T = T;
+    sq.H = H;
+    sq.N = (T - 1) / 64 + 1;
+    sq.n_chunks = B * sq.N;
+    return sq;
+}
+
+int pieces64(int d) { return (d + 63) / 64; }
+
+}  // namespace
+
+extern "C" {
+
+int lla_linear_forward(const void* q, const void* k, const void* v, const float* log_a, const float* state0, void* out,
+                       float* state_out, int B, int B0, int H, int T, int dk, int dv, void* stream, int dtype) {
+    int st = validate_linear(q, k, v, log_a, state0, B, B0, H, (int64_t)B * H * T, T, dk, dv, dtype);
+    if (st != LLA_OK) return st;
+    if (!out || !aligned16(out) || !aligned16(state_out)) return LLA_ERR_INVALID_ARG;
+    const size_t msz = (size_t)dk * dv * sizeof(float);
+    if (overlap(state0, B0 * H * msz, state_out, B * H * msz)) return LLA_ERR_INVALID_ARG;
+    const int dev = current_device();
+    if (dev < 0) return LLA_ERR_CUDA;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const lla::LinSeqs sq = dense_seqs(B, H, T);
+    PoolBuffer ws(s);
+    if ((st = ws.take(dev, (size_t)H * sq.n_chunks * msz)) != LLA_OK) return st;
+    float* states = reinterpret_cast<float*>(ws.p);
+    lla::LinStateJobs jobs = {{{k, v, states, state0, state_out, B0 == 1, 0, dk, dv, pieces64(dk) * pieces64(dv)}}, 1};
+    lla::LinScans scans = {{{q, k, v, out, states, 0, 0, dk, dv, pieces64(dv)}}, 1};
+    return ws.give(lla::linear_run(dtype, jobs, scans, sq, log_a, s));
+}
+
+int lla_linear_forward_varlen(const void* q, const void* k, const void* v, const float* log_a, const float* state0,
+                              void* out, float* state_out, const int32_t* cu_seqlens, int n_seq, int n0, int H,
+                              int total_T, int max_T, int dk, int dv, void* stream, int dtype) {
+    if (!cu_seqlens || !aligned16(cu_seqlens) || total_T < 1) return LLA_ERR_INVALID_ARG;
+    int st = validate_linear(q, k, v, log_a, state0, n_seq, n0, H, (int64_t)H * total_T, max_T, dk, dv, dtype);
+    if (st != LLA_OK) return st;
+    if (!out || !aligned16(out) || !aligned16(state_out)) return LLA_ERR_INVALID_ARG;
+    const size_t msz = (size_t)dk * dv * sizeof(float);
+    if (overlap(state0, n0 * H * msz, state_out, n_seq * H * msz)) return LLA_ERR_INVALID_ARG;
+    const int dev = current_device();
+    if (dev < 0) return LLA_ERR_CUDA;
+    int* err = error_word(dev);
+    if (!err) return LLA_ERR_CUDA;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    lla::LinSeqs sq = {};
+    sq.n = n_seq;
+    sq.T = max_T;
+    sq.H = H;
+    sq.total = total_T;
+    sq.n_chunks = total_T / 64 + n_seq;
+    const size_t tab_b = up256((size_t)n_seq * sizeof(int2)), off_b = up256(((size_t)n_seq + 1) * sizeof(int));
+    PoolBuffer ws(s);
+    if ((st = ws.take(dev, tab_b + off_b + (size_t)H * sq.n_chunks * msz)) != LLA_OK) return st;
+    int2* tab = reinterpret_cast<int2*>(ws.p);
+    int* coff = reinterpret_cast<int*>(ws.p + tab_b);
+    float* states = reinterpret_cast<float*>(ws.p + tab_b + off_b);
+    sq.tab = tab;
+    sq.coff = coff;
+    cudaError_t e = lla::linear_table(cu_seqlens, n_seq, total_T, max_T, tab, coff, nullptr, err, s);
+    lla::LinStateJobs jobs = {{{k, v, states, state0, state_out, n0 == 1, 0, dk, dv, pieces64(dk) * pieces64(dv)}}, 1};
+    lla::LinScans scans = {{{q, k, v, out, states, 0, 0, dk, dv, pieces64(dv)}}, 1};
+    if (e == cudaSuccess) e = lla::linear_run(dtype, jobs, scans, sq, log_a, s);
+    return ws.give(e);
+}
+
+int lla_linear_backward(const void* q, const void* k, const void* v, const float* log_a, const float* state0,
+                        const void* dout, const float* dstate_out, void* dq, void* dk, void* dv, float* dstate0, int B,
+                        int B0, int H, int T, int dk_, int dv_, void* stream, int dtype) {
+    int st = validate_linear(q, k, v, log_a, state0, B, B0, H, (int64_t)B * H * T, T, dk_, dv_, dtype);
+    if (st != LLA_OK) return st;
+    if (!dout || !dq || !dk || !dv || !aligned16(dout) || !aligned16(dstate_out) || !aligned16(dq) || !aligned16(dk) ||
+        !aligned16(dv) || !aligned16(dstate0))
+        return LLA_ERR_INVALID_ARG;
+    if (dstate0 && B0 == 0) return LLA_ERR_INVALID_ARG;
+    const int dev = current_device();
+    if (dev < 0) return LLA_ERR_CUDA;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const lla::LinSeqs sq = dense_seqs(B, H, T);
+    const size_t msz = (size_t)dk_ * dv_ * sizeof(float);
+    const size_t st_b = up256((size_t)H * sq.n_chunks * msz);
+    const bool sum = dstate0 && B0 == 1 && B > 1;  // gradients of one shared state: a part per sequence, then their sum
+    PoolBuffer ws(s);
+    if ((st = ws.take(dev, 2 * st_b + (sum ? (size_t)B * H * msz : 0))) != LLA_OK) return st;
+    float* fw = reinterpret_cast<float*>(ws.p);
+    float* bw = reinterpret_cast<float*>(ws.p + st_b);
+    float* parts = reinterpret_cast<float*>(ws.p + 2 * st_b);
+    const int sp = pieces64(dk_) * pieces64(dv_);
+    lla::LinStateJobs jobs = {{{k, v, fw, state0, nullptr, B0 == 1, 0, dk_, dv_, sp},
+                               {q, dout, bw, dstate_out, sum ? parts : dstate0, 0, 1, dk_, dv_, sp}},
+                              2};
+    lla::LinScans scans = {{{dout, v, k, dq, fw, 1, 0, dv_, dk_, pieces64(dk_)},
+                            {v, dout, q, dk, bw, 1, 1, dv_, dk_, pieces64(dk_)},
+                            {k, q, dout, dv, bw, 0, 1, dk_, dv_, pieces64(dv_)}},
+                           3};
+    cudaError_t e = lla::linear_run(dtype, jobs, scans, sq, log_a, s);
+    if (e == cudaSuccess && sum) e = lla::linear_sum_batch(parts, dstate0, B, (int64_t)H * dk_ * dv_, s);
+    return ws.give(e);
+}
+
+int lla_linear_decode_step(const void* q, const void* k, const void* v, const float* log_a, float* state, void* out,
+                           void* stream, int B, int H, int dk, int dv, int dtype) {
+    if (!q || !k || !v || !log_a || !state || !out) return LLA_ERR_INVALID_ARG;
+    if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(log_a) || !aligned16(state) || !aligned16(out))
+        return LLA_ERR_INVALID_ARG;
+    if (dtype != LLA_BF16 && dtype != LLA_F32) return LLA_ERR_INVALID_ARG;
+    if (B < 1 || H < 1 || dk < 1 || dv < 1) return LLA_ERR_INVALID_ARG;
+    if (dk > 128 || dv > 128) return LLA_ERR_UNSUPPORTED;
+    if ((int64_t)B * H > 0x7fffffff) return LLA_ERR_UNSUPPORTED;
+    if (current_device() < 0) return LLA_ERR_CUDA;
+    return lla::linear_decode_step(dtype, q, k, v, log_a, state, out, B, H, dk, dv,
+                                   static_cast<cudaStream_t>(stream)) == cudaSuccess
+               ? LLA_OK
+               : LLA_ERR_CUDA;
+}
+
+int lla_decode_step_shared(const void* q, const void* k, const void* v, const float* log_a, const float* lambda,
+                           const float* prefix_states, int64_t prefix_len, int Lp, float* prefix_decay,
+                           float* fenwick_states, const int64_t* t, void* out, void* stream, int B, int H, int dk,
+                           int dv, int Lmax, int dtype) {
+    if (!q || !k || !v || !log_a || !lambda || !prefix_states || !prefix_decay || !fenwick_states || !t || !out)
+        return LLA_ERR_INVALID_ARG;
+    for (const void* p : {q, k, v, static_cast<const void*>(log_a), static_cast<const void*>(lambda),
+                          static_cast<const void*>(prefix_states), static_cast<const void*>(prefix_decay),
+                          static_cast<const void*>(fenwick_states), static_cast<const void*>(t),
+                          static_cast<const void*>(out)})
+        if (!aligned16(p)) return LLA_ERR_INVALID_ARG;
+    if (dtype != LLA_BF16 && dtype != LLA_F32) return LLA_ERR_INVALID_ARG;
+    if (B < 1 || H < 1 || dk < 1 || dv < 1 || Lmax < 1 || Lmax > 40 || Lp < 1 || Lp > 40) return LLA_ERR_INVALID_ARG;
+    if (prefix_len < 1 || prefix_len >= ((int64_t)1 << (Lmax - 1)) || lla_num_levels(prefix_len) > Lp)
+        return LLA_ERR_INVALID_ARG;
+    if (dk > 256 || (dv != 16 && dv != 32 && dv != 64 && dv != 128)) return LLA_ERR_UNSUPPORTED;
+    if ((int64_t)B * H > 0x7fffffff || H > 65535 || B > 65535) return LLA_ERR_UNSUPPORTED;
+    const int dev = current_device();
+    if (dev < 0) return LLA_ERR_CUDA;
+    int* err = error_word(dev);
+    if (!err) return LLA_ERR_CUDA;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    PoolBuffer ws(s);
+    const int st = ws.take(dev, lla::shared_workspace_bytes(B, H, dv, prefix_len));
+    if (st != LLA_OK) return st;
+    return ws.give(lla::decode_step_shared(dtype, q, k, v, log_a, lambda, prefix_states, prefix_len, Lp, prefix_decay,
+                                           fenwick_states, t, out, ws.p, B, H, dk, dv, Lmax, err, s));
 }
 
 }  // extern "C"

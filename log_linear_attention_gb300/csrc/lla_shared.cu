@@ -1,0 +1,201 @@
+// The log-linear decode step of a batch over one shared prefix.
+//
+// Every sequence starts with the same P tokens. The Fenwick walk of P - 1 splits them into
+// aligned blocks, each wholly inside one bucket of any later position t: the highest bit in which
+// t and a position of the block differ lies above the block. So
+//     o = sum_l lambda^(l) (own^(l))^T q + exp(D) sum_j lambda^(l(t, block j)) (prefix^(j))^T q,
+// where own^(l) is bucket l restricted to positions >= P, prefix^(j) the prefix's state of block
+// j decayed to P - 1, and D the sum of log_a over P..t. The prefix states are read once for the
+// whole batch and never written; a sequence reads and writes only the buckets that hold own
+// tokens. Bucket l >= 1 of position pos (bit l - 1 of pos set) is [(pos >> l) << l, + 2^(l-1)):
+// it holds own tokens when its end is past P.
+#include "lla_linear.cuh"
+
+namespace lla {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kMaxDk = 256;
+
+// slot l is held at pos and has a position >= P
+__device__ __forceinline__ bool own_held(int64_t pos, int64_t P, int l) {
+    if (pos < P) return false;
+    if (l == 0) return true;
+    if (((pos >> (l - 1)) & 1) == 0) return false;
+    return ((pos >> l) << l) + (int64_t(1) << (l - 1)) > P;
+}
+
+// part[j][bh][x] = sum_i prefix[h][slot j][i][x] q[bh][i]. grid (held prefix slots, H, batch tiles).
+template <typename T>
+__global__ void __launch_bounds__(kThreads) shared_prefix(const T* __restrict__ q, const float* __restrict__ prefix,
+                                                          float* __restrict__ part, int64_t P, int B, int H, int dk,
+                                                          int dv, int Lp) {
+    __shared__ float qs[8][kMaxDk];
+    const int j = blockIdx.x, h = blockIdx.y, b0 = blockIdx.z * 8, tid = threadIdx.x;
+    int l = 0;  // the j-th held slot of the walk of P - 1
+    for (int left = j; left > 0;) {
+        l++;
+        if (((P - 1) >> (l - 1)) & 1) left--;
+    }
+    const float* S = prefix + (static_cast<int64_t>(h) * Lp + l) * dk * dv;
+    const int nb = B - b0 < 8 ? B - b0 : 8;
+    for (int e = tid; e < nb * dk; e += kThreads)
+        qs[e / dk][e % dk] = load_f(q + (static_cast<int64_t>(b0 + e / dk) * H + h) * dk + e % dk);
+    __syncthreads();
+    for (int e = tid; e < nb * dv; e += kThreads) {
+        const int b = e / dv, x = e % dv;
+        float s = 0.f;
+        for (int i = 0; i < dk; i++) s += S[static_cast<int64_t>(i) * dv + x] * qs[b][i];
+        part[((static_cast<int64_t>(j) * B + b0 + b) * H + h) * dv + x] = s;
+    }
+}
+
+// One CTA per (b, h): the own buckets (carry, decay, read) and the prefix's parts.
+template <typename T, int DV4>
+__global__ void __launch_bounds__(kThreads) shared_own(const T* __restrict__ q, const T* __restrict__ k,
+                                                       const T* __restrict__ v, const float* __restrict__ log_a,
+                                                       const float* __restrict__ lambda,
+                                                       const float* __restrict__ part, float* __restrict__ decay,
+                                                       float* __restrict__ states, const int64_t* __restrict__ tpos,
+                                                       T* __restrict__ out, int64_t P, int B, int H, int dk, int Lmax,
+                                                       int* err) {
+    constexpr int DV = DV4 * 4;
+    constexpr int kRows = kThreads / DV4;
+    __shared__ float qs[kMaxDk], ks[kMaxDk], lam[40];
+    __shared__ float red[kThreads / 32][DV];
+    const int tid = threadIdx.x;
+    const int64_t bh = blockIdx.x;
+    const int b = static_cast<int>(bh / H);
+    const int64_t t = tpos[b];
+    if (t < P || t >= (int64_t(1) << (Lmax - 1))) {
+        if (tid == 0) record_error(err, kDevBadInput);
+        return;
+    }
+    for (int x = tid; x < dk; x += kThreads) {
+        qs[x] = load_f(q + bh * dk + x);
+        ks[x] = load_f(k + bh * dk + x);
+    }
+    for (int x = tid; x < Lmax; x += kThreads) lam[x] = lambda[bh * Lmax + x];
+    const float la = log_a[bh];
+    const float D = (t > P ? decay[bh] : 0.f) + la;
+    __syncthreads();
+    if (tid == 0) decay[bh] = D;  // after every thread has read it
+
+    const float a = expf(la);
+    const int c = __ffsll(static_cast<long long>(t)) - 1;   // trailing zeros of t (t >= P >= 1)
+    const int top = 64 - __clzll(static_cast<long long>(t));  // highest slot that t holds
+    const int col4 = tid % DV4;
+    const int64_t msz4 = static_cast<int64_t>(dk) * DV4;
+    float4* S = reinterpret_cast<float4*>(states) + bh * Lmax * msz4;
+    const T* vp = v + bh * DV + col4 * 4;
+    const float4 v4 = make_float4(load_f(vp), load_f(vp + 1), load_f(vp + 2), load_f(vp + 3));
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int i = tid / DV4; i < dk; i += kRows) {
+        const int64_t e = static_cast<int64_t>(i) * DV4 + col4;
+        const float qi = qs[i];
+        if (t > P) {
+            float4 m = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int l = 0; l <= c; l++) {
+                if (!own_held(t - 1, P, l)) continue;
+                const float4 x = S[l * msz4 + e];
+                m.x += x.x; m.y += x.y; m.z += x.z; m.w += x.w;
+            }
+            m.x *= a; m.y *= a; m.z *= a; m.w *= a;
+            S[(c + 1) * msz4 + e] = m;
+            const float w = lam[c + 1] * qi;
+            o.x += w * m.x; o.y += w * m.y; o.z += w * m.z; o.w += w * m.w;
+            for (int l = c + 2; l <= top; l++) {
+                if (!own_held(t - 1, P, l)) continue;
+                float4 x = S[l * msz4 + e];
+                x.x *= a; x.y *= a; x.z *= a; x.w *= a;
+                S[l * msz4 + e] = x;
+                const float wl = lam[l] * qi;
+                o.x += wl * x.x; o.y += wl * x.y; o.z += wl * x.z; o.w += wl * x.w;
+            }
+        }
+        const float ki = ks[i];
+        const float4 x0 = make_float4(ki * v4.x, ki * v4.y, ki * v4.z, ki * v4.w);
+        S[e] = x0;
+        const float w0 = lam[0] * qi;
+        o.x += w0 * x0.x; o.y += w0 * x0.y; o.z += w0 * x0.z; o.w += w0 * x0.w;
+    }
+#pragma unroll
+    for (int off = DV4; off < 32; off <<= 1) {
+        o.x += __shfl_xor_sync(0xffffffffu, o.x, off);
+        o.y += __shfl_xor_sync(0xffffffffu, o.y, off);
+        o.z += __shfl_xor_sync(0xffffffffu, o.z, off);
+        o.w += __shfl_xor_sync(0xffffffffu, o.w, off);
+    }
+    const int warp = tid >> 5, lane = tid & 31;
+    if (lane < DV4) {
+        red[warp][lane * 4 + 0] = o.x;
+        red[warp][lane * 4 + 1] = o.y;
+        red[warp][lane * 4 + 2] = o.z;
+        red[warp][lane * 4 + 3] = o.w;
+    }
+    __syncthreads();
+    if (tid < DV) {
+        float s = 0.f;
+#pragma unroll
+        for (int w = 0; w < kThreads / 32; w++) s += red[w][tid];
+        // prefix blocks: slot l of the walk of P - 1 starts at ((P - 1) >> l) << l
+        float far = 0.f;
+        int j = 0;
+        for (int l = 0; (int64_t(1) << l) <= 2 * (P - 1) || l == 0; l++) {
+            if (l > 0 && (((P - 1) >> (l - 1)) & 1) == 0) continue;
+            const int lev = 64 - __clzll(static_cast<long long>(t ^ (((P - 1) >> l) << l)));
+            far += lam[lev] * part[(static_cast<int64_t>(j) * B * H + bh) * DV + tid];
+            j++;
+        }
+        store_f(out + bh * DV + tid, s + expf(D) * far);
+    }
+}
+
+int held_slots(int64_t prefix_len) {
+    int n = 1;
+    for (int64_t x = prefix_len - 1; x > 0; x &= x - 1) n++;
+    return n;
+}
+
+template <typename T>
+cudaError_t shared_t(const void* q, const void* k, const void* v, const float* log_a, const float* lambda,
+                     const float* prefix, int64_t P, int Lp, float* decay, float* states, const int64_t* t, void* out,
+                     float* part, int B, int H, int dk, int dv, int Lmax, int* err, cudaStream_t stream) {
+    const T* qp = static_cast<const T*>(q);
+    shared_prefix<T><<<dim3(held_slots(P), H, (B + 7) / 8), kThreads, 0, stream>>>(qp, prefix, part, P, B, H, dk, dv,
+                                                                                  Lp);
+    note_launch(stream, "shared_prefix");
+    auto go = [&](auto kern) {
+        kern<<<static_cast<unsigned>(B) * H, kThreads, 0, stream>>>(
+            qp, static_cast<const T*>(k), static_cast<const T*>(v), log_a, lambda, static_cast<const float*>(part),
+            decay, states, t, static_cast<T*>(out), P, B, H, dk, Lmax, err);
+    };
+    switch (dv) {
+        case 16: go(shared_own<T, 4>); break;
+        case 32: go(shared_own<T, 8>); break;
+        case 64: go(shared_own<T, 16>); break;
+        default: go(shared_own<T, 32>); break;
+    }
+    note_launch(stream, "shared_own");
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+size_t shared_workspace_bytes(int B, int H, int dv, int64_t prefix_len) {
+    return static_cast<size_t>(held_slots(prefix_len)) * B * H * dv * sizeof(float);
+}
+
+cudaError_t decode_step_shared(int dtype, const void* q, const void* k, const void* v, const float* log_a,
+                               const float* lambda, const float* prefix_states, int64_t prefix_len, int Lp,
+                               float* prefix_decay, float* states, const int64_t* t, void* out, void* workspace,
+                               int B, int H, int dk, int dv, int Lmax, int* err, cudaStream_t stream) {
+    float* part = static_cast<float*>(workspace);
+    if (dtype == 1)
+        return shared_t<float>(q, k, v, log_a, lambda, prefix_states, prefix_len, Lp, prefix_decay, states, t, out,
+                               part, B, H, dk, dv, Lmax, err, stream);
+    return shared_t<__nv_bfloat16>(q, k, v, log_a, lambda, prefix_states, prefix_len, Lp, prefix_decay, states, t, out,
+                                   part, B, H, dk, dv, Lmax, err, stream);
+}
+
+}  // namespace lla

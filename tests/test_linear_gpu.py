@@ -1,0 +1,440 @@
+"""GPU checks of linear attention with one decay per head against the 64-bit pair sums of tests/_linear.py."""
+import numpy as np
+import pytest
+
+from tests import _linear as L
+
+torch = pytest.importorskip("torch")
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _cuda():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+
+
+@pytest.fixture()
+def lla():
+    from log_linear_attention_gb300 import binding
+    yield binding
+    assert binding.device_error() == 0
+
+
+def slopes(H, seed=0):
+    """Decays from fast (about 0.5) to slow (about 0.996), one head without decay, one that forgets at once."""
+    la = -np.exp2(-8.0 * np.arange(1, H + 1) / H) * (0.9 + 0.2 * np.random.default_rng(seed).random(H))
+    if H >= 3:
+        la[1] = 0.0
+        la[2] = -np.inf
+    return la.astype(np.float32)
+
+
+def problem(B, H, T, dk, dv, dtype, B0, seed=0):
+    """{name: (float64 array, CUDA tensor)}"""
+    r = np.random.default_rng(seed)
+    p = {"q": L.make(r, (B, H, T, dk), dtype, dk ** -0.5), "k": L.make(r, (B, H, T, dk), dtype, dk ** -0.5),
+         "v": L.make(r, (B, H, T, dv), dtype), "dout": L.make(r, (B, H, T, dv), dtype),
+         "ds": L.make(r, (B, H, dk, dv), "f32", dk ** -0.5)}
+    if B0:
+        p["s0"] = L.make(r, (B0, H, dk, dv), "f32", dk ** -0.5)
+    la = slopes(H, seed)
+    p["la"] = la.astype(np.float64), torch.from_numpy(la)
+    return {n: (a, t.cuda()) for n, (a, t) in p.items()}
+
+
+def val(p, n):
+    return p[n][0] if n in p else None
+
+
+def dev(p, n):
+    return p[n][1] if n in p else None
+
+
+def sizes(*x):
+    return [None if a is None else np.abs(a) for a in x]
+
+
+def host(t):
+    return t.double().cpu().numpy()
+
+
+SHAPES = [
+    # B, H, T, dk, dv, dtype, B0
+    (1, 1, 1, 64, 64, "bf16", 0), (3, 4, 1, 128, 64, "bf16", 3), (2, 3, 2, 16, 8, "bf16", 1),
+    (2, 3, 63, 64, 128, "bf16", 2), (1, 4, 64, 128, 128, "bf16", 1), (2, 4, 65, 8, 24, "bf16", 0),
+    (1, 4, 127, 72, 80, "bf16", 1), (2, 4, 128, 128, 64, "bf16", 2), (1, 5, 129, 64, 64, "bf16", 0),
+    (2, 4, 255, 96, 72, "bf16", 2), (2, 4, 256, 128, 128, "bf16", 0), (2, 8, 700, 128, 128, "bf16", 1),
+    (1, 4, 1301, 80, 104, "bf16", 1), (1, 4, 300, 50, 33, "bf16", 1), (2, 3, 130, 127, 128, "bf16", 2),
+    (1, 1, 1, 1, 1, "f32", 0), (2, 3, 1, 20, 30, "f32", 2), (1, 4, 64, 64, 64, "f32", 1), (2, 4, 65, 128, 128, "f32", 2),
+    (2, 4, 200, 100, 36, "f32", 1), (1, 3, 1000, 17, 65, "f32", 0),
+]
+
+
+@pytest.mark.parametrize("B,H,T,dk,dv,dtype,B0", SHAPES)
+def test_forward(lla, B, H, T, dk, dv, dtype, B0):
+    p = problem(B, H, T, dk, dv, dtype, B0, seed=T)
+    s1 = torch.full((B, H, dk, dv), float("nan"), device="cuda")
+    out = lla.linear_forward(dev(p, "q"), dev(p, "k"), dev(p, "v"), dev(p, "la"), state0=dev(p, "s0"), state_out=s1)
+    x = [val(p, n) for n in ("q", "k", "v", "la", "s0")]
+    ref, ref_s = L.forward(*x)
+    size, size_s = L.forward(*sizes(*x[:3]), x[3], *sizes(x[4]))
+    L.check(host(out), ref, size, dtype, T + dk, "out")
+    L.check(host(s1), ref_s, size_s, "f32", T, "state")
+    # without a state to write, the outputs are the same
+    again = lla.linear_forward(dev(p, "q"), dev(p, "k"), dev(p, "v"), dev(p, "la"), state0=dev(p, "s0"))
+    assert torch.equal(out, again)
+
+
+@pytest.mark.parametrize("B,H,T,dk,dv,dtype,B0", SHAPES)
+def test_backward(lla, B, H, T, dk, dv, dtype, B0):
+    p = problem(B, H, T, dk, dv, dtype, B0, seed=T + 1)
+    got = lla.linear_backward(*(dev(p, n) for n in ("q", "k", "v", "la", "dout")), state0=dev(p, "s0"),
+                              dstate_out=dev(p, "ds"))
+    x = [val(p, n) for n in ("q", "k", "v", "la", "dout", "s0", "ds")]
+    ref = list(L.backward(*x))
+    size = list(L.backward(*sizes(*x[:3]), x[3], *sizes(*x[4:])))
+    for n, i in (("dq", 0), ("dk", 1), ("dv", 2)):
+        L.check(host(got[i]), ref[i], size[i], dtype, T + max(dk, dv), n)
+    if not B0:
+        assert got[3] is None
+        return
+    if B0 == 1:
+        ref[3], size[3] = ref[3].sum(0, keepdims=True), size[3].sum(0, keepdims=True)
+    L.check(host(got[3]), ref[3], size[3], "f32", T + B, "dstate0")
+
+
+def test_backward_without_state_gradient(lla):
+    p = problem(2, 3, 150, 64, 64, "bf16", 0)
+    got = lla.linear_backward(*(dev(p, n) for n in ("q", "k", "v", "la", "dout")))
+    x = [val(p, n) for n in ("q", "k", "v", "la", "dout")]
+    ref, size = L.backward(*x), L.backward(*sizes(*x[:3]), x[3], *sizes(x[4]))
+    for i in range(3):
+        L.check(host(got[i]), ref[i], size[i], "bf16", 214, i)
+
+
+@pytest.mark.parametrize("dk,dv", [(16, 8), (128, 64), (12, 6)])
+def test_backward_is_the_forward_s_difference(lla, dk, dv):
+    """Along random directions: fp32 inputs, loss in 64 bits from fp32 outputs. The loss is linear in each input,
+    so the difference over +-1 of a direction has no error but the forward's roundings: at most
+    (T + dk + 16) 2^-23 of the terms' sizes for each side."""
+    B, H, T = 2, 3, 70
+    p = problem(B, H, T, dk, dv, "f32", 2, seed=5)
+    args = {n: dev(p, n) for n in ("q", "k", "v", "s0")}
+
+    def loss(a):
+        s1 = torch.empty(B, H, dk, dv, device="cuda")
+        o = lla.linear_forward(a["q"], a["k"], a["v"], dev(p, "la"), state0=a["s0"], state_out=s1)
+        return float((o.double() * dev(p, "dout").double()).sum() + (s1.double() * dev(p, "ds").double()).sum())
+
+    def total(a):
+        o, s = L.forward(*sizes(a["q"], a["k"], a["v"]), val(p, "la"), *sizes(a["s0"]))
+        return (o * np.abs(val(p, "dout"))).sum() + (s * np.abs(val(p, "ds"))).sum()
+
+    grads = dict(zip(("q", "k", "v", "s0"), lla.linear_backward(args["q"], args["k"], args["v"], dev(p, "la"),
+                                                                 dev(p, "dout"), state0=args["s0"],
+                                                                 dstate_out=dev(p, "ds"))))
+    r = np.random.default_rng(6)
+    for n, x in args.items():
+        d = torch.from_numpy(np.sign(r.standard_normal(x.shape)).astype(np.float32) * 0.25).cuda()
+        up, down = {**args, n: x + d}, {**args, n: x - d}
+        diff = (loss(up) - loss(down)) / 2
+        want = float((grads[n].double() * d.double()).sum())
+        tol = (T + dk + 16) * 2 * L.U32 * max(total({m: host(t) for m, t in a.items()}) for a in (up, down)) * 2
+        assert abs(diff - want) <= tol, (n, diff, want, tol)
+
+
+def pack(lengths, H, dk, dv, dtype, n0, tail, seed):
+    r = np.random.default_rng(seed)
+    total = sum(lengths) + tail
+    p = {"q": L.make(r, (H, total, dk), dtype, dk ** -0.5), "k": L.make(r, (H, total, dk), dtype, dk ** -0.5),
+         "v": L.make(r, (H, total, dv), dtype)}
+    if n0:
+        p["s0"] = L.make(r, (n0, H, dk, dv), "f32", dk ** -0.5)
+    la = slopes(H, seed)
+    p["la"] = la.astype(np.float64), torch.from_numpy(la)
+    cu = np.concatenate([[0], np.cumsum(lengths)]).astype(np.int32)
+    return {n: (a, t.cuda()) for n, (a, t) in p.items()}, cu
+
+
+def check_packed(p, cu, out, s1, dtype, skip=()):
+    n = len(cu) - 1
+    for b in range(n):
+        if b in skip:
+            continue
+        rows = slice(cu[b], cu[b + 1])
+        T = cu[b + 1] - cu[b]
+        s0 = val(p, "s0")
+        s0 = None if s0 is None else s0[b if s0.shape[0] > 1 else 0][None]
+        if T == 0:
+            want = np.zeros_like(s1[b]) if s0 is None else s0[0]
+            assert np.array_equal(s1[b], want)
+            continue
+        x = [val(p, m)[None, :, rows] for m in ("q", "k", "v")] + [val(p, "la"), s0]
+        ref, ref_s = L.forward(*x)
+        size, size_s = L.forward(*sizes(*x[:3]), x[3], *sizes(s0))
+        L.check(out[None, :, rows], ref, size, dtype, T + x[0].shape[-1], f"out {b}")
+        L.check(s1[None, b], ref_s, size_s, "f32", T, f"state {b}")
+
+
+@pytest.mark.parametrize("lengths,H,dk,dv,dtype,n0,tail", [
+    ([1], 3, 64, 64, "bf16", 0, 0), ([0, 0, 5, 0], 3, 64, 64, "bf16", 4, 3), ([0], 2, 64, 32, "bf16", 1, 4),
+    ([1, 37, 128, 300, 129, 0, 257, 1], 4, 128, 64, "bf16", 1, 130), ([700, 3, 128, 64], 3, 64, 128, "bf16", 4, 1),
+    ([100, 31, 200], 4, 24, 40, "bf16", 0, 9), ([1, 63, 64, 65, 0, 200], 3, 20, 36, "f32", 6, 70),
+    ([5, 130], 3, 128, 128, "f32", 1, 0), ([90, 2], 3, 30, 50, "bf16", 1, 2),
+])
+def test_varlen(lla, lengths, H, dk, dv, dtype, n0, tail):
+    p, cu = pack(lengths, H, dk, dv, dtype, n0, tail, seed=len(lengths))
+    n, total = len(lengths), sum(lengths) + tail
+    out = torch.full((H, total, dv), 7.0, device="cuda", dtype=p["q"][1].dtype)
+    s1 = torch.full((n, H, dk, dv), float("nan"), device="cuda")
+    got = lla.linear_forward_varlen(dev(p, "q"), dev(p, "k"), dev(p, "v"), dev(p, "la"), torch.from_numpy(cu).cuda(),
+                                    max(max(lengths), 1), state0=dev(p, "s0"), state_out=s1, out=out)
+    assert got is out
+    o = host(out)
+    check_packed(p, cu, o, host(s1), dtype)
+    assert (o[:, cu[-1]:] == 7.0).all()
+
+
+@pytest.mark.parametrize("dtype,dk", [("bf16", 64), ("f32", 64), ("bf16", 20)])
+def test_varlen_rows_of_others_never_reach_a_sequence(lla, dtype, dk):
+    """Every row outside the sequences under test holds NaN or infinities."""
+    lengths, H, dv = [70, 130, 1, 200, 40], 3, 64
+    p, cu = pack(lengths, H, dk, dv, dtype, 0, 60, seed=3)
+    bad = [b for b in range(5) if b % 2]
+    for n in ("q", "k", "v"):
+        for b in bad:
+            p[n][1][:, cu[b]:cu[b + 1]] = float("nan") if b == 1 else float("inf")
+        p[n][1][:, cu[-1]:] = float("-inf")
+    s1 = torch.zeros(5, H, dk, dv, device="cuda")
+    out = torch.zeros(H, sum(lengths) + 60, dv, device="cuda", dtype=p["q"][1].dtype)
+    lla.linear_forward_varlen(dev(p, "q"), dev(p, "k"), dev(p, "v"), dev(p, "la"), torch.from_numpy(cu).cuda(), 200,
+                              state_out=s1, out=out)
+    check_packed(p, cu, host(out), host(s1), dtype, skip=bad)
+    assert (host(out)[:, cu[-1]:] == 0).all()
+
+
+def test_values_that_are_not_finite_obey_causality_beyond_their_chunk(lla):
+    """An infinity in v at token t leaves every row of earlier 128-token chunks as it was, and one in k or q every
+    earlier row."""
+    for name, t, first in (("v", 300, 256), ("k", 300, 300), ("q", 300, 300)):
+        p = problem(1, 2, 500, 64, 64, "bf16", 0, seed=8)
+        args = {n: dev(p, n).clone() for n in ("q", "k", "v")}
+        clean = lla.linear_forward(*args.values(), dev(p, "la"))
+        args[name][:, :, t] = float("nan")
+        out = lla.linear_forward(*args.values(), dev(p, "la"))
+        assert torch.equal(out[:, :, :first], clean[:, :, :first]), name
+        if name == "q":
+            assert torch.equal(out[:, :, t + 1:], clean[:, :, t + 1:])
+        assert not torch.isfinite(out[:, :, t].float()).any()
+
+
+@pytest.mark.parametrize("dk,dtype", [(64, "bf16"), (32, "f32")])
+def test_varlen_bad_bounds_are_reported_and_skipped(dk, dtype):
+    from log_linear_attention_gb300 import binding as lla
+    lengths, H, dv = [50, 60, 70, 80], 2, 64
+    p, good = pack(lengths, H, dk, dv, dtype, 0, 0, seed=4)
+    for bad, skip in (([0, 50, 110, 40, 260], (2,)),      # falls: sequence 2 is out, 3 starts below row 110
+                      ([0, 50, 110, 180, 300], (3,)),     # past the tensor
+                      ([-5, 50, 110, 180, 260], (0,)),    # before it
+                      ([0, 50, 230, 230, 260], (1,))):    # longer than max_T
+        cu = np.array(bad, dtype=np.int32)
+        out = torch.full((H, 260, dv), 3.0, device="cuda", dtype=p["q"][1].dtype)
+        s1 = torch.full((4, H, dk, dv), 3.0, device="cuda")
+        lla.linear_forward_varlen(dev(p, "q"), dev(p, "k"), dev(p, "v"), dev(p, "la"), torch.from_numpy(cu).cuda(),
+                                  100, state_out=s1, out=out)
+        assert lla.device_error() == lla.LLA_ERR_DEVICE
+        assert lla.device_error() == 0
+        if bad[3] == 40:
+            skip = (2, 3)
+        for b in skip:
+            assert (host(s1)[b] == 3.0).all(), (bad, b)
+        ok = [b for b in range(4) if b not in skip]
+        for b in ok:
+            assert not (host(s1)[b] == 3.0).all()
+        check_packed(p, cu, host(out), host(s1), dtype, skip=skip)
+        covered = np.zeros(260, dtype=bool)
+        for b in ok:
+            covered[cu[b]:cu[b + 1]] = True
+        assert (host(out)[:, ~covered] == 3.0).all(), bad
+
+
+@pytest.mark.parametrize("B,H,dk,dv,dtype", [
+    (1, 1, 1, 1, "f32"), (3, 2, 64, 64, "bf16"), (2, 3, 128, 128, "f32"), (5, 3, 100, 36, "bf16"), (2, 2, 17, 33, "f32"),
+    (2, 2, 128, 2, "bf16"), (300, 4, 16, 128, "bf16"),
+])
+def test_decode(lla, B, H, dk, dv, dtype):
+    p = problem(B, H, 1, dk, dv, dtype, B, seed=dk)
+    st = dev(p, "s0").clone()
+    q, k, v = (dev(p, n)[:, :, 0].contiguous() for n in ("q", "k", "v"))
+    out = lla.linear_decode_step(q, k, v, dev(p, "la"), st)
+    x = [val(p, n) for n in ("q", "k", "v", "la", "s0")]
+    ref, ref_s = L.forward(*x)
+    size, size_s = L.forward(*sizes(*x[:3]), x[3], *sizes(x[4]))
+    # the state is fp32 throughout, so a bf16 output has its own rounding alone
+    err = np.abs(host(out)[:, :, None] - ref)
+    assert (err <= (L.UBF if dtype == "bf16" else 0) * np.abs(ref) + (dk + 16) * 2 * L.U32 * size).all()
+    L.check(host(st), ref_s, size_s, "f32", 4, "state")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_prompt_then_tokens_is_the_whole(lla, dtype):
+    """Prompts cut anywhere, the state handed on, then single tokens: each piece against the whole's sums."""
+    B, H, T, dk, dv = 2, 4, 333, 64, 48
+    p = problem(B, H, T, dk, dv, dtype, 1, seed=11)
+    x = [val(p, n) for n in ("q", "k", "v", "la", "s0")]
+    ref, ref_s = L.forward(*x)
+    size, size_s = L.forward(*sizes(*x[:3]), x[3], *sizes(x[4]))
+    state, outs, at = dev(p, "s0"), [], 0
+    for n in (130, 1, 199):
+        part = [dev(p, m)[:, :, at:at + n].contiguous() for m in ("q", "k", "v")]
+        s1 = torch.empty(B, H, dk, dv, device="cuda")
+        outs.append(lla.linear_forward(*part, dev(p, "la"), state0=state, state_out=s1))
+        state, at = s1, at + n
+    for t in range(at, T):
+        part = [dev(p, m)[:, :, t].contiguous() for m in ("q", "k", "v")]
+        outs.append(lla.linear_decode_step(*part, dev(p, "la"), state)[:, :, None])
+    L.check(host(torch.cat(outs, 2)), ref, size, dtype, T + dk, "out")
+    L.check(host(state), ref_s, size_s, "f32", T, "state")
+
+
+def test_equals_the_hierarchy_with_equal_levels(lla):
+    """lla_forward with lambda = 1 and one decay at every token: both are within their roundings of the sums."""
+    B, H, T, dk, dv = 1, 4, 256, 64, 32
+    p = problem(B, H, T, dk, dv, "f32", 0, seed=12)
+    la = torch.where(torch.isinf(dev(p, "la")), torch.tensor(-2.0, device="cuda"), dev(p, "la"))
+    lam = torch.ones(B, H, T, lla.num_levels(T), device="cuda")
+    a = lla.linear_forward(dev(p, "q"), dev(p, "k"), dev(p, "v"), la)
+    b = lla.forward(dev(p, "q"), dev(p, "k"), dev(p, "v"), la[None, :, None].expand(B, H, T).contiguous(), lam, 64)
+    assert float((a - b).abs().max() / a.abs().max()) <= 1e-4  # the hierarchy's own bar for fp32
+
+
+@pytest.mark.parametrize("dtype,dk", [("bf16", 64), ("f32", 30)])
+def test_calls_repeat_to_the_bit(lla, dtype, dk):
+    p = problem(2, 3, 400, dk, 64, dtype, 1, seed=13)
+    names = ("q", "k", "v", "la")
+    run = lambda: [lla.linear_forward(*(dev(p, n) for n in names), state0=dev(p, "s0"))] + list(  # noqa: E731
+        lla.linear_backward(*(dev(p, n) for n in names), dev(p, "dout"), state0=dev(p, "s0"), dstate_out=dev(p, "ds")))
+    first = run()
+    for _ in range(3):
+        for a, b in zip(first, run()):
+            assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("dtype,dk", [("bf16", 64), ("f32", 30)])
+def test_graphs_and_streams(lla, dtype, dk):
+    """Two captured graphs (prompt, gradients, packed prompt, token) replayed at the same time on two streams, new
+    inputs copied in between replays; and a call on a stream of its own."""
+    lengths = [100, 0, 260]
+    work = []
+    for seed in (20, 21):
+        p = problem(2, 3, 300, dk, 64, dtype, 1, seed=seed)
+        pk, cu = pack(lengths, 3, dk, 64, dtype, 0, 5, seed=seed)
+        work.append(dict(p=p, pk=pk, cu=torch.from_numpy(cu).cuda(), s1=torch.zeros(2, 3, dk, 64, device="cuda"),
+                         st=torch.zeros(2, 3, dk, 64, device="cuda")))
+
+    def calls(w):
+        p, pk = w["p"], w["pk"]
+        o = lla.linear_forward(dev(p, "q"), dev(p, "k"), dev(p, "v"), dev(p, "la"), state0=dev(p, "s0"),
+                               state_out=w["s1"])
+        g = lla.linear_backward(dev(p, "q"), dev(p, "k"), dev(p, "v"), dev(p, "la"), dev(p, "dout"),
+                                state0=dev(p, "s0"), dstate_out=dev(p, "ds"))
+        out = torch.zeros(3, sum(lengths) + 5, 64, device="cuda", dtype=o.dtype)
+        u = lla.linear_forward_varlen(dev(pk, "q"), dev(pk, "k"), dev(pk, "v"), dev(pk, "la"), w["cu"], 260, out=out)
+        w["st"].copy_(w["s1"])
+        d = lla.linear_decode_step(*(dev(p, n)[:, :, 0].contiguous() for n in ("q", "k", "v")), dev(p, "la"), w["st"])
+        return [o, *g, u, d, w["s1"], w["st"]]
+
+    want = [[x.clone() for x in calls(w)] for w in work]
+    graphs, outs = [], []
+    for w in work:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(calls(w))
+        graphs.append(g)
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    for _ in range(4):
+        for g, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+    torch.cuda.synchronize()
+    for o, r in zip(outs, want):
+        for a, b in zip(o, r):
+            assert torch.equal(a, b)
+    # new inputs in the captured buffers
+    for n in ("q", "k", "v"):
+        work[0]["p"][n][1].copy_(work[1]["p"][n][1])
+    graphs[0].replay()
+    torch.cuda.synchronize()
+    again = calls(work[0])
+    torch.cuda.synchronize()
+    for a, b in zip(outs[0], again):
+        assert torch.equal(a, b)
+    # a stream of its own, given to the call
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    p = work[1]["p"]
+    o = lla.linear_forward(dev(p, "q"), dev(p, "k"), dev(p, "v"), dev(p, "la"), state0=dev(p, "s0"), stream=side)
+    side.synchronize()
+    assert torch.equal(o, want[1][0])
+
+
+def test_serving_and_training_run(lla):
+    """As the operators are used together: a common prefix once, packed turns that go on from its state, single
+    tokens after them, then a training step of the same rows from the shared state."""
+    H, dk, dv, P = 4, 64, 64, 200
+    lengths = [30, 0, 150]
+    pre = problem(1, H, P, dk, dv, "bf16", 0, seed=30)
+    la = dev(pre, "la")
+    shared = torch.empty(1, H, dk, dv, device="cuda")
+    lla.linear_forward(dev(pre, "q"), dev(pre, "k"), dev(pre, "v"), la, state_out=shared)
+    pk, cu = pack(lengths, H, dk, dv, "bf16", 0, 0, seed=31)
+    states = torch.empty(3, H, dk, dv, device="cuda")
+    out = lla.linear_forward_varlen(dev(pk, "q"), dev(pk, "k"), dev(pk, "v"), la, torch.from_numpy(cu).cuda(), 150,
+                                    state0=shared, state_out=states)
+    tok = problem(3, H, 1, dk, dv, "bf16", 0, seed=32)
+    last = lla.linear_decode_step(*(dev(tok, n)[:, :, 0].contiguous() for n in ("q", "k", "v")), la, states)
+    for b, n in enumerate(lengths):
+        rows = slice(cu[b], cu[b + 1])
+        x = [np.concatenate([val(pre, m)[0], val(pk, m)[:, rows], val(tok, m)[b]], 1)[None] for m in ("q", "k", "v")]
+        ref, ref_s = L.forward(*x, val(pre, "la"))
+        size, size_s = L.forward(*sizes(*x), val(pre, "la"))
+        whole = np.concatenate([host(out)[:, rows], host(last)[b][:, None]], 1)[None]
+        L.check(whole, ref[:, :, P:], size[:, :, P:], "bf16", P + n + dk, b)
+        L.check(host(states)[None, b], ref_s, size_s, "f32", P + n, b)
+    # the whole of it as one training sequence equals the prefix with the turn's gradient handed back
+    b, n = 2, 150
+    turn = {m: dev(pk, m)[None, :, cu[b]:cu[b + 1]].contiguous() for m in ("q", "k", "v")}
+    do = torch.randn(1, H, n, dv, device="cuda").bfloat16()
+    g2 = lla.linear_backward(*turn.values(), la, do, state0=shared)
+    zero = torch.zeros(1, H, P, dv, device="cuda", dtype=torch.bfloat16)
+    g1 = lla.linear_backward(dev(pre, "q"), dev(pre, "k"), dev(pre, "v"), la, zero, dstate_out=g2[3])
+    x = [np.concatenate([val(pre, m)[0], val(pk, m)[:, cu[b]:cu[b + 1]]], 1)[None] for m in ("q", "k", "v")]
+    d = np.concatenate([host(zero), host(do)], 2)
+    ref, size = L.backward(*x, val(pre, "la"), d), L.backward(*sizes(*x), val(pre, "la"), np.abs(d))
+    for i in range(3):
+        L.check(host(torch.cat([g1[i], g2[i]], 2)), ref[i], size[i], "bf16", P + n + dk, i)
+
+
+def test_binding_refuses(lla):
+    p = problem(2, 3, 20, 16, 16, "f32", 1)
+    q, k, v, la, s0 = (dev(p, n) for n in ("q", "k", "v", "la", "s0"))
+    for bad in (dict(la=la[:2].contiguous()), dict(la=la.double()), dict(k=k.bfloat16()), dict(k=k[:, :, :10].contiguous()),
+                dict(v=v[:, :, :10].contiguous()), dict(q=q.transpose(1, 2)), dict(s0=s0.double()),
+                dict(s0=torch.cat([s0] * 3)), dict(s0=s0[..., :8].contiguous()), dict(s0=s0.cpu())):
+        a = {"q": q, "k": k, "v": v, "la": la, "s0": s0, **bad}
+        with pytest.raises((ValueError, TypeError)):
+            lla.linear_forward(a["q"], a["k"], a["v"], a["la"], state0=a["s0"])
+    state = s0.expand(2, -1, -1, -1).contiguous()
+    with pytest.raises(lla.LLAError):
+        lla.linear_forward(q, k, v, la, state0=state, state_out=state)
+    with pytest.raises(ValueError):
+        lla.linear_forward(q, k, v, la, out=torch.empty(2, 3, 20, 8, device="cuda"))
+    with pytest.raises(TypeError):
+        lla.linear_forward(q.half(), k.half(), v.half(), la)
+    with pytest.raises(ValueError):
+        lla.linear_decode_step(q[:, :, 0].contiguous(), k[:, :, 0].contiguous(), v[:, :, 0].contiguous(), la, s0)
+    with pytest.raises(TypeError):
+        lla.linear_forward_varlen(q[0], k[0], v[0], la, torch.zeros(2, dtype=torch.int64, device="cuda"), 20)

@@ -1,0 +1,225 @@
+"""GPU checks of the decode step over a shared prefix: against the pair sums of the log-linear operator in 64
+bits, step by step from the end of the prefix, and against lla_decode_step on the whole states."""
+import numpy as np
+import pytest
+
+from tests import _linear as L
+
+torch = pytest.importorskip("torch")
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _cuda():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+
+
+@pytest.fixture()
+def lla():
+    from log_linear_attention_gb300 import binding
+    yield binding
+    assert binding.device_error() == 0
+
+
+def level(t, s):
+    return int(t ^ s).bit_length()
+
+
+def row(q, k, v, log_a, lam, t, absolute=False):
+    """o_t [H, dv] of the pair sum over s <= t: k [H, T, dk], v [H, T, dv], log_a [H, T], q [H, dk], lam [H, Lmax]."""
+    s = np.arange(t + 1)
+    cum = np.cumsum(log_a, 1)
+    w = np.exp(cum[:, t, None] - cum[:, :t + 1]) * lam[:, [level(t, x) for x in s]]
+    if absolute:
+        return np.einsum("hs,hsd,hd,hsv->hv", w, np.abs(k[:, :t + 1]), np.abs(q), np.abs(v[:, :t + 1]))
+    return np.einsum("hs,hs,hsv->hv", w, np.einsum("hsd,hd->hs", k[:, :t + 1], q), v[:, :t + 1])
+
+
+def softplus(x):
+    return np.logaddexp(0, x)
+
+
+def build(lla, P, B, H, dk, dv, dtype, steps, Lmax, seed):
+    """A prefix, `steps` own tokens of every sequence, and the prefix's states."""
+    r = np.random.default_rng(seed)
+    d = {"pk": L.make(r, (1, H, P, dk), dtype, dk ** -0.5), "pv": L.make(r, (1, H, P, dv), dtype),
+         "pa": L.make(r, (1, H, P), "f32")}
+    for n, w, sc in (("q", dk, dk ** -0.5), ("k", dk, dk ** -0.5), ("v", dv, 1.0)):
+        d[n] = L.make(r, (B, steps, H, w), dtype, sc)
+    for n, shape in (("pa", (1, H, P)), ("a", (B, steps, H))):
+        x = -softplus(r.standard_normal(shape) - 2).astype(np.float32)
+        d[n] = x.astype(np.float64), torch.from_numpy(x)
+    x = softplus(r.standard_normal((B, steps, H, Lmax))).astype(np.float32)
+    d["lam"] = x.astype(np.float64), torch.from_numpy(x)
+    d = {n: (a, t.cuda()) for n, (a, t) in d.items()}
+    Lp = lla.num_levels(P) + (seed & 1)
+    prefix = torch.full((1, H, Lp, dk, dv), float("nan"), device="cuda")
+    lla.prefill_state(d["pk"][1], d["pv"][1], d["pa"][1], prefix)
+    return d, prefix[0]
+
+
+def step_args(d, i, t):
+    """Inputs of every sequence's own token i."""
+    return [d[n][1][:, i].clone() for n in ("q", "k", "v", "a", "lam")], t
+
+
+@pytest.mark.parametrize("P,B,H,dk,dv,dtype,steps", [
+    (1, 2, 2, 16, 16, "f32", 20), (2, 1, 1, 20, 32, "f32", 10), (3, 3, 2, 32, 64, "bf16", 14),
+    (8, 2, 2, 64, 16, "f32", 17), (63, 2, 2, 128, 64, "bf16", 5), (64, 9, 3, 128, 64, "bf16", 5),
+    (65, 2, 2, 100, 128, "f32", 70), (127, 17, 2, 64, 64, "f32", 4), (300, 2, 2, 256, 32, "f32", 30),
+    (511, 2, 1, 128, 128, "bf16", 6),
+])
+def test_steps_from_the_prefix(lla, P, B, H, dk, dv, dtype, steps):
+    Lmax = lla.num_levels(P + steps) + 1
+    if dk > 128:  # the prefill takes 128: two halves of the keys, side by side
+        a, pa = build(lla, P, B, H, dk // 2, dv, dtype, steps, Lmax, seed=P)
+        b, pb = build(lla, P, B, H, dk // 2, dv, dtype, steps, Lmax, seed=P + 2)
+        d = dict(a)
+        for n in ("pk", "q", "k"):
+            d[n] = np.concatenate([a[n][0], b[n][0]], -1), torch.cat([a[n][1], b[n][1]], -1)
+        lla.prefill_state(b["pk"][1], a["pv"][1], a["pa"][1], pb[None])
+        prefix = torch.cat([pa, pb], 2).contiguous()
+    else:
+        d, prefix = build(lla, P, B, H, dk, dv, dtype, steps, Lmax, seed=P)
+    kept = prefix.clone()
+    states = torch.full((B, H, Lmax, dk, dv), float("nan"), device="cuda")
+    decay = torch.full((B, H), float("nan"), device="cuda")
+    for i in range(steps):
+        t = torch.full((B,), P + i, dtype=torch.int64, device="cuda")
+        args, _ = step_args(d, i, t)
+        out = lla.decode_step_shared(*args[:4], args[4], prefix, P, decay, states, t)
+        got = out.double().cpu().numpy()
+        for b in range(B):
+            k = np.concatenate([d["pk"][0][0], d["k"][0][b, :i + 1].transpose(1, 0, 2)], 1)
+            v = np.concatenate([d["pv"][0][0], d["v"][0][b, :i + 1].transpose(1, 0, 2)], 1)
+            a = np.concatenate([d["pa"][0][0], d["a"][0][b, :i + 1].T], 1)
+            q, lam = d["q"][0][b, i], d["lam"][0][b, i]
+            ref, size = row(q, k, v, a, lam, P + i), row(q, k, v, a, lam, P + i, absolute=True)
+            # fp32 sums of P + i + dk terms and a decay of a sum of as many logs, whose rounding of 2^-24 of up to
+            # sum |log a| enters every term; prefill_state itself keeps 16 bits of bf16 values' products
+            logs = np.abs(a).sum(1)[:, None]
+            tol = ((P + i + dk + 16) * 2 * L.U32 + (i + 2) * L.U32 * logs) * size
+            if dtype == "bf16":
+                tol = tol + L.UBF * np.abs(ref) + 2.0 ** -16 * size
+            assert (np.abs(got[b] - ref) <= tol).all(), (i, b, np.max(np.abs(got[b] - ref) / tol))
+    assert torch.equal(prefix.nan_to_num(9.0), kept.nan_to_num(9.0))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_equals_decode_step_on_whole_states(lla, dtype):
+    """Sequences at different positions, from the prefix's end to far behind it; a whole-state batch beside it."""
+    P, B, H, dk, dv, Lmax = 1000, 6, 2, 128, 64, 14
+    n = [0, 1, 23, 24, 25, 400]
+    r = np.random.default_rng(5)
+    d, prefix = build(lla, P, B, H, dk, dv, dtype, 1, Lmax, seed=7)
+    whole = torch.zeros(B, H, Lmax, dk, dv, device="cuda")
+    whole[:, :, :prefix.shape[1]] = prefix.nan_to_num(0.0)
+    states = torch.full((B, H, Lmax, dk, dv), float("nan"), device="cuda")
+    decay = torch.full((B, H), float("nan"), device="cuda")
+    for i in range(max(n) + 1):
+        live = [b for b in range(B) if n[b] >= i]
+        x = torch.tensor(live, device="cuda")
+        tok = [L.make(r, (len(live), H, w), dtype, w ** -0.5)[1].cuda() for w in (dk, dk, dv)]
+        a = torch.from_numpy(-softplus(r.standard_normal((len(live), H)) - 2).astype(np.float32)).cuda()
+        lam = torch.from_numpy(softplus(r.standard_normal((len(live), H, Lmax))).astype(np.float32)).cuda()
+        t = torch.full((len(live),), P + i, dtype=torch.int64, device="cuda")
+        w, s, D = whole[x], states[x], decay[x]
+        ref = lla.decode_step(*tok, a, lam, w, t)
+        got = lla.decode_step_shared(*tok, a, lam, prefix, P, D, s, t)
+        whole[x], states[x], decay[x] = w, s, D
+        # both are fp32 sums of the same terms in other orders, rounded once: one step of bf16 apart at most; fp32:
+        # some 1400 roundings of 2^-24, on values of at most the sum of sizes, about 30 times the largest
+        scale = ref.float().abs().max()
+        tol = 2 * L.UBF if dtype == "bf16" else 1400 * 30 * L.U32
+        assert float((got.float() - ref.float()).abs().max() / scale) <= tol
+
+
+def test_positions_outside_are_skipped():
+    from log_linear_attention_gb300 import binding as lla
+    P, B, H, dk, dv, Lmax = 10, 4, 2, 32, 16, 6
+    d, prefix = build(lla, P, B, H, dk, dv, "f32", 1, Lmax, seed=1)
+    states = torch.randn(B, H, Lmax, dk, dv, device="cuda")
+    decay = torch.zeros(B, H, device="cuda")
+    kept = states.clone()
+    out = torch.full((B, H, dv), 5.0, device="cuda")
+    t = torch.tensor([9, 32, -1, 10], dtype=torch.int64, device="cuda")
+    args, _ = step_args(d, 0, t)
+    lla.decode_step_shared(*args[:4], args[4], prefix, P, decay, states, t, out=out)
+    assert lla.device_error() == lla.LLA_ERR_DEVICE
+    assert torch.equal(states[:3], kept[:3]) and (out[:3] == 5.0).all() and (decay[:3] == 0).all()
+    assert not torch.equal(states[3], kept[3]) and not (out[3] == 5.0).any()
+    # slots that hold nothing own after t = 10 are left as they were
+    assert torch.equal(states[3, :, 1:], kept[3, :, 1:])
+
+
+def test_own_prompt_behind_an_aligned_prefix(lla):
+    """P a multiple of 64: the states of a prompt of up to 64 own tokens come from prefill_state."""
+    P, B, H, dk, dv, n = 192, 2, 2, 128, 64, 50
+    Lmax = lla.num_levels(P + n) + 1
+    d, prefix = build(lla, P, B, H, dk, dv, "f32", n + 1, Lmax, seed=3)
+    a = torch.full((B, H, Lmax, dk, dv), float("nan"), device="cuda")
+    own = [d[m][1][:, :n].transpose(1, 2).contiguous() for m in ("k", "v", "a")]
+    lla.prefill_state(*own, a)
+    Da = own[2].sum(-1).contiguous()
+    b, Db = torch.full_like(a, float("nan")), torch.full((B, H), float("nan"), device="cuda")
+    for i in range(n):
+        args, t = step_args(d, i, torch.full((B,), P + i, dtype=torch.int64, device="cuda"))
+        lla.decode_step_shared(*args[:4], args[4], prefix, P, Db, b, t)
+    args, t = step_args(d, n, torch.full((B,), P + n, dtype=torch.int64, device="cuda"))
+    x = lla.decode_step_shared(*args[:4], args[4], prefix, P, Da, a, t)
+    y = lla.decode_step_shared(*args[:4], args[4], prefix, P, Db, b, t)
+    assert float((x - y).abs().max() / x.abs().max()) <= 1e-4  # the hand-off's own bar for fp32
+
+
+def test_graph_replay(lla):
+    """A captured step, replayed with t advanced on the device, equals the eager steps; two graphs at once."""
+    P, B, H, dk, dv, Lmax, steps = 100, 3, 2, 64, 64, 9, 6
+    sets = []
+    for seed in (1, 2):
+        d, prefix = build(lla, P, B, H, dk, dv, "bf16", steps, Lmax, seed=seed)
+        sets.append(dict(d=d, prefix=prefix, states=torch.zeros(B, H, Lmax, dk, dv, device="cuda"),
+                         decay=torch.zeros(B, H, device="cuda"), t=torch.full((B,), P, dtype=torch.int64, device="cuda"),
+                         args=[d[n][1][:, 0].clone() for n in ("q", "k", "v", "a", "lam")]))
+
+    def one(s):
+        o = lla.decode_step_shared(*s["args"], s["prefix"], P, s["decay"], s["states"], s["t"])
+        s["t"] += 1
+        return o
+
+    def reset(s):
+        s["t"].fill_(P)
+        s["states"].zero_()
+        s["decay"].zero_()
+
+    def load(s, i):
+        for x, n in zip(s["args"], ("q", "k", "v", "a", "lam")):
+            x.copy_(s["d"][n][1][:, i])
+
+    want = []
+    for s in sets:
+        rows = []
+        for i in range(steps):
+            load(s, i)
+            rows.append(one(s).clone())
+        want.append(rows)
+        reset(s)
+    graphs, outs = [], []
+    for s in sets:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(one(s))
+        graphs.append(g)
+        reset(s)
+    streams = [torch.cuda.Stream() for _ in sets]
+    for i in range(steps):
+        for s in sets:
+            load(s, i)
+        torch.cuda.synchronize()
+        for g, st in zip(graphs, streams):
+            with torch.cuda.stream(st):
+                g.replay()
+        torch.cuda.synchronize()
+        for o, w in zip(outs, want):
+            assert torch.equal(o, w[i])
