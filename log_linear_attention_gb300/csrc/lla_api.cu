@@ -695,8 +695,17 @@ int lla_linear_forward(const void* q, const void* k, const void* v, const float*
     const int dev = current_device();
     if (dev < 0) return LLA_ERR_CUDA;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
+    int* err = error_word(dev);
+    if (!err) return LLA_ERR_CUDA;
     const lla::LinSeqs sq = dense_seqs(B, H, T);
     PoolBuffer ws(s);
+    lla::LinTcPlan tp;
+    if (lla::linear_tc_supported(dtype, dk, dv) && lla::linear_tc_plan(&tp, B, H, T, (int64_t)B * H * T, pieces64(dv))) {
+        if ((st = ws.take(dev, tp.seg_bytes)) != LLA_OK) return st;
+        const lla::LinTcMap maps[3] = {{q, dk}, {k, dk}, {v, dv}};
+        const lla::LinTcScan scan = {0, 1, 2, out, state0, state_out, B0 == 1, 0, 0, dk, dv, 0, 0};
+        return ws.give(lla::linear_tc_run(tp, maps, 3, &scan, 1, sq, log_a, reinterpret_cast<float*>(ws.p), err, s));
+    }
     if ((st = ws.take(dev, (size_t)H * sq.n_chunks * msz)) != LLA_OK) return st;
     float* states = reinterpret_cast<float*>(ws.p);
     lla::LinStateJobs jobs = {{{k, v, states, state0, state_out, B0 == 1, 0, dk, dv, pieces64(dk) * pieces64(dv)}}, 1};
@@ -726,6 +735,24 @@ int lla_linear_forward_varlen(const void* q, const void* k, const void* v, const
     sq.n_chunks = total_T / 64 + n_seq;
     const size_t tab_b = up256((size_t)n_seq * sizeof(int2)), off_b = up256(((size_t)n_seq + 1) * sizeof(int));
     PoolBuffer ws(s);
+    lla::LinTcPlan tp;
+    if (lla::linear_tc_supported(dtype, dk, dv) &&
+        lla::linear_tc_plan(&tp, n_seq, H, max_T, (int64_t)H * total_T, pieces64(dv))) {
+        if ((st = ws.take(dev, tab_b + 2 * off_b + tp.seg_bytes)) != LLA_OK) return st;
+        int2* tab = reinterpret_cast<int2*>(ws.p);
+        int* coff = reinterpret_cast<int*>(ws.p + tab_b);
+        int* order = reinterpret_cast<int*>(ws.p + tab_b + off_b);
+        sq.tab = tab;
+        sq.coff = coff;
+        sq.order = order;
+        cudaError_t e = lla::linear_table(cu_seqlens, n_seq, total_T, max_T, tab, coff, order, err, s);
+        const lla::LinTcMap maps[3] = {{q, dk}, {k, dk}, {v, dv}};
+        const lla::LinTcScan scan = {0, 1, 2, out, state0, state_out, n0 == 1, 0, 0, dk, dv, 0, 0};
+        if (e == cudaSuccess)
+            e = lla::linear_tc_run(tp, maps, 3, &scan, 1, sq, log_a,
+                                   reinterpret_cast<float*>(ws.p + tab_b + 2 * off_b), err, s);
+        return ws.give(e);
+    }
     if ((st = ws.take(dev, tab_b + off_b + (size_t)H * sq.n_chunks * msz)) != LLA_OK) return st;
     int2* tab = reinterpret_cast<int2*>(ws.p);
     int* coff = reinterpret_cast<int*>(ws.p + tab_b);
@@ -753,9 +780,27 @@ int lla_linear_backward(const void* q, const void* k, const void* v, const float
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const lla::LinSeqs sq = dense_seqs(B, H, T);
     const size_t msz = (size_t)dk_ * dv_ * sizeof(float);
-    const size_t st_b = up256((size_t)H * sq.n_chunks * msz);
+    int* err = error_word(dev);
+    if (!err) return LLA_ERR_CUDA;
     const bool sum = dstate0 && B0 == 1 && B > 1;  // gradients of one shared state: a part per sequence, then their sum
+    const size_t sum_b = sum ? up256((size_t)B * H * msz) : 0;
     PoolBuffer ws(s);
+    lla::LinTcPlan tp;
+    if (lla::linear_tc_supported(dtype, dk_, dv_) &&
+        lla::linear_tc_plan(&tp, B, H, T, (int64_t)B * H * T, 2 * pieces64(dk_) + pieces64(dv_))) {
+        if ((st = ws.take(dev, sum_b + tp.seg_bytes)) != LLA_OK) return st;
+        float* parts = reinterpret_cast<float*>(ws.p);
+        const lla::LinTcMap maps[4] = {{q, dk_}, {k, dk_}, {v, dv_}, {dout, dv_}};
+        const lla::LinTcScan scans[3] = {
+            {3, 2, 1, dq, state0, nullptr, B0 == 1, 1, 0, dv_, dk_, 0, 0},
+            {2, 3, 0, dk, dstate_out, nullptr, 0, 1, 1, dv_, dk_, 0, 0},
+            {1, 0, 3, dv, dstate_out, sum ? parts : dstate0, 0, 0, 1, dk_, dv_, 0, 0}};
+        cudaError_t e = lla::linear_tc_run(tp, maps, 4, scans, 3, sq, log_a, reinterpret_cast<float*>(ws.p + sum_b),
+                                           err, s);
+        if (e == cudaSuccess && sum) e = lla::linear_sum_batch(parts, dstate0, B, (int64_t)H * dk_ * dv_, s);
+        return ws.give(e);
+    }
+    const size_t st_b = up256((size_t)H * sq.n_chunks * msz);
     if ((st = ws.take(dev, 2 * st_b + (sum ? (size_t)B * H * msz : 0))) != LLA_OK) return st;
     float* fw = reinterpret_cast<float*>(ws.p);
     float* bw = reinterpret_cast<float*>(ws.p + st_b);

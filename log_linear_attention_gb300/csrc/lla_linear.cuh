@@ -53,6 +53,30 @@ cudaError_t linear_sum_batch(const float* src, float* dst, int B, int64_t size, 
 cudaError_t linear_decode_step(int dtype, const void* q, const void* k, const void* v, const float* log_a,
                                float* state, void* out, int B, int H, int dk, int dv, cudaStream_t stream);
 
+// Tensor-core path (lla_linear_tc.cu): bf16, dk and dv multiples of 8. A scan names its row tensors
+// by their index among the call's tensor maps.
+struct LinTcMap {
+    const void* base;
+    int cols;
+};
+struct LinTcScan {
+    int ia, ib, ic;
+    void* out;
+    const float* in;  // entering state [batch or 1][H], each [d1][d2] (in_t: [d2][d1]), or null for zeros
+    float* leave;     // leaving state [batch][H][d1][d2], or null
+    int in_shared, in_t, reverse, d1, d2;
+    int tiles, seg_base;  // filled by linear_tc_run
+};
+struct LinTcPlan {
+    int batch, nseg, seg_chunks;  // segments of a sequence, 128-token chunks of a segment
+    size_t seg_bytes;
+};
+bool linear_tc_supported(int dtype, int dk, int dv);
+// rows: token rows of the call; tiles: 64-column tiles over all scans of one head
+bool linear_tc_plan(LinTcPlan* plan, int batch, int H, int T, int64_t rows, int tiles);
+cudaError_t linear_tc_run(const LinTcPlan& plan, const LinTcMap* maps, int n_maps, const LinTcScan* scans, int count,
+                          const LinSeqs& sq, const float* log_a, float* seg, int* err, cudaStream_t stream);
+
 size_t shared_workspace_bytes(int B, int H, int dv, int64_t prefix_len);
 cudaError_t decode_step_shared(int dtype, const void* q, const void* k, const void* v, const float* log_a,
                                const float* lambda, const float* prefix_states, int64_t prefix_len, int Lp,
