@@ -7,7 +7,7 @@
 //     own     B^T [hi | mid | lo]        [d1 x 192]   -> TMEM, w o C split into three bf16 parts, so that
 //                                                     the state keeps the 24 bits of fp32
 //     far     A X                        [128 x 64]   X = entering state, rounded to bf16
-//     near    P C                        [128 x 64]   P = scores o g^|i-j|, bf16, read from TMEM
+//     near    P C                        [128 x 64]   P = scores o g^|i-j|, bf16, in TMEM
 //     out_i = near_i + f_i far_i,   X <- g^n X + own
 // with w_i = g^(n-1-i), f_i = g^(i+1) forwards and w_i = g^(i+1), f_i = g^(n-1-i) backwards. P and X are
 // rounded to bf16 as the operands of a bf16 product must be (2^-8 of each term, as the output itself);
@@ -28,7 +28,7 @@
 namespace lla {
 namespace {
 
-constexpr int kScanThreads = 512;
+constexpr int kScanThreads = 1024;
 constexpr int kMaxStages = 3;
 constexpr int kDepth = 64;  // columns of c per CTA
 constexpr int kWcBytes = 3 * kPanelBytes;
@@ -37,7 +37,7 @@ constexpr int kSmemMost = 232448 - 2048;  // 227 KB less the static part
 // TMEM columns
 constexpr uint32_t kColS = 0, kColP = 128, kColNear = 192, kColFar = 256, kColOwn = 320;
 
-struct alignas(64) ScanParams {
+struct ScanParams {
     CUtensorMap map[4];
     LinTcScan scan[3];
     const float* log_a;
@@ -77,8 +77,76 @@ __device__ __forceinline__ void tmem_st16_issue(uint32_t taddr, const uint32_t* 
 }
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-// Warps: 0 TMA producer, 1 TMEM owner and MMA issuer, 4..7 P, 8..11 state, 12..15 scale c and write out.
-// Warp w reaches TMEM lanes 32 (w % 4)..+31: rows of scores and out, rows of the state.
+// Two fp32 values in one register pair: one instruction for both (issue slots are what the roles share).
+using f32x2 = unsigned long long;
+__device__ __forceinline__ f32x2 pair2(float lo, float hi) {
+    f32x2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ float2 split2(f32x2 x) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(x));
+    return r;
+}
+__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
+    f32x2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
+    f32x2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint32_t pack_bf16(f32x2 x) {
+    const float2 f = split2(x);
+    return pack_bf16(f.x, f.y);
+}
+
+// 16 or 32 consecutive fp32 TMEM columns of this warp's lanes as pairs.
+__device__ __forceinline__ void tmem_ld16x2(uint32_t taddr, f32x2* v) {
+    uint32_t r[16];
+    tmem_ld16_issue(taddr, r);
+    tmem_ld16_wait(r);
+#pragma unroll
+    for (int i = 0; i < 8; i++) v[i] = pair2(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1]));
+}
+
+// One lane of a converged warp; code behind it counts as uniform, so descriptors stay in uniform registers.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p != 0;
+}
+
+// Bounded waits. The phase is mostly complete already: one inline test, and a call only where it is not (a call a
+// wait cost the issuing thread some 250 cycles). They give up when another role has.
+__device__ __noinline__ bool wait_long(uint64_t* bar, uint32_t parity, volatile int* fail) {
+    const long long start = clock64();
+    while (!mbar_try_wait(bar, parity)) {
+        if (*fail || clock64() - start > kWaitCycles) return false;
+    }
+    return true;
+}
+__device__ __forceinline__ bool wait_one(uint64_t* bar, uint32_t parity, volatile int* fail) {
+    return mbar_try_wait(bar, parity) || wait_long(bar, parity, fail);
+}
+__device__ __noinline__ bool wait_long_warp(uint64_t* bar, uint32_t parity, volatile int* fail) {
+    const long long start = clock64();
+    while (true) {
+        const bool done = mbar_try_wait(bar, parity);
+        if (__all_sync(0xffffffffu, done)) return true;
+        const bool late = *fail || clock64() - start > kWaitCycles;
+        if (__any_sync(0xffffffffu, late)) return false;
+    }
+}
+__device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, volatile int* fail) {
+    return __all_sync(0xffffffffu, mbar_try_wait(bar, parity)) || wait_long_warp(bar, parity, fail);
+}
+
+// Warps: 0 TMA producer, 1 TMEM owner and MMA issuer, 4..11 P (every other block of 32 keys), 12..19 state
+// (32 columns each), 20..23 write out, 24..31 split w o C. Warp w reaches TMEM lanes 32 (w % 4)..+31: rows of scores and out, rows of the state.
 template <bool kStateOnly>
 __global__ void __launch_bounds__(kScanThreads, 1) linear_scan_kernel(const __grid_constant__ ScanParams pr, int* err) {
     extern __shared__ uint8_t smem_raw[];
@@ -88,7 +156,7 @@ __global__ void __launch_bounds__(kScanThreads, 1) linear_scan_kernel(const __gr
     __shared__ uint32_t tmem_base_sh;
     __shared__ int fail_sh;
     __shared__ float pw[132];    // g^n
-    __shared__ float colw[32];   // weight of key c of an off-diagonal 32-key block
+    __shared__ __align__(16) float colw[32];  // weight of key c of an off-diagonal 32-key block
     __shared__ float diag[64];   // weight of key c for row r of a diagonal block, at 31 + r - c
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -141,13 +209,13 @@ __global__ void __launch_bounds__(kScanThreads, 1) linear_scan_kernel(const __gr
             mbar_init(&qk_free[s], 1);
             mbar_init(&v_free[s], 1);
         }
-        mbar_init(&scaled, 4);
+        mbar_init(&scaled, 8);
         mbar_init(&own_full, 1);
-        mbar_init(&own_read, 4);
-        mbar_init(&x_ready, 4);
+        mbar_init(&own_read, 8);
+        mbar_init(&x_ready, 8);
         mbar_init(&x_free, 1);
         mbar_init(&s_full, 1);
-        mbar_init(&p_ready, 4);
+        mbar_init(&p_ready, 8);
         mbar_init(&o_full, 1);
         mbar_init(&o_read, 4);
         mbar_init(&drain, 1);
@@ -169,14 +237,15 @@ __global__ void __launch_bounds__(kScanThreads, 1) linear_scan_kernel(const __gr
     auto fail_now = [&]() {
         if (atomicExch(&fail_sh, 1) == 0) record_error(err, kDevTimeout);
     };
-    int sent_qk = 0, sent_v = 0;  // producer: copies issued
 
     if (warp == 0) {
-        if (lane == 0) {
-            for (int j = 0; j < n && !*fail; j++) {
-                const int s = j % nst, t0 = row0 + chunk_of(j) * kTile;
-                uint8_t* st = smem + s * stage_bytes;
-                if (j >= nst && !mbar_wait(&qk_free[s], (j / nst - 1) & 1)) {
+        if (elect_one()) {
+            int s = 0, sent_qk = 0, sent_v = 0, t0 = row0 + chunk_of(0) * kTile;
+            const int dt = rev ? -kTile : kTile;
+            uint32_t ph = 1;
+            uint8_t* st = smem;
+            for (int j = 0; j < n; j++, t0 += dt) {
+                if (j >= nst && !wait_one(&qk_free[s], ph, fail)) {
                     fail_now();
                     break;
                 }
@@ -186,128 +255,157 @@ __global__ void __launch_bounds__(kScanThreads, 1) linear_scan_kernel(const __gr
                     tma_load_3d(st + k_off + p * kPanelBytes, &pr.map[sc.ib], &qk_full[s], 64 * p, t0, z);
                 }
                 sent_qk++;
-                if (j >= nst && !mbar_wait(&v_free[s], (j / nst - 1) & 1)) {
+                if (j >= nst && !wait_one(&v_free[s], ph, fail)) {
                     fail_now();
                     break;
                 }
                 mbar_expect_tx(&v_full[s], kPanelBytes);
                 tma_load_3d(st + v_off, &pr.map[sc.ic], &v_full[s], c0, t0, z);
                 sent_v++;
+                st += stage_bytes;
+                if (++s == nst) {
+                    s = 0;
+                    st = smem;
+                    ph ^= 1u;
+                }
             }
+            // every copy has landed before the shared memory goes away
+            for (int i = sent_qk > nst ? sent_qk - nst : 0; i < sent_qk; i++) mbar_wait(&qk_full[i % nst], (i / nst) & 1);
+            for (int i = sent_v > nst ? sent_v - nst : 0; i < sent_v; i++) mbar_wait(&v_full[i % nst], (i / nst) & 1);
         }
     } else if (warp == 1) {
-        if (lane == 0) {
+        if (elect_one()) {
             constexpr uint32_t kIdS = idesc_bf16(kTile, kTile, 0, 0);    // A B^T, both K-major
             constexpr uint32_t kIdX = idesc_bf16(kTile, kDepth, 0, 1);   // A X and P C: B MN-major
             constexpr uint32_t kIdOwn = idesc_bf16(kTile, 3 * kDepth, 1, 1);
-            const uint32_t base = smem_u32(smem), wcb = smem_u32(wc), xb = smem_u32(xs);
-            auto scores = [&](int j) {
-                const int s = j % nst;
-                if (!mbar_wait(&qk_full[s], (j / nst) & 1)) return false;
+            // operands of the current stage and what a stage, a 16-column step of a K-major operand and a 16-row
+            // step of an MN-major one (128) add to a descriptor's address field
+            const uint64_t step = static_cast<uint64_t>(stage_bytes >> 4);
+            const uint64_t a_first = sdesc(smem_u32(smem), 16, 1024), kmaj = sdesc(0, kPanelBytes, 1024) - sdesc(0, 16, 1024);
+            const uint64_t w0 = sdesc(smem_u32(wc), kPanelBytes, 1024), x0 = sdesc(smem_u32(xs), kPanelBytes, 1024);
+            const uint64_t to_b = static_cast<uint64_t>(k_off >> 4), to_c = static_cast<uint64_t>(v_off >> 4);
+            auto kstep = [](int kk) { return static_cast<uint64_t>(((kk >> 2) * kPanelBytes + (kk & 3) * 32) >> 4); };
+            auto scores = [&](uint64_t a, uint64_t* full, uint32_t ph) {
+                if (!wait_one(full, ph, fail)) return false;
                 tc_fence_after();
-                const uint32_t qb = base + s * stage_bytes, kb = qb + k_off;
-                for (int kk = 0; kk < ksteps; kk++) {
-                    const uint32_t off = (kk >> 2) * kPanelBytes + (kk & 3) * 32;
-                    mma_bf16(tmem + kColS, sdesc(qb + off, 16, 1024), sdesc(kb + off, 16, 1024), kIdS, kk > 0);
+#pragma unroll
+                for (int kk = 0; kk < 4; kk++)
+                    if (kk < ksteps) mma_bf16(tmem + kColS, a + kstep(kk), a + to_b + kstep(kk), kIdS, kk > 0);
+                if (ksteps > 4) {
+#pragma unroll
+                    for (int kk = 4; kk < 8; kk++)
+                        if (kk < ksteps) mma_bf16(tmem + kColS, a + kstep(kk), a + to_b + kstep(kk), kIdS, 1);
                 }
                 mma_commit(&s_full);
                 return true;
             };
             bool ok = true;
-            if (!kStateOnly && n > 0) ok = scores(0);
-            for (int j = 0; j < n && ok && !*fail; j++) {
-                const int s = j % nst;
-                const uint32_t sb = base + s * stage_bytes;
-                ok = mbar_wait(&scaled, j & 1) && (!kStateOnly || mbar_wait(&qk_full[s], (j / nst) & 1)) &&
-                     (j == 0 || mbar_wait(&own_read, (j - 1) & 1));
+            int s = 0;
+            uint32_t ph = 0;       // phase of stage s
+            uint32_t par = 0;      // j & 1
+            uint64_t a = a_first;  // stage s
+            if (!kStateOnly && n > 0) ok = scores(a, &qk_full[0], 0);
+            for (int j = 0; j < n && ok; j++) {
+                ok = wait_one(&scaled, par, fail) && (!kStateOnly || wait_one(&qk_full[s], ph, fail)) &&
+                     (j == 0 || wait_one(&own_read, par ^ 1u, fail));
                 if (!ok) break;
                 tc_fence_after();
+                const uint64_t bt = a + to_b + kmaj;
 #pragma unroll
-                for (int kk = 0; kk < kTile / 16; kk++)
-                    mma_bf16(tmem + kColOwn, sdesc(sb + k_off + kk * 2048, kPanelBytes, 1024),
-                             sdesc(wcb + kk * 2048, kPanelBytes, 1024), kIdOwn, kk > 0);
+                for (int kk = 0; kk < kTile / 16; kk++) mma_bf16(tmem + kColOwn, bt + 128u * kk, w0 + 128u * kk, kIdOwn, kk > 0);
                 mma_commit(&own_full);
                 if (kStateOnly) {
                     mma_commit(&qk_free[s]);
                     mma_commit(&v_free[s]);  // the scale warps are done with c too
-                    continue;
-                }
-                ok = mbar_wait(&x_ready, j & 1) && (j == 0 || mbar_wait(&o_read, (j - 1) & 1));
-                if (!ok) break;
-                tc_fence_after();
-                for (int kk = 0; kk < ksteps; kk++) {
-                    const uint32_t off = (kk >> 2) * kPanelBytes + (kk & 3) * 32;
-                    mma_bf16(tmem + kColFar, sdesc(sb + off, 16, 1024), sdesc(xb + kk * 2048, kPanelBytes, 1024), kIdX,
-                             kk > 0);
-                }
-                mma_commit(&x_free);
-                mma_commit(&qk_free[s]);
-                // P is built: the scores' columns are free for the next chunk
-                ok = mbar_wait(&p_ready, j & 1);
-                if (!ok) break;
-                tc_fence_after();
-                if (j + 1 < n) ok = scores(j + 1);
-                if (!ok) break;
+                } else {
+                    ok = wait_one(&x_ready, par, fail) && (j == 0 || wait_one(&o_read, par ^ 1u, fail));
+                    if (!ok) break;
+                    tc_fence_after();
 #pragma unroll
-                for (int kk = 0; kk < kTile / 16; kk++)
-                    mma_bf16_ta(tmem + kColNear, tmem + kColP + kk * 8, sdesc(sb + v_off + kk * 2048, kPanelBytes, 1024),
-                                kIdX, kk > 0);
-                mma_commit(&o_full);
-                mma_commit(&v_free[s]);
+                    for (int kk = 0; kk < 8; kk++)
+                        if (kk < ksteps) mma_bf16(tmem + kColFar, a + kstep(kk), x0 + 128u * kk, kIdX, kk > 0);
+                    mma_commit(&x_free);
+                    mma_commit(&qk_free[s]);
+                    ok = wait_one(&p_ready, par, fail);
+                    if (!ok) break;
+                    tc_fence_after();
+                    // the scores are read: the next chunk's, from which the next P is built while the next own and far
+                    // products run
+                    const uint64_t ct = a + to_c + kmaj;
+                    const bool wrap = s + 1 == nst;
+                    if (j + 1 < n)
+                        ok = scores(wrap ? a_first : a + step, &qk_full[wrap ? 0 : s + 1], wrap ? ph ^ 1u : ph);
+                    if (!ok) break;
+#pragma unroll
+                    for (int kk = 0; kk < kTile / 16; kk++)
+                        mma_bf16_ta(tmem + kColNear, tmem + kColP + kk * 8, ct + 128u * kk, kIdX, kk > 0);
+                    mma_commit(&o_full);
+                    mma_commit(&v_free[s]);
+                }
+                a += step;
+                if (++s == nst) {
+                    s = 0;
+                    ph ^= 1u;
+                    a = a_first;
+                }
+                par ^= 1u;
             }
             if (!ok) fail_now();
             // every MMA issued above has completed before TMEM and shared memory go away
             mma_commit(&drain);
             if (!mbar_wait(&drain, 0)) fail_now();
         }
-    } else if (warp >= 4 && warp < 8 && !kStateOnly) {
+    } else if (warp >= 4 && warp < 12 && !kStateOnly) {
         const int w = warp & 3;
         const uint32_t lanes = tmem + (static_cast<uint32_t>(w * 32) << 16);
         for (int j = 0; j < n; j++) {
-            if (__any_sync(0xffffffffu, *fail != 0)) break;
-            if (!warp_wait(&s_full, j & 1)) {
+            if (!wait_warp(&s_full, j & 1, fail)) {
                 if (lane == 0) fail_now();
                 break;
             }
             tc_fence_after();
             bool ok = true;
 #pragma unroll 1
-            for (int cb = 0; cb < 4; cb++) {
+            for (int cb = (warp - 4) >> 2; cb < 4; cb += 2) {
                 uint32_t r[16];
                 if (rev ? cb < w : cb > w) {  // wholly on the other side of time
 #pragma unroll
                     for (int i = 0; i < 16; i++) r[i] = 0u;
                 } else {
-                    float x[32];
-                    tmem_ld32(lanes + kColS + 32 * cb, x);
                     if (cb == w) {
+                        float x[32];
+                        tmem_ld32(lanes + kColS + 32 * cb, x);
                         const float* dg = diag + 31 + lane;
 #pragma unroll
                         for (int i = 0; i < 32; i++) {
                             const float f = dg[-i];
                             x[i] = f != 0.f ? x[i] * f : 0.f;  // masked: never the product with an infinity
                         }
+#pragma unroll
+                        for (int i = 0; i < 16; i++) r[i] = pack_bf16(x[2 * i], x[2 * i + 1]);
                     } else {
                         const float rw = pw[rev ? 32 * cb - (32 * w + lane) : 32 * w + lane - 32 * cb - 31];
-                        const float4* cw = reinterpret_cast<const float4*>(colw);
+                        const f32x2 rw2 = pair2(rw, rw);
+                        const ulonglong2* cw = reinterpret_cast<const ulonglong2*>(colw);
 #pragma unroll
-                        for (int i = 0; i < 8; i++) {
-                            const float4 f = cw[i];
-                            x[4 * i] *= f.x * rw;
-                            x[4 * i + 1] *= f.y * rw;
-                            x[4 * i + 2] *= f.z * rw;
-                            x[4 * i + 3] *= f.w * rw;
+                        for (int hh = 0; hh < 2; hh++) {
+                            f32x2 x[8];
+                            tmem_ld16x2(lanes + kColS + 32 * cb + 16 * hh, x);
+#pragma unroll
+                            for (int i = 0; i < 4; i++) {
+                                const ulonglong2 f = cw[4 * hh + i];
+                                r[8 * hh + 2 * i] = pack_bf16(mul2(mul2(x[2 * i], f.x), rw2));
+                                r[8 * hh + 2 * i + 1] = pack_bf16(mul2(mul2(x[2 * i + 1], f.y), rw2));
+                            }
                         }
                     }
-#pragma unroll
-                    for (int i = 0; i < 16; i++) r[i] = pack_bf16(x[2 * i], x[2 * i + 1]);
                 }
                 // P C of the chunk before has read P
-                if (cb == 0 && j > 0 && !warp_wait(&o_full, (j - 1) & 1)) {
-                    ok = false;
-                    break;
+                if (cb < 2 && j > 0) {
+                    ok = wait_warp(&o_full, (j - 1) & 1, fail);
+                    if (!ok) break;
+                    tc_fence_after();
                 }
-                if (cb == 0) tc_fence_after();
                 tmem_st16_issue(lanes + kColP + 16 * cb, r);
             }
             if (!ok) {
@@ -319,7 +417,7 @@ __global__ void __launch_bounds__(kScanThreads, 1) linear_scan_kernel(const __gr
             __syncwarp();
             if (lane == 0) mbar_arrive(&p_ready);
         }
-    } else if (warp >= 8 && warp < 12) {
+    } else if (warp >= 12 && warp < 20) {
         const int d = (warp & 3) * 32 + lane;  // row of the state
         const uint32_t lanes = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
         const int64_t slot = (static_cast<int64_t>(sc.seg_base) + (static_cast<int64_t>(bh) * (pr.nseg - 1)) * sc.tiles) *
@@ -327,23 +425,24 @@ __global__ void __launch_bounds__(kScanThreads, 1) linear_scan_kernel(const __gr
         auto seg_at = [&](int gg) {
             return pr.seg + slot + (static_cast<int64_t>(gg) * sc.tiles + tile) * (kDepth * kTile) + d;
         };
-        float x[kDepth];
-#pragma unroll
-        for (int c = 0; c < kDepth; c++) x[c] = 0.f;
+        const int cw = (warp - 12) / 4 * 32, cg = c0 + cw;  // first of this warp's columns, in the tile and in c
+        f32x2 x2[16];  // column pairs
         if (!kStateOnly) {
+            float x[32];
+#pragma unroll
+            for (int c = 0; c < 32; c++) x[c] = 0.f;
             if (sc.in && d < d1) {
                 const float* in = sc.in + static_cast<int64_t>(sc.in_shared ? h : bh) * d1 * d2;
                 const float f = gpow(la, before(p0));
-                // rows of 4-column groups, or columns of the transpose
                 if (sc.in_t) {
 #pragma unroll
-                    for (int c = 0; c < kDepth; c++)
-                        if (c0 + c < d2) x[c] = f * in[static_cast<int64_t>(c0 + c) * d1 + d];
+                    for (int c = 0; c < 32; c++)
+                        if (cg + c < d2) x[c] = f * in[static_cast<int64_t>(cg + c) * d1 + d];
                 } else {
 #pragma unroll
-                    for (int c = 0; c < kDepth; c += 4)
-                        if (c0 + c < d2) {
-                            const float4 y = *reinterpret_cast<const float4*>(in + static_cast<int64_t>(d) * d2 + c0 + c);
+                    for (int c = 0; c < 32; c += 4)
+                        if (cg + c < d2) {
+                            const float4 y = *reinterpret_cast<const float4*>(in + static_cast<int64_t>(d) * d2 + cg + c);
                             x[c] = f * y.x;
                             x[c + 1] = f * y.y;
                             x[c + 2] = f * y.z;
@@ -355,16 +454,21 @@ __global__ void __launch_bounds__(kScanThreads, 1) linear_scan_kernel(const __gr
                 const float f = gpow(la, before(p0) - before((gg + 1) * pr.seg_chunks));
                 const float* sg = seg_at(gg);
 #pragma unroll
-                for (int c = 0; c < kDepth; c++) x[c] += f * sg[c * kTile];
+                for (int c = 0; c < 32; c++) x[c] += f * sg[(cw + c) * kTile];
             }
+#pragma unroll
+            for (int c = 0; c < 16; c++) x2[c] = pair2(x[2 * c], x[2 * c + 1]);
+        } else {
+#pragma unroll
+            for (int c = 0; c < 16; c++) x2[c] = 0ull;
         }
         auto put_x = [&]() {
             if (d < 64 * np) {
 #pragma unroll
-                for (int c = 0; c < 8; c++)
-                    *reinterpret_cast<uint4*>(xs + sw128_off(d, c)) =
-                        make_uint4(pack_bf16(x[8 * c], x[8 * c + 1]), pack_bf16(x[8 * c + 2], x[8 * c + 3]),
-                                   pack_bf16(x[8 * c + 4], x[8 * c + 5]), pack_bf16(x[8 * c + 6], x[8 * c + 7]));
+                for (int c = 0; c < 4; c++)
+                    *reinterpret_cast<uint4*>(xs + sw128_off(d, cw / 8 + c)) =
+                        make_uint4(pack_bf16(x2[4 * c]), pack_bf16(x2[4 * c + 1]), pack_bf16(x2[4 * c + 2]),
+                                   pack_bf16(x2[4 * c + 3]));
             }
             fence_async_smem();
             __syncwarp();
@@ -373,38 +477,30 @@ __global__ void __launch_bounds__(kScanThreads, 1) linear_scan_kernel(const __gr
         if (!kStateOnly && n > 0) put_x();
         bool ok = true;
         for (int j = 0; j < n; j++) {
-            if (__any_sync(0xffffffffu, *fail != 0)) {
-                ok = false;
-                break;
-            }
-            if (!warp_wait(&own_full, j & 1)) {
+            if (!wait_warp(&own_full, j & 1, fail)) {
                 if (lane == 0) fail_now();
                 ok = false;
                 break;
             }
             tc_fence_after();
             const float gn = pw[rows_of(chunk_of(j))];
+            f32x2 decay = pair2(gn, gn);
+#pragma unroll 1
+            for (int part = 2; part >= 0; part--) {  // smallest first
 #pragma unroll
-            for (int c = 0; c < kDepth; c += 16) {
-                uint32_t r[16];
-                tmem_ld16_issue(lanes + kColOwn + c, r);
-                tmem_ld16_wait(r);
+                for (int c2 = 0; c2 < 16; c2 += 8) {
+                    f32x2 y[8];
+                    tmem_ld16x2(lanes + kColOwn + part * kDepth + cw + 2 * c2, y);
 #pragma unroll
-                for (int i = 0; i < 16; i++) x[c + i] = gn * x[c + i] + __uint_as_float(r[i]);
-                tmem_ld16_issue(lanes + kColOwn + kDepth + c, r);
-                tmem_ld16_wait(r);
-#pragma unroll
-                for (int i = 0; i < 16; i++) x[c + i] += __uint_as_float(r[i]);
-                tmem_ld16_issue(lanes + kColOwn + 2 * kDepth + c, r);
-                tmem_ld16_wait(r);
-#pragma unroll
-                for (int i = 0; i < 16; i++) x[c + i] += __uint_as_float(r[i]);
+                    for (int c = 0; c < 8; c++) x2[c2 + c] = fma2(decay, x2[c2 + c], y[c]);
+                }
+                decay = pair2(1.f, 1.f);
             }
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&own_read);
             if (!kStateOnly && j + 1 < n) {
-                if (!warp_wait(&x_free, j & 1)) {
+                if (!wait_warp(&x_free, j & 1, fail)) {
                     if (lane == 0) fail_now();
                     ok = false;
                     break;
@@ -416,115 +512,137 @@ __global__ void __launch_bounds__(kScanThreads, 1) linear_scan_kernel(const __gr
             if (kStateOnly) {
                 float* sg = seg_at(g);
 #pragma unroll
-                for (int c = 0; c < kDepth; c++) sg[c * kTile] = x[c];
+                for (int c = 0; c < 16; c++) {
+                    const float2 y = split2(x2[c]);
+                    sg[(cw + 2 * c) * kTile] = y.x;
+                    sg[(cw + 2 * c + 1) * kTile] = y.y;
+                }
             } else if (sc.leave && g == have - 1 && d < d1) {
-                float* o = sc.leave + (static_cast<int64_t>(bh) * d1 + d) * d2 + c0;
+                float* o = sc.leave + (static_cast<int64_t>(bh) * d1 + d) * d2 + cg;
 #pragma unroll
-                for (int c = 0; c < kDepth; c += 4)
-                    if (c0 + c < d2) *reinterpret_cast<float4*>(o + c) = make_float4(x[c], x[c + 1], x[c + 2], x[c + 3]);
+                for (int c = 0; c < 32; c += 4)
+                    if (cg + c < d2) *reinterpret_cast<ulonglong2*>(o + c) = make_ulonglong2(x2[c / 2], x2[c / 2 + 1]);
             }
         }
-    } else if (warp >= 12) {
+    } else if (warp >= 20 && warp < 24 && !kStateOnly) {
         const int quad = warp & 3, row = quad * 32 + lane;
         const uint32_t lanes = tmem + (static_cast<uint32_t>(quad * 32) << 16);
-        // out rows of chunk j
-        auto write_out = [&](int j) {
-            if (!warp_wait(&o_full, j & 1)) return false;
+        __nv_bfloat16* out = static_cast<__nv_bfloat16*>(sc.out) +
+                             (pr.packed ? static_cast<int64_t>(h) * pr.sq.total + row0
+                                        : static_cast<int64_t>(bh) * pr.sq.T) * d2 + c0;
+        for (int j = 0; j < n; j++) {
+            if (!wait_warp(&o_full, j & 1, fail)) {
+                if (lane == 0) fail_now();
+                break;
+            }
             tc_fence_after();
             const int ch = chunk_of(j), nr = rows_of(ch);
             const float f = row < nr ? pw[rev ? nr - 1 - row : row + 1] : 0.f;
-            __nv_bfloat16* out = static_cast<__nv_bfloat16*>(sc.out) +
-                                 ((pr.packed ? static_cast<int64_t>(h) * pr.sq.total + row0
-                                             : static_cast<int64_t>(bh) * pr.sq.T) +
-                                  static_cast<int64_t>(ch) * kTile) * d2 + c0;
-            uint4 ch4[2][4];
-#pragma unroll
+            const f32x2 f2 = pair2(f, f);
+#pragma unroll 1
             for (int hh = 0; hh < 2; hh++) {
-                float a[32], y[32];
-                tmem_ld32(lanes + kColNear + 32 * hh, a);
-                tmem_ld32(lanes + kColFar + 32 * hh, y);
+                uint4 o16[4];  // 32 of the row's outputs as 16-byte pieces
 #pragma unroll
-                for (int i = 0; i < 4; i++)
-                    ch4[hh][i] = make_uint4(pack_bf16(a[8 * i] + f * y[8 * i], a[8 * i + 1] + f * y[8 * i + 1]),
-                                            pack_bf16(a[8 * i + 2] + f * y[8 * i + 2], a[8 * i + 3] + f * y[8 * i + 3]),
-                                            pack_bf16(a[8 * i + 4] + f * y[8 * i + 4], a[8 * i + 5] + f * y[8 * i + 5]),
-                                            pack_bf16(a[8 * i + 6] + f * y[8 * i + 6], a[8 * i + 7] + f * y[8 * i + 7]));
-            }
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&o_read);
+                for (int c = 0; c < 2; c++) {
+                    f32x2 a[8], y[8];
+                    tmem_ld16x2(lanes + kColNear + 32 * hh + 16 * c, a);
+                    tmem_ld16x2(lanes + kColFar + 32 * hh + 16 * c, y);
 #pragma unroll
-            for (int hh = 0; hh < 2; hh++) {
-                lane_group_transpose(ch4[hh], lane);
+                    for (int i = 0; i < 8; i++) a[i] = fma2(f2, y[i], a[i]);
+#pragma unroll
+                    for (int i = 0; i < 2; i++)
+                        o16[2 * c + i] = make_uint4(pack_bf16(a[4 * i]), pack_bf16(a[4 * i + 1]),
+                                                    pack_bf16(a[4 * i + 2]), pack_bf16(a[4 * i + 3]));
+                }
+                if (hh == 1) {
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&o_read);
+                }
+                lane_group_transpose(o16, lane);
                 const int col = 32 * hh + 8 * (lane & 3);
 #pragma unroll
                 for (int i = 0; i < 4; i++) {
                     const int r = quad * 32 + (lane & ~3) + i;
                     if (r < nr && c0 + col < d2)
-                        *reinterpret_cast<uint4*>(out + static_cast<int64_t>(r) * d2 + col) = ch4[hh][i];
+                        *reinterpret_cast<uint4*>(out + (static_cast<int64_t>(ch) * kTile + r) * d2 + col) = o16[i];
                 }
             }
-            return true;
-        };
+        }
+    } else if (warp >= 24) {
+        // thread: half a row of c, split before the products of the chunk before are done with the parts' place
+        const int row = (warp & 3) * 32 + lane, h4 = (warp - 24) >> 2 << 2;
         bool ok = true;
-        for (int j = 0; j < n && ok; j++) {
-            if (__any_sync(0xffffffffu, *fail != 0)) break;
-            const int s = j % nst, nr = rows_of(chunk_of(j));
-            uint8_t* st = smem + s * stage_bytes;
-            ok = warp_wait(&v_full[s], (j / nst) & 1) && (j == 0 || warp_wait(&own_full, (j - 1) & 1));
+        int s = 0;
+        uint32_t ph = 0;
+        uint8_t* st = smem;
+        for (int j = 0; j < n; j++) {
+            const int nr = rows_of(chunk_of(j));
+            ok = wait_warp(&v_full[s], ph, fail);
             if (ok && nr < kTile) {
                 // rows behind the sequence's end count nothing, whatever they hold
-                ok = warp_wait(&qk_full[s], (j / nst) & 1);
+                ok = wait_warp(&qk_full[s], ph, fail);
                 if (ok && row >= nr) {
                     const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll 1
-                    for (int c = 0; c < 8; c++) {
-                        *reinterpret_cast<uint4*>(st + v_off + row * 128 + c * 16) = zero;
-                        for (int p = 0; p < np; p++)
-                            *reinterpret_cast<uint4*>(st + k_off + p * kPanelBytes + row * 128 + c * 16) = zero;
+                    for (int c = h4; c < h4 + 4; c++) {
+                        const uint32_t off = sw128_off(row, c);
+                        *reinterpret_cast<uint4*>(st + v_off + off) = zero;
+                        for (int p = 0; p < np; p++) *reinterpret_cast<uint4*>(st + k_off + p * kPanelBytes + off) = zero;
                     }
                 }
             }
             if (!ok) break;
             const float wt = row < nr ? pw[rev ? row + 1 : nr - 1 - row] : 0.f;
-#pragma unroll 2
-            for (int c = 0; c < 8; c++) {
-                const uint32_t off = sw128_off(row, c);
-                const uint4 xv = *reinterpret_cast<const uint4*>(st + v_off + off);
+            const f32x2 wt2 = pair2(wt, wt), minus = pair2(-1.f, -1.f);
+            auto cut = [](f32x2 f) {
+                const float2 y = split2(f);
+                return __byte_perm(__float_as_uint(y.x), __float_as_uint(y.y), 0x7632);
+            };
+            auto less = [&](f32x2 f, uint32_t p) {
+                return fma2(pair2(__uint_as_float(p << 16), __uint_as_float(p & 0xffff0000u)), minus, f);
+            };
+            uint32_t p1[16], p2[16], p3[16];
+#pragma unroll
+            for (int c = 0; c < 4; c++) {
+                const uint4 xv = *reinterpret_cast<const uint4*>(st + v_off + sw128_off(row, h4 + c));
                 const uint32_t in[4] = {xv.x, xv.y, xv.z, xv.w};
-                uint32_t p1[4], p2[4], p3[4];
 #pragma unroll
                 for (int q = 0; q < 4; q++) {
-                    float2 f = unpack_bf16(in[q]);
-                    f.x *= wt;
-                    f.y *= wt;
-                    p1[q] = pack_bf16(f.x, f.y);
-                    float2 t = unpack_bf16(p1[q]);
-                    f.x -= t.x;
-                    f.y -= t.y;
-                    p2[q] = pack_bf16(f.x, f.y);
-                    t = unpack_bf16(p2[q]);
-                    p3[q] = pack_bf16(f.x - t.x, f.y - t.y);
+                    // three cuts of 8 bits: exact, 24 bits in all
+                    const int e = 4 * c + q;
+                    f32x2 f = mul2(pair2(__uint_as_float(in[q] << 16), __uint_as_float(in[q] & 0xffff0000u)), wt2);
+                    p1[e] = cut(f);
+                    f = less(f, p1[e]);
+                    p2[e] = cut(f);
+                    f = less(f, p2[e]);
+                    p3[e] = cut(f);
                 }
-                *reinterpret_cast<uint4*>(wc + off) = make_uint4(p1[0], p1[1], p1[2], p1[3]);
-                *reinterpret_cast<uint4*>(wc + kPanelBytes + off) = make_uint4(p2[0], p2[1], p2[2], p2[3]);
-                *reinterpret_cast<uint4*>(wc + 2 * kPanelBytes + off) = make_uint4(p3[0], p3[1], p3[2], p3[3]);
+            }
+            if (j > 0) ok = wait_warp(&own_full, (j - 1) & 1, fail);
+            if (!ok) break;
+#pragma unroll
+            for (int c = 0; c < 4; c++) {
+                const uint32_t off = sw128_off(row, h4 + c);
+                *reinterpret_cast<uint4*>(wc + off) = make_uint4(p1[4 * c], p1[4 * c + 1], p1[4 * c + 2], p1[4 * c + 3]);
+                *reinterpret_cast<uint4*>(wc + kPanelBytes + off) =
+                    make_uint4(p2[4 * c], p2[4 * c + 1], p2[4 * c + 2], p2[4 * c + 3]);
+                *reinterpret_cast<uint4*>(wc + 2 * kPanelBytes + off) =
+                    make_uint4(p3[4 * c], p3[4 * c + 1], p3[4 * c + 2], p3[4 * c + 3]);
             }
             fence_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(&scaled);
-            if (!kStateOnly && j > 0) ok = write_out(j - 1);
+            st += stage_bytes;
+            if (++s == nst) {
+                s = 0;
+                st = smem;
+                ph ^= 1u;
+            }
         }
-        if (ok && !kStateOnly && n > 0 && !__any_sync(0xffffffffu, *fail != 0)) ok = write_out(n - 1);
         if (!ok && lane == 0) fail_now();
     }
 
-    __syncthreads();
-    if (*fail && tid == 0) {
-        // let the copies still in flight land before the shared memory goes away
-        for (int i = sent_qk > nst ? sent_qk - nst : 0; i < sent_qk; i++) mbar_wait(&qk_full[i % nst], (i / nst) & 1);
-        for (int i = sent_v > nst ? sent_v - nst : 0; i < sent_v; i++) mbar_wait(&v_full[i % nst], (i / nst) & 1);
-    }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -583,7 +701,7 @@ bool linear_tc_plan(LinTcPlan* pl, int batch, int H, int T, int64_t rows, int ti
         if ((nch + L - 1) / L != s) continue;  // the same cut as fewer segments
         auto waves = [&](double it, double share) {
             const double full = (it / sms > 1 ? std::ceil(it / sms) : 1.0) * (L + 2.0);
-            const double spread = work * share / sms + L;  // ragged sequences: the longest item ends late
+            const double spread = work * share / sms * (1 + 2.0 / L) + L + 2.0;  // ragged sequences: the longest item ends late
             return rows < static_cast<int64_t>(batch) * H * T && spread < full ? spread : full;
         };
         double c = waves(static_cast<double>(items) * s, 1.0);
