@@ -37,6 +37,8 @@ class LLAError(RuntimeError):
 def load() -> ctypes.CDLL:
     """Load liblla.so (once). Raises if it has not been built."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(LIB_PATH):
@@ -102,9 +104,15 @@ def num_levels(T: int) -> int:
     return int(load().lla_num_levels(int(T)))
 
 
+_torch_module = None
+
+
 def _torch():
-    import torch
-    return torch
+    global _torch_module
+    if _torch_module is None:
+        import torch
+        _torch_module = torch
+    return _torch_module
 
 
 def _dtype_code(t) -> int:
@@ -415,42 +423,43 @@ def device_error(stream=None) -> int:
     return int(load().lla_device_error(_stream_handle(stream)))
 
 
-def _linear_inputs(named, log_a, H):
-    """Checks of the linear-attention calls: ``named`` {name: tensor} of one dtype, log_a [H] fp32."""
+def _linear_inputs(names, tensors, log_a, H):
+    """Checks of the linear-attention calls: CUDA tensors of one dtype and device, log_a [H] fp32."""
     torch = _torch()
-    q = next(iter(named.values()))
-    for n, t_ in named.items():
-        _check(t_, n, q.device)
-        if t_.dtype != q.dtype:
-            raise TypeError(f"{', '.join(named)} must share one dtype")
-    _check(log_a, "log_a", q.device)
+    q = tensors[0]
+    device, dtype = q.device, q.dtype
+    for n, t_ in zip(names, tensors):
+        _check(t_, n, device)
+        if t_.dtype != dtype:
+            raise TypeError(f"{', '.join(names)} must share one dtype")
+    _check(log_a, "log_a", device)
     if log_a.dtype != torch.float32 or log_a.shape != (H,):
         raise ValueError(f"log_a must be float32 [{H}] (one decay per head)")
 
 
 def _state(t_, name, shape, device):
     """Address of an optional fp32 state tensor of the given shape (None: NULL)."""
-    torch = _torch()
     if t_ is None:
         return None
     _check(t_, name, device)
-    if t_.dtype != torch.float32 or tuple(t_.shape) != tuple(shape):
+    if t_.dtype != _torch().float32 or t_.shape != shape:
         raise ValueError(f"{name} must be float32 {list(shape)}, got {t_.dtype} {list(t_.shape)}")
     return t_.data_ptr()
 
 
-def _on(device, stream):
-    """Contexts that make ``device`` and the launch stream current, so that what a call allocates
-    belongs to the stream that writes it."""
+def _on(device, stream, call):
+    """call(stream handle) with ``device`` and the launch stream current, so that what it allocates belongs to
+    the stream that writes it."""
     torch = _torch()
-    import contextlib
-    ctx = contextlib.ExitStack()
-    ctx.enter_context(torch.cuda.device(device))
-    if stream is not None:
+    if stream is None and torch.cuda.current_device() == device.index:  # the usual case, without context managers
+        return call(torch._C._cuda_getCurrentRawStream(device.index))
+    with torch.cuda.device(device):
+        if stream is None:
+            return call(torch.cuda.current_stream().cuda_stream)
         if stream.device != device:
             raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
-        ctx.enter_context(torch.cuda.stream(stream))
-    return ctx
+        with torch.cuda.stream(stream):
+            return call(stream.cuda_stream)
 
 
 def _given(out, shape, like):
@@ -459,7 +468,7 @@ def _given(out, shape, like):
     if out is None:
         return torch.empty(shape, dtype=like.dtype, device=like.device)
     _check(out, "out", like.device)
-    if out.dtype != like.dtype or tuple(out.shape) != tuple(shape):
+    if out.dtype != like.dtype or out.shape != shape:
         raise ValueError(f"out must be {like.dtype} {list(shape)}, got {out.dtype} {list(out.shape)}")
     return out
 
@@ -473,18 +482,20 @@ def linear_forward(q, k, v, log_a, state0=None, state_out=None, out=None, stream
     ``state_out`` fp32 [B,H,dk,dv] is written with the state after the last token (see linear_decode_step)."""
     B, H, T, dk = q.shape
     dv = v.shape[-1]
-    _linear_inputs({"q": q, "k": k, "v": v}, log_a, H)
+    _linear_inputs(("q", "k", "v"), (q, k, v), log_a, H)
     if k.shape != q.shape or v.shape != (B, H, T, dv):
         raise ValueError("shape mismatch between q, k and v")
     B0 = 0 if state0 is None else int(state0.shape[0])
     s0 = _state(state0, "state0", (1 if B0 == 1 else B, H, dk, dv), q.device)
     s1 = _state(state_out, "state_out", (B, H, dk, dv), q.device)
-    with _on(q.device, stream):
-        out = _given(out, (B, H, T, dv), q)
-        _call(load().lla_linear_forward(q.data_ptr(), k.data_ptr(), v.data_ptr(), log_a.data_ptr(), s0,
-                                        out.data_ptr(), s1, B, B0, H, T, dk, dv, _stream_handle(stream),
-                                        _dtype_code(q)), "lla_linear_forward")
-    return out
+
+    def call(sh):
+        o = _given(out, (B, H, T, dv), q)
+        _call(load().lla_linear_forward(q.data_ptr(), k.data_ptr(), v.data_ptr(), log_a.data_ptr(), s0, o.data_ptr(),
+                                        s1, B, B0, H, T, dk, dv, sh, _dtype_code(q)), "lla_linear_forward")
+        return o
+
+    return _on(q.device, stream, call)
 
 
 def linear_forward_varlen(q, k, v, log_a, cu_seqlens, max_T: int, state0=None, state_out=None, out=None, stream=None):
@@ -494,7 +505,7 @@ def linear_forward_varlen(q, k, v, log_a, cu_seqlens, max_T: int, state0=None, s
     torch = _torch()
     H, total, dk = q.shape
     dv = v.shape[-1]
-    _linear_inputs({"q": q, "k": k, "v": v}, log_a, H)
+    _linear_inputs(("q", "k", "v"), (q, k, v), log_a, H)
     _check(cu_seqlens, "cu_seqlens", q.device)
     if cu_seqlens.dtype != torch.int32 or cu_seqlens.dim() != 1:
         raise TypeError("cu_seqlens must be int32 [n+1]")
@@ -504,13 +515,15 @@ def linear_forward_varlen(q, k, v, log_a, cu_seqlens, max_T: int, state0=None, s
     n0 = 0 if state0 is None else int(state0.shape[0])
     s0 = _state(state0, "state0", (1 if n0 == 1 else n, H, dk, dv), q.device)
     s1 = _state(state_out, "state_out", (n, H, dk, dv), q.device)
-    with _on(q.device, stream):
-        out = _given(out, (H, total, dv), q)
+
+    def call(sh):
+        o = _given(out, (H, total, dv), q)
         _call(load().lla_linear_forward_varlen(q.data_ptr(), k.data_ptr(), v.data_ptr(), log_a.data_ptr(), s0,
-                                               out.data_ptr(), s1, cu_seqlens.data_ptr(), n, n0, H, total,
-                                               int(max_T), dk, dv, _stream_handle(stream), _dtype_code(q)),
-              "lla_linear_forward_varlen")
-    return out
+                                               o.data_ptr(), s1, cu_seqlens.data_ptr(), n, n0, H, total, int(max_T),
+                                               dk, dv, sh, _dtype_code(q)), "lla_linear_forward_varlen")
+        return o
+
+    return _on(q.device, stream, call)
 
 
 def linear_backward(q, k, v, log_a, dout, state0=None, dstate_out=None, stream=None):
@@ -521,20 +534,23 @@ def linear_backward(q, k, v, log_a, dout, state0=None, dstate_out=None, stream=N
     torch = _torch()
     B, H, T, dk = q.shape
     dv = v.shape[-1]
-    _linear_inputs({"q": q, "k": k, "v": v, "dout": dout}, log_a, H)
+    _linear_inputs(("q", "k", "v", "dout"), (q, k, v, dout), log_a, H)
     if k.shape != q.shape or v.shape != (B, H, T, dv) or dout.shape != v.shape:
         raise ValueError("shape mismatch between q, k, v and dout")
     B0 = 0 if state0 is None else int(state0.shape[0])
     s0 = _state(state0, "state0", (1 if B0 == 1 else B, H, dk, dv), q.device)
     s1 = _state(dstate_out, "dstate_out", (B, H, dk, dv), q.device)
-    with _on(q.device, stream):
+
+    def call(sh):
         dq, dk_, dv_ = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
         ds = None if state0 is None else torch.empty_like(state0)
         _call(load().lla_linear_backward(q.data_ptr(), k.data_ptr(), v.data_ptr(), log_a.data_ptr(), s0,
                                          dout.data_ptr(), s1, dq.data_ptr(), dk_.data_ptr(), dv_.data_ptr(),
-                                         None if ds is None else ds.data_ptr(), B, B0, H, T, dk, dv,
-                                         _stream_handle(stream), _dtype_code(q)), "lla_linear_backward")
-    return dq, dk_, dv_, ds
+                                         None if ds is None else ds.data_ptr(), B, B0, H, T, dk, dv, sh,
+                                         _dtype_code(q)), "lla_linear_backward")
+        return dq, dk_, dv_, ds
+
+    return _on(q.device, stream, call)
 
 
 def linear_decode_step(q, k, v, log_a, state, out=None, stream=None):
@@ -542,18 +558,21 @@ def linear_decode_step(q, k, v, log_a, state, out=None, stream=None):
     ``state`` [B,H,dk,dv] fp32 is updated in place. Returns out [B,H,dv]."""
     B, H, dk = q.shape
     dv = v.shape[-1]
-    _linear_inputs({"q": q, "k": k, "v": v}, log_a, H)
+    _linear_inputs(("q", "k", "v"), (q, k, v), log_a, H)
     if k.shape != q.shape or v.shape != (B, H, dv):
         raise ValueError("shape mismatch between q, k and v")
     if state is None:
         raise ValueError("state is needed")
     sp = _state(state, "state", (B, H, dk, dv), q.device)
-    with _on(q.device, stream):
-        out = _given(out, (B, H, dv), q)
+
+    def call(sh):
+        o = _given(out, (B, H, dv), q)
         _call(load().lla_linear_decode_step(q.data_ptr(), k.data_ptr(), v.data_ptr(), log_a.data_ptr(), sp,
-                                            out.data_ptr(), _stream_handle(stream), B, H, dk, dv, _dtype_code(q)),
+                                            o.data_ptr(), sh, B, H, dk, dv, _dtype_code(q)),
               "lla_linear_decode_step")
-    return out
+        return o
+
+    return _on(q.device, stream, call)
 
 
 def decode_step_shared(q, k, v, log_a, lam, prefix_states, prefix_len: int, prefix_decay, states, t, out=None,
@@ -582,10 +601,13 @@ def decode_step_shared(q, k, v, log_a, lam, prefix_states, prefix_len: int, pref
     sp = _state(states, "states", (B, H, Lmax, dk, dv), q.device)
     if lam.shape != (B, H, Lmax) or log_a.shape != (B, H) or k.shape != q.shape or v.shape != (B, H, dv):
         raise ValueError("shape mismatch in decode inputs")
-    with _on(q.device, stream):
-        out = _given(out, (B, H, dv), q)
+
+    def call(sh):
+        o = _given(out, (B, H, dv), q)
         _call(load().lla_decode_step_shared(q.data_ptr(), k.data_ptr(), v.data_ptr(), log_a.data_ptr(),
                                             lam.data_ptr(), pp, int(prefix_len), Lp, dp, sp, t.data_ptr(),
-                                            out.data_ptr(), _stream_handle(stream), B, H, dk, dv, Lmax,
-                                            _dtype_code(q)), "lla_decode_step_shared")
-    return out
+                                            o.data_ptr(), sh, B, H, dk, dv, Lmax, _dtype_code(q)),
+              "lla_decode_step_shared")
+        return o
+
+    return _on(q.device, stream, call)

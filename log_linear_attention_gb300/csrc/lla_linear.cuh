@@ -68,7 +68,9 @@ struct LinTcScan {
     int tiles, seg_base;  // filled by linear_tc_run
 };
 struct LinTcPlan {
-    int batch, nseg, seg_chunks;  // segments of a sequence, 128-token chunks of a segment
+    int batch;
+    int nseg, seg_chunks;      // segments of a sequence, 128-token chunks of a segment
+    int npiece, piece_chunks;  // pieces of all segments but the last, whose own states are formed first
     size_t seg_bytes;
 };
 bool linear_tc_supported(int dtype, int dk, int dv);

@@ -4,8 +4,8 @@
 // or backwards in time) over one (sequence, head, 64 columns of c) in chunks of 128 tokens. The state
 // (d1 x 64, fp32) never leaves the registers of four warps. Per chunk, n valid rows:
 //     scores  A B^T                      [128 x 128]  -> TMEM
-//     own     B^T [hi | mid | lo]        [d1 x 192]   -> TMEM, w o C split into three bf16 parts, so that
-//                                                     the state keeps the 24 bits of fp32
+//     own     B^T [hi | mid + lo]        [d1 x 128]   -> TMEM, w o C cut into three bf16 parts, so that the
+//                                                     state keeps the 24 bits of fp32
 //     far     A X                        [128 x 64]   X = entering state, rounded to bf16
 //     near    P C                        [128 x 64]   P = scores o g^|i-j|, bf16, in TMEM
 //     out_i = near_i + f_i far_i,   X <- g^n X + own
@@ -13,9 +13,10 @@
 // rounded to bf16 as the operands of a bf16 product must be (2^-8 of each term, as the output itself);
 // scores, sums, weights and the state stay fp32.
 //
-// Heads alone do not fill the GPU when they are few, so a scan may be cut into segments: a first launch
-// (kStateOnly) forms the own state of every segment but the last, and each segment's CTA joins those
-// before it, decayed, in order.
+// Heads alone do not fill the GPU when they are few, so a scan may be cut into segments, one CTA each: a first
+// launch (kStateOnly) forms the own states of pieces of every segment but the last (smaller than segments, as
+// it is launched without the last segment's share), and each segment's CTA sums those before it, decayed, in
+// order.
 //
 // Rows of a chunk behind its sequence's end (another sequence's, when packed) are set to zero in shared
 // memory before any product sums over them. Every wait is bounded; on overrun the kernel records
@@ -35,15 +36,17 @@ constexpr int kWcBytes = 3 * kPanelBytes;
 constexpr int kSmemMost = 232448 - 2048;  // 227 KB less the static part
 
 // TMEM columns
-constexpr uint32_t kColS = 0, kColP = 128, kColNear = 192, kColFar = 256, kColOwn = 320;
+// two buffers of scores (P takes the place of its scores: 32 keys in the first 16 of their 32 columns); own: the
+// high part's product, then that of the middle and low parts
+constexpr uint32_t kColS = 0, kColNear = 256, kColFar = 320, kColOwn = 384;
 
 struct ScanParams {
     CUtensorMap map[4];
     LinTcScan scan[3];
     const float* log_a;
-    float* seg;  // segments' own states
+    float* seg;  // pieces' own states
     LinSeqs sq;
-    int count, nseg, seg_chunks, packed, batch;
+    int count, nseg, seg_chunks, npiece, piece_chunks, packed, batch;
 };
 
 __device__ __forceinline__ float gpow(float la, int n) { return n == 0 ? 1.f : expf(la * static_cast<float>(n)); }
@@ -104,13 +107,18 @@ __device__ __forceinline__ uint32_t pack_bf16(f32x2 x) {
     return pack_bf16(f.x, f.y);
 }
 
-// 16 or 32 consecutive fp32 TMEM columns of this warp's lanes as pairs.
-__device__ __forceinline__ void tmem_ld16x2(uint32_t taddr, f32x2* v) {
-    uint32_t r[16];
-    tmem_ld16_issue(taddr, r);
+// 16 consecutive fp32 TMEM columns at each of two places, as pairs: both loads in flight, one wait.
+__device__ __forceinline__ void tmem_ld16x2(uint32_t ta, uint32_t tb, f32x2* va, f32x2* vb) {
+    uint32_t r[16], q[16];
+    tmem_ld16_issue(ta, r);
+    tmem_ld16_issue(tb, q);
     tmem_ld16_wait(r);
+    tmem_ld16_wait(q);  // nothing is left to wait for: keeps the uses of q behind the wait
 #pragma unroll
-    for (int i = 0; i < 8; i++) v[i] = pair2(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1]));
+    for (int i = 0; i < 8; i++) {
+        va[i] = pair2(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1]));
+        vb[i] = pair2(__uint_as_float(q[2 * i]), __uint_as_float(q[2 * i + 1]));
+    }
 }
 
 // One lane of a converged warp; code behind it counts as uniform, so descriptors stay in uniform registers.
@@ -120,39 +128,59 @@ __device__ __forceinline__ bool elect_one() {
     return p != 0;
 }
 
-// Bounded waits. The phase is mostly complete already: one inline test, and a call only where it is not (a call a
-// wait cost the issuing thread some 250 cycles). They give up when another role has.
+// Up to kTries tests of a barrier's phase, three instructions each: a test suspends the thread for some hundred
+// cycles only, and two dozen waiting warps that did more between tests took most of the issue slots.
+constexpr uint32_t kTries = 1024;
+__device__ __forceinline__ bool mbar_try_many(uint64_t* bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t.reg .u32 i;\n\tmov.u32 i, %4;\n"
+        "TRY:\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "@p bra DONE;\n\t"
+        "sub.u32 i, i, 1;\n\t"
+        "setp.ne.u32 q, i, 0;\n\t"
+        "@q bra TRY;\n"
+        "DONE:\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity), "n"(kSuspendNs), "n"(kTries)
+        : "memory");
+    return ok != 0;
+}
+
+// Bounded waits. They give up when another role has.
 __device__ __noinline__ bool wait_long(uint64_t* bar, uint32_t parity, volatile int* fail) {
     const long long start = clock64();
-    while (!mbar_try_wait(bar, parity)) {
+    while (!mbar_try_many(bar, parity)) {
         if (*fail || clock64() - start > kWaitCycles) return false;
     }
     return true;
 }
 __device__ __forceinline__ bool wait_one(uint64_t* bar, uint32_t parity, volatile int* fail) {
-    return mbar_try_wait(bar, parity) || wait_long(bar, parity, fail);
+    return mbar_try_many(bar, parity) || wait_long(bar, parity, fail);
 }
 __device__ __noinline__ bool wait_long_warp(uint64_t* bar, uint32_t parity, volatile int* fail) {
     const long long start = clock64();
     while (true) {
-        const bool done = mbar_try_wait(bar, parity);
+        const bool done = mbar_try_many(bar, parity);
         if (__all_sync(0xffffffffu, done)) return true;
         const bool late = *fail || clock64() - start > kWaitCycles;
         if (__any_sync(0xffffffffu, late)) return false;
     }
 }
 __device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, volatile int* fail) {
-    return __all_sync(0xffffffffu, mbar_try_wait(bar, parity)) || wait_long_warp(bar, parity, fail);
+    return __all_sync(0xffffffffu, mbar_try_many(bar, parity)) || wait_long_warp(bar, parity, fail);
 }
 
-// Warps: 0 TMA producer, 1 TMEM owner and MMA issuer, 4..11 P (every other block of 32 keys), 12..19 state
+// Warps: 0 and 2 TMA producers, 1 TMEM owner and MMA issuer, 4..11 P (every other block of 32 keys), 12..19 state
 // (32 columns each), 20..23 write out, 24..31 split w o C. Warp w reaches TMEM lanes 32 (w % 4)..+31: rows of scores and out, rows of the state.
 template <bool kStateOnly>
 __global__ void __launch_bounds__(kScanThreads, 1) linear_scan_kernel(const __grid_constant__ ScanParams pr, int* err) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     __shared__ uint64_t qk_full[kMaxStages], v_full[kMaxStages], qk_free[kMaxStages], v_free[kMaxStages];
-    __shared__ uint64_t scaled, own_full, own_read, x_ready, x_free, s_full, p_ready, o_full, o_read, drain;
+    __shared__ uint64_t scaled, own_full, own_read, x_ready, x_free, s_full[2], p_ready, o_full, o_read, drain;
     __shared__ uint32_t tmem_base_sh;
     __shared__ int fail_sh;
     __shared__ float pw[132];    // g^n
@@ -164,14 +192,14 @@ __global__ void __launch_bounds__(kScanThreads, 1) linear_scan_kernel(const __gr
     grid_dep_launch();
     // ---- which scan, 64 columns, segment, sequence and head
     int blk = blockIdx.x, si = 0;
-    const int nseg = kStateOnly ? pr.nseg - 1 : pr.nseg;
-    while (si + 1 < pr.count && blk >= pr.batch * pr.sq.H * nseg * pr.scan[si].tiles)
-        blk -= pr.batch * pr.sq.H * nseg * pr.scan[si++].tiles;
+    const int ncta = kStateOnly ? pr.npiece : pr.nseg;  // of one sequence, head and 64 columns
+    while (si + 1 < pr.count && blk >= pr.batch * pr.sq.H * ncta * pr.scan[si].tiles)
+        blk -= pr.batch * pr.sq.H * ncta * pr.scan[si++].tiles;
     const LinTcScan& sc = pr.scan[si];
     const int tile = blk % sc.tiles;
     blk /= sc.tiles;
-    const int g = blk % nseg;
-    blk /= nseg;
+    const int g = blk % ncta;
+    blk /= ncta;
     const int h = blk % pr.sq.H;
     int b = blk / pr.sq.H, len = pr.sq.T, row0 = 0;
     if (pr.packed) {
@@ -184,9 +212,10 @@ __global__ void __launch_bounds__(kScanThreads, 1) linear_scan_kernel(const __gr
     const int z = pr.packed ? h : bh;  // outermost coordinate of the tensor maps
     const int nch = (len + kTile - 1) / kTile;
     const int have = nch <= pr.seg_chunks ? 1 : (nch + pr.seg_chunks - 1) / pr.seg_chunks;
-    if (g >= (kStateOnly ? have - 1 : have)) return;
-    const int p0 = g * pr.seg_chunks;
-    const int n = nch - p0 < pr.seg_chunks ? nch - p0 : pr.seg_chunks;  // chunks of this CTA
+    const int span = kStateOnly ? pr.piece_chunks : pr.seg_chunks;
+    const int p0 = g * span;
+    if (kStateOnly ? p0 >= (have - 1) * pr.seg_chunks : g >= have) return;
+    const int n = nch - p0 < span ? nch - p0 : span;  // chunks of this CTA
     const bool rev = sc.reverse != 0;
     auto chunk_of = [&](int j) { return rev ? nch - 1 - (p0 + j) : p0 + j; };
     auto rows_of = [&](int c) { return len - c * kTile < kTile ? len - c * kTile : kTile; };
@@ -214,7 +243,8 @@ __global__ void __launch_bounds__(kScanThreads, 1) linear_scan_kernel(const __gr
         mbar_init(&own_read, 8);
         mbar_init(&x_ready, 8);
         mbar_init(&x_free, 1);
-        mbar_init(&s_full, 1);
+        mbar_init(&s_full[0], 1);
+        mbar_init(&s_full[1], 1);
         mbar_init(&p_ready, 8);
         mbar_init(&o_full, 1);
         mbar_init(&o_read, 4);
@@ -234,34 +264,61 @@ __global__ void __launch_bounds__(kScanThreads, 1) linear_scan_kernel(const __gr
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = tmem_base_sh;
+    // own states of the sequence's pieces, [64 columns][128 rows] each
+    float* seg0 = pr.seg + (static_cast<int64_t>(sc.seg_base) +
+                            static_cast<int64_t>(bh) * pr.npiece * sc.tiles + tile) * (kDepth * kTile);
+    const int64_t seg_step = static_cast<int64_t>(sc.tiles) * (kDepth * kTile);
+    if (!kStateOnly && g > 0) {
+        // the pieces before this segment, decayed to its start and summed in order
+        float4 sum[2] = {};
+        const int np_before = p0 / pr.piece_chunks;
+#pragma unroll 2
+        for (int gg = 0; gg < np_before; gg++) {
+            const float f = gpow(la, before(p0) - before((gg + 1) * pr.piece_chunks));
+            const float4* sg = reinterpret_cast<const float4*>(seg0 + gg * seg_step);
+#pragma unroll
+            for (int i = 0; i < 2; i++) {
+                const float4 y = sg[tid + i * kScanThreads];
+                sum[i].x += f * y.x;
+                sum[i].y += f * y.y;
+                sum[i].z += f * y.z;
+                sum[i].w += f * y.w;
+            }
+        }
+        reinterpret_cast<float4*>(wc)[tid] = sum[0];
+        reinterpret_cast<float4*>(wc)[tid + kScanThreads] = sum[1];
+        __syncthreads();
+    }
     auto fail_now = [&]() {
         if (atomicExch(&fail_sh, 1) == 0) record_error(err, kDevTimeout);
     };
 
-    if (warp == 0) {
+    if (warp == 0 || warp == 2) {
+        // a and b, and in a warp of its own c: its place is free earlier, and waited for longer
         if (elect_one()) {
-            int s = 0, sent_qk = 0, sent_v = 0, t0 = row0 + chunk_of(0) * kTile;
+            const bool is_c = warp == 2;
+            uint64_t* full = is_c ? v_full : qk_full;
+            uint64_t* free_ = is_c ? v_free : qk_free;
+            int s = 0, sent = 0, t0 = row0 + chunk_of(0) * kTile;
             const int dt = rev ? -kTile : kTile;
             uint32_t ph = 1;
             uint8_t* st = smem;
             for (int j = 0; j < n; j++, t0 += dt) {
-                if (j >= nst && !wait_one(&qk_free[s], ph, fail)) {
+                if (j >= nst && !wait_one(&free_[s], ph, fail)) {
                     fail_now();
                     break;
                 }
-                mbar_expect_tx(&qk_full[s], v_off);
-                for (int p = 0; p < np; p++) {
-                    if (!kStateOnly) tma_load_3d(st + p * kPanelBytes, &pr.map[sc.ia], &qk_full[s], 64 * p, t0, z);
-                    tma_load_3d(st + k_off + p * kPanelBytes, &pr.map[sc.ib], &qk_full[s], 64 * p, t0, z);
+                if (is_c) {
+                    mbar_expect_tx(&v_full[s], kPanelBytes);
+                    tma_load_3d(st + v_off, &pr.map[sc.ic], &v_full[s], c0, t0, z);
+                } else {
+                    mbar_expect_tx(&qk_full[s], v_off);
+                    for (int p = 0; p < np; p++) {
+                        if (!kStateOnly) tma_load_3d(st + p * kPanelBytes, &pr.map[sc.ia], &qk_full[s], 64 * p, t0, z);
+                        tma_load_3d(st + k_off + p * kPanelBytes, &pr.map[sc.ib], &qk_full[s], 64 * p, t0, z);
+                    }
                 }
-                sent_qk++;
-                if (j >= nst && !wait_one(&v_free[s], ph, fail)) {
-                    fail_now();
-                    break;
-                }
-                mbar_expect_tx(&v_full[s], kPanelBytes);
-                tma_load_3d(st + v_off, &pr.map[sc.ic], &v_full[s], c0, t0, z);
-                sent_v++;
+                sent++;
                 st += stage_bytes;
                 if (++s == nst) {
                     s = 0;
@@ -270,14 +327,13 @@ __global__ void __launch_bounds__(kScanThreads, 1) linear_scan_kernel(const __gr
                 }
             }
             // every copy has landed before the shared memory goes away
-            for (int i = sent_qk > nst ? sent_qk - nst : 0; i < sent_qk; i++) mbar_wait(&qk_full[i % nst], (i / nst) & 1);
-            for (int i = sent_v > nst ? sent_v - nst : 0; i < sent_v; i++) mbar_wait(&v_full[i % nst], (i / nst) & 1);
+            for (int i = sent > nst ? sent - nst : 0; i < sent; i++) mbar_wait(&full[i % nst], (i / nst) & 1);
         }
     } else if (warp == 1) {
         if (elect_one()) {
             constexpr uint32_t kIdS = idesc_bf16(kTile, kTile, 0, 0);    // A B^T, both K-major
             constexpr uint32_t kIdX = idesc_bf16(kTile, kDepth, 0, 1);   // A X and P C: B MN-major
-            constexpr uint32_t kIdOwn = idesc_bf16(kTile, 3 * kDepth, 1, 1);
+            constexpr uint32_t kIdOwn2 = idesc_bf16(kTile, 2 * kDepth, 1, 1), kIdOwn1 = idesc_bf16(kTile, kDepth, 1, 1);
             // operands of the current stage and what a stage, a 16-column step of a K-major operand and a 16-row
             // step of an MN-major one (128) add to a descriptor's address field
             const uint64_t step = static_cast<uint64_t>(stage_bytes >> 4);
@@ -285,18 +341,18 @@ __global__ void __launch_bounds__(kScanThreads, 1) linear_scan_kernel(const __gr
             const uint64_t w0 = sdesc(smem_u32(wc), kPanelBytes, 1024), x0 = sdesc(smem_u32(xs), kPanelBytes, 1024);
             const uint64_t to_b = static_cast<uint64_t>(k_off >> 4), to_c = static_cast<uint64_t>(v_off >> 4);
             auto kstep = [](int kk) { return static_cast<uint64_t>(((kk >> 2) * kPanelBytes + (kk & 3) * 32) >> 4); };
-            auto scores = [&](uint64_t a, uint64_t* full, uint32_t ph) {
+            auto scores = [&](uint64_t a, uint64_t* full, uint32_t ph, uint32_t buf) {
                 if (!wait_one(full, ph, fail)) return false;
                 tc_fence_after();
 #pragma unroll
                 for (int kk = 0; kk < 4; kk++)
-                    if (kk < ksteps) mma_bf16(tmem + kColS, a + kstep(kk), a + to_b + kstep(kk), kIdS, kk > 0);
+                    if (kk < ksteps) mma_bf16(tmem + kColS + buf * kTile, a + kstep(kk), a + to_b + kstep(kk), kIdS, kk > 0);
                 if (ksteps > 4) {
 #pragma unroll
                     for (int kk = 4; kk < 8; kk++)
-                        if (kk < ksteps) mma_bf16(tmem + kColS, a + kstep(kk), a + to_b + kstep(kk), kIdS, 1);
+                        if (kk < ksteps) mma_bf16(tmem + kColS + buf * kTile, a + kstep(kk), a + to_b + kstep(kk), kIdS, 1);
                 }
-                mma_commit(&s_full);
+                mma_commit(&s_full[buf]);
                 return true;
             };
             bool ok = true;
@@ -304,7 +360,7 @@ __global__ void __launch_bounds__(kScanThreads, 1) linear_scan_kernel(const __gr
             uint32_t ph = 0;       // phase of stage s
             uint32_t par = 0;      // j & 1
             uint64_t a = a_first;  // stage s
-            if (!kStateOnly && n > 0) ok = scores(a, &qk_full[0], 0);
+            if (!kStateOnly && n > 0) ok = scores(a, &qk_full[0], 0, 0);
             for (int j = 0; j < n && ok; j++) {
                 ok = wait_one(&scaled, par, fail) && (!kStateOnly || wait_one(&qk_full[s], ph, fail)) &&
                      (j == 0 || wait_one(&own_read, par ^ 1u, fail));
@@ -312,7 +368,10 @@ __global__ void __launch_bounds__(kScanThreads, 1) linear_scan_kernel(const __gr
                 tc_fence_after();
                 const uint64_t bt = a + to_b + kmaj;
 #pragma unroll
-                for (int kk = 0; kk < kTile / 16; kk++) mma_bf16(tmem + kColOwn, bt + 128u * kk, w0 + 128u * kk, kIdOwn, kk > 0);
+                for (int kk = 0; kk < kTile / 16; kk++) mma_bf16(tmem + kColOwn, bt + 128u * kk, w0 + 128u * kk, kIdOwn2, kk > 0);
+#pragma unroll
+                for (int kk = 0; kk < kTile / 16; kk++)
+                    mma_bf16(tmem + kColOwn + kDepth, bt + 128u * kk, w0 + 2 * (kPanelBytes >> 4) + 128u * kk, kIdOwn1, 1);
                 mma_commit(&own_full);
                 if (kStateOnly) {
                     mma_commit(&qk_free[s]);
@@ -326,21 +385,20 @@ __global__ void __launch_bounds__(kScanThreads, 1) linear_scan_kernel(const __gr
                         if (kk < ksteps) mma_bf16(tmem + kColFar, a + kstep(kk), x0 + 128u * kk, kIdX, kk > 0);
                     mma_commit(&x_free);
                     mma_commit(&qk_free[s]);
-                    ok = wait_one(&p_ready, par, fail);
-                    if (!ok) break;
-                    tc_fence_after();
-                    // the scores are read: the next chunk's, from which the next P is built while the next own and far
-                    // products run
+                    // the next chunk's scores, so that its P is built while this one's is multiplied
                     const uint64_t ct = a + to_c + kmaj;
                     const bool wrap = s + 1 == nst;
                     if (j + 1 < n)
-                        ok = scores(wrap ? a_first : a + step, &qk_full[wrap ? 0 : s + 1], wrap ? ph ^ 1u : ph);
+                        ok = scores(wrap ? a_first : a + step, &qk_full[wrap ? 0 : s + 1], wrap ? ph ^ 1u : ph, par ^ 1u);
+                    ok = ok && wait_one(&p_ready, par, fail);
                     if (!ok) break;
+                    tc_fence_after();
 #pragma unroll
                     for (int kk = 0; kk < kTile / 16; kk++)
-                        mma_bf16_ta(tmem + kColNear, tmem + kColP + kk * 8, ct + 128u * kk, kIdX, kk > 0);
-                    mma_commit(&o_full);
+                        mma_bf16_ta(tmem + kColNear, tmem + kColS + par * kTile + kk / 2 * 32 + kk % 2 * 8, ct + 128u * kk,
+                                    kIdX, kk > 0);
                     mma_commit(&v_free[s]);
+                    mma_commit(&o_full);
                 }
                 a += step;
                 if (++s == nst) {
@@ -359,12 +417,12 @@ __global__ void __launch_bounds__(kScanThreads, 1) linear_scan_kernel(const __gr
         const int w = warp & 3;
         const uint32_t lanes = tmem + (static_cast<uint32_t>(w * 32) << 16);
         for (int j = 0; j < n; j++) {
-            if (!wait_warp(&s_full, j & 1, fail)) {
+            if (!wait_warp(&s_full[j & 1], (j >> 1) & 1, fail)) {
                 if (lane == 0) fail_now();
                 break;
             }
             tc_fence_after();
-            bool ok = true;
+            const uint32_t cols = lanes + kColS + (j & 1) * kTile;
 #pragma unroll 1
             for (int cb = (warp - 4) >> 2; cb < 4; cb += 2) {
                 uint32_t r[16];
@@ -374,7 +432,7 @@ __global__ void __launch_bounds__(kScanThreads, 1) linear_scan_kernel(const __gr
                 } else {
                     if (cb == w) {
                         float x[32];
-                        tmem_ld32(lanes + kColS + 32 * cb, x);
+                        tmem_ld32(cols + 32 * cb, x);
                         const float* dg = diag + 31 + lane;
 #pragma unroll
                         for (int i = 0; i < 32; i++) {
@@ -389,28 +447,20 @@ __global__ void __launch_bounds__(kScanThreads, 1) linear_scan_kernel(const __gr
                         const ulonglong2* cw = reinterpret_cast<const ulonglong2*>(colw);
 #pragma unroll
                         for (int hh = 0; hh < 2; hh++) {
-                            f32x2 x[8];
-                            tmem_ld16x2(lanes + kColS + 32 * cb + 16 * hh, x);
+                            uint32_t y[16];
+                            tmem_ld16_issue(cols + 32 * cb + 16 * hh, y);
+                            tmem_ld16_wait(y);
 #pragma unroll
                             for (int i = 0; i < 4; i++) {
                                 const ulonglong2 f = cw[4 * hh + i];
-                                r[8 * hh + 2 * i] = pack_bf16(mul2(mul2(x[2 * i], f.x), rw2));
-                                r[8 * hh + 2 * i + 1] = pack_bf16(mul2(mul2(x[2 * i + 1], f.y), rw2));
+                                auto at = [&](int e) { return pair2(__uint_as_float(y[e]), __uint_as_float(y[e + 1])); };
+                                r[8 * hh + 2 * i] = pack_bf16(mul2(mul2(at(4 * i), f.x), rw2));
+                                r[8 * hh + 2 * i + 1] = pack_bf16(mul2(mul2(at(4 * i + 2), f.y), rw2));
                             }
                         }
                     }
                 }
-                // P C of the chunk before has read P
-                if (cb < 2 && j > 0) {
-                    ok = wait_warp(&o_full, (j - 1) & 1, fail);
-                    if (!ok) break;
-                    tc_fence_after();
-                }
-                tmem_st16_issue(lanes + kColP + 16 * cb, r);
-            }
-            if (!ok) {
-                if (lane == 0) fail_now();
-                break;
+                tmem_st16_issue(cols + 32 * cb, r);
             }
             tmem_st_wait();
             tc_fence_before();
@@ -420,11 +470,6 @@ __global__ void __launch_bounds__(kScanThreads, 1) linear_scan_kernel(const __gr
     } else if (warp >= 12 && warp < 20) {
         const int d = (warp & 3) * 32 + lane;  // row of the state
         const uint32_t lanes = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
-        const int64_t slot = (static_cast<int64_t>(sc.seg_base) + (static_cast<int64_t>(bh) * (pr.nseg - 1)) * sc.tiles) *
-                             (kDepth * kTile);
-        auto seg_at = [&](int gg) {
-            return pr.seg + slot + (static_cast<int64_t>(gg) * sc.tiles + tile) * (kDepth * kTile) + d;
-        };
         const int cw = (warp - 12) / 4 * 32, cg = c0 + cw;  // first of this warp's columns, in the tile and in c
         f32x2 x2[16];  // column pairs
         if (!kStateOnly) {
@@ -450,11 +495,10 @@ __global__ void __launch_bounds__(kScanThreads, 1) linear_scan_kernel(const __gr
                         }
                 }
             }
-            for (int gg = 0; gg < g; gg++) {
-                const float f = gpow(la, before(p0) - before((gg + 1) * pr.seg_chunks));
-                const float* sg = seg_at(gg);
+            if (g > 0) {
+                const float* sum = reinterpret_cast<const float*>(wc) + d;
 #pragma unroll
-                for (int c = 0; c < 32; c++) x[c] += f * sg[(cw + c) * kTile];
+                for (int c = 0; c < 32; c++) x[c] += sum[(cw + c) * kTile];
             }
 #pragma unroll
             for (int c = 0; c < 16; c++) x2[c] = pair2(x[2 * c], x[2 * c + 1]);
@@ -486,13 +530,13 @@ __global__ void __launch_bounds__(kScanThreads, 1) linear_scan_kernel(const __gr
             const float gn = pw[rows_of(chunk_of(j))];
             f32x2 decay = pair2(gn, gn);
 #pragma unroll 1
-            for (int part = 2; part >= 0; part--) {  // smallest first
+            for (int part = 1; part >= 0; part--) {  // the smaller first
+                f32x2 y[8], u[8];
+                tmem_ld16x2(lanes + kColOwn + part * kDepth + cw, lanes + kColOwn + part * kDepth + cw + 16, y, u);
 #pragma unroll
-                for (int c2 = 0; c2 < 16; c2 += 8) {
-                    f32x2 y[8];
-                    tmem_ld16x2(lanes + kColOwn + part * kDepth + cw + 2 * c2, y);
-#pragma unroll
-                    for (int c = 0; c < 8; c++) x2[c2 + c] = fma2(decay, x2[c2 + c], y[c]);
+                for (int c = 0; c < 8; c++) {
+                    x2[c] = fma2(decay, x2[c], y[c]);
+                    x2[c + 8] = fma2(decay, x2[c + 8], u[c]);
                 }
                 decay = pair2(1.f, 1.f);
             }
@@ -510,7 +554,7 @@ __global__ void __launch_bounds__(kScanThreads, 1) linear_scan_kernel(const __gr
         }
         if (ok) {
             if (kStateOnly) {
-                float* sg = seg_at(g);
+                float* sg = seg0 + static_cast<int64_t>(g) * seg_step + d;
 #pragma unroll
                 for (int c = 0; c < 16; c++) {
                     const float2 y = split2(x2[c]);
@@ -530,6 +574,7 @@ __global__ void __launch_bounds__(kScanThreads, 1) linear_scan_kernel(const __gr
         __nv_bfloat16* out = static_cast<__nv_bfloat16*>(sc.out) +
                              (pr.packed ? static_cast<int64_t>(h) * pr.sq.total + row0
                                         : static_cast<int64_t>(bh) * pr.sq.T) * d2 + c0;
+        const bool wide = d2 % 16 == 0 && (reinterpret_cast<uintptr_t>(sc.out) & 31) == 0;
         for (int j = 0; j < n; j++) {
             if (!wait_warp(&o_full, j & 1, fail)) {
                 if (lane == 0) fail_now();
@@ -539,33 +584,29 @@ __global__ void __launch_bounds__(kScanThreads, 1) linear_scan_kernel(const __gr
             const int ch = chunk_of(j), nr = rows_of(ch);
             const float f = row < nr ? pw[rev ? nr - 1 - row : row + 1] : 0.f;
             const f32x2 f2 = pair2(f, f);
+            __nv_bfloat16* orow = out + (static_cast<int64_t>(ch) * kTile + row) * d2;
 #pragma unroll 1
-            for (int hh = 0; hh < 2; hh++) {
-                uint4 o16[4];  // 32 of the row's outputs as 16-byte pieces
-#pragma unroll
-                for (int c = 0; c < 2; c++) {
-                    f32x2 a[8], y[8];
-                    tmem_ld16x2(lanes + kColNear + 32 * hh + 16 * c, a);
-                    tmem_ld16x2(lanes + kColFar + 32 * hh + 16 * c, y);
-#pragma unroll
-                    for (int i = 0; i < 8; i++) a[i] = fma2(f2, y[i], a[i]);
-#pragma unroll
-                    for (int i = 0; i < 2; i++)
-                        o16[2 * c + i] = make_uint4(pack_bf16(a[4 * i]), pack_bf16(a[4 * i + 1]),
-                                                    pack_bf16(a[4 * i + 2]), pack_bf16(a[4 * i + 3]));
-                }
-                if (hh == 1) {
+            for (int c = 0; c < kDepth; c += 16) {
+                f32x2 a[8], y[8];
+                tmem_ld16x2(lanes + kColNear + c, lanes + kColFar + c, a, y);
+                if (c == kDepth - 16) {
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&o_read);
                 }
-                lane_group_transpose(o16, lane);
-                const int col = 32 * hh + 8 * (lane & 3);
+                uint32_t o[8];
 #pragma unroll
-                for (int i = 0; i < 4; i++) {
-                    const int r = quad * 32 + (lane & ~3) + i;
-                    if (r < nr && c0 + col < d2)
-                        *reinterpret_cast<uint4*>(out + (static_cast<int64_t>(ch) * kTile + r) * d2 + col) = o16[i];
+                for (int i = 0; i < 8; i++) o[i] = pack_bf16(fma2(f2, y[i], a[i]));
+                if (row < nr && c0 + c < d2) {
+                    // a whole 32-byte sector of the row in one store; 16 bytes each where rows are not so aligned
+                    if (wide) {
+                        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(orow + c), "r"(o[0]),
+                                     "r"(o[1]), "r"(o[2]), "r"(o[3]), "r"(o[4]), "r"(o[5]), "r"(o[6]), "r"(o[7])
+                                     : "memory");
+                    } else {
+                        *reinterpret_cast<uint4*>(orow + c) = make_uint4(o[0], o[1], o[2], o[3]);
+                        if (c0 + c + 8 < d2) *reinterpret_cast<uint4*>(orow + c + 8) = make_uint4(o[4], o[5], o[6], o[7]);
+                    }
                 }
             }
         }
@@ -619,7 +660,9 @@ __global__ void __launch_bounds__(kScanThreads, 1) linear_scan_kernel(const __gr
                     p3[e] = cut(f);
                 }
             }
+            // the products of the chunk before, and at first the state warps' reading of the sum, are done with this place
             if (j > 0) ok = wait_warp(&own_full, (j - 1) & 1, fail);
+            else if (!kStateOnly) ok = wait_warp(&x_ready, 0, fail);
             if (!ok) break;
 #pragma unroll
             for (int c = 0; c < 4; c++) {
@@ -689,31 +732,44 @@ bool linear_tc_plan(LinTcPlan* pl, int batch, int H, int T, int64_t rows, int ti
     pl->batch = batch;
     const int64_t items = static_cast<int64_t>(batch) * H * tiles;
     const int nch = (T - 1) / kTile + 1;
-    const int sms = sm_count();
-    // chunks of all items (packed sequences: fewer than batch x nch)
-    const double work = static_cast<double>(rows) / kTile * tiles;
-    // segments: time in units of one chunk of the main kernel; a chunk of the state launch is about half of one,
-    // a CTA's start and end about two, the extra launch about two
+    const double sms = sm_count();
+    const bool ragged = rows < static_cast<int64_t>(batch) * H * T;
+    const double total = static_cast<double>(rows) / kTile * tiles;  // chunks of all items
+    // Microseconds of `it` CTAs of L chunks at c a chunk and `fixed` a CTA, one CTA per SM at a time; ragged sequences
+    // (longest first) end about one CTA after the even share.
+    auto cost = [&](double it, int L, double share, double c, double fixed) {
+        const double waves = std::ceil(it / sms) * (L * c + fixed);
+        if (!ragged) return waves;
+        const double even = total * share / sms * (c + fixed / L) + L * c + fixed;
+        return even < waves ? even : waves;
+    };
+    // Measured at d = 128 and 64: a chunk 2.1 us (1.2 where only the state is formed), a CTA's start and end 5 (4), the
+    // second launch 3, a piece in a segment's sum 0.1.
     double best = 0;
     pl->nseg = 1;
+    pl->seg_chunks = pl->piece_chunks = nch;
+    pl->npiece = 0;
     for (int s = 1; s <= 64 && s <= nch; s++) {
         const int L = (nch + s - 1) / s;
         if ((nch + L - 1) / L != s) continue;  // the same cut as fewer segments
-        auto waves = [&](double it, double share) {
-            const double full = (it / sms > 1 ? std::ceil(it / sms) : 1.0) * (L + 2.0);
-            const double spread = work * share / sms * (1 + 2.0 / L) + L + 2.0;  // ragged sequences: the longest item ends late
-            return rows < static_cast<int64_t>(batch) * H * T && spread < full ? spread : full;
-        };
-        double c = waves(static_cast<double>(items) * s, 1.0);
-        if (s > 1) c += 0.5 * waves(static_cast<double>(items) * (s - 1), (s - 1.0) / s) + 2.0;
-        if (s == 1 || c < best) {
-            best = c;
-            pl->nseg = s;
+        const double main = cost(static_cast<double>(items) * s, L, 1.0, 2.1, 5.0);
+        for (int r = 1; r <= 8; r *= 2) {  // pieces of a segment
+            if (L % r != 0) break;
+            const int P = (s - 1) * r;
+            const double c = s == 1 ? main
+                                    : main + cost(static_cast<double>(items) * P, L / r, (s - 1.0) / s, 1.2, 4.0) + 3.0 +
+                                          0.1 * P;
+            if (best == 0 || c < best) {
+                best = c;
+                pl->nseg = s;
+                pl->seg_chunks = L;
+                pl->npiece = P;
+                pl->piece_chunks = L / r;
+            }
         }
     }
-    pl->seg_chunks = (nch + pl->nseg - 1) / pl->nseg;
-    pl->seg_bytes = static_cast<size_t>(items) * (pl->nseg - 1) * kDepth * kTile * sizeof(float);
-    return items * pl->nseg <= 0x7fffffff;
+    pl->seg_bytes = static_cast<size_t>(items) * pl->npiece * kDepth * kTile * sizeof(float);
+    return items * (pl->nseg > pl->npiece ? pl->nseg : pl->npiece) <= 0x7fffffff;
 }
 
 cudaError_t linear_tc_run(const LinTcPlan& pl, const LinTcMap* maps, int n_maps, const LinTcScan* scans, int count,
@@ -730,6 +786,8 @@ cudaError_t linear_tc_run(const LinTcPlan& pl, const LinTcMap* maps, int n_maps,
     pr.count = count;
     pr.nseg = pl.nseg;
     pr.seg_chunks = pl.seg_chunks;
+    pr.npiece = pl.npiece;
+    pr.piece_chunks = pl.piece_chunks;
     pr.packed = packed;
     pr.batch = pl.batch;
     int base = 0, tiles = 0, d1 = 0;
@@ -737,7 +795,7 @@ cudaError_t linear_tc_run(const LinTcPlan& pl, const LinTcMap* maps, int n_maps,
         pr.scan[i] = scans[i];
         pr.scan[i].tiles = (scans[i].d2 + kDepth - 1) / kDepth;
         pr.scan[i].seg_base = base;
-        base += pl.batch * sq.H * (pl.nseg - 1) * pr.scan[i].tiles;
+        base += pl.batch * sq.H * pl.npiece * pr.scan[i].tiles;
         tiles += pr.scan[i].tiles;
         if (scans[i].d1 > d1) d1 = scans[i].d1;
     }
@@ -747,7 +805,7 @@ cudaError_t linear_tc_run(const LinTcPlan& pl, const LinTcMap* maps, int n_maps,
         const int smem = smem_bytes(true, d1);
         e = cudaFuncSetAttribute(linear_scan_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMost);
         if (e != cudaSuccess) return e;
-        linear_scan_kernel<true><<<per_seg * (pl.nseg - 1), kScanThreads, smem, stream>>>(pr, err);
+        linear_scan_kernel<true><<<per_seg * pl.npiece, kScanThreads, smem, stream>>>(pr, err);
         note_launch(stream, "linear_scan_state");
     }
     const int smem = smem_bytes(false, d1);
