@@ -462,14 +462,13 @@ def _on(device, stream, call):
             return call(stream.cuda_stream)
 
 
-def _given(out, shape, like):
-    """The caller's output tensor, checked, or a new one."""
-    torch = _torch()
+def _given(out, v):
+    """The caller's output tensor, checked, or a new one: like v in shape, dtype and device."""
     if out is None:
-        return torch.empty(shape, dtype=like.dtype, device=like.device)
-    _check(out, "out", like.device)
-    if out.dtype != like.dtype or out.shape != shape:
-        raise ValueError(f"out must be {like.dtype} {list(shape)}, got {out.dtype} {list(out.shape)}")
+        return _torch().empty_like(v)
+    _check(out, "out", v.device)
+    if out.dtype != v.dtype or out.shape != v.shape:
+        raise ValueError(f"out must be {v.dtype} {list(v.shape)}, got {out.dtype} {list(out.shape)}")
     return out
 
 
@@ -490,7 +489,7 @@ def linear_forward(q, k, v, log_a, state0=None, state_out=None, out=None, stream
     s1 = _state(state_out, "state_out", (B, H, dk, dv), q.device)
 
     def call(sh):
-        o = _given(out, (B, H, T, dv), q)
+        o = _given(out, v)
         _call(load().lla_linear_forward(q.data_ptr(), k.data_ptr(), v.data_ptr(), log_a.data_ptr(), s0, o.data_ptr(),
                                         s1, B, B0, H, T, dk, dv, sh, _dtype_code(q)), "lla_linear_forward")
         return o
@@ -517,7 +516,7 @@ def linear_forward_varlen(q, k, v, log_a, cu_seqlens, max_T: int, state0=None, s
     s1 = _state(state_out, "state_out", (n, H, dk, dv), q.device)
 
     def call(sh):
-        o = _given(out, (H, total, dv), q)
+        o = _given(out, v)
         _call(load().lla_linear_forward_varlen(q.data_ptr(), k.data_ptr(), v.data_ptr(), log_a.data_ptr(), s0,
                                                o.data_ptr(), s1, cu_seqlens.data_ptr(), n, n0, H, total, int(max_T),
                                                dk, dv, sh, _dtype_code(q)), "lla_linear_forward_varlen")
@@ -566,7 +565,7 @@ def linear_decode_step(q, k, v, log_a, state, out=None, stream=None):
     sp = _state(state, "state", (B, H, dk, dv), q.device)
 
     def call(sh):
-        o = _given(out, (B, H, dv), q)
+        o = _given(out, v)
         _call(load().lla_linear_decode_step(q.data_ptr(), k.data_ptr(), v.data_ptr(), log_a.data_ptr(), sp,
                                             o.data_ptr(), sh, B, H, dk, dv, _dtype_code(q)),
               "lla_linear_decode_step")
@@ -603,7 +602,7 @@ def decode_step_shared(q, k, v, log_a, lam, prefix_states, prefix_len: int, pref
         raise ValueError("shape mismatch in decode inputs")
 
     def call(sh):
-        o = _given(out, (B, H, dv), q)
+        o = _given(out, v)
         _call(load().lla_decode_step_shared(q.data_ptr(), k.data_ptr(), v.data_ptr(), log_a.data_ptr(),
                                             lam.data_ptr(), pp, int(prefix_len), Lp, dp, sp, t.data_ptr(),
                                             o.data_ptr(), sh, B, H, dk, dv, Lmax, _dtype_code(q)),

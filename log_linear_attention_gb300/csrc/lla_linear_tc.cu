@@ -21,6 +21,7 @@
 // Rows of a chunk behind its sequence's end (another sequence's, when packed) are set to zero in shared
 // memory before any product sums over them. Every wait is bounded; on overrun the kernel records
 // LLA_ERR_TIMEOUT in the device error word, lets its own copies and MMAs land and returns.
+#include <atomic>
 #include <cmath>
 
 #include "lla_linear.cuh"
@@ -706,13 +707,27 @@ bool make_map_3d(CUtensorMap* m, const void* base, uint64_t z, uint64_t rows, ui
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// What is asked of a device once: its SMs, and both kernels' shared memory (0: not asked yet).
+constexpr int kMaxDevices = 64;
+std::atomic<int> g_sms[kMaxDevices];
+
 int sm_count() {
-    int dev = 0, sms = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess ||
-        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms <= 0) {
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) {
         cudaGetLastError();
-        sms = 152;
+        return 0;
     }
+    int sms = g_sms[dev].load(std::memory_order_acquire);
+    if (sms) return sms;
+    if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
+        cudaFuncSetAttribute(linear_scan_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMost) !=
+            cudaSuccess ||
+        cudaFuncSetAttribute(linear_scan_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMost) !=
+            cudaSuccess) {
+        cudaGetLastError();
+        return 0;
+    }
+    g_sms[dev].store(sms, std::memory_order_release);
     return sms;
 }
 
@@ -733,6 +748,7 @@ bool linear_tc_plan(LinTcPlan* pl, int batch, int H, int T, int64_t rows, int ti
     const int64_t items = static_cast<int64_t>(batch) * H * tiles;
     const int nch = (T - 1) / kTile + 1;
     const double sms = sm_count();
+    if (sms <= 0) return false;
     const bool ragged = rows < static_cast<int64_t>(batch) * H * T;
     const double total = static_cast<double>(rows) / kTile * tiles;  // chunks of all items
     // Microseconds of `it` CTAs of L chunks at c a chunk and `fixed` a CTA, one CTA per SM at a time; ragged sequences
@@ -800,19 +816,14 @@ cudaError_t linear_tc_run(const LinTcPlan& pl, const LinTcMap* maps, int n_maps,
         if (scans[i].d1 > d1) d1 = scans[i].d1;
     }
     const unsigned per_seg = static_cast<unsigned>(pl.batch) * sq.H * tiles;
-    cudaError_t e;
     if (pl.nseg > 1) {
         const int smem = smem_bytes(true, d1);
-        e = cudaFuncSetAttribute(linear_scan_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMost);
-        if (e != cudaSuccess) return e;
         linear_scan_kernel<true><<<per_seg * pl.npiece, kScanThreads, smem, stream>>>(pr, err);
         note_launch(stream, "linear_scan_state");
     }
     const int smem = smem_bytes(false, d1);
-    e = cudaFuncSetAttribute(linear_scan_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMost);
-    if (e != cudaSuccess) return e;
     if (pl.nseg > 1) {
-        e = launch_pdl(linear_scan_kernel<false>, dim3(per_seg * pl.nseg), dim3(kScanThreads), smem, stream, pr, err);
+        const cudaError_t e = launch_pdl(linear_scan_kernel<false>, dim3(per_seg * pl.nseg), dim3(kScanThreads), smem, stream, pr, err);
         if (e != cudaSuccess) return e;
     } else {
         linear_scan_kernel<false><<<per_seg, kScanThreads, smem, stream>>>(pr, err);

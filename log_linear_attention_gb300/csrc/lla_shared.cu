@@ -25,32 +25,71 @@ __device__ __forceinline__ bool own_held(int64_t pos, int64_t P, int l) {
     return ((pos >> l) << l) + (int64_t(1) << (l - 1)) > P;
 }
 
-// part[j][bh][x] = sum_i prefix[h][slot j][i][x] q[bh][i]. grid (held prefix slots, H, batch tiles).
-template <typename T>
+// Programmatic dependent launch: grid_dep_launch() lets the next kernel of the stream start, grid_dep_wait()
+// blocks until the one before has completed and its writes are visible.
+__device__ __forceinline__ void grid_dep_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void grid_dep_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
+__device__ __forceinline__ void fma4(float4& o, float w, const float4& x) {
+    o.x += w * x.x;
+    o.y += w * x.y;
+    o.z += w * x.z;
+    o.w += w * x.w;
+}
+
+constexpr int kBatchTile = 32;  // sequences per CTA of the prefix kernel
+
+// part[j][bh][x] = sum_i prefix[h][slot j][i][x] q[bh][i]. grid (held prefix slots, H, batch tiles): each
+// slot is read once for kBatchTile sequences. Thread: four columns, kBatchTile DV4 / kThreads sequences.
+template <typename T, int DV4>
 __global__ void __launch_bounds__(kThreads) shared_prefix(const T* __restrict__ q, const float* __restrict__ prefix,
                                                           float* __restrict__ part, int64_t P, int B, int H, int dk,
-                                                          int dv, int Lp) {
-    __shared__ float qs[8][kMaxDk];
-    const int j = blockIdx.x, h = blockIdx.y, b0 = blockIdx.z * 8, tid = threadIdx.x;
+                                                          int Lp) {
+    constexpr int kGroups = kThreads / DV4;                                    // thread groups over the sequences
+    constexpr int kSeq = kBatchTile / kGroups > 0 ? kBatchTile / kGroups : 1;  // sequences of a thread
+    __shared__ float qs[kMaxDk][kBatchTile + 1];
+    grid_dep_launch();
+    const int j = blockIdx.x, h = blockIdx.y, b0 = blockIdx.z * kBatchTile, tid = threadIdx.x;
     int l = 0;  // the j-th held slot of the walk of P - 1
     for (int left = j; left > 0;) {
         l++;
         if (((P - 1) >> (l - 1)) & 1) left--;
     }
-    const float* S = prefix + (static_cast<int64_t>(h) * Lp + l) * dk * dv;
-    const int nb = B - b0 < 8 ? B - b0 : 8;
-    for (int e = tid; e < nb * dk; e += kThreads)
-        qs[e / dk][e % dk] = load_f(q + (static_cast<int64_t>(b0 + e / dk) * H + h) * dk + e % dk);
+    const int nb = B - b0 < kBatchTile ? B - b0 : kBatchTile;
+    for (int e = tid; e < kBatchTile * dk; e += kThreads) {
+        const int b = e / dk, i = e - b * dk;
+        qs[i][b] = b < nb ? load_f(q + (static_cast<int64_t>(b0 + b) * H + h) * dk + i) : 0.f;
+    }
     __syncthreads();
-    for (int e = tid; e < nb * dv; e += kThreads) {
-        const int b = e / dv, x = e % dv;
-        float s = 0.f;
-        for (int i = 0; i < dk; i++) s += S[static_cast<int64_t>(i) * dv + x] * qs[b][i];
-        part[((static_cast<int64_t>(j) * B + b0 + b) * H + h) * dv + x] = s;
+    const int col4 = tid % DV4, g = tid / DV4;
+    if (g * kSeq >= nb) return;
+    const float4* S =
+        reinterpret_cast<const float4*>(prefix) + (static_cast<int64_t>(h) * Lp + l) * dk * DV4 + col4;
+    float4 o[kSeq];
+#pragma unroll
+    for (int u = 0; u < kSeq; u++) o[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int i0 = 0; i0 < dk; i0 += 8) {
+        float4 x[8];
+#pragma unroll
+        for (int r = 0; r < 8; r++)
+            if (i0 + r < dk) x[r] = S[static_cast<int64_t>(i0 + r) * DV4];
+#pragma unroll
+        for (int r = 0; r < 8; r++)
+            if (i0 + r < dk) {
+#pragma unroll
+                for (int u = 0; u < kSeq; u++) fma4(o[u], qs[i0 + r][g * kSeq + u], x[r]);
+            }
+    }
+#pragma unroll
+    for (int u = 0; u < kSeq; u++) {
+        const int b = g * kSeq + u;
+        if (b < nb)
+            reinterpret_cast<float4*>(part)[((static_cast<int64_t>(j) * B + b0 + b) * H + h) * DV4 + col4] = o[u];
     }
 }
 
-// One CTA per (b, h): the own buckets (carry, decay, read) and the prefix's parts.
+// One CTA per (b, h): the own buckets (carry, decay, read) and the prefix's parts. Level by level, four
+// 16-byte loads of a thread in flight; each held state is read once and written once, past L2's retention.
 template <typename T, int DV4>
 __global__ void __launch_bounds__(kThreads) shared_own(const T* __restrict__ q, const T* __restrict__ k,
                                                        const T* __restrict__ v, const float* __restrict__ log_a,
@@ -61,6 +100,7 @@ __global__ void __launch_bounds__(kThreads) shared_own(const T* __restrict__ q, 
                                                        int* err) {
     constexpr int DV = DV4 * 4;
     constexpr int kRows = kThreads / DV4;
+    constexpr int U = 4;  // rows of a thread in flight
     __shared__ float qs[kMaxDk], ks[kMaxDk], lam[40];
     __shared__ float red[kThreads / 32][DV];
     const int tid = threadIdx.x;
@@ -84,40 +124,57 @@ __global__ void __launch_bounds__(kThreads) shared_own(const T* __restrict__ q, 
     const float a = expf(la);
     const int c = __ffsll(static_cast<long long>(t)) - 1;   // trailing zeros of t (t >= P >= 1)
     const int top = 64 - __clzll(static_cast<long long>(t));  // highest slot that t holds
-    const int col4 = tid % DV4;
+    const int col4 = tid % DV4, row0 = tid / DV4;
     const int64_t msz4 = static_cast<int64_t>(dk) * DV4;
-    float4* S = reinterpret_cast<float4*>(states) + bh * Lmax * msz4;
+    float4* S = reinterpret_cast<float4*>(states) + bh * Lmax * msz4 + col4;
     const T* vp = v + bh * DV + col4 * 4;
     const float4 v4 = make_float4(load_f(vp), load_f(vp + 1), load_f(vp + 2), load_f(vp + 3));
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int i = tid / DV4; i < dk; i += kRows) {
-        const int64_t e = static_cast<int64_t>(i) * DV4 + col4;
-        const float qi = qs[i];
+    for (int i0 = row0; i0 < dk; i0 += U * kRows) {
         if (t > P) {
-            float4 m = make_float4(0.f, 0.f, 0.f, 0.f);
+            float4 m[U];
+#pragma unroll
+            for (int r = 0; r < U; r++) m[r] = make_float4(0.f, 0.f, 0.f, 0.f);
+            // the carry: slots 0..c of t - 1 into slot c + 1, its decay with the others' below
             for (int l = 0; l <= c; l++) {
                 if (!own_held(t - 1, P, l)) continue;
-                const float4 x = S[l * msz4 + e];
-                m.x += x.x; m.y += x.y; m.z += x.z; m.w += x.w;
+                float4 x[U];
+#pragma unroll
+                for (int r = 0; r < U; r++)
+                    if (i0 + r * kRows < dk) x[r] = __ldcs(S + l * msz4 + static_cast<int64_t>(i0 + r * kRows) * DV4);
+#pragma unroll
+                for (int r = 0; r < U; r++)
+                    if (i0 + r * kRows < dk) fma4(m[r], 1.f, x[r]);
             }
-            m.x *= a; m.y *= a; m.z *= a; m.w *= a;
-            S[(c + 1) * msz4 + e] = m;
-            const float w = lam[c + 1] * qi;
-            o.x += w * m.x; o.y += w * m.y; o.z += w * m.z; o.w += w * m.w;
-            for (int l = c + 2; l <= top; l++) {
-                if (!own_held(t - 1, P, l)) continue;
-                float4 x = S[l * msz4 + e];
-                x.x *= a; x.y *= a; x.z *= a; x.w *= a;
-                S[l * msz4 + e] = x;
-                const float wl = lam[l] * qi;
-                o.x += wl * x.x; o.y += wl * x.y; o.z += wl * x.z; o.w += wl * x.w;
+            for (int l = c + 1; l <= top; l++) {
+                if (l > c + 1) {  // a slot that both t - 1 and t hold
+                    if (!own_held(t - 1, P, l)) continue;
+#pragma unroll
+                    for (int r = 0; r < U; r++)
+                        if (i0 + r * kRows < dk) m[r] = __ldcs(S + l * msz4 + static_cast<int64_t>(i0 + r * kRows) * DV4);
+                }
+                const float ll = lam[l];
+#pragma unroll
+                for (int r = 0; r < U; r++) {
+                    if (i0 + r * kRows < dk) {
+                        m[r].x *= a; m[r].y *= a; m[r].z *= a; m[r].w *= a;
+                        __stcs(S + l * msz4 + static_cast<int64_t>(i0 + r * kRows) * DV4, m[r]);
+                        fma4(o, ll * qs[i0 + r * kRows], m[r]);
+                    }
+                }
             }
         }
-        const float ki = ks[i];
-        const float4 x0 = make_float4(ki * v4.x, ki * v4.y, ki * v4.z, ki * v4.w);
-        S[e] = x0;
-        const float w0 = lam[0] * qi;
-        o.x += w0 * x0.x; o.y += w0 * x0.y; o.z += w0 * x0.z; o.w += w0 * x0.w;
+        const float l0 = lam[0];
+#pragma unroll
+        for (int r = 0; r < U; r++) {
+            const int i = i0 + r * kRows;
+            if (i < dk) {
+                const float ki = ks[i];
+                const float4 x0 = make_float4(ki * v4.x, ki * v4.y, ki * v4.z, ki * v4.w);
+                __stcs(S + static_cast<int64_t>(i) * DV4, x0);
+                fma4(o, l0 * qs[i], x0);
+            }
+        }
     }
 #pragma unroll
     for (int off = DV4; off < 32; off <<= 1) {
@@ -133,6 +190,7 @@ __global__ void __launch_bounds__(kThreads) shared_own(const T* __restrict__ q, 
         red[warp][lane * 4 + 2] = o.z;
         red[warp][lane * 4 + 3] = o.w;
     }
+    grid_dep_wait();  // the prefix's parts (this kernel starts beside the one that forms them)
     __syncthreads();
     if (tid < DV) {
         float s = 0.f;
@@ -162,22 +220,32 @@ cudaError_t shared_t(const void* q, const void* k, const void* v, const float* l
                      const float* prefix, int64_t P, int Lp, float* decay, float* states, const int64_t* t, void* out,
                      float* part, int B, int H, int dk, int dv, int Lmax, int* err, cudaStream_t stream) {
     const T* qp = static_cast<const T*>(q);
-    shared_prefix<T><<<dim3(held_slots(P), H, (B + 7) / 8), kThreads, 0, stream>>>(qp, prefix, part, P, B, H, dk, dv,
-                                                                                  Lp);
-    note_launch(stream, "shared_prefix");
-    auto go = [&](auto kern) {
-        kern<<<static_cast<unsigned>(B) * H, kThreads, 0, stream>>>(
-            qp, static_cast<const T*>(k), static_cast<const T*>(v), log_a, lambda, static_cast<const float*>(part),
-            decay, states, t, static_cast<T*>(out), P, B, H, dk, Lmax, err);
+    cudaError_t e = cudaSuccess;
+    auto go = [&](auto pre, auto own) {
+        pre<<<dim3(held_slots(P), H, (B + kBatchTile - 1) / kBatchTile), kThreads, 0, stream>>>(qp, prefix, part, P, B, H,
+                                                                                              dk, Lp);
+        note_launch(stream, "shared_prefix");
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(static_cast<unsigned>(B) * H);
+        cfg.blockDim = dim3(kThreads);
+        cfg.stream = stream;
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[0].val.programmaticStreamSerializationAllowed = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        e = cudaLaunchKernelEx(&cfg, own, qp, static_cast<const T*>(k), static_cast<const T*>(v), log_a, lambda,
+                               static_cast<const float*>(part), decay, states, t, static_cast<T*>(out), P, B, H, dk,
+                               Lmax, err);
+        note_launch(stream, "shared_own");
     };
     switch (dv) {
-        case 16: go(shared_own<T, 4>); break;
-        case 32: go(shared_own<T, 8>); break;
-        case 64: go(shared_own<T, 16>); break;
-        default: go(shared_own<T, 32>); break;
+        case 16: go(shared_prefix<T, 4>, shared_own<T, 4>); break;
+        case 32: go(shared_prefix<T, 8>, shared_own<T, 8>); break;
+        case 64: go(shared_prefix<T, 16>, shared_own<T, 16>); break;
+        default: go(shared_prefix<T, 32>, shared_own<T, 32>); break;
     }
-    note_launch(stream, "shared_own");
-    return cudaGetLastError();
+    return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 }  // namespace
