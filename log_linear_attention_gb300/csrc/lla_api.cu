@@ -709,7 +709,7 @@ int lla_linear_forward(const void* q, const void* k, const void* v, const float*
     if ((st = ws.take(dev, (size_t)H * sq.n_chunks * msz)) != LLA_OK) return st;
     float* states = reinterpret_cast<float*>(ws.p);
     lla::LinStateJobs jobs = {{{k, v, states, state0, state_out, B0 == 1, 0, dk, dv, pieces64(dk) * pieces64(dv)}}, 1};
-    lla::LinScans scans = {{{q, k, v, out, states, 0, 0, dk, dv, pieces64(dv)}}, 1};
+    lla::LinScans scans = {{{q, k, v, out, states, 0, 0, dk, dv}}, 1};
     return ws.give(lla::linear_run(dtype, jobs, scans, sq, log_a, s));
 }
 
@@ -761,7 +761,7 @@ int lla_linear_forward_varlen(const void* q, const void* k, const void* v, const
     sq.coff = coff;
     cudaError_t e = lla::linear_table(cu_seqlens, n_seq, total_T, max_T, tab, coff, nullptr, err, s);
     lla::LinStateJobs jobs = {{{k, v, states, state0, state_out, n0 == 1, 0, dk, dv, pieces64(dk) * pieces64(dv)}}, 1};
-    lla::LinScans scans = {{{q, k, v, out, states, 0, 0, dk, dv, pieces64(dv)}}, 1};
+    lla::LinScans scans = {{{q, k, v, out, states, 0, 0, dk, dv}}, 1};
     if (e == cudaSuccess) e = lla::linear_run(dtype, jobs, scans, sq, log_a, s);
     return ws.give(e);
 }
@@ -809,9 +809,9 @@ int lla_linear_backward(const void* q, const void* k, const void* v, const float
     lla::LinStateJobs jobs = {{{k, v, fw, state0, nullptr, B0 == 1, 0, dk_, dv_, sp},
                                {q, dout, bw, dstate_out, sum ? parts : dstate0, 0, 1, dk_, dv_, sp}},
                               2};
-    lla::LinScans scans = {{{dout, v, k, dq, fw, 1, 0, dv_, dk_, pieces64(dk_)},
-                            {v, dout, q, dk, bw, 1, 1, dv_, dk_, pieces64(dk_)},
-                            {k, q, dout, dv, bw, 0, 1, dk_, dv_, pieces64(dv_)}},
+    lla::LinScans scans = {{{dout, v, k, dq, fw, 1, 0, dv_, dk_},
+                            {v, dout, q, dk, bw, 1, 1, dv_, dk_},
+                            {k, q, dout, dv, bw, 0, 1, dk_, dv_}},
                            3};
     cudaError_t e = lla::linear_run(dtype, jobs, scans, sq, log_a, s);
     if (e == cudaSuccess && sum) e = lla::linear_sum_batch(parts, dstate0, B, (int64_t)H * dk_ * dv_, s);

@@ -28,7 +28,9 @@ namespace lla {
 namespace {
 
 constexpr int kC = 64;         // tokens per chunk
-constexpr int kThreads = 256;  // 16 x 16 threads, each a 4 x 4 piece of a 64 x 64 product
+constexpr int kThreads = 256;
+constexpr int kMulThreads = 128;  // 8 x 16 threads, each an 8 x 4 piece of a 64 x 64 product
+constexpr int kSlab = 32;         // summed indices staged at a time
 constexpr int kLd = kC + 4;    // leading dimension of the transposed tiles (16-byte rows)
 constexpr int kMaxD = 128;
 
@@ -69,24 +71,90 @@ __device__ __forceinline__ bool chunk_at(const LinSeqs& sq, int id, int h, Chunk
     return true;
 }
 
-// acc[i][j] += sum_{k < K} X[k][i0 + i] Y[k][j0 + j]; rows of X and Y are ldx and ldy floats.
-__device__ __forceinline__ void mul44(float (&acc)[4][4], const float* X, int ldx, const float* Y, int ldy, int K) {
-#pragma unroll 4
+// acc[i][j] += sum_{k < K} X[k][i0 + i] Y[k][j0 + j], rows of kLd floats, i0 = 8 (tid / 16), j0 = 4 (tid % 16):
+// four shared-memory wavefronts for 32 FMAs of a warp (4 x 4 pieces took six).
+template <int K>
+__device__ __forceinline__ void mul84(float (&acc)[8][4], const float* X, const float* Y) {
+    X += threadIdx.x / 16 * 8;
+    Y += threadIdx.x % 16 * 4;
+#pragma unroll 8
     for (int k = 0; k < K; k++) {
-        const float4 x = *reinterpret_cast<const float4*>(X + k * ldx);
-        const float4 y = *reinterpret_cast<const float4*>(Y + k * ldy);
-        const float xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
+        const float4 x0 = *reinterpret_cast<const float4*>(X + k * kLd);
+        const float4 x1 = *reinterpret_cast<const float4*>(X + k * kLd + 4);
+        const float4 y = *reinterpret_cast<const float4*>(Y + k * kLd);
+        const float xs[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w}, ys[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
-        for (int i = 0; i < 4; i++)
+        for (int i = 0; i < 8; i++)
 #pragma unroll
             for (int j = 0; j < 4; j++) acc[i][j] += xs[i] * ys[j];
     }
 }
 
-// grid (chunks, H, pieces of 64 x 64 over every job), kThreads. states[job] += nothing: written.
+// Four consecutive columns d..d+3 of a row of D columns, zeros past it; one load where rows keep it aligned.
 template <typename T>
-__global__ void __launch_bounds__(kThreads) lin_chunk_state(LinStateJobs jobs, LinSeqs sq, const float* log_a) {
-    __shared__ __align__(16) float X[kC][kLd], Y[kC][kLd];
+__device__ __forceinline__ float4 load4(const T* row, int d, int D, bool vec) {
+    if (vec && d + 3 < D) {
+        if constexpr (sizeof(T) == 4) {
+            return *reinterpret_cast<const float4*>(row + d);
+        } else {
+            const uint2 u = *reinterpret_cast<const uint2*>(row + d);
+            return make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xffff0000u),
+                               __uint_as_float(u.y << 16), __uint_as_float(u.y & 0xffff0000u));
+        }
+    }
+    return make_float4(d < D ? load_f(row + d) : 0.f, d + 1 < D ? load_f(row + d + 1) : 0.f,
+                       d + 2 < D ? load_f(row + d + 2) : 0.f, d + 3 < D ? load_f(row + d + 3) : 0.f);
+}
+
+// A slab of 2048 values passes through four 16-byte registers of each thread, so that the next slab's loads are in
+// flight while this one is multiplied.
+struct Slab {
+    float4 x[4];
+};
+
+// kSlab columns d0.. of 64 rows, transposed: S[d - d0][i]. Lanes take rows, so that the stores of a warp fall into 32
+// banks. `row` is this thread's row (tid % 64).
+template <typename T>
+__device__ __forceinline__ void fetch_t(Slab& s, const T* row, int d0, int D, bool vec, bool valid) {
+#pragma unroll
+    for (int u = 0; u < 4; u++) {
+        const int d = d0 + (threadIdx.x >> 6) * (kSlab / 2) + 4 * u;
+        s.x[u] = valid && d < D ? load4(row, d, D, vec) : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+}
+__device__ __forceinline__ void put_t(const Slab& s, float (*S)[kLd]) {
+    const int i = threadIdx.x & 63, d = (threadIdx.x >> 6) * (kSlab / 2);
+#pragma unroll
+    for (int u = 0; u < 4; u++) {
+        S[d + 4 * u][i] = s.x[u].x;
+        S[d + 4 * u + 1][i] = s.x[u].y;
+        S[d + 4 * u + 2][i] = s.x[u].z;
+        S[d + 4 * u + 3][i] = s.x[u].w;
+    }
+}
+
+// kSlab rows r0.. of 64 columns c0..: S[r - r0][col]; rows from `rows` on are zeros.
+template <typename T>
+__device__ __forceinline__ void fetch(Slab& s, const T* base, int r0, int rows, int c0, int D, bool vec) {
+#pragma unroll
+    for (int u = 0; u < 4; u++) {
+        const int e = threadIdx.x + u * kMulThreads, r = r0 + (e >> 4), col = c0 + (e & 15) * 4;
+        s.x[u] = r < rows && col < D ? load4(base + static_cast<int64_t>(r) * D, col, D, vec)
+                                     : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+}
+__device__ __forceinline__ void put(const Slab& s, float (*S)[kLd]) {
+#pragma unroll
+    for (int u = 0; u < 4; u++) {
+        const int e = threadIdx.x + u * kMulThreads;
+        *reinterpret_cast<float4*>(&S[e >> 4][(e & 15) * 4]) = s.x[u];
+    }
+}
+
+// grid (chunks, H, pieces of 64 x 64 over every job), kMulThreads.
+template <typename T>
+__global__ void __launch_bounds__(kMulThreads, 4) lin_chunk_state(LinStateJobs jobs, LinSeqs sq, const float* log_a) {
+    __shared__ __align__(16) float X[kSlab][kLd], Y[kSlab][kLd];
     __shared__ float w[kC];
     const int h = blockIdx.y, tid = threadIdx.x;
     int piece = blockIdx.z, j = 0;
@@ -97,26 +165,44 @@ __global__ void __launch_bounds__(kThreads) lin_chunk_state(LinStateJobs jobs, L
     ChunkAt at;
     if (!chunk_at(sq, blockIdx.x, h, &at)) return;
     if (tid < kC) w[tid] = tid < at.n ? gpow(log_a[h], jb.reverse ? tid + 1 : at.n - 1 - tid) : 0.f;
-    __syncthreads();
-    const T* b = static_cast<const T*>(jb.b);
-    const T* c = static_cast<const T*>(jb.c);
-    for (int e = tid; e < kC * 64; e += kThreads) {
-        const int i = e >> 6, d = e & 63;
-        const int64_t row = at.row + i;
-        X[i][d] = (i < at.n && r0 + d < jb.d1) ? load_f(b + row * jb.d1 + r0 + d) : 0.f;
-        Y[i][d] = (i < at.n && c0 + d < jb.d2) ? w[i] * load_f(c + row * jb.d2 + c0 + d) : 0.f;
+    const T* b = static_cast<const T*>(jb.b) + at.row * jb.d1;
+    const T* c = static_cast<const T*>(jb.c) + at.row * jb.d2;
+    const bool v1 = jb.d1 % 4 == 0, v2 = jb.d2 % 4 == 0;
+    float acc[8][4] = {};
+    Slab x, y;
+    fetch(x, b, 0, at.n, r0, jb.d1, v1);
+    fetch(y, c, 0, at.n, c0, jb.d2, v2);
+    for (int t0 = 0; t0 < at.n; t0 += kSlab) {
+        __syncthreads();  // the slabs are free, w is written
+        put(x, X);
+#pragma unroll
+        for (int u = 0; u < 4; u++) {
+            const int r = t0 + ((tid + u * kMulThreads) >> 4);
+            const float f = w[r];
+            if (r < at.n) y.x[u] = make_float4(f * y.x[u].x, f * y.x[u].y, f * y.x[u].z, f * y.x[u].w);
+        }
+        put(y, Y);
+        __syncthreads();
+        if (t0 + kSlab < at.n) {
+            fetch(x, b, t0 + kSlab, at.n, r0, jb.d1, v1);
+            fetch(y, c, t0 + kSlab, at.n, c0, jb.d2, v2);
+        }
+        mul84<kSlab>(acc, &X[0][0], &Y[0][0]);
     }
-    __syncthreads();
-    const int i0 = tid / 16 * 4, j0 = tid % 16 * 4;
-    float acc[4][4] = {};
-    mul44(acc, &X[0][i0], kLd, &Y[0][j0], kLd, kC);
+    const int i0 = tid / 16 * 8, j0 = c0 + tid % 16 * 4;
     float* dst = jb.states + at.state * jb.d1 * jb.d2;
 #pragma unroll
-    for (int i = 0; i < 4; i++)
+    for (int i = 0; i < 8; i++) {
+        if (r0 + i0 + i >= jb.d1) break;
+        float* to = dst + static_cast<int64_t>(r0 + i0 + i) * jb.d2 + j0;
+        if (v2 && j0 + 3 < jb.d2) {
+            *reinterpret_cast<float4*>(to) = make_float4(acc[i][0], acc[i][1], acc[i][2], acc[i][3]);
+        } else {
 #pragma unroll
-        for (int q = 0; q < 4; q++)
-            if (r0 + i0 + i < jb.d1 && c0 + j0 + q < jb.d2)
-                dst[static_cast<int64_t>(r0 + i0 + i) * jb.d2 + c0 + j0 + q] = acc[i][q];
+            for (int q = 0; q < 4; q++)
+                if (j0 + q < jb.d2) to[q] = acc[i][q];
+        }
+    }
 }
 
 // Entering state of every chunk in place of its own, and the leaving state of every sequence.
@@ -159,109 +245,125 @@ __global__ void __launch_bounds__(kThreads) lin_carry(LinStateJobs jobs, LinSeqs
     if (jb.out) jb.out[(static_cast<int64_t>(b) * sq.H + h) * msz + e] = x;
 }
 
-// grid (chunks, H, 64-column pieces over every scan), kThreads.
+// grid (chunks, H, scans), kMulThreads. The weighted scores are formed once and serve every 64 columns of c. Operands
+// pass through two small slabs (35 KB a block with the scores), so that several blocks share an SM; whole tiles in
+// shared memory left two.
 template <typename T>
-__global__ void __launch_bounds__(kThreads) lin_out(LinScans scans, LinSeqs sq, const float* log_a) {
-    extern __shared__ __align__(16) float sm[];
+__global__ void __launch_bounds__(kMulThreads, 4) lin_out(LinScans scans, LinSeqs sq, const float* log_a) {
+    __shared__ __align__(16) float X[kSlab][kLd], Y[kSlab][kLd], Pt[kC][kLd];
     __shared__ float pw[kC + 1];
     const int h = blockIdx.y, tid = threadIdx.x;
-    int piece = blockIdx.z, j = 0;
-    while (piece >= scans.scan[j].pieces) piece -= scans.scan[j++].pieces;
-    const LinScan& sc = scans.scan[j];
-    const int c0 = piece * 64, d1 = sc.d1, d2 = sc.d2;
+    const LinScan& sc = scans.scan[blockIdx.z];
+    const int d1 = sc.d1, d2 = sc.d2;
     ChunkAt at;
     if (!chunk_at(sq, blockIdx.x, h, &at)) return;
     const int n = at.n;
     if (tid <= kC) pw[tid] = gpow(log_a[h], tid);
-    float* A = sm;             // [d1][kLd], a transposed
-    float* Bt = A + d1 * kLd;  // [d1][kLd], b transposed, then X [d1][kLd]
-    float* V = Bt + d1 * kLd;  // [kC][kLd]
-    float* Pt = V + kC * kLd;  // [kC][kLd], weighted scores transposed
-    const T* a = static_cast<const T*>(sc.a);
-    const T* b = static_cast<const T*>(sc.b);
-    const T* c = static_cast<const T*>(sc.c);
-    for (int e = tid; e < kC * d1; e += kThreads) {
-        const int i = e / d1, d = e - i * d1;
-        A[d * kLd + i] = i < n ? load_f(a + (at.row + i) * d1 + d) : 0.f;
-        Bt[d * kLd + i] = i < n ? load_f(b + (at.row + i) * d1 + d) : 0.f;
-    }
-    for (int e = tid; e < kC * 64; e += kThreads) {
-        const int i = e >> 6, d = e & 63;
-        V[i * kLd + d] = (i < n && c0 + d < d2) ? load_f(c + (at.row + i) * d2 + c0 + d) : 0.f;
-    }
-    __syncthreads();
-    const int i0 = tid / 16 * 4, j0 = tid % 16 * 4;
-    float p[4][4] = {};
-    mul44(p, A + i0, kLd, Bt + j0, kLd, d1);
-#pragma unroll
-    for (int i = 0; i < 4; i++)
-#pragma unroll
-        for (int q = 0; q < 4; q++) {
-            const int gap = sc.reverse ? j0 + q - (i0 + i) : i0 + i - (j0 + q);
-            p[i][q] = gap >= 0 ? p[i][q] * pw[gap] : 0.f;
-        }
-    __syncthreads();  // Bt is free
-#pragma unroll
-    for (int q = 0; q < 4; q++)
-        *reinterpret_cast<float4*>(Pt + (j0 + q) * kLd + i0) = make_float4(p[0][q], p[1][q], p[2][q], p[3][q]);
-    // X[d1][64 columns]: the state is [d1][d2], or [d2][d1] where the scan reads its transpose
-    const float* X = sc.states + at.state * d1 * d2;
-    for (int e = tid; e < d1 * 64; e += kThreads) {
-        int d, col;
-        if (sc.state_t) {
-            col = e / d1;
-            d = e - col * d1;
-        } else {
-            d = e >> 6;
-            col = e & 63;
-        }
-        float x = 0.f;
-        if (c0 + col < d2)
-            x = sc.state_t ? X[static_cast<int64_t>(c0 + col) * d1 + d] : X[static_cast<int64_t>(d) * d2 + c0 + col];
-        Bt[d * kLd + col] = x;
-    }
-    __syncthreads();
-    float o[4][4] = {}, far[4][4] = {};
-    mul44(o, Pt + i0, kLd, V + j0, kLd, kC);
-    mul44(far, A + i0, kLd, Bt + j0, kLd, d1);
+    const bool v1 = d1 % 4 == 0, v2 = d2 % 4 == 0;
+    const int row = tid & 63;
+    const T* a = static_cast<const T*>(sc.a) + (at.row + row) * d1;
+    const T* b = static_cast<const T*>(sc.b) + (at.row + row) * d1;
+    const T* c = static_cast<const T*>(sc.c) + at.row * d2;
+    const int i0 = tid / 16 * 8, j0 = tid % 16 * 4;
     T* out = static_cast<T*>(sc.out);
+    const float* state = sc.states + at.state * d1 * d2;
+    // steps: nd slabs of a and b (scores), then for every 64 columns of c nd slabs of a and the entering state and nt
+    // slabs of c
+    const int nd = (d1 + kSlab - 1) / kSlab, nt = (n + kSlab - 1) / kSlab, per = nd + nt;
+    const int steps = nd + (d2 + 63) / 64 * per;
+    Slab x, y;
+    auto get = [&](int st) {
+        if (st < nd) {
+            fetch_t(x, a, st * kSlab, d1, v1, row < n);
+            fetch_t(y, b, st * kSlab, d1, v1, row < n);
+            return;
+        }
+        const int c0 = (st - nd) / per * 64, u = (st - nd) % per;
+        if (u < nd) {
+            fetch_t(x, a, u * kSlab, d1, v1, row < n);
+            // the entering state is [d1][d2], or [d2][d1] where the scan reads its transpose
+            if (sc.state_t) fetch_t(y, state + static_cast<int64_t>(c0 + row) * d1, u * kSlab, d1, v1, c0 + row < d2);
+            else fetch(y, state, u * kSlab, d1, c0, d2, v2);
+        } else {
+            fetch(y, c, (u - nd) * kSlab, n, c0, d2, v2);
+        }
+    };
+    get(0);
+    float o[8][4] = {};
+    for (int st = 0; st < steps; st++) {
+        const int u = st < nd ? st : (st - nd) % per;  // step of its group
+        const bool scores = st < nd, near = !scores && u >= nd;
+        __syncthreads();
+        if (!near) put_t(x, X);
+        if (scores || (!near && sc.state_t)) put_t(y, Y);
+        else put(y, Y);
+        __syncthreads();
+        if (st + 1 < steps) get(st + 1);
+        mul84<kSlab>(o, near ? &Pt[(u - nd) * kSlab][0] : &X[0][0], &Y[0][0]);
+        if (scores && u == nd - 1) {
 #pragma unroll
-    for (int i = 0; i < 4; i++) {
-        const int r = i0 + i;
-        if (r >= n) continue;
-        const float f = pw[sc.reverse ? n - 1 - r : r + 1];
+            for (int q = 0; q < 4; q++) {
 #pragma unroll
-        for (int q = 0; q < 4; q++)
-            if (c0 + j0 + q < d2) store_f(out + (at.row + r) * d2 + c0 + j0 + q, o[i][q] + f * far[i][q]);
+                for (int i = 0; i < 8; i++) {
+                    const int gap = sc.reverse ? j0 + q - (i0 + i) : i0 + i - (j0 + q);
+                    o[i][q] = gap >= 0 ? o[i][q] * pw[gap] : 0.f;
+                }
+                float4* to = reinterpret_cast<float4*>(&Pt[j0 + q][i0]);
+                to[0] = make_float4(o[0][q], o[1][q], o[2][q], o[3][q]);
+                to[1] = make_float4(o[4][q], o[5][q], o[6][q], o[7][q]);
+#pragma unroll
+                for (int i = 0; i < 8; i++) o[i][q] = 0.f;
+            }
+        } else if (!scores && u == nd - 1) {
+#pragma unroll
+            for (int i = 0; i < 8; i++) {
+                const int r = i0 + i;
+                const float f = r < n ? pw[sc.reverse ? n - 1 - r : r + 1] : 0.f;
+#pragma unroll
+                for (int q = 0; q < 4; q++) o[i][q] *= f;
+            }
+        } else if (near && u == per - 1) {
+            const int c0 = (st - nd) / per * 64;
+#pragma unroll
+            for (int i = 0; i < 8; i++) {
+                const int r = i0 + i;
+                T* to = out + (at.row + r) * d2 + c0 + j0;
+                if (r < n && v2 && c0 + j0 + 3 < d2) {
+                    if constexpr (sizeof(T) == 4) {
+                        *reinterpret_cast<float4*>(to) = make_float4(o[i][0], o[i][1], o[i][2], o[i][3]);
+                    } else {
+                        const __nv_bfloat162 lo = __floats2bfloat162_rn(o[i][0], o[i][1]),
+                                             hi = __floats2bfloat162_rn(o[i][2], o[i][3]);
+                        *reinterpret_cast<uint2*>(to) = make_uint2(*reinterpret_cast<const uint32_t*>(&lo),
+                                                                   *reinterpret_cast<const uint32_t*>(&hi));
+                    }
+                } else if (r < n) {
+#pragma unroll
+                    for (int q = 0; q < 4; q++)
+                        if (c0 + j0 + q < d2) store_f(to + q, o[i][q]);
+                }
+#pragma unroll
+                for (int q = 0; q < 4; q++) o[i][q] = 0.f;
+            }
+        }
     }
 }
-
-size_t out_smem(int d1) { return static_cast<size_t>(2 * d1 + 2 * kC) * kLd * sizeof(float); }
 
 template <typename T>
 cudaError_t run_t(const LinStateJobs& jobs, const LinScans& scans, const LinSeqs& sq, const float* log_a,
                   cudaStream_t stream) {
     const int batch = sq.tab ? sq.n : sq.n_chunks / sq.N;
-    int pieces = 0, msz = 0, d1 = 0;
+    int pieces = 0, msz = 0;
     for (int i = 0; i < jobs.count; i++) {
         pieces += jobs.job[i].pieces;
         msz = jobs.job[i].d1 * jobs.job[i].d2;  // every job has the same d1 x d2
     }
-    lin_chunk_state<T><<<dim3(sq.n_chunks, sq.H, pieces), kThreads, 0, stream>>>(jobs, sq, log_a);
+    lin_chunk_state<T><<<dim3(sq.n_chunks, sq.H, pieces), kMulThreads, 0, stream>>>(jobs, sq, log_a);
     note_launch(stream, "lin_chunk_state");
     lin_carry<<<dim3((msz + kThreads - 1) / kThreads, batch * sq.H, jobs.count), kThreads, 0, stream>>>(jobs, sq,
                                                                                                        log_a);
     note_launch(stream, "lin_carry");
-    pieces = 0;
-    for (int i = 0; i < scans.count; i++) {
-        pieces += scans.scan[i].pieces;
-        if (scans.scan[i].d1 > d1) d1 = scans.scan[i].d1;
-    }
-    const size_t smem = out_smem(d1);
-    cudaError_t e = cudaFuncSetAttribute(lin_out<T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         static_cast<int>(out_smem(kMaxD)));
-    if (e != cudaSuccess) return e;
-    lin_out<T><<<dim3(sq.n_chunks, sq.H, pieces), kThreads, smem, stream>>>(scans, sq, log_a);
+    lin_out<T><<<dim3(sq.n_chunks, sq.H, scans.count), kMulThreads, 0, stream>>>(scans, sq, log_a);
     note_launch(stream, "lin_out");
     return cudaGetLastError();
 }

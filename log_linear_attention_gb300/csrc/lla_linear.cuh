@@ -38,7 +38,7 @@ struct LinScan {
     const void *a, *b, *c;
     void* out;
     const float* states;
-    int state_t, reverse, d1, d2, pieces;
+    int state_t, reverse, d1, d2;
 };
 struct LinScans {
     LinScan scan[3];
