@@ -700,11 +700,12 @@ int lla_linear_forward(const void* q, const void* k, const void* v, const float*
     const lla::LinSeqs sq = dense_seqs(B, H, T);
     PoolBuffer ws(s);
     lla::LinTcPlan tp;
-    if (lla::linear_tc_supported(dtype, dk, dv) && lla::linear_tc_plan(&tp, B, H, T, (int64_t)B * H * T, pieces64(dv))) {
+    if (lla::linear_tc_supported(dtype, dk, dv) && lla::linear_tc_plan(&tp, B, H, T, (int64_t)B * H * T, pieces64(dv), false)) {
         if ((st = ws.take(dev, tp.seg_bytes)) != LLA_OK) return st;
         const lla::LinTcMap maps[3] = {{q, dk}, {k, dk}, {v, dv}};
-        const lla::LinTcScan scan = {0, 1, 2, out, state0, state_out, B0 == 1, 0, 0, dk, dv, 0, 0};
-        return ws.give(lla::linear_tc_run(tp, maps, 3, &scan, 1, sq, log_a, reinterpret_cast<float*>(ws.p), err, s));
+        const lla::LinTcScan scan = {0, 1, 2, out, state0, state_out, B0 == 1, 0, dk, dv, pieces64(dv), 0, 0};
+        return ws.give(lla::linear_tc_run(tp, maps, 3, &scan, 1, sq, log_a, reinterpret_cast<float*>(ws.p), nullptr,
+                                          err, s));
     }
     if ((st = ws.take(dev, (size_t)H * sq.n_chunks * msz)) != LLA_OK) return st;
     float* states = reinterpret_cast<float*>(ws.p);
@@ -737,7 +738,7 @@ int lla_linear_forward_varlen(const void* q, const void* k, const void* v, const
     PoolBuffer ws(s);
     lla::LinTcPlan tp;
     if (lla::linear_tc_supported(dtype, dk, dv) &&
-        lla::linear_tc_plan(&tp, n_seq, H, max_T, (int64_t)H * total_T, pieces64(dv))) {
+        lla::linear_tc_plan(&tp, n_seq, H, max_T, (int64_t)H * total_T, pieces64(dv), false)) {
         if ((st = ws.take(dev, tab_b + 2 * off_b + tp.seg_bytes)) != LLA_OK) return st;
         int2* tab = reinterpret_cast<int2*>(ws.p);
         int* coff = reinterpret_cast<int*>(ws.p + tab_b);
@@ -747,10 +748,10 @@ int lla_linear_forward_varlen(const void* q, const void* k, const void* v, const
         sq.order = order;
         cudaError_t e = lla::linear_table(cu_seqlens, n_seq, total_T, max_T, tab, coff, order, err, s);
         const lla::LinTcMap maps[3] = {{q, dk}, {k, dk}, {v, dv}};
-        const lla::LinTcScan scan = {0, 1, 2, out, state0, state_out, n0 == 1, 0, 0, dk, dv, 0, 0};
+        const lla::LinTcScan scan = {0, 1, 2, out, state0, state_out, n0 == 1, 0, dk, dv, pieces64(dv), 0, 0};
         if (e == cudaSuccess)
             e = lla::linear_tc_run(tp, maps, 3, &scan, 1, sq, log_a,
-                                   reinterpret_cast<float*>(ws.p + tab_b + 2 * off_b), err, s);
+                                   reinterpret_cast<float*>(ws.p + tab_b + 2 * off_b), nullptr, err, s);
         return ws.give(e);
     }
     if ((st = ws.take(dev, tab_b + off_b + (size_t)H * sq.n_chunks * msz)) != LLA_OK) return st;
@@ -787,16 +788,20 @@ int lla_linear_backward(const void* q, const void* k, const void* v, const float
     PoolBuffer ws(s);
     lla::LinTcPlan tp;
     if (lla::linear_tc_supported(dtype, dk_, dv_) &&
-        lla::linear_tc_plan(&tp, B, H, T, (int64_t)B * H * T, 2 * pieces64(dk_) + pieces64(dv_))) {
-        if ((st = ws.take(dev, sum_b + tp.seg_bytes)) != LLA_OK) return st;
+        lla::linear_tc_plan(&tp, B, H, T, (int64_t)B * H * T, 2 * pieces64(dv_), true)) {
+        const size_t seg_b = up256(tp.seg_bytes);
+        if ((st = ws.take(dev, sum_b + seg_b + lla::linear_grad_state_bytes(B * H, T, dv_))) != LLA_OK) return st;
         float* parts = reinterpret_cast<float*>(ws.p);
+        void* states = ws.p + sum_b + seg_b;
+        const int tiles = pieces64(dv_), chunks = (T - 1) / 128 + 1;
         const lla::LinTcMap maps[4] = {{q, dk_}, {k, dk_}, {v, dv_}, {dout, dv_}};
-        const lla::LinTcScan scans[3] = {
-            {3, 2, 1, dq, state0, nullptr, B0 == 1, 1, 0, dv_, dk_, 0, 0},
-            {2, 3, 0, dk, dstate_out, nullptr, 0, 1, 1, dv_, dk_, 0, 0},
-            {1, 0, 3, dv, dstate_out, sum ? parts : dstate0, 0, 0, 1, dk_, dv_, 0, 0}};
-        cudaError_t e = lla::linear_tc_run(tp, maps, 4, scans, 3, sq, log_a, reinterpret_cast<float*>(ws.p + sum_b),
-                                           err, s);
+        const lla::LinTcScan scans[2] = {
+            {0, 1, 2, nullptr, state0, nullptr, B0 == 1, 0, dk_, dv_, tiles, 0, 0},
+            {0, 0, 3, nullptr, dstate_out, sum ? parts : dstate0, 0, 1, dk_, dv_, tiles, B * H * chunks, 0}};
+        cudaError_t e = lla::linear_tc_run(tp, maps, 4, scans, 2, sq, log_a, reinterpret_cast<float*>(ws.p + sum_b),
+                                           states, err, s);
+        if (e == cudaSuccess)
+            e = lla::linear_tc_grads(q, k, v, dout, log_a, states, dq, dk, dv, B * H, H, T, dk_, dv_, err, s);
         if (e == cudaSuccess && sum) e = lla::linear_sum_batch(parts, dstate0, B, (int64_t)H * dk_ * dv_, s);
         return ws.give(e);
     }

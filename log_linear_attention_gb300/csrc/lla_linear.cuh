@@ -62,10 +62,12 @@ struct LinTcMap {
 struct LinTcScan {
     int ia, ib, ic;
     void* out;
-    const float* in;  // entering state [batch or 1][H], each [d1][d2] (in_t: [d2][d1]), or null for zeros
+    const float* in;  // entering state [batch or 1][H][d1][d2], or null for zeros
     float* leave;     // leaving state [batch][H][d1][d2], or null
-    int in_shared, in_t, reverse, d1, d2;
-    int tiles, seg_base;  // filled by linear_tc_run
+    int in_shared, reverse, d1, d2;
+    int tiles;        // 64-column tiles of c
+    int states_base;  // first (b, h, chunk) of this scan in `states`
+    int seg_base;     // filled by linear_tc_run
 };
 struct LinTcPlan {
     int batch;
@@ -74,10 +76,19 @@ struct LinTcPlan {
     size_t seg_bytes;
 };
 bool linear_tc_supported(int dtype, int dk, int dv);
-// rows: token rows of the call; tiles: 64-column tiles over all scans of one head
-bool linear_tc_plan(LinTcPlan* plan, int batch, int H, int T, int64_t rows, int tiles);
+// rows: token rows of the call; tiles: 64-column tiles over all scans of one head; states: only the states are formed
+bool linear_tc_plan(LinTcPlan* plan, int batch, int H, int T, int64_t rows, int tiles, bool states);
+// One forward scan (states null), or up to two of either direction (dense) that leave the state entering each
+// chunk, bf16 [scan][b, h][chunk][tile][128][64], in `states`.
 cudaError_t linear_tc_run(const LinTcPlan& plan, const LinTcMap* maps, int n_maps, const LinTcScan* scans, int count,
-                          const LinSeqs& sq, const float* log_a, float* seg, int* err, cudaStream_t stream);
+                          const LinSeqs& sq, const float* log_a, float* seg, void* states, int* err,
+                          cudaStream_t stream);
+// Gradients from the states entering each chunk (lla_linear_grad.cu): fw of k, v forwards and bw of q, dout backwards,
+// both as linear_tc_run leaves them, in one buffer.
+size_t linear_grad_state_bytes(int BH, int T, int dv);
+cudaError_t linear_tc_grads(const void* q, const void* k, const void* v, const void* dout, const float* log_a,
+                            const void* states, void* dq, void* dk, void* dv, int BH, int H, int T, int d_k, int d_v,
+                            int* err, cudaStream_t stream);
 
 size_t shared_workspace_bytes(int B, int H, int dv, int64_t prefix_len);
 cudaError_t decode_step_shared(int dtype, const void* q, const void* k, const void* v, const float* log_a,

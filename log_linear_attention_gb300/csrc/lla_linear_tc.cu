@@ -1,7 +1,6 @@
 // Linear attention with one decay per head on tensor cores: bf16 rows, dk and dv multiples of 8.
 //
-// One kernel walks a scan (see lla_linear.cu: out_t = S_t^T a_t, S_t = g S_{t-1} + b_t c_t^T, forwards
-// or backwards in time) over one (sequence, head, 64 columns of c) in chunks of 128 tokens. The state
+// One kernel walks a scan (see lla_linear.cu: out_t = S_t^T a_t, S_t = g S_{t-1} + b_t c_t^T) over one (sequence, head, 64 columns of c) in chunks of 128 tokens. The state
 // (d1 x 64, fp32) never leaves the registers of four warps. Per chunk, n valid rows:
 //     scores  A B^T                      [128 x 128]  -> TMEM
 //     own     B^T [hi | mid + lo]        [d1 x 128]   -> TMEM, w o C cut into three bf16 parts, so that the
@@ -9,14 +8,15 @@
 //     far     A X                        [128 x 64]   X = entering state, rounded to bf16
 //     near    P C                        [128 x 64]   P = scores o g^|i-j|, bf16, in TMEM
 //     out_i = near_i + f_i far_i,   X <- g^n X + own
-// with w_i = g^(n-1-i), f_i = g^(i+1) forwards and w_i = g^(i+1), f_i = g^(n-1-i) backwards. P and X are
+// with w_i = g^(n-1-i), f_i = g^(i+1) (states formed backwards: w_i = g^(i+1)). P and X are
 // rounded to bf16 as the operands of a bf16 product must be (2^-8 of each term, as the output itself);
 // scores, sums, weights and the state stay fp32.
 //
 // Heads alone do not fill the GPU when they are few, so a scan may be cut into segments, one CTA each: a first
-// launch (kStateOnly) forms the own states of pieces of every segment but the last (smaller than segments, as
+// launch (kPieces) forms the own states of pieces of every segment but the last (smaller than segments, as
 // it is launched without the last segment's share), and each segment's CTA sums those before it, decayed, in
-// order.
+// order. kFull does all of the above, forwards; kStates only forms the states, forwards or backwards, and
+// writes the one that enters each chunk in bf16 for the kernel of the gradients (lla_linear_grad.cu).
 //
 // Rows of a chunk behind its sequence's end (another sequence's, when packed) are set to zero in shared
 // memory before any product sums over them. Every wait is bounded; on overrun the kernel records
@@ -24,15 +24,13 @@
 #include <atomic>
 #include <cmath>
 
-#include "lla_linear.cuh"
-#include "lla_tc_ptx.cuh"
+#include "lla_linear_tc.cuh"
 
 namespace lla {
 namespace {
 
 constexpr int kScanThreads = 1024;
 constexpr int kMaxStages = 3;
-constexpr int kDepth = 64;  // columns of c per CTA
 constexpr int kWcBytes = 3 * kPanelBytes;
 constexpr int kSmemMost = 232448 - 2048;  // 227 KB less the static part
 
@@ -41,143 +39,23 @@ constexpr int kSmemMost = 232448 - 2048;  // 227 KB less the static part
 // high part's product, then that of the middle and low parts
 constexpr uint32_t kColS = 0, kColNear = 256, kColFar = 320, kColOwn = 384;
 
+enum { kFull, kPieces, kStates };  // what a launch forms: see above
+
 struct ScanParams {
     CUtensorMap map[4];
-    LinTcScan scan[3];
+    LinTcScan scan[2];
     const float* log_a;
-    float* seg;  // pieces' own states
+    float* seg;             // pieces' own states
+    __nv_bfloat16* states;  // kStates: the entering states
     LinSeqs sq;
     int count, nseg, seg_chunks, npiece, piece_chunks, packed, batch;
 };
 
-__device__ __forceinline__ float gpow(float la, int n) { return n == 0 ? 1.f : expf(la * static_cast<float>(n)); }
-
-__device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, uint64_t* bar, int x, int y, int z) {
-    asm volatile(
-        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(
-            smem_u32(dst)),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z)
-        : "memory");
-}
-
-// D[tmem] (+)= A[tmem] * B[smem]: A's row i is lane i, two bf16 K elements per 32-bit column.
-__device__ __forceinline__ void mma_bf16_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
-                                            uint32_t accumulate) {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-        "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
-        : "memory");
-}
-
-__device__ __forceinline__ void tmem_st16_issue(uint32_t taddr, const uint32_t* r) {
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
-        "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
-        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
-        "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
-        : "memory");
-}
-__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
-
-// Two fp32 values in one register pair: one instruction for both (issue slots are what the roles share).
-using f32x2 = unsigned long long;
-__device__ __forceinline__ f32x2 pair2(float lo, float hi) {
-    f32x2 r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
-    return r;
-}
-__device__ __forceinline__ float2 split2(f32x2 x) {
-    float2 r;
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(x));
-    return r;
-}
-__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
-    f32x2 r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
-    f32x2 r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-    return r;
-}
-__device__ __forceinline__ uint32_t pack_bf16(f32x2 x) {
-    const float2 f = split2(x);
-    return pack_bf16(f.x, f.y);
-}
-
-// 16 consecutive fp32 TMEM columns at each of two places, as pairs: both loads in flight, one wait.
-__device__ __forceinline__ void tmem_ld16x2(uint32_t ta, uint32_t tb, f32x2* va, f32x2* vb) {
-    uint32_t r[16], q[16];
-    tmem_ld16_issue(ta, r);
-    tmem_ld16_issue(tb, q);
-    tmem_ld16_wait(r);
-    tmem_ld16_wait(q);  // nothing is left to wait for: keeps the uses of q behind the wait
-#pragma unroll
-    for (int i = 0; i < 8; i++) {
-        va[i] = pair2(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1]));
-        vb[i] = pair2(__uint_as_float(q[2 * i]), __uint_as_float(q[2 * i + 1]));
-    }
-}
-
-// One lane of a converged warp; code behind it counts as uniform, so descriptors stay in uniform registers.
-__device__ __forceinline__ bool elect_one() {
-    uint32_t p;
-    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
-    return p != 0;
-}
-
-// Up to kTries tests of a barrier's phase, three instructions each: a test suspends the thread for some hundred
-// cycles only, and two dozen waiting warps that did more between tests took most of the issue slots.
-constexpr uint32_t kTries = 1024;
-__device__ __forceinline__ bool mbar_try_many(uint64_t* bar, uint32_t parity) {
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p, q;\n\t.reg .u32 i;\n\tmov.u32 i, %4;\n"
-        "TRY:\n\t"
-        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
-        "@p bra DONE;\n\t"
-        "sub.u32 i, i, 1;\n\t"
-        "setp.ne.u32 q, i, 0;\n\t"
-        "@q bra TRY;\n"
-        "DONE:\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(smem_u32(bar)), "r"(parity), "n"(kSuspendNs), "n"(kTries)
-        : "memory");
-    return ok != 0;
-}
-
-// Bounded waits. They give up when another role has.
-__device__ __noinline__ bool wait_long(uint64_t* bar, uint32_t parity, volatile int* fail) {
-    const long long start = clock64();
-    while (!mbar_try_many(bar, parity)) {
-        if (*fail || clock64() - start > kWaitCycles) return false;
-    }
-    return true;
-}
-__device__ __forceinline__ bool wait_one(uint64_t* bar, uint32_t parity, volatile int* fail) {
-    return mbar_try_many(bar, parity) || wait_long(bar, parity, fail);
-}
-__device__ __noinline__ bool wait_long_warp(uint64_t* bar, uint32_t parity, volatile int* fail) {
-    const long long start = clock64();
-    while (true) {
-        const bool done = mbar_try_many(bar, parity);
-        if (__all_sync(0xffffffffu, done)) return true;
-        const bool late = *fail || clock64() - start > kWaitCycles;
-        if (__any_sync(0xffffffffu, late)) return false;
-    }
-}
-__device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, volatile int* fail) {
-    return __all_sync(0xffffffffu, mbar_try_many(bar, parity)) || wait_long_warp(bar, parity, fail);
-}
-
 // Warps: 0 and 2 TMA producers, 1 TMEM owner and MMA issuer, 4..11 P (every other block of 32 keys), 12..19 state
 // (32 columns each), 20..23 write out, 24..31 split w o C. Warp w reaches TMEM lanes 32 (w % 4)..+31: rows of scores and out, rows of the state.
-template <bool kStateOnly>
+template <int kMode>
 __global__ void __launch_bounds__(kScanThreads, 1) linear_scan_kernel(const __grid_constant__ ScanParams pr, int* err) {
+    constexpr bool kStateOnly = kMode != kFull;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     __shared__ uint64_t qk_full[kMaxStages], v_full[kMaxStages], qk_free[kMaxStages], v_free[kMaxStages];
@@ -193,7 +71,7 @@ __global__ void __launch_bounds__(kScanThreads, 1) linear_scan_kernel(const __gr
     grid_dep_launch();
     // ---- which scan, 64 columns, segment, sequence and head
     int blk = blockIdx.x, si = 0;
-    const int ncta = kStateOnly ? pr.npiece : pr.nseg;  // of one sequence, head and 64 columns
+    const int ncta = kMode == kPieces ? pr.npiece : pr.nseg;  // of one sequence, head and 64 columns
     while (si + 1 < pr.count && blk >= pr.batch * pr.sq.H * ncta * pr.scan[si].tiles)
         blk -= pr.batch * pr.sq.H * ncta * pr.scan[si++].tiles;
     const LinTcScan& sc = pr.scan[si];
@@ -213,11 +91,11 @@ __global__ void __launch_bounds__(kScanThreads, 1) linear_scan_kernel(const __gr
     const int z = pr.packed ? h : bh;  // outermost coordinate of the tensor maps
     const int nch = (len + kTile - 1) / kTile;
     const int have = nch <= pr.seg_chunks ? 1 : (nch + pr.seg_chunks - 1) / pr.seg_chunks;
-    const int span = kStateOnly ? pr.piece_chunks : pr.seg_chunks;
+    const int span = kMode == kPieces ? pr.piece_chunks : pr.seg_chunks;
     const int p0 = g * span;
-    if (kStateOnly ? p0 >= (have - 1) * pr.seg_chunks : g >= have) return;
+    if (kMode == kPieces ? p0 >= (have - 1) * pr.seg_chunks : g >= have) return;
     const int n = nch - p0 < span ? nch - p0 : span;  // chunks of this CTA
-    const bool rev = sc.reverse != 0;
+    const bool rev = kStateOnly && sc.reverse != 0;
     auto chunk_of = [&](int j) { return rev ? nch - 1 - (p0 + j) : p0 + j; };
     auto rows_of = [&](int c) { return len - c * kTile < kTile ? len - c * kTile : kTile; };
     // tokens ahead of the p-th chunk in scan order
@@ -256,10 +134,10 @@ __global__ void __launch_bounds__(kScanThreads, 1) linear_scan_kernel(const __gr
     if (warp == 1) tmem_alloc(&tmem_base_sh, 512);
     const float la = pr.log_a[h];
     if (tid >= 64 && tid < 64 + 129) pw[tid - 64] = gpow(la, tid - 64);
-    if (tid >= 256 && tid < 288) colw[tid - 256] = gpow(la, rev ? tid - 256 : 31 - (tid - 256));
+    if (tid >= 256 && tid < 288) colw[tid - 256] = gpow(la, 31 - (tid - 256));
     if (tid >= 320 && tid < 383) {
         const int u = tid - 320 - 31;  // r - c
-        diag[tid - 320] = rev ? (u <= 0 ? gpow(la, -u) : 0.f) : (u >= 0 ? gpow(la, u) : 0.f);
+        diag[tid - 320] = u >= 0 ? gpow(la, u) : 0.f;
     }
     tc_fence_before();
     __syncthreads();
@@ -269,7 +147,7 @@ __global__ void __launch_bounds__(kScanThreads, 1) linear_scan_kernel(const __gr
     float* seg0 = pr.seg + (static_cast<int64_t>(sc.seg_base) +
                             static_cast<int64_t>(bh) * pr.npiece * sc.tiles + tile) * (kDepth * kTile);
     const int64_t seg_step = static_cast<int64_t>(sc.tiles) * (kDepth * kTile);
-    if (!kStateOnly && g > 0) {
+    if (kMode != kPieces && g > 0) {
         // the pieces before this segment, decayed to its start and summed in order
         float4 sum[2] = {};
         const int np_before = p0 / pr.piece_chunks;
@@ -427,7 +305,7 @@ __global__ void __launch_bounds__(kScanThreads, 1) linear_scan_kernel(const __gr
 #pragma unroll 1
             for (int cb = (warp - 4) >> 2; cb < 4; cb += 2) {
                 uint32_t r[16];
-                if (rev ? cb < w : cb > w) {  // wholly on the other side of time
+                if (cb > w) {  // wholly ahead in time
 #pragma unroll
                     for (int i = 0; i < 16; i++) r[i] = 0u;
                 } else {
@@ -443,7 +321,7 @@ __global__ void __launch_bounds__(kScanThreads, 1) linear_scan_kernel(const __gr
 #pragma unroll
                         for (int i = 0; i < 16; i++) r[i] = pack_bf16(x[2 * i], x[2 * i + 1]);
                     } else {
-                        const float rw = pw[rev ? 32 * cb - (32 * w + lane) : 32 * w + lane - 32 * cb - 31];
+                        const float rw = pw[32 * w + lane - 32 * cb - 31];
                         const f32x2 rw2 = pair2(rw, rw);
                         const ulonglong2* cw = reinterpret_cast<const ulonglong2*>(colw);
 #pragma unroll
@@ -473,28 +351,22 @@ __global__ void __launch_bounds__(kScanThreads, 1) linear_scan_kernel(const __gr
         const uint32_t lanes = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
         const int cw = (warp - 12) / 4 * 32, cg = c0 + cw;  // first of this warp's columns, in the tile and in c
         f32x2 x2[16];  // column pairs
-        if (!kStateOnly) {
+        if (kMode != kPieces) {
             float x[32];
 #pragma unroll
             for (int c = 0; c < 32; c++) x[c] = 0.f;
             if (sc.in && d < d1) {
                 const float* in = sc.in + static_cast<int64_t>(sc.in_shared ? h : bh) * d1 * d2;
                 const float f = gpow(la, before(p0));
-                if (sc.in_t) {
 #pragma unroll
-                    for (int c = 0; c < 32; c++)
-                        if (cg + c < d2) x[c] = f * in[static_cast<int64_t>(cg + c) * d1 + d];
-                } else {
-#pragma unroll
-                    for (int c = 0; c < 32; c += 4)
-                        if (cg + c < d2) {
-                            const float4 y = *reinterpret_cast<const float4*>(in + static_cast<int64_t>(d) * d2 + cg + c);
-                            x[c] = f * y.x;
-                            x[c + 1] = f * y.y;
-                            x[c + 2] = f * y.z;
-                            x[c + 3] = f * y.w;
-                        }
-                }
+                for (int c = 0; c < 32; c += 4)
+                    if (cg + c < d2) {
+                        const float4 y = *reinterpret_cast<const float4*>(in + static_cast<int64_t>(d) * d2 + cg + c);
+                        x[c] = f * y.x;
+                        x[c + 1] = f * y.y;
+                        x[c + 2] = f * y.z;
+                        x[c + 3] = f * y.w;
+                    }
             }
             if (g > 0) {
                 const float* sum = reinterpret_cast<const float*>(wc) + d;
@@ -519,9 +391,26 @@ __global__ void __launch_bounds__(kScanThreads, 1) linear_scan_kernel(const __gr
             __syncwarp();
             if (lane == 0) mbar_arrive(&x_ready);
         };
-        if (!kStateOnly && n > 0) put_x();
+        if (kMode == kFull && n > 0) put_x();
+        if (kMode == kStates) {  // the sum of the pieces is read
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&x_ready);
+        }
         bool ok = true;
         for (int j = 0; j < n; j++) {
+            if (kMode == kStates && d < 64 * np) {
+                // the entering state of this chunk, [128 rows][64 columns]
+                __nv_bfloat16* to =
+                    pr.states + ((static_cast<int64_t>(sc.states_base) + static_cast<int64_t>(bh) * nch + chunk_of(j)) *
+                                     sc.tiles + tile) * (kTile * kDepth) + d * kDepth + cw;
+#pragma unroll
+                for (int c = 0; c < 2; c++) {
+                    uint32_t o[8];
+#pragma unroll
+                    for (int i = 0; i < 8; i++) o[i] = pack_bf16(x2[8 * c + i]);
+                    store32(to + 16 * c, o, true, true);
+                }
+            }
             if (!wait_warp(&own_full, j & 1, fail)) {
                 if (lane == 0) fail_now();
                 ok = false;
@@ -544,7 +433,7 @@ __global__ void __launch_bounds__(kScanThreads, 1) linear_scan_kernel(const __gr
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&own_read);
-            if (!kStateOnly && j + 1 < n) {
+            if (kMode == kFull && j + 1 < n) {
                 if (!wait_warp(&x_free, j & 1, fail)) {
                     if (lane == 0) fail_now();
                     ok = false;
@@ -554,7 +443,7 @@ __global__ void __launch_bounds__(kScanThreads, 1) linear_scan_kernel(const __gr
             }
         }
         if (ok) {
-            if (kStateOnly) {
+            if (kMode == kPieces) {
                 float* sg = seg0 + static_cast<int64_t>(g) * seg_step + d;
 #pragma unroll
                 for (int c = 0; c < 16; c++) {
@@ -583,7 +472,7 @@ __global__ void __launch_bounds__(kScanThreads, 1) linear_scan_kernel(const __gr
             }
             tc_fence_after();
             const int ch = chunk_of(j), nr = rows_of(ch);
-            const float f = row < nr ? pw[rev ? nr - 1 - row : row + 1] : 0.f;
+            const float f = row < nr ? pw[row + 1] : 0.f;
             const f32x2 f2 = pair2(f, f);
             __nv_bfloat16* orow = out + (static_cast<int64_t>(ch) * kTile + row) * d2;
 #pragma unroll 1
@@ -598,17 +487,7 @@ __global__ void __launch_bounds__(kScanThreads, 1) linear_scan_kernel(const __gr
                 uint32_t o[8];
 #pragma unroll
                 for (int i = 0; i < 8; i++) o[i] = pack_bf16(fma2(f2, y[i], a[i]));
-                if (row < nr && c0 + c < d2) {
-                    // a whole 32-byte sector of the row in one store; 16 bytes each where rows are not so aligned
-                    if (wide) {
-                        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(orow + c), "r"(o[0]),
-                                     "r"(o[1]), "r"(o[2]), "r"(o[3]), "r"(o[4]), "r"(o[5]), "r"(o[6]), "r"(o[7])
-                                     : "memory");
-                    } else {
-                        *reinterpret_cast<uint4*>(orow + c) = make_uint4(o[0], o[1], o[2], o[3]);
-                        if (c0 + c + 8 < d2) *reinterpret_cast<uint4*>(orow + c + 8) = make_uint4(o[4], o[5], o[6], o[7]);
-                    }
-                }
+                if (row < nr && c0 + c < d2) store32(orow + c, o, wide, c0 + c + 8 < d2);
             }
         }
     } else if (warp >= 24) {
@@ -663,7 +542,7 @@ __global__ void __launch_bounds__(kScanThreads, 1) linear_scan_kernel(const __gr
             }
             // the products of the chunk before, and at first the state warps' reading of the sum, are done with this place
             if (j > 0) ok = wait_warp(&own_full, (j - 1) & 1, fail);
-            else if (!kStateOnly) ok = wait_warp(&x_ready, 0, fail);
+            else if (kMode != kPieces) ok = wait_warp(&x_ready, 0, fail);
             if (!ok) break;
 #pragma unroll
             for (int c = 0; c < 4; c++) {
@@ -693,21 +572,7 @@ __global__ void __launch_bounds__(kScanThreads, 1) linear_scan_kernel(const __gr
     if (warp == 1) tmem_dealloc(tmem, 512);
 }
 
-// [z][rows][cols] bf16, box 64 columns x 128 rows of one z, 128-byte swizzle; columns and rows past
-// the tensor's read as zero.
-bool make_map_3d(CUtensorMap* m, const void* base, uint64_t z, uint64_t rows, uint64_t cols) {
-    auto fn = encode_fn();
-    if (!fn) return false;
-    cuuint64_t dims[3] = {cols, rows, z};
-    cuuint64_t strides[2] = {cols * 2, rows * cols * 2};
-    cuuint32_t box[3] = {64, 128, 1};
-    cuuint32_t estr[3] = {1, 1, 1};
-    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
-              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-// What is asked of a device once: its SMs, and both kernels' shared memory (0: not asked yet).
+// What is asked of a device once: its SMs, and the kernels' shared memory (0: not asked yet).
 constexpr int kMaxDevices = 64;
 std::atomic<int> g_sms[kMaxDevices];
 
@@ -720,9 +585,11 @@ int sm_count() {
     int sms = g_sms[dev].load(std::memory_order_acquire);
     if (sms) return sms;
     if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
-        cudaFuncSetAttribute(linear_scan_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMost) !=
+        cudaFuncSetAttribute(linear_scan_kernel<kFull>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMost) !=
             cudaSuccess ||
-        cudaFuncSetAttribute(linear_scan_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMost) !=
+        cudaFuncSetAttribute(linear_scan_kernel<kPieces>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMost) !=
+            cudaSuccess ||
+        cudaFuncSetAttribute(linear_scan_kernel<kStates>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMost) !=
             cudaSuccess) {
         cudaGetLastError();
         return 0;
@@ -742,11 +609,12 @@ int smem_bytes(bool state_only, int d1) {
 
 bool linear_tc_supported(int dtype, int dk, int dv) { return dtype == 0 && dk % 8 == 0 && dv % 8 == 0; }
 
-bool linear_tc_plan(LinTcPlan* pl, int batch, int H, int T, int64_t rows, int tiles) {
+bool linear_tc_plan(LinTcPlan* pl, int batch, int H, int T, int64_t rows, int tiles, bool states) {
     if (T > (1 << 30) || rows / H > (1 << 30)) return false;  // token offsets are ints
     pl->batch = batch;
     const int64_t items = static_cast<int64_t>(batch) * H * tiles;
     const int nch = (T - 1) / kTile + 1;
+    if (states && static_cast<int64_t>(batch) * H * nch * 4 > 0x7fffffff) return false;  // state tiles are counted in ints
     const double sms = sm_count();
     if (sms <= 0) return false;
     const bool ragged = rows < static_cast<int64_t>(batch) * H * T;
@@ -768,7 +636,7 @@ bool linear_tc_plan(LinTcPlan* pl, int batch, int H, int T, int64_t rows, int ti
     for (int s = 1; s <= 64 && s <= nch; s++) {
         const int L = (nch + s - 1) / s;
         if ((nch + L - 1) / L != s) continue;  // the same cut as fewer segments
-        const double main = cost(static_cast<double>(items) * s, L, 1.0, 2.1, 5.0);
+        const double main = cost(static_cast<double>(items) * s, L, 1.0, states ? 1.2 : 2.1, states ? 4.0 : 5.0);
         for (int r = 1; r <= 8; r *= 2) {  // pieces of a segment
             if (L % r != 0) break;
             const int P = (s - 1) * r;
@@ -789,15 +657,17 @@ bool linear_tc_plan(LinTcPlan* pl, int batch, int H, int T, int64_t rows, int ti
 }
 
 cudaError_t linear_tc_run(const LinTcPlan& pl, const LinTcMap* maps, int n_maps, const LinTcScan* scans, int count,
-                          const LinSeqs& sq, const float* log_a, float* seg, int* err, cudaStream_t stream) {
+                          const LinSeqs& sq, const float* log_a, float* seg, void* states, int* err,
+                          cudaStream_t stream) {
     ScanParams pr = {};
     const bool packed = sq.tab != nullptr;
     for (int i = 0; i < n_maps; i++)
         if (!make_map_3d(&pr.map[i], maps[i].base, packed ? sq.H : static_cast<uint64_t>(pl.batch) * sq.H,
-                         packed ? sq.total : sq.T, maps[i].cols))
+                         packed ? sq.total : sq.T, maps[i].cols, kTile))
             return cudaErrorInvalidValue;
     pr.log_a = log_a;
     pr.seg = seg;
+    pr.states = static_cast<__nv_bfloat16*>(states);
     pr.sq = sq;
     pr.count = count;
     pr.nseg = pl.nseg;
@@ -809,26 +679,25 @@ cudaError_t linear_tc_run(const LinTcPlan& pl, const LinTcMap* maps, int n_maps,
     int base = 0, tiles = 0, d1 = 0;
     for (int i = 0; i < count; i++) {
         pr.scan[i] = scans[i];
-        pr.scan[i].tiles = (scans[i].d2 + kDepth - 1) / kDepth;
         pr.scan[i].seg_base = base;
-        base += pl.batch * sq.H * pl.npiece * pr.scan[i].tiles;
-        tiles += pr.scan[i].tiles;
+        base += pl.batch * sq.H * pl.npiece * scans[i].tiles;
+        tiles += scans[i].tiles;
         if (scans[i].d1 > d1) d1 = scans[i].d1;
     }
     const unsigned per_seg = static_cast<unsigned>(pl.batch) * sq.H * tiles;
     if (pl.nseg > 1) {
-        const int smem = smem_bytes(true, d1);
-        linear_scan_kernel<true><<<per_seg * pl.npiece, kScanThreads, smem, stream>>>(pr, err);
-        note_launch(stream, "linear_scan_state");
+        linear_scan_kernel<kPieces><<<per_seg * pl.npiece, kScanThreads, smem_bytes(true, d1), stream>>>(pr, err);
+        note_launch(stream, "linear_scan_pieces");
     }
-    const int smem = smem_bytes(false, d1);
+    const auto kern = states ? linear_scan_kernel<kStates> : linear_scan_kernel<kFull>;
+    const int smem = smem_bytes(states != nullptr, d1);
     if (pl.nseg > 1) {
-        const cudaError_t e = launch_pdl(linear_scan_kernel<false>, dim3(per_seg * pl.nseg), dim3(kScanThreads), smem, stream, pr, err);
+        const cudaError_t e = launch_pdl(kern, dim3(per_seg * pl.nseg), dim3(kScanThreads), smem, stream, pr, err);
         if (e != cudaSuccess) return e;
     } else {
-        linear_scan_kernel<false><<<per_seg, kScanThreads, smem, stream>>>(pr, err);
+        kern<<<per_seg, kScanThreads, smem, stream>>>(pr, err);
     }
-    note_launch(stream, "linear_scan");
+    note_launch(stream, states ? "linear_scan_states" : "linear_scan");
     return cudaGetLastError();
 }
 
