@@ -30,16 +30,16 @@ constexpr uint32_t kColS = 0, kColO = 256;
 
 struct GradKind {
     int ia, ib, ic;  // tensor maps: 0 q, 1 k, 2 v, 3 dout
-    int d1, d2, tiles, reverse;
+    int d1, tiles, reverse;
     int state_t;      // X is read as the transpose of the stored rows
     int states_base;  // first (b, h, chunk) of its state in the buffer
-    __nv_bfloat16* out;
 };
 
 struct GradParams {
-    CUtensorMap map[4], xmap;
+    CUtensorMap map[4], omap[3];
     GradKind kind[3];
     const float* log_a;
+    const __nv_bfloat16* states;  // tiles of 128 rows of 64, each row's 16-byte pieces swizzled as shared memory wants them
     int BH, H, T, nch, v_tiles, per_chunk;  // per_chunk: items of one chunk
 };
 
@@ -77,7 +77,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) linear_grad_kernel(const __gr
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     __shared__ uint64_t ax_full[kMaxStages], b_full[kMaxStages], c_full[kMaxStages];
     __shared__ uint64_t ax_free[kMaxStages], b_free[kMaxStages], c_free[kMaxStages];
-    __shared__ uint64_t s_full[2], p_ready[2], o_full[2], o_read[2], drain;
+    __shared__ uint64_t s_full[2], p_ready[2], o_full[2], o_read[2], out_put, out_free, drain;
     __shared__ uint32_t tmem_base_sh;
     __shared__ int fail_sh;
     // per P warp: weight of key c for row r of a diagonal 32-key block at 31 + r - c, and of key c of another block
@@ -91,6 +91,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) linear_grad_kernel(const __gr
     // a stage: a | b | c | X
     const int b_off = np_most * kPanelBytes, c_off = 2 * b_off, x_off = c_off + kPanelBytes;
     const int stage_bytes = x_off + np_most * kXPanel;
+    uint8_t* stage_out = smem + nst * stage_bytes;  // an item's output rows on their way to memory
     volatile int* fail = &fail_sh;
 
     if (tid == 0) {
@@ -108,6 +109,8 @@ __global__ void __launch_bounds__(kGradThreads, 1) linear_grad_kernel(const __gr
             mbar_init(&o_full[i], 1);
             mbar_init(&o_read[i], 8);
         }
+        mbar_init(&out_put, 8);
+        mbar_init(&out_free, 1);
         mbar_init(&drain, 1);
         fence_mbar_init();
         fail_sh = 0;
@@ -139,12 +142,14 @@ __global__ void __launch_bounds__(kGradThreads, 1) linear_grad_kernel(const __gr
                 uint8_t* st = smem + s * stage_bytes;
                 if (warp == 0) {
                     mbar_expect_tx(&full[s], np * (kPanelBytes + kXPanel));
-                    const int x0 = (kd.states_base + it.bh * pr.nch + it.ch) * pr.v_tiles;
+                    const int64_t x0 = static_cast<int64_t>(kd.states_base + it.bh * pr.nch + it.ch) * pr.v_tiles;
                     for (int p = 0; p < np; p++) {
                         tma_load_3d(st + p * kPanelBytes, &pr.map[kd.ia], &full[s], 64 * p, t0, it.bh);
                         // 64 state rows of one 64-column tile: rows of X, or of 64 columns of d1 of its transpose
-                        tma_load_3d(st + x_off + p * kXPanel, &pr.xmap, &full[s], 0, 64 * (kd.state_t ? it.tile : p),
-                                    x0 + (kd.state_t ? p : it.tile));
+                        bulk_load(st + x_off + p * kXPanel,
+                                  pr.states + ((x0 + (kd.state_t ? p : it.tile)) * 2 + (kd.state_t ? it.tile : p)) *
+                                                  (kXPanel / 2),
+                                  kXPanel, &full[s]);
                     }
                 } else if (warp == 2) {
                     mbar_expect_tx(&full[s], np * kPanelBytes);
@@ -306,15 +311,17 @@ __global__ void __launch_bounds__(kGradThreads, 1) linear_grad_kernel(const __gr
         const int row = (warp & 3) * 32 + lane, cw = (warp - 12) / 4 * 32;
         const uint32_t lanes = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
         Item it = item_at(pr, first);
+        int made = -1;
+        float la = 0.f;
         for (int j = 0; j < m; j++) {
-            const GradKind& kd = pr.kind[it.k];
+            const int rev = pr.kind[it.k].reverse, h = it.bh % pr.H;
+            if (h != made) {
+                made = h;
+                la = pr.log_a[h];
+            }
             const int nr = pr.T - it.ch * kTile < kTile ? pr.T - it.ch * kTile : kTile;
-            const float f = row < nr ? gpow(pr.log_a[it.bh % pr.H], kd.reverse ? nr - 1 - row : row + 1) : 0.f;
+            const float f = row < nr ? gpow(la, rev ? nr - 1 - row : row + 1) : 0.f;
             const f32x2 f2 = pair2(f, f);
-            const int col = it.tile * kDepth + cw, d2 = kd.d2;
-            __nv_bfloat16* orow =
-                kd.out + (static_cast<int64_t>(it.bh) * pr.T + static_cast<int64_t>(it.ch) * kTile + row) * d2 + col;
-            const bool wide = d2 % 16 == 0 && (reinterpret_cast<uintptr_t>(kd.out) & 31) == 0;
             if (!wait_warp(&o_full[j & 1], (j >> 1) & 1, fail)) {
                 if (lane == 0) fail_now();
                 break;
@@ -332,12 +339,35 @@ __global__ void __launch_bounds__(kGradThreads, 1) linear_grad_kernel(const __gr
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&o_read[j & 1]);
-            if (row < nr) {
-                if (col < d2) store32(orow, o[0], wide, col + 8 < d2);
-                if (col + 16 < d2) store32(orow + 16, o[1], wide, col + 24 < d2);
+            if (j > 0 && !wait_warp(&out_free, (j - 1) & 1, fail)) {
+                if (lane == 0) fail_now();
+                break;
+            }
+#pragma unroll
+            for (int c = 0; c < 4; c++)
+                *reinterpret_cast<uint4*>(stage_out + sw128_off(row, cw / 8 + c)) =
+                    make_uint4(o[c / 2][c % 2 * 4], o[c / 2][c % 2 * 4 + 1], o[c / 2][c % 2 * 4 + 2],
+                               o[c / 2][c % 2 * 4 + 3]);
+            fence_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&out_put);
+            if (warp == 12) {
+                if (elect_one()) {
+                    // rows past T and columns past the tensor's are not written
+                    if (wait_one(&out_put, j & 1, fail)) {
+                        tma_store_3d(&pr.omap[it.k], stage_out, it.tile * kDepth, it.ch * kTile, it.bh);
+                        bulk_commit();
+                        bulk_wait_read0();
+                        mbar_arrive(&out_free);
+                    } else {
+                        fail_now();
+                    }
+                }
+                __syncwarp();
             }
             it.next(pr);
         }
+        if (warp == 12) bulk_wait0();
     }
 
     tc_fence_before();
@@ -385,11 +415,13 @@ cudaError_t linear_tc_grads(const void* q, const void* k, const void* v, const v
     const void* rows[4] = {q, k, v, dout};
     for (int i = 0; i < 4; i++)
         if (!make_map_3d(&pr.map[i], rows[i], BH, T, i < 2 ? d_k : d_v, kTile)) return cudaErrorInvalidValue;
-    if (!make_map_3d(&pr.xmap, states, static_cast<uint64_t>(2) * BH * nch * vt, kTile, kDepth, 64))
-        return cudaErrorInvalidValue;
-    pr.kind[0] = {3, 2, 1, d_v, d_k, kt, 0, 1, 0, static_cast<__nv_bfloat16*>(dq)};
-    pr.kind[1] = {2, 3, 0, d_v, d_k, kt, 1, 1, BH * nch, static_cast<__nv_bfloat16*>(dk)};
-    pr.kind[2] = {1, 0, 3, d_k, d_v, vt, 1, 0, BH * nch, static_cast<__nv_bfloat16*>(dv)};
+    void* outs[3] = {dq, dk, dv};
+    for (int i = 0; i < 3; i++)
+        if (!make_map_3d(&pr.omap[i], outs[i], BH, T, i < 2 ? d_k : d_v, kTile)) return cudaErrorInvalidValue;
+    pr.kind[0] = {3, 2, 1, d_v, kt, 0, 1, 0};
+    pr.kind[1] = {2, 3, 0, d_v, kt, 1, 1, BH * nch};
+    pr.kind[2] = {1, 0, 3, d_k, vt, 1, 0, BH * nch};
+    pr.states = static_cast<const __nv_bfloat16*>(states);
     pr.log_a = log_a;
     pr.BH = BH;
     pr.H = H;
@@ -398,7 +430,7 @@ cudaError_t linear_tc_grads(const void* q, const void* k, const void* v, const v
     pr.v_tiles = vt;
     pr.per_chunk = 2 * kt + vt;
     const int np = (d_k > d_v ? d_k : d_v) > 64 ? 2 : 1, nst = np == 2 ? 2 : 3;
-    const int smem = nst * ((2 * np + 1) * kPanelBytes + np * kXPanel) + 1024;
+    const int smem = nst * ((2 * np + 1) * kPanelBytes + np * kXPanel) + kPanelBytes + 1024;
     const int64_t items = static_cast<int64_t>(BH) * nch * pr.per_chunk;
     const unsigned grid = static_cast<unsigned>(items < sms ? items : sms);
     const cudaError_t e = launch_pdl(linear_grad_kernel, dim3(grid), dim3(kGradThreads), smem, stream, pr, nst, np, err);

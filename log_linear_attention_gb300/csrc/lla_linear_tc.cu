@@ -59,7 +59,7 @@ __global__ void __launch_bounds__(kScanThreads, 1) linear_scan_kernel(const __gr
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     __shared__ uint64_t qk_full[kMaxStages], v_full[kMaxStages], qk_free[kMaxStages], v_free[kMaxStages];
-    __shared__ uint64_t scaled, own_full, own_read, x_ready, x_free, s_full[2], p_ready, o_full, o_read, drain;
+    __shared__ uint64_t scaled[2], own_full[2], own_read[2], x_ready, x_free, x_put[2], x_sent[2], s_full[2], p_ready, o_full, o_read, drain;
     __shared__ uint32_t tmem_base_sh;
     __shared__ int fail_sh;
     __shared__ float pw[132];    // g^n
@@ -102,24 +102,32 @@ __global__ void __launch_bounds__(kScanThreads, 1) linear_scan_kernel(const __gr
     auto before = [&](int p) { return !rev ? p * kTile : (p == 0 ? 0 : len - (nch - p) * kTile); };
     const int d1 = sc.d1, d2 = sc.d2, c0 = tile * kDepth;
     const int np = d1 > 64 ? 2 : 1, ksteps = (d1 + 15) / 16;
+    // Shared memory. kFull: stages of a | b | c, two (three of narrow rows), then the parts of w o C and X. Only states:
+    // three or two of b, two of c (free once cut), two of the parts, so that cutting, product and copies all overlap, and
+    // two of the states on their way to memory.
     const int k_bytes = np * kPanelBytes;
-    const int v_off = (kStateOnly ? 1 : 2) * k_bytes, stage_bytes = v_off + kPanelBytes;
-    const int k_off = kStateOnly ? 0 : k_bytes;
-    const int nst = (kStateOnly || np == 1) ? 3 : 2;
-    uint8_t* wc = smem + nst * stage_bytes;
-    uint8_t* xs = wc + kWcBytes;
+    const int nk = (kMode == kPieces || np == 1) ? 3 : 2, nv = kStateOnly ? 2 : nk;
+    const int k_step = kStateOnly ? k_bytes : 2 * k_bytes + kPanelBytes;  // from one stage of b to the next
+    const int v_step = kStateOnly ? kPanelBytes : k_step;
+    const int k_off = kStateOnly ? 0 : k_bytes, v_off = kStateOnly ? nk * k_bytes : 2 * k_bytes;
+    uint8_t* wc = smem + (kStateOnly ? v_off + nv * kPanelBytes : nk * k_step);
+    uint8_t* xs = wc + (kStateOnly ? 2 : 1) * kWcBytes;  // kFull, kStates
     volatile int* fail = &fail_sh;
 
     if (tid == 0) {
-        for (int s = 0; s < nst; s++) {
+        for (int s = 0; s < kMaxStages; s++) {
             mbar_init(&qk_full[s], 1);
             mbar_init(&v_full[s], 1);
             mbar_init(&qk_free[s], 1);
-            mbar_init(&v_free[s], 1);
+            mbar_init(&v_free[s], kStateOnly ? 8 : 1);
         }
-        mbar_init(&scaled, 8);
-        mbar_init(&own_full, 1);
-        mbar_init(&own_read, 8);
+        for (int s = 0; s < 2; s++) {  // kFull: the first of each
+            mbar_init(&scaled[s], 8);
+            mbar_init(&own_full[s], 1);
+            mbar_init(&own_read[s], 8);
+            mbar_init(&x_put[s], 8);
+            mbar_init(&x_sent[s], 1);
+        }
         mbar_init(&x_ready, 8);
         mbar_init(&x_free, 1);
         mbar_init(&s_full[0], 1);
@@ -178,11 +186,12 @@ __global__ void __launch_bounds__(kScanThreads, 1) linear_scan_kernel(const __gr
             const bool is_c = warp == 2;
             uint64_t* full = is_c ? v_full : qk_full;
             uint64_t* free_ = is_c ? v_free : qk_free;
+            const int nst = is_c ? nv : nk;
             int s = 0, sent = 0, t0 = row0 + chunk_of(0) * kTile;
             const int dt = rev ? -kTile : kTile;
             uint32_t ph = 1;
-            uint8_t* st = smem;
             for (int j = 0; j < n; j++, t0 += dt) {
+                uint8_t* st = smem + s * (is_c ? v_step : k_step);
                 if (j >= nst && !wait_one(&free_[s], ph, fail)) {
                     fail_now();
                     break;
@@ -191,17 +200,15 @@ __global__ void __launch_bounds__(kScanThreads, 1) linear_scan_kernel(const __gr
                     mbar_expect_tx(&v_full[s], kPanelBytes);
                     tma_load_3d(st + v_off, &pr.map[sc.ic], &v_full[s], c0, t0, z);
                 } else {
-                    mbar_expect_tx(&qk_full[s], v_off);
+                    mbar_expect_tx(&qk_full[s], kStateOnly ? k_bytes : 2 * k_bytes);
                     for (int p = 0; p < np; p++) {
                         if (!kStateOnly) tma_load_3d(st + p * kPanelBytes, &pr.map[sc.ia], &qk_full[s], 64 * p, t0, z);
                         tma_load_3d(st + k_off + p * kPanelBytes, &pr.map[sc.ib], &qk_full[s], 64 * p, t0, z);
                     }
                 }
                 sent++;
-                st += stage_bytes;
                 if (++s == nst) {
                     s = 0;
-                    st = smem;
                     ph ^= 1u;
                 }
             }
@@ -215,7 +222,7 @@ __global__ void __launch_bounds__(kScanThreads, 1) linear_scan_kernel(const __gr
             constexpr uint32_t kIdOwn2 = idesc_bf16(kTile, 2 * kDepth, 1, 1), kIdOwn1 = idesc_bf16(kTile, kDepth, 1, 1);
             // operands of the current stage and what a stage, a 16-column step of a K-major operand and a 16-row
             // step of an MN-major one (128) add to a descriptor's address field
-            const uint64_t step = static_cast<uint64_t>(stage_bytes >> 4);
+            const uint64_t step = static_cast<uint64_t>(k_step >> 4);
             const uint64_t a_first = sdesc(smem_u32(smem), 16, 1024), kmaj = sdesc(0, kPanelBytes, 1024) - sdesc(0, 16, 1024);
             const uint64_t w0 = sdesc(smem_u32(wc), kPanelBytes, 1024), x0 = sdesc(smem_u32(xs), kPanelBytes, 1024);
             const uint64_t to_b = static_cast<uint64_t>(k_off >> 4), to_c = static_cast<uint64_t>(v_off >> 4);
@@ -241,20 +248,22 @@ __global__ void __launch_bounds__(kScanThreads, 1) linear_scan_kernel(const __gr
             uint64_t a = a_first;  // stage s
             if (!kStateOnly && n > 0) ok = scores(a, &qk_full[0], 0, 0);
             for (int j = 0; j < n && ok; j++) {
-                ok = wait_one(&scaled, par, fail) && (!kStateOnly || wait_one(&qk_full[s], ph, fail)) &&
-                     (j == 0 || wait_one(&own_read, par ^ 1u, fail));
+                // the parts and their product: two places of each where only the states are formed
+                const uint32_t pl = kStateOnly ? par : 0u, use = kStateOnly ? (j >> 1) & 1 : par;
+                ok = wait_one(&scaled[pl], use, fail) && (!kStateOnly || wait_one(&qk_full[s], ph, fail)) &&
+                     (j < (kStateOnly ? 2 : 1) || wait_one(&own_read[pl], use ^ 1u, fail));
                 if (!ok) break;
                 tc_fence_after();
-                const uint64_t bt = a + to_b + kmaj;
+                const uint64_t bt = a + to_b + kmaj, wp = w0 + static_cast<uint64_t>(kWcBytes >> 4) * pl;
+                const uint32_t own = tmem + (kStateOnly ? 2 * kDepth * pl : kColOwn);
 #pragma unroll
-                for (int kk = 0; kk < kTile / 16; kk++) mma_bf16(tmem + kColOwn, bt + 128u * kk, w0 + 128u * kk, kIdOwn2, kk > 0);
+                for (int kk = 0; kk < kTile / 16; kk++) mma_bf16(own, bt + 128u * kk, wp + 128u * kk, kIdOwn2, kk > 0);
 #pragma unroll
                 for (int kk = 0; kk < kTile / 16; kk++)
-                    mma_bf16(tmem + kColOwn + kDepth, bt + 128u * kk, w0 + 2 * (kPanelBytes >> 4) + 128u * kk, kIdOwn1, 1);
-                mma_commit(&own_full);
+                    mma_bf16(own + kDepth, bt + 128u * kk, wp + 2 * (kPanelBytes >> 4) + 128u * kk, kIdOwn1, 1);
+                mma_commit(&own_full[pl]);
                 if (kStateOnly) {
                     mma_commit(&qk_free[s]);
-                    mma_commit(&v_free[s]);  // the scale warps are done with c too
                 } else {
                     ok = wait_one(&x_ready, par, fail) && (j == 0 || wait_one(&o_read, par ^ 1u, fail));
                     if (!ok) break;
@@ -266,7 +275,7 @@ __global__ void __launch_bounds__(kScanThreads, 1) linear_scan_kernel(const __gr
                     mma_commit(&qk_free[s]);
                     // the next chunk's scores, so that its P is built while this one's is multiplied
                     const uint64_t ct = a + to_c + kmaj;
-                    const bool wrap = s + 1 == nst;
+                    const bool wrap = s + 1 == nk;
                     if (j + 1 < n)
                         ok = scores(wrap ? a_first : a + step, &qk_full[wrap ? 0 : s + 1], wrap ? ph ^ 1u : ph, par ^ 1u);
                     ok = ok && wait_one(&p_ready, par, fail);
@@ -280,7 +289,7 @@ __global__ void __launch_bounds__(kScanThreads, 1) linear_scan_kernel(const __gr
                     mma_commit(&o_full);
                 }
                 a += step;
-                if (++s == nst) {
+                if (++s == nk) {
                     s = 0;
                     ph ^= 1u;
                     a = a_first;
@@ -291,6 +300,23 @@ __global__ void __launch_bounds__(kScanThreads, 1) linear_scan_kernel(const __gr
             // every MMA issued above has completed before TMEM and shared memory go away
             mma_commit(&drain);
             if (!mbar_wait(&drain, 0)) fail_now();
+        }
+    } else if (warp == 3 && kMode == kStates) {
+        // the states to memory, as they lie in shared memory (rows of 128 bytes, swizzled)
+        if (elect_one()) {
+            for (int j = 0; j < n; j++) {
+                if (!wait_one(&x_put[j & 1], (j >> 1) & 1, fail)) {
+                    fail_now();
+                    break;
+                }
+                const int64_t at = (static_cast<int64_t>(sc.states_base) + static_cast<int64_t>(bh) * nch + chunk_of(j)) *
+                                       sc.tiles + tile;
+                bulk_store(pr.states + at * (kTile * kDepth), xs + (j & 1) * kPanelBytes, np * (kPanelBytes / 2));
+                bulk_commit();
+                bulk_wait_read0();
+                mbar_arrive(&x_sent[j & 1]);
+            }
+            bulk_wait0();
         }
     } else if (warp >= 4 && warp < 12 && !kStateOnly) {
         const int w = warp & 3;
@@ -304,42 +330,8 @@ __global__ void __launch_bounds__(kScanThreads, 1) linear_scan_kernel(const __gr
             const uint32_t cols = lanes + kColS + (j & 1) * kTile;
 #pragma unroll 1
             for (int cb = (warp - 4) >> 2; cb < 4; cb += 2) {
-                uint32_t r[16];
-                if (cb > w) {  // wholly ahead in time
-#pragma unroll
-                    for (int i = 0; i < 16; i++) r[i] = 0u;
-                } else {
-                    if (cb == w) {
-                        float x[32];
-                        tmem_ld32(cols + 32 * cb, x);
-                        const float* dg = diag + 31 + lane;
-#pragma unroll
-                        for (int i = 0; i < 32; i++) {
-                            const float f = dg[-i];
-                            x[i] = f != 0.f ? x[i] * f : 0.f;  // masked: never the product with an infinity
-                        }
-#pragma unroll
-                        for (int i = 0; i < 16; i++) r[i] = pack_bf16(x[2 * i], x[2 * i + 1]);
-                    } else {
-                        const float rw = pw[32 * w + lane - 32 * cb - 31];
-                        const f32x2 rw2 = pair2(rw, rw);
-                        const ulonglong2* cw = reinterpret_cast<const ulonglong2*>(colw);
-#pragma unroll
-                        for (int hh = 0; hh < 2; hh++) {
-                            uint32_t y[16];
-                            tmem_ld16_issue(cols + 32 * cb + 16 * hh, y);
-                            tmem_ld16_wait(y);
-#pragma unroll
-                            for (int i = 0; i < 4; i++) {
-                                const ulonglong2 f = cw[4 * hh + i];
-                                auto at = [&](int e) { return pair2(__uint_as_float(y[e]), __uint_as_float(y[e + 1])); };
-                                r[8 * hh + 2 * i] = pack_bf16(mul2(mul2(at(4 * i), f.x), rw2));
-                                r[8 * hh + 2 * i + 1] = pack_bf16(mul2(mul2(at(4 * i + 2), f.y), rw2));
-                            }
-                        }
-                    }
-                }
-                tmem_st16_issue(cols + 32 * cb, r);
+                const float rw = cb < w ? pw[32 * w + lane - 32 * cb - 31] : 0.f;
+                weigh_block(cols + 32 * cb, cb == w ? 0 : cb < w ? 1 : -1, diag + 31 + lane, colw, rw);
             }
             tmem_st_wait();
             tc_fence_before();
@@ -379,16 +371,19 @@ __global__ void __launch_bounds__(kScanThreads, 1) linear_scan_kernel(const __gr
 #pragma unroll
             for (int c = 0; c < 16; c++) x2[c] = 0ull;
         }
-        auto put_x = [&]() {
+        auto stage_x = [&](uint8_t* to) {
             if (d < 64 * np) {
 #pragma unroll
                 for (int c = 0; c < 4; c++)
-                    *reinterpret_cast<uint4*>(xs + sw128_off(d, cw / 8 + c)) =
+                    *reinterpret_cast<uint4*>(to + sw128_off(d, cw / 8 + c)) =
                         make_uint4(pack_bf16(x2[4 * c]), pack_bf16(x2[4 * c + 1]), pack_bf16(x2[4 * c + 2]),
                                    pack_bf16(x2[4 * c + 3]));
             }
             fence_async_smem();
             __syncwarp();
+        };
+        auto put_x = [&]() {
+            stage_x(xs);
             if (lane == 0) mbar_arrive(&x_ready);
         };
         if (kMode == kFull && n > 0) put_x();
@@ -398,20 +393,18 @@ __global__ void __launch_bounds__(kScanThreads, 1) linear_scan_kernel(const __gr
         }
         bool ok = true;
         for (int j = 0; j < n; j++) {
-            if (kMode == kStates && d < 64 * np) {
-                // the entering state of this chunk, [128 rows][64 columns]
-                __nv_bfloat16* to =
-                    pr.states + ((static_cast<int64_t>(sc.states_base) + static_cast<int64_t>(bh) * nch + chunk_of(j)) *
-                                     sc.tiles + tile) * (kTile * kDepth) + d * kDepth + cw;
-#pragma unroll
-                for (int c = 0; c < 2; c++) {
-                    uint32_t o[8];
-#pragma unroll
-                    for (int i = 0; i < 8; i++) o[i] = pack_bf16(x2[8 * c + i]);
-                    store32(to + 16 * c, o, true, true);
+            if (kMode == kStates) {
+                // the entering state of this chunk, on its way to memory by warp 3
+                if (j >= 2 && !wait_warp(&x_sent[j & 1], ((j >> 1) & 1) ^ 1u, fail)) {
+                    if (lane == 0) fail_now();
+                    ok = false;
+                    break;
                 }
+                stage_x(xs + (j & 1) * kPanelBytes);
+                if (lane == 0) mbar_arrive(&x_put[j & 1]);
             }
-            if (!wait_warp(&own_full, j & 1, fail)) {
+            const int pl = kStateOnly ? j & 1 : 0;
+            if (!wait_warp(&own_full[pl], kStateOnly ? (j >> 1) & 1 : j & 1, fail)) {
                 if (lane == 0) fail_now();
                 ok = false;
                 break;
@@ -422,7 +415,8 @@ __global__ void __launch_bounds__(kScanThreads, 1) linear_scan_kernel(const __gr
 #pragma unroll 1
             for (int part = 1; part >= 0; part--) {  // the smaller first
                 f32x2 y[8], u[8];
-                tmem_ld16x2(lanes + kColOwn + part * kDepth + cw, lanes + kColOwn + part * kDepth + cw + 16, y, u);
+                const uint32_t from = lanes + (kStateOnly ? 2 * kDepth * pl : kColOwn) + part * kDepth + cw;
+                tmem_ld16x2(from, from + 16, y, u);
 #pragma unroll
                 for (int c = 0; c < 8; c++) {
                     x2[c] = fma2(decay, x2[c], y[c]);
@@ -432,7 +426,7 @@ __global__ void __launch_bounds__(kScanThreads, 1) linear_scan_kernel(const __gr
             }
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&own_read);
+            if (lane == 0) mbar_arrive(&own_read[pl]);
             if (kMode == kFull && j + 1 < n) {
                 if (!wait_warp(&x_free, j & 1, fail)) {
                     if (lane == 0) fail_now();
@@ -491,25 +485,26 @@ __global__ void __launch_bounds__(kScanThreads, 1) linear_scan_kernel(const __gr
             }
         }
     } else if (warp >= 24) {
-        // thread: half a row of c, split before the products of the chunk before are done with the parts' place
+        // thread: half a row of c
         const int row = (warp & 3) * 32 + lane, h4 = (warp - 24) >> 2 << 2;
         bool ok = true;
-        int s = 0;
-        uint32_t ph = 0;
-        uint8_t* st = smem;
+        int s = 0, ks = 0;            // stages of c and of b
+        uint32_t ph = 0, kph = 0;
         for (int j = 0; j < n; j++) {
             const int nr = rows_of(chunk_of(j));
+            uint8_t* st = smem + v_off + s * v_step;
             ok = wait_warp(&v_full[s], ph, fail);
             if (ok && nr < kTile) {
                 // rows behind the sequence's end count nothing, whatever they hold
-                ok = wait_warp(&qk_full[s], ph, fail);
+                ok = wait_warp(&qk_full[ks], kph, fail);
                 if (ok && row >= nr) {
                     const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll 1
                     for (int c = h4; c < h4 + 4; c++) {
                         const uint32_t off = sw128_off(row, c);
-                        *reinterpret_cast<uint4*>(st + v_off + off) = zero;
-                        for (int p = 0; p < np; p++) *reinterpret_cast<uint4*>(st + k_off + p * kPanelBytes + off) = zero;
+                        *reinterpret_cast<uint4*>(st + off) = zero;
+                        for (int p = 0; p < np; p++)
+                            *reinterpret_cast<uint4*>(smem + k_off + ks * k_step + p * kPanelBytes + off) = zero;
                     }
                 }
             }
@@ -523,44 +518,47 @@ __global__ void __launch_bounds__(kScanThreads, 1) linear_scan_kernel(const __gr
             auto less = [&](f32x2 f, uint32_t p) {
                 return fma2(pair2(__uint_as_float(p << 16), __uint_as_float(p & 0xffff0000u)), minus, f);
             };
-            uint32_t p1[16], p2[16], p3[16];
-#pragma unroll
-            for (int c = 0; c < 4; c++) {
-                const uint4 xv = *reinterpret_cast<const uint4*>(st + v_off + sw128_off(row, h4 + c));
+            // the products of the chunk (only states: two chunks) before, and at first the state warps' reading of the
+            // sum, are done with this place
+            const int pl = kStateOnly ? j & 1 : 0;
+            if (j >= (kStateOnly ? 2 : 1)) ok = wait_warp(&own_full[pl], kStateOnly ? ((j >> 1) & 1) ^ 1 : (j - 1) & 1, fail);
+            else if (j == 0 && kMode != kPieces) ok = wait_warp(&x_ready, 0, fail);
+            if (!ok) break;
+            uint8_t* to = wc + pl * kWcBytes;
+            // rolled: the unrolled loop's 300 instructions were fetched anew for every chunk and took three times as long
+#pragma unroll 1
+            for (int c = h4; c < h4 + 4; c++) {
+                const uint32_t off = sw128_off(row, c);
+                const uint4 xv = *reinterpret_cast<const uint4*>(st + off);
                 const uint32_t in[4] = {xv.x, xv.y, xv.z, xv.w};
+                uint32_t p1[4], p2[4], p3[4];
 #pragma unroll
                 for (int q = 0; q < 4; q++) {
                     // three cuts of 8 bits: exact, 24 bits in all
-                    const int e = 4 * c + q;
                     f32x2 f = mul2(pair2(__uint_as_float(in[q] << 16), __uint_as_float(in[q] & 0xffff0000u)), wt2);
-                    p1[e] = cut(f);
-                    f = less(f, p1[e]);
-                    p2[e] = cut(f);
-                    f = less(f, p2[e]);
-                    p3[e] = cut(f);
+                    p1[q] = cut(f);
+                    f = less(f, p1[q]);
+                    p2[q] = cut(f);
+                    f = less(f, p2[q]);
+                    p3[q] = cut(f);
                 }
-            }
-            // the products of the chunk before, and at first the state warps' reading of the sum, are done with this place
-            if (j > 0) ok = wait_warp(&own_full, (j - 1) & 1, fail);
-            else if (kMode != kPieces) ok = wait_warp(&x_ready, 0, fail);
-            if (!ok) break;
-#pragma unroll
-            for (int c = 0; c < 4; c++) {
-                const uint32_t off = sw128_off(row, h4 + c);
-                *reinterpret_cast<uint4*>(wc + off) = make_uint4(p1[4 * c], p1[4 * c + 1], p1[4 * c + 2], p1[4 * c + 3]);
-                *reinterpret_cast<uint4*>(wc + kPanelBytes + off) =
-                    make_uint4(p2[4 * c], p2[4 * c + 1], p2[4 * c + 2], p2[4 * c + 3]);
-                *reinterpret_cast<uint4*>(wc + 2 * kPanelBytes + off) =
-                    make_uint4(p3[4 * c], p3[4 * c + 1], p3[4 * c + 2], p3[4 * c + 3]);
+                *reinterpret_cast<uint4*>(to + off) = make_uint4(p1[0], p1[1], p1[2], p1[3]);
+                *reinterpret_cast<uint4*>(to + kPanelBytes + off) = make_uint4(p2[0], p2[1], p2[2], p2[3]);
+                *reinterpret_cast<uint4*>(to + 2 * kPanelBytes + off) = make_uint4(p3[0], p3[1], p3[2], p3[3]);
             }
             fence_async_smem();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&scaled);
-            st += stage_bytes;
-            if (++s == nst) {
+            if (lane == 0) {
+                mbar_arrive(&scaled[pl]);
+                if (kStateOnly) mbar_arrive(&v_free[s]);
+            }
+            if (++s == nv) {
                 s = 0;
-                st = smem;
                 ph ^= 1u;
+            }
+            if (++ks == nk) {
+                ks = 0;
+                kph ^= 1u;
             }
         }
         if (!ok && lane == 0) fail_now();
@@ -598,11 +596,12 @@ int sm_count() {
     return sms;
 }
 
-int smem_bytes(bool state_only, int d1) {
+int smem_bytes(int mode, int d1) {
     const int np = d1 > 64 ? 2 : 1;
-    const int stage = ((state_only ? 1 : 2) * np + 1) * kPanelBytes;
-    const int nst = (state_only || np == 1) ? 3 : 2;
-    return nst * stage + kWcBytes + (state_only ? 0 : kPanelBytes) + 1024;
+    int panels;
+    if (mode == kFull) panels = (np == 1 ? 3 : 2) * (2 * np + 1) + 3 + 1;
+    else panels = (mode == kPieces || np == 1 ? 3 : 2) * np + 2 + 6 + (mode == kStates ? 2 : 0);
+    return panels * kPanelBytes + 1024;
 }
 
 }  // namespace
@@ -686,11 +685,11 @@ cudaError_t linear_tc_run(const LinTcPlan& pl, const LinTcMap* maps, int n_maps,
     }
     const unsigned per_seg = static_cast<unsigned>(pl.batch) * sq.H * tiles;
     if (pl.nseg > 1) {
-        linear_scan_kernel<kPieces><<<per_seg * pl.npiece, kScanThreads, smem_bytes(true, d1), stream>>>(pr, err);
+        linear_scan_kernel<kPieces><<<per_seg * pl.npiece, kScanThreads, smem_bytes(kPieces, d1), stream>>>(pr, err);
         note_launch(stream, "linear_scan_pieces");
     }
     const auto kern = states ? linear_scan_kernel<kStates> : linear_scan_kernel<kFull>;
-    const int smem = smem_bytes(states != nullptr, d1);
+    const int smem = smem_bytes(states ? kStates : kFull, d1);
     if (pl.nseg > 1) {
         const cudaError_t e = launch_pdl(kern, dim3(per_seg * pl.nseg), dim3(kScanThreads), smem, stream, pr, err);
         if (e != cudaSuccess) return e;

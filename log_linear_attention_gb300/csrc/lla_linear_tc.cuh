@@ -20,6 +20,19 @@ __device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, u
         : "memory");
 }
 
+// Shared -> global: a box of a tensor map (what lies outside the tensor is not written), or contiguous bytes (16-byte
+// aligned, a multiple of 16); completion by the issuing thread's bulk groups.
+__device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, const void* src, int x, int y, int z) {
+    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(
+                     reinterpret_cast<uint64_t>(map)),
+                 "r"(smem_u32(src)), "r"(x), "r"(y), "r"(z)
+                 : "memory");
+}
+__device__ __forceinline__ void bulk_store(void* dst, const void* src, uint32_t bytes) {
+    asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(smem_u32(src)), "r"(bytes)
+                 : "memory");
+}
+
 // D[tmem] (+)= A[tmem] * B[smem]: A's row i is lane i, two bf16 K elements per 32-bit column.
 __device__ __forceinline__ void mma_bf16_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
                                             uint32_t accumulate) {
@@ -31,6 +44,11 @@ __device__ __forceinline__ void mma_bf16_ta(uint32_t d_tmem, uint32_t a_tmem, ui
         : "memory");
 }
 
+__device__ __forceinline__ void tmem_st8_issue(uint32_t taddr, const uint32_t* r) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "r"(r[0]),
+                 "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                 : "memory");
+}
 __device__ __forceinline__ void tmem_st16_issue(uint32_t taddr, const uint32_t* r) {
     asm volatile(
         "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
@@ -79,6 +97,52 @@ __device__ __forceinline__ void tmem_ld16x2(uint32_t ta, uint32_t tb, f32x2* va,
     for (int i = 0; i < 8; i++) {
         va[i] = pair2(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1]));
         vb[i] = pair2(__uint_as_float(q[2 * i]), __uint_as_float(q[2 * i + 1]));
+    }
+}
+
+// P of this thread's row and one block of 32 keys, in place of its scores (fp32, 32 columns at `cols`; P in the first 16):
+// side 1: the keys lie in the row's reach, their weights colw[key] rw; 0: the diagonal block, weight diag[-key], 0 out of
+// reach; -1: out of reach. Rolled by 16 keys, which keeps the loop in the instruction cache.
+__device__ __forceinline__ void weigh_block(uint32_t cols, int side, const float* diag, const float* colw, float rw) {
+    const f32x2 rw2 = pair2(rw, rw);
+    uint32_t keep[8];  // the first half: its columns hold scores still to be read
+#pragma unroll 1
+    for (int half = 0; half < 2; half++) {
+        uint32_t r[8], y[16];
+        if (side < 0) {
+#pragma unroll
+            for (int i = 0; i < 8; i++) r[i] = 0u;
+        } else {
+            tmem_ld16_issue(cols + 16 * half, y);
+            tmem_ld16_wait(y);
+            if (side == 0) {
+                const float* dg = diag - 16 * half;
+#pragma unroll
+                for (int i = 0; i < 8; i++) {
+                    const float f = dg[-2 * i], g = dg[-2 * i - 1];
+                    // out of reach: never the product with an infinity
+                    r[i] = pack_bf16(f != 0.f ? __uint_as_float(y[2 * i]) * f : 0.f,
+                                     g != 0.f ? __uint_as_float(y[2 * i + 1]) * g : 0.f);
+                }
+            } else {
+                const ulonglong2* cw = reinterpret_cast<const ulonglong2*>(colw + 16 * half);
+#pragma unroll
+                for (int i = 0; i < 4; i++) {
+                    const ulonglong2 f = cw[i];
+                    r[2 * i] = pack_bf16(
+                        mul2(mul2(pair2(__uint_as_float(y[4 * i]), __uint_as_float(y[4 * i + 1])), f.x), rw2));
+                    r[2 * i + 1] = pack_bf16(
+                        mul2(mul2(pair2(__uint_as_float(y[4 * i + 2]), __uint_as_float(y[4 * i + 3])), f.y), rw2));
+                }
+            }
+        }
+        if (half == 0) {
+#pragma unroll
+            for (int i = 0; i < 8; i++) keep[i] = r[i];
+        } else {
+            tmem_st8_issue(cols, keep);
+            tmem_st8_issue(cols + 8, r);
+        }
     }
 }
 
