@@ -596,6 +596,8 @@ int sm_count() {
     return sms;
 }
 
+constexpr int64_t kMostPieces = 16384;  // 512 MB of workspace
+
 int smem_bytes(int mode, int d1) {
     const int np = d1 > 64 ? 2 : 1;
     int panels;
@@ -626,28 +628,27 @@ bool linear_tc_plan(LinTcPlan* pl, int batch, int H, int T, int64_t rows, int ti
         const double even = total * share / sms * (c + fixed / L) + L * c + fixed;
         return even < waves ? even : waves;
     };
-    // Measured at d = 128 and 64: a chunk 2.1 us (1.2 where only the state is formed), a CTA's start and end 5 (4), the
+    // Measured at d = 128 and 64: a chunk 2.1 us (1.4 where only the state is formed), a CTA's start and end 5 (4), the
     // second launch 3, a piece in a segment's sum 0.1.
-    double best = 0;
+    const double chunk = states ? 1.4 : 2.1, fixed = states ? 4.0 : 5.0;
+    double best = cost(static_cast<double>(items), nch, 1.0, chunk, fixed);
     pl->nseg = 1;
     pl->seg_chunks = pl->piece_chunks = nch;
     pl->npiece = 0;
-    for (int s = 1; s <= 64 && s <= nch; s++) {
-        const int L = (nch + s - 1) / s;
-        if ((nch + L - 1) / L != s) continue;  // the same cut as fewer segments
-        const double main = cost(static_cast<double>(items) * s, L, 1.0, states ? 1.2 : 2.1, states ? 4.0 : 5.0);
+    for (int s = 2; s <= 64 && s <= nch; s++) {
         for (int r = 1; r <= 8; r *= 2) {  // pieces of a segment
-            if (L % r != 0) break;
-            const int P = (s - 1) * r;
-            const double c = s == 1 ? main
-                                    : main + cost(static_cast<double>(items) * P, L / r, (s - 1.0) / s, 1.2, 4.0) + 3.0 +
-                                          0.1 * P;
-            if (best == 0 || c < best) {
+            const int P = ((nch + s - 1) / s + r - 1) / r, L = P * r;
+            const int n = (nch + L - 1) / L, np = (n - 1) * r;
+            if (n < 2 || items * np > kMostPieces) continue;
+            const double share = static_cast<double>(np) * P / nch;
+            const double c = cost(static_cast<double>(items) * n, L, 1.0, chunk, fixed) +
+                             cost(static_cast<double>(items) * np, P, share, 1.4, 4.0) + 3.0 + 0.1 * np;
+            if (c < best) {
                 best = c;
-                pl->nseg = s;
+                pl->nseg = n;
                 pl->seg_chunks = L;
-                pl->npiece = P;
-                pl->piece_chunks = L / r;
+                pl->npiece = np;
+                pl->piece_chunks = P;
             }
         }
     }
