@@ -7,7 +7,7 @@
 //
 // An item is 64 columns of one of them for one 128-token chunk, with rows a (d1 wide), b (d1 wide) and
 // c (64 columns) and the chunk's state X:
-//     scores  A B^T  [128 x 128] -> P = scores o g^|i-j| (bf16, in TMEM in place of the scores)
+//     scores  A B^T  [128 x 128] -> P = scores o g^|i-j| (two bf16 parts, in TMEM in place of the scores)
 //     far     A X    [128 x 64]     X as it lies (dv), or the same rows read as its transpose (dq, dk)
 //     near    P C    [128 x 64]     out_i = near_i + f_i far_i
 // With the states given, chunks do not wait for one another: items are dealt out evenly to one CTA per SM
@@ -233,8 +233,11 @@ __global__ void __launch_bounds__(kGradThreads, 1) linear_grad_kernel(const __gr
                 if (!ok) break;
                 tc_fence_after();
 #pragma unroll
-                for (int kk = 0; kk < kTile / 16; kk++)
-                    mma_bf16_ta(d, tmem + kColS + buf * kTile + kk / 2 * 32 + kk % 2 * 8, ct + 128u * kk, kIdMn, kk > 0);
+                for (int kk = 0; kk < kTile / 16; kk++) {
+                    const uint32_t p = tmem + kColS + buf * kTile + 16 * kk;
+                    mma_bf16_ta(d, p, ct + 128u * kk, kIdMn, kk > 0);
+                    mma_bf16_ta(d, p + 8, ct + 128u * kk, kIdMn, 1);
+                }
                 mma_commit(&o_full[buf]);
                 mma_commit(&c_free[cs]);
             }
@@ -272,34 +275,9 @@ __global__ void __launch_bounds__(kGradThreads, 1) linear_grad_kernel(const __gr
             const uint32_t cols = lanes + kColS + (j & 1) * kTile;
 #pragma unroll 1
             for (int cb = (warp - 4) >> 2; cb < 4; cb += 2) {
-                uint32_t r[16];
-                if (rev ? cb < w : cb > w) {  // wholly on the other side of time
-#pragma unroll
-                    for (int i = 0; i < 16; i++) r[i] = 0u;
-                } else if (cb == w) {
-                    float x[32];
-                    tmem_ld32(cols + 32 * cb, x);
-#pragma unroll
-                    for (int i = 0; i < 32; i++) {
-                        const float f = wt[31 + lane - i];
-                        x[i] = f != 0.f ? x[i] * f : 0.f;  // masked: never the product with an infinity
-                    }
-#pragma unroll
-                    for (int i = 0; i < 16; i++) r[i] = pack_bf16(x[2 * i], x[2 * i + 1]);
-                } else {
-                    const float rw = gpow(la, rev ? 32 * cb - (32 * w + lane) : 32 * w + lane - 32 * cb - 31);
-                    const f32x2 rw2 = pair2(rw, rw);
-                    const ulonglong2* cw = reinterpret_cast<const ulonglong2*>(wt + 64);
-                    f32x2 x[16];
-                    tmem_ld16x2(cols + 32 * cb, cols + 32 * cb + 16, x, x + 8);
-#pragma unroll
-                    for (int i = 0; i < 8; i++) {
-                        const ulonglong2 f = cw[i];
-                        r[2 * i] = pack_bf16(mul2(mul2(x[2 * i], f.x), rw2));
-                        r[2 * i + 1] = pack_bf16(mul2(mul2(x[2 * i + 1], f.y), rw2));
-                    }
-                }
-                tmem_st16_issue(cols + 32 * cb, r);
+                const int side = cb == w ? 0 : (rev ? cb > w : cb < w) ? 1 : -1;
+                const float rw = side > 0 ? gpow(la, rev ? 32 * cb - (32 * w + lane) : 32 * w + lane - 32 * cb - 31) : 0.f;
+                weigh_block<2>(cols + 32 * cb, side, wt + 31 + lane, wt + 64, rw);
             }
             tmem_st_wait();
             tc_fence_before();

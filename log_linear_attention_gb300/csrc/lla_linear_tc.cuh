@@ -44,11 +44,6 @@ __device__ __forceinline__ void mma_bf16_ta(uint32_t d_tmem, uint32_t a_tmem, ui
         : "memory");
 }
 
-__device__ __forceinline__ void tmem_st8_issue(uint32_t taddr, const uint32_t* r) {
-    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "r"(r[0]),
-                 "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
-                 : "memory");
-}
 __device__ __forceinline__ void tmem_st16_issue(uint32_t taddr, const uint32_t* r) {
     asm volatile(
         "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
@@ -100,19 +95,29 @@ __device__ __forceinline__ void tmem_ld16x2(uint32_t ta, uint32_t tb, f32x2* va,
     }
 }
 
-// P of this thread's row and one block of 32 keys, in place of its scores (fp32, 32 columns at `cols`; P in the first 16):
+// x in two bf16 parts, two values at once: the first 8 bits cut off, the rest rounded.
+__device__ __forceinline__ void split_pair(f32x2 x, uint32_t& hi, uint32_t& lo) {
+    const float2 f = split2(x);
+    hi = __byte_perm(__float_as_uint(f.x), __float_as_uint(f.y), 0x7632);
+    lo = pack_bf16(fma2(pair2(__uint_as_float(hi << 16), __uint_as_float(hi & 0xffff0000u)), pair2(-1.f, -1.f), x));
+}
+
+// P of this thread's row and one block of 32 keys, in place of its scores (fp32, 32 columns at `cols`): for every 16 keys
+// eight columns of P's high parts and eight of its low ones, so that P keeps 16 bits and only the state and the output
+// are rounded to bf16's eight.
 // side 1: the keys lie in the row's reach, their weights colw[key] rw; 0: the diagonal block, weight diag[-key], 0 out of
-// reach; -1: out of reach. Rolled by 16 keys, which keeps the loop in the instruction cache.
+// reach; -1: out of reach.
+template <int kUnroll>
 __device__ __forceinline__ void weigh_block(uint32_t cols, int side, const float* diag, const float* colw, float rw) {
     const f32x2 rw2 = pair2(rw, rw);
-    uint32_t keep[8];  // the first half: its columns hold scores still to be read
-#pragma unroll 1
+#pragma unroll(kUnroll)
     for (int half = 0; half < 2; half++) {
-        uint32_t r[8], y[16];
+        uint32_t r[16];
         if (side < 0) {
 #pragma unroll
-            for (int i = 0; i < 8; i++) r[i] = 0u;
+            for (int i = 0; i < 16; i++) r[i] = 0u;
         } else {
+            uint32_t y[16];
             tmem_ld16_issue(cols + 16 * half, y);
             tmem_ld16_wait(y);
             if (side == 0) {
@@ -121,28 +126,22 @@ __device__ __forceinline__ void weigh_block(uint32_t cols, int side, const float
                 for (int i = 0; i < 8; i++) {
                     const float f = dg[-2 * i], g = dg[-2 * i - 1];
                     // out of reach: never the product with an infinity
-                    r[i] = pack_bf16(f != 0.f ? __uint_as_float(y[2 * i]) * f : 0.f,
-                                     g != 0.f ? __uint_as_float(y[2 * i + 1]) * g : 0.f);
+                    split_pair(pair2(f != 0.f ? __uint_as_float(y[2 * i]) * f : 0.f,
+                                     g != 0.f ? __uint_as_float(y[2 * i + 1]) * g : 0.f), r[i], r[8 + i]);
                 }
             } else {
                 const ulonglong2* cw = reinterpret_cast<const ulonglong2*>(colw + 16 * half);
 #pragma unroll
                 for (int i = 0; i < 4; i++) {
                     const ulonglong2 f = cw[i];
-                    r[2 * i] = pack_bf16(
-                        mul2(mul2(pair2(__uint_as_float(y[4 * i]), __uint_as_float(y[4 * i + 1])), f.x), rw2));
-                    r[2 * i + 1] = pack_bf16(
-                        mul2(mul2(pair2(__uint_as_float(y[4 * i + 2]), __uint_as_float(y[4 * i + 3])), f.y), rw2));
+                    split_pair(mul2(mul2(pair2(__uint_as_float(y[4 * i]), __uint_as_float(y[4 * i + 1])), f.x), rw2),
+                               r[2 * i], r[8 + 2 * i]);
+                    split_pair(mul2(mul2(pair2(__uint_as_float(y[4 * i + 2]), __uint_as_float(y[4 * i + 3])), f.y), rw2),
+                               r[2 * i + 1], r[9 + 2 * i]);
                 }
             }
         }
-        if (half == 0) {
-#pragma unroll
-            for (int i = 0; i < 8; i++) keep[i] = r[i];
-        } else {
-            tmem_st8_issue(cols, keep);
-            tmem_st8_issue(cols + 8, r);
-        }
+        tmem_st16_issue(cols + 16 * half, r);
     }
 }
 
