@@ -45,9 +45,15 @@ cudaMemPool_t workspace_pool(int dev) {
         props.location.type = cudaMemLocationTypeDevice;
         props.location.id = dev;
         cudaMemPool_t pool;
-        if (cudaMemPoolCreate(&pool, &props) != cudaSuccess) return nullptr;
+        // a process's first call may come while its stream is being captured: creating the pool is no work of
+        // that stream, and only the relaxed mode lets it by
+        cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
+        if (cudaThreadExchangeStreamCaptureMode(&mode) != cudaSuccess) return nullptr;
+        cudaError_t e = cudaMemPoolCreate(&pool, &props);
         uint64_t keep = UINT64_MAX;
-        cudaMemPoolSetAttribute(pool, cudaMemPoolAttrReleaseThreshold, &keep);
+        if (e == cudaSuccess) cudaMemPoolSetAttribute(pool, cudaMemPoolAttrReleaseThreshold, &keep);
+        cudaThreadExchangeStreamCaptureMode(&mode);
+        if (e != cudaSuccess) return nullptr;
         g_pool[dev] = pool;
         g_pool_ready[dev] = true;
     }

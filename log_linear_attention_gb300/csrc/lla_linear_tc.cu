@@ -1,7 +1,8 @@
 // Linear attention with one decay per head on tensor cores: bf16 rows, dk and dv multiples of 8.
 //
-// One kernel walks a scan (see lla_linear.cu: out_t = S_t^T a_t, S_t = g S_{t-1} + b_t c_t^T) over one (sequence, head, 64 columns of c) in chunks of 128 tokens. The state
-// (d1 x 64, fp32) never leaves the registers of four warps. Per chunk, n valid rows:
+// One kernel walks a scan (see lla_linear.cu: out_t = S_t^T a_t, S_t = g S_{t-1} + b_t c_t^T) over one
+// (sequence, head, 64 columns of c) in chunks of 128 tokens. The state (d1 x 64, fp32) never leaves the
+// registers of eight warps. Per chunk, n valid rows:
 //     scores  A B^T                      [128 x 128]  -> TMEM
 //     own     B^T [hi | mid + lo]        [d1 x 128]   -> TMEM, w o C cut into three bf16 parts, so that the
 //                                                     state keeps the 24 bits of fp32
@@ -53,7 +54,8 @@ struct ScanParams {
 };
 
 // Warps: 0 and 2 TMA producers, 1 TMEM owner and MMA issuer, 4..11 P (every other block of 32 keys), 12..19 state
-// (32 columns each), 20..23 write out, 24..31 split w o C. Warp w reaches TMEM lanes 32 (w % 4)..+31: rows of scores and out, rows of the state.
+// (32 columns each), 20..23 write out, 24..31 cut w o C. Warp w reaches TMEM lanes 32 (w % 4)..+31: rows of scores and
+// out, rows of the state.
 template <int kMode>
 __global__ void __launch_bounds__(kScanThreads, 1) linear_scan_kernel(const __grid_constant__ ScanParams pr, int* err) {
     constexpr bool kStateOnly = kMode != kFull;

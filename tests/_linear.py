@@ -83,3 +83,23 @@ def make(rng, shape, dtype, scale=1.0):
     if dtype == "bf16":
         t = t.bfloat16()
     return t.double().numpy(), t
+
+
+def tokens(q, k, v, log_a, s0, dout, ds):
+    """The recurrence and its adjoint token by token in float64 on the tensors' device, for shapes too long for pair
+    sums: q, k [N, T, dk], v, dout [N, T, dv], log_a [N], s0, ds [N, dk, dv]. (out, state, dq, dk, dv, dstate0)."""
+    import torch
+    q, k, v, dout, S = (x.double() for x in (q, k, v, dout, s0))
+    g = torch.exp(log_a.double())[:, None, None]
+    out, dq, gk, gv = (torch.empty_like(x) for x in (v, q, k, v))
+    for t in range(q.shape[1]):
+        S = g * S + k[:, t, :, None] * v[:, t, None, :]
+        out[:, t] = (q[:, t, :, None] * S).sum(1)
+        dq[:, t] = (S * dout[:, t, None, :]).sum(2)
+    R = ds.double()
+    for t in reversed(range(q.shape[1])):
+        R = R + q[:, t, :, None] * dout[:, t, None, :]
+        gk[:, t] = (R * v[:, t, None, :]).sum(2)
+        gv[:, t] = (R * k[:, t, :, None]).sum(1)
+        R = g * R
+    return out, S, dq, gk, gv, R

@@ -438,3 +438,65 @@ def test_binding_refuses(lla):
         lla.linear_decode_step(q[:, :, 0].contiguous(), k[:, :, 0].contiguous(), v[:, :, 0].contiguous(), la, s0)
     with pytest.raises(TypeError):
         lla.linear_forward_varlen(q[0], k[0], v[0], la, torch.zeros(2, dtype=torch.int64, device="cuda"), 20)
+
+
+FIRST = """
+import sys, torch
+from log_linear_attention_gb300 import binding as lla
+q = torch.randn(2, 3, 300, 64, device="cuda").bfloat16()
+la, la2 = -torch.rand(3, device="cuda"), -torch.rand(2, 3, device="cuda")
+x, f = q[:, :, 0].clone(), q.float()
+cu = torch.tensor([0, 100, 300], dtype=torch.int32, device="cuda")
+state, decay = torch.zeros(2, 3, 64, 64, device="cuda"), torch.zeros(2, 3, device="cuda")
+prefix, states = torch.zeros(3, 11, 64, 64, device="cuda"), torch.zeros(2, 3, 14, 64, 64, device="cuda")
+lam, t = torch.rand(2, 3, 14, device="cuda"), torch.full((2,), 1050, device="cuda")
+call = {"forward": lambda: lla.linear_forward(q, q, q, la), "fp32": lambda: lla.linear_forward(f, f, f, la),
+        "varlen": lambda: lla.linear_forward_varlen(q[0], q[0], q[0], la, cu, 200),
+        "backward": lambda: lla.linear_backward(q, q, q, la, q)[0],
+        "decode": lambda: lla.linear_decode_step(x, x, x, la, state),
+        "shared": lambda: lla.decode_step_shared(x, x, x, la2, lam, prefix, 1000, decay, states, t)}[sys.argv[1]]
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    o = call()
+for s in (state, decay, states):
+    s.zero_()
+g.replay()
+torch.cuda.synchronize()
+for s in (state, decay, states):
+    s.zero_()
+assert torch.equal(o, call()) and lla.device_error() == 0
+print("same")
+"""
+
+
+@pytest.mark.parametrize("what", ["forward", "fp32", "varlen", "backward", "decode", "shared"])
+def test_first_call_of_a_process_may_be_captured(what):
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", FIRST, what], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "same" in r.stdout, r.stderr[-2000:]
+
+
+@pytest.mark.parametrize("B,H,T,dk,dv", [(4, 16, 8192, 128, 64), (10, 17, 1100, 64, 128), (1, 2, 20000, 128, 128),
+                                         (200, 5, 130, 64, 64)])
+def test_full_sizes_sampled(lla, B, H, T, dk, dv):
+    """The headline shape, more heads than SMs, a long document of two heads, many short sequences: some heads
+    against the recurrence in 64 bits. The norm bounds of tests/_linear.py; states are fp32 sums of T terms."""
+    g = torch.Generator(device="cuda").manual_seed(T)
+    rand = lambda *s: torch.randn(*s, generator=g, device="cuda")  # noqa: E731
+    q, k = (rand(B, H, T, dk).mul_(dk ** -0.5).bfloat16() for _ in range(2))
+    v, do = (rand(B, H, T, dv).bfloat16() for _ in range(2))
+    la = -torch.exp2(-8.0 * torch.arange(1, H + 1, device="cuda") / H)
+    s0, ds = rand(B, H, dk, dv) * 0.1, rand(B, H, dk, dv) * 0.1
+    s1 = torch.empty_like(s0)
+    out = lla.linear_forward(q, k, v, la, state0=s0, state_out=s1)
+    got = [out, s1, *lla.linear_backward(q, k, v, la, do, state0=s0, dstate_out=ds)]
+    for b, h in ((0, 0), (B - 1, H - 1), (B // 2, H // 2)):
+        ref = L.tokens(q[b, h][None], k[b, h][None], v[b, h][None], la[h][None], s0[b, h][None], do[b, h][None],
+                       ds[b, h][None])
+        for n, x, r in zip(("out", "state", "dq", "dk", "dv", "dstate0"), got, ref):
+            rel = float((x[b, h].double() - r[0]).norm() / r[0].norm())
+            assert rel <= (5e-3 if x.dtype == torch.bfloat16 else 4 * (T + 16) ** 0.5 * L.U32), (n, b, h, rel)
