@@ -32,7 +32,7 @@ namespace lla {
 namespace {
 
 constexpr int kScanThreads = 1024;
-constexpr int kMaxStages = 3;
+constexpr int kMaxStages = 4;
 constexpr int kWcBytes = 3 * kPanelBytes;
 constexpr int kSmemMost = 232448 - 2048;  // 227 KB less the static part
 
@@ -59,10 +59,11 @@ struct ScanParams {
 template <int kMode>
 __global__ void __launch_bounds__(kScanThreads, 1) linear_scan_kernel(const __grid_constant__ ScanParams pr, int* err) {
     constexpr bool kStateOnly = kMode != kFull;
+    constexpr int kCutWarps = kStateOnly ? 16 : 8;  // where there is no P, its warps cut w o C too
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     __shared__ uint64_t qk_full[kMaxStages], v_full[kMaxStages], qk_free[kMaxStages], v_free[kMaxStages];
-    __shared__ uint64_t scaled[2], own_full[2], own_read[2], x_ready, x_free, x_put[2], x_sent[2], s_full[2], p_ready, o_full, o_read, drain;
+    __shared__ uint64_t scaled[2], own_full[2], own_read[2], x_ready, x_free, x_put, x_sent, s_full[2], p_ready, o_full, o_read, drain;
     __shared__ uint32_t tmem_base_sh;
     __shared__ int fail_sh;
     __shared__ float pw[132];    // g^n
@@ -106,10 +107,10 @@ __global__ void __launch_bounds__(kScanThreads, 1) linear_scan_kernel(const __gr
     const int d1 = sc.d1, d2 = sc.d2, c0 = tile * kDepth;
     const int np = d1 > 64 ? 2 : 1, ksteps = (d1 + 15) / 16;
     // Shared memory. kFull: stages of a | b | c, two (three of narrow rows), then the parts of w o C and X. Only states:
-    // three or two of b, two of c (free once cut), two of the parts, so that cutting, product and copies all overlap, and
-    // two of the states on their way to memory.
+    // as many of b, four of c (free once cut; kStates: three, and one of the states on its way to memory) and two of the
+    // parts, so that copies, cutting and product all overlap.
     const int k_bytes = np * kPanelBytes;
-    const int nk = (kMode == kPieces || np == 1) ? 3 : 2, nv = kStateOnly ? 2 : nk;
+    const int nk = np == 1 ? 3 : 2, nv = kMode == kFull ? nk : kMode == kPieces ? 4 : 3;
     const int k_step = kStateOnly ? k_bytes : 2 * k_bytes + kPanelBytes;  // from one stage of b to the next
     const int v_step = kStateOnly ? kPanelBytes : k_step;
     const int k_off = kStateOnly ? 0 : k_bytes, v_off = kStateOnly ? nk * k_bytes : 2 * k_bytes;
@@ -122,17 +123,17 @@ __global__ void __launch_bounds__(kScanThreads, 1) linear_scan_kernel(const __gr
             mbar_init(&qk_full[s], 1);
             mbar_init(&v_full[s], 1);
             mbar_init(&qk_free[s], 1);
-            mbar_init(&v_free[s], kStateOnly ? 8 : 1);
+            mbar_init(&v_free[s], kStateOnly ? kCutWarps : 1);
         }
         for (int s = 0; s < 2; s++) {  // kFull: the first of each
-            mbar_init(&scaled[s], 8);
+            mbar_init(&scaled[s], kCutWarps);
             mbar_init(&own_full[s], 1);
             mbar_init(&own_read[s], 8);
-            mbar_init(&x_put[s], 8);
-            mbar_init(&x_sent[s], 1);
         }
         mbar_init(&x_ready, 8);
         mbar_init(&x_free, 1);
+        mbar_init(&x_put, 8);
+        mbar_init(&x_sent, 1);
         mbar_init(&s_full[0], 1);
         mbar_init(&s_full[1], 1);
         mbar_init(&p_ready, 8);
@@ -200,6 +201,10 @@ __global__ void __launch_bounds__(kScanThreads, 1) linear_scan_kernel(const __gr
                     break;
                 }
                 if (is_c) {
+                    // kFull with two stages: a chunk's c is waited for longest (its place is free last and the cutting takes the
+                    // time before its product), so that of two chunks on comes from L2 (4% of the headline prompt; three
+                    // stages do without, and prefetching a and b too costs more than it gives)
+                    if (kMode == kFull && np == 2 && j + 2 < n) tma_prefetch_l2_3d(&pr.map[sc.ic], c0, t0 + 2 * dt, z);
                     mbar_expect_tx(&v_full[s], kPanelBytes);
                     tma_load_3d(st + v_off, &pr.map[sc.ic], &v_full[s], c0, t0, z);
                 } else {
@@ -310,16 +315,16 @@ __global__ void __launch_bounds__(kScanThreads, 1) linear_scan_kernel(const __gr
         // the states to memory, as they lie in shared memory (rows of 128 bytes, swizzled)
         if (elect_one()) {
             for (int j = 0; j < n; j++) {
-                if (!wait_one(&x_put[j & 1], (j >> 1) & 1, fail)) {
+                if (!wait_one(&x_put, j & 1, fail)) {
                     fail_now();
                     break;
                 }
                 const int64_t at = (static_cast<int64_t>(sc.states_base) + static_cast<int64_t>(bh) * nch + chunk_of(j)) *
                                        sc.tiles + tile;
-                bulk_store(pr.states + at * (kTile * kDepth), xs + (j & 1) * kPanelBytes, np * (kPanelBytes / 2));
+                bulk_store(pr.states + at * (kTile * kDepth), xs, np * (kPanelBytes / 2));
                 bulk_commit();
                 bulk_wait_read0();
-                mbar_arrive(&x_sent[j & 1]);
+                mbar_arrive(&x_sent);
             }
             bulk_wait0();
         }
@@ -400,13 +405,13 @@ __global__ void __launch_bounds__(kScanThreads, 1) linear_scan_kernel(const __gr
         for (int j = 0; j < n; j++) {
             if (kMode == kStates) {
                 // the entering state of this chunk, on its way to memory by warp 3
-                if (j >= 2 && !wait_warp(&x_sent[j & 1], ((j >> 1) & 1) ^ 1u, fail)) {
+                if (j > 0 && !wait_warp(&x_sent, (j - 1) & 1, fail)) {
                     if (lane == 0) fail_now();
                     ok = false;
                     break;
                 }
-                stage_x(xs + (j & 1) * kPanelBytes);
-                if (lane == 0) mbar_arrive(&x_put[j & 1]);
+                stage_x(xs);
+                if (lane == 0) mbar_arrive(&x_put);
             }
             const int pl = kStateOnly ? j & 1 : 0;
             if (!wait_warp(&own_full[pl], kStateOnly ? (j >> 1) & 1 : j & 1, fail)) {
@@ -489,9 +494,10 @@ __global__ void __launch_bounds__(kScanThreads, 1) linear_scan_kernel(const __gr
                 if (row < nr && c0 + c < d2) store32(orow + c, o, wide, c0 + c + 8 < d2);
             }
         }
-    } else if (warp >= 24) {
-        // thread: half a row of c
-        const int row = (warp & 3) * 32 + lane, h4 = (warp - 24) >> 2 << 2;
+    } else if (warp >= 24 || (kStateOnly && warp >= 4 && warp < 12)) {
+        // thread: a half or a quarter of a row of c, 16-byte pieces c_first..
+        constexpr int kCut = 32 / kCutWarps;
+        const int row = (warp & 3) * 32 + lane, c_first = (warp >= 24 ? (warp - 24) >> 2 : (warp - 4) / 4 + 2) * kCut;
         bool ok = true;
         int s = 0, ks = 0;            // stages of c and of b
         uint32_t ph = 0, kph = 0;
@@ -505,7 +511,7 @@ __global__ void __launch_bounds__(kScanThreads, 1) linear_scan_kernel(const __gr
                 if (ok && row >= nr) {
                     const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll 1
-                    for (int c = h4; c < h4 + 4; c++) {
+                    for (int c = c_first; c < c_first + kCut; c++) {
                         const uint32_t off = sw128_off(row, c);
                         *reinterpret_cast<uint4*>(st + off) = zero;
                         for (int p = 0; p < np; p++)
@@ -532,7 +538,7 @@ __global__ void __launch_bounds__(kScanThreads, 1) linear_scan_kernel(const __gr
             uint8_t* to = wc + pl * kWcBytes;
             // rolled: the unrolled loop's 300 instructions were fetched anew for every chunk and took three times as long
 #pragma unroll 1
-            for (int c = h4; c < h4 + 4; c++) {
+            for (int c = c_first; c < c_first + kCut; c++) {
                 const uint32_t off = sw128_off(row, c);
                 const uint4 xv = *reinterpret_cast<const uint4*>(st + off);
                 const uint32_t in[4] = {xv.x, xv.y, xv.z, xv.w};
@@ -607,7 +613,7 @@ int smem_bytes(int mode, int d1) {
     const int np = d1 > 64 ? 2 : 1;
     int panels;
     if (mode == kFull) panels = (np == 1 ? 3 : 2) * (2 * np + 1) + 3 + 1;
-    else panels = (mode == kPieces || np == 1 ? 3 : 2) * np + 2 + 6 + (mode == kStates ? 2 : 0);
+    else panels = (np == 1 ? 3 : 2) * np + 4 + 6;
     return panels * kPanelBytes + 1024;
 }
 
