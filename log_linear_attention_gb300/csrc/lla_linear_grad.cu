@@ -45,7 +45,7 @@ struct GradParams {
 
 // An item and its successor; every role walks its CTA's items with one of these.
 struct Item {
-    int bh, ch, k, tile;
+    int bh, h, ch, k, tile;
     __device__ __forceinline__ void next(const GradParams& pr) {
         if (++tile < pr.kind[k].tiles) return;
         tile = 0;
@@ -54,6 +54,7 @@ struct Item {
         if (++ch < pr.nch) return;
         ch = 0;
         bh++;
+        if (++h == pr.H) h = 0;
     }
 };
 
@@ -62,6 +63,7 @@ __device__ __forceinline__ Item item_at(const GradParams& pr, int64_t i) {
     const int64_t c = i / pr.per_chunk;
     int r = static_cast<int>(i - c * pr.per_chunk);
     it.bh = static_cast<int>(c / pr.nch);
+    it.h = it.bh % pr.H;
     it.ch = static_cast<int>(c - static_cast<int64_t>(it.bh) * pr.nch);
     it.k = 0;
     while (r >= pr.kind[it.k].tiles) r -= pr.kind[it.k++].tiles;
@@ -252,12 +254,12 @@ __global__ void __launch_bounds__(kGradThreads, 1) linear_grad_kernel(const __gr
         float* wt = weights[warp - 4];
         Item it = item_at(pr, first);
         int made = -1;  // head and direction of the table
-        float la = 0.f;
+        float far[3] = {};  // the row's part of the weight of a block one, two, three blocks off
         for (int j = 0; j < m; j++) {
-            const int rev = pr.kind[it.k].reverse, key = 2 * (it.bh % pr.H) + rev;
+            const int rev = pr.kind[it.k].reverse, key = 2 * it.h + rev;
             if (key != made) {
                 made = key;
-                la = pr.log_a[it.bh % pr.H];
+                const float la = pr.log_a[it.h];
                 __syncwarp();
 #pragma unroll
                 for (int u = 0; u < 2; u++) {
@@ -265,6 +267,8 @@ __global__ void __launch_bounds__(kGradThreads, 1) linear_grad_kernel(const __gr
                     wt[x] = gap >= 0 ? gpow(la, gap) : 0.f;
                 }
                 wt[64 + lane] = gpow(la, rev ? lane : 31 - lane);
+#pragma unroll
+                for (int u = 0; u < 3; u++) far[u] = gpow(la, rev ? 32 * (u + 1) - lane : 32 * u + lane + 1);
                 __syncwarp();
             }
             if (!wait_warp(&s_full[j & 1], (j >> 1) & 1, fail)) {
@@ -276,7 +280,8 @@ __global__ void __launch_bounds__(kGradThreads, 1) linear_grad_kernel(const __gr
 #pragma unroll 1
             for (int cb = (warp - 4) >> 2; cb < 4; cb += 2) {
                 const int side = cb == w ? 0 : (rev ? cb > w : cb < w) ? 1 : -1;
-                const float rw = side > 0 ? gpow(la, rev ? 32 * cb - (32 * w + lane) : 32 * w + lane - 32 * cb - 31) : 0.f;
+                const int off = rev ? cb - w : w - cb;
+                const float rw = off == 1 ? far[0] : off == 2 ? far[1] : far[2];
                 weigh_block<2>(cols + 32 * cb, side, wt + 31 + lane, wt + 64, rw);
             }
             tmem_st_wait();
@@ -292,10 +297,10 @@ __global__ void __launch_bounds__(kGradThreads, 1) linear_grad_kernel(const __gr
         int made = -1;
         float la = 0.f;
         for (int j = 0; j < m; j++) {
-            const int rev = pr.kind[it.k].reverse, h = it.bh % pr.H;
-            if (h != made) {
-                made = h;
-                la = pr.log_a[h];
+            const int rev = pr.kind[it.k].reverse;
+            if (it.h != made) {
+                made = it.h;
+                la = pr.log_a[it.h];
             }
             const int nr = pr.T - it.ch * kTile < kTile ? pr.T - it.ch * kTile : kTile;
             const float f = row < nr ? gpow(la, rev ? nr - 1 - row : row + 1) : 0.f;
