@@ -86,7 +86,6 @@ __global__ void __launch_bounds__(kGradThreads, 1) linear_grad_kernel(const __gr
     __shared__ __align__(16) float weights[8][96];
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    grid_dep_wait();
     const int64_t total = static_cast<int64_t>(pr.BH) * pr.nch * pr.per_chunk;
     const int64_t first = total * blockIdx.x / gridDim.x;
     const int m = static_cast<int>(total * (blockIdx.x + 1) / gridDim.x - first);  // items of this CTA
@@ -121,6 +120,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) linear_grad_kernel(const __gr
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    grid_dep_wait();  // the states
     const uint32_t tmem = tmem_base_sh;
     auto fail_now = [&]() {
         if (atomicExch(&fail_sh, 1) == 0) record_error(err, kDevTimeout);

@@ -71,7 +71,7 @@ __global__ void __launch_bounds__(kScanThreads, 1) linear_scan_kernel(const __gr
     __shared__ float diag[64];   // weight of key c for row r of a diagonal block, at 31 + r - c
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    grid_dep_wait();    // the sequence table, the segments' states
+    if (pr.packed) grid_dep_wait();  // the sequence table; pieces' states are waited for below
     grid_dep_launch();
     // ---- which scan, 64 columns, segment, sequence and head
     int blk = blockIdx.x, si = 0;
@@ -159,27 +159,33 @@ __global__ void __launch_bounds__(kScanThreads, 1) linear_scan_kernel(const __gr
     float* seg0 = pr.seg + (static_cast<int64_t>(sc.seg_base) +
                             static_cast<int64_t>(bh) * pr.npiece * sc.tiles + tile) * (kDepth * kTile);
     const int64_t seg_step = static_cast<int64_t>(sc.tiles) * (kDepth * kTile);
-    if (kMode != kPieces && g > 0) {
-        // the pieces before this segment, decayed to its start and summed in order
-        float4 sum[2] = {};
+    if (kMode != kPieces && g > 0 && warp >= 4 && warp < 20) {
+        // the pieces before this segment, decayed to its start and summed in order, while the first copies and scores run
+        grid_dep_wait();
+        constexpr int kSumThreads = 512;
+        const int t = tid - 128;
+        float4 sum[4] = {};
         const int np_before = p0 / pr.piece_chunks;
-#pragma unroll 2
         for (int gg = 0; gg < np_before; gg++) {
             const float f = gpow(la, before(p0) - before((gg + 1) * pr.piece_chunks));
             const float4* sg = reinterpret_cast<const float4*>(seg0 + gg * seg_step);
 #pragma unroll
-            for (int i = 0; i < 2; i++) {
-                const float4 y = sg[tid + i * kScanThreads];
+            for (int i = 0; i < 4; i++) {
+                const float4 y = sg[t + i * kSumThreads];
                 sum[i].x += f * y.x;
                 sum[i].y += f * y.y;
                 sum[i].z += f * y.z;
                 sum[i].w += f * y.w;
             }
         }
-        reinterpret_cast<float4*>(wc)[tid] = sum[0];
-        reinterpret_cast<float4*>(wc)[tid + kScanThreads] = sum[1];
-        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < 4; i++) reinterpret_cast<float4*>(wc)[t + i * kSumThreads] = sum[i];
+        asm volatile("bar.sync 1, %0;" ::"n"(kSumThreads) : "memory");
     }
+    // A CTA's last chunk adds to no state that is read, unless the state leaves here; a ragged one has its rows set to
+    // zero on the way.
+    const int n_own =
+        n > 0 && !kStateOnly && !(sc.leave && g == have - 1) && rows_of(chunk_of(n - 1)) == kTile ? n - 1 : n;
     auto fail_now = [&]() {
         if (atomicExch(&fail_sh, 1) == 0) record_error(err, kDevTimeout);
     };
@@ -256,20 +262,22 @@ __global__ void __launch_bounds__(kScanThreads, 1) linear_scan_kernel(const __gr
             uint64_t a = a_first;  // stage s
             if (!kStateOnly && n > 0) ok = scores(a, &qk_full[0], 0, 0);
             for (int j = 0; j < n && ok; j++) {
-                // the parts and their product: two places of each where only the states are formed
-                const uint32_t pl = kStateOnly ? par : 0u, use = kStateOnly ? (j >> 1) & 1 : par;
-                ok = wait_one(&scaled[pl], use, fail) && (!kStateOnly || wait_one(&qk_full[s], ph, fail)) &&
-                     (j < (kStateOnly ? 2 : 1) || wait_one(&own_read[pl], use ^ 1u, fail));
-                if (!ok) break;
-                tc_fence_after();
-                const uint64_t bt = a + to_b + kmaj, wp = w0 + static_cast<uint64_t>(kWcBytes >> 4) * pl;
-                const uint32_t own = tmem + (kStateOnly ? 2 * kDepth * pl : kColOwn);
+                if (j < n_own) {
+                    // the parts and their product: two places of each where only the states are formed
+                    const uint32_t pl = kStateOnly ? par : 0u, use = kStateOnly ? (j >> 1) & 1 : par;
+                    ok = wait_one(&scaled[pl], use, fail) && (!kStateOnly || wait_one(&qk_full[s], ph, fail)) &&
+                         (j < (kStateOnly ? 2 : 1) || wait_one(&own_read[pl], use ^ 1u, fail));
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint64_t bt = a + to_b + kmaj, wp = w0 + static_cast<uint64_t>(kWcBytes >> 4) * pl;
+                    const uint32_t own = tmem + (kStateOnly ? 2 * kDepth * pl : kColOwn);
 #pragma unroll
-                for (int kk = 0; kk < kTile / 16; kk++) mma_bf16(own, bt + 128u * kk, wp + 128u * kk, kIdOwn2, kk > 0);
+                    for (int kk = 0; kk < kTile / 16; kk++) mma_bf16(own, bt + 128u * kk, wp + 128u * kk, kIdOwn2, kk > 0);
 #pragma unroll
-                for (int kk = 0; kk < kTile / 16; kk++)
-                    mma_bf16(own + kDepth, bt + 128u * kk, wp + 2 * (kPanelBytes >> 4) + 128u * kk, kIdOwn1, 1);
-                mma_commit(&own_full[pl]);
+                    for (int kk = 0; kk < kTile / 16; kk++)
+                        mma_bf16(own + kDepth, bt + 128u * kk, wp + 2 * (kPanelBytes >> 4) + 128u * kk, kIdOwn1, 1);
+                    mma_commit(&own_full[pl]);
+                }
                 if (kStateOnly) {
                     mma_commit(&qk_free[s]);
                 } else {
@@ -402,7 +410,7 @@ __global__ void __launch_bounds__(kScanThreads, 1) linear_scan_kernel(const __gr
             if (lane == 0) mbar_arrive(&x_ready);
         }
         bool ok = true;
-        for (int j = 0; j < n; j++) {
+        for (int j = 0; j < n_own; j++) {
             if (kMode == kStates) {
                 // the entering state of this chunk, on its way to memory by warp 3
                 if (j > 0 && !wait_warp(&x_sent, (j - 1) & 1, fail)) {
@@ -501,7 +509,7 @@ __global__ void __launch_bounds__(kScanThreads, 1) linear_scan_kernel(const __gr
         bool ok = true;
         int s = 0, ks = 0;            // stages of c and of b
         uint32_t ph = 0, kph = 0;
-        for (int j = 0; j < n; j++) {
+        for (int j = 0; j < n_own; j++) {
             const int nr = rows_of(chunk_of(j));
             uint8_t* st = smem + v_off + s * v_step;
             ok = wait_warp(&v_full[s], ph, fail);
