@@ -19,7 +19,9 @@
 //                     X <- g^n X + own, and the state that leaves the last chunk
 //   lin_out         : out_i = sum_j M_ij (a_i . b_j) c_j + f_i X^T a_i, M_ij = g^|i-j| on the
 //                     causal side, f_i = g^(i+1) forwards, g^(n-1-i) backwards.
-// All products are 64 x 64 register-tiled fp32 products out of shared memory. No exponent is ever
+// All products are 64 x 64 register-tiled fp32 products out of shared memory. FMAs bound them: the pipe is 50% busy over
+// launches of 1.6 waves of CTAs (gradients of 3 x 5 heads, T = 1301, 96 x 80: 145 us; prompts of 2 x 16 heads, T = 4096,
+// 128 x 128: 433 us, 30 TFLOP/s). No exponent is ever
 // negative, so no factor overflows for g <= 1; g^0 is 1 also for g = 0 (log_a = -inf).
 #include "lla_internal.cuh"
 #include "lla_linear.cuh"
@@ -34,8 +36,6 @@ constexpr int kSlab = 32;         // summed indices staged at a time
 constexpr int kLd = kC + 4;    // leading dimension of the transposed tiles (16-byte rows)
 constexpr int kMaxD = 128;
 
-// g^n for n >= 0
-__device__ __forceinline__ float gpow(float la, int n) { return n == 0 ? 1.f : expf(la * static_cast<float>(n)); }
 
 // One 64-token chunk: its sequence's batch index, its rows and the place of its state.
 struct ChunkAt {
@@ -72,22 +72,37 @@ __device__ __forceinline__ bool chunk_at(const LinSeqs& sq, int id, int h, Chunk
 }
 
 // acc[i][j] += sum_{k < K} X[k][i0 + i] Y[k][j0 + j], rows of kLd floats, i0 = 8 (tid / 16), j0 = 4 (tid % 16):
-// four shared-memory wavefronts for 32 FMAs of a warp (4 x 4 pieces took six).
+// four shared-memory wavefronts for 32 FMAs of a warp (4 x 4 pieces took six), two rows to an instruction (prompts
+// and gradients of 128 x 128 heads, T = 4096: 460 -> 433 us, 583 -> 564 us).
 template <int K>
 __device__ __forceinline__ void mul84(float (&acc)[8][4], const float* X, const float* Y) {
     X += threadIdx.x / 16 * 8;
     Y += threadIdx.x % 16 * 4;
+    f32x2 s[4][4];
+#pragma unroll
+    for (int i = 0; i < 4; i++)
+#pragma unroll
+        for (int j = 0; j < 4; j++) s[i][j] = pair2(acc[2 * i][j], acc[2 * i + 1][j]);
 #pragma unroll 8
     for (int k = 0; k < K; k++) {
-        const float4 x0 = *reinterpret_cast<const float4*>(X + k * kLd);
-        const float4 x1 = *reinterpret_cast<const float4*>(X + k * kLd + 4);
+        const ulonglong2 x0 = *reinterpret_cast<const ulonglong2*>(X + k * kLd);
+        const ulonglong2 x1 = *reinterpret_cast<const ulonglong2*>(X + k * kLd + 4);
         const float4 y = *reinterpret_cast<const float4*>(Y + k * kLd);
-        const float xs[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w}, ys[4] = {y.x, y.y, y.z, y.w};
+        const f32x2 xs[4] = {x0.x, x0.y, x1.x, x1.y};
+        const f32x2 ys[4] = {pair2(y.x, y.x), pair2(y.y, y.y), pair2(y.z, y.z), pair2(y.w, y.w)};
 #pragma unroll
-        for (int i = 0; i < 8; i++)
+        for (int i = 0; i < 4; i++)
 #pragma unroll
-            for (int j = 0; j < 4; j++) acc[i][j] += xs[i] * ys[j];
+            for (int j = 0; j < 4; j++) s[i][j] = fma2(xs[i], ys[j], s[i][j]);
     }
+#pragma unroll
+    for (int i = 0; i < 4; i++)
+#pragma unroll
+        for (int j = 0; j < 4; j++) {
+            const float2 f = split2(s[i][j]);
+            acc[2 * i][j] = f.x;
+            acc[2 * i + 1][j] = f.y;
+        }
 }
 
 // Four consecutive columns d..d+3 of a row of D columns, zeros past it; one load where rows keep it aligned.
@@ -452,7 +467,8 @@ __global__ void __launch_bounds__(kThreads) lin_sum_batch(const float* __restric
 // ---- decode step
 
 // One CTA per (b, h): S <- g S + k v^T and o = S^T q in one pass. Thread tid owns the column group
-// tid % G of VEC columns and rows tid / G + r * (kThreads / G).
+// tid % G of VEC columns and rows tid / G + r * (kThreads / G). Bound by the state's bytes: 64 x 16 heads of 128 x 64,
+// 67 MB, 8.3 us where half of it stays in L2 from step to step.
 template <typename T, int VEC>
 __global__ void __launch_bounds__(kThreads) lin_decode(const T* __restrict__ q, const T* __restrict__ k,
                                                        const T* __restrict__ v, const float* __restrict__ log_a,

@@ -12,8 +12,12 @@
 //     near    P C    [128 x 64]     out_i = near_i + f_i far_i
 // With the states given, chunks do not wait for one another: items are dealt out evenly to one CTA per SM
 // whatever the number of heads, where one scan per gradient took whole waves of CTAs (320 equal scans on 152
-// SMs at the headline shape: three waves for 2.1 waves of work, 367 us for the backward; now see below).
+// SMs at 4 x 16 heads, T = 8192, 128 x 64: three waves for 2.1 waves of work, 367 us for the backward against 270).
 // Consecutive items share their chunk's rows in L2. Two items are in flight: both kinds of accumulator are double.
+//
+// Measured there: 184 us for 20480 items, 848 MB at 4.6 TB/s (68% of the copy rate), tensor pipe 38% and issue slots 54%
+// busy; an item is 1.3 us. What bounds it is the chain scores -> P -> near -> out of two items in flight, with the
+// issue slots that P and out take; the two state scans before it take 89 us (514 MB at 5.8 TB/s).
 #include <atomic>
 
 #include "lla_linear_tc.cuh"

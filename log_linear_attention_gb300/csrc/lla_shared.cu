@@ -9,6 +9,9 @@
 // whole batch and never written; a sequence reads and writes only the buckets that hold own
 // tokens. Bucket l >= 1 of position pos (bit l - 1 of pos set) is [(pos >> l) << l, + 2^(l-1)):
 // it holds own tokens when its end is past P.
+//
+// Bound by the own states' bytes: 64 x 16 heads of 128 x 64, P = 30011, up to 4096 own tokens: 91 us for 492 MB, 80% of
+// the copy rate, half of it writes. The prefix's kernel (22 us by itself) runs beside the own states' streams.
 #include "lla_linear.cuh"
 
 namespace lla {
@@ -109,6 +112,7 @@ __global__ void __launch_bounds__(kThreads) shared_own(const T* __restrict__ q, 
     const int64_t t = tpos[b];
     if (t < P || t >= (int64_t(1) << (Lmax - 1))) {
         if (tid == 0) record_error(err, kDevBadInput);
+        grid_dep_wait();  // with every sequence skipped too, this kernel ends after the one that writes the workspace
         return;
     }
     for (int x = tid; x < dk; x += kThreads) {
