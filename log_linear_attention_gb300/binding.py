@@ -423,15 +423,27 @@ def device_error(stream=None) -> int:
     return int(load().lla_device_error(_stream_handle(stream)))
 
 
+def _ready(t_, dtype, shape, index):
+    """True for a contiguous tensor of this dtype and shape on GPU ``index``: the usual case, found in one expression
+    (single tokens are bound by the host). Anything else goes through the checks that name what is wrong."""
+    return (type(t_) is _torch_module.Tensor and t_.dtype is dtype and t_.shape == shape and t_.get_device() == index
+            and t_.is_contiguous())
+
+
 def _linear_inputs(names, tensors, log_a, H):
     """Checks of the linear-attention calls: CUDA tensors of one dtype and device, log_a [H] fp32."""
     torch = _torch()
     q = tensors[0]
     device, dtype = q.device, q.dtype
+    index = q.get_device()
     for n, t_ in zip(names, tensors):
+        if type(t_) is torch.Tensor and t_.dtype is dtype and t_.get_device() == index >= 0 and t_.is_contiguous():
+            continue
         _check(t_, n, device)
         if t_.dtype != dtype:
             raise TypeError(f"{', '.join(names)} must share one dtype")
+    if _ready(log_a, torch.float32, (H,), index):
+        return
     _check(log_a, "log_a", device)
     if log_a.dtype != torch.float32 or log_a.shape != (H,):
         raise ValueError(f"log_a must be float32 [{H}] (one decay per head)")
@@ -441,9 +453,10 @@ def _state(t_, name, shape, device):
     """Address of an optional fp32 state tensor of the given shape (None: NULL)."""
     if t_ is None:
         return None
-    _check(t_, name, device)
-    if t_.dtype != _torch().float32 or t_.shape != shape:
-        raise ValueError(f"{name} must be float32 {list(shape)}, got {t_.dtype} {list(t_.shape)}")
+    if not _ready(t_, _torch().float32, shape, device.index):
+        _check(t_, name, device)
+        if t_.dtype != _torch().float32 or t_.shape != shape:
+            raise ValueError(f"{name} must be float32 {list(shape)}, got {t_.dtype} {list(t_.shape)}")
     return t_.data_ptr()
 
 
@@ -584,14 +597,20 @@ def decode_step_shared(q, k, v, log_a, lam, prefix_states, prefix_len: int, pref
     torch = _torch()
     B, H, dk = q.shape
     dv = v.shape[-1]
-    for t_, n in ((q, "q"), (k, "k"), (v, "v"), (log_a, "log_a"), (lam, "lambda"), (t, "t")):
-        _check(t_, n, q.device)
-    if k.dtype != q.dtype or v.dtype != q.dtype:
-        raise TypeError("q, k and v must share one dtype")
-    if log_a.dtype != torch.float32 or lam.dtype != torch.float32:
-        raise TypeError("log_a and lambda must be float32")
-    if t.dtype != torch.int64 or t.shape != (B,):
-        raise ValueError("t must be int64 [B]")
+    index = q.get_device()
+    f32 = torch.float32
+    if not (index >= 0 and _ready(k, q.dtype, q.shape, index) and _ready(v, q.dtype, (B, H, dv), index)
+            and q.is_contiguous() and _ready(log_a, f32, (B, H), index) and type(lam) is torch.Tensor
+            and lam.get_device() == index and lam.is_contiguous() and lam.dtype is f32
+            and _ready(t, torch.int64, (B,), index)):
+        for t_, n in ((q, "q"), (k, "k"), (v, "v"), (log_a, "log_a"), (lam, "lambda"), (t, "t")):
+            _check(t_, n, q.device)
+        if k.dtype != q.dtype or v.dtype != q.dtype:
+            raise TypeError("q, k and v must share one dtype")
+        if log_a.dtype != f32 or lam.dtype != f32:
+            raise TypeError("log_a and lambda must be float32")
+        if t.dtype != torch.int64 or t.shape != (B,):
+            raise ValueError("t must be int64 [B]")
     if prefix_states is None or prefix_decay is None or states is None or prefix_states.dim() != 4 or states.dim() != 5:
         raise ValueError("prefix_states [H,Lp,dk,dv], prefix_decay [B,H] and states [B,H,Lmax,dk,dv] are needed")
     Lp, Lmax = int(prefix_states.shape[1]), int(states.shape[2])
