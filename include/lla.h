@@ -322,8 +322,10 @@ int lla_gdn_forward_profile(const void* q, const void* k, const void* v, const f
  *   state0    [B0,H,dk,dv]   fp32   S_{-1}, the state that the sequences go on from: B0 = 0 (state0
  *                                   NULL: zeros), 1 (one state for the whole batch, e.g. of a common
  *                                   prefix that was computed once) or B (one each).
- *   state_out [B,H,dk,dv]    fp32   written: S_{T-1}. NULL: not wanted. Must not overlap state0.
+ *   state_out [B,H,dk,dv]    fp32   written: S_{T-1}. NULL: not wanted.
  *   q, k [B,H,T,dk], v, out [B,H,T,dv]  dtype, as lla_forward; any T >= 1 (no chunk argument).
+ *   Nothing that a call writes may overlap what it reads or writes besides (refused: LLA_ERR_INVALID_ARG),
+ *   but for the states that a step updates in place. Prompts: B H (packed: n_seq H) up to 65535.
  *   dk, dv 1..128. bf16 with dk and dv multiples of 8 runs on tensor cores (128-token chunks, bf16
  *   operands, fp32 accumulation, states in fp32); every other shape runs fp32 arithmetic on CUDA
  *   cores. Sums are formed in a fixed order: repeated calls give identical bits.
@@ -345,8 +347,7 @@ int lla_gdn_forward_profile(const void* q, const void* k, const void* v, const f
  *   dstate_out [B,H,dk,dv]  fp32    upstream gradient of state_out; NULL: zeros
  *   dq, dk [B,H,T,dk], dv [B,H,T,dv]  dtype, written
  *   dstate0    [B0,H,dk,dv] fp32    written (B0 = 1: summed over the batch in order); NULL: not wanted
- *   The outputs must not overlap any input or each other. Nothing of the forward is kept: its states
- *   are formed again from k, v and state0.
+ *   Nothing of the forward is kept: its states are formed again from k, v and state0.
  *
  * lla_linear_decode_step: one token of every sequence; state [B,H,dk,dv] fp32 is read and written in
  *   place (S_{t-1} on entry, S_t on return; what lla_linear_forward leaves in state_out). q, k
@@ -390,6 +391,7 @@ int lla_linear_decode_step(const void* q, const void* k, const void* v, const fl
  *   and output untouched) and LLA_ERR_DEVICE is recorded in the device error word.
  *   After a prompt of n own tokens handled by lla_prefill_state on its own, the states are valid here
  *   where P is a multiple of a power of two >= n (then own levels do not depend on P).
+ *   Nothing that is written may overlap another argument (refused: LLA_ERR_INVALID_ARG).
  *   dk 1..256; dv in {16, 32, 64, 128}; Lmax in 1..40. Workspace from the library's pool.
  */
 int lla_decode_step_shared(const void* q, const void* k, const void* v, const float* log_a, const float* lambda,

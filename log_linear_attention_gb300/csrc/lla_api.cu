@@ -1,6 +1,7 @@
 // Host side of the C ABI declared in include/lla.h: argument validation,
 // path selection (tcgen05 tensor-core path or SIMT path), workspace handling
 // and the per-device error word.
+#include <initializer_list>
 #include <mutex>
 
 #include "../../include/lla.h"
@@ -632,10 +633,29 @@ int lla_device_error(void* stream) {
 
 namespace {
 
-bool overlap(const void* a, size_t na, const void* b, size_t nb) {
-    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-    return a && b && x < y + nb && y < x + na;
+// One argument's bytes (p null: not given).
+struct Span {
+    const void* p;
+    size_t bytes;
+};
+
+bool overlap(const Span& a, const Span& b) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
+    return a.p && b.p && x < y + b.bytes && y < x + a.bytes;
 }
+
+// Whether a written argument overlaps one that is read, or another written one.
+bool clash(std::initializer_list<Span> written, std::initializer_list<Span> read) {
+    for (const Span* w = written.begin(); w != written.end(); w++) {
+        for (const Span& r : read)
+            if (overlap(*w, r)) return true;
+        for (const Span* o = written.begin(); o != w; o++)
+            if (overlap(*w, *o)) return true;
+    }
+    return false;
+}
+
+size_t type_bytes(int dtype) { return dtype == LLA_BF16 ? 2 : 4; }
 
 // Checks shared by the linear prefill, packed prefill and backward: `rows` = rows of one tensor,
 // batch = sequences, b0 = entering states.
@@ -670,6 +690,7 @@ struct PoolBuffer {  // workspace from the library pool on one stream, returned 
     }
     int give(cudaError_t e) {
         const cudaError_t f = p ? cudaFreeAsync(p, s) : cudaSuccess;
+        if (e != cudaSuccess || f != cudaSuccess) cudaGetLastError();  // reported here, not by the next call
         return (e == cudaSuccess && f == cudaSuccess) ? LLA_OK : LLA_ERR_CUDA;
     }
 };
@@ -697,7 +718,10 @@ int lla_linear_forward(const void* q, const void* k, const void* v, const float*
     if (st != LLA_OK) return st;
     if (!out || !aligned16(out) || !aligned16(state_out)) return LLA_ERR_INVALID_ARG;
     const size_t msz = (size_t)dk * dv * sizeof(float);
-    if (overlap(state0, B0 * H * msz, state_out, B * H * msz)) return LLA_ERR_INVALID_ARG;
+    const size_t heads = (size_t)B * H, row = heads * T * type_bytes(dtype);
+    if (clash({{out, row * dv}, {state_out, heads * msz}},
+              {{q, row * dk}, {k, row * dk}, {v, row * dv}, {log_a, H * sizeof(float)}, {state0, B0 * H * msz}}))
+        return LLA_ERR_INVALID_ARG;
     const int dev = current_device();
     if (dev < 0) return LLA_ERR_CUDA;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
@@ -728,7 +752,11 @@ int lla_linear_forward_varlen(const void* q, const void* k, const void* v, const
     if (st != LLA_OK) return st;
     if (!out || !aligned16(out) || !aligned16(state_out)) return LLA_ERR_INVALID_ARG;
     const size_t msz = (size_t)dk * dv * sizeof(float);
-    if (overlap(state0, n0 * H * msz, state_out, n_seq * H * msz)) return LLA_ERR_INVALID_ARG;
+    const size_t row = (size_t)H * total_T * type_bytes(dtype);
+    if (clash({{out, row * dv}, {state_out, n_seq * H * msz}},
+              {{q, row * dk}, {k, row * dk}, {v, row * dv}, {log_a, H * sizeof(float)}, {state0, n0 * H * msz},
+               {cu_seqlens, ((size_t)n_seq + 1) * sizeof(int32_t)}}))
+        return LLA_ERR_INVALID_ARG;
     const int dev = current_device();
     if (dev < 0) return LLA_ERR_CUDA;
     int* err = error_word(dev);
@@ -782,11 +810,16 @@ int lla_linear_backward(const void* q, const void* k, const void* v, const float
         !aligned16(dv) || !aligned16(dstate0))
         return LLA_ERR_INVALID_ARG;
     if (dstate0 && B0 == 0) return LLA_ERR_INVALID_ARG;
+    const size_t msz = (size_t)dk_ * dv_ * sizeof(float);
+    const size_t heads = (size_t)B * H, row = heads * T * type_bytes(dtype);
+    if (clash({{dq, row * dk_}, {dk, row * dk_}, {dv, row * dv_}, {dstate0, B0 * H * msz}},
+              {{q, row * dk_}, {k, row * dk_}, {v, row * dv_}, {dout, row * dv_}, {log_a, H * sizeof(float)},
+               {state0, B0 * H * msz}, {dstate_out, heads * msz}}))
+        return LLA_ERR_INVALID_ARG;
     const int dev = current_device();
     if (dev < 0) return LLA_ERR_CUDA;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const lla::LinSeqs sq = dense_seqs(B, H, T);
-    const size_t msz = (size_t)dk_ * dv_ * sizeof(float);
     int* err = error_word(dev);
     if (!err) return LLA_ERR_CUDA;
     const bool sum = dstate0 && B0 == 1 && B > 1;  // gradients of one shared state: a part per sequence, then their sum
@@ -838,6 +871,10 @@ int lla_linear_decode_step(const void* q, const void* k, const void* v, const fl
     if (B < 1 || H < 1 || dk < 1 || dv < 1) return LLA_ERR_INVALID_ARG;
     if (dk > 128 || dv > 128) return LLA_ERR_UNSUPPORTED;
     if ((int64_t)B * H > 0x7fffffff) return LLA_ERR_UNSUPPORTED;
+    const size_t heads = (size_t)B * H, row = heads * type_bytes(dtype);
+    if (clash({{out, row * dv}, {state, heads * dk * dv * sizeof(float)}},
+              {{q, row * dk}, {k, row * dk}, {v, row * dv}, {log_a, H * sizeof(float)}}))
+        return LLA_ERR_INVALID_ARG;
     if (current_device() < 0) return LLA_ERR_CUDA;
     return lla::linear_decode_step(dtype, q, k, v, log_a, state, out, B, H, dk, dv,
                                    static_cast<cudaStream_t>(stream)) == cudaSuccess
@@ -862,6 +899,12 @@ int lla_decode_step_shared(const void* q, const void* k, const void* v, const fl
         return LLA_ERR_INVALID_ARG;
     if (dk > 256 || (dv != 16 && dv != 32 && dv != 64 && dv != 128)) return LLA_ERR_UNSUPPORTED;
     if ((int64_t)B * H > 0x7fffffff || H > 65535 || B > 65535) return LLA_ERR_UNSUPPORTED;
+    const size_t heads = (size_t)B * H, row = heads * type_bytes(dtype), msz = (size_t)dk * dv * sizeof(float);
+    if (clash({{out, row * dv}, {fenwick_states, heads * Lmax * msz}, {prefix_decay, heads * sizeof(float)}},
+              {{q, row * dk}, {k, row * dk}, {v, row * dv}, {log_a, heads * sizeof(float)},
+               {lambda, heads * Lmax * sizeof(float)}, {prefix_states, (size_t)H * Lp * msz},
+               {t, B * sizeof(int64_t)}}))
+        return LLA_ERR_INVALID_ARG;
     const int dev = current_device();
     if (dev < 0) return LLA_ERR_CUDA;
     int* err = error_word(dev);

@@ -84,6 +84,43 @@ def test_shared_refuses(lib, over, expect):
                                       2, a["dk"], a["dv"], a["Lmax"], a["dtype"]) == expect
 
 
+# arguments far enough apart for the sizes below, each at its own place; `over` moves one onto another
+NAMES = ("q", "k", "v", "log_a", "state0", "dout", "dstate_out", "out", "state_out", "dq", "dk", "dv", "dstate0", "cu",
+         "lambda", "prefix", "decay", "states", "t")
+AT = {n: A + (i << 24) for i, n in enumerate(NAMES)}
+
+
+@pytest.mark.parametrize("call,written,onto", [
+    ("forward", "out", "v"), ("forward", "out", "q"), ("forward", "out", "state0"), ("forward", "state_out", "k"),
+    ("forward", "state_out", "state0"), ("forward", "state_out", "out"), ("forward", "out", "log_a"),
+    ("varlen", "out", "v"), ("varlen", "out", "cu"), ("varlen", "state_out", "state0"), ("varlen", "state_out", "out"),
+    ("backward", "dq", "q"), ("backward", "dk", "dout"), ("backward", "dv", "dq"), ("backward", "dstate0", "dstate_out"),
+    ("backward", "dstate0", "state0"), ("backward", "dv", "v"),
+    ("decode", "out", "v"), ("decode", "states", "out"), ("decode", "states", "q"),
+    ("shared", "out", "q"), ("shared", "states", "prefix"), ("shared", "decay", "log_a"), ("shared", "decay", "states"),
+    ("shared", "states", "t"), ("shared", "out", "lambda"),
+])
+@pytest.mark.parametrize("by", [0, 16, -16])
+def test_overlaps_are_refused(lib, call, written, onto, by):
+    """Also by the last 16 bytes of one and the first of the other: every argument here has at least 32."""
+    a = dict(AT)
+    a[written] = a[onto] + by
+    x = lambda *names: [a[n] for n in names]  # noqa: E731
+    if call == "forward":
+        st = lib.lla_linear_forward(*x("q", "k", "v", "log_a", "state0", "out", "state_out"), 3, 3, 8, 5, 16, 16, None, 1)
+    elif call == "varlen":
+        st = lib.lla_linear_forward_varlen(*x("q", "k", "v", "log_a", "state0", "out", "state_out", "cu"), 8, 8, 8, 50, 20,
+                                           16, 16, None, 1)
+    elif call == "backward":
+        st = lib.lla_linear_backward(*x("q", "k", "v", "log_a", "state0", "dout", "dstate_out", "dq", "dk", "dv",
+                                        "dstate0"), 3, 3, 8, 5, 16, 16, None, 1)
+    elif call == "decode":
+        st = lib.lla_linear_decode_step(*x("q", "k", "v", "log_a", "states", "out"), None, 3, 8, 16, 16, 1)
+    else:
+        st = lib.lla_decode_step_shared(*x("q", "k", "v", "log_a", "lambda", "prefix"), 9, 5,
+                                        *x("decay", "states", "t", "out"), None, 4, 8, 16, 16, 5, 1)
+    assert st == BAD
+
 def test_binding_refuses_host_tensors():
     torch = pytest.importorskip("torch")
     x = torch.zeros(1, 1, 4, 16)
