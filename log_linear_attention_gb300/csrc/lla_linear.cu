@@ -234,7 +234,7 @@ __global__ void __launch_bounds__(kThreads) lin_carry(LinStateJobs jobs, LinSeqs
         first = sq.coff[b];
         if (len < 0) return;  // rejected by the table kernel: nothing of it is written
     }
-    const int N = (len + kC - 1) / kC;
+    const int N = static_cast<int>((static_cast<unsigned>(len) + kC - 1) / kC);  // len may be 2^31 - 1
     const float la = log_a[h];
     const float gC = gpow(la, kC), gl = gpow(la, len - (N - 1) * kC);
     float x = jb.in ? jb.in[(static_cast<int64_t>(jb.in_shared ? 0 : b) * sq.H + h) * msz + e] : 0.f;
@@ -390,11 +390,15 @@ cudaError_t run_t(const LinStateJobs& jobs, const LinScans& scans, const LinSeqs
 // its rows lie behind every earlier entry of cu and inside the tensor and it is no longer than
 // max_T; accepted ones are disjoint, so their chunks fit the total / kC + n that the host counts
 // with. One block of 1024 threads.
+constexpr int kMostSorted = 1024;
 __global__ void __launch_bounds__(1024) lin_table(const int32_t* __restrict__ cu, int n, int total, int max_T,
                                                   int2* __restrict__ tab, int* __restrict__ coff,
                                                   int* __restrict__ order, int* err) {
     __shared__ int wsum[32], wmax[32];
+    __shared__ __align__(16) int lens[kMostSorted];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the tensor-core scan sets up beside this kernel
+    if (tid < kMostSorted) lens[tid] = -2;  // shorter than any sequence
     int carry = 0, high = 0;
     for (int b0 = 0; b0 < n; b0 += 1024) {
         const int b = b0 + tid;
@@ -414,7 +418,7 @@ __global__ void __launch_bounds__(1024) lin_table(const int32_t* __restrict__ cu
         const bool ok = b < n && c0 >= 0 && c0 >= m && c1 >= c0 && c1 <= total && c1 - c0 <= max_T;
         if (b < n && !ok) record_error(err, kDevBadInput);
         const int len = ok ? c1 - c0 : 0;
-        const int chunks = (len + kC - 1) / kC;
+        const int chunks = static_cast<int>((static_cast<unsigned>(len) + kC - 1) / kC);
         int incl = chunks;
 #pragma unroll
         for (int off = 1; off < 32; off <<= 1) {
@@ -427,6 +431,7 @@ __global__ void __launch_bounds__(1024) lin_table(const int32_t* __restrict__ cu
         for (int w = 0; w < warp; w++) sum += wsum[w];
         if (b < n) {
             tab[b] = make_int2(ok ? c0 : 0, ok ? len : -1);
+            if (b < kMostSorted) lens[b] = ok ? len : -1;
             coff[b] = sum + incl - chunks;
         }
         for (int w = warp; w < 32; w++) sum += wsum[w];
@@ -438,16 +443,16 @@ __global__ void __launch_bounds__(1024) lin_table(const int32_t* __restrict__ cu
     if (tid == 0) coff[n] = carry;
     __syncthreads();
     if (!order) return;
-    // longest first (ties by index); past 4096 sequences the n^2 comparisons cost more than the
-    // order gives, and so many sequences balance by their number
+    // longest first (ties by index); more sequences than kMostSorted balance by their number
     for (int b = tid; b < n; b += 1024) {
         int rank = b;
-        if (n <= 4096) {
+        if (n <= kMostSorted) {
             rank = 0;
-            const int len = tab[b].y;
-            for (int x = 0; x < n; x++) {
-                const int y = tab[x].y;
-                rank += y > len || (y == len && x < b);
+            const int len = lens[b];
+            for (int x = 0; x < n; x += 4) {
+                const int4 y = *reinterpret_cast<const int4*>(lens + x);
+                rank += (y.x > len || (y.x == len && x < b)) + (y.y > len || (y.y == len && x + 1 < b)) +
+                        (y.z > len || (y.z == len && x + 2 < b)) + (y.w > len || (y.w == len && x + 3 < b));
             }
         }
         order[rank] = b;

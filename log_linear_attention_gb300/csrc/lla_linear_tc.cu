@@ -76,53 +76,6 @@ __global__ void __launch_bounds__(kScanThreads, 1) linear_scan_kernel(const __gr
     __shared__ float diag[64];   // weight of key c for row r of a diagonal block, at 31 + r - c
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    if (pr.packed) grid_dep_wait();  // the sequence table; pieces' states are waited for below
-    grid_dep_launch();
-    // ---- which scan, 64 columns, segment, sequence and head
-    int blk = blockIdx.x, si = 0;
-    const int ncta = kMode == kPieces ? pr.npiece : pr.nseg;  // of one sequence, head and 64 columns
-    while (si + 1 < pr.count && blk >= pr.batch * pr.sq.H * ncta * pr.scan[si].tiles)
-        blk -= pr.batch * pr.sq.H * ncta * pr.scan[si++].tiles;
-    const LinTcScan& sc = pr.scan[si];
-    const int tile = blk % sc.tiles;
-    blk /= sc.tiles;
-    const int g = blk % ncta;
-    blk /= ncta;
-    const int h = blk % pr.sq.H;
-    int b = blk / pr.sq.H, len = pr.sq.T, row0 = 0;
-    if (pr.packed) {
-        b = pr.sq.order[b];
-        row0 = pr.sq.tab[b].x;
-        len = pr.sq.tab[b].y;
-        if (len < 0) return;
-    }
-    const int bh = b * pr.sq.H + h;
-    const int z = pr.packed ? h : bh;  // outermost coordinate of the tensor maps
-    const int nch = (len + kTile - 1) / kTile;
-    const int have = nch <= pr.seg_chunks ? 1 : (nch + pr.seg_chunks - 1) / pr.seg_chunks;
-    const int span = kMode == kPieces ? pr.piece_chunks : pr.seg_chunks;
-    const int p0 = g * span;
-    if (kMode == kPieces ? p0 >= (have - 1) * pr.seg_chunks : g >= have) return;
-    const int n = nch - p0 < span ? nch - p0 : span;  // chunks of this CTA
-    const bool rev = kStateOnly && sc.reverse != 0;
-    auto chunk_of = [&](int j) { return rev ? nch - 1 - (p0 + j) : p0 + j; };
-    auto rows_of = [&](int c) { return len - c * kTile < kTile ? len - c * kTile : kTile; };
-    // tokens ahead of the p-th chunk in scan order
-    auto before = [&](int p) { return !rev ? p * kTile : (p == 0 ? 0 : len - (nch - p) * kTile); };
-    const int d1 = sc.d1, d2 = sc.d2, c0 = tile * kDepth;
-    const int np = d1 > 64 ? 2 : 1, ksteps = (d1 + 15) / 16;
-    // Shared memory. kFull: stages of a | b | c, two (three of narrow rows), then the parts of w o C and X. Only states:
-    // as many of b, four of c (free once cut; kStates: three, and one of the states on its way to memory) and two of the
-    // parts, so that copies, cutting and product all overlap.
-    const int k_bytes = np * kPanelBytes;
-    const int nk = np == 1 ? 3 : 2, nv = kMode == kFull ? nk : kMode == kPieces ? 4 : 3;
-    const int k_step = kStateOnly ? k_bytes : 2 * k_bytes + kPanelBytes;  // from one stage of b to the next
-    const int v_step = kStateOnly ? kPanelBytes : k_step;
-    const int k_off = kStateOnly ? 0 : k_bytes, v_off = kStateOnly ? nk * k_bytes : 2 * k_bytes;
-    uint8_t* wc = smem + (kStateOnly ? v_off + nv * kPanelBytes : nk * k_step);
-    uint8_t* xs = wc + (kStateOnly ? 2 : 1) * kWcBytes;  // kFull, kStates
-    volatile int* fail = &fail_sh;
-
     if (tid == 0) {
         for (int s = 0; s < kMaxStages; s++) {
             mbar_init(&qk_full[s], 1);
@@ -148,6 +101,53 @@ __global__ void __launch_bounds__(kScanThreads, 1) linear_scan_kernel(const __gr
         fence_mbar_init();
         fail_sh = 0;
     }
+    if (pr.packed) grid_dep_wait();  // the sequence table; pieces' states are waited for below
+    grid_dep_launch();
+    // ---- which scan, 64 columns, segment, sequence and head
+    int blk = blockIdx.x, si = 0;
+    const int ncta = kMode == kPieces ? pr.npiece : pr.nseg;  // of one sequence, head and 64 columns
+    while (si + 1 < pr.count && blk >= pr.batch * pr.sq.H * ncta * pr.scan[si].tiles)
+        blk -= pr.batch * pr.sq.H * ncta * pr.scan[si++].tiles;
+    const LinTcScan& sc = pr.scan[si];
+    const int tile = blk % sc.tiles;
+    blk /= sc.tiles;
+    const int g = blk % ncta;
+    blk /= ncta;
+    const int h = blk % pr.sq.H;
+    int b = blk / pr.sq.H, len = pr.sq.T, row0 = 0;
+    if (pr.packed) {
+        b = pr.sq.order[b];
+        row0 = pr.sq.tab[b].x;
+        len = pr.sq.tab[b].y;
+        if (len < 0) return;
+    }
+    const int bh = b * pr.sq.H + h;
+    const int z = pr.packed ? h : bh;  // outermost coordinate of the tensor maps
+    const int nch = static_cast<int>((static_cast<unsigned>(len) + kTile - 1) / kTile);  // len may be 2^31 - 1
+    const int have = nch <= pr.seg_chunks ? 1 : (nch + pr.seg_chunks - 1) / pr.seg_chunks;
+    const int span = kMode == kPieces ? pr.piece_chunks : pr.seg_chunks;
+    const int p0 = g * span;
+    if (kMode == kPieces ? p0 >= (have - 1) * pr.seg_chunks : g >= have) return;
+    const int n = nch - p0 < span ? nch - p0 : span;  // chunks of this CTA
+    const bool rev = kStateOnly && sc.reverse != 0;
+    auto chunk_of = [&](int j) { return rev ? nch - 1 - (p0 + j) : p0 + j; };
+    auto rows_of = [&](int c) { return len - c * kTile < kTile ? len - c * kTile : kTile; };
+    // tokens ahead of the p-th chunk in scan order
+    auto before = [&](int p) { return !rev ? p * kTile : (p == 0 ? 0 : len - (nch - p) * kTile); };
+    const int d1 = sc.d1, d2 = sc.d2, c0 = tile * kDepth;
+    const int np = d1 > 64 ? 2 : 1, ksteps = (d1 + 15) / 16;
+    // Shared memory. kFull: stages of a | b | c, two (three of narrow rows), then the parts of w o C and X. Only states:
+    // as many of b, four of c (free once cut; kStates: three, and one of the states on its way to memory) and two of the
+    // parts, so that copies, cutting and product all overlap.
+    const int k_bytes = np * kPanelBytes;
+    const int nk = np == 1 ? 3 : 2, nv = kMode == kFull ? nk : kMode == kPieces ? 4 : 3;
+    const int k_step = kStateOnly ? k_bytes : 2 * k_bytes + kPanelBytes;  // from one stage of b to the next
+    const int v_step = kStateOnly ? kPanelBytes : k_step;
+    const int k_off = kStateOnly ? 0 : k_bytes, v_off = kStateOnly ? nk * k_bytes : 2 * k_bytes;
+    uint8_t* wc = smem + (kStateOnly ? v_off + nv * kPanelBytes : nk * k_step);
+    uint8_t* xs = wc + (kStateOnly ? 2 : 1) * kWcBytes;  // kFull, kStates
+    volatile int* fail = &fail_sh;
+
     if (warp == 1) tmem_alloc(&tmem_base_sh, 512);
     const float la = pr.log_a[h];
     if (tid >= 64 && tid < 64 + 129) pw[tid - 64] = gpow(la, tid - 64);
@@ -709,18 +709,21 @@ cudaError_t linear_tc_run(const LinTcPlan& pl, const LinTcMap* maps, int n_maps,
         if (scans[i].d1 > d1) d1 = scans[i].d1;
     }
     const unsigned per_seg = static_cast<unsigned>(pl.batch) * sq.H * tiles;
+    // beside the end of the kernel before it, where that is the table's or the pieces'
+    auto launch = [&](auto kern, unsigned ctas, int smem, bool beside) {
+        if (beside) return launch_pdl(kern, dim3(ctas), dim3(kScanThreads), smem, stream, pr, err);
+        kern<<<ctas, kScanThreads, smem, stream>>>(pr, err);
+        return cudaSuccess;
+    };
     if (pl.nseg > 1) {
-        linear_scan_kernel<kPieces><<<per_seg * pl.npiece, kScanThreads, smem_bytes(kPieces, d1), stream>>>(pr, err);
+        const cudaError_t e = launch(linear_scan_kernel<kPieces>, per_seg * pl.npiece, smem_bytes(kPieces, d1), packed);
+        if (e != cudaSuccess) return e;
         note_launch(stream, "linear_scan_pieces");
     }
     const auto kern = states ? linear_scan_kernel<kStates> : linear_scan_kernel<kFull>;
     const int smem = smem_bytes(states ? kStates : kFull, d1);
-    if (pl.nseg > 1) {
-        const cudaError_t e = launch_pdl(kern, dim3(per_seg * pl.nseg), dim3(kScanThreads), smem, stream, pr, err);
-        if (e != cudaSuccess) return e;
-    } else {
-        kern<<<per_seg, kScanThreads, smem, stream>>>(pr, err);
-    }
+    const cudaError_t e = launch(kern, per_seg * pl.nseg, smem, packed || pl.nseg > 1);
+    if (e != cudaSuccess) return e;
     note_launch(stream, states ? "linear_scan_states" : "linear_scan");
     return cudaGetLastError();
 }
