@@ -37,7 +37,6 @@ namespace lla {
 namespace {
 
 constexpr int kScanThreads = 1024;
-constexpr int kMaxStages = 4;
 constexpr int kWcBytes = 3 * kPanelBytes;
 constexpr int kSmemMost = 232448 - 2048;  // 227 KB less the static part
 
@@ -67,8 +66,12 @@ __global__ void __launch_bounds__(kScanThreads, 1) linear_scan_kernel(const __gr
     constexpr int kCutWarps = kStateOnly ? 16 : 8;  // where there is no P, its warps cut w o C too
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    __shared__ uint64_t qk_full[kMaxStages], v_full[kMaxStages], qk_free[kMaxStages], v_free[kMaxStages];
-    __shared__ uint64_t scaled[2], own_full[2], own_read[2], x_ready, x_free, x_put, x_sent, s_full[2], p_ready, o_full, o_read, drain;
+    // one barrier per lane of the warp that sets them up
+    __shared__ uint64_t bars[32];
+    uint64_t *const qk_full = bars, *const v_full = bars + 4, *const qk_free = bars + 8, *const v_free = bars + 12;
+    uint64_t *const scaled = bars + 16, *const own_full = bars + 18, *const own_read = bars + 20, *const s_full = bars + 22;
+    uint64_t &x_ready = bars[24], &x_free = bars[25], &x_put = bars[26], &x_sent = bars[27];
+    uint64_t &p_ready = bars[28], &o_full = bars[29], &o_read = bars[30], &drain = bars[31];
     __shared__ uint32_t tmem_base_sh;
     __shared__ int fail_sh;
     __shared__ float pw[132];    // g^n
@@ -76,31 +79,6 @@ __global__ void __launch_bounds__(kScanThreads, 1) linear_scan_kernel(const __gr
     __shared__ float diag[64];   // weight of key c for row r of a diagonal block, at 31 + r - c
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    if (tid == 0) {
-        for (int s = 0; s < kMaxStages; s++) {
-            mbar_init(&qk_full[s], 1);
-            mbar_init(&v_full[s], 1);
-            mbar_init(&qk_free[s], 1);
-            mbar_init(&v_free[s], kStateOnly ? kCutWarps : 1);
-        }
-        for (int s = 0; s < 2; s++) {  // kFull: the first of each
-            mbar_init(&scaled[s], kCutWarps);
-            mbar_init(&own_full[s], 1);
-            mbar_init(&own_read[s], 8);
-        }
-        mbar_init(&x_ready, 8);
-        mbar_init(&x_free, 1);
-        mbar_init(&x_put, 8);
-        mbar_init(&x_sent, 1);
-        mbar_init(&s_full[0], 1);
-        mbar_init(&s_full[1], 1);
-        mbar_init(&p_ready, 8);
-        mbar_init(&o_full, 1);
-        mbar_init(&o_read, 4);
-        mbar_init(&drain, 1);
-        fence_mbar_init();
-        fail_sh = 0;
-    }
     if (pr.packed) grid_dep_wait();  // the sequence table; pieces' states are waited for below
     grid_dep_launch();
     // ---- which scan, 64 columns, segment, sequence and head
@@ -148,6 +126,14 @@ __global__ void __launch_bounds__(kScanThreads, 1) linear_scan_kernel(const __gr
     uint8_t* xs = wc + (kStateOnly ? 2 : 1) * kWcBytes;  // kFull, kStates
     volatile int* fail = &fail_sh;
 
+    if (warp == 0) {
+        // arrivals of a phase: one but where several warps take part
+        const int parties = lane >= 12 && lane < 16 ? (kStateOnly ? kCutWarps : 1) : lane == 16 || lane == 17 ? kCutWarps :
+                            lane == 20 || lane == 21 || lane == 24 || lane == 26 || lane == 28 ? 8 : lane == 30 ? 4 : 1;
+        mbar_init(&bars[lane], parties);
+        fence_mbar_init();
+        if (lane == 0) fail_sh = 0;
+    }
     if (warp == 1) tmem_alloc(&tmem_base_sh, 512);
     const float la = pr.log_a[h];
     if (tid >= 64 && tid < 64 + 129) pw[tid - 64] = gpow(la, tid - 64);
@@ -160,7 +146,8 @@ __global__ void __launch_bounds__(kScanThreads, 1) linear_scan_kernel(const __gr
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = tmem_base_sh;
-    // own states of the sequence's pieces, [64 columns][128 rows] each
+    // own states of the sequence's pieces, [64 columns][prow rows] each, at every 64 x 128
+    const int prow = 64 * np;
     float* seg0 = pr.seg + (static_cast<int64_t>(sc.seg_base) +
                             static_cast<int64_t>(bh) * pr.npiece * sc.tiles + tile) * (kDepth * kTile);
     const int64_t seg_step = static_cast<int64_t>(sc.tiles) * (kDepth * kTile);
@@ -168,23 +155,32 @@ __global__ void __launch_bounds__(kScanThreads, 1) linear_scan_kernel(const __gr
         // the pieces before this segment, decayed to its start and summed in order, while the first copies and scores run
         grid_dep_wait();
         constexpr int kSumThreads = 512;
-        const int t = tid - 128;
-        float4 sum[4] = {};
-        const int np_before = p0 / pr.piece_chunks;
-        for (int gg = 0; gg < np_before; gg++) {
-            const float f = gpow(la, before(p0) - before((gg + 1) * pr.piece_chunks));
-            const float4* sg = reinterpret_cast<const float4*>(seg0 + gg * seg_step);
+        const float gp = gpow(la, pr.piece_chunks * kTile);
+        const int count = p0 / pr.piece_chunks;
+        // round trips are what this takes, so four pieces' loads are in flight (2 x 4 heads, T = 2048: 18.4 -> 15.9 us;
+        // eight take 0.3 off that and cost the roles registers: 97 -> 99.7 us at 4 x 16 heads, T = 8192)
+        constexpr int kAhead = 4;
+#pragma unroll 1
+        for (int at = tid - 128; at < 16 * prow; at += kSumThreads) {
+            const float4* src = reinterpret_cast<const float4*>(seg0) + at;
+            float4 sum = {};
+#pragma unroll 1
+            for (int left = count; left > 0; left -= kAhead, src += kAhead * (seg_step / 4)) {
+                float4 y[kAhead];
 #pragma unroll
-            for (int i = 0; i < 4; i++) {
-                const float4 y = sg[t + i * kSumThreads];
-                sum[i].x += f * y.x;
-                sum[i].y += f * y.y;
-                sum[i].z += f * y.z;
-                sum[i].w += f * y.w;
+                for (int u = 0; u < kAhead; u++)
+                    if (u < left) y[u] = src[u * (seg_step / 4)];
+#pragma unroll
+                for (int u = 0; u < kAhead; u++)
+                    if (u < left) {
+                        sum.x = gp * sum.x + y[u].x;
+                        sum.y = gp * sum.y + y[u].y;
+                        sum.z = gp * sum.z + y[u].z;
+                        sum.w = gp * sum.w + y[u].w;
+                    }
             }
+            reinterpret_cast<float4*>(wc)[at] = sum;
         }
-#pragma unroll
-        for (int i = 0; i < 4; i++) reinterpret_cast<float4*>(wc)[t + i * kSumThreads] = sum[i];
         asm volatile("bar.sync 1, %0;" ::"n"(kSumThreads) : "memory");
     }
     // A CTA's last chunk adds to no state that is read, unless the state leaves here; a ragged one has its rows set to
@@ -384,9 +380,9 @@ __global__ void __launch_bounds__(kScanThreads, 1) linear_scan_kernel(const __gr
                     }
             }
             if (g > 0) {
-                const float* sum = reinterpret_cast<const float*>(wc) + d;
+                const float* sum = reinterpret_cast<const float*>(wc) + (d < prow ? d : 0);  // rows past d1 are not used
 #pragma unroll
-                for (int c = 0; c < 32; c++) x[c] += sum[(cw + c) * kTile];
+                for (int c = 0; c < 32; c++) x[c] += sum[(cw + c) * prow];
             }
 #pragma unroll
             for (int c = 0; c < 16; c++) x2[c] = pair2(x[2 * c], x[2 * c + 1]);
@@ -462,11 +458,13 @@ __global__ void __launch_bounds__(kScanThreads, 1) linear_scan_kernel(const __gr
         if (ok) {
             if (kMode == kPieces) {
                 float* sg = seg0 + static_cast<int64_t>(g) * seg_step + d;
+                if (d < prow) {
 #pragma unroll
-                for (int c = 0; c < 16; c++) {
-                    const float2 y = split2(x2[c]);
-                    sg[(cw + 2 * c) * kTile] = y.x;
-                    sg[(cw + 2 * c + 1) * kTile] = y.y;
+                    for (int c = 0; c < 16; c++) {
+                        const float2 y = split2(x2[c]);
+                        sg[(cw + 2 * c) * prow] = y.x;
+                        sg[(cw + 2 * c + 1) * prow] = y.y;
+                    }
                 }
             } else if (sc.leave && g == have - 1 && d < d1) {
                 float* o = sc.leave + (static_cast<int64_t>(bh) * d1 + d) * d2 + cg;
