@@ -10,8 +10,10 @@
 // tokens. Bucket l >= 1 of position pos (bit l - 1 of pos set) is [(pos >> l) << l, + 2^(l-1)):
 // it holds own tokens when its end is past P.
 //
-// Bound by the own states' bytes: 64 x 16 heads of 128 x 64, P = 30011, up to 4096 own tokens: 91 us for 492 MB, 80% of
+// Bound by the own states' bytes: 64 x 16 heads of 128 x 64, P = 30011, up to 4096 own tokens: 86 us for 492 MB, 85% of
 // the copy rate, half of it writes. The prefix's kernel (22 us by itself) runs beside the own states' streams.
+#include <type_traits>
+
 #include "lla_linear.cuh"
 
 namespace lla {
@@ -93,8 +95,11 @@ __global__ void __launch_bounds__(kThreads) shared_prefix(const T* __restrict__ 
 
 // One CTA per (b, h): the own buckets (carry, decay, read) and the prefix's parts. Level by level, four
 // 16-byte loads of a thread in flight; each held state is read once and written once, past L2's retention.
-template <typename T, int DV4>
-__global__ void __launch_bounds__(kThreads) shared_own(const T* __restrict__ q, const T* __restrict__ k,
+// kOwnThreads: 256 where they hold all dk rows in one pass of four rows a thread, else 512 (64 x 16 heads of 128 x 64:
+// 86 us against 89; 4 x 4 heads of 64 x 64: 6.9 against 6.5). The next level's loads issued ahead cost more registers
+// than they give (101 us), two or eight rows a thread as much or more.
+template <typename T, int DV4, int kOwnThreads>
+__global__ void __launch_bounds__(kOwnThreads) shared_own(const T* __restrict__ q, const T* __restrict__ k,
                                                        const T* __restrict__ v, const float* __restrict__ log_a,
                                                        const float* __restrict__ lambda,
                                                        const float* __restrict__ part, float* __restrict__ decay,
@@ -102,10 +107,11 @@ __global__ void __launch_bounds__(kThreads) shared_own(const T* __restrict__ q, 
                                                        T* __restrict__ out, int64_t P, int B, int H, int dk, int Lmax,
                                                        int* err) {
     constexpr int DV = DV4 * 4;
-    constexpr int kRows = kThreads / DV4;
+    constexpr int kRows = kOwnThreads / DV4;
     constexpr int U = 4;  // rows of a thread in flight
     __shared__ float qs[kMaxDk], ks[kMaxDk], lam[40];
-    __shared__ float red[kThreads / 32][DV];
+    constexpr int kGroups = kOwnThreads / DV;  // thread groups over the prefix's parts
+    __shared__ float red[kOwnThreads / 32][DV], red_far[kGroups][DV], far_w[40];
     const int tid = threadIdx.x;
     const int64_t bh = blockIdx.x;
     const int b = static_cast<int>(bh / H);
@@ -115,11 +121,11 @@ __global__ void __launch_bounds__(kThreads) shared_own(const T* __restrict__ q, 
         grid_dep_wait();  // with every sequence skipped too, this kernel ends after the one that writes the workspace
         return;
     }
-    for (int x = tid; x < dk; x += kThreads) {
+    for (int x = tid; x < dk; x += kOwnThreads) {
         qs[x] = load_f(q + bh * dk + x);
         ks[x] = load_f(k + bh * dk + x);
     }
-    for (int x = tid; x < Lmax; x += kThreads) lam[x] = lambda[bh * Lmax + x];
+    for (int x = tid; x < Lmax; x += kOwnThreads) lam[x] = lambda[bh * Lmax + x];
     const float la = log_a[bh];
     const float D = (t > P ? decay[bh] : 0.f) + la;
     __syncthreads();
@@ -194,21 +200,28 @@ __global__ void __launch_bounds__(kThreads) shared_own(const T* __restrict__ q, 
         red[warp][lane * 4 + 2] = o.z;
         red[warp][lane * 4 + 3] = o.w;
     }
+    // the prefix block of slot l of the walk of P - 1 starts at ((P - 1) >> l) << l: its weight, at its place among the parts
+    const int parts = 1 + __popcll(static_cast<unsigned long long>(P - 1));
+    if (tid < 40 && (tid == 0 || ((P - 1) >> (tid - 1) & 1))) {
+        const int64_t below = tid == 0 ? 0 : (int64_t(1) << (tid - 1)) - 1;
+        const int j = tid == 0 ? 0 : 1 + __popcll(static_cast<unsigned long long>((P - 1) & below));
+        far_w[j] = lam[64 - __clzll(static_cast<long long>(t ^ (((P - 1) >> tid) << tid)))];
+    }
     grid_dep_wait();  // the prefix's parts (this kernel starts beside the one that forms them)
+    __syncthreads();
+    const int col = tid % DV, part0 = tid / DV;
+    float far = 0.f;
+#pragma unroll 4
+    for (int j = part0; j < parts; j += kGroups) far += far_w[j] * part[(static_cast<int64_t>(j) * B * H + bh) * DV + col];
+    red_far[part0][col] = far;
     __syncthreads();
     if (tid < DV) {
         float s = 0.f;
+        far = 0.f;
 #pragma unroll
-        for (int w = 0; w < kThreads / 32; w++) s += red[w][tid];
-        // prefix blocks: slot l of the walk of P - 1 starts at ((P - 1) >> l) << l
-        float far = 0.f;
-        int j = 0;
-        for (int l = 0; (int64_t(1) << l) <= 2 * (P - 1) || l == 0; l++) {
-            if (l > 0 && (((P - 1) >> (l - 1)) & 1) == 0) continue;
-            const int lev = 64 - __clzll(static_cast<long long>(t ^ (((P - 1) >> l) << l)));
-            far += lam[lev] * part[(static_cast<int64_t>(j) * B * H + bh) * DV + tid];
-            j++;
-        }
+        for (int w = 0; w < kOwnThreads / 32; w++) s += red[w][tid];
+#pragma unroll
+        for (int u = 0; u < kGroups; u++) far += red_far[u][tid];
         store_f(out + bh * DV + tid, s + expf(D) * far);
     }
 }
@@ -225,13 +238,13 @@ cudaError_t shared_t(const void* q, const void* k, const void* v, const float* l
                      float* part, int B, int H, int dk, int dv, int Lmax, int* err, cudaStream_t stream) {
     const T* qp = static_cast<const T*>(q);
     cudaError_t e = cudaSuccess;
-    auto go = [&](auto pre, auto own) {
+    auto go = [&](auto pre, auto own, int own_threads) {
         pre<<<dim3(held_slots(P), H, (B + kBatchTile - 1) / kBatchTile), kThreads, 0, stream>>>(qp, prefix, part, P, B, H,
                                                                                               dk, Lp);
         note_launch(stream, "shared_prefix");
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3(static_cast<unsigned>(B) * H);
-        cfg.blockDim = dim3(kThreads);
+        cfg.blockDim = dim3(own_threads);
         cfg.stream = stream;
         cudaLaunchAttribute attr[1];
         attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -243,11 +256,16 @@ cudaError_t shared_t(const void* q, const void* k, const void* v, const float* l
                                Lmax, err);
         note_launch(stream, "shared_own");
     };
+    auto pick = [&](auto dv4) {
+        constexpr int DV4 = decltype(dv4)::value;
+        if (dk <= 4 * (256 / DV4)) go(shared_prefix<T, DV4>, shared_own<T, DV4, 256>, 256);
+        else go(shared_prefix<T, DV4>, shared_own<T, DV4, 512>, 512);
+    };
     switch (dv) {
-        case 16: go(shared_prefix<T, 4>, shared_own<T, 4>); break;
-        case 32: go(shared_prefix<T, 8>, shared_own<T, 8>); break;
-        case 64: go(shared_prefix<T, 16>, shared_own<T, 16>); break;
-        default: go(shared_prefix<T, 32>, shared_own<T, 32>); break;
+        case 16: pick(std::integral_constant<int, 4>()); break;
+        case 32: pick(std::integral_constant<int, 8>()); break;
+        case 64: pick(std::integral_constant<int, 16>()); break;
+        default: pick(std::integral_constant<int, 32>()); break;
     }
     return e != cudaSuccess ? e : cudaGetLastError();
 }
