@@ -25,6 +25,7 @@
 // negative, so no factor overflows for g <= 1; g^0 is 1 also for g = 0 (log_a = -inf).
 #include "lla_internal.cuh"
 #include "lla_linear.cuh"
+#include "lla_tc_ptx.cuh"
 
 namespace lla {
 namespace {
@@ -35,6 +36,7 @@ constexpr int kMulThreads = 128;  // 8 x 16 threads, each an 8 x 4 piece of a 64
 constexpr int kSlab = 32;         // summed indices staged at a time
 constexpr int kLd = kC + 4;    // leading dimension of the transposed tiles (16-byte rows)
 constexpr int kMaxD = 128;
+constexpr int kFull = 4 * 152;  // blocks of lin_out that fill the GPU once
 
 
 // One 64-token chunk: its sequence's batch index, its rows and the place of its state.
@@ -171,6 +173,7 @@ template <typename T>
 __global__ void __launch_bounds__(kMulThreads, 4) lin_chunk_state(LinStateJobs jobs, LinSeqs sq, const float* log_a) {
     __shared__ __align__(16) float X[kSlab][kLd], Y[kSlab][kLd];
     __shared__ float w[kC];
+    grid_dep_launch();
     const int h = blockIdx.y, tid = threadIdx.x;
     int piece = blockIdx.z, j = 0;
     while (piece >= jobs.job[j].pieces) piece -= jobs.job[j++].pieces;
@@ -223,6 +226,8 @@ __global__ void __launch_bounds__(kMulThreads, 4) lin_chunk_state(LinStateJobs j
 // Entering state of every chunk in place of its own, and the leaving state of every sequence.
 // grid (elements / kThreads, sequences x H, jobs). One thread per state element.
 __global__ void __launch_bounds__(kThreads) lin_carry(LinStateJobs jobs, LinSeqs sq, const float* log_a) {
+    grid_dep_launch();
+    grid_dep_wait();  // the own states
     const LinStateJob& jb = jobs.job[blockIdx.z];
     const int e = blockIdx.x * kThreads + threadIdx.x;
     const int msz = jb.d1 * jb.d2;
@@ -271,7 +276,10 @@ __global__ void __launch_bounds__(kMulThreads, 4) lin_out(LinScans scans, LinSeq
     const LinScan& sc = scans.scan[blockIdx.z];
     const int d1 = sc.d1, d2 = sc.d2;
     ChunkAt at;
-    if (!chunk_at(sq, blockIdx.x, h, &at)) return;
+    if (!chunk_at(sq, blockIdx.x, h, &at)) {
+        grid_dep_wait();  // with no chunk at all too, this kernel ends after the one that writes the workspace
+        return;
+    }
     const int n = at.n;
     if (tid <= kC) pw[tid] = gpow(log_a[h], tid);
     const bool v1 = d1 % 4 == 0, v2 = d2 % 4 == 0;
@@ -313,6 +321,7 @@ __global__ void __launch_bounds__(kMulThreads, 4) lin_out(LinScans scans, LinSeq
         if (scores || (!near && sc.state_t)) put_t(y, Y);
         else put(y, Y);
         __syncthreads();
+        if (st + 1 == nd) grid_dep_wait();  // the entering states; the scores are formed beside the kernels before
         if (st + 1 < steps) get(st + 1);
         mul84<kSlab>(o, near ? &Pt[(u - nd) * kSlab][0] : &X[0][0], &Y[0][0]);
         if (scores && u == nd - 1) {
@@ -375,10 +384,21 @@ cudaError_t run_t(const LinStateJobs& jobs, const LinScans& scans, const LinSeqs
     }
     lin_chunk_state<T><<<dim3(sq.n_chunks, sq.H, pieces), kMulThreads, 0, stream>>>(jobs, sq, log_a);
     note_launch(stream, "lin_chunk_state");
-    lin_carry<<<dim3((msz + kThreads - 1) / kThreads, batch * sq.H, jobs.count), kThreads, 0, stream>>>(jobs, sq,
-                                                                                                       log_a);
+    // Each beside the end of the one before, where lin_out's blocks fill the GPU (four to an SM): fewer would be placed four
+    // to an SM on the SMs that the others leave free (240 blocks: 56 us for the three kernels against 39; 2048: 422
+    // against 428).
+    const dim3 blocks(sq.n_chunks, sq.H, scans.count);
+    const bool beside = static_cast<int64_t>(blocks.x) * blocks.y * blocks.z >= kFull;
+    auto launch = [&](auto kern, dim3 grid, int threads, const auto& what) {
+        if (beside) return launch_pdl(kern, grid, dim3(threads), 0, stream, what, sq, log_a);
+        kern<<<grid, threads, 0, stream>>>(what, sq, log_a);
+        return cudaGetLastError();
+    };
+    cudaError_t e = launch(lin_carry, dim3((msz + kThreads - 1) / kThreads, batch * sq.H, jobs.count), kThreads, jobs);
+    if (e != cudaSuccess) return e;
     note_launch(stream, "lin_carry");
-    lin_out<T><<<dim3(sq.n_chunks, sq.H, scans.count), kMulThreads, 0, stream>>>(scans, sq, log_a);
+    e = launch(lin_out<T>, blocks, kMulThreads, scans);
+    if (e != cudaSuccess) return e;
     note_launch(stream, "lin_out");
     return cudaGetLastError();
 }
@@ -397,7 +417,7 @@ __global__ void __launch_bounds__(1024) lin_table(const int32_t* __restrict__ cu
     __shared__ int wsum[32], wmax[32];
     __shared__ __align__(16) int lens[kMostSorted];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the tensor-core scan sets up beside this kernel
+    grid_dep_launch();  // the tensor-core scan sets up beside this kernel
     if (tid < kMostSorted) lens[tid] = -2;  // shorter than any sequence
     int carry = 0, high = 0;
     for (int b0 = 0; b0 < n; b0 += 1024) {

@@ -15,6 +15,7 @@
 #include <type_traits>
 
 #include "lla_linear.cuh"
+#include "lla_tc_ptx.cuh"
 
 namespace lla {
 namespace {
@@ -29,11 +30,6 @@ __device__ __forceinline__ bool own_held(int64_t pos, int64_t P, int l) {
     if (((pos >> (l - 1)) & 1) == 0) return false;
     return ((pos >> l) << l) + (int64_t(1) << (l - 1)) > P;
 }
-
-// Programmatic dependent launch: grid_dep_launch() lets the next kernel of the stream start, grid_dep_wait()
-// blocks until the one before has completed and its writes are visible.
-__device__ __forceinline__ void grid_dep_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-__device__ __forceinline__ void grid_dep_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
 __device__ __forceinline__ void fma4(float4& o, float w, const float4& x) {
     o.x += w * x.x;
@@ -242,18 +238,9 @@ cudaError_t shared_t(const void* q, const void* k, const void* v, const float* l
         pre<<<dim3(held_slots(P), H, (B + kBatchTile - 1) / kBatchTile), kThreads, 0, stream>>>(qp, prefix, part, P, B, H,
                                                                                               dk, Lp);
         note_launch(stream, "shared_prefix");
-        cudaLaunchConfig_t cfg = {};
-        cfg.gridDim = dim3(static_cast<unsigned>(B) * H);
-        cfg.blockDim = dim3(own_threads);
-        cfg.stream = stream;
-        cudaLaunchAttribute attr[1];
-        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-        attr[0].val.programmaticStreamSerializationAllowed = 1;
-        cfg.attrs = attr;
-        cfg.numAttrs = 1;
-        e = cudaLaunchKernelEx(&cfg, own, qp, static_cast<const T*>(k), static_cast<const T*>(v), log_a, lambda,
-                               static_cast<const float*>(part), decay, states, t, static_cast<T*>(out), P, B, H, dk,
-                               Lmax, err);
+        e = launch_pdl(own, dim3(static_cast<unsigned>(B) * H), dim3(own_threads), 0, stream, qp,
+                       static_cast<const T*>(k), static_cast<const T*>(v), log_a, lambda, static_cast<const float*>(part),
+                       decay, states, t, static_cast<T*>(out), P, B, H, dk, Lmax, err);
         note_launch(stream, "shared_own");
     };
     auto pick = [&](auto dv4) {
