@@ -54,7 +54,7 @@ struct ScanParams {
     float* seg;             // pieces' own states
     __nv_bfloat16* states;  // kStates: the entering states
     LinSeqs sq;
-    int count, nseg, seg_chunks, npiece, piece_chunks, packed, batch;
+    int count, nseg, seg_chunks, npiece, piece_chunks, seg_pieces, packed;
 };
 
 // Warps: 0 and 2 TMA producers, 1 TMEM owner and MMA issuer, 4..11 P (every other block of 32 keys), 12..19 state
@@ -81,18 +81,15 @@ __global__ void __launch_bounds__(kScanThreads, 1) linear_scan_kernel(const __gr
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     if (pr.packed) grid_dep_wait();  // the sequence table; pieces' states are waited for below
     grid_dep_launch();
-    // ---- which scan, 64 columns, segment, sequence and head
-    int blk = blockIdx.x, si = 0;
+    // ---- which scan, segment and 64 columns (one or two of them), sequence and head. Divisions are kept out: a CTA's
+    // start is a quarter of a short prompt
     const int ncta = kMode == kPieces ? pr.npiece : pr.nseg;  // of one sequence, head and 64 columns
-    while (si + 1 < pr.count && blk >= pr.batch * pr.sq.H * ncta * pr.scan[si].tiles)
-        blk -= pr.batch * pr.sq.H * ncta * pr.scan[si++].tiles;
+    int x = blockIdx.x, si = 0;
+    if (pr.count > 1 && x >= ncta * pr.scan[0].tiles) x -= ncta * pr.scan[si++].tiles;
     const LinTcScan& sc = pr.scan[si];
-    const int tile = blk % sc.tiles;
-    blk /= sc.tiles;
-    const int g = blk % ncta;
-    blk /= ncta;
-    const int h = blk % pr.sq.H;
-    int b = blk / pr.sq.H, len = pr.sq.T, row0 = 0;
+    const int tile = x & (sc.tiles - 1), g = x >> (sc.tiles - 1);
+    int b = blockIdx.y / pr.sq.H, len = pr.sq.T, row0 = 0;
+    const int h = blockIdx.y - b * pr.sq.H;
     if (pr.packed) {
         b = pr.sq.order[b];
         row0 = pr.sq.tab[b].x;
@@ -102,7 +99,7 @@ __global__ void __launch_bounds__(kScanThreads, 1) linear_scan_kernel(const __gr
     const int bh = b * pr.sq.H + h;
     const int z = pr.packed ? h : bh;  // outermost coordinate of the tensor maps
     const int nch = static_cast<int>((static_cast<unsigned>(len) + kTile - 1) / kTile);  // len may be 2^31 - 1
-    const int have = nch <= pr.seg_chunks ? 1 : (nch + pr.seg_chunks - 1) / pr.seg_chunks;
+    const int have = nch <= pr.seg_chunks ? 1 : pr.packed ? (nch + pr.seg_chunks - 1) / pr.seg_chunks : pr.nseg;
     const int span = kMode == kPieces ? pr.piece_chunks : pr.seg_chunks;
     const int p0 = g * span;
     if (kMode == kPieces ? p0 >= (have - 1) * pr.seg_chunks : g >= have) return;
@@ -156,7 +153,7 @@ __global__ void __launch_bounds__(kScanThreads, 1) linear_scan_kernel(const __gr
         grid_dep_wait();
         constexpr int kSumThreads = 512;
         const float gp = gpow(la, pr.piece_chunks * kTile);
-        const int count = p0 / pr.piece_chunks;
+        const int count = g * pr.seg_pieces;
         // round trips are what this takes, so four pieces' loads are in flight (2 x 4 heads, T = 2048: 18.4 -> 15.9 us;
         // eight take 0.3 off that and cost the roles registers: 97 -> 99.7 us at 4 x 16 heads, T = 8192)
         constexpr int kAhead = 4;
@@ -697,8 +694,8 @@ cudaError_t linear_tc_run(const LinTcPlan& pl, const LinTcMap* maps, int n_maps,
     pr.seg_chunks = pl.seg_chunks;
     pr.npiece = pl.npiece;
     pr.piece_chunks = pl.piece_chunks;
+    pr.seg_pieces = pl.seg_chunks / pl.piece_chunks;
     pr.packed = packed;
-    pr.batch = pl.batch;
     int base = 0, tiles = 0, d1 = 0;
     for (int i = 0; i < count; i++) {
         pr.scan[i] = scans[i];
@@ -707,21 +704,21 @@ cudaError_t linear_tc_run(const LinTcPlan& pl, const LinTcMap* maps, int n_maps,
         tiles += scans[i].tiles;
         if (scans[i].d1 > d1) d1 = scans[i].d1;
     }
-    const unsigned per_seg = static_cast<unsigned>(pl.batch) * sq.H * tiles;
     // beside the end of the kernel before it, where that is the table's or the pieces'
-    auto launch = [&](auto kern, unsigned ctas, int smem, bool beside) {
-        if (beside) return launch_pdl(kern, dim3(ctas), dim3(kScanThreads), smem, stream, pr, err);
-        kern<<<ctas, kScanThreads, smem, stream>>>(pr, err);
+    auto launch = [&](auto kern, int ncta, int smem, bool beside) {
+        const dim3 grid(tiles * ncta, pl.batch * sq.H);
+        if (beside) return launch_pdl(kern, grid, dim3(kScanThreads), smem, stream, pr, err);
+        kern<<<grid, kScanThreads, smem, stream>>>(pr, err);
         return cudaSuccess;
     };
     if (pl.nseg > 1) {
-        const cudaError_t e = launch(linear_scan_kernel<kPieces>, per_seg * pl.npiece, smem_bytes(kPieces, d1), packed);
+        const cudaError_t e = launch(linear_scan_kernel<kPieces>, pl.npiece, smem_bytes(kPieces, d1), packed);
         if (e != cudaSuccess) return e;
         note_launch(stream, "linear_scan_pieces");
     }
     const auto kern = states ? linear_scan_kernel<kStates> : linear_scan_kernel<kFull>;
     const int smem = smem_bytes(states ? kStates : kFull, d1);
-    const cudaError_t e = launch(kern, per_seg * pl.nseg, smem, packed || pl.nseg > 1);
+    const cudaError_t e = launch(kern, pl.nseg, smem, packed || pl.nseg > 1);
     if (e != cudaSuccess) return e;
     note_launch(stream, states ? "linear_scan_states" : "linear_scan");
     return cudaGetLastError();
