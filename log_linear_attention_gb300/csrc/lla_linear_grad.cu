@@ -10,15 +10,18 @@
 //     scores  A B^T  [128 x 128] -> P = scores o g^|i-j| (two bf16 parts, in TMEM in place of the scores)
 //     far     A X    [128 x 64]     X as it lies (dv), or the same rows read as its transpose (dq, dk)
 //     near    P C    [128 x 64]     out_i = near_i + f_i far_i
-// With the states given, chunks do not wait for one another: items are dealt out evenly to one CTA per SM
-// whatever the number of heads, where one scan per gradient took whole waves of CTAs (320 equal scans on 152
-// SMs at 4 x 16 heads, T = 8192, 128 x 64: three waves for 2.1 waves of work, 367 us for the backward against 270).
-// Consecutive items share their chunk's rows in L2. Two items are in flight: both kinds of accumulator are double.
+// With the states given, chunks do not wait for one another: items are dealt out evenly to one CTA per SM whatever the
+// number of heads, where one scan per gradient took whole waves of CTAs (320 equal scans on 152 SMs at 4 x 16 heads,
+// T = 8192, 128 x 64: three waves for 2.1 waves of work). A CTA holds a chunk's rows of all four tensors, copied once
+// for its items (two chunks where they fit), and S and R; the items of one gradient share scores and P. Two items are in
+// flight: both kinds of accumulator are double.
 //
-// Measured there: 184 us for 20480 items, 848 MB at 4.6 TB/s (68% of the copy rate), tensor pipe 38% and issue slots 54%
-// busy; an item is 1.3 us. What bounds it is the chain scores -> P -> near -> out of two items in flight, with the
-// issue slots that P and out take; the two state scans before it take 89 us (514 MB at 5.8 TB/s).
+// Measured there: the whole backward 233 us, 143 of it this kernel. With every item's operands copied for itself, its own
+// scores and the places of its operands looked up by the issuing thread it took 180 (gradients as scans: 278); the
+// rows shared, but looked up: 174. The instructions of the thread that issues the MMAs are the chain that is left, and
+// the rows in and out take 110 us of HBM; the state scans before it take 89 us (514 MB at 5.8 TB/s).
 #include <atomic>
+#include <type_traits>
 
 #include "lla_linear_tc.cuh"
 
@@ -26,32 +29,35 @@ namespace lla {
 namespace {
 
 constexpr int kGradThreads = 640;
-constexpr int kMaxStages = 3;
 constexpr int kXPanel = 64 * 128;  // 64 rows of 64 bf16
-constexpr int kSmemMost = 232448 - 6144;
+constexpr int kSmemMost = 232448 - 2048;  // 227 KB less the static part
 // TMEM columns: two buffers of scores, two of [near | far]
 constexpr uint32_t kColS = 0, kColO = 256;
 
 struct GradKind {
-    int ia, ib, ic;  // tensor maps: 0 q, 1 k, 2 v, 3 dout
+    int ia, ib, ic;  // row tensors: 0 q, 1 k, 2 v, 3 dout
     int d1, tiles, reverse;
-    int state_t;      // X is read as the transpose of the stored rows
-    int states_base;  // first (b, h, chunk) of its state in the buffer
+    int state_t;  // X is read as the transpose of the stored rows
+    int cols;     // of the output
 };
 
 struct GradParams {
-    CUtensorMap map[4], omap[3];
+    CUtensorMap map[4];
     GradKind kind[3];
+    __nv_bfloat16* out[3];
     const float* log_a;
     const __nv_bfloat16* states;  // tiles of 128 rows of 64, each row's 16-byte pieces swizzled as shared memory wants them
-    int BH, H, T, nch, v_tiles, per_chunk;  // per_chunk: items of one chunk
+    int rows_at[4], panels[4];    // a stage's rows of each tensor: first byte, panels of 64 columns
+    int stage_bytes, nst;
+    int BH, H, T, nch, v_tiles, k_panels, per_chunk;  // per_chunk: items of one chunk
+    bool wide;  // 32-byte stores
 };
 
-// An item and its successor; every role walks its CTA's items with one of these.
+// An item and its successors; every role walks its CTA's items with one of these. The items of one gradient and chunk
+// (its columns' tiles) are a group: they share scores and P.
 struct Item {
     int bh, h, ch, k, tile;
-    __device__ __forceinline__ void next(const GradParams& pr) {
-        if (++tile < pr.kind[k].tiles) return;
+    __device__ __forceinline__ void next_group(const GradParams& pr) {
         tile = 0;
         if (++k < 3) return;
         k = 0;
@@ -59,6 +65,9 @@ struct Item {
         ch = 0;
         bh++;
         if (++h == pr.H) h = 0;
+    }
+    __device__ __forceinline__ void next(const GradParams& pr) {
+        if (++tile == pr.kind[k].tiles) next_group(pr);
     }
 };
 
@@ -75,47 +84,39 @@ __device__ __forceinline__ Item item_at(const GradParams& pr, int64_t i) {
     return it;
 }
 
-// Warps: 0 copies a and X, 2 b, 3 c; 1 issues the MMAs; 4..11 P (every other block of 32 keys), 12..19 write out
+// Warps: 0 copies a chunk's rows, 2 S and 3 R; 1 issues the MMAs; 4..11 P (every other block of 32 keys), 12..19 write out
 // (32 columns each). Warp w reaches TMEM lanes 32 (w % 4)..+31.
-__global__ void __launch_bounds__(kGradThreads, 1) linear_grad_kernel(const __grid_constant__ GradParams pr, int nst,
-                                                                      int np_most, int* err) {
+__global__ void __launch_bounds__(kGradThreads, 1) linear_grad_kernel(const __grid_constant__ GradParams pr, int* err) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    __shared__ uint64_t ax_full[kMaxStages], b_full[kMaxStages], c_full[kMaxStages];
-    __shared__ uint64_t ax_free[kMaxStages], b_free[kMaxStages], c_free[kMaxStages];
-    __shared__ uint64_t s_full[2], p_ready[2], o_full[2], o_read[2], out_put, out_free, drain;
+    __shared__ uint64_t rows_full[2], rows_free[2];  // of a stage
+    __shared__ uint64_t x_full[2], x_free[2];        // of S, of R
+    __shared__ uint64_t s_full[2], p_ready[2], o_full[2], o_read[2], drain;
     __shared__ uint32_t tmem_base_sh;
     __shared__ int fail_sh;
-    // per P warp: weight of key c for row r of a diagonal 32-key block at 31 + r - c, and of key c of another block
-    __shared__ __align__(16) float weights[8][96];
+    // forwards and backwards: weight of key c for row r of a diagonal 32-key block at 31 + r - c, and of key c of another
+    // block. Each P warp writes what it reads, all the same, and none is a head's two groups of one direction ahead.
+    __shared__ __align__(16) float weights[2][96];
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int64_t total = static_cast<int64_t>(pr.BH) * pr.nch * pr.per_chunk;
     const int64_t first = total * blockIdx.x / gridDim.x;
     const int m = static_cast<int>(total * (blockIdx.x + 1) / gridDim.x - first);  // items of this CTA
-    // a stage: a | b | c | X
-    const int b_off = np_most * kPanelBytes, c_off = 2 * b_off, x_off = c_off + kPanelBytes;
-    const int stage_bytes = x_off + np_most * kXPanel;
-    uint8_t* stage_out = smem + nst * stage_bytes;  // an item's output rows on their way to memory
+    const int nst = pr.nst, x_bytes = pr.v_tiles * pr.k_panels * kXPanel;
+    uint8_t* xs = smem + nst * pr.stage_bytes;  // the entering states S and R of a chunk, all their tiles
     volatile int* fail = &fail_sh;
 
     if (tid == 0) {
-        for (int s = 0; s < nst; s++) {
-            mbar_init(&ax_full[s], 1);
-            mbar_init(&b_full[s], 1);
-            mbar_init(&c_full[s], 1);
-            mbar_init(&ax_free[s], 1);
-            mbar_init(&b_free[s], 1);
-            mbar_init(&c_free[s], 1);
-        }
         for (int i = 0; i < 2; i++) {
+            mbar_init(&rows_full[i], 1);
+            mbar_init(&rows_free[i], 1);
+            mbar_init(&x_full[i], 1);
+            mbar_init(&x_free[i], 1);
             mbar_init(&s_full[i], 1);
             mbar_init(&p_ready[i], 8);
             mbar_init(&o_full[i], 1);
             mbar_init(&o_read[i], 8);
         }
-        mbar_init(&out_put, 8);
-        mbar_init(&out_free, 1);
         mbar_init(&drain, 1);
         fence_mbar_init();
         fail_sh = 0;
@@ -131,121 +132,167 @@ __global__ void __launch_bounds__(kGradThreads, 1) linear_grad_kernel(const __gr
     };
 
     if (warp == 0 || warp == 2 || warp == 3) {
-        // each operand is free at another time, so each is waited for by a warp of its own
         if (m > 0 && elect_one()) {
-            uint64_t* full = warp == 0 ? ax_full : warp == 2 ? b_full : c_full;
-            uint64_t* free_ = warp == 0 ? ax_free : warp == 2 ? b_free : c_free;
-            Item it = item_at(pr, first);
-            int s = 0, sent = 0;
-            uint32_t ph = 1;
-            for (int j = 0; j < m; j++) {
-                if (j >= nst && !wait_one(&free_[s], ph, fail)) {
-                    fail_now();
-                    break;
-                }
-                const GradKind& kd = pr.kind[it.k];
-                const int np = kd.d1 > 64 ? 2 : 1, t0 = it.ch * kTile;
-                uint8_t* st = smem + s * stage_bytes;
-                if (warp == 0) {
-                    mbar_expect_tx(&full[s], np * (kPanelBytes + kXPanel));
-                    const int64_t x0 = static_cast<int64_t>(kd.states_base + it.bh * pr.nch + it.ch) * pr.v_tiles;
-                    for (int p = 0; p < np; p++) {
-                        tma_load_3d(st + p * kPanelBytes, &pr.map[kd.ia], &full[s], 64 * p, t0, it.bh);
-                        // 64 state rows of one 64-column tile: rows of X, or of 64 columns of d1 of its transpose
-                        bulk_load(st + x_off + p * kXPanel,
-                                  pr.states + ((x0 + (kd.state_t ? p : it.tile)) * 2 + (kd.state_t ? it.tile : p)) *
-                                                  (kXPanel / 2),
-                                  kXPanel, &full[s]);
+            const int64_t c0 = first / pr.per_chunk, c1 = (first + m - 1) / pr.per_chunk;
+            if (warp == 0) {
+                int s = 0, sent = 0;
+                uint32_t ph = 1;
+                for (int64_t c = c0; c <= c1; c++) {
+                    if (sent >= nst && !wait_one(&rows_free[s], ph, fail)) {
+                        fail_now();
+                        break;
                     }
-                } else if (warp == 2) {
-                    mbar_expect_tx(&full[s], np * kPanelBytes);
-                    for (int p = 0; p < np; p++)
-                        tma_load_3d(st + b_off + p * kPanelBytes, &pr.map[kd.ib], &full[s], 64 * p, t0, it.bh);
-                } else {
-                    mbar_expect_tx(&full[s], kPanelBytes);
-                    tma_load_3d(st + c_off, &pr.map[kd.ic], &full[s], it.tile * kDepth, t0, it.bh);
+                    const int bh = static_cast<int>(c / pr.nch), t0 = static_cast<int>(c - static_cast<int64_t>(bh) * pr.nch) * kTile;
+                    mbar_expect_tx(&rows_full[s], pr.stage_bytes);
+                    // in the order of their use
+                    for (int u = 0; u < 4; u++) {
+                        const int i = u == 0 ? 3 : u == 1 ? 2 : u == 2 ? 1 : 0;
+                        for (int p = 0; p < pr.panels[i]; p++)
+                            tma_load_3d(smem + s * pr.stage_bytes + pr.rows_at[i] + p * kPanelBytes, &pr.map[i], &rows_full[s],
+                                        64 * p, t0, bh);
+                    }
+                    sent++;
+                    if (++s == nst) {
+                        s = 0;
+                        ph ^= 1u;
+                    }
                 }
-                sent++;
-                it.next(pr);
-                if (++s == nst) {
-                    s = 0;
-                    ph ^= 1u;
+                // every copy has landed before the shared memory goes away
+                for (int i = sent > nst ? sent - nst : 0; i < sent; i++) mbar_wait(&rows_full[i % nst], (i / nst) & 1);
+            } else {
+                // S for the first gradient's items, R for the others'
+                const int r = warp - 2, firsts = pr.kind[0].tiles;
+                const int64_t from = r == 0 && first - c0 * pr.per_chunk >= firsts ? c0 + 1 : c0;
+                const int64_t to = r == 1 && first + m - 1 - c1 * pr.per_chunk < firsts ? c1 - 1 : c1;
+                int sent = 0;
+                for (int64_t c = from; c <= to; c++, sent++) {
+                    if (sent > 0 && !wait_one(&x_free[r], (sent - 1) & 1, fail)) {
+                        fail_now();
+                        break;
+                    }
+                    mbar_expect_tx(&x_full[r], x_bytes);
+                    const __nv_bfloat16* x =
+                        pr.states + (static_cast<int64_t>(r) * pr.BH * pr.nch + c) * pr.v_tiles * (kTile * kDepth);
+                    for (int t = 0; t < pr.v_tiles; t++)
+                        bulk_load(xs + r * x_bytes + t * pr.k_panels * kXPanel, x + t * (kTile * kDepth),
+                                  pr.k_panels * kXPanel, &x_full[r]);
                 }
+                if (sent > 0) mbar_wait(&x_full[r], (sent - 1) & 1);
             }
-            // every copy has landed before the shared memory goes away
-            for (int i = sent > nst ? sent - nst : 0; i < sent; i++) mbar_wait(&full[i % nst], (i / nst) & 1);
         }
     } else if (warp == 1) {
         if (m > 0 && elect_one()) {
             constexpr uint32_t kIdS = idesc_bf16(kTile, kTile, 0, 0);
             constexpr uint32_t kIdMn = idesc_bf16(kTile, kDepth, 0, 1), kIdK = idesc_bf16(kTile, kDepth, 0, 0);
-            const uint64_t step = static_cast<uint64_t>(stage_bytes >> 4);
-            const uint64_t a_first = sdesc(smem_u32(smem), 16, 1024), mn = sdesc(0, kPanelBytes, 1024) - sdesc(0, 16, 1024);
-            const uint64_t to_b = static_cast<uint64_t>(b_off >> 4), to_c = static_cast<uint64_t>(c_off >> 4) + mn;
-            const uint64_t to_x = static_cast<uint64_t>(x_off >> 4);
+            // descriptors of the first stage's rows and of the states; a stage, a 64-column tile of X, a panel further
+            const uint64_t base = sdesc(smem_u32(smem), 16, 1024), mn = sdesc(0, kPanelBytes, 1024) - sdesc(0, 16, 1024);
+            const uint64_t at[4] = {base + static_cast<uint64_t>(pr.rows_at[0] >> 4), base + static_cast<uint64_t>(pr.rows_at[1] >> 4),
+                                    base + static_cast<uint64_t>(pr.rows_at[2] >> 4), base + static_cast<uint64_t>(pr.rows_at[3] >> 4)};
+            const uint64_t x_at[2] = {sdesc(smem_u32(xs), 16, 1024), sdesc(smem_u32(xs) + x_bytes, 16, 1024)};
+            const uint64_t st_step = static_cast<uint64_t>(pr.stage_bytes >> 4);
+            const uint64_t t_step = static_cast<uint64_t>((pr.k_panels * kXPanel) >> 4);
+            const int k_tiles = pr.kind[0].tiles, v_tiles = pr.kind[2].tiles;
+            const int v_steps = (pr.kind[0].d1 + 15) / 16, k_steps = (pr.kind[2].d1 + 15) / 16;
             auto kstep = [](int kk) { return static_cast<uint64_t>(((kk >> 2) * kPanelBytes + (kk & 3) * 32) >> 4); };
-            auto scores = [&](uint64_t a, int s, uint32_t ph, uint32_t buf, int ksteps) {
-                if (!wait_one(&ax_full[s], ph, fail) || !wait_one(&b_full[s], ph, fail)) return false;
-                tc_fence_after();
+            // a gradient's row tensors a, b, c
+            constexpr int kA[3] = {3, 2, 1}, kB[3] = {2, 3, 0}, kC[3] = {1, 0, 3};
+            auto scores = [&](auto kind, uint64_t stage, uint32_t buf) {
+                constexpr int K = decltype(kind)::value;
+                const uint64_t a = at[kA[K]] + stage, b = at[kB[K]] + stage;
+                const int steps = K == 2 ? k_steps : v_steps;
 #pragma unroll
                 for (int kk = 0; kk < 8; kk++)
-                    if (kk < ksteps)
-                        mma_bf16(tmem + kColS + buf * kTile, a + kstep(kk), a + to_b + kstep(kk), kIdS, kk > 0);
+                    if (kk < steps) mma_bf16(tmem + kColS + buf * kTile, a + kstep(kk), b + kstep(kk), kIdS, kk > 0);
                 mma_commit(&s_full[buf]);
-                mma_commit(&b_free[s]);
-                return true;
             };
+            using K0 = std::integral_constant<int, 0>;
+            using K1 = std::integral_constant<int, 1>;
+            using K2 = std::integral_constant<int, 2>;
             Item it = item_at(pr, first);
-            int s = 0;
-            uint32_t ph = 0;
-            uint64_t a = a_first;
-            int ksteps = (pr.kind[it.k].d1 + 15) / 16;
-            bool ok = scores(a, 0, 0, 0, ksteps);
-            for (int j = 0; j < m && ok; j++) {
-                const uint32_t buf = j & 1, use = (j >> 1) & 1;
+            int k = it.k, tile = it.tile, j = 0, s = 0;  // s: stage of the chunk
+            uint64_t stage = 0;                          // and what it adds to a descriptor
+            uint32_t ph = 0, grp = 0;                    // its phase; groups so far
+            uint32_t xph[2] = {0, 0};                    // phases of S and R
+            bool ok = wait_one(&rows_full[0], 0, fail);
+            if (ok) {
+                tc_fence_after();
+                if (k == 0) scores(K0(), 0, 0);
+                else if (k == 1) scores(K1(), 0, 0);
+                else scores(K2(), 0, 0);
+            }
+            // one item of gradient K; each gradient's code has its operands' places as constants, as this thread's
+            // instructions are what the kernel waits for
+            auto item = [&](auto kind) {
+                constexpr int K = decltype(kind)::value, R = K == 0 ? 0 : 1;
+                const int tiles = K == 2 ? v_tiles : k_tiles, steps = K == 2 ? k_steps : v_steps;
+                const uint32_t buf = j & 1, use = (j >> 1) & 1, sbuf = grp & 1;
                 const uint32_t d = tmem + kColO + buf * kTile;
-                if (j >= 2) ok = wait_one(&o_read[buf], use ^ 1u, fail);
-                if (!ok) break;
+                const bool opens = j == 0 || tile == 0, closes = tile + 1 == tiles;
+                if (j >= 2 && !wait_one(&o_read[buf], use ^ 1u, fail)) return false;
+                if (opens && (K < 2 || j == 0)) {  // the first item here that reads this state
+                    if (!wait_one(&x_full[R], xph[R], fail)) return false;
+                    xph[R] ^= 1u;
+                }
                 tc_fence_after();
-                if (pr.kind[it.k].state_t) {
+                const uint64_t a = at[kA[K]] + stage;
+                if constexpr (K < 2) {
+                    const uint64_t xt = x_at[R] + static_cast<uint64_t>((tile * kXPanel) >> 4);
 #pragma unroll
                     for (int kk = 0; kk < 8; kk++)
-                        if (kk < ksteps)
-                            mma_bf16(d + kDepth, a + kstep(kk),
-                                     a + to_x + static_cast<uint64_t>(((kk >> 2) * kXPanel + (kk & 3) * 32) >> 4), kIdK,
-                                     kk > 0);
+                        if (kk < steps)
+                            mma_bf16(d + kDepth, a + kstep(kk), xt + (kk >> 2) * t_step + static_cast<uint64_t>((kk & 3) * 2),
+                                     kIdK, kk > 0);
                 } else {
+                    const uint64_t xt = x_at[R] + mn + tile * t_step;
 #pragma unroll
                     for (int kk = 0; kk < 8; kk++)
-                        if (kk < ksteps) mma_bf16(d + kDepth, a + kstep(kk), a + to_x + mn + 128u * kk, kIdMn, kk > 0);
+                        if (kk < steps) mma_bf16(d + kDepth, a + kstep(kk), xt + 128u * kk, kIdMn, kk > 0);
                 }
-                mma_commit(&ax_free[s]);
-                // the next item's scores, so that its P is built while this one's is multiplied
-                const uint64_t ct = a + to_c;
-                const int cs = s;
-                const uint32_t cph = ph;
-                a += step;
-                if (++s == nst) {
-                    s = 0;
-                    ph ^= 1u;
-                    a = a_first;
+                if (closes && K != 1) mma_commit(&x_free[R]);
+                // the next group's scores, so that its P is built while this one's is multiplied. With one stage the next
+                // chunk's rows come only when this chunk is done
+                const bool wrap = s + 1 == nst;
+                if (opens && j + tiles - tile < m) {
+                    if constexpr (K < 2) {
+                        scores(std::integral_constant<int, K < 2 ? K + 1 : 0>(), stage, sbuf ^ 1u);
+                    } else if (nst > 1) {
+                        if (!wait_one(&rows_full[wrap ? 0 : s + 1], wrap ? ph ^ 1u : ph, fail)) return false;
+                        tc_fence_after();
+                        scores(K0(), wrap ? 0 : stage + st_step, sbuf ^ 1u);
+                    }
                 }
-                it.next(pr);
-                if (j + 1 < m) {
-                    ksteps = (pr.kind[it.k].d1 + 15) / 16;
-                    ok = scores(a, s, ph, buf ^ 1u, ksteps);
+                if (opens) {
+                    if (!wait_one(&p_ready[sbuf], (grp >> 1) & 1, fail)) return false;
+                    tc_fence_after();
                 }
-                ok = ok && wait_one(&p_ready[buf], use, fail) && wait_one(&c_full[cs], cph, fail);
-                if (!ok) break;
-                tc_fence_after();
+                const uint64_t c = at[kC[K]] + stage + static_cast<uint64_t>((tile * kPanelBytes) >> 4) + mn;
+                const uint32_t p = tmem + kColS + sbuf * kTile;
 #pragma unroll
                 for (int kk = 0; kk < kTile / 16; kk++) {
-                    const uint32_t p = tmem + kColS + buf * kTile + 16 * kk;
-                    mma_bf16_ta(d, p, ct + 128u * kk, kIdMn, kk > 0);
-                    mma_bf16_ta(d, p + 8, ct + 128u * kk, kIdMn, 1);
+                    mma_bf16_ta(d, p + 16 * kk, c + 128u * kk, kIdMn, kk > 0);
+                    mma_bf16_ta(d, p + 16 * kk + 8, c + 128u * kk, kIdMn, 1);
                 }
                 mma_commit(&o_full[buf]);
-                mma_commit(&c_free[cs]);
+                if (K == 2 && closes) {
+                    mma_commit(&rows_free[s]);
+                    ph = wrap ? ph ^ 1u : ph;
+                    stage = wrap ? 0 : stage + st_step;
+                    s = wrap ? 0 : s + 1;
+                    if (nst == 1 && j + 1 < m) {
+                        if (!wait_one(&rows_full[0], ph, fail)) return false;
+                        tc_fence_after();
+                        scores(K0(), 0, sbuf ^ 1u);
+                    }
+                }
+                grp += closes;
+                tile = closes ? 0 : tile + 1;
+                j++;
+                return true;
+            };
+            while (ok && j < m) {
+                for (; k == 0 && ok && j < m; k += ok && tile == 0) ok = item(K0());
+                for (; k == 1 && ok && j < m; k += ok && tile == 0) ok = item(K1());
+                for (; k == 2 && ok && j < m; k = ok && tile == 0 ? 0 : k) ok = item(K2());
             }
             if (!ok) fail_now();
             // every MMA issued above has completed before TMEM and shared memory go away
@@ -255,44 +302,51 @@ __global__ void __launch_bounds__(kGradThreads, 1) linear_grad_kernel(const __gr
     } else if (warp >= 4 && warp < 12) {
         const int w = warp & 3;
         const uint32_t lanes = tmem + (static_cast<uint32_t>(w * 32) << 16);
-        float* wt = weights[warp - 4];
         Item it = item_at(pr, first);
-        int made = -1;  // head and direction of the table
-        float far[3] = {};  // the row's part of the weight of a block one, two, three blocks off
-        for (int j = 0; j < m; j++) {
-            const int rev = pr.kind[it.k].reverse, key = 2 * it.h + rev;
-            if (key != made) {
-                made = key;
+        int made[2] = {-1, -1};  // head of the tables
+        float far[2][3] = {};    // the row's part of the weight of a block one, two, three blocks off
+        for (int j = 0, grp = 0; j < m; grp++) {
+            const int rev = pr.kind[it.k].reverse, buf = grp & 1;
+            float* wt = weights[rev];
+            if (!wait_warp(&s_full[buf], (grp >> 1) & 1, fail)) {
+                if (lane == 0) fail_now();
+                break;
+            }
+            // these scores came after the P of every warp for the group before the last
+            if (it.h != (rev ? made[1] : made[0])) {
                 const float la = pr.log_a[it.h];
-                __syncwarp();
 #pragma unroll
                 for (int u = 0; u < 2; u++) {
                     const int x = lane + 32 * u, gap = rev ? 31 - x : x - 31;
                     wt[x] = gap >= 0 ? gpow(la, gap) : 0.f;
                 }
                 wt[64 + lane] = gpow(la, rev ? lane : 31 - lane);
+                made[0] = rev ? made[0] : it.h;
+                made[1] = rev ? it.h : made[1];
 #pragma unroll
-                for (int u = 0; u < 3; u++) far[u] = gpow(la, rev ? 32 * (u + 1) - lane : 32 * u + lane + 1);
+                for (int u = 0; u < 3; u++) {
+                    const float f = gpow(la, rev ? 32 * (u + 1) - lane : 32 * u + lane + 1);
+                    far[0][u] = rev ? far[0][u] : f;
+                    far[1][u] = rev ? f : far[1][u];
+                }
                 __syncwarp();
             }
-            if (!wait_warp(&s_full[j & 1], (j >> 1) & 1, fail)) {
-                if (lane == 0) fail_now();
-                break;
-            }
             tc_fence_after();
-            const uint32_t cols = lanes + kColS + (j & 1) * kTile;
+            const uint32_t cols = lanes + kColS + buf * kTile;
 #pragma unroll 1
             for (int cb = (warp - 4) >> 2; cb < 4; cb += 2) {
                 const int side = cb == w ? 0 : (rev ? cb > w : cb < w) ? 1 : -1;
                 const int off = rev ? cb - w : w - cb;
-                const float rw = off == 1 ? far[0] : off == 2 ? far[1] : far[2];
+                const float rw = rev ? (off == 1 ? far[1][0] : off == 2 ? far[1][1] : far[1][2])
+                                     : (off == 1 ? far[0][0] : off == 2 ? far[0][1] : far[0][2]);
                 weigh_block<2>(cols + 32 * cb, side, wt + 31 + lane, wt + 64, rw);
             }
             tmem_st_wait();
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&p_ready[j & 1]);
-            it.next(pr);
+            if (lane == 0) mbar_arrive(&p_ready[buf]);
+            j += pr.kind[it.k].tiles - it.tile;
+            it.next_group(pr);
         }
     } else {
         const int row = (warp & 3) * 32 + lane, cw = (warp - 12) / 4 * 32;
@@ -301,7 +355,8 @@ __global__ void __launch_bounds__(kGradThreads, 1) linear_grad_kernel(const __gr
         int made = -1;
         float la = 0.f;
         for (int j = 0; j < m; j++) {
-            const int rev = pr.kind[it.k].reverse;
+            const GradKind& kd = pr.kind[it.k];
+            const int rev = kd.reverse;
             if (it.h != made) {
                 made = it.h;
                 la = pr.log_a[it.h];
@@ -309,6 +364,8 @@ __global__ void __launch_bounds__(kGradThreads, 1) linear_grad_kernel(const __gr
             const int nr = pr.T - it.ch * kTile < kTile ? pr.T - it.ch * kTile : kTile;
             const float f = row < nr ? gpow(la, rev ? nr - 1 - row : row + 1) : 0.f;
             const f32x2 f2 = pair2(f, f);
+            const int col = it.tile * kDepth + cw;
+            __nv_bfloat16* to = pr.out[it.k] + (static_cast<int64_t>(it.bh) * pr.T + it.ch * kTile + row) * kd.cols + col;
             if (!wait_warp(&o_full[j & 1], (j >> 1) & 1, fail)) {
                 if (lane == 0) fail_now();
                 break;
@@ -326,35 +383,13 @@ __global__ void __launch_bounds__(kGradThreads, 1) linear_grad_kernel(const __gr
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&o_read[j & 1]);
-            if (j > 0 && !wait_warp(&out_free, (j - 1) & 1, fail)) {
-                if (lane == 0) fail_now();
-                break;
-            }
+            // rows past T and columns past the tensor's are not written
 #pragma unroll
-            for (int c = 0; c < 4; c++)
-                *reinterpret_cast<uint4*>(stage_out + sw128_off(row, cw / 8 + c)) =
-                    make_uint4(o[c / 2][c % 2 * 4], o[c / 2][c % 2 * 4 + 1], o[c / 2][c % 2 * 4 + 2],
-                               o[c / 2][c % 2 * 4 + 3]);
-            fence_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&out_put);
-            if (warp == 12) {
-                if (elect_one()) {
-                    // rows past T and columns past the tensor's are not written
-                    if (wait_one(&out_put, j & 1, fail)) {
-                        tma_store_3d(&pr.omap[it.k], stage_out, it.tile * kDepth, it.ch * kTile, it.bh);
-                        bulk_commit();
-                        bulk_wait_read0();
-                        mbar_arrive(&out_free);
-                    } else {
-                        fail_now();
-                    }
-                }
-                __syncwarp();
-            }
+            for (int c = 0; c < 2; c++)
+                if (row < nr && col + 16 * c < kd.cols)
+                    store32(to + 16 * c, o[c], pr.wide && kd.cols % 16 == 0, col + 16 * c + 8 < kd.cols);
             it.next(pr);
         }
-        if (warp == 12) bulk_wait0();
     }
 
     tc_fence_before();
@@ -400,14 +435,21 @@ cudaError_t linear_tc_grads(const void* q, const void* k, const void* v, const v
     const int nch = (T - 1) / kTile + 1;
     const int kt = (d_k + kDepth - 1) / kDepth, vt = (d_v + kDepth - 1) / kDepth;
     const void* rows[4] = {q, k, v, dout};
-    for (int i = 0; i < 4; i++)
+    for (int i = 0; i < 4; i++) {
         if (!make_map_3d(&pr.map[i], rows[i], BH, T, i < 2 ? d_k : d_v, kTile)) return cudaErrorInvalidValue;
+        pr.panels[i] = i < 2 ? kt : vt;
+        pr.rows_at[i] = pr.stage_bytes;
+        pr.stage_bytes += pr.panels[i] * kPanelBytes;
+    }
     void* outs[3] = {dq, dk, dv};
-    for (int i = 0; i < 3; i++)
-        if (!make_map_3d(&pr.omap[i], outs[i], BH, T, i < 2 ? d_k : d_v, kTile)) return cudaErrorInvalidValue;
-    pr.kind[0] = {3, 2, 1, d_v, kt, 0, 1, 0};
-    pr.kind[1] = {2, 3, 0, d_v, kt, 1, 1, BH * nch};
-    pr.kind[2] = {1, 0, 3, d_k, vt, 1, 0, BH * nch};
+    pr.wide = true;
+    for (int i = 0; i < 3; i++) {
+        pr.out[i] = static_cast<__nv_bfloat16*>(outs[i]);
+        if (reinterpret_cast<uintptr_t>(outs[i]) % 32) pr.wide = false;
+    }
+    pr.kind[0] = {3, 2, 1, d_v, kt, 0, 1, d_k};
+    pr.kind[1] = {2, 3, 0, d_v, kt, 1, 1, d_k};
+    pr.kind[2] = {1, 0, 3, d_k, vt, 1, 0, d_v};
     pr.states = static_cast<const __nv_bfloat16*>(states);
     pr.log_a = log_a;
     pr.BH = BH;
@@ -415,12 +457,15 @@ cudaError_t linear_tc_grads(const void* q, const void* k, const void* v, const v
     pr.T = T;
     pr.nch = nch;
     pr.v_tiles = vt;
+    pr.k_panels = kt;
     pr.per_chunk = 2 * kt + vt;
-    const int np = (d_k > d_v ? d_k : d_v) > 64 ? 2 : 1, nst = np == 2 ? 2 : 3;
-    const int smem = nst * ((2 * np + 1) * kPanelBytes + np * kXPanel) + kPanelBytes + 1024;
+    // two stages but where both dk and dv are above 64
+    const int x_bytes = 2 * vt * kt * kXPanel + 1024;
+    pr.nst = 2 * pr.stage_bytes + x_bytes <= kSmemMost ? 2 : 1;
+    const int smem = pr.nst * pr.stage_bytes + x_bytes;
     const int64_t items = static_cast<int64_t>(BH) * nch * pr.per_chunk;
     const unsigned grid = static_cast<unsigned>(items < sms ? items : sms);
-    const cudaError_t e = launch_pdl(linear_grad_kernel, dim3(grid), dim3(kGradThreads), smem, stream, pr, nst, np, err);
+    const cudaError_t e = launch_pdl(linear_grad_kernel, dim3(grid), dim3(kGradThreads), smem, stream, pr, err);
     if (e != cudaSuccess) return e;
     note_launch(stream, "linear_grad");
     return cudaGetLastError();
