@@ -16,7 +16,7 @@
 // for its items (two chunks where they fit), and S and R; the items of one gradient share scores and P. Two items are in
 // flight: both kinds of accumulator are double.
 //
-// Measured there: the whole backward 233 us, 143 of it this kernel. With every item's operands copied for itself, its own
+// Measured there: the whole backward 227 us, 138 of it this kernel. With every item's operands copied for itself, its own
 // scores and the places of its operands looked up by the issuing thread it took 180 (gradients as scans: 278); the
 // rows shared, but looked up: 174. The instructions of the thread that issues the MMAs are the chain that is left, and
 // the rows in and out take 110 us of HBM; the state scans before it take 89 us (514 MB at 5.8 TB/s).
@@ -35,10 +35,8 @@ constexpr int kSmemMost = 232448 - 2048;  // 227 KB less the static part
 constexpr uint32_t kColS = 0, kColO = 256;
 
 struct GradKind {
-    int ia, ib, ic;  // row tensors: 0 q, 1 k, 2 v, 3 dout
     int d1, tiles, reverse;
-    int state_t;  // X is read as the transpose of the stored rows
-    int cols;     // of the output
+    int cols;  // of the output
 };
 
 struct GradParams {
@@ -142,14 +140,15 @@ __global__ void __launch_bounds__(kGradThreads, 1) linear_grad_kernel(const __gr
                         fail_now();
                         break;
                     }
-                    const int bh = static_cast<int>(c / pr.nch), t0 = static_cast<int>(c - static_cast<int64_t>(bh) * pr.nch) * kTile;
+                    const int bh = static_cast<int>(c / pr.nch);
+                    const int t0 = static_cast<int>(c - static_cast<int64_t>(bh) * pr.nch) * kTile;
                     mbar_expect_tx(&rows_full[s], pr.stage_bytes);
                     // in the order of their use
                     for (int u = 0; u < 4; u++) {
                         const int i = u == 0 ? 3 : u == 1 ? 2 : u == 2 ? 1 : 0;
                         for (int p = 0; p < pr.panels[i]; p++)
-                            tma_load_3d(smem + s * pr.stage_bytes + pr.rows_at[i] + p * kPanelBytes, &pr.map[i], &rows_full[s],
-                                        64 * p, t0, bh);
+                            tma_load_3d(smem + s * pr.stage_bytes + pr.rows_at[i] + p * kPanelBytes, &pr.map[i],
+                                        &rows_full[s], 64 * p, t0, bh);
                     }
                     sent++;
                     if (++s == nst) {
@@ -186,8 +185,8 @@ __global__ void __launch_bounds__(kGradThreads, 1) linear_grad_kernel(const __gr
             constexpr uint32_t kIdMn = idesc_bf16(kTile, kDepth, 0, 1), kIdK = idesc_bf16(kTile, kDepth, 0, 0);
             // descriptors of the first stage's rows and of the states; a stage, a 64-column tile of X, a panel further
             const uint64_t base = sdesc(smem_u32(smem), 16, 1024), mn = sdesc(0, kPanelBytes, 1024) - sdesc(0, 16, 1024);
-            const uint64_t at[4] = {base + static_cast<uint64_t>(pr.rows_at[0] >> 4), base + static_cast<uint64_t>(pr.rows_at[1] >> 4),
-                                    base + static_cast<uint64_t>(pr.rows_at[2] >> 4), base + static_cast<uint64_t>(pr.rows_at[3] >> 4)};
+            const uint64_t at[4] = {further(base, pr.rows_at[0] >> 4), further(base, pr.rows_at[1] >> 4),
+                                    further(base, pr.rows_at[2] >> 4), further(base, pr.rows_at[3] >> 4)};
             const uint64_t x_at[2] = {sdesc(smem_u32(xs), 16, 1024), sdesc(smem_u32(xs) + x_bytes, 16, 1024)};
             const uint64_t st_step = static_cast<uint64_t>(pr.stage_bytes >> 4);
             const uint64_t t_step = static_cast<uint64_t>((pr.k_panels * kXPanel) >> 4);
@@ -198,11 +197,11 @@ __global__ void __launch_bounds__(kGradThreads, 1) linear_grad_kernel(const __gr
             constexpr int kA[3] = {3, 2, 1}, kB[3] = {2, 3, 0}, kC[3] = {1, 0, 3};
             auto scores = [&](auto kind, uint64_t stage, uint32_t buf) {
                 constexpr int K = decltype(kind)::value;
-                const uint64_t a = at[kA[K]] + stage, b = at[kB[K]] + stage;
+                const uint64_t a = further(at[kA[K]], stage), b = further(at[kB[K]], stage);
                 const int steps = K == 2 ? k_steps : v_steps;
 #pragma unroll
                 for (int kk = 0; kk < 8; kk++)
-                    if (kk < steps) mma_bf16(tmem + kColS + buf * kTile, a + kstep(kk), b + kstep(kk), kIdS, kk > 0);
+                    if (kk < steps) mma_bf16(tmem + kColS + buf * kTile, further(a, kstep(kk)), further(b, kstep(kk)), kIdS, kk > 0);
                 mma_commit(&s_full[buf]);
             };
             using K0 = std::integral_constant<int, 0>;
@@ -234,19 +233,19 @@ __global__ void __launch_bounds__(kGradThreads, 1) linear_grad_kernel(const __gr
                     xph[R] ^= 1u;
                 }
                 tc_fence_after();
-                const uint64_t a = at[kA[K]] + stage;
+                const uint64_t a = further(at[kA[K]], stage);
                 if constexpr (K < 2) {
-                    const uint64_t xt = x_at[R] + static_cast<uint64_t>((tile * kXPanel) >> 4);
+                    const uint64_t xt = further(x_at[R], (tile * kXPanel) >> 4);
 #pragma unroll
                     for (int kk = 0; kk < 8; kk++)
                         if (kk < steps)
-                            mma_bf16(d + kDepth, a + kstep(kk), xt + (kk >> 2) * t_step + static_cast<uint64_t>((kk & 3) * 2),
-                                     kIdK, kk > 0);
+                            mma_bf16(d + kDepth, further(a, kstep(kk)), further(xt, (kk >> 2) * t_step + (kk & 3) * 2), kIdK,
+                                     kk > 0);
                 } else {
-                    const uint64_t xt = x_at[R] + mn + tile * t_step;
+                    const uint64_t xt = further(x_at[R], mn + tile * t_step);
 #pragma unroll
                     for (int kk = 0; kk < 8; kk++)
-                        if (kk < steps) mma_bf16(d + kDepth, a + kstep(kk), xt + 128u * kk, kIdMn, kk > 0);
+                        if (kk < steps) mma_bf16(d + kDepth, further(a, kstep(kk)), further(xt, 128u * kk), kIdMn, kk > 0);
                 }
                 if (closes && K != 1) mma_commit(&x_free[R]);
                 // the next group's scores, so that its P is built while this one's is multiplied. With one stage the next
@@ -265,12 +264,12 @@ __global__ void __launch_bounds__(kGradThreads, 1) linear_grad_kernel(const __gr
                     if (!wait_one(&p_ready[sbuf], (grp >> 1) & 1, fail)) return false;
                     tc_fence_after();
                 }
-                const uint64_t c = at[kC[K]] + stage + static_cast<uint64_t>((tile * kPanelBytes) >> 4) + mn;
+                const uint64_t c = further(at[kC[K]], stage + ((tile * kPanelBytes) >> 4) + mn);
                 const uint32_t p = tmem + kColS + sbuf * kTile;
 #pragma unroll
                 for (int kk = 0; kk < kTile / 16; kk++) {
-                    mma_bf16_ta(d, p + 16 * kk, c + 128u * kk, kIdMn, kk > 0);
-                    mma_bf16_ta(d, p + 16 * kk + 8, c + 128u * kk, kIdMn, 1);
+                    mma_bf16_ta(d, p + 16 * kk, further(c, 128u * kk), kIdMn, kk > 0);
+                    mma_bf16_ta(d, p + 16 * kk + 8, further(c, 128u * kk), kIdMn, 1);
                 }
                 mma_commit(&o_full[buf]);
                 if (K == 2 && closes) {
@@ -447,9 +446,9 @@ cudaError_t linear_tc_grads(const void* q, const void* k, const void* v, const v
         pr.out[i] = static_cast<__nv_bfloat16*>(outs[i]);
         if (reinterpret_cast<uintptr_t>(outs[i]) % 32) pr.wide = false;
     }
-    pr.kind[0] = {3, 2, 1, d_v, kt, 0, 1, d_k};
-    pr.kind[1] = {2, 3, 0, d_v, kt, 1, 1, d_k};
-    pr.kind[2] = {1, 0, 3, d_k, vt, 1, 0, d_v};
+    pr.kind[0] = {d_v, kt, 0, d_k};
+    pr.kind[1] = {d_v, kt, 1, d_k};
+    pr.kind[2] = {d_k, vt, 1, d_v};
     pr.states = static_cast<const __nv_bfloat16*>(states);
     pr.log_a = log_a;
     pr.BH = BH;

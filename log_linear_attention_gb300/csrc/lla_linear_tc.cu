@@ -244,11 +244,11 @@ __global__ void __launch_bounds__(kScanThreads, 1) linear_scan_kernel(const __gr
                 tc_fence_after();
 #pragma unroll
                 for (int kk = 0; kk < 4; kk++)
-                    if (kk < ksteps) mma_bf16(tmem + kColS + buf * kTile, a + kstep(kk), a + to_b + kstep(kk), kIdS, kk > 0);
+                    if (kk < ksteps) mma_bf16(tmem + kColS + buf * kTile, further(a, kstep(kk)), further(a, to_b + kstep(kk)), kIdS, kk > 0);
                 if (ksteps > 4) {
 #pragma unroll
                     for (int kk = 4; kk < 8; kk++)
-                        if (kk < ksteps) mma_bf16(tmem + kColS + buf * kTile, a + kstep(kk), a + to_b + kstep(kk), kIdS, 1);
+                        if (kk < ksteps) mma_bf16(tmem + kColS + buf * kTile, further(a, kstep(kk)), further(a, to_b + kstep(kk)), kIdS, 1);
                 }
                 mma_commit(&s_full[buf]);
                 return true;
@@ -267,13 +267,13 @@ __global__ void __launch_bounds__(kScanThreads, 1) linear_scan_kernel(const __gr
                          (j < (kStateOnly ? 2 : 1) || wait_one(&own_read[pl], use ^ 1u, fail));
                     if (!ok) break;
                     tc_fence_after();
-                    const uint64_t bt = a + to_b + kmaj, wp = w0 + static_cast<uint64_t>(kWcBytes >> 4) * pl;
+                    const uint64_t bt = further(a, to_b + kmaj), wp = further(w0, static_cast<uint64_t>(kWcBytes >> 4) * pl);
                     const uint32_t own = tmem + (kStateOnly ? 2 * kDepth * pl : kColOwn);
 #pragma unroll
-                    for (int kk = 0; kk < kTile / 16; kk++) mma_bf16(own, bt + 128u * kk, wp + 128u * kk, kIdOwn2, kk > 0);
+                    for (int kk = 0; kk < kTile / 16; kk++) mma_bf16(own, further(bt, 128u * kk), further(wp, 128u * kk), kIdOwn2, kk > 0);
 #pragma unroll
                     for (int kk = 0; kk < kTile / 16; kk++)
-                        mma_bf16(own + kDepth, bt + 128u * kk, wp + 2 * (kPanelBytes >> 4) + 128u * kk, kIdOwn1, 1);
+                        mma_bf16(own + kDepth, further(bt, 128u * kk), further(wp, 2 * (kPanelBytes >> 4) + 128u * kk), kIdOwn1, 1);
                     mma_commit(&own_full[pl]);
                 }
                 if (kStateOnly) {
@@ -284,27 +284,27 @@ __global__ void __launch_bounds__(kScanThreads, 1) linear_scan_kernel(const __gr
                     tc_fence_after();
 #pragma unroll
                     for (int kk = 0; kk < 8; kk++)
-                        if (kk < ksteps) mma_bf16(tmem + kColFar, a + kstep(kk), x0 + 128u * kk, kIdX, kk > 0);
+                        if (kk < ksteps) mma_bf16(tmem + kColFar, further(a, kstep(kk)), further(x0, 128u * kk), kIdX, kk > 0);
                     mma_commit(&x_free);
                     mma_commit(&qk_free[s]);
                     // the next chunk's scores, so that its P is built while this one's is multiplied
-                    const uint64_t ct = a + to_c + kmaj;
+                    const uint64_t ct = further(a, to_c + kmaj);
                     const bool wrap = s + 1 == nk;
                     if (j + 1 < n)
-                        ok = scores(wrap ? a_first : a + step, &qk_full[wrap ? 0 : s + 1], wrap ? ph ^ 1u : ph, par ^ 1u);
+                        ok = scores(wrap ? a_first : further(a, step), &qk_full[wrap ? 0 : s + 1], wrap ? ph ^ 1u : ph, par ^ 1u);
                     ok = ok && wait_one(&p_ready, par, fail);
                     if (!ok) break;
                     tc_fence_after();
 #pragma unroll
                     for (int kk = 0; kk < kTile / 16; kk++) {
                         const uint32_t p = tmem + kColS + par * kTile + 16 * kk;
-                        mma_bf16_ta(tmem + kColNear, p, ct + 128u * kk, kIdX, kk > 0);
-                        mma_bf16_ta(tmem + kColNear, p + 8, ct + 128u * kk, kIdX, 1);
+                        mma_bf16_ta(tmem + kColNear, p, further(ct, 128u * kk), kIdX, kk > 0);
+                        mma_bf16_ta(tmem + kColNear, p + 8, further(ct, 128u * kk), kIdX, 1);
                     }
                     mma_commit(&v_free[s]);
                     mma_commit(&o_full);
                 }
-                a += step;
+                a = further(a, step);
                 if (++s == nk) {
                     s = 0;
                     ph ^= 1u;

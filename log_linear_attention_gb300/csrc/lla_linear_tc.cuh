@@ -26,14 +26,6 @@ __device__ __forceinline__ void tma_prefetch_l2_3d(const CUtensorMap* map, int x
                  : "memory");
 }
 
-// Shared -> global: a box of a tensor map (what lies outside the tensor is not written), or contiguous bytes (16-byte
-// aligned, a multiple of 16); completion by the issuing thread's bulk groups.
-__device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, const void* src, int x, int y, int z) {
-    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(
-                     reinterpret_cast<uint64_t>(map)),
-                 "r"(smem_u32(src)), "r"(x), "r"(y), "r"(z)
-                 : "memory");
-}
 __device__ __forceinline__ void bulk_store(void* dst, const void* src, uint32_t bytes) {
     asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(smem_u32(src)), "r"(bytes)
                  : "memory");
@@ -48,6 +40,12 @@ __device__ __forceinline__ void mma_bf16_ta(uint32_t d_tmem, uint32_t a_tmem, ui
         "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
         "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
         : "memory");
+}
+
+// A shared-memory descriptor moved on: address and strides lie in the low word and do not carry out of it, so that one
+// addition does (the thread that issues the MMAs is on the longest path of its kernels).
+__device__ __forceinline__ uint64_t further(uint64_t desc, uint64_t by) {
+    return (desc & 0xffffffff00000000ull) | (static_cast<uint32_t>(desc) + static_cast<uint32_t>(by));
 }
 
 __device__ __forceinline__ void tmem_st16_issue(uint32_t taddr, const uint32_t* r) {
