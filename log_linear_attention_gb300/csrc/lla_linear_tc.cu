@@ -20,10 +20,12 @@
 // order. kFull does all of the above, forwards; kStates only forms the states, forwards or backwards, and
 // writes the one that enters each chunk in bf16 for the kernel of the gradients (lla_linear_grad.cu).
 //
-// Measured (GB300): a chunk takes about 2.0 us (1.2 where only the state is formed), the chain c copied -> w o C cut ->
-// own -> X -> far, near -> out with two stages (shared memory is full: 224 KB), issue slots 53% and tensor pipe 46% busy.
-// 4 x 16 heads, T = 8192, 128 x 64: 98 us for 403 MB, 503 with the pieces' (79 + 25 us cold). 16 heads, T = 65536,
-// 128 x 128: 385 us. 32 packed sequences of 256..8192: 252 us for 1.53 GB, 90% of the copy rate.
+// Measured (GB300): a chunk takes about 2.0 us (1.2 where only the state is formed). What bounds it is shared memory: at
+// d = 128 its products read 256 KB of operands, the copies write 80 KB, the cut reads and writes 64 KB and X takes 16: 416 KB,
+// 3250 of the 3900 cycles at 128 bytes each. (Two warps issuing the MMAs, each half of them, took 101 us where one takes
+// 97.) Two stages, as shared memory is full: 224 KB.
+// 4 x 16 heads, T = 8192, 128 x 64: 97 us for 403 MB, 503 with the pieces'. 16 heads, T = 65536, 128 x 128: 355 us. 32
+// packed sequences of 256..8192: 250 us for 1.53 GB, 90% of the copy rate.
 //
 // Rows of a chunk behind its sequence's end (another sequence's, when packed) are set to zero in shared
 // memory before any product sums over them. Every wait is bounded; on overrun the kernel records
@@ -66,12 +68,13 @@ __global__ void __launch_bounds__(kScanThreads, 1) linear_scan_kernel(const __gr
     constexpr int kCutWarps = kStateOnly ? 16 : 8;  // where there is no P, its warps cut w o C too
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    // one barrier per lane of the warp that sets them up
-    __shared__ uint64_t bars[32];
+    // one barrier per lane of the warp that sets them up, and one more
+    __shared__ uint64_t bars[33];
     uint64_t *const qk_full = bars, *const v_full = bars + 4, *const qk_free = bars + 8, *const v_free = bars + 12;
     uint64_t *const scaled = bars + 16, *const own_full = bars + 18, *const own_read = bars + 20, *const s_full = bars + 22;
     uint64_t &x_ready = bars[24], &x_free = bars[25], &x_put = bars[26], &x_sent = bars[27];
-    uint64_t &p_ready = bars[28], &o_full = bars[29], &o_read = bars[30], &drain = bars[31];
+    // p_ready of even and odd chunks: the next chunk's scores may be there before a P warp is done with this one's
+    uint64_t *const p_ready = bars + 28, &o_full = bars[30], &o_read = bars[31], &drain = bars[32];
     __shared__ uint32_t tmem_base_sh;
     __shared__ int fail_sh;
     __shared__ float pw[132];    // g^n
@@ -126,8 +129,10 @@ __global__ void __launch_bounds__(kScanThreads, 1) linear_scan_kernel(const __gr
     if (warp == 0) {
         // arrivals of a phase: one but where several warps take part
         const int parties = lane >= 12 && lane < 16 ? (kStateOnly ? kCutWarps : 1) : lane == 16 || lane == 17 ? kCutWarps :
-                            lane == 20 || lane == 21 || lane == 24 || lane == 26 || lane == 28 ? 8 : lane == 30 ? 4 : 1;
+                            lane == 20 || lane == 21 || lane == 24 || lane == 26 || lane == 28 || lane == 29 ? 8 :
+                            lane == 31 ? 4 : 1;
         mbar_init(&bars[lane], parties);
+        if (lane == 0) mbar_init(&drain, 1);
         fence_mbar_init();
         if (lane == 0) fail_sh = 0;
     }
@@ -292,7 +297,7 @@ __global__ void __launch_bounds__(kScanThreads, 1) linear_scan_kernel(const __gr
                     const bool wrap = s + 1 == nk;
                     if (j + 1 < n)
                         ok = scores(wrap ? a_first : further(a, step), &qk_full[wrap ? 0 : s + 1], wrap ? ph ^ 1u : ph, par ^ 1u);
-                    ok = ok && wait_one(&p_ready, par, fail);
+                    ok = ok && wait_one(&p_ready[par], (j >> 1) & 1, fail);
                     if (!ok) break;
                     tc_fence_after();
 #pragma unroll
@@ -352,7 +357,7 @@ __global__ void __launch_bounds__(kScanThreads, 1) linear_scan_kernel(const __gr
             tmem_st_wait();
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&p_ready);
+            if (lane == 0) mbar_arrive(&p_ready[j & 1]);
         }
     } else if (warp >= 12 && warp < 20) {
         const int d = (warp & 3) * 32 + lane;  // row of the state
