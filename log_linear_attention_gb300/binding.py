@@ -423,28 +423,19 @@ def device_error(stream=None) -> int:
     return int(load().lla_device_error(_stream_handle(stream)))
 
 
-def _ready(t_, dtype, shape, index):
-    """True for a contiguous tensor of this dtype and shape on GPU ``index``: the usual case, found in one expression
-    (single tokens are bound by the host). Anything else goes through the checks that name what is wrong."""
-    return (type(t_) is _torch_module.Tensor and t_.dtype is dtype and t_.shape == shape and t_.get_device() == index
-            and t_.is_contiguous())
-
+# The calls below are short on the GPU where they serve single tokens, so what the host does counts: each finds in
+# one expression that its arguments are as they should be, and only otherwise goes through the checks that name what
+# is wrong.
 
 def _linear_inputs(names, tensors, log_a, H):
     """Checks of the linear-attention calls: CUDA tensors of one dtype and device, log_a [H] fp32."""
     torch = _torch()
     q = tensors[0]
-    device, dtype = q.device, q.dtype
-    index = q.get_device()
     for n, t_ in zip(names, tensors):
-        if type(t_) is torch.Tensor and t_.dtype is dtype and t_.get_device() == index >= 0 and t_.is_contiguous():
-            continue
-        _check(t_, n, device)
-        if t_.dtype != dtype:
+        _check(t_, n, q.device)
+        if t_.dtype != q.dtype:
             raise TypeError(f"{', '.join(names)} must share one dtype")
-    if _ready(log_a, torch.float32, (H,), index):
-        return
-    _check(log_a, "log_a", device)
+    _check(log_a, "log_a", q.device)
     if log_a.dtype != torch.float32 or log_a.shape != (H,):
         raise ValueError(f"log_a must be float32 [{H}] (one decay per head)")
 
@@ -453,32 +444,30 @@ def _state(t_, name, shape, device):
     """Address of an optional fp32 state tensor of the given shape (None: NULL)."""
     if t_ is None:
         return None
-    if not _ready(t_, _torch().float32, shape, device.index):
+    torch = _torch_module
+    if not (type(t_) is torch.Tensor and t_.dtype is torch.float32 and t_.shape == shape and t_.is_contiguous()
+            and t_.device == device):
         _check(t_, name, device)
-        if t_.dtype != _torch().float32 or t_.shape != shape:
+        if t_.dtype != torch.float32 or t_.shape != shape:
             raise ValueError(f"{name} must be float32 {list(shape)}, got {t_.dtype} {list(t_.shape)}")
     return t_.data_ptr()
 
 
-def _on(device, stream, call):
-    """call(stream handle) with ``device`` and the launch stream current, so that what it allocates belongs to
-    the stream that writes it."""
+def _elsewhere(device, stream, call, *args):
+    """call(*args) with ``device`` and ``stream`` current, so that what it allocates belongs to the stream that
+    writes it."""
     torch = _torch()
-    if stream is None and torch.cuda.current_device() == device.index:  # the usual case, without context managers
-        return call(torch._C._cuda_getCurrentRawStream(device.index))
     with torch.cuda.device(device):
         if stream is None:
-            return call(torch.cuda.current_stream().cuda_stream)
+            return call(*args)
         if stream.device != device:
             raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
         with torch.cuda.stream(stream):
-            return call(stream.cuda_stream)
+            return call(*args)
 
 
 def _given(out, v):
-    """The caller's output tensor, checked, or a new one: like v in shape, dtype and device."""
-    if out is None:
-        return _torch().empty_like(v)
+    """The caller's output tensor, checked: like v in shape, dtype and device."""
     _check(out, "out", v.device)
     if out.dtype != v.dtype or out.shape != v.shape:
         raise ValueError(f"out must be {v.dtype} {list(v.shape)}, got {out.dtype} {list(out.shape)}")
@@ -492,22 +481,27 @@ def linear_forward(q, k, v, log_a, state0=None, state_out=None, out=None, stream
     q, k [B,H,T,dk]; v [B,H,T,dv] (bf16 or fp32, one dtype, any T >= 1); log_a [H] fp32. ``state0`` fp32
     [B,H,dk,dv], or [1,H,dk,dv] for one state shared by the batch, is the state the sequences go on from;
     ``state_out`` fp32 [B,H,dk,dv] is written with the state after the last token (see linear_decode_step)."""
+    torch = _torch()
     B, H, T, dk = q.shape
     dv = v.shape[-1]
-    _linear_inputs(("q", "k", "v"), (q, k, v), log_a, H)
-    if k.shape != q.shape or v.shape != (B, H, T, dv):
-        raise ValueError("shape mismatch between q, k and v")
+    dtype, device, index = q.dtype, q.device, q.get_device()
+    if not (type(q) is type(k) is type(v) is type(log_a) is torch.Tensor and index >= 0 and k.dtype is dtype
+            and v.dtype is dtype and log_a.dtype is torch.float32 and k.shape == q.shape and v.shape == (B, H, T, dv)
+            and log_a.shape == (H,) and k.get_device() == v.get_device() == log_a.get_device() == index
+            and q.is_contiguous() and k.is_contiguous() and v.is_contiguous() and log_a.is_contiguous()):
+        _linear_inputs(("q", "k", "v"), (q, k, v), log_a, H)
+        if k.shape != q.shape or v.shape != (B, H, T, dv):
+            raise ValueError("shape mismatch between q, k and v")
+    if stream is not None or index != torch._C._cuda_getDevice():
+        return _elsewhere(device, stream, linear_forward, q, k, v, log_a, state0, state_out, out)
     B0 = 0 if state0 is None else int(state0.shape[0])
-    s0 = _state(state0, "state0", (1 if B0 == 1 else B, H, dk, dv), q.device)
-    s1 = _state(state_out, "state_out", (B, H, dk, dv), q.device)
-
-    def call(sh):
-        o = _given(out, v)
-        _call(load().lla_linear_forward(q.data_ptr(), k.data_ptr(), v.data_ptr(), log_a.data_ptr(), s0, o.data_ptr(),
-                                        s1, B, B0, H, T, dk, dv, sh, _dtype_code(q)), "lla_linear_forward")
-        return o
-
-    return _on(q.device, stream, call)
+    s0 = _state(state0, "state0", (1 if B0 == 1 else B, H, dk, dv), device)
+    s1 = _state(state_out, "state_out", (B, H, dk, dv), device)
+    o = torch.empty_like(v) if out is None else _given(out, v)
+    _call(load().lla_linear_forward(q.data_ptr(), k.data_ptr(), v.data_ptr(), log_a.data_ptr(), s0, o.data_ptr(), s1, B,
+                                    B0, H, T, dk, dv, torch._C._cuda_getCurrentRawStream(index), _dtype_code(q)),
+          "lla_linear_forward")
+    return o
 
 
 def linear_forward_varlen(q, k, v, log_a, cu_seqlens, max_T: int, state0=None, state_out=None, out=None, stream=None):
@@ -517,25 +511,33 @@ def linear_forward_varlen(q, k, v, log_a, cu_seqlens, max_T: int, state0=None, s
     torch = _torch()
     H, total, dk = q.shape
     dv = v.shape[-1]
-    _linear_inputs(("q", "k", "v"), (q, k, v), log_a, H)
-    _check(cu_seqlens, "cu_seqlens", q.device)
-    if cu_seqlens.dtype != torch.int32 or cu_seqlens.dim() != 1:
-        raise TypeError("cu_seqlens must be int32 [n+1]")
+    dtype, device, index = q.dtype, q.device, q.get_device()
+    if not (type(q) is type(k) is type(v) is type(log_a) is type(cu_seqlens) is torch.Tensor and index >= 0
+            and k.dtype is dtype and v.dtype is dtype and log_a.dtype is torch.float32
+            and cu_seqlens.dtype is torch.int32 and k.shape == q.shape and v.shape == (H, total, dv)
+            and log_a.shape == (H,) and cu_seqlens.dim() == 1
+            and k.get_device() == v.get_device() == log_a.get_device() == cu_seqlens.get_device() == index
+            and q.is_contiguous() and k.is_contiguous() and v.is_contiguous() and log_a.is_contiguous()
+            and cu_seqlens.is_contiguous()):
+        _linear_inputs(("q", "k", "v"), (q, k, v), log_a, H)
+        _check(cu_seqlens, "cu_seqlens", device)
+        if cu_seqlens.dtype != torch.int32 or cu_seqlens.dim() != 1:
+            raise TypeError("cu_seqlens must be int32 [n+1]")
+        if k.shape != q.shape or v.shape != (H, total, dv):
+            raise ValueError("shape mismatch between packed q, k and v")
+    if stream is not None or index != torch._C._cuda_getDevice():
+        return _elsewhere(device, stream, linear_forward_varlen, q, k, v, log_a, cu_seqlens, max_T, state0, state_out,
+                          out)
     n = cu_seqlens.numel() - 1
-    if k.shape != q.shape or v.shape != (H, total, dv):
-        raise ValueError("shape mismatch between packed q, k and v")
     n0 = 0 if state0 is None else int(state0.shape[0])
-    s0 = _state(state0, "state0", (1 if n0 == 1 else n, H, dk, dv), q.device)
-    s1 = _state(state_out, "state_out", (n, H, dk, dv), q.device)
-
-    def call(sh):
-        o = _given(out, v)
-        _call(load().lla_linear_forward_varlen(q.data_ptr(), k.data_ptr(), v.data_ptr(), log_a.data_ptr(), s0,
-                                               o.data_ptr(), s1, cu_seqlens.data_ptr(), n, n0, H, total, int(max_T),
-                                               dk, dv, sh, _dtype_code(q)), "lla_linear_forward_varlen")
-        return o
-
-    return _on(q.device, stream, call)
+    s0 = _state(state0, "state0", (1 if n0 == 1 else n, H, dk, dv), device)
+    s1 = _state(state_out, "state_out", (n, H, dk, dv), device)
+    o = torch.empty_like(v) if out is None else _given(out, v)
+    _call(load().lla_linear_forward_varlen(q.data_ptr(), k.data_ptr(), v.data_ptr(), log_a.data_ptr(), s0, o.data_ptr(),
+                                           s1, cu_seqlens.data_ptr(), n, n0, H, total, int(max_T), dk, dv,
+                                           torch._C._cuda_getCurrentRawStream(index), _dtype_code(q)),
+          "lla_linear_forward_varlen")
+    return o
 
 
 def linear_backward(q, k, v, log_a, dout, state0=None, dstate_out=None, stream=None):
@@ -546,45 +548,50 @@ def linear_backward(q, k, v, log_a, dout, state0=None, dstate_out=None, stream=N
     torch = _torch()
     B, H, T, dk = q.shape
     dv = v.shape[-1]
+    device, index = q.device, q.get_device()
     _linear_inputs(("q", "k", "v", "dout"), (q, k, v, dout), log_a, H)
     if k.shape != q.shape or v.shape != (B, H, T, dv) or dout.shape != v.shape:
         raise ValueError("shape mismatch between q, k, v and dout")
+    if stream is not None or index != torch._C._cuda_getDevice():
+        return _elsewhere(device, stream, linear_backward, q, k, v, log_a, dout, state0, dstate_out)
     B0 = 0 if state0 is None else int(state0.shape[0])
-    s0 = _state(state0, "state0", (1 if B0 == 1 else B, H, dk, dv), q.device)
-    s1 = _state(dstate_out, "dstate_out", (B, H, dk, dv), q.device)
-
-    def call(sh):
-        dq, dk_, dv_ = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
-        ds = None if state0 is None else torch.empty_like(state0)
-        _call(load().lla_linear_backward(q.data_ptr(), k.data_ptr(), v.data_ptr(), log_a.data_ptr(), s0,
-                                         dout.data_ptr(), s1, dq.data_ptr(), dk_.data_ptr(), dv_.data_ptr(),
-                                         None if ds is None else ds.data_ptr(), B, B0, H, T, dk, dv, sh,
-                                         _dtype_code(q)), "lla_linear_backward")
-        return dq, dk_, dv_, ds
-
-    return _on(q.device, stream, call)
+    s0 = _state(state0, "state0", (1 if B0 == 1 else B, H, dk, dv), device)
+    s1 = _state(dstate_out, "dstate_out", (B, H, dk, dv), device)
+    dq, dk_, dv_ = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
+    ds = None if state0 is None else torch.empty_like(state0)
+    _call(load().lla_linear_backward(q.data_ptr(), k.data_ptr(), v.data_ptr(), log_a.data_ptr(), s0, dout.data_ptr(),
+                                     s1, dq.data_ptr(), dk_.data_ptr(), dv_.data_ptr(),
+                                     None if ds is None else ds.data_ptr(), B, B0, H, T, dk, dv,
+                                     torch._C._cuda_getCurrentRawStream(index), _dtype_code(q)), "lla_linear_backward")
+    return dq, dk_, dv_, ds
 
 
 def linear_decode_step(q, k, v, log_a, state, out=None, stream=None):
     """One token of every sequence, lla_linear_decode_step. q, k [B,H,dk]; v [B,H,dv]; log_a [H] fp32;
     ``state`` [B,H,dk,dv] fp32 is updated in place. Returns out [B,H,dv]."""
+    torch = _torch()
     B, H, dk = q.shape
     dv = v.shape[-1]
-    _linear_inputs(("q", "k", "v"), (q, k, v), log_a, H)
-    if k.shape != q.shape or v.shape != (B, H, dv):
-        raise ValueError("shape mismatch between q, k and v")
-    if state is None:
-        raise ValueError("state is needed")
-    sp = _state(state, "state", (B, H, dk, dv), q.device)
-
-    def call(sh):
-        o = _given(out, v)
-        _call(load().lla_linear_decode_step(q.data_ptr(), k.data_ptr(), v.data_ptr(), log_a.data_ptr(), sp,
-                                            o.data_ptr(), sh, B, H, dk, dv, _dtype_code(q)),
-              "lla_linear_decode_step")
-        return o
-
-    return _on(q.device, stream, call)
+    dtype, index = q.dtype, q.get_device()
+    if not (type(q) is type(k) is type(v) is type(log_a) is type(state) is torch.Tensor and index >= 0
+            and k.dtype is dtype and v.dtype is dtype and log_a.dtype is state.dtype is torch.float32
+            and k.shape == q.shape and v.shape == (B, H, dv) and log_a.shape == (H,) and state.shape == (B, H, dk, dv)
+            and k.get_device() == v.get_device() == log_a.get_device() == state.get_device() == index
+            and q.is_contiguous() and k.is_contiguous() and v.is_contiguous() and log_a.is_contiguous()
+            and state.is_contiguous()):
+        _linear_inputs(("q", "k", "v"), (q, k, v), log_a, H)
+        if k.shape != q.shape or v.shape != (B, H, dv):
+            raise ValueError("shape mismatch between q, k and v")
+        if state is None:
+            raise ValueError("state is needed")
+        _state(state, "state", (B, H, dk, dv), q.device)
+    if stream is not None or index != torch._C._cuda_getDevice():
+        return _elsewhere(q.device, stream, linear_decode_step, q, k, v, log_a, state, out)
+    o = torch.empty_like(v) if out is None else _given(out, v)
+    _call(load().lla_linear_decode_step(q.data_ptr(), k.data_ptr(), v.data_ptr(), log_a.data_ptr(), state.data_ptr(),
+                                        o.data_ptr(), torch._C._cuda_getCurrentRawStream(index), B, H, dk, dv,
+                                        _dtype_code(q)), "lla_linear_decode_step")
+    return o
 
 
 def decode_step_shared(q, k, v, log_a, lam, prefix_states, prefix_len: int, prefix_decay, states, t, out=None,
@@ -597,35 +604,41 @@ def decode_step_shared(q, k, v, log_a, lam, prefix_states, prefix_len: int, pref
     torch = _torch()
     B, H, dk = q.shape
     dv = v.shape[-1]
-    index = q.get_device()
-    f32 = torch.float32
-    if not (index >= 0 and _ready(k, q.dtype, q.shape, index) and _ready(v, q.dtype, (B, H, dv), index)
-            and q.is_contiguous() and _ready(log_a, f32, (B, H), index) and type(lam) is torch.Tensor
-            and lam.get_device() == index and lam.is_contiguous() and lam.dtype is f32
-            and _ready(t, torch.int64, (B,), index)):
+    if prefix_states is None or prefix_decay is None or states is None or prefix_states.dim() != 4 or states.dim() != 5:
+        raise ValueError("prefix_states [H,Lp,dk,dv], prefix_decay [B,H] and states [B,H,Lmax,dk,dv] are needed")
+    Lp, Lmax = prefix_states.shape[1], states.shape[2]
+    dtype, f32, index = q.dtype, torch.float32, q.get_device()
+    if not (type(q) is type(k) is type(v) is type(log_a) is type(lam) is type(prefix_states) is type(prefix_decay)
+            is type(states) is type(t) is torch.Tensor and index >= 0 and k.dtype is dtype and v.dtype is dtype
+            and log_a.dtype is lam.dtype is prefix_states.dtype is prefix_decay.dtype is states.dtype is f32
+            and t.dtype is torch.int64 and k.shape == q.shape and v.shape == (B, H, dv) and log_a.shape == (B, H)
+            and lam.shape == (B, H, Lmax) and prefix_states.shape == (H, Lp, dk, dv) and prefix_decay.shape == (B, H)
+            and states.shape == (B, H, Lmax, dk, dv) and t.shape == (B,)
+            and k.get_device() == v.get_device() == log_a.get_device() == lam.get_device() == t.get_device()
+            == prefix_states.get_device() == prefix_decay.get_device() == states.get_device() == index
+            and q.is_contiguous() and k.is_contiguous() and v.is_contiguous() and log_a.is_contiguous()
+            and lam.is_contiguous() and prefix_states.is_contiguous() and prefix_decay.is_contiguous()
+            and states.is_contiguous() and t.is_contiguous()):
         for t_, n in ((q, "q"), (k, "k"), (v, "v"), (log_a, "log_a"), (lam, "lambda"), (t, "t")):
             _check(t_, n, q.device)
-        if k.dtype != q.dtype or v.dtype != q.dtype:
+        if k.dtype != dtype or v.dtype != dtype:
             raise TypeError("q, k and v must share one dtype")
         if log_a.dtype != f32 or lam.dtype != f32:
             raise TypeError("log_a and lambda must be float32")
         if t.dtype != torch.int64 or t.shape != (B,):
             raise ValueError("t must be int64 [B]")
-    if prefix_states is None or prefix_decay is None or states is None or prefix_states.dim() != 4 or states.dim() != 5:
-        raise ValueError("prefix_states [H,Lp,dk,dv], prefix_decay [B,H] and states [B,H,Lmax,dk,dv] are needed")
-    Lp, Lmax = int(prefix_states.shape[1]), int(states.shape[2])
-    pp = _state(prefix_states, "prefix_states", (H, Lp, dk, dv), q.device)
-    dp = _state(prefix_decay, "prefix_decay", (B, H), q.device)
-    sp = _state(states, "states", (B, H, Lmax, dk, dv), q.device)
-    if lam.shape != (B, H, Lmax) or log_a.shape != (B, H) or k.shape != q.shape or v.shape != (B, H, dv):
-        raise ValueError("shape mismatch in decode inputs")
-
-    def call(sh):
-        o = _given(out, v)
-        _call(load().lla_decode_step_shared(q.data_ptr(), k.data_ptr(), v.data_ptr(), log_a.data_ptr(),
-                                            lam.data_ptr(), pp, int(prefix_len), Lp, dp, sp, t.data_ptr(),
-                                            o.data_ptr(), sh, B, H, dk, dv, Lmax, _dtype_code(q)),
-              "lla_decode_step_shared")
-        return o
-
-    return _on(q.device, stream, call)
+        _state(prefix_states, "prefix_states", (H, Lp, dk, dv), q.device)
+        _state(prefix_decay, "prefix_decay", (B, H), q.device)
+        _state(states, "states", (B, H, Lmax, dk, dv), q.device)
+        if lam.shape != (B, H, Lmax) or log_a.shape != (B, H) or k.shape != q.shape or v.shape != (B, H, dv):
+            raise ValueError("shape mismatch in decode inputs")
+    if stream is not None or index != torch._C._cuda_getDevice():
+        return _elsewhere(q.device, stream, decode_step_shared, q, k, v, log_a, lam, prefix_states, prefix_len,
+                          prefix_decay, states, t, out)
+    o = torch.empty_like(v) if out is None else _given(out, v)
+    _call(load().lla_decode_step_shared(q.data_ptr(), k.data_ptr(), v.data_ptr(), log_a.data_ptr(), lam.data_ptr(),
+                                        prefix_states.data_ptr(), int(prefix_len), Lp, prefix_decay.data_ptr(),
+                                        states.data_ptr(), t.data_ptr(), o.data_ptr(),
+                                        torch._C._cuda_getCurrentRawStream(index), B, H, dk, dv, Lmax, _dtype_code(q)),
+          "lla_decode_step_shared")
+    return o

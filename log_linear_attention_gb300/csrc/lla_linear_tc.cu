@@ -660,9 +660,12 @@ bool linear_tc_plan(LinTcPlan* pl, int batch, int H, int T, int64_t rows, int ti
     pl->nseg = 1;
     pl->seg_chunks = pl->piece_chunks = nch;
     pl->npiece = 0;
-    for (int s = 2; s <= 64 && s <= nch; s++) {
-        for (int r = 1; r <= 8; r++) {  // pieces of a segment
-            const int P = ((nch + s - 1) / s + r - 1) / r, L = P * r;
+    for (int s = 2, last = 0; s <= 64 && s <= nch; s++) {
+        const int base = (nch + s - 1) / s;  // chunks of a segment; the same ones for several s
+        if (base == last) continue;
+        last = base;
+        for (int r = 1; r <= 8 && r <= base; r++) {  // pieces of a segment
+            const int P = (base + r - 1) / r, L = P * r;
             const int n = (nch + L - 1) / L, np = (n - 1) * r;
             if (n < 2 || items * np > kMostPieces) continue;
             const double share = static_cast<double>(np) * P / nch;
