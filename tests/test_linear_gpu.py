@@ -105,6 +105,46 @@ def test_backward(lla, B, H, T, dk, dv, dtype, B0):
     L.check(host(got[3]), ref[3], size[3], "f32", T + B, "dstate0")
 
 
+@pytest.mark.parametrize("B,H,T,dk,dv", [(1, 7, 1100, 128, 64), (2, 9, 700, 128, 128), (3, 11, 900, 64, 128),
+                                         (1, 5, 800, 72, 40), (2, 8, 1300, 64, 64), (1, 16, 2000, 8, 128)])
+def test_backward_where_blocks_begin_inside_chunks(lla, B, H, T, dk, dv):
+    """More pieces of work than blocks, and not a multiple: every block begins and ends at another place of a chunk."""
+    test_backward(lla, B, H, T, dk, dv, "bf16", 1)
+
+
+def test_calls_of_several_threads_do_not_meet(lla):
+    """Prompts and gradients from threads with streams of their own give what they give alone, to the bit."""
+    import threading
+
+    def calls(seed):
+        p = problem(2, 4, 700 + 100 * seed, 64, 64, "bf16", 1, seed)
+        args = [dev(p, n) for n in ("q", "k", "v", "la")]
+        return lambda: (lla.linear_forward(*args, state0=dev(p, "s0")),
+                        *lla.linear_backward(*args, dev(p, "dout"), state0=dev(p, "s0"), dstate_out=dev(p, "ds")))
+
+    jobs = [calls(seed) for seed in range(3)]
+    alone = [job() for job in jobs]
+    torch.cuda.synchronize()
+    wrong = []
+
+    def work(i):
+        s = torch.cuda.Stream()
+        with torch.cuda.stream(s):
+            for _ in range(20):
+                got = jobs[i]()
+                s.synchronize()
+                if not all(torch.equal(x, y) for x, y in zip(got, alone[i])):
+                    wrong.append(i)
+        s.synchronize()
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(3)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not wrong
+
+
 def test_backward_without_state_gradient(lla):
     p = problem(2, 3, 150, 64, 64, "bf16", 0)
     got = lla.linear_backward(*(dev(p, n) for n in ("q", "k", "v", "la", "dout")))
