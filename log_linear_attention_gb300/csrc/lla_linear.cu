@@ -20,8 +20,8 @@
 //   lin_out         : out_i = sum_j M_ij (a_i . b_j) c_j + f_i X^T a_i, M_ij = g^|i-j| on the
 //                     causal side, f_i = g^(i+1) forwards, g^(n-1-i) backwards.
 // All products are 64 x 64 register-tiled fp32 products out of shared memory. FMAs bound them: the pipe is 50% busy over
-// launches of 1.6 waves of CTAs (gradients of 3 x 5 heads, T = 1301, 96 x 80: 145 us; prompts of 2 x 16 heads, T = 4096,
-// 128 x 128: 433 us, 30 TFLOP/s). No exponent is ever
+// launches of 1.6 waves of CTAs (gradients of 3 x 5 heads, T = 1301, 96 x 80: 139 us; prompts of 2 x 16 heads, T = 4096,
+// 128 x 128: 415 us, 31 TFLOP/s counting whole squares). No exponent is ever
 // negative, so no factor overflows for g <= 1; g^0 is 1 also for g = 0 (log_a = -inf).
 #include "lla_internal.cuh"
 #include "lla_linear.cuh"
@@ -73,13 +73,21 @@ __device__ __forceinline__ bool chunk_at(const LinSeqs& sq, int id, int h, Chunk
     return true;
 }
 
-// acc[i][j] += sum_{k < K} X[k][i0 + i] Y[k][j0 + j], rows of kLd floats, i0 = 8 (tid / 16), j0 = 4 (tid % 16):
-// four shared-memory wavefronts for 32 FMAs of a warp (4 x 4 pieces took six), two rows to an instruction (prompts
-// and gradients of 128 x 128 heads, T = 4096: 460 -> 433 us, 583 -> 564 us).
+// A warp's quarter of a 64 x 64 product, 32 x 32, and this thread's 8 x 4 piece of it. Which warp takes which is turned
+// from block to block, so that quarters with less to do fall to all sub-partitions of an SM.
+struct Piece {
+    int wr, wc, i0, j0;
+};
+__device__ __forceinline__ Piece piece_of(int turn) {
+    const int role = ((threadIdx.x >> 5) + turn) & 3, lane = threadIdx.x & 31;
+    return {role >> 1, role & 1, (role >> 1) * 32 + (lane >> 3) * 8, (role & 1) * 32 + (lane & 7) * 4};
+}
+
+// acc[i][j] += sum_{k < K} X[k][i] Y[k][j], rows of kLd floats: three shared-memory wavefronts for 32 FMAs of a warp
+// (4 x 4 pieces took six), two rows to an instruction (prompts and gradients of 128 x 128 heads, T = 4096:
+// 460 -> 433 us, 583 -> 564 us).
 template <int K>
 __device__ __forceinline__ void mul84(float (&acc)[8][4], const float* X, const float* Y) {
-    X += threadIdx.x / 16 * 8;
-    Y += threadIdx.x % 16 * 4;
     f32x2 s[4][4];
 #pragma unroll
     for (int i = 0; i < 4; i++)
@@ -186,6 +194,7 @@ __global__ void __launch_bounds__(kMulThreads, 4) lin_chunk_state(LinStateJobs j
     const T* b = static_cast<const T*>(jb.b) + at.row * jb.d1;
     const T* c = static_cast<const T*>(jb.c) + at.row * jb.d2;
     const bool v1 = jb.d1 % 4 == 0, v2 = jb.d2 % 4 == 0;
+    const Piece at_piece = piece_of(0);
     float acc[8][4] = {};
     Slab x, y;
     fetch(x, b, 0, at.n, r0, jb.d1, v1);
@@ -205,9 +214,9 @@ __global__ void __launch_bounds__(kMulThreads, 4) lin_chunk_state(LinStateJobs j
             fetch(x, b, t0 + kSlab, at.n, r0, jb.d1, v1);
             fetch(y, c, t0 + kSlab, at.n, c0, jb.d2, v2);
         }
-        mul84<kSlab>(acc, &X[0][0], &Y[0][0]);
+        mul84<kSlab>(acc, &X[0][at_piece.i0], &Y[0][at_piece.j0]);
     }
-    const int i0 = tid / 16 * 8, j0 = c0 + tid % 16 * 4;
+    const int i0 = at_piece.i0, j0 = c0 + at_piece.j0;
     float* dst = jb.states + at.state * jb.d1 * jb.d2;
 #pragma unroll
     for (int i = 0; i < 8; i++) {
@@ -287,7 +296,9 @@ __global__ void __launch_bounds__(kMulThreads, 4) lin_out(LinScans scans, LinSeq
     const T* a = static_cast<const T*>(sc.a) + (at.row + row) * d1;
     const T* b = static_cast<const T*>(sc.b) + (at.row + row) * d1;
     const T* c = static_cast<const T*>(sc.c) + at.row * d2;
-    const int i0 = tid / 16 * 8, j0 = tid % 16 * 4;
+    const Piece pc = piece_of(blockIdx.x + blockIdx.y + blockIdx.z);
+    const int i0 = pc.i0, j0 = pc.j0;
+    const int idle = sc.reverse ? 1 : 0;  // rows of quarter `idle` see no keys of the other half
     T* out = static_cast<T*>(sc.out);
     const float* state = sc.states + at.state * d1 * d2;
     // steps: nd slabs of a and b (scores), then for every 64 columns of c nd slabs of a and the entering state and nt
@@ -323,7 +334,9 @@ __global__ void __launch_bounds__(kMulThreads, 4) lin_out(LinScans scans, LinSeq
         __syncthreads();
         if (st + 1 == nd) grid_dep_wait();  // the entering states; the scores are formed beside the kernels before
         if (st + 1 < steps) get(st + 1);
-        mul84<kSlab>(o, near ? &Pt[(u - nd) * kSlab][0] : &X[0][0], &Y[0][0]);
+        // causality leaves a quarter of the scores out, and a half of the keys for half of the rows
+        const bool skip = pc.wr == idle && ((scores && pc.wc != idle) || (near && u - nd != idle));
+        if (!skip) mul84<kSlab>(o, near ? &Pt[(u - nd) * kSlab][i0] : &X[0][i0], &Y[0][j0]);
         if (scores && u == nd - 1) {
 #pragma unroll
             for (int q = 0; q < 4; q++) {
