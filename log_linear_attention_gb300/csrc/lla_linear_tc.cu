@@ -518,8 +518,13 @@ __global__ void __launch_bounds__(kScanThreads, 1) linear_scan_kernel(const __gr
             const int nr = rows_of(chunk_of(j));
             uint8_t* st = smem + v_off + s * v_step;
             ok = wait_warp(&v_full[s], ph, fail);
+            // the products of the chunk (only states: two chunks) before are done with the parts' place
+            const int pl = kStateOnly ? j & 1 : 0;
+            if (ok && j >= (kStateOnly ? 2 : 1))
+                ok = wait_warp(&own_full[pl], kStateOnly ? ((j >> 1) & 1) ^ 1 : (j - 1) & 1, fail);
             if (ok && nr < kTile) {
-                // rows behind the sequence's end count nothing, whatever they hold
+                // Rows behind the sequence's end count nothing, whatever they hold. Behind the wait above, as only then
+                // the stage's rows before these have landed for sure and the barrier's phase tells these from them.
                 ok = wait_warp(&qk_full[ks], kph, fail);
                 if (ok && row >= nr) {
                     const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
@@ -532,6 +537,8 @@ __global__ void __launch_bounds__(kScanThreads, 1) linear_scan_kernel(const __gr
                     }
                 }
             }
+            // and at first the state warps with the sum that lies there
+            if (ok && j == 0 && kMode != kPieces) ok = wait_warp(&x_ready, 0, fail);
             if (!ok) break;
             const float wt = row < nr ? pw[rev ? row + 1 : nr - 1 - row] : 0.f;
             const f32x2 wt2 = pair2(wt, wt), minus = pair2(-1.f, -1.f);
@@ -542,12 +549,6 @@ __global__ void __launch_bounds__(kScanThreads, 1) linear_scan_kernel(const __gr
             auto less = [&](f32x2 f, uint32_t p) {
                 return fma2(pair2(__uint_as_float(p << 16), __uint_as_float(p & 0xffff0000u)), minus, f);
             };
-            // the products of the chunk (only states: two chunks) before, and at first the state warps' reading of the
-            // sum, are done with this place
-            const int pl = kStateOnly ? j & 1 : 0;
-            if (j >= (kStateOnly ? 2 : 1)) ok = wait_warp(&own_full[pl], kStateOnly ? ((j >> 1) & 1) ^ 1 : (j - 1) & 1, fail);
-            else if (j == 0 && kMode != kPieces) ok = wait_warp(&x_ready, 0, fail);
-            if (!ok) break;
             uint8_t* to = wc + pl * kWcBytes;
             // rolled: the unrolled loop's 300 instructions were fetched anew for every chunk and took three times as long
 #pragma unroll 1

@@ -112,6 +112,31 @@ def test_backward_where_blocks_begin_inside_chunks(lla, B, H, T, dk, dv):
     test_backward(lla, B, H, T, dk, dv, "bf16", 1)
 
 
+@pytest.mark.parametrize("B,H,T,dk,dv", [(8, 16, 1562, 128, 64), (8, 16, 1562, 96, 104), (8, 16, 1562, 64, 64)])
+def test_many_heads_whose_last_chunk_is_ragged(lla, B, H, T, dk, dv):
+    """More heads than SMs, so that copies and products are apart by as much as the rings allow: every head against the
+    CUDA cores' fp32 arithmetic on the same values (5e-3 of a head's norm, see tests/_linear.py: that arithmetic's own
+    error is a thousandth of it), and every repetition the same to the bit."""
+    g = torch.Generator(device="cuda").manual_seed(T)
+    rand = lambda *s: torch.randn(*s, generator=g, device="cuda")  # noqa: E731
+    q, k = (rand(B, H, T, dk).mul_(dk ** -0.5).bfloat16() for _ in range(2))
+    v, do = (rand(B, H, T, dv).bfloat16() for _ in range(2))
+    la = -torch.exp2(-8.0 * torch.arange(1, H + 1, device="cuda") / H)
+
+    def run(*x):
+        return lla.linear_forward(x[0], x[1], x[2], la), *lla.linear_backward(x[0], x[1], x[2], la, x[3])[:3]
+
+    ref = run(q.float(), k.float(), v.float(), do.float())
+    first = None
+    for _ in range(8):
+        got = run(q, k, v, do)
+        first = first or got
+        for n, x, y, r in zip(("out", "dq", "dk", "dv"), got, first, ref):
+            rel = (x.float() - r).norm(dim=(2, 3)) / r.norm(dim=(2, 3))
+            assert float(rel.max()) <= 5e-3, (n, int(rel.argmax()), float(rel.max()))
+            assert torch.equal(x, y), n
+
+
 def test_calls_of_several_threads_do_not_meet(lla):
     """Prompts and gradients from threads with streams of their own give what they give alone, to the bit."""
     import threading
