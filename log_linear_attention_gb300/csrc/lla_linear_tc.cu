@@ -186,7 +186,8 @@ __global__ void __launch_bounds__(kScanThreads, 1) linear_scan_kernel(const __gr
         asm volatile("bar.sync 1, %0;" ::"n"(kSumThreads) : "memory");
     }
     // A CTA's last chunk adds to no state that is read, unless the state leaves here; a ragged one has its rows set to
-    // zero on the way.
+    // zero on the way. Where it is left out no warp cuts that chunk's c, so nobody tells the thread that issues the MMAs
+    // that c has landed: it waits for the copy itself before the product that reads it.
     const int n_own =
         n > 0 && !kStateOnly && !(sc.leave && g == have - 1) && rows_of(chunk_of(n - 1)) == kTile ? n - 1 : n;
     auto fail_now = [&]() {
@@ -297,7 +298,7 @@ __global__ void __launch_bounds__(kScanThreads, 1) linear_scan_kernel(const __gr
                     const bool wrap = s + 1 == nk;
                     if (j + 1 < n)
                         ok = scores(wrap ? a_first : further(a, step), &qk_full[wrap ? 0 : s + 1], wrap ? ph ^ 1u : ph, par ^ 1u);
-                    ok = ok && wait_one(&p_ready[par], (j >> 1) & 1, fail);
+                    ok = ok && wait_one(&p_ready[par], (j >> 1) & 1, fail) && (j < n_own || wait_one(&v_full[s], ph, fail));
                     if (!ok) break;
                     tc_fence_after();
 #pragma unroll

@@ -565,3 +565,44 @@ def test_full_sizes_sampled(lla, B, H, T, dk, dv):
         for n, x, r in zip(("out", "state", "dq", "dk", "dv", "dstate0"), got, ref):
             rel = float((x[b, h].double() - r[0]).norm() / r[0].norm())
             assert rel <= (5e-3 if x.dtype == torch.bfloat16 else 4 * (T + 16) ** 0.5 * L.U32), (n, b, h, rel)
+
+
+@pytest.mark.parametrize("B,H,T,dk,dv", [(8, 20, 1024, 128, 64), (8, 20, 512, 64, 128), (2, 4, 2048, 128, 64),
+                                         (2, 4, 2048, 64, 64), (1, 3, 1024, 96, 128), (3, 60, 128, 128, 128)])
+def test_whole_last_chunks_wait_for_their_rows(lla, B, H, T, dk, dv):
+    """Prompts of whole chunks whose state nobody takes, while another stream keeps the memory busy, so that copies are
+    late: a block's last chunk adds to no state, and its product has to wait for its rows of v all the same. More heads
+    than SMs, and cuts down to a chunk a block. Every head against the CUDA cores' fp32 arithmetic (5e-3 of a head's
+    norm, see tests/_linear.py) and every repetition to the bit."""
+    g = torch.Generator(device="cuda").manual_seed(T + dv)
+    rand = lambda *s: torch.randn(*s, generator=g, device="cuda")  # noqa: E731
+    inputs = []
+    for _ in range(3):
+        q, k = (rand(B, H, T, dk).mul_(dk ** -0.5).bfloat16() for _ in range(2))
+        inputs.append((q, k, rand(B, H, T, dv).bfloat16()))
+    la = -torch.exp2(-8.0 * torch.arange(1, H + 1, device="cuda") / H)
+    refs = [lla.linear_forward(*(t.float() for t in x), la) for x in inputs]
+    # the same rows as packed sequences of whole chunks
+    rows = [[t.transpose(0, 1).reshape(H, B * T, -1).contiguous() for t in x] for x in inputs]
+    cu = torch.arange(B + 1, device="cuda", dtype=torch.int32) * T
+    a, b = (torch.empty(1 << 28, device="cuda") for _ in range(2))  # 1 GiB each
+    busy, here = torch.cuda.Stream(), torch.cuda.current_stream()
+    busy.wait_stream(here)
+    first = [None, None]
+    for turn in range(6):
+        with torch.cuda.stream(busy):
+            for _ in range(4):
+                b.copy_(a)
+        got = []
+        for x, p in zip(inputs, rows):  # other rows lie in shared memory from call to call
+            got.append((lla.linear_forward(*x, la),
+                        lla.linear_forward_varlen(*p, la, cu, T).reshape(H, B, T, dv).transpose(0, 1)))
+        for i, (outs, r) in enumerate(zip(got, refs)):
+            for out in outs:
+                rel = (out.float() - r).norm(dim=(2, 3)) / r.norm(dim=(2, 3))
+                assert float(rel.max()) <= 5e-3, (turn, i, int(rel.argmax()), float(rel.max()))
+        if turn:
+            assert all(torch.equal(x, y) for xs, ys in zip(got, first) for x, y in zip(xs, ys)), turn
+        else:
+            first = got
+    busy.synchronize()
