@@ -5,7 +5,7 @@
 // registers of eight warps. Per chunk, n valid rows:
 //     scores  A B^T                      [128 x 128]  -> TMEM
 //     own     B^T [hi | mid + lo]        [d1 x 128]   -> TMEM, w o C cut into three bf16 parts, so that the
-//                                                     state keeps the 24 bits of fp32
+//                                                     state keeps the 24 bits of fp32 (only states: [hi | mid | lo])
 //     far     A X                        [128 x 64]   X = entering state, rounded to bf16
 //     near    P C                        [128 x 64]   P = scores o g^|i-j|, two bf16 parts in TMEM
 //     out_i = near_i + f_i far_i,   X <- g^n X + own
@@ -44,8 +44,8 @@ constexpr int kSmemMost = 232448 - 2048;  // 227 KB less the static part
 
 // TMEM columns
 // two buffers of scores (P takes the place of its scores: per 16 keys eight columns of high parts, eight of low); own: the
-// high part's product, then that of the middle and low parts
-constexpr uint32_t kColS = 0, kColNear = 256, kColFar = 320, kColOwn = 384;
+// high part's product, then that of the middle and low parts. Only states: two buffers of own, each part's product apart
+constexpr uint32_t kColS = 0, kColNear = 256, kColFar = 320, kColOwn = 384, kOwnStates = 3 * kDepth;
 
 enum { kFull, kPieces, kStates };  // what a launch forms: see above
 
@@ -237,7 +237,7 @@ __global__ void __launch_bounds__(kScanThreads, 1) linear_scan_kernel(const __gr
         if (elect_one()) {
             constexpr uint32_t kIdS = idesc_bf16(kTile, kTile, 0, 0);    // A B^T, both K-major
             constexpr uint32_t kIdX = idesc_bf16(kTile, kDepth, 0, 1);   // A X and P C: B MN-major
-            constexpr uint32_t kIdOwn2 = idesc_bf16(kTile, 2 * kDepth, 1, 1), kIdOwn1 = idesc_bf16(kTile, kDepth, 1, 1);
+            constexpr uint32_t kIdOwn = idesc_bf16(kTile, kDepth, 1, 1), kIdOwn3 = idesc_bf16(kTile, 3 * kDepth, 1, 1);
             // operands of the current stage and what a stage, a 16-column step of a K-major operand and a 16-row
             // step of an MN-major one (128) add to a descriptor's address field
             const uint64_t step = static_cast<uint64_t>(k_step >> 4);
@@ -273,13 +273,26 @@ __global__ void __launch_bounds__(kScanThreads, 1) linear_scan_kernel(const __gr
                          (j < (kStateOnly ? 2 : 1) || wait_one(&own_read[pl], use ^ 1u, fail));
                     if (!ok) break;
                     tc_fence_after();
+                    // Only MMAs of one accumulator and one shape are ordered among themselves, so columns that two parts are
+                    // added to see one shape. (High and middle part as one product of 128 columns, the low part onto the
+                    // last 64 of them, took 2% off the headline prompt and rested on an order that nothing promises.)
                     const uint64_t bt = further(a, to_b + kmaj), wp = further(w0, static_cast<uint64_t>(kWcBytes >> 4) * pl);
-                    const uint32_t own = tmem + (kStateOnly ? 2 * kDepth * pl : kColOwn);
+                    const uint64_t part = kPanelBytes >> 4;
+                    const uint32_t own = tmem + (kStateOnly ? kOwnStates * pl : kColOwn);
+                    if (kStateOnly) {
 #pragma unroll
-                    for (int kk = 0; kk < kTile / 16; kk++) mma_bf16(own, further(bt, 128u * kk), further(wp, 128u * kk), kIdOwn2, kk > 0);
+                        for (int kk = 0; kk < kTile / 16; kk++)
+                            mma_bf16(own, further(bt, 128u * kk), further(wp, 128u * kk), kIdOwn3, kk > 0);
+                    } else {
 #pragma unroll
-                    for (int kk = 0; kk < kTile / 16; kk++)
-                        mma_bf16(own + kDepth, further(bt, 128u * kk), further(wp, 2 * (kPanelBytes >> 4) + 128u * kk), kIdOwn1, 1);
+                        for (int kk = 0; kk < kTile / 16; kk++)
+                            mma_bf16(own, further(bt, 128u * kk), further(wp, 128u * kk), kIdOwn, kk > 0);
+#pragma unroll
+                        for (int kk = 0; kk < kTile / 16; kk++) {
+                            mma_bf16(own + kDepth, further(bt, 128u * kk), further(wp, part + 128u * kk), kIdOwn, kk > 0);
+                            mma_bf16(own + kDepth, further(bt, 128u * kk), further(wp, 2 * part + 128u * kk), kIdOwn, 1);
+                        }
+                    }
                     mma_commit(&own_full[pl]);
                 }
                 if (kStateOnly) {
@@ -435,9 +448,9 @@ __global__ void __launch_bounds__(kScanThreads, 1) linear_scan_kernel(const __gr
             const float gn = pw[rows_of(chunk_of(j))];
             f32x2 decay = pair2(gn, gn);
 #pragma unroll 1
-            for (int part = 1; part >= 0; part--) {  // the smaller first
+            for (int part = kStateOnly ? 2 : 1; part >= 0; part--) {  // the smaller first
                 f32x2 y[8], u[8];
-                const uint32_t from = lanes + (kStateOnly ? 2 * kDepth * pl : kColOwn) + part * kDepth + cw;
+                const uint32_t from = lanes + (kStateOnly ? kOwnStates * pl : kColOwn) + part * kDepth + cw;
                 tmem_ld16x2(from, from + 16, y, u);
 #pragma unroll
                 for (int c = 0; c < 8; c++) {

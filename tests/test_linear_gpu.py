@@ -606,3 +606,31 @@ def test_whole_last_chunks_wait_for_their_rows(lla, B, H, T, dk, dv):
         else:
             first = got
     busy.synchronize()
+
+
+@pytest.mark.parametrize("B,H,T,dk,dv", [(1, 2, 128, 64, 64), (2, 2, 384, 128, 128), (1, 2, 2048, 72, 40),
+                                         (40, 2, 300, 128, 64)])
+def test_states_keep_the_bits_of_fp32(lla, B, H, T, dk, dv):
+    """One token of each 128 has a key and a query, so a state is a sum of few terms and shows each of its roundings:
+    both states (after the last token; the gradient of the first) within them. Steps of 2^-22, of a term c chunks from
+    where it is read: the weight's expf and its product 5/4, three parts' sums in fp32, truncated, 3/2, the sum with the
+    state 1/4, together below 4; 5/4 for each chunk's decay on the way. The last eight bits of a term, which are a part
+    of their own in the products, weigh up to 2^-15."""
+    la = np.array([-2.0 ** -6, -2.0 ** -7])  # times a token count: exact
+    r = np.random.default_rng(T + dk)
+    t = np.arange(T)
+    lit = (t % 128 == 37)[None, None, :, None]
+    (k, kt), (q, qt), (v, vt), (do, dot) = (L.make(r, (B, H, T, d), "bf16") for d in (dk, dk, dv, dv))
+    k, q, kt, qt = k * lit, q * lit, kt * torch.from_numpy(lit), qt * torch.from_numpy(lit)
+    s0, s1 = torch.zeros(B, H, dk, dv, device="cuda"), torch.empty(B, H, dk, dv, device="cuda")
+    x = [y.cuda() for y in (qt, kt, vt, torch.from_numpy(la).float())]
+    lla.linear_forward(*x, state_out=s1)
+    ds0 = lla.linear_backward(*x, dot.cuda(), state0=s0)[3]
+    n = (T + 127) // 128
+    for what, got, a, c, gap, passed in (("state", s1, k, v, T - 1 - t, n - 1 - t // 128),
+                                         ("dstate0", ds0, q, do, t + 1, t // 128)):
+        w = L.powers(la, gap)[..., None]
+        ref = np.swapaxes(a * w, -1, -2) @ c
+        bound = np.swapaxes(np.abs(a) * w * (4 + 1.25 * passed)[:, None], -1, -2) @ np.abs(c) * 2.0 ** -22
+        worst = np.max(np.abs(host(got) - ref) - bound)
+        assert worst <= 1e-37, (what, worst)
