@@ -251,10 +251,14 @@ __global__ void __launch_bounds__(kGradThreads, 1) linear_grad_kernel(const __gr
                 // the next group's scores, so that its P is built while this one's is multiplied. With one stage the next
                 // chunk's rows come only when this chunk is done
                 const bool wrap = s + 1 == nst;
-                if (opens && j + tiles - tile < m) {
+                if (opens && j + tiles - tile < m && (K < 2 || nst > 1)) {
+                    // they take the place of the P that the item before this one read: MMAs of different accumulators are
+                    // ordered by their completion only. This item's far product runs meanwhile
+                    if (j > 0 && !wait_one(&o_full[buf ^ 1u], ((j - 1) >> 1) & 1, fail)) return false;
+                    tc_fence_after();
                     if constexpr (K < 2) {
                         scores(std::integral_constant<int, K < 2 ? K + 1 : 0>(), stage, sbuf ^ 1u);
-                    } else if (nst > 1) {
+                    } else {
                         if (!wait_one(&rows_full[wrap ? 0 : s + 1], wrap ? ph ^ 1u : ph, fail)) return false;
                         tc_fence_after();
                         scores(K0(), wrap ? 0 : stage + st_step, sbuf ^ 1u);

@@ -634,3 +634,30 @@ def test_states_keep_the_bits_of_fp32(lla, B, H, T, dk, dv):
         bound = np.swapaxes(np.abs(a) * w * (4 + 1.25 * passed)[:, None], -1, -2) @ np.abs(c) * 2.0 ** -22
         worst = np.max(np.abs(host(got) - ref) - bound)
         assert worst <= 1e-37, (what, worst)
+
+
+@pytest.mark.parametrize("B,H,T,dk,dv", [(6, 30, 640, 64, 64), (6, 30, 640, 8, 128), (6, 30, 500, 128, 64),
+                                         (3, 30, 640, 128, 128)])
+def test_gradients_beside_a_busy_stream(lla, B, H, T, dk, dv):
+    """Gradients whose groups of pieces are of one item and of two, while another stream keeps the memory busy: every
+    head against the CUDA cores' fp32 arithmetic (5e-3 of a head's norm), every repetition to the bit."""
+    g = torch.Generator(device="cuda").manual_seed(T + dk)
+    rand = lambda *s: torch.randn(*s, generator=g, device="cuda")  # noqa: E731
+    q, k = (rand(B, H, T, dk).mul_(dk ** -0.5).bfloat16() for _ in range(2))
+    v, do = (rand(B, H, T, dv).bfloat16() for _ in range(2))
+    la = -torch.exp2(-8.0 * torch.arange(1, H + 1, device="cuda") / H)
+    ref = lla.linear_backward(q.float(), k.float(), v.float(), la, do.float())
+    a, b = (torch.empty(1 << 28, device="cuda") for _ in range(2))  # 1 GiB each
+    busy = torch.cuda.Stream()
+    busy.wait_stream(torch.cuda.current_stream())
+    first = None
+    for _ in range(8):
+        with torch.cuda.stream(busy):
+            b.copy_(a)
+        got = lla.linear_backward(q, k, v, la, do)
+        first = first or got
+        for n, x, y, r in zip(("dq", "dk", "dv"), got, first, ref):
+            rel = (x.float() - r).norm(dim=(2, 3)) / r.norm(dim=(2, 3))
+            assert float(rel.max()) <= 5e-3, (n, int(rel.argmax()), float(rel.max()))
+            assert torch.equal(x, y), n
+    busy.synchronize()
