@@ -93,12 +93,13 @@ __global__ void __launch_bounds__(kThreads) shared_prefix(const T* __restrict__ 
 // 16-byte loads of a thread in flight; each held state is read once and written once, past L2's retention.
 // kOwnThreads: 256 where they hold all dk rows in one pass of four rows a thread, else 512 (64 x 16 heads of 128 x 64:
 // 86 us against 89; 4 x 4 heads of 64 x 64: 6.9 against 6.5). The next level's loads issued ahead cost more registers
-// than they give (101 us), two or eight rows a thread as much or more.
+// than they give (101 us), two or eight rows a thread as much or more. `part` is written while this kernel already runs,
+// so it is neither __restrict__ nor read through L1.
 template <typename T, int DV4, int kOwnThreads>
 __global__ void __launch_bounds__(kOwnThreads) shared_own(const T* __restrict__ q, const T* __restrict__ k,
                                                        const T* __restrict__ v, const float* __restrict__ log_a,
                                                        const float* __restrict__ lambda,
-                                                       const float* __restrict__ part, float* __restrict__ decay,
+                                                       const float* part, float* __restrict__ decay,
                                                        float* __restrict__ states, const int64_t* __restrict__ tpos,
                                                        T* __restrict__ out, int64_t P, int B, int H, int dk, int Lmax,
                                                        int* err) {
@@ -208,7 +209,8 @@ __global__ void __launch_bounds__(kOwnThreads) shared_own(const T* __restrict__ 
     const int col = tid % DV, part0 = tid / DV;
     float far = 0.f;
 #pragma unroll 4
-    for (int j = part0; j < parts; j += kGroups) far += far_w[j] * part[(static_cast<int64_t>(j) * B * H + bh) * DV + col];
+    for (int j = part0; j < parts; j += kGroups)
+        far += far_w[j] * __ldcg(part + (static_cast<int64_t>(j) * B * H + bh) * DV + col);
     red_far[part0][col] = far;
     __syncthreads();
     if (tid < DV) {

@@ -223,3 +223,41 @@ def test_graph_replay(lla):
         torch.cuda.synchronize()
         for o, w in zip(outs, want):
             assert torch.equal(o, w[i])
+
+
+def test_prefix_s_parts_are_those_of_the_call(lla):
+    """Calls over two prefixes in turn, whose parts lie in the same workspace one after the other, while another stream
+    keeps the memory busy: the kernel that reads the parts starts beside the one that writes them. At t = P an output is
+    lam_0 (q . k) v + exp(log_a) sum_j lam_j S_j^T q, in fp32 sums of dk (slots + 1) terms, and expf within 2^-22."""
+    P, B, H, dk, dv = 30011, 70, 8, 128, 64
+    Lmax = lla.num_levels(P) + 1
+    g = torch.Generator(device="cuda").manual_seed(1)
+    rand = lambda *s: torch.randn(*s, generator=g, device="cuda")  # noqa: E731
+    prefixes = [rand(H, Lmax, dk, dv) for _ in range(2)]
+    q, k, v = rand(B, H, dk), rand(B, H, dk) * dk ** -0.5, rand(B, H, dv)
+    log_a, lam = -torch.rand(B, H, generator=g, device="cuda"), torch.rand(B, H, Lmax, generator=g, device="cuda")
+    t = torch.full((B,), P, dtype=torch.int64, device="cuda")
+    held = [0] + [x for x in range(1, Lmax) if (P - 1) >> (x - 1) & 1]
+    w = torch.stack([lam[:, :, level(P, (P - 1) >> x << x)] for x in held], 2).double() * log_a.double().exp()[..., None]
+
+    def sums(prefix, q, k, v):
+        return (lam[:, :, 0, None].double() * (q * k).sum(-1, keepdim=True) * v
+                + torch.einsum("bhj,hjdv,bhd->bhv", w, prefix[:, held].double(), q))
+
+    x = [y.double() for y in (q, k, v)]
+    refs = [sums(p, *x) for p in prefixes]
+    sizes_ = [sums(p.abs(), *(y.abs() for y in x)) for p in prefixes]
+    states, decay = torch.empty(B, H, Lmax, dk, dv, device="cuda"), torch.empty(B, H, device="cuda")
+    a, b = (torch.empty(1 << 28, device="cuda") for _ in range(2))  # 1 GiB each
+    busy = torch.cuda.Stream()
+    busy.wait_stream(torch.cuda.current_stream())
+    first = None
+    for _ in range(6):
+        with torch.cuda.stream(busy):
+            b.copy_(a)
+        got = [lla.decode_step_shared(q, k, v, log_a, lam, p, P, decay, states, t) for p in prefixes]
+        for o, r, s in zip(got, refs, sizes_):
+            assert ((o.double() - r).abs() <= ((dk + len(held) + 16) * 2 * L.U32 + 2.0 ** -22) * s).all()
+        first = first or got
+        assert all(torch.equal(o, f) for o, f in zip(got, first))
+    busy.synchronize()
