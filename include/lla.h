@@ -402,10 +402,12 @@ int lla_decode_step_shared(const void* q, const void* k, const void* v, const fl
 /*
  * Test hook for the failure path of the bounded waits (no counterpart on the
  * pages; not for production use). On the current device, for the tensor-core
- * prefill output kernel of dv = 64: limit_cycles > 0 bounds each of its pipeline
+ * prefill output kernel of dv = 64 and the tensor-core kernels of linear
+ * attention: limit_cycles > 0 bounds each of its pipeline
  * waits to that many SM cycles (<= 0 restores the default, about 2 s at the
- * maximum clock); hold != 0 makes its epilogue first wait on a barrier that
- * nothing arrives at, so that wait runs out. The kernel then records
+ * maximum clock); hold != 0 makes its epilogue (where only states are formed,
+ * the warps that hold the state) first wait on a barrier that nothing arrives
+ * at, so that wait runs out. The kernel then records
  * LLA_ERR_TIMEOUT in the device error word, lets its own in-flight copies and
  * MMAs land (those drain waits keep the full bound), frees its tensor memory and
  * returns; the call's output is then undefined. Synchronous with the host; takes

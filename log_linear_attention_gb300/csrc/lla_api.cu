@@ -611,6 +611,7 @@ int lla_gdn_decode_step(const void* q, const void* k, const void* v, const float
 
 int lla_debug_set_waits(int64_t limit_cycles, int hold) {
     if (current_device() < 0) return LLA_ERR_CUDA;
+    lla::linear_set_waits({static_cast<long long>(limit_cycles), hold != 0});
     return lla::tc_set_debug_waits(static_cast<long long>(limit_cycles), hold) == cudaSuccess ? LLA_OK : LLA_ERR_CUDA;
 }
 

@@ -104,6 +104,14 @@ struct LinTcPlan {
     size_t seg_bytes;
 };
 bool linear_tc_supported(int dtype, int dk, int dv);
+// Failure-path test hooks of the tensor-core kernels on the current device, for launches from here on: the bound of their
+// pipeline waits in SM cycles (<= 0: the default) and a wait that nothing completes.
+struct LinWaits {
+    long long cycles;
+    int hold;
+};
+void linear_set_waits(LinWaits waits);
+LinWaits linear_waits();
 // rows: token rows of the call; tiles: 64-column tiles over all scans of one head; states: only the states are formed
 bool linear_tc_plan(LinTcPlan* plan, int batch, int H, int T, int64_t rows, int tiles, bool states);
 // One forward scan (states null), or up to two of either direction (dense) that leave the state entering each

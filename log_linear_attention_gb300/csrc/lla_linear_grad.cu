@@ -49,6 +49,7 @@ struct GradParams {
     int stage_bytes, nst;
     int BH, H, T, nch, v_tiles, k_panels, per_chunk;  // per_chunk: items of one chunk
     bool wide;  // 32-byte stores
+    LinWaits waits;
 };
 
 // An item and its successors; every role walks its CTA's items with one of these. The items of one gradient and chunk
@@ -90,8 +91,9 @@ __global__ void __launch_bounds__(kGradThreads, 1) linear_grad_kernel(const __gr
     __shared__ uint64_t rows_full[2], rows_free[2];  // of a stage
     __shared__ uint64_t x_full[2], x_free[2];        // of S, of R
     __shared__ uint64_t s_full[2], p_ready[2], o_full[2], o_read[2], drain;
+    __shared__ uint64_t never;  // nothing arrives here: for the test hook
     __shared__ uint32_t tmem_base_sh;
-    __shared__ int fail_sh;
+    __shared__ Bound bound;
     // forwards and backwards: weight of key c for row r of a diagonal 32-key block at 31 + r - c, and of key c of another
     // block. Each P warp writes what it reads, all the same, and none is a head's two groups of one direction ahead.
     __shared__ __align__(16) float weights[2][96];
@@ -102,7 +104,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) linear_grad_kernel(const __gr
     const int m = static_cast<int>(total * (blockIdx.x + 1) / gridDim.x - first);  // items of this CTA
     const int nst = pr.nst, x_bytes = pr.v_tiles * pr.k_panels * kXPanel;
     uint8_t* xs = smem + nst * pr.stage_bytes;  // the entering states S and R of a chunk, all their tiles
-    volatile int* fail = &fail_sh;
+    volatile Bound* const fail = &bound;
 
     if (tid == 0) {
         for (int i = 0; i < 2; i++) {
@@ -116,8 +118,9 @@ __global__ void __launch_bounds__(kGradThreads, 1) linear_grad_kernel(const __gr
             mbar_init(&o_read[i], 8);
         }
         mbar_init(&drain, 1);
+        mbar_init(&never, 1);
         fence_mbar_init();
-        fail_sh = 0;
+        bound = {pr.waits.cycles, 0};
     }
     if (warp == 1) tmem_alloc(&tmem_base_sh, 512);
     tc_fence_before();
@@ -126,7 +129,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) linear_grad_kernel(const __gr
     grid_dep_wait();  // the states
     const uint32_t tmem = tmem_base_sh;
     auto fail_now = [&]() {
-        if (atomicExch(&fail_sh, 1) == 0) record_error(err, kDevTimeout);
+        if (atomicExch(&bound.fail, 1) == 0) record_error(err, kDevTimeout);
     };
 
     if (warp == 0 || warp == 2 || warp == 3) {
@@ -357,7 +360,9 @@ __global__ void __launch_bounds__(kGradThreads, 1) linear_grad_kernel(const __gr
         Item it = item_at(pr, first);
         int made = -1;
         float la = 0.f;
-        for (int j = 0; j < m; j++) {
+        const bool held = pr.waits.hold && !wait_warp(&never, 0, fail);
+        if (held && lane == 0) fail_now();
+        for (int j = 0; j < m && !held; j++) {
             const GradKind& kd = pr.kind[it.k];
             const int rev = kd.reverse;
             if (it.h != made) {
@@ -459,6 +464,7 @@ cudaError_t linear_tc_grads(const void* q, const void* k, const void* v, const v
     pr.H = H;
     pr.T = T;
     pr.nch = nch;
+    pr.waits = linear_waits();
     pr.v_tiles = vt;
     pr.k_panels = kt;
     pr.per_chunk = 2 * kt + vt;

@@ -57,6 +57,7 @@ struct ScanParams {
     __nv_bfloat16* states;  // kStates: the entering states
     LinSeqs sq;
     int count, nseg, seg_chunks, npiece, piece_chunks, seg_pieces, packed;
+    LinWaits waits;
 };
 
 // Warps: 0 and 2 TMA producers, 1 TMEM owner and MMA issuer, 4..11 P (every other block of 32 keys), 12..19 state
@@ -76,7 +77,7 @@ __global__ void __launch_bounds__(kScanThreads, 1) linear_scan_kernel(const __gr
     // p_ready of even and odd chunks: the next chunk's scores may be there before a P warp is done with this one's
     uint64_t *const p_ready = bars + 28, &o_full = bars[30], &o_read = bars[31], &drain = bars[32];
     __shared__ uint32_t tmem_base_sh;
-    __shared__ int fail_sh;
+    __shared__ Bound bound;
     __shared__ float pw[132];    // g^n
     __shared__ __align__(16) float colw[32];  // weight of key c of an off-diagonal 32-key block
     __shared__ float diag[64];   // weight of key c for row r of a diagonal block, at 31 + r - c
@@ -124,7 +125,8 @@ __global__ void __launch_bounds__(kScanThreads, 1) linear_scan_kernel(const __gr
     const int k_off = kStateOnly ? 0 : k_bytes, v_off = kStateOnly ? nk * k_bytes : 2 * k_bytes;
     uint8_t* wc = smem + (kStateOnly ? v_off + nv * kPanelBytes : nk * k_step);
     uint8_t* xs = wc + (kStateOnly ? 2 : 1) * kWcBytes;  // kFull, kStates
-    volatile int* fail = &fail_sh;
+    volatile Bound* const fail = &bound;
+    uint64_t* const never = kStateOnly ? s_full : &x_put;  // a barrier that no role of this mode uses, for the test hook
 
     if (warp == 0) {
         // arrivals of a phase: one but where several warps take part
@@ -134,7 +136,7 @@ __global__ void __launch_bounds__(kScanThreads, 1) linear_scan_kernel(const __gr
         mbar_init(&bars[lane], parties);
         if (lane == 0) mbar_init(&drain, 1);
         fence_mbar_init();
-        if (lane == 0) fail_sh = 0;
+        if (lane == 0) bound = {pr.waits.cycles, 0};
     }
     if (warp == 1) tmem_alloc(&tmem_base_sh, 512);
     const float la = pr.log_a[h];
@@ -191,7 +193,7 @@ __global__ void __launch_bounds__(kScanThreads, 1) linear_scan_kernel(const __gr
     const int n_own =
         n > 0 && !kStateOnly && !(sc.leave && g == have - 1) && rows_of(chunk_of(n - 1)) == kTile ? n - 1 : n;
     auto fail_now = [&]() {
-        if (atomicExch(&fail_sh, 1) == 0) record_error(err, kDevTimeout);
+        if (atomicExch(&bound.fail, 1) == 0) record_error(err, kDevTimeout);
     };
 
     if (warp == 0 || warp == 2) {
@@ -427,7 +429,11 @@ __global__ void __launch_bounds__(kScanThreads, 1) linear_scan_kernel(const __gr
             if (lane == 0) mbar_arrive(&x_ready);
         }
         bool ok = true;
-        for (int j = 0; j < n_own; j++) {
+        if (kStateOnly && pr.waits.hold && !wait_warp(never, 0, fail)) {
+            if (lane == 0) fail_now();
+            ok = false;
+        }
+        for (int j = 0; j < n_own && ok; j++) {
             if (kMode == kStates) {
                 // the entering state of this chunk, on its way to memory by warp 3
                 if (j > 0 && !wait_warp(&x_sent, (j - 1) & 1, fail)) {
@@ -496,7 +502,9 @@ __global__ void __launch_bounds__(kScanThreads, 1) linear_scan_kernel(const __gr
                              (pr.packed ? static_cast<int64_t>(h) * pr.sq.total + row0
                                         : static_cast<int64_t>(bh) * pr.sq.T) * d2 + c0;
         const bool wide = d2 % 16 == 0 && (reinterpret_cast<uintptr_t>(sc.out) & 31) == 0;
-        for (int j = 0; j < n; j++) {
+        const bool held = pr.waits.hold && !wait_warp(never, 0, fail);
+        if (held && lane == 0) fail_now();
+        for (int j = 0; j < n && !held; j++) {
             if (!wait_warp(&o_full, j & 1, fail)) {
                 if (lane == 0) fail_now();
                 break;
@@ -635,6 +643,9 @@ int sm_count() {
     return sms;
 }
 
+std::atomic<long long> g_wait_cycles[kMaxDevices];  // 0: the default
+std::atomic<int> g_hold[kMaxDevices];
+
 constexpr int64_t kMostPieces = 16384;  // 512 MB of workspace
 
 int smem_bytes(int mode, int d1) {
@@ -646,6 +657,20 @@ int smem_bytes(int mode, int d1) {
 }
 
 }  // namespace
+
+void linear_set_waits(LinWaits waits) {
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return;
+    g_wait_cycles[dev].store(waits.cycles > 0 ? waits.cycles : 0);
+    g_hold[dev].store(waits.hold);
+}
+
+LinWaits linear_waits() {
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return {kWaitCycles, 0};
+    const long long cycles = g_wait_cycles[dev].load(std::memory_order_relaxed);
+    return {cycles ? cycles : kWaitCycles, g_hold[dev].load(std::memory_order_relaxed)};
+}
 
 bool linear_tc_supported(int dtype, int dk, int dv) { return dtype == 0 && dk % 8 == 0 && dv % 8 == 0; }
 
@@ -719,6 +744,7 @@ cudaError_t linear_tc_run(const LinTcPlan& pl, const LinTcMap* maps, int n_maps,
     pr.piece_chunks = pl.piece_chunks;
     pr.seg_pieces = pl.seg_chunks / pl.piece_chunks;
     pr.packed = packed;
+    pr.waits = linear_waits();
     int base = 0, tiles = 0, d1 = 0;
     for (int i = 0; i < count; i++) {
         pr.scan[i] = scans[i];

@@ -157,27 +157,31 @@ __device__ __forceinline__ bool mbar_try_many(uint64_t* bar, uint32_t parity) {
 }
 
 // Bounded waits. They give up when another role has.
-__device__ __noinline__ bool wait_long(uint64_t* bar, uint32_t parity, volatile int* fail) {
+struct Bound {  // in shared memory
+    long long cycles;
+    int fail;  // set by the role that gave up first
+};
+__device__ __noinline__ bool wait_long(uint64_t* bar, uint32_t parity, volatile Bound* to) {
     const long long start = clock64();
     while (!mbar_try_many(bar, parity)) {
-        if (*fail || clock64() - start > kWaitCycles) return false;
+        if (to->fail || clock64() - start > to->cycles) return false;
     }
     return true;
 }
-__device__ __forceinline__ bool wait_one(uint64_t* bar, uint32_t parity, volatile int* fail) {
-    return mbar_try_many(bar, parity) || wait_long(bar, parity, fail);
+__device__ __forceinline__ bool wait_one(uint64_t* bar, uint32_t parity, volatile Bound* to) {
+    return mbar_try_many(bar, parity) || wait_long(bar, parity, to);
 }
-__device__ __noinline__ bool wait_long_warp(uint64_t* bar, uint32_t parity, volatile int* fail) {
+__device__ __noinline__ bool wait_long_warp(uint64_t* bar, uint32_t parity, volatile Bound* to) {
     const long long start = clock64();
     while (true) {
         const bool done = mbar_try_many(bar, parity);
         if (__all_sync(0xffffffffu, done)) return true;
-        const bool late = *fail || clock64() - start > kWaitCycles;
+        const bool late = to->fail || clock64() - start > to->cycles;
         if (__any_sync(0xffffffffu, late)) return false;
     }
 }
-__device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, volatile int* fail) {
-    return __all_sync(0xffffffffu, mbar_try_many(bar, parity)) || wait_long_warp(bar, parity, fail);
+__device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, volatile Bound* to) {
+    return __all_sync(0xffffffffu, mbar_try_many(bar, parity)) || wait_long_warp(bar, parity, to);
 }
 
 // 32 bytes of a global row in one store: a whole sector (16 bytes each where rows are not so aligned, `second` false
