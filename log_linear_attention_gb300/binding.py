@@ -453,6 +453,19 @@ def _state(t_, name, shape, device):
     return t_.data_ptr()
 
 
+def _small(t_, where, *written):
+    """A per-head or per-sequence array at the library's alignment of 16 bytes: itself, or a copy where it starts between
+    (a rank's part of the decays, the positions of a part of the batch). The library sees the copy, so that the call
+    writes nothing over the array itself is found here."""
+    at = t_.data_ptr()
+    if at & 15 == 0:
+        return t_
+    for w in written:
+        if w is not None and w.data_ptr() < at + t_.numel() * t_.element_size() and at < w.data_ptr() + w.numel() * w.element_size():
+            raise LLAError(LLA_ERR_INVALID_ARG, where)
+    return t_.clone()
+
+
 def _elsewhere(device, stream, call, *args):
     """call(*args) with ``device`` and ``stream`` current, so that what it allocates belongs to the stream that
     writes it."""
@@ -498,6 +511,7 @@ def linear_forward(q, k, v, log_a, state0=None, state_out=None, out=None, stream
     s0 = _state(state0, "state0", (1 if B0 == 1 else B, H, dk, dv), device)
     s1 = _state(state_out, "state_out", (B, H, dk, dv), device)
     o = torch.empty_like(v) if out is None else _given(out, v)
+    log_a = _small(log_a, "lla_linear_forward", o, state_out)
     _call(load().lla_linear_forward(q.data_ptr(), k.data_ptr(), v.data_ptr(), log_a.data_ptr(), s0, o.data_ptr(), s1, B,
                                     B0, H, T, dk, dv, torch._C._cuda_getCurrentRawStream(index), _dtype_code(q)),
           "lla_linear_forward")
@@ -533,6 +547,8 @@ def linear_forward_varlen(q, k, v, log_a, cu_seqlens, max_T: int, state0=None, s
     s0 = _state(state0, "state0", (1 if n0 == 1 else n, H, dk, dv), device)
     s1 = _state(state_out, "state_out", (n, H, dk, dv), device)
     o = torch.empty_like(v) if out is None else _given(out, v)
+    log_a = _small(log_a, "lla_linear_forward_varlen", o, state_out)
+    cu_seqlens = _small(cu_seqlens, "lla_linear_forward_varlen", o, state_out)
     _call(load().lla_linear_forward_varlen(q.data_ptr(), k.data_ptr(), v.data_ptr(), log_a.data_ptr(), s0, o.data_ptr(),
                                            s1, cu_seqlens.data_ptr(), n, n0, H, total, int(max_T), dk, dv,
                                            torch._C._cuda_getCurrentRawStream(index), _dtype_code(q)),
@@ -559,6 +575,7 @@ def linear_backward(q, k, v, log_a, dout, state0=None, dstate_out=None, stream=N
     s1 = _state(dstate_out, "dstate_out", (B, H, dk, dv), device)
     dq, dk_, dv_ = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
     ds = None if state0 is None else torch.empty_like(state0)
+    log_a = _small(log_a, "lla_linear_backward")
     _call(load().lla_linear_backward(q.data_ptr(), k.data_ptr(), v.data_ptr(), log_a.data_ptr(), s0, dout.data_ptr(),
                                      s1, dq.data_ptr(), dk_.data_ptr(), dv_.data_ptr(),
                                      None if ds is None else ds.data_ptr(), B, B0, H, T, dk, dv,
@@ -588,6 +605,7 @@ def linear_decode_step(q, k, v, log_a, state, out=None, stream=None):
     if stream is not None or index != torch._C._cuda_getDevice():
         return _elsewhere(q.device, stream, linear_decode_step, q, k, v, log_a, state, out)
     o = torch.empty_like(v) if out is None else _given(out, v)
+    log_a = _small(log_a, "lla_linear_decode_step", o, state)
     _call(load().lla_linear_decode_step(q.data_ptr(), k.data_ptr(), v.data_ptr(), log_a.data_ptr(), state.data_ptr(),
                                         o.data_ptr(), torch._C._cuda_getCurrentRawStream(index), B, H, dk, dv,
                                         _dtype_code(q)), "lla_linear_decode_step")
@@ -636,9 +654,14 @@ def decode_step_shared(q, k, v, log_a, lam, prefix_states, prefix_len: int, pref
         return _elsewhere(q.device, stream, decode_step_shared, q, k, v, log_a, lam, prefix_states, prefix_len,
                           prefix_decay, states, t, out)
     o = torch.empty_like(v) if out is None else _given(out, v)
+    where, written = "lla_decode_step_shared", (o, states, prefix_decay)
+    decay = _small(prefix_decay, where, q, k, v, log_a, lam, prefix_states, states, t, o)
+    log_a, lam, t = _small(log_a, where, *written), _small(lam, where, *written), _small(t, where, *written)
     _call(load().lla_decode_step_shared(q.data_ptr(), k.data_ptr(), v.data_ptr(), log_a.data_ptr(), lam.data_ptr(),
-                                        prefix_states.data_ptr(), int(prefix_len), Lp, prefix_decay.data_ptr(),
+                                        prefix_states.data_ptr(), int(prefix_len), Lp, decay.data_ptr(),
                                         states.data_ptr(), t.data_ptr(), o.data_ptr(),
                                         torch._C._cuda_getCurrentRawStream(index), B, H, dk, dv, Lmax, _dtype_code(q)),
           "lla_decode_step_shared")
+    if decay is not prefix_decay:
+        prefix_decay.copy_(decay)
     return o

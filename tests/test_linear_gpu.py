@@ -661,3 +661,31 @@ def test_gradients_beside_a_busy_stream(lla, B, H, T, dk, dv):
             assert float(rel.max()) <= 5e-3, (n, int(rel.argmax()), float(rel.max()))
             assert torch.equal(x, y), n
     busy.synchronize()
+
+
+def test_a_rank_s_part_of_the_decays(lla):
+    """slopes[r h : (r + 1) h] begins at any multiple of 4 bytes, and so does a part of cu_seqlens: the same bits as from
+    tensors of their own."""
+    B, H, T, dk, dv = 2, 3, 200, 64, 64
+    for dtype in ("bf16", "f32"):
+        p = problem(B, 4 * H, T, dk, dv, dtype, B, seed=40)
+        cu = torch.tensor([7, 0, 60, B * T - 5], dtype=torch.int32, device="cuda")
+        for r in range(4):
+            heads = slice(r * H, (r + 1) * H)
+            part, whole = dev(p, "la")[heads], dev(p, "la")[heads].clone()
+            assert whole.data_ptr() % 16 == 0 and part.data_ptr() % 16 == (12 * r) % 16
+            q, k, v, do = (dev(p, n)[:, heads].contiguous() for n in ("q", "k", "v", "dout"))
+            s0 = dev(p, "s0")[:, heads].contiguous()
+            rows = [x.transpose(0, 1).reshape(H, B * T, -1).contiguous() for x in (q, k, v)]
+            tok = [x[:, :, 0].contiguous() for x in (q, k, v)]
+            got = []
+            for la, c in ((part, cu[1:]), (whole, cu[1:].clone())):
+                st, s1 = s0.clone(), torch.empty_like(s0)
+                got.append([lla.linear_forward(q, k, v, la, state0=s0, state_out=s1), s1,
+                            lla.linear_forward_varlen(*rows, la, c, B * T, out=torch.zeros_like(rows[2])),
+                            *lla.linear_backward(q, k, v, la, do, state0=s0),
+                            lla.linear_decode_step(*tok, la, st), st])
+            assert all(torch.equal(x, y) for x, y in zip(*got)), (dtype, r)
+    store = torch.zeros(B * H * 64 + 3, device="cuda")  # decays in the last bytes of the output
+    with pytest.raises(lla.LLAError):
+        lla.linear_decode_step(*tok, store[-H - 2:-2], st, out=store[:B * H * 64].view(B, H, 64))

@@ -261,3 +261,23 @@ def test_prefix_s_parts_are_those_of_the_call(lla):
         first = first or got
         assert all(torch.equal(o, f) for o, f in zip(got, first))
     busy.synchronize()
+
+
+def test_a_part_of_the_batch(lla):
+    """Sequences 1.. of a batch whose heads are odd in number: decay, decays of the step, lambda and positions begin
+    between the library's 16 bytes, and the decays are updated in place all the same."""
+    P, B, H, dk, dv, Lmax = 100, 4, 3, 64, 64, 9
+    d, prefix = build(lla, P, B, H, dk, dv, "f32", 3, Lmax, seed=2)
+    whole, part = [(torch.zeros(B, H, Lmax, dk, dv, device="cuda"), torch.full((B, H), 5.0, device="cuda")) for _ in "ab"]
+    for i in range(3):
+        t = torch.full((B,), P + i, dtype=torch.int64, device="cuda")
+        args, _ = step_args(d, i, t)
+        want = lla.decode_step_shared(*args, prefix, P, whole[1], whole[0], t)
+        q, k, v, a, lam = args
+        got = lla.decode_step_shared(q[1:].clone(), k[1:].clone(), v[1:].clone(), a[1:], lam[1:], prefix, P, part[1][1:],
+                                     part[0][1:], t[1:])
+        assert torch.equal(got, want[1:]) and torch.equal(part[1][1:], whole[1][1:])
+        assert torch.equal(part[0][1:], whole[0][1:]) and (part[1][0] == 5.0).all()
+    with pytest.raises(lla.LLAError):  # decays over the step's own
+        lla.decode_step_shared(q[1:].clone(), k[1:].clone(), v[1:].clone(), a[1:], lam[1:], prefix, P, a[1:],
+                               part[0][1:], t[1:])
