@@ -749,7 +749,10 @@ int lla_linear_forward_varlen(const void* q, const void* k, const void* v, const
                               void* out, float* state_out, const int32_t* cu_seqlens, int n_seq, int n0, int H,
                               int total_T, int max_T, int dk, int dv, void* stream, int dtype) {
     if (!cu_seqlens || !aligned16(cu_seqlens) || total_T < 1) return LLA_ERR_INVALID_ARG;
-    int st = validate_linear(q, k, v, log_a, state0, n_seq, n0, H, (int64_t)H * total_T, max_T, dk, dv, dtype);
+    // a bound above the rows that there are (a server's longest context, say) bounds nothing more: it must not count in the
+    // plan, nor turn a call away
+    const int longest = max_T < total_T ? max_T : total_T;
+    int st = validate_linear(q, k, v, log_a, state0, n_seq, n0, H, (int64_t)H * total_T, longest, dk, dv, dtype);
     if (st != LLA_OK) return st;
     if (!out || !aligned16(out) || !aligned16(state_out)) return LLA_ERR_INVALID_ARG;
     const size_t msz = (size_t)dk * dv * sizeof(float);
@@ -765,7 +768,7 @@ int lla_linear_forward_varlen(const void* q, const void* k, const void* v, const
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     lla::LinSeqs sq = {};
     sq.n = n_seq;
-    sq.T = max_T;
+    sq.T = longest;
     sq.H = H;
     sq.total = total_T;
     sq.n_chunks = total_T / 64 + n_seq;
@@ -773,7 +776,7 @@ int lla_linear_forward_varlen(const void* q, const void* k, const void* v, const
     PoolBuffer ws(s);
     lla::LinTcPlan tp;
     if (lla::linear_tc_supported(dtype, dk, dv) &&
-        lla::linear_tc_plan(&tp, n_seq, H, max_T, (int64_t)H * total_T, pieces64(dv), false)) {
+        lla::linear_tc_plan(&tp, n_seq, H, longest, (int64_t)H * total_T, pieces64(dv), false)) {
         if ((st = ws.take(dev, tab_b + 2 * off_b + tp.seg_bytes)) != LLA_OK) return st;
         int2* tab = reinterpret_cast<int2*>(ws.p);
         int* coff = reinterpret_cast<int*>(ws.p + tab_b);
@@ -781,7 +784,7 @@ int lla_linear_forward_varlen(const void* q, const void* k, const void* v, const
         sq.tab = tab;
         sq.coff = coff;
         sq.order = order;
-        cudaError_t e = lla::linear_table(cu_seqlens, n_seq, total_T, max_T, tab, coff, order, err, s);
+        cudaError_t e = lla::linear_table(cu_seqlens, n_seq, total_T, longest, tab, coff, order, err, s);
         const lla::LinTcMap maps[3] = {{q, dk}, {k, dk}, {v, dv}};
         const lla::LinTcScan scan = {0, 1, 2, out, state0, state_out, n0 == 1, 0, dk, dv, pieces64(dv), 0, 0};
         if (e == cudaSuccess)
@@ -795,7 +798,7 @@ int lla_linear_forward_varlen(const void* q, const void* k, const void* v, const
     float* states = reinterpret_cast<float*>(ws.p + tab_b + off_b);
     sq.tab = tab;
     sq.coff = coff;
-    cudaError_t e = lla::linear_table(cu_seqlens, n_seq, total_T, max_T, tab, coff, nullptr, err, s);
+    cudaError_t e = lla::linear_table(cu_seqlens, n_seq, total_T, longest, tab, coff, nullptr, err, s);
     lla::LinStateJobs jobs = {{{k, v, states, state0, state_out, n0 == 1, 0, dk, dv, pieces64(dk) * pieces64(dv)}}, 1};
     lla::LinScans scans = {{{q, k, v, out, states, 0, 0, dk, dv}}, 1};
     if (e == cudaSuccess) e = lla::linear_run(dtype, jobs, scans, sq, log_a, s);

@@ -689,3 +689,21 @@ def test_a_rank_s_part_of_the_decays(lla):
     store = torch.zeros(B * H * 64 + 3, device="cuda")  # decays in the last bytes of the output
     with pytest.raises(lla.LLAError):
         lla.linear_decode_step(*tok, store[-H - 2:-2], st, out=store[:B * H * 64].view(B, H, 64))
+
+
+@pytest.mark.parametrize("dtype,n", [("bf16", 3), ("bf16", 80), ("f32", 70)])
+def test_varlen_bounds_above_the_rows(lla, dtype, n):
+    """max_T beyond every row of the tensors is the same call as max_T of all of them, to the bit: a bound of 2^31 - 1
+    moved bf16 to the CUDA cores, and with 64 sequences or more was refused."""
+    H, dk, dv = 3, 64, 64
+    lengths = [(37 * b) % 150 for b in range(n)]
+    p, cu = pack(lengths, H, dk, dv, dtype, 0, 5, seed=n)
+    x = [dev(p, m) for m in ("q", "k", "v", "la")]
+    total, c = sum(lengths) + 5, torch.from_numpy(cu).cuda()
+    got = []
+    for most in (total, total + 1, 1 << 30, 2 ** 31 - 1):
+        s1 = torch.empty(n, H, dk, dv, device="cuda")
+        got.append((lla.linear_forward_varlen(*x, c, most, state_out=s1, out=torch.zeros_like(x[2])), s1))
+    check_packed(p, cu, host(got[0][0]), host(got[0][1]), dtype)
+    for a, b in got[1:]:
+        assert torch.equal(a, got[0][0]) and torch.equal(b, got[0][1])
