@@ -23,6 +23,8 @@
 // launches of 1.6 waves of CTAs (gradients of 3 x 5 heads, T = 1301, 96 x 80: 139 us; prompts of 2 x 16 heads, T = 4096,
 // 128 x 128: 415 us, 31 TFLOP/s counting whole squares). No exponent is ever
 // negative, so no factor overflows for g <= 1; g^0 is 1 also for g = 0 (log_a = -inf).
+#include <atomic>
+
 #include "lla_internal.cuh"
 #include "lla_linear.cuh"
 #include "lla_tc_ptx.cuh"
@@ -36,8 +38,27 @@ constexpr int kMulThreads = 128;  // 8 x 16 threads, each an 8 x 4 piece of a 64
 constexpr int kSlab = 32;         // summed indices staged at a time
 constexpr int kLd = kC + 4;    // leading dimension of the transposed tiles (16-byte rows)
 constexpr int kMaxD = 128;
-constexpr int kFull = 4 * 152;  // blocks of lin_out that fill the GPU once
+constexpr int kBlocksPerSm = 4;  // of lin_chunk_state and lin_out
 
+// blocks of lin_out that fill the current device once (asked once of a device)
+int64_t full_blocks() {
+    constexpr int kMaxDevices = 64;
+    static std::atomic<int> sms[kMaxDevices];
+    int dev = 0, n = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) {
+        cudaGetLastError();
+        return INT64_MAX;
+    }
+    n = sms[dev].load(std::memory_order_relaxed);
+    if (!n) {
+        if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
+            cudaGetLastError();
+            return INT64_MAX;
+        }
+        sms[dev].store(n, std::memory_order_relaxed);
+    }
+    return static_cast<int64_t>(n) * kBlocksPerSm;
+}
 
 // One 64-token chunk: its sequence's batch index, its rows and the place of its state.
 struct ChunkAt {
@@ -178,7 +199,7 @@ __device__ __forceinline__ void put(const Slab& s, float (*S)[kLd]) {
 
 // grid (chunks, H, pieces of 64 x 64 over every job), kMulThreads.
 template <typename T>
-__global__ void __launch_bounds__(kMulThreads, 4) lin_chunk_state(LinStateJobs jobs, LinSeqs sq, const float* log_a) {
+__global__ void __launch_bounds__(kMulThreads, kBlocksPerSm) lin_chunk_state(LinStateJobs jobs, LinSeqs sq, const float* log_a) {
     __shared__ __align__(16) float X[kSlab][kLd], Y[kSlab][kLd];
     __shared__ float w[kC];
     grid_dep_launch();
@@ -278,7 +299,7 @@ __global__ void __launch_bounds__(kThreads) lin_carry(LinStateJobs jobs, LinSeqs
 // pass through two small slabs (35 KB a block with the scores), so that several blocks share an SM; whole tiles in
 // shared memory left two.
 template <typename T>
-__global__ void __launch_bounds__(kMulThreads, 4) lin_out(LinScans scans, LinSeqs sq, const float* log_a) {
+__global__ void __launch_bounds__(kMulThreads, kBlocksPerSm) lin_out(LinScans scans, LinSeqs sq, const float* log_a) {
     __shared__ __align__(16) float X[kSlab][kLd], Y[kSlab][kLd], Pt[kC][kLd];
     __shared__ float pw[kC + 1];
     const int h = blockIdx.y, tid = threadIdx.x;
@@ -401,7 +422,7 @@ cudaError_t run_t(const LinStateJobs& jobs, const LinScans& scans, const LinSeqs
     // to an SM on the SMs that the others leave free (240 blocks: 56 us for the three kernels against 39; 2048: 422
     // against 428).
     const dim3 blocks(sq.n_chunks, sq.H, scans.count);
-    const bool beside = static_cast<int64_t>(blocks.x) * blocks.y * blocks.z >= kFull;
+    const bool beside = static_cast<int64_t>(blocks.x) * blocks.y * blocks.z >= full_blocks();
     auto launch = [&](auto kern, dim3 grid, int threads, const auto& what) {
         if (beside) return launch_pdl(kern, grid, dim3(threads), 0, stream, what, sq, log_a);
         kern<<<grid, threads, 0, stream>>>(what, sq, log_a);

@@ -167,3 +167,13 @@ def test_reference_gradients_are_the_differences(T):
                 d.append(loss(*x))
             # the loss is bilinear, so the central difference is exact but for roundings (1e-16 / 1e-5 of it)
             assert abs((d[0] - d[1]) / 2e-5 - g[at]) < 1e-8
+
+
+def test_no_rule_counts_on_one_chip():
+    """How many SMs there are is asked of the device: the count of one chip stands in comments only."""
+    import glob
+    import re
+    for path in glob.glob(os.path.join(build.CSRC, "lla_linear*.cu*")) + glob.glob(os.path.join(build.CSRC, "lla_shared.cu")):
+        with open(path) as f:
+            code = [line.split("//")[0] for line in f]
+        assert not [line for line in code if re.search(r"\b15[0-9]\b", line)], path
