@@ -329,9 +329,12 @@ int lla_gdn_forward_profile(const void* q, const void* k, const void* v, const f
  *   dk, dv 1..128. bf16 with dk and dv multiples of 8 runs on tensor cores (128-token chunks, bf16
  *   operands, fp32 accumulation, states in fp32); every other shape runs fp32 arithmetic on CUDA
  *   cores. Sums are formed in a fixed order: repeated calls give identical bits.
- * Tokens are mixed in chunks of 128 (64 on CUDA cores), so an infinity or NaN in v may reach the
- * other rows of its own chunk, as well as every later row; one in k or q obeys causality. Rows of
- * other sequences (and, packed, rows of no sequence) are never mixed in.
+ * Tokens are mixed in chunks of 128 (64 on CUDA cores): a chunk's tokens out of reach enter its
+ * last product with weight 0. So an infinity or NaN in v may reach the other rows of its own chunk,
+ * as well as every later row, in its own column; one in k or q obeys causality. Of the gradients,
+ * the same goes for one in k and dq, one in q and dk (every earlier row), one in dout and dv (every
+ * earlier row), and one in v obeys causality. An infinity may come out as NaN, in a state too. Rows
+ * of other sequences (and, packed, rows of no sequence) are never mixed in.
  *
  * lla_linear_forward: prompts of one length.
  *

@@ -707,3 +707,32 @@ def test_varlen_bounds_above_the_rows(lla, dtype, n):
     check_packed(p, cu, host(got[0][0]), host(got[0][1]), dtype)
     for a, b in got[1:]:
         assert torch.equal(a, got[0][0]) and torch.equal(b, got[0][1])
+
+
+@pytest.mark.parametrize("dtype,chunk", [("bf16", 128), ("f32", 64)])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_gradients_of_values_that_are_not_finite(lla, dtype, chunk, bad):
+    """One element (t, column 5) of each input: what depends on it is not finite, what may share its chunk is as the
+    header says, and every other element keeps its bits. dq_i = sum_{j <= i} (dO_i . v_j) k_j, dk_i = sum_{j >= i}
+    (v_i . dO_j) q_j, dv_i = sum_{j >= i} (k_i . q_j) dO_j."""
+    T, t, col, d = 500, 300, 5, 64
+    p = problem(1, 2, T, d, d, dtype, 0, seed=41)
+    clean = [lla.linear_backward(*(dev(p, n) for n in ("q", "k", "v", "la", "dout")))[i] for i in range(3)]
+    lo, hi = t // chunk * chunk, t // chunk * chunk + chunk
+    everywhere = slice(None)
+    # input: for dq, dk, dv the rows and columns that may change
+    reach = {"k": ((slice(lo, None), col), None, (slice(t, t + 1), everywhere)),
+             "q": (None, (slice(0, hi), col), (slice(0, t + 1), everywhere)),
+             "dout": ((slice(t, t + 1), everywhere), (slice(0, t + 1), everywhere), (slice(0, hi), col)),
+             "v": ((slice(t, None), everywhere), (slice(t, t + 1), everywhere), None)}
+    for name, may in reach.items():
+        x = {n: dev(p, n) for n in ("q", "k", "v", "la", "dout")}
+        x[name] = x[name].clone()
+        x[name][:, :, t, col] = bad
+        got = lla.linear_backward(*x.values())[:3]
+        for n, g, c, m in zip(("dq", "dk", "dv"), got, clean, may):
+            same = torch.ones(T, d, dtype=torch.bool, device="cuda")
+            if m is not None:
+                same[m] = False
+                assert not torch.isfinite(g[:, :, t][..., m[1]].float()).all(), (name, n)
+            assert torch.equal(g[:, :, same], c[:, :, same]), (name, n)
