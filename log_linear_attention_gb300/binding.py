@@ -105,12 +105,22 @@ def num_levels(T: int) -> int:
 
 
 _torch_module = None
+_current_device = _raw_stream = None  # the current device's index; the handle of a device's current stream
+
+
+def _cuda_calls(torch):
+    """(current device, current stream's handle), as torch's own bindings give them without building objects, or through
+    torch.cuda where a torch has no such bindings."""
+    device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+    stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    return device, stream or (lambda index: int(torch.cuda.current_stream(index).cuda_stream))
 
 
 def _torch():
-    global _torch_module
+    global _torch_module, _current_device, _raw_stream
     if _torch_module is None:
         import torch
+        _current_device, _raw_stream = _cuda_calls(torch)
         _torch_module = torch
     return _torch_module
 
@@ -505,7 +515,7 @@ def linear_forward(q, k, v, log_a, state0=None, state_out=None, out=None, stream
         _linear_inputs(("q", "k", "v"), (q, k, v), log_a, H)
         if k.shape != q.shape or v.shape != (B, H, T, dv):
             raise ValueError("shape mismatch between q, k and v")
-    if stream is not None or index != torch._C._cuda_getDevice():
+    if stream is not None or index != _current_device():
         return _elsewhere(device, stream, linear_forward, q, k, v, log_a, state0, state_out, out)
     B0 = 0 if state0 is None else int(state0.shape[0])
     s0 = _state(state0, "state0", (1 if B0 == 1 else B, H, dk, dv), device)
@@ -513,7 +523,7 @@ def linear_forward(q, k, v, log_a, state0=None, state_out=None, out=None, stream
     o = torch.empty_like(v) if out is None else _given(out, v)
     log_a = _small(log_a, "lla_linear_forward", o, state_out)
     _call(load().lla_linear_forward(q.data_ptr(), k.data_ptr(), v.data_ptr(), log_a.data_ptr(), s0, o.data_ptr(), s1, B,
-                                    B0, H, T, dk, dv, torch._C._cuda_getCurrentRawStream(index), _dtype_code(q)),
+                                    B0, H, T, dk, dv, _raw_stream(index), _dtype_code(q)),
           "lla_linear_forward")
     return o
 
@@ -539,7 +549,7 @@ def linear_forward_varlen(q, k, v, log_a, cu_seqlens, max_T: int, state0=None, s
             raise TypeError("cu_seqlens must be int32 [n+1]")
         if k.shape != q.shape or v.shape != (H, total, dv):
             raise ValueError("shape mismatch between packed q, k and v")
-    if stream is not None or index != torch._C._cuda_getDevice():
+    if stream is not None or index != _current_device():
         return _elsewhere(device, stream, linear_forward_varlen, q, k, v, log_a, cu_seqlens, max_T, state0, state_out,
                           out)
     n = cu_seqlens.numel() - 1
@@ -551,7 +561,7 @@ def linear_forward_varlen(q, k, v, log_a, cu_seqlens, max_T: int, state0=None, s
     cu_seqlens = _small(cu_seqlens, "lla_linear_forward_varlen", o, state_out)
     _call(load().lla_linear_forward_varlen(q.data_ptr(), k.data_ptr(), v.data_ptr(), log_a.data_ptr(), s0, o.data_ptr(),
                                            s1, cu_seqlens.data_ptr(), n, n0, H, total, int(max_T), dk, dv,
-                                           torch._C._cuda_getCurrentRawStream(index), _dtype_code(q)),
+                                           _raw_stream(index), _dtype_code(q)),
           "lla_linear_forward_varlen")
     return o
 
@@ -568,7 +578,7 @@ def linear_backward(q, k, v, log_a, dout, state0=None, dstate_out=None, stream=N
     _linear_inputs(("q", "k", "v", "dout"), (q, k, v, dout), log_a, H)
     if k.shape != q.shape or v.shape != (B, H, T, dv) or dout.shape != v.shape:
         raise ValueError("shape mismatch between q, k, v and dout")
-    if stream is not None or index != torch._C._cuda_getDevice():
+    if stream is not None or index != _current_device():
         return _elsewhere(device, stream, linear_backward, q, k, v, log_a, dout, state0, dstate_out)
     B0 = 0 if state0 is None else int(state0.shape[0])
     s0 = _state(state0, "state0", (1 if B0 == 1 else B, H, dk, dv), device)
@@ -579,7 +589,7 @@ def linear_backward(q, k, v, log_a, dout, state0=None, dstate_out=None, stream=N
     _call(load().lla_linear_backward(q.data_ptr(), k.data_ptr(), v.data_ptr(), log_a.data_ptr(), s0, dout.data_ptr(),
                                      s1, dq.data_ptr(), dk_.data_ptr(), dv_.data_ptr(),
                                      None if ds is None else ds.data_ptr(), B, B0, H, T, dk, dv,
-                                     torch._C._cuda_getCurrentRawStream(index), _dtype_code(q)), "lla_linear_backward")
+                                     _raw_stream(index), _dtype_code(q)), "lla_linear_backward")
     return dq, dk_, dv_, ds
 
 
@@ -602,12 +612,12 @@ def linear_decode_step(q, k, v, log_a, state, out=None, stream=None):
         if state is None:
             raise ValueError("state is needed")
         _state(state, "state", (B, H, dk, dv), q.device)
-    if stream is not None or index != torch._C._cuda_getDevice():
+    if stream is not None or index != _current_device():
         return _elsewhere(q.device, stream, linear_decode_step, q, k, v, log_a, state, out)
     o = torch.empty_like(v) if out is None else _given(out, v)
     log_a = _small(log_a, "lla_linear_decode_step", o, state)
     _call(load().lla_linear_decode_step(q.data_ptr(), k.data_ptr(), v.data_ptr(), log_a.data_ptr(), state.data_ptr(),
-                                        o.data_ptr(), torch._C._cuda_getCurrentRawStream(index), B, H, dk, dv,
+                                        o.data_ptr(), _raw_stream(index), B, H, dk, dv,
                                         _dtype_code(q)), "lla_linear_decode_step")
     return o
 
@@ -650,7 +660,7 @@ def decode_step_shared(q, k, v, log_a, lam, prefix_states, prefix_len: int, pref
         _state(states, "states", (B, H, Lmax, dk, dv), q.device)
         if lam.shape != (B, H, Lmax) or log_a.shape != (B, H) or k.shape != q.shape or v.shape != (B, H, dv):
             raise ValueError("shape mismatch in decode inputs")
-    if stream is not None or index != torch._C._cuda_getDevice():
+    if stream is not None or index != _current_device():
         return _elsewhere(q.device, stream, decode_step_shared, q, k, v, log_a, lam, prefix_states, prefix_len,
                           prefix_decay, states, t, out)
     o = torch.empty_like(v) if out is None else _given(out, v)
@@ -660,7 +670,7 @@ def decode_step_shared(q, k, v, log_a, lam, prefix_states, prefix_len: int, pref
     _call(load().lla_decode_step_shared(q.data_ptr(), k.data_ptr(), v.data_ptr(), log_a.data_ptr(), lam.data_ptr(),
                                         prefix_states.data_ptr(), int(prefix_len), Lp, decay.data_ptr(),
                                         states.data_ptr(), t.data_ptr(), o.data_ptr(),
-                                        torch._C._cuda_getCurrentRawStream(index), B, H, dk, dv, Lmax, _dtype_code(q)),
+                                        _raw_stream(index), B, H, dk, dv, Lmax, _dtype_code(q)),
           "lla_decode_step_shared")
     if decay is not prefix_decay:
         prefix_decay.copy_(decay)

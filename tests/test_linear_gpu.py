@@ -736,3 +736,23 @@ def test_gradients_of_values_that_are_not_finite(lla, dtype, chunk, bad):
                 same[m] = False
                 assert not torch.isfinite(g[:, :, t][..., m[1]].float()).all(), (name, n)
             assert torch.equal(g[:, :, same], c[:, :, same]), (name, n)
+
+
+def test_without_torch_s_private_calls(lla, monkeypatch):
+    """The public calls name the same device and stream: the same bits, on a stream of its own too."""
+    from types import SimpleNamespace as N
+    p = problem(2, 3, 200, 64, 64, "bf16", 0, seed=42)
+    x = [dev(p, n) for n in ("q", "k", "v", "la")]
+    want = lla.linear_forward(*x)
+    device, stream = lla._cuda_calls(N(_C=N(), cuda=torch.cuda))
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        assert device() == lla._current_device() and stream(device()) == lla._raw_stream(device()) == side.cuda_stream
+    monkeypatch.setattr(lla, "_current_device", device)
+    monkeypatch.setattr(lla, "_raw_stream", stream)
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        got = lla.linear_forward(*x)
+    given = lla.linear_forward(*x, stream=side)
+    side.synchronize()
+    assert torch.equal(got, want) and torch.equal(given, want)

@@ -177,3 +177,13 @@ def test_no_rule_counts_on_one_chip():
         with open(path) as f:
             code = [line.split("//")[0] for line in f]
         assert not [line for line in code if re.search(r"\b15[0-9]\b", line)], path
+
+
+def test_binding_does_without_torch_s_private_calls():
+    from types import SimpleNamespace as N
+    cuda = N(current_device=lambda: 3, current_stream=lambda index: N(cuda_stream=100 + index))
+    device, stream = binding._cuda_calls(N(_C=N(), cuda=cuda))
+    assert device() == 3 and stream(2) == 102
+    device, stream = binding._cuda_calls(N(_C=N(_cuda_getDevice=lambda: 1, _cuda_getCurrentRawStream=lambda i: 7 + i),
+                                           cuda=cuda))
+    assert device() == 1 and stream(2) == 9
