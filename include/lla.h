@@ -356,9 +356,11 @@ int lla_gdn_forward_profile(const void* q, const void* k, const void* v, const f
  *   place (S_{t-1} on entry, S_t on return; what lla_linear_forward leaves in state_out). q, k
  *   [B,H,dk], v, out [B,H,dv] dtype.
  *
- * Workspace comes from the library's stream-ordered pool. Errors: LLA_ERR_INVALID_ARG /
- * LLA_ERR_UNSUPPORTED before any launch, LLA_ERR_NOMEM if the pool cannot grow, LLA_ERR_CUDA on a
- * launch failure; a bounded wait that runs out is reported by lla_device_error as LLA_ERR_TIMEOUT.
+ * Workspace comes from the library's stream-ordered pool: at most 0.5 GiB for the pieces of a
+ * tensor-core call (gradients keep 256 bytes for each row and 64 columns of v besides); on CUDA
+ * cores the states of 64-token chunks, 1 GiB of them or one head's at a time. Errors:
+ * LLA_ERR_INVALID_ARG / LLA_ERR_UNSUPPORTED before any launch, LLA_ERR_NOMEM if the pool cannot
+ * grow, LLA_ERR_CUDA on a launch failure; a bounded wait that runs out is reported by lla_device_error as LLA_ERR_TIMEOUT.
  */
 int lla_linear_forward(const void* q, const void* k, const void* v, const float* log_a, const float* state0, void* out,
                        float* state_out, int B, int B0, int H, int T, int dk, int dv, void* stream, int dtype);

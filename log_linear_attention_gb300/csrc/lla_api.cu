@@ -701,13 +701,32 @@ size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 lla::LinSeqs dense_seqs(int B, int H, int T) {
     lla::LinSeqs sq = {};
     sq.T = T;
-    sq.H = H;
+    sq.H = sq.state_heads = H;
     sq.N = (T - 1) / 64 + 1;
     sq.n_chunks = B * sq.N;
     return sq;
 }
 
 int pieces64(int d) { return (d + 63) / 64; }
+
+// The CUDA-core path keeps the state of every 64-token chunk of the heads that it runs together: as many heads as stay
+// within kMostStates bytes (at least one), so that a long prompt of many heads does not take all its states at once. 1 GiB
+// is 16384 states of 128 x 128, 100 times what fills the GPU.
+constexpr size_t kMostStates = size_t(1) << 30;
+struct HeadGroups {
+    int nb, nh;  // sequences and heads of a group: whole sequences, or some heads of one
+};
+HeadGroups head_groups(int B, int H, size_t head_bytes) {
+    const size_t most = kMostStates / head_bytes;
+    const size_t b = most / H;
+    if (b >= 1) return {b < static_cast<size_t>(B) ? static_cast<int>(b) : B, H};
+    return {1, most > 1 ? static_cast<int>(most) : 1};
+}
+
+const void* further(const void* p, size_t bytes) { return static_cast<const char*>(p) + bytes; }
+void* further(void* p, size_t bytes) { return static_cast<char*>(p) + bytes; }
+const float* states_at(const float* p, size_t n) { return p ? p + n : nullptr; }
+float* states_at(float* p, size_t n) { return p ? p + n : nullptr; }
 
 }  // namespace
 
@@ -738,11 +757,23 @@ int lla_linear_forward(const void* q, const void* k, const void* v, const float*
         return ws.give(lla::linear_tc_run(tp, maps, 3, &scan, 1, sq, log_a, reinterpret_cast<float*>(ws.p), nullptr,
                                           err, s));
     }
-    if ((st = ws.take(dev, (size_t)H * sq.n_chunks * msz)) != LLA_OK) return st;
+    const HeadGroups gr = head_groups(B, H, sq.N * msz);
+    if ((st = ws.take(dev, (size_t)gr.nb * gr.nh * sq.N * msz)) != LLA_OK) return st;
     float* states = reinterpret_cast<float*>(ws.p);
-    lla::LinStateJobs jobs = {{{k, v, states, state0, state_out, B0 == 1, 0, dk, dv, pieces64(dk) * pieces64(dv)}}, 1};
-    lla::LinScans scans = {{{q, k, v, out, states, 0, 0, dk, dv}}, 1};
-    return ws.give(lla::linear_run(dtype, jobs, scans, sq, log_a, s));
+    const size_t ek = (size_t)T * dk * type_bytes(dtype), ev = (size_t)T * dv * type_bytes(dtype), ms = (size_t)dk * dv;
+    cudaError_t e = cudaSuccess;
+    for (int b = 0; b < B && e == cudaSuccess; b += gr.nb)
+        for (int h = 0; h < H && e == cudaSuccess; h += gr.nh) {
+            const int nb = B - b < gr.nb ? B - b : gr.nb, nh = H - h < gr.nh ? H - h : gr.nh;
+            const size_t at = (size_t)b * H + h;
+            const void *kg = further(k, at * ek), *vg = further(v, at * ev);
+            lla::LinStateJobs jobs = {{{kg, vg, states, states_at(state0, (B0 == 1 ? h : at) * ms),
+                                        states_at(state_out, at * ms), B0 == 1, 0, dk, dv, pieces64(dk) * pieces64(dv)}},
+                                      1};
+            lla::LinScans scans = {{{further(q, at * ek), kg, vg, further(out, at * ev), states, 0, 0, dk, dv}}, 1};
+            e = lla::linear_run(dtype, jobs, scans, dense_seqs(nb, nh, T), log_a + h, s);
+        }
+    return ws.give(e);
 }
 
 int lla_linear_forward_varlen(const void* q, const void* k, const void* v, const float* log_a, const float* state0,
@@ -769,7 +800,7 @@ int lla_linear_forward_varlen(const void* q, const void* k, const void* v, const
     lla::LinSeqs sq = {};
     sq.n = n_seq;
     sq.T = longest;
-    sq.H = H;
+    sq.H = sq.state_heads = H;
     sq.total = total_T;
     sq.n_chunks = total_T / 64 + n_seq;
     const size_t tab_b = up256((size_t)n_seq * sizeof(int2)), off_b = up256(((size_t)n_seq + 1) * sizeof(int));
@@ -792,16 +823,25 @@ int lla_linear_forward_varlen(const void* q, const void* k, const void* v, const
                                    reinterpret_cast<float*>(ws.p + tab_b + 2 * off_b), nullptr, err, s);
         return ws.give(e);
     }
-    if ((st = ws.take(dev, tab_b + off_b + (size_t)H * sq.n_chunks * msz)) != LLA_OK) return st;
+    const int group = head_groups(1, H, sq.n_chunks * msz).nh;
+    if ((st = ws.take(dev, tab_b + off_b + (size_t)group * sq.n_chunks * msz)) != LLA_OK) return st;
     int2* tab = reinterpret_cast<int2*>(ws.p);
     int* coff = reinterpret_cast<int*>(ws.p + tab_b);
     float* states = reinterpret_cast<float*>(ws.p + tab_b + off_b);
     sq.tab = tab;
     sq.coff = coff;
     cudaError_t e = lla::linear_table(cu_seqlens, n_seq, total_T, longest, tab, coff, nullptr, err, s);
-    lla::LinStateJobs jobs = {{{k, v, states, state0, state_out, n0 == 1, 0, dk, dv, pieces64(dk) * pieces64(dv)}}, 1};
-    lla::LinScans scans = {{{q, k, v, out, states, 0, 0, dk, dv}}, 1};
-    if (e == cudaSuccess) e = lla::linear_run(dtype, jobs, scans, sq, log_a, s);
+    const size_t ek = (size_t)total_T * dk * type_bytes(dtype), ev = (size_t)total_T * dv * type_bytes(dtype);
+    for (int h = 0; h < H && e == cudaSuccess; h += group) {
+        const void *kg = further(k, h * ek), *vg = further(v, h * ev);
+        const size_t at = (size_t)h * dk * dv;
+        sq.H = H - h < group ? H - h : group;
+        lla::LinStateJobs jobs = {{{kg, vg, states, states_at(state0, at), states_at(state_out, at), n0 == 1, 0, dk, dv,
+                                    pieces64(dk) * pieces64(dv)}},
+                                  1};
+        lla::LinScans scans = {{{further(q, h * ek), kg, vg, further(out, h * ev), states, 0, 0, dk, dv}}, 1};
+        e = lla::linear_run(dtype, jobs, scans, sq, log_a + h, s);
+    }
     return ws.give(e);
 }
 
@@ -848,20 +888,33 @@ int lla_linear_backward(const void* q, const void* k, const void* v, const float
         if (e == cudaSuccess && sum) e = lla::linear_sum_batch(parts, dstate0, B, (int64_t)H * dk_ * dv_, s);
         return ws.give(e);
     }
-    const size_t st_b = up256((size_t)H * sq.n_chunks * msz);
+    const HeadGroups gr = head_groups(B, H, 2 * sq.N * msz);
+    const size_t st_b = up256((size_t)gr.nb * gr.nh * sq.N * msz);
     if ((st = ws.take(dev, 2 * st_b + (sum ? (size_t)B * H * msz : 0))) != LLA_OK) return st;
     float* fw = reinterpret_cast<float*>(ws.p);
     float* bw = reinterpret_cast<float*>(ws.p + st_b);
     float* parts = reinterpret_cast<float*>(ws.p + 2 * st_b);
     const int sp = pieces64(dk_) * pieces64(dv_);
-    lla::LinStateJobs jobs = {{{k, v, fw, state0, nullptr, B0 == 1, 0, dk_, dv_, sp},
-                               {q, dout, bw, dstate_out, sum ? parts : dstate0, 0, 1, dk_, dv_, sp}},
-                              2};
-    lla::LinScans scans = {{{dout, v, k, dq, fw, 1, 0, dv_, dk_},
-                            {v, dout, q, dk, bw, 1, 1, dv_, dk_},
-                            {k, q, dout, dv, bw, 0, 1, dk_, dv_}},
-                           3};
-    cudaError_t e = lla::linear_run(dtype, jobs, scans, sq, log_a, s);
+    const size_t ek = (size_t)T * dk_ * type_bytes(dtype), ev = (size_t)T * dv_ * type_bytes(dtype),
+                 ms = (size_t)dk_ * dv_;
+    cudaError_t e = cudaSuccess;
+    for (int b = 0; b < B && e == cudaSuccess; b += gr.nb)
+        for (int h = 0; h < H && e == cudaSuccess; h += gr.nh) {
+            const int nb = B - b < gr.nb ? B - b : gr.nb, nh = H - h < gr.nh ? H - h : gr.nh;
+            const size_t at = (size_t)b * H + h;
+            const void *qg = further(q, at * ek), *kg = further(k, at * ek), *vg = further(v, at * ev),
+                       *og = further(dout, at * ev);
+            lla::LinStateJobs jobs = {{{kg, vg, fw, states_at(state0, (B0 == 1 ? h : at) * ms), nullptr, B0 == 1, 0, dk_,
+                                        dv_, sp},
+                                       {qg, og, bw, states_at(dstate_out, at * ms),
+                                        states_at(sum ? parts : dstate0, at * ms), 0, 1, dk_, dv_, sp}},
+                                      2};
+            lla::LinScans scans = {{{og, vg, kg, further(dq, at * ek), fw, 1, 0, dv_, dk_},
+                                    {vg, og, qg, further(dk, at * ek), bw, 1, 1, dv_, dk_},
+                                    {kg, qg, og, further(dv, at * ev), bw, 0, 1, dk_, dv_}},
+                                   3};
+            e = lla::linear_run(dtype, jobs, scans, dense_seqs(nb, nh, T), log_a + h, s);
+        }
     if (e == cudaSuccess && sum) e = lla::linear_sum_batch(parts, dstate0, B, (int64_t)H * dk_ * dv_, s);
     return ws.give(e);
 }

@@ -272,7 +272,7 @@ __global__ void __launch_bounds__(kThreads) lin_carry(LinStateJobs jobs, LinSeqs
     const int N = static_cast<int>((static_cast<unsigned>(len) + kC - 1) / kC);  // len may be 2^31 - 1
     const float la = log_a[h];
     const float gC = gpow(la, kC), gl = gpow(la, len - (N - 1) * kC);
-    float x = jb.in ? jb.in[(static_cast<int64_t>(jb.in_shared ? 0 : b) * sq.H + h) * msz + e] : 0.f;
+    float x = jb.in ? jb.in[(static_cast<int64_t>(jb.in_shared ? 0 : b) * sq.state_heads + h) * msz + e] : 0.f;
     float* s = jb.states + (static_cast<int64_t>(h) * sq.n_chunks + first) * msz + e;
     // eight chunks' loads in flight
     for (int c0 = 0; c0 < N; c0 += 8) {
@@ -292,7 +292,7 @@ __global__ void __launch_bounds__(kThreads) lin_carry(LinStateJobs jobs, LinSeqs
             }
         }
     }
-    if (jb.out) jb.out[(static_cast<int64_t>(b) * sq.H + h) * msz + e] = x;
+    if (jb.out) jb.out[(static_cast<int64_t>(b) * sq.state_heads + h) * msz + e] = x;
 }
 
 // grid (chunks, H, scans), kMulThreads. The weighted scores are formed once and serve every 64 columns of c. Operands

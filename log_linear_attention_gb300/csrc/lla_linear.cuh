@@ -45,6 +45,7 @@ struct LinSeqs {
     int n, T, H, total;
     int N;             // dense: 64-token chunks of a sequence
     int n_chunks;      // 64-token chunks of one head (packed: at most)
+    int state_heads;   // heads of the states that enter and leave (packed: H may be a part of them)
 };
 
 // A chunk-state job of the CUDA-core path: states [H][n_chunks][d1][d2] of sum w b c^T.

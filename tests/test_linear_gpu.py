@@ -756,3 +756,88 @@ def test_without_torch_s_private_calls(lla, monkeypatch):
     given = lla.linear_forward(*x, stream=side)
     side.synchronize()
     assert torch.equal(got, want) and torch.equal(given, want)
+
+
+@pytest.mark.parametrize("B,H,T,dk,dv,dtype,B0", [(1, 64, 20001, 128, 128, "f32", 1), (5, 22, 18000, 128, 127, "bf16", 5),
+                                                  (3, 40, 20001, 126, 128, "f32", 1)])
+def test_long_prompts_of_many_heads_in_groups(lla, B, H, T, dk, dv, dtype, B0):
+    """More chunk states than the CUDA-core path keeps at a time: each head has the bits of a call of its own, whole
+    sequences to a group and parts of one."""
+    g = torch.Generator(device="cuda").manual_seed(T)
+    rand = lambda *s: torch.randn(*s, generator=g, device="cuda")  # noqa: E731
+    t = torch.bfloat16 if dtype == "bf16" else torch.float32
+    q, k = (rand(B, H, T, dk).mul_(dk ** -0.5).to(t) for _ in range(2))
+    v, do = (rand(B, H, T, dv).to(t) for _ in range(2))
+    la = -torch.exp2(-8.0 * torch.arange(1, H + 1, device="cuda") / H)
+    s0, ds, s1 = rand(B0, H, dk, dv), rand(B, H, dk, dv), torch.empty(B, H, dk, dv, device="cuda")
+    out = lla.linear_forward(q, k, v, la, state0=s0, state_out=s1)
+    grads = lla.linear_backward(q, k, v, la, do, state0=s0, dstate_out=ds)
+    cut = lambda x, b, h: x[min(b, x.shape[0] - 1), h][None, None].clone()  # noqa: E731
+    # parts of the gradient of a shared state, summed in order as the call does
+    total = torch.zeros_like(s0) if B0 == 1 else None
+    for b in range(B):
+        for h in range(H):
+            if B0 > 1 and (h, b) not in ((0, 0), (1, 1), (H - 1, 2), (H // 2, 3), (3, 4), (H - 1, 4)):
+                continue
+            x = [cut(y, b, h) for y in (q, k, v)]
+            a = la[h:h + 1].clone()
+            mine = lla.linear_backward(*x, a, cut(do, b, h), state0=cut(s0, b, h), dstate_out=cut(ds, b, h))
+            if B0 == 1:
+                total[0, h] += mine[3][0, 0]
+            else:
+                assert torch.equal(mine[3][0, 0], grads[3][b, h]), (b, h)
+            for got, want in zip(grads[:3], mine[:3]):
+                assert torch.equal(got[b, h], want[0, 0]), (b, h)
+            if (b + h) % 7 == 0 or h in (0, H - 1):
+                s = torch.empty(1, 1, dk, dv, device="cuda")
+                o = lla.linear_forward(*x, a, state0=cut(s0, b, h), state_out=s)
+                assert torch.equal(out[b, h], o[0, 0]) and torch.equal(s1[b, h], s[0, 0]), (b, h)
+    if B0 == 1:
+        assert torch.equal(total, grads[3])
+
+
+def test_packed_rows_of_many_heads_in_groups(lla):
+    H, dk, dv, lengths = 64, 128, 126, [9000, 0, 7001, 1, 4000]
+    total, n = sum(lengths) + 3, len(lengths)
+    g = torch.Generator(device="cuda").manual_seed(3)
+    rand = lambda *s: torch.randn(*s, generator=g, device="cuda")  # noqa: E731
+    q, k, v = (rand(H, total, d) for d in (dk, dk, dv))
+    la = -torch.exp2(-8.0 * torch.arange(1, H + 1, device="cuda") / H)
+    cu = torch.tensor(np.concatenate([[0], np.cumsum(lengths)]).astype(np.int32)).cuda()
+    for s0 in (rand(n, H, dk, dv), rand(1, H, dk, dv), None):
+        s1, out = torch.empty(n, H, dk, dv, device="cuda"), torch.full((H, total, dv), 7.0, device="cuda")
+        lla.linear_forward_varlen(q, k, v, la, cu, 9000, state0=s0, state_out=s1, out=out)
+        for h in (0, 1, 50, 51, 52, 53, H - 1):
+            s, o = torch.empty(n, 1, dk, dv, device="cuda"), torch.full((1, total, dv), 7.0, device="cuda")
+            lla.linear_forward_varlen(q[h:h + 1].clone(), k[h:h + 1].clone(), v[h:h + 1].clone(), la[h:h + 1], cu, 9000,
+                                      state0=None if s0 is None else s0[:, h:h + 1].contiguous(), state_out=s, out=o)
+            assert torch.equal(out[h], o[0]) and torch.equal(s1[:, h], s[:, 0]), h
+
+
+MEMORY = """
+import torch
+from log_linear_attention_gb300 import binding as lla
+q, k, v, do = (torch.randn(1, 64, 40000, 128, device="cuda") for _ in range(4))
+la, out = -torch.rand(64, device="cuda"), torch.empty_like(v)
+outs = [torch.empty_like(q) for _ in range(3)]
+del outs  # torch keeps the memory for the gradients
+lla.linear_forward(q[:, :1, :64].contiguous(), q[:, :1, :64].contiguous(), q[:, :1, :64].contiguous(), la[:1])
+torch.cuda.synchronize()
+free = torch.cuda.mem_get_info()[0]
+lla.linear_forward(q, k, v, la, out=out)
+lla.linear_backward(q, k, v, la, do)
+torch.cuda.synchronize()
+taken = free - torch.cuda.mem_get_info()[0]
+assert lla.device_error() == 0 and taken <= (1 << 30) + (64 << 20), taken
+print("kept within", taken)
+"""
+
+
+def test_long_prompts_keep_their_workspace_within_a_bound():
+    """64 heads, T = 40000, 128 x 128 in fp32: 2.6 GB of chunk states forwards and twice that backwards, 1 GiB at a time."""
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", MEMORY], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "kept within" in r.stdout, r.stderr[-2000:]
