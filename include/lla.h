@@ -360,7 +360,8 @@ int lla_gdn_forward_profile(const void* q, const void* k, const void* v, const f
  * tensor-core call (gradients keep 256 bytes for each row and 64 columns of v besides); on CUDA
  * cores the states of 64-token chunks, 1 GiB of them or one head's at a time. Errors:
  * LLA_ERR_INVALID_ARG / LLA_ERR_UNSUPPORTED before any launch, LLA_ERR_NOMEM if the pool cannot
- * grow, LLA_ERR_CUDA on a launch failure; a bounded wait that runs out is reported by lla_device_error as LLA_ERR_TIMEOUT.
+ * grow, LLA_ERR_CUDA on a launch failure; a bounded wait that runs out is reported by
+ * lla_device_error as LLA_ERR_TIMEOUT.
  */
 int lla_linear_forward(const void* q, const void* k, const void* v, const float* log_a, const float* state0, void* out,
                        float* state_out, int B, int B0, int H, int T, int dk, int dv, void* stream, int dtype);

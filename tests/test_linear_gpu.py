@@ -841,3 +841,53 @@ def test_long_prompts_keep_their_workspace_within_a_bound():
     root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
     r = subprocess.run([sys.executable, "-c", MEMORY], cwd=root, capture_output=True, text=True, timeout=300)
     assert r.returncode == 0 and "kept within" in r.stdout, r.stderr[-2000:]
+
+
+@pytest.mark.parametrize("n", [1024, 1025, 2500])
+@pytest.mark.parametrize("dtype,dk", [("bf16", 64), ("f32", 20)])
+def test_varlen_more_sequences_than_a_block_has_threads(dtype, dk, n):
+    """The table of the sequences is made in rounds of 1024: lengths of zero and more, a few long ones, and bounds that
+    break the rules on both sides of a round's end."""
+    from log_linear_attention_gb300 import binding as lla
+    H, dv = 2, 32
+    r = np.random.default_rng(n)
+    lengths = [int(x) for x in r.integers(0, 12, n)]
+    for b in (5, 1022, n - 1):
+        lengths[b] = 300 + b % 7
+    p, cu = pack(lengths, H, dk, dv, dtype, 0, 40, seed=n)
+    total = sum(lengths) + 40
+    x = [dev(p, m) for m in ("q", "k", "v", "la")]
+    for spoil in ((), (700, 1023) if n == 1024 else (700, 1023, 1024)):
+        bounds, skip = cu.copy(), set()
+        for b in spoil:  # sequence b - 1 ends past the tensors, b begins there: both are out
+            bounds[b] = total + 1 + b
+            skip |= {b - 1, b}
+        # whatever begins below a bound that came before it is out too
+        high = np.maximum.accumulate(bounds)
+        skip |= {b for b in range(n) if bounds[b] < high[b] or bounds[b + 1] < bounds[b] or bounds[b + 1] > total}
+        s1 = torch.full((n, H, dk, dv), 3.0, device="cuda")
+        out = torch.full((H, total, dv), 7.0, device="cuda", dtype=x[2].dtype)
+        lla.linear_forward_varlen(*x, torch.from_numpy(bounds).cuda(), 400, state_out=s1, out=out)
+        assert lla.device_error() == (lla.LLA_ERR_DEVICE if spoil else 0)
+        o, s = host(out), host(s1)
+        check_packed(p, bounds, o, s, dtype, skip=skip)
+        covered = np.zeros(total, dtype=bool)
+        for b in range(n):
+            if b in skip:
+                assert (s[b] == 3.0).all(), b
+            else:
+                covered[bounds[b]:bounds[b + 1]] = True
+        assert (o[:, ~covered] == 7.0).all()
+
+
+@pytest.mark.parametrize("lengths,dk,dv,dtype,n0", [([5000, 3, 2701, 64, 0, 4097], 64, 64, "f32", 6),
+                                                    ([3000, 1, 2999], 36, 100, "f32", 1),
+                                                    ([4000, 129], 50, 33, "bf16", 2), ([6000, 5, 4100], 128, 64, "bf16", 3)])
+def test_varlen_of_many_chunks(lla, lengths, dk, dv, dtype, n0):
+    p, cu = pack(lengths, 3, dk, dv, dtype, n0, 17, seed=len(lengths))
+    s1 = torch.empty(len(lengths), 3, dk, dv, device="cuda")
+    out = torch.full((3, sum(lengths) + 17, dv), 7.0, device="cuda", dtype=p["q"][1].dtype)
+    lla.linear_forward_varlen(*(dev(p, m) for m in ("q", "k", "v", "la")), torch.from_numpy(cu).cuda(), max(lengths),
+                              state0=dev(p, "s0"), state_out=s1, out=out)
+    check_packed(p, cu, host(out), host(s1), dtype)
+    assert (host(out)[:, cu[-1]:] == 7.0).all()

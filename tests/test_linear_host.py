@@ -187,3 +187,30 @@ def test_binding_does_without_torch_s_private_calls():
     device, stream = binding._cuda_calls(N(_C=N(_cuda_getDevice=lambda: 1, _cuda_getCurrentRawStream=lambda i: 7 + i),
                                            cuda=cuda))
     assert device() == 1 and stream(2) == 9
+
+
+def test_calls_for_another_device_or_stream_run_there(monkeypatch):
+    """What a call allocates belongs to the stream that writes it: device first, then stream, and a stream of another
+    device is refused."""
+    from contextlib import contextmanager
+    from types import SimpleNamespace as N
+    now = []
+
+    def entered(kind):
+        @contextmanager
+        def inside(x):
+            now.append((kind, x))
+            try:
+                yield
+            finally:
+                now.pop()
+        return inside
+
+    monkeypatch.setattr(binding, "_torch", lambda: N(cuda=N(device=entered("device"), stream=entered("stream"))))
+    seen = lambda *args: (tuple(now), args)  # noqa: E731
+    side = N(device="cuda:1")
+    assert binding._elsewhere("cuda:1", None, seen, 1, 2) == ((("device", "cuda:1"),), (1, 2))
+    assert binding._elsewhere("cuda:1", side, seen, 3) == ((("device", "cuda:1"), ("stream", side)), (3,))
+    with pytest.raises(ValueError, match="cuda:1"):
+        binding._elsewhere("cuda:0", side, seen)
+    assert not now
