@@ -891,3 +891,88 @@ def test_varlen_of_many_chunks(lla, lengths, dk, dv, dtype, n0):
                               state0=dev(p, "s0"), state_out=s1, out=out)
     check_packed(p, cu, host(out), host(s1), dtype)
     assert (host(out)[:, cu[-1]:] == 7.0).all()
+
+
+def test_outputs_given_and_streams_given(lla):
+    """Every call with its output tensor and its stream named, against the same call without, to the bit."""
+    B, H, T, dk, dv = 2, 3, 300, 64, 64
+    p = problem(B, H, T, dk, dv, "bf16", B, seed=50)
+    q, k, v, la, do, s0, ds = (dev(p, n) for n in ("q", "k", "v", "la", "dout", "s0", "ds"))
+    rows = [x.transpose(0, 1).reshape(H, B * T, -1).contiguous() for x in (q, k, v)]
+    cu = torch.tensor([0, 200, B * T], dtype=torch.int32, device="cuda")
+    tok = [x[:, :, 0].contiguous() for x in (q, k, v)]
+    lam, pre = torch.rand(B, H, 9, device="cuda"), torch.randn(H, 8, dk, dv, device="cuda")
+    t = torch.full((B,), 100, dtype=torch.int64, device="cuda")
+
+    def calls(stream, given):
+        new = lambda like: torch.zeros_like(like) if given else None  # noqa: E731
+        st, own, decay = s0.clone(), torch.zeros(B, H, 9, dk, dv, device="cuda"), torch.zeros(B, H, device="cuda")
+        outs = [new(v), new(rows[2]), new(tok[2]), new(tok[2])]
+        s1, s2 = torch.empty_like(s0), torch.empty_like(s0)
+        if stream is not None:
+            stream.wait_stream(torch.cuda.current_stream())
+        got = [lla.linear_forward(q, k, v, la, state0=s0, state_out=s1, out=outs[0], stream=stream),
+               lla.linear_forward_varlen(*rows, la, cu, B * T, state0=s0, state_out=s2, out=outs[1], stream=stream),
+               lla.linear_decode_step(*tok, la, st, out=outs[2], stream=stream),
+               lla.decode_step_shared(*tok, -la[None].expand(B, H).abs().contiguous().clamp(max=2.0), lam, pre, 100, decay,
+                                      own, t, out=outs[3], stream=stream)]
+        grads = lla.linear_backward(q, k, v, la, do, state0=s0, dstate_out=ds, stream=stream)
+        torch.cuda.synchronize()
+        if given:
+            assert all(a is b for a, b in zip(got, outs))
+        return [*got, *grads, s1, s2, st, decay, own[:, :, 0].clone()]
+
+    want = calls(None, False)
+    for stream, given in ((None, True), (torch.cuda.Stream(), False), (torch.cuda.Stream(), True)):
+        for i, (a, b) in enumerate(zip(calls(stream, given), want)):
+            assert torch.equal(a, b), i
+
+
+def test_offsets_past_32_bits(lla):
+    """Tensors of more than 2^31 elements: the first and the last head against fp32 arithmetic on that head alone (5e-3
+    of its norm, see tests/_linear.py); token steps to the bit."""
+    B, H, T, d = 33, 64, 16400, 64
+    assert B * H * T * d > 2 ** 31
+    g = torch.Generator(device="cuda").manual_seed(7)
+    rand = lambda *s: torch.randn(*s, generator=g, device="cuda", dtype=torch.bfloat16)  # noqa: E731
+    q, k, v, do = rand(B, H, T, d).mul_(d ** -0.5), rand(B, H, T, d).mul_(d ** -0.5), rand(B, H, T, d), rand(B, H, T, d)
+    la = -torch.exp2(-8.0 * torch.arange(1, H + 1, device="cuda") / H)
+    got = [lla.linear_forward(q, k, v, la), *lla.linear_backward(q, k, v, la, do)[:3]]
+    for b, h in ((0, 0), (B - 1, H - 1)):
+        x = [t[b, h][None, None].float() for t in (q, k, v)]
+        a = la[h:h + 1].clone()
+        ref = [lla.linear_forward(*x, a), *lla.linear_backward(*x, a, do[b, h][None, None].float())[:3]]
+        for y, r in zip(got, ref):
+            assert float((y[b, h].float() - r[0, 0]).norm() / r.norm()) <= 5e-3, (b, h)
+    del got, do
+    # the same rows packed, one tensor of [H, B T, d]: its last sequence lies past 2^31 elements
+    rows = [t.view(H, B * T, d) for t in (q, k, v)]
+    cu = torch.tensor([0, 1000, (B - 1) * T, B * T], dtype=torch.int32, device="cuda")
+    out = lla.linear_forward_varlen(*rows, la, cu, B * T)
+    x = [t[H - 1:, (B - 1) * T:].float().contiguous() for t in rows]
+    ref = lla.linear_forward(*(t[None] for t in x), la[H - 1:].clone())
+    assert float((out[H - 1, (B - 1) * T:].float() - ref[0, 0]).norm() / ref.norm()) <= 5e-3
+    del out, rows, q, k, v
+    # one token: states of more than 2^31 elements
+    B, d = 2100, 128
+    state = torch.randn(B, H, d, d, generator=g, device="cuda")
+    assert state.numel() > 2 ** 31
+    q, k, v = (torch.randn(B, H, d, generator=g, device="cuda") for _ in range(3))
+    last = state[-1:].clone()
+    out = lla.linear_decode_step(q, k, v, la, state)
+    one = lla.linear_decode_step(q[-1:].clone(), k[-1:].clone(), v[-1:].clone(), la, last)
+    assert torch.equal(out[-1:], one) and torch.equal(state[-1:], last)
+
+
+def test_shared_offsets_past_32_bits(lla):
+    B, H, L, d, P = 130, 64, 18, 128, 70001
+    states = torch.randn(B, H, L, d, d, device="cuda")
+    assert states.numel() > 2 ** 31
+    q, k, v = (torch.randn(B, H, d, device="cuda") for _ in range(3))
+    la, lam = -torch.rand(B, H, device="cuda"), torch.rand(B, H, L, device="cuda")
+    pre, decay = torch.randn(H, L, d, d, device="cuda"), -torch.rand(B, H, device="cuda")
+    t = P + torch.arange(B, device="cuda") * 7
+    last, kept = states[-1:].clone(), decay[-1:].clone()
+    out = lla.decode_step_shared(q, k, v, la, lam, pre, P, decay, states, t)
+    one = lla.decode_step_shared(*(x[-1:].clone() for x in (q, k, v, la, lam)), pre, P, kept, last, t[-1:].clone())
+    assert torch.equal(out[-1:], one) and torch.equal(states[-1:], last) and torch.equal(decay[-1:], kept)
