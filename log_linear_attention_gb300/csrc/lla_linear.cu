@@ -19,10 +19,10 @@
 //                     X <- g^n X + own, and the state that leaves the last chunk
 //   lin_out         : out_i = sum_j M_ij (a_i . b_j) c_j + f_i X^T a_i, M_ij = g^|i-j| on the
 //                     causal side, f_i = g^(i+1) forwards, g^(n-1-i) backwards.
-// All products are 64 x 64 register-tiled fp32 products out of shared memory. FMAs bound them: the pipe is 50% busy over
-// launches of 1.6 waves of CTAs (gradients of 3 x 5 heads, T = 1301, 96 x 80: 139 us; prompts of 2 x 16 heads, T = 4096,
-// 128 x 128: 415 us, 31 TFLOP/s counting whole squares). No exponent is ever
-// negative, so no factor overflows for g <= 1; g^0 is 1 also for g = 0 (log_a = -inf).
+// All products are 64 x 64 register-tiled fp32 products out of shared memory. FMAs bound them, over launches of 1.6 waves
+// of CTAs: packed FMA instructions, two products each, are 31 to 34% of what the pipe's counter could hold (gradients of
+// 3 x 5 heads, T = 1301, 96 x 80: 140 us; prompts of 2 x 16 heads, T = 4096, 128 x 128: 420 us, 31 TFLOP/s counting whole
+// squares). No exponent is ever negative, so no factor overflows for g <= 1; g^0 is 1 also for g = 0 (log_a = -inf).
 #include <atomic>
 
 #include "lla_internal.cuh"

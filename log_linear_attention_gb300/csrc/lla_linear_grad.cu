@@ -16,10 +16,10 @@
 // for its items (two chunks where they fit), and S and R; the items of one gradient share scores and P. Two items are in
 // flight: both kinds of accumulator are double.
 //
-// Measured there: the whole backward 227 us, 138 of it this kernel. With every item's operands copied for itself, its own
-// scores and the places of its operands looked up by the issuing thread it took 180 (gradients as scans: 278); the
-// rows shared, but looked up: 174. The instructions of the thread that issues the MMAs are the chain that is left, and
-// the rows in and out take 110 us of HBM; the state scans before it take 89 us (514 MB at 5.8 TB/s).
+// Measured there: the whole backward 231 us; under ncu, cold, this kernel 143 and the state scans before it 96. With every
+// item's operands copied for itself, its own scores and the places of its operands looked up by the issuing thread this
+// kernel took 42 us more (gradients as scans: the whole 278); the rows shared, but looked up: 36. The instructions of the
+// thread that issues the MMAs are the chain that is left, and the bytes that it moves (844 MB) take 125 us at the copy rate.
 #include <atomic>
 #include <type_traits>
 

@@ -20,12 +20,12 @@
 // order. kFull does all of the above, forwards; kStates only forms the states, forwards or backwards, and
 // writes the one that enters each chunk in bf16 for the kernel of the gradients (lla_linear_grad.cu).
 //
-// Measured (GB300): a chunk takes about 2.0 us (1.2 where only the state is formed). What bounds it is shared memory: at
-// d = 128 its products read 256 KB of operands, the copies write 80 KB, the cut reads and writes 64 KB and X takes 16: 416 KB,
-// 3250 of the 3900 cycles at 128 bytes each. (Two warps issuing the MMAs, each half of them, took 101 us where one takes
+// Measured (GB300): a chunk takes about 2.1 us (1.2 where only the state is formed). What bounds it is shared memory: at
+// d = 128 its products read 288 KB of operands, the copies write 80 KB, the cut reads and writes 64 KB and X takes 16: 448 KB,
+// 3500 of the 4000 cycles at 128 bytes each. (Two warps issuing the MMAs, each half of them, took 101 us where one took
 // 97.) Two stages, as shared memory is full: 224 KB.
-// 4 x 16 heads, T = 8192, 128 x 64: 97 us for 403 MB, 503 with the pieces'. 16 heads, T = 65536, 128 x 128: 355 us. 32
-// packed sequences of 256..8192: 250 us for 1.53 GB, 90% of the copy rate.
+// 4 x 16 heads, T = 8192, 128 x 64: 99 us for 403 MB, 492 with the pieces'. 16 heads, T = 65536, 128 x 128: 366 us. 32
+// packed sequences of 256..8192: 252 us for 1.53 GB, 90% of the copy rate.
 //
 // Rows of a chunk behind its sequence's end (another sequence's, when packed) are set to zero in shared
 // memory before any product sums over them. Every wait is bounded; on overrun the kernel records
