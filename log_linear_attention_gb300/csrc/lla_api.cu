@@ -658,7 +658,7 @@ bool clash(std::initializer_list<Span> written, std::initializer_list<Span> read
 
 size_t type_bytes(int dtype) { return dtype == LLA_BF16 ? 2 : 4; }
 
-// Checks shared by the linear prefill, packed prefill and backward: `rows` = rows of one tensor,
+// Checks shared by the linear prefill, packed prefill and backward: `rows` = rows of one head,
 // batch = sequences, b0 = entering states.
 int validate_linear(const void* q, const void* k, const void* v, const float* log_a, const float* state0, int batch,
                     int b0, int H, int64_t rows, int T, int dk, int dv, int dtype) {
@@ -670,8 +670,8 @@ int validate_linear(const void* q, const void* k, const void* v, const float* lo
     if ((b0 != 0 && b0 != 1 && b0 != batch) || (b0 == 0) != (state0 == nullptr)) return LLA_ERR_INVALID_ARG;
     if (dk > 128 || dv > 128) return LLA_ERR_UNSUPPORTED;
     if ((int64_t)batch * H > 65535) return LLA_ERR_UNSUPPORTED;
-    if (rows * (dk > dv ? dk : dv) > ((int64_t)1 << 40)) return LLA_ERR_UNSUPPORTED;
-    if ((int64_t)batch * ((T - 1) / 64 + 1) > 0x7fffffff) return LLA_ERR_UNSUPPORTED;
+    if (H * rows * (dk > dv ? dk : dv) > ((int64_t)1 << 40)) return LLA_ERR_UNSUPPORTED;
+    if (rows / 64 + batch > 0x7fffffff) return LLA_ERR_UNSUPPORTED;  // 64-token chunks of a head are counted in an int
     return LLA_OK;
 }
 
@@ -734,7 +734,7 @@ extern "C" {
 
 int lla_linear_forward(const void* q, const void* k, const void* v, const float* log_a, const float* state0, void* out,
                        float* state_out, int B, int B0, int H, int T, int dk, int dv, void* stream, int dtype) {
-    int st = validate_linear(q, k, v, log_a, state0, B, B0, H, (int64_t)B * H * T, T, dk, dv, dtype);
+    int st = validate_linear(q, k, v, log_a, state0, B, B0, H, (int64_t)B * T, T, dk, dv, dtype);
     if (st != LLA_OK) return st;
     if (!out || !aligned16(out) || !aligned16(state_out)) return LLA_ERR_INVALID_ARG;
     const size_t msz = (size_t)dk * dv * sizeof(float);
@@ -783,7 +783,7 @@ int lla_linear_forward_varlen(const void* q, const void* k, const void* v, const
     // a bound above the rows that there are (a server's longest context, say) bounds nothing more: it must not count in the
     // plan, nor turn a call away
     const int longest = max_T < total_T ? max_T : total_T;
-    int st = validate_linear(q, k, v, log_a, state0, n_seq, n0, H, (int64_t)H * total_T, longest, dk, dv, dtype);
+    int st = validate_linear(q, k, v, log_a, state0, n_seq, n0, H, total_T, longest, dk, dv, dtype);
     if (st != LLA_OK) return st;
     if (!out || !aligned16(out) || !aligned16(state_out)) return LLA_ERR_INVALID_ARG;
     const size_t msz = (size_t)dk * dv * sizeof(float);
@@ -848,7 +848,7 @@ int lla_linear_forward_varlen(const void* q, const void* k, const void* v, const
 int lla_linear_backward(const void* q, const void* k, const void* v, const float* log_a, const float* state0,
                         const void* dout, const float* dstate_out, void* dq, void* dk, void* dv, float* dstate0, int B,
                         int B0, int H, int T, int dk_, int dv_, void* stream, int dtype) {
-    int st = validate_linear(q, k, v, log_a, state0, B, B0, H, (int64_t)B * H * T, T, dk_, dv_, dtype);
+    int st = validate_linear(q, k, v, log_a, state0, B, B0, H, (int64_t)B * T, T, dk_, dv_, dtype);
     if (st != LLA_OK) return st;
     if (!dout || !dq || !dk || !dv || !aligned16(dout) || !aligned16(dstate_out) || !aligned16(dq) || !aligned16(dk) ||
         !aligned16(dv) || !aligned16(dstate0))

@@ -976,3 +976,29 @@ def test_shared_offsets_past_32_bits(lla):
     out = lla.decode_step_shared(q, k, v, la, lam, pre, P, decay, states, t)
     one = lla.decode_step_shared(*(x[-1:].clone() for x in (q, k, v, la, lam)), pre, P, kept, last, t[-1:].clone())
     assert torch.equal(out[-1:], one) and torch.equal(states[-1:], last) and torch.equal(decay[-1:], kept)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_varlen_many_rows_under_a_loose_bound(lla, dtype):
+    """4000 sequences of 37 million rows with max_T as large as all of them: a bound times the sequences counted as chunks
+    that there might be, and the call was refused. Some sequences against calls of their own in fp32."""
+    n, d = 4000, 16
+    r = np.random.default_rng(9)
+    lengths = r.integers(0, 17000, n)
+    lengths[[3, 2500]] = 1 << 20, 1 << 19
+    cu = np.concatenate([[0], np.cumsum(lengths)])
+    total = int(cu[-1])
+    assert n * (total // 64) > 2 ** 31
+    g = torch.Generator(device="cuda").manual_seed(9)
+    t = torch.bfloat16 if dtype == "bf16" else torch.float32
+    q, k, v = (torch.randn(1, total, d, generator=g, device="cuda", dtype=t) for _ in range(3))
+    la = torch.full((1,), -0.01, device="cuda")
+    s1 = torch.empty(n, 1, d, d, device="cuda")
+    out = lla.linear_forward_varlen(q, k, v, la, torch.from_numpy(cu.astype(np.int32)).cuda(), total, state_out=s1)
+    for b in (0, 3, 4, 1999, 2500, n - 1):
+        rows = slice(int(cu[b]), int(cu[b + 1]))
+        s = torch.empty(1, 1, d, d, device="cuda")
+        ref = lla.linear_forward(*(x[:, None, rows].float().contiguous() for x in (q, k, v)), la, state_out=s)
+        # fp32: sums of some 100 terms (the decay's reach) in other orders
+        assert float((out[:, rows].float() - ref[0]).norm() / ref.norm()) <= (5e-3 if dtype == "bf16" else 1e-5), b
+        assert float((s1[b] - s[0]).norm() / s.norm()) <= 1e-4, b
