@@ -343,7 +343,9 @@ int lla_gdn_forward_profile(const void* q, const void* k, const void* v, const f
  *   state_out [n_seq,H,dk,dv]. A sequence may be empty: its state_out is its state0 (or zeros).
  *   Rows of out that belong to no sequence are left as they were. A sequence whose bounds break the
  *   rules (cu_seqlens not rising, rows past total_T, more than max_T of them) is skipped, its rows and
- *   state_out left as they were, and lla_device_error reports LLA_ERR_DEVICE.
+ *   state_out left as they were, and lla_device_error reports LLA_ERR_DEVICE. max_T may be any bound of
+ *   the lengths, but the cut into segments is made for a sequence of max_T tokens: the nearer it is
+ *   to the longest, the faster the call.
  *
  * lla_linear_backward: gradients of sum(dout . out) + sum(dstate_out . state_out).
  *   dout       [B,H,T,dv]   dtype   upstream gradient of out
