@@ -408,6 +408,111 @@ int lla_decode_step_shared(const void* q, const void* k, const void* v, const fl
                            int dv, int Lmax, int dtype);
 
 /*
+ * The gated linear recurrence: a state per channel, every channel by itself, with a gate for each
+ * token and channel (the vector-state layers that models mix with matrix-state ones):
+ *
+ *     h_t = exp(log_a_t) h_{t-1} + x_t,   h_{-1} = state0
+ *
+ * Gates of the input (1 - a_t, sqrt(1 - a_t^2) and the like) are the caller's, folded into x.
+ *
+ *   x, out    [B,T,D]   dtype       any T, D >= 1. Layers with heads: [B,H,T,d] is [B H,T,d], and
+ *                                   [B,T,H,d] is [B,T,H d]; to the recurrence all channels are alike.
+ *   log_a     [B,T,D]   gate_dtype  log of the gate (<= 0 expected; -inf, a gate of 0, is valid; positive
+ *                                   values are computed as given). gate_dtype: LLA_F32, or dtype.
+ *   state0    [B0,D]    fp32        h_{-1}: B0 = 0 (state0 NULL: zeros), 1 (one for the whole batch) or B.
+ *   state_out [B,D]     fp32        written: h_{T-1} before its rounding to dtype. NULL: not wanted.
+ * The recurrence is computed in fp32, sums in a fixed order: repeated calls give identical bits. Channels
+ * never mix; within one, an infinity or NaN reaches every later row of its sequence (gradients: every
+ * earlier one) and no row of another.
+ * Nothing that is written may overlap another argument (refused: LLA_ERR_INVALID_ARG).
+ *
+ * lla_gated_forward_varlen: packed sequences, x, log_a, out [total_T,D]; cu_seqlens device int32 [n_seq+1],
+ *   non-decreasing, 0 <= cu_seqlens[0], cu_seqlens[n_seq] <= total_T. state0 [n0,D], n0 in {0, 1, n_seq};
+ *   state_out [n_seq,D]. A sequence may be empty: its state_out is its state0 (or zeros). Rows of out that
+ *   belong to no sequence are left as they were. Where cu_seqlens breaks these rules the call writes nothing
+ *   and lla_device_error reports LLA_ERR_DEVICE.
+ *
+ * lla_gated_backward(_varlen): gradients of sum(dout . out) + sum(dstate_out . state_out).
+ *   out        the forward's outputs as it left them (no x is needed: with F_t the gradient that reaches
+ *              h_{t-1}, dlog_a_t = F_t h_{t-1}). In bf16 that h is the rounded one: dlog_a is exact for the
+ *              outputs given, 2^-8 of each value from that of the unrounded states at most.
+ *   dout       like out;  dstate_out [B,D] fp32, NULL: zeros
+ *   dx         [B,T,D] dtype, dlog_a [B,T,D] gate_dtype: written (packed: 0 for rows of no sequence)
+ *   dstate0    [B0,D] fp32, written (B0 = 1: summed over the batch in order); NULL: not wanted
+ *
+ * lla_gated_decode_step: one token of every sequence; x, log_a, out [B,D], state [B,D] fp32 read and written
+ *   in place (h_{t-1} on entry, h_t on return; what the prompt left in state_out).
+ *
+ * Limits: rows x D up to 2^40; T (packed: total_T) up to 2^31 - 2^16. Workspace: only for dstate0 with B0 = 1
+ * (B D floats, the library's pool).
+ */
+int lla_gated_forward(const void* x, const void* log_a, const float* state0, void* out, float* state_out, int B, int B0,
+                      int T, int D, void* stream, int dtype, int gate_dtype);
+int lla_gated_forward_varlen(const void* x, const void* log_a, const float* state0, void* out, float* state_out,
+                             const int32_t* cu_seqlens, int n_seq, int n0, int total_T, int D, void* stream, int dtype,
+                             int gate_dtype);
+int lla_gated_backward(const void* log_a, const void* out, const float* state0, const void* dout,
+                       const float* dstate_out, void* dx, void* dlog_a, float* dstate0, int B, int B0, int T, int D,
+                       void* stream, int dtype, int gate_dtype);
+int lla_gated_backward_varlen(const void* log_a, const void* out, const float* state0, const void* dout,
+                              const float* dstate_out, void* dx, void* dlog_a, float* dstate0,
+                              const int32_t* cu_seqlens, int n_seq, int n0, int total_T, int D, void* stream, int dtype,
+                              int gate_dtype);
+int lla_gated_decode_step(const void* x, const void* log_a, float* state, void* out, void* stream, int B, int D,
+                          int dtype, int gate_dtype);
+
+/*
+ * Drafted tokens (speculative decoding). A draft is a tree of N tokens: parent[i] < i is the node that node i
+ * goes on from, or -1 for the last token that the states hold; -2 marks a place without a node (trees of
+ * different sizes in one batch), which no node may name. A tree call computes the outputs of all nodes from
+ * states that it only reads: what decode steps along each branch would give, with no copy of the states and
+ * nothing to take back. A commit then appends the accepted tokens to the states in one pass: what a decode
+ * step for each would leave.
+ *
+ *   parent [BP,N] int32, device: BP = 1 (one tree for the whole batch) or B. A sequence whose tree breaks the
+ *          rules is skipped (its rows of out left as they were) and LLA_ERR_DEVICE is recorded. Rows of out of
+ *          places without a node are left as they were, their inputs not used.
+ *   count  [B] int32, device: accepted tokens of every sequence, 0 .. M (0: its states are left as they were).
+ *   path   [B,M] int32, device: their node indexes in order (entries past count are not read; the same node
+ *          twice is its token twice). NULL, with M = 0: the tokens 0 .. count-1, count <= N (a chain, or a
+ *          few tokens at a time). A count or index out of range: that sequence is skipped, LLA_ERR_DEVICE.
+ *   N, M 1..128.
+ *
+ * lla_decode_tree: node i at depth d_i (0 below parent -1) is the token at position t + d_i; its output is
+ * lla_decode_step's after the nodes above it.
+ *   q, k [B,H,N,dk], v, out [B,H,N,dv] dtype; log_a [B,H,N], lambda [B,H,N,Lmax] fp32
+ *   fenwick_states [B,H,Lmax,dk,dv] fp32, read: tokens 0 .. t-1, as lla_decode_step takes them
+ *   t [B] int64, device: needs 0 <= t and t + d_i < 2^(Lmax-1) (else skipped, LLA_ERR_DEVICE)
+ * lla_decode_commit: the states after the accepted tokens t .. t + count - 1; t is not advanced. Slots that the
+ *   last of them leaves empty stay as they were. Needs 0 <= t and t + count <= 2^(Lmax-1).
+ * lla_linear_decode_tree, lla_linear_decode_commit: the same for lla_linear_decode_step; log_a [H] fp32,
+ *   state [B,H,dk,dv] fp32.
+ *   dk, dv 1..128; Lmax 1..40. Products with the states run on tensor cores: bf16 queries as they are, states
+ *   in two bf16 parts (2^-16 of each element), fp32 calls in three parts of both; sums in fp32 in a fixed order
+ *   (repeated calls give identical bits). An infinity in the states may come out as NaN; one in a node reaches
+ *   only that node's and its descendants' outputs.
+ * lla_gated_decode_tree, lla_gated_decode_commit: the same for lla_gated_decode_step; x, log_a, out [B,N,D],
+ *   state [B,D] fp32; B up to 65535. (h of a node: exp(log_a_i) h_parent(i) + x_i.)
+ *
+ * Nothing that is written may overlap another argument (refused: LLA_ERR_INVALID_ARG). No workspace.
+ */
+int lla_decode_tree(const void* q, const void* k, const void* v, const float* log_a, const float* lambda,
+                    const float* fenwick_states, const int64_t* t, const int32_t* parent, void* out, void* stream, int B,
+                    int BP, int H, int N, int dk, int dv, int Lmax, int dtype);
+int lla_decode_commit(const void* k, const void* v, const float* log_a, float* fenwick_states, const int64_t* t,
+                      const int32_t* count, const int32_t* path, void* stream, int B, int H, int N, int M, int dk, int dv,
+                      int Lmax, int dtype);
+int lla_linear_decode_tree(const void* q, const void* k, const void* v, const float* log_a, const float* state,
+                           const int32_t* parent, void* out, void* stream, int B, int BP, int H, int N, int dk, int dv,
+                           int dtype);
+int lla_linear_decode_commit(const void* k, const void* v, const float* log_a, float* state, const int32_t* count,
+                             const int32_t* path, void* stream, int B, int H, int N, int M, int dk, int dv, int dtype);
+int lla_gated_decode_tree(const void* x, const void* log_a, const float* state, const int32_t* parent, void* out,
+                          void* stream, int B, int BP, int N, int D, int dtype, int gate_dtype);
+int lla_gated_decode_commit(const void* x, const void* log_a, float* state, const int32_t* count, const int32_t* path,
+                            void* stream, int B, int N, int M, int D, int dtype, int gate_dtype);
+
+/*
  * Test hook for the failure path of the bounded waits (no counterpart on the
  * pages; not for production use). On the current device, for the tensor-core
  * prefill output kernel of dv = 64 and the tensor-core kernels of linear

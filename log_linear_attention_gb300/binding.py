@@ -92,6 +92,21 @@ def load() -> ctypes.CDLL:
             lib.lla_decode_step_shared.argtypes = ([vp, vp, vp, fp, fp, fp, ctypes.c_int64, i, fp, fp, vp, vp, vp]
                                                    + [i] * 6)
             lib.lla_decode_step_shared.restype = i
+            for name, types in {
+                "lla_gated_forward": [vp, vp, fp, vp, fp] + [i] * 4 + [vp, i, i],
+                "lla_gated_forward_varlen": [vp, vp, fp, vp, fp, vp] + [i] * 4 + [vp, i, i],
+                "lla_gated_backward": [vp, vp, fp, vp, fp, vp, vp, fp] + [i] * 4 + [vp, i, i],
+                "lla_gated_backward_varlen": [vp, vp, fp, vp, fp, vp, vp, fp, vp] + [i] * 4 + [vp, i, i],
+                "lla_gated_decode_step": [vp, vp, fp, vp, vp] + [i] * 4,
+                "lla_gated_decode_tree": [vp, vp, fp, vp, vp, vp] + [i] * 6,
+                "lla_gated_decode_commit": [vp, vp, fp, vp, vp, vp] + [i] * 6,
+                "lla_decode_tree": [vp, vp, vp, fp, fp, fp, vp, vp, vp, vp] + [i] * 8,
+                "lla_decode_commit": [vp, vp, fp, fp, vp, vp, vp, vp] + [i] * 8,
+                "lla_linear_decode_tree": [vp, vp, vp, fp, fp, vp, vp, vp] + [i] * 7,
+                "lla_linear_decode_commit": [vp, vp, fp, fp, vp, vp, vp] + [i] * 7,
+            }.items():
+                getattr(lib, name).argtypes = types
+                getattr(lib, name).restype = i
             _lib = lib
     return _lib
 
@@ -675,3 +690,322 @@ def decode_step_shared(q, k, v, log_a, lam, prefix_states, prefix_len: int, pref
     if decay is not prefix_decay:
         prefix_decay.copy_(decay)
     return o
+
+
+def _fits(t_, dtype, shape, index):
+    return (type(t_) is _torch_module.Tensor and t_.dtype is dtype and t_.shape == shape and t_.get_device() == index
+            and t_.is_contiguous())
+
+
+def _want(t_, name, dtype, shape, device):
+    """Says what is wrong with an argument that does not fit."""
+    _check(t_, name, device)
+    if t_.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t_.dtype}")
+    if t_.shape != shape:
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t_.shape)}")
+
+
+def _gated_inputs(x, log_a, *like, dims, name="x"):
+    """(device index, dtype code, gate's dtype code) of a gated call: x, log_a of one shape, the gate fp32 or of x's type."""
+    torch = _torch()
+    _check(x, name)
+    code = _dtype_code(x)
+    if x.dim() != dims:
+        raise ValueError(f"{name} must have {dims} dimensions, got {list(x.shape)}")
+    gate = torch.float32 if isinstance(log_a, torch.Tensor) and log_a.dtype == torch.float32 else x.dtype
+    index = x.get_device()
+    if not _fits(log_a, gate, x.shape, index):
+        _want(log_a, "log_a", gate, x.shape, x.device)
+    for n, t_ in like:
+        if not _fits(t_, x.dtype, x.shape, index):
+            _want(t_, n, x.dtype, x.shape, x.device)
+    return index, code, LLA_F32 if gate is torch.float32 else code
+
+
+def _gated_state(t_, name, n, D, device):
+    """(rows, address) of an entering state [n,D] or [1,D], or (0, NULL)."""
+    if t_ is None:
+        return 0, None
+    one = t_.dim() == 2 and t_.shape[0] == 1
+    return (1 if one else n), _state(t_, name, (1 if one else n, D), device)
+
+
+def _cu(cu_seqlens, device):
+    torch = _torch()
+    _check(cu_seqlens, "cu_seqlens", device)
+    if cu_seqlens.dtype != torch.int32 or cu_seqlens.dim() != 1 or cu_seqlens.numel() < 2:
+        raise TypeError("cu_seqlens must be int32 [n+1]")
+    return cu_seqlens.numel() - 1
+
+
+def gated_forward(x, log_a, state0=None, state_out=None, out=None, stream=None):
+    """The gated linear recurrence, lla_gated_forward: h_t = exp(log_a_t) h_{t-1} + x_t, every channel by itself.
+    Returns out [B,T,D], the states in x's type.
+
+    x [B,T,D] (bf16 or fp32, any T and D >= 1); log_a [B,T,D], fp32 or x's type. ``state0`` fp32 [B,D], or [1,D] for
+    one state shared by the batch; ``state_out`` fp32 [B,D] is written with the last state (see gated_decode_step)."""
+    index, code, gate = _gated_inputs(x, log_a, dims=3)
+    if stream is not None or index != _current_device():
+        return _elsewhere(x.device, stream, gated_forward, x, log_a, state0, state_out, out)
+    B, T, D = x.shape
+    n0, s0 = _gated_state(state0, "state0", B, D, x.device)
+    s1 = _state(state_out, "state_out", (B, D), x.device)
+    o = _torch_module.empty_like(x) if out is None else _given(out, x)
+    _call(load().lla_gated_forward(x.data_ptr(), log_a.data_ptr(), s0, o.data_ptr(), s1, B, n0, T, D, _raw_stream(index),
+                                   code, gate), "lla_gated_forward")
+    return o
+
+
+def gated_forward_varlen(x, log_a, cu_seqlens, state0=None, state_out=None, out=None, stream=None):
+    """lla_gated_forward_varlen: packed sequences. x, log_a [total,D]; cu_seqlens int32 [n+1] on the device; state0
+    [n,D] or [1,D] (shared); state_out [n,D]. Rows of ``out`` that belong to no sequence are left as they were
+    (uninitialised in a new ``out``)."""
+    index, code, gate = _gated_inputs(x, log_a, dims=2)
+    n = _cu(cu_seqlens, x.device)
+    if stream is not None or index != _current_device():
+        return _elsewhere(x.device, stream, gated_forward_varlen, x, log_a, cu_seqlens, state0, state_out, out)
+    T, D = x.shape
+    n0, s0 = _gated_state(state0, "state0", n, D, x.device)
+    s1 = _state(state_out, "state_out", (n, D), x.device)
+    o = _torch_module.empty_like(x) if out is None else _given(out, x)
+    cu_seqlens = _small(cu_seqlens, "lla_gated_forward_varlen", o, state_out)
+    _call(load().lla_gated_forward_varlen(x.data_ptr(), log_a.data_ptr(), s0, o.data_ptr(), s1, cu_seqlens.data_ptr(), n,
+                                          n0, T, D, _raw_stream(index), code, gate), "lla_gated_forward_varlen")
+    return o
+
+
+def gated_backward(log_a, out, dout, state0=None, dstate_out=None, stream=None):
+    """lla_gated_backward: gradients of sum(dout * out) + sum(dstate_out * state_out) of gated_forward, whose output
+    is given as it was kept.
+
+    Returns (dx, dlog_a, dstate0): dx in out's type, dlog_a in log_a's, dstate0 fp32 like state0 (None without one;
+    summed over the batch where state0 is shared)."""
+    index, code, gate = _gated_inputs(out, log_a, ("dout", dout), dims=3, name="out")
+    if stream is not None or index != _current_device():
+        return _elsewhere(out.device, stream, gated_backward, log_a, out, dout, state0, dstate_out)
+    B, T, D = out.shape
+    n0, s0 = _gated_state(state0, "state0", B, D, out.device)
+    s1 = _state(dstate_out, "dstate_out", (B, D), out.device)
+    dx, da = _torch_module.empty_like(out), _torch_module.empty_like(log_a)
+    ds = None if state0 is None else _torch_module.empty_like(state0)
+    _call(load().lla_gated_backward(log_a.data_ptr(), out.data_ptr(), s0, dout.data_ptr(), s1, dx.data_ptr(),
+                                    da.data_ptr(), None if ds is None else ds.data_ptr(), B, n0, T, D,
+                                    _raw_stream(index), code, gate), "lla_gated_backward")
+    return dx, da, ds
+
+
+def gated_backward_varlen(log_a, out, dout, cu_seqlens, state0=None, dstate_out=None, stream=None):
+    """lla_gated_backward_varlen: gradients of packed sequences (see gated_forward_varlen); dstate_out [n,D]. Gradients
+    of rows that belong to no sequence are 0."""
+    index, code, gate = _gated_inputs(out, log_a, ("dout", dout), dims=2, name="out")
+    n = _cu(cu_seqlens, out.device)
+    if stream is not None or index != _current_device():
+        return _elsewhere(out.device, stream, gated_backward_varlen, log_a, out, dout, cu_seqlens, state0, dstate_out)
+    T, D = out.shape
+    n0, s0 = _gated_state(state0, "state0", n, D, out.device)
+    s1 = _state(dstate_out, "dstate_out", (n, D), out.device)
+    dx, da = _torch_module.empty_like(out), _torch_module.empty_like(log_a)
+    ds = None if state0 is None else _torch_module.empty_like(state0)
+    cu_seqlens = _small(cu_seqlens, "lla_gated_backward_varlen")
+    _call(load().lla_gated_backward_varlen(log_a.data_ptr(), out.data_ptr(), s0, dout.data_ptr(), s1, dx.data_ptr(),
+                                           da.data_ptr(), None if ds is None else ds.data_ptr(), cu_seqlens.data_ptr(),
+                                           n, n0, T, D, _raw_stream(index), code, gate), "lla_gated_backward_varlen")
+    return dx, da, ds
+
+
+def gated_decode_step(x, log_a, state, out=None, stream=None):
+    """One token of every sequence, lla_gated_decode_step. x, log_a [B,D]; ``state`` [B,D] fp32 is updated in place.
+    Returns out [B,D]."""
+    index, code, gate = _gated_inputs(x, log_a, dims=2)
+    if stream is not None or index != _current_device():
+        return _elsewhere(x.device, stream, gated_decode_step, x, log_a, state, out)
+    B, D = x.shape
+    if not _fits(state, _torch_module.float32, x.shape, index):
+        _want(state, "state", _torch_module.float32, x.shape, x.device)
+    o = _torch_module.empty_like(x) if out is None else _given(out, x)
+    _call(load().lla_gated_decode_step(x.data_ptr(), log_a.data_ptr(), state.data_ptr(), o.data_ptr(),
+                                       _raw_stream(index), B, D, code, gate), "lla_gated_decode_step")
+    return o
+
+
+def _parent(parent, B, N, index, device):
+    """Rows of a parent array: int32 [N] or [1,N] (one tree for the batch), or [B,N]."""
+    torch = _torch()
+    if _fits(parent, torch.int32, (B, N), index):
+        return B
+    if not (_fits(parent, torch.int32, (N,), index) or _fits(parent, torch.int32, (1, N), index)):
+        _check(parent, "parent", device)
+        raise ValueError(f"parent must be int32 [{N}] or [{B},{N}], got {parent.dtype} {list(parent.shape)}")
+    return 1
+
+
+def _accepted(count, path, B, index, device):
+    """M of a commit: count int32 [B], path int32 [B,M] or None (M = 0)."""
+    torch = _torch()
+    if not _fits(count, torch.int32, (B,), index):
+        _want(count, "count", torch.int32, (B,), device)
+    if path is None:
+        return 0
+    if path.dim() != 2 or path.shape[0] != B or path.shape[1] < 1:
+        raise ValueError(f"path must be int32 [{B},M], got {list(path.shape)}")
+    if not _fits(path, torch.int32, path.shape, index):
+        _want(path, "path", torch.int32, path.shape, device)
+    return path.shape[1]
+
+
+def gated_decode_tree(x, log_a, state, parent, out=None, stream=None):
+    """Outputs of a tree of drafted tokens, lla_gated_decode_tree: h_i = exp(log_a_i) h_parent(i) + x_i. x, log_a
+    [B,N,D]; ``state`` [B,D] fp32 is read; ``parent`` int32 [N] or [B,N] (see decode_tree). Returns out [B,N,D]."""
+    index, code, gate = _gated_inputs(x, log_a, dims=3)
+    if stream is not None or index != _current_device():
+        return _elsewhere(x.device, stream, gated_decode_tree, x, log_a, state, parent, out)
+    B, N, D = x.shape
+    if not _fits(state, _torch_module.float32, (B, D), index):
+        _want(state, "state", _torch_module.float32, (B, D), x.device)
+    trees = _parent(parent, B, N, index, x.device)
+    o = _torch_module.empty_like(x) if out is None else _given(out, x)
+    parent = _small(parent, "lla_gated_decode_tree", o)
+    _call(load().lla_gated_decode_tree(x.data_ptr(), log_a.data_ptr(), state.data_ptr(), parent.data_ptr(), o.data_ptr(),
+                                       _raw_stream(index), B, trees, N, D, code, gate), "lla_gated_decode_tree")
+    return o
+
+
+def gated_decode_commit(x, log_a, state, count, path=None, stream=None):
+    """Accepted tokens into the states, lla_gated_decode_commit (see decode_commit). x, log_a [B,N,D]; ``state`` [B,D]
+    fp32 is updated in place and returned."""
+    index, code, gate = _gated_inputs(x, log_a, dims=3)
+    if stream is not None or index != _current_device():
+        return _elsewhere(x.device, stream, gated_decode_commit, x, log_a, state, count, path)
+    B, N, D = x.shape
+    if not _fits(state, _torch_module.float32, (B, D), index):
+        _want(state, "state", _torch_module.float32, (B, D), x.device)
+    M = _accepted(count, path, B, index, x.device)
+    count = _small(count, "lla_gated_decode_commit", state)
+    path = None if path is None else _small(path, "lla_gated_decode_commit", state)
+    _call(load().lla_gated_decode_commit(x.data_ptr(), log_a.data_ptr(), state.data_ptr(), count.data_ptr(),
+                                         None if path is None else path.data_ptr(), _raw_stream(index), B, N, M, D, code,
+                                         gate), "lla_gated_decode_commit")
+    return state
+
+
+def _nodes(k, v, log_a, gates, q=None):
+    """(B, H, N, dk, dv, device index) of a tree's or a commit's tokens: q, k [B,H,N,dk], v [B,H,N,dv] of one dtype,
+    log_a fp32 of the shape ``gates(B, H, N)``."""
+    torch = _torch()
+    _check(k, "k")
+    _check(v, "v", k.device)
+    if k.dim() != 4 or v.dim() != 4:
+        raise ValueError("k must be [B,H,N,dk] and v [B,H,N,dv]")
+    B, H, N, dk = k.shape
+    dv, index, dtype = v.shape[3], k.get_device(), k.dtype
+    if q is not None and not _fits(q, dtype, k.shape, index):
+        _want(q, "q", dtype, k.shape, k.device)
+    if v.dtype != dtype or v.shape != (B, H, N, dv):
+        _want(v, "v", dtype, (B, H, N, dv), k.device)
+    shape = gates(B, H, N)
+    if not _fits(log_a, torch.float32, shape, index):
+        _want(log_a, "log_a", torch.float32, shape, k.device)
+    return B, H, N, dk, dv, index
+
+
+def _one_gate(B, H, N):
+    return (H,)
+
+
+def _node_gates(B, H, N):
+    return (B, H, N)
+
+
+def decode_tree(q, k, v, log_a, lam, states, t, parent, out=None, stream=None):
+    """Outputs of a tree of drafted tokens over the states of decode_step, lla_decode_tree. Nothing but ``out`` is
+    written: the accepted tokens go into the states with decode_commit.
+
+    q, k [B,H,N,dk]; v [B,H,N,dv] (bf16 or fp32, N up to 128); log_a [B,H,N], lam [B,H,N,Lmax] fp32; ``states``
+    [B,H,Lmax,dk,dv] fp32 with tokens 0..t-1, ``t`` int64 [B] on the device. ``parent`` int32 [N] (one tree for the
+    batch) or [B,N] on the device: the node that a node goes on from, before it in the list, -1 for the last token of
+    the states, -2 for no node (its row of ``out`` is left as it was; uninitialised in a new ``out``). Returns out
+    [B,H,N,dv]."""
+    B, H, N, dk, dv, index = _nodes(k, v, log_a, _node_gates, q)
+    if stream is not None or index != _current_device():
+        return _elsewhere(q.device, stream, decode_tree, q, k, v, log_a, lam, states, t, parent, out)
+    torch = _torch_module
+    if states is None or states.dim() != 5:
+        raise ValueError("states must be float32 [B,H,Lmax,dk,dv]")
+    L = states.shape[2]
+    if not (_fits(states, torch.float32, (B, H, L, dk, dv), index) and _fits(lam, torch.float32, (B, H, N, L), index)
+            and _fits(t, torch.int64, (B,), index)):
+        _want(states, "states", torch.float32, (B, H, L, dk, dv), q.device)
+        _want(lam, "lambda", torch.float32, (B, H, N, L), q.device)
+        _want(t, "t", torch.int64, (B,), q.device)
+    trees = _parent(parent, B, N, index, q.device)
+    o = torch.empty_like(v) if out is None else _given(out, v)
+    where = "lla_decode_tree"
+    log_a, lam, t, parent = _small(log_a, where, o), _small(lam, where, o), _small(t, where, o), _small(parent, where, o)
+    _call(load().lla_decode_tree(q.data_ptr(), k.data_ptr(), v.data_ptr(), log_a.data_ptr(), lam.data_ptr(),
+                                 states.data_ptr(), t.data_ptr(), parent.data_ptr(), o.data_ptr(), _raw_stream(index), B,
+                                 trees, H, N, dk, dv, L, _dtype_code(q)), where)
+    return o
+
+
+def decode_commit(k, v, log_a, states, t, count, path=None, stream=None):
+    """Accepted tokens into the states of decode_step, lla_decode_commit: what a decode step for each would leave, in
+    one pass. k [B,H,N,dk]; v [B,H,N,dv]; log_a [B,H,N] fp32, as decode_tree takes them; ``states`` [B,H,Lmax,dk,dv]
+    fp32 is updated in place and returned; ``t`` int64 [B], not advanced (the caller adds ``count``).
+
+    ``count`` int32 [B]: accepted tokens of each sequence (0: left as it is); ``path`` int32 [B,M]: their nodes in order
+    (entries past count are not read); without it tokens 0..count-1."""
+    B, H, N, dk, dv, index = _nodes(k, v, log_a, _node_gates)
+    if stream is not None or index != _current_device():
+        return _elsewhere(k.device, stream, decode_commit, k, v, log_a, states, t, count, path)
+    torch = _torch_module
+    if states is None or states.dim() != 5:
+        raise ValueError("states must be float32 [B,H,Lmax,dk,dv]")
+    L = states.shape[2]
+    if not (_fits(states, torch.float32, (B, H, L, dk, dv), index) and _fits(t, torch.int64, (B,), index)):
+        _want(states, "states", torch.float32, (B, H, L, dk, dv), k.device)
+        _want(t, "t", torch.int64, (B,), k.device)
+    M = _accepted(count, path, B, index, k.device)
+    where = "lla_decode_commit"
+    log_a, t, count = _small(log_a, where, states), _small(t, where, states), _small(count, where, states)
+    path = None if path is None else _small(path, where, states)
+    _call(load().lla_decode_commit(k.data_ptr(), v.data_ptr(), log_a.data_ptr(), states.data_ptr(), t.data_ptr(),
+                                   count.data_ptr(), None if path is None else path.data_ptr(), _raw_stream(index), B, H,
+                                   N, M, dk, dv, L, _dtype_code(k)), where)
+    return states
+
+
+def linear_decode_tree(q, k, v, log_a, state, parent, out=None, stream=None):
+    """Outputs of a tree of drafted tokens over the state of linear_decode_step, lla_linear_decode_tree (see
+    decode_tree). log_a [H] fp32; ``state`` [B,H,dk,dv] fp32 is read. Returns out [B,H,N,dv]."""
+    B, H, N, dk, dv, index = _nodes(k, v, log_a, _one_gate, q)
+    if stream is not None or index != _current_device():
+        return _elsewhere(q.device, stream, linear_decode_tree, q, k, v, log_a, state, parent, out)
+    if not _fits(state, _torch_module.float32, (B, H, dk, dv), index):
+        _want(state, "state", _torch_module.float32, (B, H, dk, dv), q.device)
+    trees = _parent(parent, B, N, index, q.device)
+    o = _torch_module.empty_like(v) if out is None else _given(out, v)
+    where = "lla_linear_decode_tree"
+    log_a, parent = _small(log_a, where, o), _small(parent, where, o)
+    _call(load().lla_linear_decode_tree(q.data_ptr(), k.data_ptr(), v.data_ptr(), log_a.data_ptr(), state.data_ptr(),
+                                        parent.data_ptr(), o.data_ptr(), _raw_stream(index), B, trees, H, N, dk, dv,
+                                        _dtype_code(q)), where)
+    return o
+
+
+def linear_decode_commit(k, v, log_a, state, count, path=None, stream=None):
+    """Accepted tokens into the state of linear_decode_step, lla_linear_decode_commit (see decode_commit). log_a [H]
+    fp32; ``state`` [B,H,dk,dv] fp32 is updated in place and returned."""
+    B, H, N, dk, dv, index = _nodes(k, v, log_a, _one_gate)
+    if stream is not None or index != _current_device():
+        return _elsewhere(k.device, stream, linear_decode_commit, k, v, log_a, state, count, path)
+    if not _fits(state, _torch_module.float32, (B, H, dk, dv), index):
+        _want(state, "state", _torch_module.float32, (B, H, dk, dv), k.device)
+    M = _accepted(count, path, B, index, k.device)
+    where = "lla_linear_decode_commit"
+    log_a, count = _small(log_a, where, state), _small(count, where, state)
+    path = None if path is None else _small(path, where, state)
+    _call(load().lla_linear_decode_commit(k.data_ptr(), v.data_ptr(), log_a.data_ptr(), state.data_ptr(),
+                                          count.data_ptr(), None if path is None else path.data_ptr(),
+                                          _raw_stream(index), B, H, N, M, dk, dv, _dtype_code(k)), where)
+    return state

@@ -7,6 +7,7 @@
 #include "../../include/lla.h"
 #include "lla_internal.cuh"
 #include "lla_linear.cuh"
+#include "lla_drafts.cuh"
 
 // One error word per device (each device holds its own copy of this variable).
 __device__ int lla_device_error_word;
@@ -972,6 +973,231 @@ int lla_decode_step_shared(const void* q, const void* k, const void* v, const fl
     if (st != LLA_OK) return st;
     return ws.give(lla::decode_step_shared(dtype, q, k, v, log_a, lambda, prefix_states, prefix_len, Lp, prefix_decay,
                                            fenwick_states, t, out, ws.p, B, H, dk, dv, Lmax, err, s));
+}
+
+}  // extern "C"
+
+// ---- the gated recurrence, trees of drafted tokens and their commits
+
+namespace {
+
+bool any_misaligned(std::initializer_list<const void*> ptrs) {
+    for (const void* p : ptrs)
+        if (!aligned16(p)) return true;
+    return false;
+}
+
+size_t gate_bytes(int gate_dtype) { return type_bytes(gate_dtype); }
+
+// Types and sizes that every call of the gated recurrence shares: `rows` rows of D channels in all.
+int validate_gated(int dtype, int gate_dtype, int64_t rows, int D) {
+    if (dtype != LLA_BF16 && dtype != LLA_F32) return LLA_ERR_INVALID_ARG;
+    if (gate_dtype != LLA_F32 && gate_dtype != dtype) return LLA_ERR_INVALID_ARG;
+    if (rows < 1 || D < 1) return LLA_ERR_INVALID_ARG;
+    if (rows > ((int64_t)1 << 40) / D) return LLA_ERR_UNSUPPORTED;
+    return LLA_OK;
+}
+
+// A pass over n sequences in `rows` rows (packed: cu given, T = rows).
+int gated_pass(bool back, const void* x, const void* log_a, const float* state0, const void* dout,
+               const float* dstate_out, void* out, void* dlog_a, float* leave, const int32_t* cu, int n, int n0, int T,
+               int D, void* stream, int dtype, int gate_dtype) {
+    if (!x || !log_a || !out || (back && (!dout || !dlog_a))) return LLA_ERR_INVALID_ARG;
+    if (any_misaligned({x, log_a, state0, dout, dstate_out, out, dlog_a, leave, cu})) return LLA_ERR_INVALID_ARG;
+    if (n < 1 || T < 1) return LLA_ERR_INVALID_ARG;
+    const int64_t rows = cu ? (int64_t)T : (int64_t)n * T;
+    int st = validate_gated(dtype, gate_dtype, rows, D);
+    if (st != LLA_OK) return st;
+    if ((n0 != 0 && n0 != 1 && n0 != n) || (n0 == 0) != (state0 == nullptr)) return LLA_ERR_INVALID_ARG;
+    if (back && leave && n0 == 0) return LLA_ERR_INVALID_ARG;
+    // packed rows and sequences are counted in an int with room for a step's overhang and a row's marks
+    if (T > 0x7fff0000 || (cu && n >= (1 << 29))) return LLA_ERR_UNSUPPORTED;
+    if (((int64_t)(D - 1) / 64 + 1) * (cu ? 1 : n) * 16 > 0x7fffffff) return LLA_ERR_UNSUPPORTED;
+    const size_t data = (size_t)rows * D * type_bytes(dtype), gates = (size_t)rows * D * gate_bytes(gate_dtype);
+    const size_t state = (size_t)D * sizeof(float);
+    const int leave_n = back ? n0 : n;
+    if (clash({{out, data}, {dlog_a, gates}, {leave, leave_n * state}},
+              {{x, data}, {log_a, gates}, {dout, data}, {state0, n0 * state}, {dstate_out, n * state},
+               {cu, cu ? ((size_t)n + 1) * sizeof(int32_t) : 0}}))
+        return LLA_ERR_INVALID_ARG;
+    const int dev = current_device();
+    if (dev < 0) return LLA_ERR_CUDA;
+    int* err = error_word(dev);
+    if (!err) return LLA_ERR_CUDA;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const bool sum = back && leave && n0 == 1 && n > 1;  // gradients of one shared state: a part per sequence, then their sum
+    PoolBuffer ws(s);
+    if ((st = ws.take(dev, sum ? n * state : 0)) != LLA_OK) return st;
+    float* parts = reinterpret_cast<float*>(ws.p);
+    const lla::GatedPass p = {log_a, x, dout, out, dlog_a, state0, dstate_out, sum ? parts : leave, cu, n, n0, T, D};
+    cudaError_t e = lla::gated_run(p, back, dtype, gate_dtype, err, s);
+    if (e == cudaSuccess && sum) e = lla::linear_sum_batch(parts, leave, n, D, s);
+    return ws.give(e);
+}
+
+int report(cudaError_t e) {
+    if (e != cudaSuccess) cudaGetLastError();
+    return e == cudaSuccess ? LLA_OK : LLA_ERR_CUDA;
+}
+
+int tree_call(lla::TreeCall c, bool linear, void* stream, int dtype) {
+    if (!c.q || !c.k || !c.v || !c.log_a || !c.states || !c.parent || !c.out || (!linear && (!c.lambda || !c.t)))
+        return LLA_ERR_INVALID_ARG;
+    if (any_misaligned({c.q, c.k, c.v, c.log_a, c.lambda, c.states, c.t, c.parent, c.out})) return LLA_ERR_INVALID_ARG;
+    if (dtype != LLA_BF16 && dtype != LLA_F32) return LLA_ERR_INVALID_ARG;
+    if (c.B < 1 || c.H < 1 || c.N < 1 || c.dk < 1 || c.dv < 1 || c.Lmax < 1 || c.Lmax > 40) return LLA_ERR_INVALID_ARG;
+    if (c.BP != 1 && c.BP != c.B) return LLA_ERR_INVALID_ARG;
+    if (c.N > lla::kMaxTree || c.dk > 128 || c.dv > 128) return LLA_ERR_UNSUPPORTED;
+    if ((int64_t)c.B * c.H > 0x7fffffff) return LLA_ERR_UNSUPPORTED;
+    const size_t heads = (size_t)c.B * c.H, row = heads * c.N * type_bytes(dtype), f = sizeof(float);
+    if (clash({{c.out, row * c.dv}},
+              {{c.q, row * c.dk}, {c.k, row * c.dk}, {c.v, row * c.dv}, {c.log_a, (linear ? c.H : heads * c.N) * f},
+               {c.lambda, heads * c.N * c.Lmax * f}, {c.states, heads * c.Lmax * c.dk * c.dv * f},
+               {c.t, c.B * sizeof(int64_t)}, {c.parent, (size_t)c.BP * c.N * sizeof(int32_t)}}))
+        return LLA_ERR_INVALID_ARG;
+    const int dev = current_device();
+    if (dev < 0) return LLA_ERR_CUDA;
+    c.err = error_word(dev);
+    if (!c.err) return LLA_ERR_CUDA;
+    return report(lla::decode_tree(dtype, c, static_cast<cudaStream_t>(stream)));
+}
+
+int commit_call(lla::CommitCall c, bool linear, void* stream, int dtype) {
+    if (!c.k || !c.v || !c.log_a || !c.states || !c.count || (!linear && !c.t)) return LLA_ERR_INVALID_ARG;
+    if (any_misaligned({c.k, c.v, c.log_a, c.states, c.t, c.count, c.path})) return LLA_ERR_INVALID_ARG;
+    if (dtype != LLA_BF16 && dtype != LLA_F32) return LLA_ERR_INVALID_ARG;
+    if (c.B < 1 || c.H < 1 || c.N < 1 || c.dk < 1 || c.dv < 1 || c.Lmax < 1 || c.Lmax > 40) return LLA_ERR_INVALID_ARG;
+    if (c.path ? c.M < 1 : c.M != 0) return LLA_ERR_INVALID_ARG;
+    if (!c.path) c.M = c.N;
+    if (c.N > lla::kMaxTree || c.M > lla::kMaxTree || c.dk > 128 || c.dv > 128) return LLA_ERR_UNSUPPORTED;
+    if ((int64_t)c.B * c.H > 0x7fffffff) return LLA_ERR_UNSUPPORTED;
+    const size_t heads = (size_t)c.B * c.H, row = heads * c.N * type_bytes(dtype), f = sizeof(float);
+    if (clash({{c.states, heads * c.Lmax * c.dk * c.dv * f}},
+              {{c.k, row * c.dk}, {c.v, row * c.dv}, {c.log_a, (linear ? c.H : heads * c.N) * f},
+               {c.t, c.B * sizeof(int64_t)}, {c.count, c.B * sizeof(int32_t)},
+               {c.path, (size_t)c.B * c.M * sizeof(int32_t)}}))
+        return LLA_ERR_INVALID_ARG;
+    const int dev = current_device();
+    if (dev < 0) return LLA_ERR_CUDA;
+    c.err = error_word(dev);
+    if (!c.err) return LLA_ERR_CUDA;
+    return report(lla::decode_commit(dtype, c, static_cast<cudaStream_t>(stream)));
+}
+
+}  // namespace
+
+extern "C" {
+
+int lla_gated_forward(const void* x, const void* log_a, const float* state0, void* out, float* state_out, int B, int B0,
+                      int T, int D, void* stream, int dtype, int gate_dtype) {
+    return gated_pass(false, x, log_a, state0, nullptr, nullptr, out, nullptr, state_out, nullptr, B, B0, T, D, stream,
+                      dtype, gate_dtype);
+}
+
+int lla_gated_forward_varlen(const void* x, const void* log_a, const float* state0, void* out, float* state_out,
+                             const int32_t* cu_seqlens, int n_seq, int n0, int total_T, int D, void* stream, int dtype,
+                             int gate_dtype) {
+    if (!cu_seqlens) return LLA_ERR_INVALID_ARG;
+    return gated_pass(false, x, log_a, state0, nullptr, nullptr, out, nullptr, state_out, cu_seqlens, n_seq, n0, total_T,
+                      D, stream, dtype, gate_dtype);
+}
+
+int lla_gated_backward(const void* log_a, const void* out, const float* state0, const void* dout,
+                       const float* dstate_out, void* dx, void* dlog_a, float* dstate0, int B, int B0, int T, int D,
+                       void* stream, int dtype, int gate_dtype) {
+    return gated_pass(true, out, log_a, state0, dout, dstate_out, dx, dlog_a, dstate0, nullptr, B, B0, T, D, stream,
+                      dtype, gate_dtype);
+}
+
+int lla_gated_backward_varlen(const void* log_a, const void* out, const float* state0, const void* dout,
+                              const float* dstate_out, void* dx, void* dlog_a, float* dstate0,
+                              const int32_t* cu_seqlens, int n_seq, int n0, int total_T, int D, void* stream, int dtype,
+                              int gate_dtype) {
+    if (!cu_seqlens) return LLA_ERR_INVALID_ARG;
+    return gated_pass(true, out, log_a, state0, dout, dstate_out, dx, dlog_a, dstate0, cu_seqlens, n_seq, n0, total_T, D,
+                      stream, dtype, gate_dtype);
+}
+
+int lla_gated_decode_step(const void* x, const void* log_a, float* state, void* out, void* stream, int B, int D,
+                          int dtype, int gate_dtype) {
+    if (!x || !log_a || !state || !out || any_misaligned({x, log_a, state, out})) return LLA_ERR_INVALID_ARG;
+    const int st = validate_gated(dtype, gate_dtype, B, D);
+    if (st != LLA_OK) return st;
+    const size_t size = (size_t)B * D;
+    if (clash({{out, size * type_bytes(dtype)}, {state, size * sizeof(float)}},
+              {{x, size * type_bytes(dtype)}, {log_a, size * gate_bytes(gate_dtype)}}))
+        return LLA_ERR_INVALID_ARG;
+    if (current_device() < 0) return LLA_ERR_CUDA;
+    return report(lla::gated_decode_step(dtype, gate_dtype, x, log_a, state, out, (int64_t)size,
+                                         static_cast<cudaStream_t>(stream)));
+}
+
+int lla_gated_decode_tree(const void* x, const void* log_a, const float* state, const int32_t* parent, void* out,
+                          void* stream, int B, int BP, int N, int D, int dtype, int gate_dtype) {
+    if (!x || !log_a || !state || !parent || !out || any_misaligned({x, log_a, state, parent, out}))
+        return LLA_ERR_INVALID_ARG;
+    if (B < 1 || N < 1 || (BP != 1 && BP != B)) return LLA_ERR_INVALID_ARG;
+    const int st = validate_gated(dtype, gate_dtype, (int64_t)B * N, D);
+    if (st != LLA_OK) return st;
+    if (N > lla::kMaxTree || B > 65535) return LLA_ERR_UNSUPPORTED;
+    const size_t size = (size_t)B * N * D;
+    if (clash({{out, size * type_bytes(dtype)}},
+              {{x, size * type_bytes(dtype)}, {log_a, size * gate_bytes(gate_dtype)},
+               {state, (size_t)B * D * sizeof(float)}, {parent, (size_t)BP * N * sizeof(int32_t)}}))
+        return LLA_ERR_INVALID_ARG;
+    const int dev = current_device();
+    if (dev < 0) return LLA_ERR_CUDA;
+    int* err = error_word(dev);
+    if (!err) return LLA_ERR_CUDA;
+    return report(lla::gated_decode_tree(dtype, gate_dtype, x, log_a, state, parent, out, B, BP, N, D, err,
+                                         static_cast<cudaStream_t>(stream)));
+}
+
+int lla_gated_decode_commit(const void* x, const void* log_a, float* state, const int32_t* count, const int32_t* path,
+                            void* stream, int B, int N, int M, int D, int dtype, int gate_dtype) {
+    if (!x || !log_a || !state || !count || any_misaligned({x, log_a, state, count, path})) return LLA_ERR_INVALID_ARG;
+    if (B < 1 || N < 1 || (path ? M < 1 : M != 0)) return LLA_ERR_INVALID_ARG;
+    const int st = validate_gated(dtype, gate_dtype, (int64_t)B * N, D);
+    if (st != LLA_OK) return st;
+    if (!path) M = N;
+    if (N > lla::kMaxTree || M > lla::kMaxTree || B > 65535) return LLA_ERR_UNSUPPORTED;
+    const size_t size = (size_t)B * N * D;
+    if (clash({{state, (size_t)B * D * sizeof(float)}},
+              {{x, size * type_bytes(dtype)}, {log_a, size * gate_bytes(gate_dtype)}, {count, B * sizeof(int32_t)},
+               {path, (size_t)B * M * sizeof(int32_t)}}))
+        return LLA_ERR_INVALID_ARG;
+    const int dev = current_device();
+    if (dev < 0) return LLA_ERR_CUDA;
+    int* err = error_word(dev);
+    if (!err) return LLA_ERR_CUDA;
+    return report(lla::gated_decode_commit(dtype, gate_dtype, x, log_a, state, count, path, B, N, M, D, err,
+                                           static_cast<cudaStream_t>(stream)));
+}
+
+int lla_decode_tree(const void* q, const void* k, const void* v, const float* log_a, const float* lambda,
+                    const float* fenwick_states, const int64_t* t, const int32_t* parent, void* out, void* stream, int B,
+                    int BP, int H, int N, int dk, int dv, int Lmax, int dtype) {
+    return tree_call({q, k, v, log_a, lambda, fenwick_states, t, parent, out, B, BP, H, N, dk, dv, Lmax, nullptr}, false,
+                     stream, dtype);
+}
+
+int lla_decode_commit(const void* k, const void* v, const float* log_a, float* fenwick_states, const int64_t* t,
+                      const int32_t* count, const int32_t* path, void* stream, int B, int H, int N, int M, int dk, int dv,
+                      int Lmax, int dtype) {
+    return commit_call({k, v, log_a, fenwick_states, t, count, path, B, H, N, M, dk, dv, Lmax, nullptr}, false, stream,
+                       dtype);
+}
+
+int lla_linear_decode_tree(const void* q, const void* k, const void* v, const float* log_a, const float* state,
+                           const int32_t* parent, void* out, void* stream, int B, int BP, int H, int N, int dk, int dv,
+                           int dtype) {
+    return tree_call({q, k, v, log_a, nullptr, state, nullptr, parent, out, B, BP, H, N, dk, dv, 1, nullptr}, true,
+                     stream, dtype);
+}
+
+int lla_linear_decode_commit(const void* k, const void* v, const float* log_a, float* state, const int32_t* count,
+                             const int32_t* path, void* stream, int B, int H, int N, int M, int dk, int dv, int dtype) {
+    return commit_call({k, v, log_a, state, nullptr, count, path, B, H, N, M, dk, dv, 1, nullptr}, true, stream, dtype);
 }
 
 }  // extern "C"
