@@ -444,7 +444,9 @@ int lla_decode_step_shared(const void* q, const void* k, const void* v, const fl
  *   in place (h_{t-1} on entry, h_t on return; what the prompt left in state_out).
  *
  * Limits: rows x D up to 2^40; T (packed: total_T) up to 2^31 - 2^16. Workspace: only for dstate0 with B0 = 1
- * (B D floats, the library's pool).
+ * (B D floats, the library's pool). A bounded wait that runs out is reported by lla_device_error as
+ * LLA_ERR_TIMEOUT. Fastest where rows of x and log_a are multiples of 16 bytes (copied by TMA); then where D is
+ * a multiple of 4.
  */
 int lla_gated_forward(const void* x, const void* log_a, const float* state0, void* out, float* state_out, int B, int B0,
                       int T, int D, void* stream, int dtype, int gate_dtype);
@@ -515,8 +517,8 @@ int lla_gated_decode_commit(const void* x, const void* log_a, float* state, cons
 /*
  * Test hook for the failure path of the bounded waits (no counterpart on the
  * pages; not for production use). On the current device, for the tensor-core
- * prefill output kernel of dv = 64 and the tensor-core kernels of linear
- * attention: limit_cycles > 0 bounds each of its pipeline
+ * prefill output kernel of dv = 64, the tensor-core kernels of linear
+ * attention and the passes of the gated recurrence: limit_cycles > 0 bounds each of its pipeline
  * waits to that many SM cycles (<= 0 restores the default, about 2 s at the
  * maximum clock); hold != 0 makes its epilogue (where only states are formed,
  * the warps that hold the state) first wait on a barrier that nothing arrives

@@ -8,34 +8,82 @@
 // h comes from the forward's outputs as they were kept (rounded to their type), so one pass does.
 //
 // A stretch of rows is the map h -> A h + s with A the product of its gates; maps of neighbours compose. One thread
-// block cluster walks 64 channels of one sequence from end to end in steps of (cluster size) x 128 rows: a thread
-// keeps 8 rows of 4 channels, forms their map, the block composes its 16 stretches, the blocks hand their maps to
-// one another through distributed shared memory, and every thread runs its rows again from the state that enters
-// them. Blocks of a cluster are resident together, so nothing waits for a block that may not run yet, and neither
-// flags nor workspace are needed. Maps are composed in one fixed order: repeated calls give identical bits.
+// block cluster walks 64 (32, 16) channels of one sequence from end to end in steps of (cluster size) x 128 (256, 512)
+// rows: a thread keeps 8 rows of 4 channels, forms their map, the warps and the block compose them, the blocks send their
+// maps to one another through distributed shared memory, and every thread runs its rows again from the state that enters
+// them. Blocks of a cluster are resident together, so nothing waits for a block that may not run yet, and neither flags
+// nor workspace are needed. Maps are composed in one fixed order: repeated calls give identical bits.
+//
+// Bound by HBM: 4 x 8192 x 1024, bf16 with fp32 gates, 43 us for 268 MB (92% of the copy rate), gradients 76 us for 470 MB
+// (91%); 65536 x 1024 with bf16 gates 68 us for 403 MB (88%; a step's latency, about 2 us with the exchange, shows). What
+// got it there: tiles by TMA two steps ahead (69 us with per-thread asynchronous copies, which cost a quarter of all
+// instructions and pass through L1), the exchange by stores that signal a barrier (a cluster barrier waits for the step's
+// stores to global memory besides: 0.7 us a step), steps without questions asked of a row, two channels to an instruction.
 //
 // Packed sequences are one row axis: a map that holds a sequence's first row does not depend on what enters. Its A is
 // kept as -1 (a product of exponentials is never negative), so that not even an infinity or NaN crosses over.
 #include "lla_drafts.cuh"
+#include "lla_linear.cuh"
 #include "lla_tc_ptx.cuh"
 
 namespace lla {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kV = 4;                    // channels of a thread
-constexpr int kL = 8;                    // rows of a thread
-constexpr int kLanes = 16;               // threads side by side on one row
-constexpr int kCols = kLanes * kV;       // channels of a block
-constexpr int kSegs = kThreads / kLanes; // stretches of a block
-constexpr int kRows = kSegs * kL;        // rows of a block
+constexpr int kWarps = kThreads / 32;
 constexpr int kMaxCluster = 8;
+constexpr int kFill = 152;    // blocks that a call should have: one for each SM of the GPU
+constexpr int kMaxBox = 256;  // rows of a TMA copy
+
+// How rows come to a thread: through shared memory by TMA (rows of a multiple of 16 bytes), or by its own loads a step
+// ahead, four channels at a time (D a multiple of 4) or one.
+enum Path { kTma, kQuads, kSingles };
+
+// Cut of a block: kLanes threads side by side, four channels each; every thread kL rows. kStages steps' tiles are in flight.
+template <typename T, typename G, bool kBack, int kPath>
+struct Cut {
+    static constexpr int row_bytes = 4 * (sizeof(G) + sizeof(T) * (kBack ? 2 : 1));  // of a thread's row
+    static constexpr int kL = kPath == kTma ? 8 : 4;  // kTma with 4 and three stages: 49 us against 43 (4 x 8192 x 1024)
+    static constexpr int kStages = 2;
+    static constexpr int stage_bytes = row_bytes * kL * kThreads;
+    static constexpr int kResident = kPath == kTma && stage_bytes * kStages > 110000 ? 1 : 2;  // blocks of an SM
+};
 
 struct Args {
+    CUtensorMap map[3];  // kTma: gates; inputs (backward: dout); backward: the forward's outputs
     GatedPass p;
-    int cluster, cols, steps;
+    int cluster, cols;
+    int spans;  // packed: parts of the row axis, cut where sequences begin
+    LinWaits waits;
     int* err;
 };
+
+// Four channels as two register pairs: one instruction for two of them.
+struct Quad {
+    f32x2 lo, hi;
+};
+__device__ __forceinline__ Quad quad(const float (&f)[4]) { return {pair2(f[0], f[1]), pair2(f[2], f[3])}; }
+__device__ __forceinline__ void split(const Quad& q, float (&f)[4]) {
+    const float2 a = split2(q.lo), b = split2(q.hi);
+    f[0] = a.x; f[1] = a.y; f[2] = b.x; f[3] = b.y;
+}
+__device__ __forceinline__ Quad mul(const Quad& a, const Quad& b) { return {mul2(a.lo, b.lo), mul2(a.hi, b.hi)}; }
+__device__ __forceinline__ Quad fma(const Quad& a, const Quad& b, const Quad& c) {
+    return {fma2(a.lo, b.lo, c.lo), fma2(a.hi, b.hi, c.hi)};
+}
+__device__ __forceinline__ float power2(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+__device__ __forceinline__ Quad gate(const Quad& log_a) {  // exp
+    const f32x2 k = pair2(kLog2e, kLog2e);
+    float f[4];
+    split({mul2(log_a.lo, k), mul2(log_a.hi, k)}, f);
+#pragma unroll
+    for (int v = 0; v < 4; v++) f[v] = power2(f[v]);
+    return quad(f);
+}
 
 template <typename T> struct Four;  // four neighbouring values as they lie in memory
 template <> struct Four<float> { using raw = float4; };
@@ -57,16 +105,16 @@ __device__ __forceinline__ void put4(__nv_bfloat16* p, const float (&f)[4]) {
     *reinterpret_cast<uint2*>(p) = r;
 }
 
-// Four channels of a row: neighbours (kVec; D a multiple of 4), or 16 apart, so that a scalar access of 16 threads is one
-// stretch of memory.
-template <bool kVec>
+// Four channels of a row: neighbours (kVec; D a multiple of 4), or kLanes apart, so that a scalar access of kLanes threads
+// is one stretch of memory.
+template <bool kVec, int kLanes>
 struct Chan {
     int c[4];
     bool any;
     int D;
     __device__ __forceinline__ Chan(int col, int lane, int D_) : D(D_) {
 #pragma unroll
-        for (int v = 0; v < 4; v++) c[v] = col * kCols + (kVec ? lane * 4 + v : lane + 16 * v);
+        for (int v = 0; v < 4; v++) c[v] = col * kLanes * 4 + at(lane, v);
         any = c[0] < D;
     }
     template <typename T> __device__ __forceinline__ void load(const T* row, float (&f)[4]) const {
@@ -89,7 +137,7 @@ struct Chan {
         }
     }
     // place of the v-th channel among the block's
-    __device__ __forceinline__ static int at(int lane, int v) { return kVec ? lane * 4 + v : lane + 16 * v; }
+    __device__ __forceinline__ static int at(int lane, int v) { return kVec ? lane * 4 + v : lane + kLanes * v; }
 };
 
 __device__ __forceinline__ uint32_t cluster_rank() {
@@ -97,12 +145,45 @@ __device__ __forceinline__ uint32_t cluster_rank() {
     asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
     return r;
 }
-__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
-__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
-__device__ __forceinline__ void store_remote(uint32_t at, uint32_t rank, float x, float y) {
-    uint32_t r;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(at), "r"(rank));
-    asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(r), "f"(x), "f"(y) : "memory");
+// All blocks of the cluster have got here. No order of memory goes with it (kInit: but the barriers set up before it), so
+// nobody waits for stores to global memory to land.
+template <bool kInit>
+__device__ __forceinline__ void cluster_meet() {
+    if (kInit) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    else asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// (x, y) to the place `at` of block `rank`, counted by that block's barrier `bar` when it is there
+__device__ __forceinline__ void send(uint32_t at, uint32_t bar, uint32_t rank, float x, float y) {
+    uint32_t to, sign;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(to) : "r"(at), "r"(rank));
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(sign) : "r"(bar), "r"(rank));
+    asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v2.f32 [%0], {%1, %2}, [%3];" ::"r"(to),
+                 "f"(x), "f"(y), "r"(sign)
+                 : "memory");
+}
+__device__ __forceinline__ bool arrived(uint64_t* bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity), "n"(kSuspendNs)
+        : "memory");
+    return ok != 0;
+}
+
+// Bounded wait for a phase of a barrier; what ran out is recorded.
+__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, long long limit, int* err) {
+    if (arrived(bar, parity)) return true;
+    const long long start = clock64();
+    while (!arrived(bar, parity))
+        if (clock64() - start > limit) {
+            record_error(err, kDevTimeout);
+            return false;
+        }
+    return true;
 }
 
 // (A, s) <- (A2, s2) after (A, s)
@@ -123,46 +204,111 @@ __device__ __forceinline__ float apply(float A, float s, float h) {
 
 // What a row of a packed call is: its sequence, and whether that one's walk begins or ends there. -1: no sequence's.
 constexpr int kBegins = 1 << 30, kEnds = 1 << 29, kSeq = kEnds - 1;
-template <bool kBack>
-__device__ __forceinline__ int row_info(const int32_t* cu, int n, int row) {
-    int lo = 0, hi = n;  // the last i with cu[i] <= row
-    if (row < cu[0] || row >= cu[n]) return -1;
+// The last entry of cu that is not behind the row is at `lo` or above, below `hi`; at(i) is entry i, and one in front of the
+// table (i = -1) is in front of every row.
+template <bool kBack, typename At>
+__device__ __forceinline__ int row_info(At at, int lo, int hi, int n, int row) {
     while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
-        if (cu[mid] <= row) lo = mid;
+        if (at(mid) <= row) lo = mid;
         else hi = mid;
     }
-    const bool first = row == cu[lo], last = row == cu[lo + 1] - 1;
+    if (lo < 0 || lo >= n) return -1;
+    const bool first = row == at(lo), last = row == at(lo + 1) - 1;
     return lo | ((kBack ? last : first) ? kBegins : 0) | ((kBack ? first : last) ? kEnds : 0);
 }
+constexpr int kWindow = 32;  // entries of cu around a block's rows
 
-template <typename T, typename G, bool kBack, bool kPacked, bool kVec>
-__global__ void __launch_bounds__(kThreads, 2) gated_scan(const Args a) {
-    __shared__ __align__(16) float seg_a[2][kSegs][kCols], seg_s[2][kSegs][kCols];
+// Four channels of a row as they lie in memory, loaded before they are needed.
+template <typename T, bool kVec>
+struct Ahead;
+template <typename T>
+struct Ahead<T, true> {
+    typename Four<T>::raw r;
+    __device__ __forceinline__ void load(const T* row, const Chan<true, 16>& ch) {
+        if (ch.any) r = __ldg(reinterpret_cast<const typename Four<T>::raw*>(row + ch.c[0]));
+    }
+    __device__ __forceinline__ void get(float (&f)[4]) const { widen(r, f); }
+};
+template <typename T>
+struct Ahead<T, false> {
+    T r[4];
+    __device__ __forceinline__ void load(const T* row, const Chan<false, 16>& ch) {
+#pragma unroll
+        for (int v = 0; v < 4; v++)
+            if (ch.c[v] < ch.D) r[v] = row[ch.c[v]];
+    }
+    __device__ __forceinline__ void get(float (&f)[4]) const {
+#pragma unroll
+        for (int v = 0; v < 4; v++) f[v] = load_f(&r[v]);
+    }
+};
+
+template <typename T, typename G, bool kBack, bool kPacked, int kPath, int kLanes>
+__global__ void __launch_bounds__(kThreads, 2) gated_scan(const __grid_constant__ Args a) {
+    using C = Cut<T, G, kBack, kPath>;
+    constexpr bool kVec = kPath != kSingles;
+    using Ch = Chan<kVec, kLanes>;
+    constexpr int kCols = kLanes * 4;               // channels of a block
+    constexpr int kL = C::kL, kStages = C::kStages;
+    constexpr int kRows = kThreads / kLanes * kL;   // rows of a block
+    constexpr int kStep = 32 / kLanes;              // stretches of a warp
+    constexpr int kBoxRows = kRows < kMaxBox ? kRows : kMaxBox;
+    __shared__ __align__(16) float warp_a[2][kWarps][kCols], warp_s[2][kWarps][kCols];
     __shared__ __align__(16) float2 part[2][kMaxCluster][kCols];
     __shared__ __align__(16) float carry[2][kCols];
     __shared__ int info[2][kPacked ? kRows : 1];
+    __shared__ int bounds[4], plain_of[2], near[2], window[2][kPacked ? kWindow : 1];
+    __shared__ __align__(8) uint64_t come[2], full[kStages], never;
+    extern __shared__ __align__(128) char staged[];
     const GatedPass& p = a.p;
-    const int tid = threadIdx.x, lane = tid % kLanes, seg = tid / kLanes;
+    const int tid = threadIdx.x, lane = tid % kLanes, seg = tid / kLanes, warp = tid / 32;
     const int R = p.T, D = p.D, cs = a.cluster;
     const int rank = cs > 1 ? static_cast<int>(cluster_rank()) : 0;
-    const int walk = blockIdx.x / cs;  // cluster: a column of one sequence
+    const int walk = blockIdx.x / cs;  // cluster: a column of one sequence (packed: of one span)
     const int col = walk % a.cols, b = walk / a.cols;
-    const Chan<kVec> ch(col, lane, D);
+    const Ch ch(col, lane, D);
+    int lo = 0, hi = R;  // the walk's rows
     if (kPacked) {
+        // a span's sequences are those that begin in its even share of the rows; the first and the last one also have the
+        // rows of no sequence before and behind
+        const int64_t cut0 = static_cast<int64_t>(R) * b / a.spans, cut1 = static_cast<int64_t>(R) * (b + 1) / a.spans;
+        if (tid < 4) bounds[tid] = tid < 2 ? R : 0;
+        __syncthreads();
         bool bad = false;
+        int first = R, next = R, before = 0, upto = 0;
         for (int i = tid; i <= p.n; i += kThreads) {
             const int x = p.cu[i];
             bad |= x < 0 || x > R || (i > 0 && x < p.cu[i - 1]);
+            if (x < cut0) before++;
+            else if (x < first) first = x;
+            if (x < cut1) upto++;
+            else if (x < next) next = x;
         }
+        atomicMin(&bounds[0], first);
+        atomicMin(&bounds[1], next);
+        atomicAdd(&bounds[2], before);
+        atomicAdd(&bounds[3], upto);
         if (__syncthreads_or(bad)) {  // every block finds the same
             if (blockIdx.x == 0 && tid == 0) record_error(a.err, kDevBadInput);
             return;
         }
+        lo = b == 0 ? 0 : bounds[0];
+        hi = b == a.spans - 1 ? R : bounds[1];
     }
+    const int len = hi - lo, steps = (len + cs * kRows - 1) / (cs * kRows);
+    if (tid == 0) {
+        mbar_init(&come[0], 1);
+        mbar_init(&come[1], 1);
+        mbar_init(&never, 1);
+        for (int i = 0; i < kStages; i++) mbar_init(&full[i], 1);
+        fence_mbar_init();
+    }
+    if (cs > 1) cluster_meet<true>();
+    else __syncthreads();
     const float* enter = kBack ? p.dstate_out : p.state0;  // what a walk begins with
-    const int64_t row0 = static_cast<int64_t>(b) * R;
-    const T* xp = static_cast<const T*>(p.x) + row0 * D;
+    const int64_t row0 = kPacked ? 0 : static_cast<int64_t>(b) * R;
+    const T* xp = static_cast<const T*>(p.x) + row0 * D;  // inputs; backward: outputs of the forward
     const G* gp = static_cast<const G*>(p.log_a) + row0 * D;
     const T* dp = kBack ? static_cast<const T*>(p.dout) + row0 * D : nullptr;
     T* op = static_cast<T*>(p.out) + row0 * D;
@@ -170,8 +316,47 @@ __global__ void __launch_bounds__(kThreads, 2) gated_scan(const Args a) {
     auto enters = [&](int i) { return enter + static_cast<int64_t>(kBack || p.n0 > 1 ? i : 0) * D; };
     auto first_state = [&](int i) { return p.state0 + static_cast<int64_t>(p.n0 > 1 ? i : 0) * D; };
 
+    // Rows a step ahead. kTma: the block's tiles, rows in the order of memory, in one stage: gates, inputs (backward: dout),
+    // and backward the outputs of the row before. Parts of a tile outside the walk belong to others or to nobody and are
+    // not used.
+    constexpr int kGBytes = kRows * kCols * sizeof(G), kXBytes = kRows * kCols * sizeof(T);
+    Ahead<G, kVec> ga[kPath == kTma ? 1 : kL];
+    Ahead<T, kVec> xa[kPath == kTma ? 1 : kL], ha[kPath == kTma || !kBack ? 1 : kL];
+    int issued = 0;  // kTma, thread 0: steps whose tiles are on their way or there
+    auto prefetch = [&](int st) {
+        if (st >= steps) return;
+        if constexpr (kPath == kTma) {
+            if (tid == 0) {
+                char* to = staged + (st % kStages) * C::stage_bytes;
+                uint64_t* bar = &full[st % kStages];
+                const int u = (st * cs + rank) * kRows;
+                const int y = static_cast<int>(row0) + (kBack ? hi - u - kRows : lo + u);
+                mbar_expect_tx(bar, kGBytes + (kBack ? 2 : 1) * kXBytes);
+                for (int r = 0; r < kRows; r += kBoxRows) {
+                    tma_load_2d(to + r * kCols * sizeof(G), &a.map[0], bar, col * kCols, y + r);
+                    tma_load_2d(to + kGBytes + r * kCols * sizeof(T), &a.map[1], bar, col * kCols, y + r);
+                    if (kBack) tma_load_2d(to + kGBytes + kXBytes + r * kCols * sizeof(T), &a.map[2], bar, col * kCols, y + r - 1);
+                }
+                issued = st + 1;
+            }
+        } else {
+            const int u0 = (st * cs + rank) * kRows + seg * kL;
+#pragma unroll
+            for (int j = 0; j < kL; j++) {
+                const int u = u0 + j;
+                const int64_t off = static_cast<int64_t>(kBack ? hi - 1 - u : lo + u) * D;
+                if (u < len) {
+                    ga[j].load(gp + off, ch);
+                    xa[j].load((kBack ? dp : xp) + off, ch);
+                    if (kBack && off > 0) ha[kBack ? j : 0].load(xp + off - D, ch);
+                }
+            }
+        }
+    };
+    for (int st = 0; st < (kPath == kTma ? kStages : 1); st++) prefetch(st);
+
     if (kPacked && p.leave) {  // empty sequences: what enters leaves
-        for (int i = rank * kSegs + seg; i < p.n; i += cs * kSegs) {
+        for (int i = (b * cs + rank) * (kThreads / kLanes) + seg; i < p.n; i += a.spans * cs * (kThreads / kLanes)) {
             if (p.cu[i] != p.cu[i + 1]) continue;
             float f[4] = {0.f, 0.f, 0.f, 0.f};
             if (enter) ch.load(enters(i), f);
@@ -183,77 +368,172 @@ __global__ void __launch_bounds__(kThreads, 2) gated_scan(const Args a) {
     float state = 0.f;
     if (!kPacked && enter && tid < kCols && my_col < D) state = enters(b)[my_col];
 
-    for (int st = 0; st < a.steps; st++) {
+    // Packed: the last warp finds ahead of each step whether a sequence begins or ends in the block's rows [y, y + kRows),
+    // and lays out the entries of cu around them: `entry` follows the walk, the first one that is not before y.
+    int entry = kPacked ? bounds[kBack ? 3 : 2] : 0;
+    auto look = [&](int st) {
+        const int u = (st * cs + rank) * kRows, l = tid & 31, y = kBack ? hi - u - kRows : lo + u;
+        for (int n = 32; n == 32;) {
+            const int i = kBack ? entry - 1 - l : entry + l;
+            const int x = i < 0 || i > p.n ? 0 : p.cu[i];
+            n = __popc(__ballot_sync(0xffffffffu, i >= 0 && i <= p.n && (kBack ? x >= y : x < y)));
+            entry += kBack ? -n : n;
+        }
+        const int e = entry - 1 + l, x = e < 0 ? -1 : e > p.n ? 0x7fffffff : p.cu[e];
+        window[st & 1][l] = x;
+        if (l == 0) near[st & 1] = entry - 1;
+        if (l == 1) plain_of[st & 1] = entry > 0 && entry <= p.n && x > y + kRows;
+        // states that walks begin with in these rows
+        if (enter && e >= 0 && e < p.n && (kBack ? x < y + kRows : l > 0 && x < y + kRows)) prefetch_l1(enters(e) + col * kCols);
+    };
+    if (kPacked) {
+        if (warp == kWarps - 1) look(0);
+        __syncthreads();
+    }
+
+    // After a wait that ran out a walk goes on to its end without waiting, sending or copying, its values undefined.
+    bool in_time = !a.waits.hold || wait(&never, 0, a.waits.cycles, a.err);
+    for (int st = 0; st < steps; st++) {
         const int buf = st & 1;
-        const int u0 = (st * cs + rank) * kRows + seg * kL;  // first of this thread's rows, in walking order
+        const int block0 = (st * cs + rank) * kRows, u0 = block0 + seg * kL;
+        // Whether the block's rows and channels are all there and no row is a sequence's first or last: the common step,
+        // without a question asked of a row.
+        bool plain = kVec && (col + 1) * kCols <= D && block0 + kRows <= len - (kBack && !kPacked ? 1 : 0);
         if (kPacked) {
-            if (tid < kRows) {
-                const int u = (st * cs + rank) * kRows + tid;
-                info[buf][tid] = u < R ? row_info<kBack>(p.cu, p.n, kBack ? R - 1 - u : u) : -1;
-            }
-            __syncthreads();
-        }
-        float g[kL][4], x[kL][4], hp[kL][4];
-#pragma unroll
-        for (int j = 0; j < kL; j++) {
-            const int u = u0 + j, row = kBack ? R - 1 - u : u;
-            const bool in = u < R && (!kPacked || info[buf][seg * kL + j] >= 0);
-#pragma unroll
-            for (int v = 0; v < 4; v++) g[j][v] = x[j][v] = hp[j][v] = 0.f;
-            if (in) {
-                ch.load(gp + static_cast<int64_t>(row) * D, g[j]);
-                ch.load((kBack ? dp : xp) + static_cast<int64_t>(row) * D, x[j]);
-                if (kBack) {
-                    const bool first = kPacked ? (info[buf][seg * kL + j] & kEnds) != 0 : row == 0;
-                    if (!first) ch.load(xp + static_cast<int64_t>(row - 1) * D, hp[j]);
-                    else if (p.state0) ch.load(first_state(kPacked ? info[buf][seg * kL + j] & kSeq : b), hp[j]);
+            plain &= plain_of[buf] != 0;
+            if (!plain) {
+                const int base = near[buf];  // entry of window[buf][0]
+                const bool enough = window[buf][kWindow - 1] > (kBack ? hi - block0 : lo + block0 + kRows);
+                for (int i = tid; i < kRows; i += kThreads) {
+                    const int u = block0 + i, row = kBack ? hi - 1 - u : lo + u;
+                    int inf = -1;
+                    if (u < len && enough)
+                        inf = row_info<kBack>([&](int e) { return window[buf][e - base]; }, base, base + kWindow - 1, p.n, row);
+                    else if (u < len)
+                        inf = row_info<kBack>([&](int e) { return e < 0 ? -1 : p.cu[e]; }, base, p.n + 1, p.n, row);
+                    info[buf][i] = inf;
                 }
+                __syncthreads();
             }
         }
-        float A[4] = {1.f, 1.f, 1.f, 1.f}, s[4] = {0.f, 0.f, 0.f, 0.f};
+        // places of this thread's first row in the stage, and from one row to the next
+        constexpr int kNextG = (kBack ? -1 : 1) * kCols * static_cast<int>(sizeof(G));
+        constexpr int kNextX = (kBack ? -1 : 1) * kCols * static_cast<int>(sizeof(T));
+        const int at = (kBack ? kRows - 1 - seg * kL : seg * kL) * kCols + lane * 4;
+        const char* sg = staged + (st % kStages) * C::stage_bytes + at * sizeof(G);
+        const char* sx = staged + (st % kStages) * C::stage_bytes + kGBytes + at * sizeof(T);
+        auto gates_of = [&](int j, float (&f)[4]) {
+            if constexpr (kPath == kTma) widen(*reinterpret_cast<const typename Four<G>::raw*>(sg + j * kNextG), f);
+            else ga[j].get(f);
+        };
+        auto inputs_of = [&](int j, float (&f)[4]) {
+            if constexpr (kPath == kTma) widen(*reinterpret_cast<const typename Four<T>::raw*>(sx + j * kNextX), f);
+            else xa[j].get(f);
+        };
+        Quad g[kL], x[kL];
+        Ahead<T, kVec> hp[kBack ? kL : 1];
+        float A[4], s[4];
+        if (kPath == kTma && in_time) in_time = wait(&full[st % kStages], (st / kStages) & 1, a.waits.cycles, a.err);
+        if (kBack) {
 #pragma unroll
-        for (int j = 0; j < kL; j++) {
-            const bool begins = kPacked && info[buf][seg * kL + j] >= 0 && (info[buf][seg * kL + j] & kBegins);
-            float e[4] = {0.f, 0.f, 0.f, 0.f};
-            if (begins && enter) ch.load(enters(info[buf][seg * kL + j] & kSeq), e);
+            for (int j = 0; j < kL; j++) {
+                if constexpr (kPath == kTma) hp[j].r = *reinterpret_cast<const typename Four<T>::raw*>(sx + kXBytes + j * kNextX);
+                else hp[j] = ha[j];
+            }
+        }
+        if (plain) {
+            Quad pa, ps;
+#pragma unroll
+            for (int j = 0; j < kL; j++) {
+                float f[4];
+                gates_of(j, f);
+                g[j] = gate(quad(f));
+                inputs_of(j, f);
+                x[j] = quad(f);
+                const Quad in = kBack ? mul(g[j], x[j]) : x[j];
+                ps = j == 0 ? in : fma(g[j], ps, in);
+                pa = j == 0 ? g[j] : mul(g[j], pa);
+            }
+            split(pa, A);
+            split(ps, s);
+        } else {
 #pragma unroll
             for (int v = 0; v < 4; v++) {
-                g[j][v] = expf(g[j][v]);
-                if (begins) {
-                    s[v] = e[v];
-                    A[v] = -1.f;
+                A[v] = 1.f;
+                s[v] = 0.f;
+            }
+#pragma unroll
+            for (int j = 0; j < kL; j++) {
+                const int inf = kPacked ? info[buf][seg * kL + j] : 0;
+                float gf[4] = {0.f, 0.f, 0.f, 0.f}, xf[4] = {0.f, 0.f, 0.f, 0.f};
+                if (u0 + j < len && (!kPacked || inf >= 0)) {
+                    gates_of(j, gf);
+                    inputs_of(j, xf);
+                    if (kPacked && (inf & kBegins)) {
+#pragma unroll
+                        for (int v = 0; v < 4; v++) {
+                            A[v] = -1.f;
+                            s[v] = 0.f;
+                        }
+                        if (enter) ch.load(enters(inf & kSeq), s);
+                    }
                 }
-                if (kBack) s[v] = g[j][v] * (x[j][v] + s[v]);
-                else s[v] = fmaf(g[j][v], s[v], x[j][v]);
-                if (!kPacked || A[v] >= 0.f) A[v] *= g[j][v];
+                g[j] = gate(quad(gf));
+                x[j] = quad(xf);
+                split(g[j], gf);
+#pragma unroll
+                for (int v = 0; v < 4; v++) {
+                    s[v] = kBack ? fmaf(gf[v], s[v], gf[v] * xf[v]) : fmaf(gf[v], s[v], xf[v]);
+                    if (!kPacked || A[v] >= 0.f) A[v] *= gf[v];
+                }
             }
         }
+        if (kPath != kTma) prefetch(st + 1);
+        // the maps of the warp's stretches up to this thread's, and before it
+        float ea[4], es[4];
 #pragma unroll
         for (int v = 0; v < 4; v++) {
-            seg_a[buf][seg][Chan<kVec>::at(lane, v)] = A[v];
-            seg_s[buf][seg][Chan<kVec>::at(lane, v)] = s[v];
+#pragma unroll
+            for (int d = kLanes; d < 32; d *= 2) {
+                const float pa = __shfl_up_sync(0xffffffffu, A[v], d), ps = __shfl_up_sync(0xffffffffu, s[v], d);
+                if ((tid & 31) >= d) {
+                    float na = pa, ns = ps;
+                    compose<kPacked>(na, ns, A[v], s[v]);
+                    A[v] = na;
+                    s[v] = ns;
+                }
+            }
+            ea[v] = __shfl_up_sync(0xffffffffu, A[v], kLanes);
+            es[v] = __shfl_up_sync(0xffffffffu, s[v], kLanes);
+        }
+        if ((tid & 31) / kLanes == kStep - 1) {
+#pragma unroll
+            for (int v = 0; v < 4; v++) {
+                warp_a[buf][warp][Ch::at(lane, v)] = A[v];
+                warp_s[buf][warp][Ch::at(lane, v)] = s[v];
+            }
         }
         __syncthreads();
-        float own_a = 1.f, own_s = 0.f;
+        if (kPath == kTma && in_time) prefetch(st + kStages);  // into the stage that all have read
+        if (kPacked && warp == kWarps - 1 && st + 1 < steps) look(st + 1);
         if (tid < kCols) {
+            float own_a = 1.f, own_s = 0.f;
 #pragma unroll
-            for (int i = 0; i < kSegs; i++) {
-                const float A2 = seg_a[buf][i][tid], s2 = seg_s[buf][i][tid];
-                seg_a[buf][i][tid] = own_a;
-                seg_s[buf][i][tid] = own_s;
+            for (int i = 0; i < kWarps; i++) {
+                const float A2 = warp_a[buf][i][tid], s2 = warp_s[buf][i][tid];
+                warp_a[buf][i][tid] = own_a;
+                warp_s[buf][i][tid] = own_s;
                 compose<kPacked>(own_a, own_s, A2, s2);
             }
             if (cs > 1) {
-                const uint32_t at = static_cast<uint32_t>(__cvta_generic_to_shared(&part[buf][rank][tid]));
-                for (int r = 0; r < cs; r++) store_remote(at, r, own_a, own_s);
-            }
-        }
-        if (cs > 1) {
-            cluster_arrive();
-            cluster_wait();
-        }
-        if (tid < kCols) {
-            if (cs > 1) {
+                // A place is written again two steps later, by a thread that has by then what this one's block sent a step
+                // later, after it had read the place.
+                if (in_time) {
+                    if (tid == 0) mbar_expect_tx(&come[buf], static_cast<uint32_t>(cs) * kCols * sizeof(float2));
+                    const uint32_t to = smem_u32(&part[buf][rank][tid]), sign = smem_u32(&come[buf]);
+                    for (int r = 0; r < cs; r++) send(to, sign, r, own_a, own_s);
+                    in_time = wait(&come[buf], (st >> 1) & 1, a.waits.cycles, a.err);
+                }
                 for (int r = 0; r < cs; r++) {
                     if (r == rank) carry[buf][tid] = state;
                     state = apply<kPacked>(part[buf][r][tid].x, part[buf][r][tid].y, state);
@@ -267,58 +547,140 @@ __global__ void __launch_bounds__(kThreads, 2) gated_scan(const Args a) {
         float h[4];
 #pragma unroll
         for (int v = 0; v < 4; v++) {
-            const int c = Chan<kVec>::at(lane, v);
-            h[v] = apply<kPacked>(seg_a[buf][seg][c], seg_s[buf][seg][c], carry[buf][c]);
+            const int c = Ch::at(lane, v);
+            h[v] = apply<kPacked>(warp_a[buf][warp][c], warp_s[buf][warp][c], carry[buf][c]);
+            if ((tid & 31) >= kLanes) h[v] = apply<kPacked>(ea[v], es[v], h[v]);
         }
+        if (plain) {
+            const int64_t first = static_cast<int64_t>(kBack ? hi - 1 - u0 : lo + u0) * D + ch.c[0];
+            const int64_t next = kBack ? -static_cast<int64_t>(D) : static_cast<int64_t>(D);
+            T* o = op + first;
+            G* da = kBack ? ap + first : nullptr;
+            Quad q = quad(h);
 #pragma unroll
-        for (int j = 0; j < kL; j++) {
-            const int u = u0 + j, row = kBack ? R - 1 - u : u;
-            const int inf = kPacked ? info[buf][seg * kL + j] : 0;
-            if (u >= R) continue;
-            if (kPacked && inf < 0) {
-                if (kBack) {  // rows of no sequence take no part in the sum that is differentiated
-                    const float z[4] = {0.f, 0.f, 0.f, 0.f};
-                    ch.store(op + static_cast<int64_t>(row) * D, z);
-                    ch.store(ap + static_cast<int64_t>(row) * D, z);
+            for (int j = 0; j < kL; j++) {
+                float f[4];
+                if constexpr (kBack) {
+                    float before[4];
+                    hp[j].get(before);
+                    q = {add2(x[j].lo, q.lo), add2(x[j].hi, q.hi)};
+                    split(q, f);
+                    put4(o, f);
+                    q = mul(g[j], q);
+                    split(mul(q, quad(before)), f);
+                    put4(da, f);
+                    da += next;
+                } else {
+                    q = fma(g[j], q, x[j]);
+                    split(q, f);
+                    put4(o, f);
                 }
-                continue;
+                o += next;
             }
-            if (kPacked && (inf & kBegins)) {
+        } else {
 #pragma unroll
-                for (int v = 0; v < 4; v++) h[v] = 0.f;
-                if (enter) ch.load(enters(inf & kSeq), h);
-            }
-            if (kBack) {
-                float d[4], da[4];
-#pragma unroll
-                for (int v = 0; v < 4; v++) {
-                    d[v] = x[j][v] + h[v];
-                    h[v] = g[j][v] * d[v];
-                    da[v] = h[v] * hp[j][v];
+            for (int j = 0; j < kL; j++) {
+                const int u = u0 + j, row = kBack ? hi - 1 - u : lo + u;
+                const int inf = kPacked ? info[buf][seg * kL + j] : 0;
+                if (u >= len) continue;
+                if (kPacked && inf < 0) {
+                    if (kBack) {  // rows of no sequence take no part in the sum that is differentiated
+                        const float z[4] = {0.f, 0.f, 0.f, 0.f};
+                        ch.store(op + static_cast<int64_t>(row) * D, z);
+                        ch.store(ap + static_cast<int64_t>(row) * D, z);
+                    }
+                    continue;
                 }
-                ch.store(op + static_cast<int64_t>(row) * D, d);
-                ch.store(ap + static_cast<int64_t>(row) * D, da);
-            } else {
+                if (kPacked && (inf & kBegins)) {
 #pragma unroll
-                for (int v = 0; v < 4; v++) h[v] = fmaf(g[j][v], h[v], x[j][v]);
-                ch.store(op + static_cast<int64_t>(row) * D, h);
+                    for (int v = 0; v < 4; v++) h[v] = 0.f;
+                    if (enter) ch.load(enters(inf & kSeq), h);
+                }
+                float gf[4], xf[4];
+                split(g[j], gf);
+                split(x[j], xf);
+                if constexpr (kBack) {
+                    float before[4] = {0.f, 0.f, 0.f, 0.f}, d[4], da[4];
+                    if (!(kPacked ? (inf & kEnds) != 0 : row == 0)) hp[j].get(before);
+                    else if (p.state0) ch.load(first_state(kPacked ? inf & kSeq : b), before);
+#pragma unroll
+                    for (int v = 0; v < 4; v++) {
+                        d[v] = xf[v] + h[v];
+                        h[v] = gf[v] * d[v];
+                        da[v] = h[v] * before[v];
+                    }
+                    ch.store(op + static_cast<int64_t>(row) * D, d);
+                    ch.store(ap + static_cast<int64_t>(row) * D, da);
+                } else {
+#pragma unroll
+                    for (int v = 0; v < 4; v++) h[v] = fmaf(gf[v], h[v], xf[v]);
+                    ch.store(op + static_cast<int64_t>(row) * D, h);
+                }
+                if (kPacked && (inf & kEnds) && p.leave) ch.store(p.leave + static_cast<int64_t>(inf & kSeq) * D, h);
             }
-            if (kPacked && (inf & kEnds) && p.leave) ch.store(p.leave + static_cast<int64_t>(inf & kSeq) * D, h);
         }
     }
     if (!kPacked && p.leave && rank == 0 && tid < kCols && my_col < D)
         p.leave[static_cast<int64_t>(b) * D + my_col] = state;
-    if (cs > 1) {  // no block leaves while another may still write to it
-        cluster_arrive();
-        cluster_wait();
-    }
+    // no block leaves while its own copies are under way, or while another may still write to it
+    if (kPath == kTma && tid == 0)
+        for (int st = issued < kStages ? 0 : issued - kStages; st < issued; st++)
+            wait(&full[st % kStages], (st / kStages) & 1, kWaitCycles, a.err);
+    if (cs > 1) cluster_meet<false>();
 }
 
-template <typename T, typename G, bool kBack, bool kPacked, bool kVec>
+// Tile map of a tensor [rows, D]
+bool tile_map(CUtensorMap* m, const void* base, bool f32, int64_t rows, int D, int cols, int box_rows) {
+    auto fn = encode_fn();
+    if (!fn) return false;
+    const cuuint64_t dims[2] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(rows)};
+    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(D) * (f32 ? 4 : 2)};
+    const cuuint32_t box[2] = {static_cast<cuuint32_t>(cols), static_cast<cuuint32_t>(box_rows)}, one[2] = {1, 1};
+    return fn(m, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims,
+              strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <typename T, typename G, bool kBack, bool kPacked, int kPath, int kLanes>
 cudaError_t launch_scan(Args& a, cudaStream_t stream) {
+    using C = Cut<T, G, kBack, kPath>;
+    auto kern = gated_scan<T, G, kBack, kPacked, kPath, kLanes>;
+    constexpr int kRows = kThreads / kLanes * C::kL;
+    a.cols = (a.p.D - 1) / (kLanes * 4) + 1;
+    const int pieces = (a.p.T - 1) / kRows + 1;
+    a.spans = kPacked ? 1 : a.p.n;
+    // The smallest cluster that gives every SM a block: an exchange costs about as much as a step of 1 us (4 x 8192 x 1024:
+    // clusters of 1, 2, 4, 8 take 60, 44, 43, 48 us; one sequence of 65536 x 1024 in 32 columns 258, 164, 86, 68).
+    // Packed sequences are cut into spans besides, for what a few waves' blocks leave to chance when lengths differ: 32
+    // sequences of 256 to 8192 rows of 1024 channels take 176 us as 2 spans of clusters of 4, 183 as one of 8, 186 as
+    // 8 spans of single blocks.
+    a.cluster = 1;
+    const int most = kPacked && a.p.n > 1 ? 4 : kMaxCluster;
+    while (a.cluster < most && static_cast<int64_t>(a.cols) * a.spans * a.cluster < kFill && a.cluster < pieces) a.cluster *= 2;
+    if (kPacked) {
+        a.spans = 128 * C::kResident / (a.cols * a.cluster);
+        if (a.spans > a.p.n) a.spans = a.p.n;
+        if (a.spans > pieces) a.spans = pieces;
+        if (a.spans < 1) a.spans = 1;
+    }
+    a.waits = linear_waits();
+    if (kPath == kTma) {
+        const int64_t rows = static_cast<int64_t>(a.p.T) * (kPacked ? 1 : a.p.n);
+        constexpr bool g32 = sizeof(G) == 4, x32 = sizeof(T) == 4;
+        constexpr int kBoxRows = kRows < kMaxBox ? kRows : kMaxBox;
+        if (!tile_map(&a.map[0], a.p.log_a, g32, rows, a.p.D, kLanes * 4, kBoxRows) ||
+            !tile_map(&a.map[1], kBack ? a.p.dout : a.p.x, x32, rows, a.p.D, kLanes * 4, kBoxRows) ||
+            (kBack && !tile_map(&a.map[2], a.p.x, x32, rows, a.p.D, kLanes * 4, kBoxRows)))
+            return cudaErrorInvalidValue;
+    }
+    const int64_t walks = static_cast<int64_t>(a.cols) * a.spans;
+    const int smem = kPath == kTma ? C::stage_bytes * (pieces <= a.cluster ? 1 : C::kStages) : 0;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(a.cluster) * a.cols * (kPacked ? 1 : a.p.n));
+    cfg.gridDim = dim3(static_cast<unsigned>(a.cluster * walks));
     cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -326,17 +688,28 @@ cudaError_t launch_scan(Args& a, cudaStream_t stream) {
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, gated_scan<T, G, kBack, kPacked, kVec>, static_cast<const Args>(a));
+    e = cudaLaunchKernelEx(&cfg, kern, static_cast<const Args>(a));
     note_launch(stream, kBack ? "gated_backward" : "gated_forward");
     return e;
 }
 
 template <typename T, typename G>
 cudaError_t run_t(Args& a, bool back, cudaStream_t stream) {
-    const bool vec = a.p.D % 4 == 0;
+    const bool tma = static_cast<int64_t>(a.p.D) * sizeof(T) % 16 == 0 && static_cast<int64_t>(a.p.D) * sizeof(G) % 16 == 0 &&
+                     static_cast<int64_t>(a.p.T) * (a.p.cu ? 1 : a.p.n) < (int64_t(1) << 31);
+    // Columns of 64 channels, whose rows are the longest stretches of memory, where clusters of up to four of them fill the
+    // GPU; else of 32, with longer steps of fewer channels (one sequence of 65536 x 1024: 68 us against 111), and of 16
+    // where even those leave more than half of it idle (65536 x 64: 36 us against 55; but 74 against 94 the other way for
+    // gradients of 65536 x 256). Packed: 32 (the mix above: 176 us against 203 with 64).
+    const int64_t walks = a.p.cu ? 1 : a.p.n, wide = ((a.p.D - 1) / 64 + 1) * walks, half = ((a.p.D - 1) / 32 + 1) * walks;
+    const int lanes = a.p.cu ? 8 : wide * 4 >= kFill ? 16 : half * 8 >= 64 ? 8 : 4;
     auto go = [&](auto kback, auto kpacked) {
         constexpr bool kB = decltype(kback)::value, kP = decltype(kpacked)::value;
-        return vec ? launch_scan<T, G, kB, kP, true>(a, stream) : launch_scan<T, G, kB, kP, false>(a, stream);
+        if (tma && lanes == 16) return launch_scan<T, G, kB, kP, kTma, kP ? 8 : 16>(a, stream);
+        if (tma && lanes == 8) return launch_scan<T, G, kB, kP, kTma, 8>(a, stream);
+        if (tma) return launch_scan<T, G, kB, kP, kTma, kP ? 8 : 4>(a, stream);
+        if (a.p.D % 4 == 0) return launch_scan<T, G, kB, kP, kQuads, 16>(a, stream);
+        return launch_scan<T, G, kB, kP, kSingles, 16>(a, stream);
     };
     using yes = std::true_type;
     using no = std::false_type;
@@ -452,12 +825,6 @@ cudaError_t gated_run(const GatedPass& p, bool backward, int dtype, int gate_dty
     Args a = {};
     a.p = p;
     a.err = err;
-    a.cols = (p.D - 1) / kCols + 1;
-    const int64_t walks = static_cast<int64_t>(a.cols) * (p.cu ? 1 : p.n);
-    const int pieces = (p.T - 1) / kRows + 1;
-    a.cluster = 1;
-    while (a.cluster < kMaxCluster && walks * a.cluster < 256 && a.cluster < pieces) a.cluster *= 2;
-    a.steps = (pieces - 1) / a.cluster + 1;
     return by_types(dtype, gate_dtype, [&](auto t, auto g) { return run_t<decltype(t), decltype(g)>(a, backward, stream); });
 }
 
