@@ -763,23 +763,25 @@ __global__ void __launch_bounds__(kTreeThreads) gated_tree(const T* __restrict__
     if (c >= D) return;
     const float h0 = state[static_cast<int64_t>(b) * D + c];
     const int64_t at = static_cast<int64_t>(b) * N * D + c;
-    for (int i0 = 0; i0 < N; i0 += 8) {
-        float xi[8], gi[8];
+    constexpr int kAhead = 16;  // nodes whose inputs are loaded together
+    for (int i0 = 0; i0 < N; i0 += kAhead) {
+        T xi[kAhead];
+        G gi[kAhead];
 #pragma unroll
-        for (int j = 0; j < 8; j++)
-            if (i0 + j < N) {
-                xi[j] = load_f(x + at + static_cast<int64_t>(i0 + j) * D);
-                gi[j] = expf(load_f(log_a + at + static_cast<int64_t>(i0 + j) * D));
-            }
+        for (int j = 0; j < kAhead; j++) {
+            const int64_t off = at + static_cast<int64_t>(i0 + j < N ? i0 + j : N - 1) * D;
+            xi[j] = x[off];
+            gi[j] = log_a[off];
+        }
 #pragma unroll
-        for (int j = 0; j < 8; j++)
-            if (i0 + j < N) {
-                const int pi = par[i0 + j];
-                if (pi == -2) continue;
-                const float h = fmaf(gi[j], pi < 0 ? h0 : hs[pi * kTreeThreads + tid], xi[j]);
-                hs[(i0 + j) * kTreeThreads + tid] = h;
-                store_f(out + at + static_cast<int64_t>(i0 + j) * D, h);
-            }
+        for (int j = 0; j < kAhead; j++) {
+            if (i0 + j >= N) break;
+            const int pi = par[i0 + j];
+            if (pi == -2) continue;
+            const float h = fmaf(expf(load_f(&gi[j])), pi < 0 ? h0 : hs[pi * kTreeThreads + tid], load_f(&xi[j]));
+            hs[(i0 + j) * kTreeThreads + tid] = h;
+            store_f(out + at + static_cast<int64_t>(i0 + j) * D, h);
+        }
     }
 }
 
