@@ -19,14 +19,13 @@
 // ring in shared memory by TMA, in swizzled boxes of 32 columns, from which a lane reads the four rows' pieces of four
 // columns of its MMA operands without bank conflicts and cuts them itself.
 #include "lla_drafts.cuh"
-#include "lla_tc_ptx.cuh"
+#include "lla_linear_tc.cuh"
 
 namespace lla {
 namespace {
 
 constexpr int kSlots = 40;
 constexpr int kMaxStages = 4;
-constexpr int kHalfSm = 111 * 1024;  // shared memory of a block of which an SM holds two
 
 // bf16 halves of two floats, the first in the low half
 __device__ __forceinline__ uint32_t pack(float lo, float hi) {
@@ -40,11 +39,12 @@ __device__ __forceinline__ float high(uint32_t r) { return __uint_as_float(r & 0
 // kParts bf16 pairs whose sum is (x, y)
 template <int kParts>
 __device__ __forceinline__ void cut(float x, float y, uint32_t (&p)[kParts]) {
+    f32x2 v = pair2(x, y);
 #pragma unroll
     for (int i = 0; i < kParts; i++) {
-        p[i] = pack(x, y);
-        x -= low(p[i]);
-        y -= high(p[i]);
+        const float2 f = split2(v);
+        p[i] = pack(f.x, f.y);
+        if (i + 1 < kParts) v = fma2(pair2(low(p[i]), high(p[i])), pair2(-1.f, -1.f), v);
     }
 }
 
@@ -74,31 +74,59 @@ __device__ __forceinline__ void load4(const float* p, float (&f)[4]) {
     const float4 y = *reinterpret_cast<const float4*>(p);
     f[0] = y.x; f[1] = y.y; f[2] = y.z; f[3] = y.w;
 }
-__device__ __forceinline__ void load4(const __nv_bfloat16* p, float (&f)[4]) {
-    const uint2 y = *reinterpret_cast<const uint2*>(p);
+__device__ __forceinline__ void load_nt(const float* p, float (&f)[4]) { load4(p, f); }
+[[maybe_unused]] __device__ __forceinline__ void load_nt(const float* p, float (&f)[2]) {
+    const float2 y = *reinterpret_cast<const float2*>(p);
+    f[0] = y.x; f[1] = y.y;
+}
+__device__ __forceinline__ void load8(const float* p, float (&f)[4], float (&h)[4]) {
+    load4(p, f);
+    load4(p + 4, h);
+}
+__device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&f)[4], float (&h)[4]) {
+    const uint4 y = *reinterpret_cast<const uint4*>(p);
     f[0] = low(y.x); f[1] = high(y.x); f[2] = low(y.y); f[3] = high(y.y);
+    h[0] = low(y.z); h[1] = high(y.z); h[2] = low(y.w); h[3] = high(y.w);
 }
 
 template <typename T> struct Parts;  // of queries and keys; of states
 template <> struct Parts<__nv_bfloat16> { static constexpr int q = 1, s = 2; };
 template <> struct Parts<float> { static constexpr int q = 3, s = 3; };
 
-struct Layout {  // shared memory of decode_tree_kernel, bytes from its start; the sums take the place of q and k
-    int q, k, v, lam, p, far, ring, stage;
-};
-// nodes of a block, all nodes, columns of a block
+// Blocks of an SM by their registers, and the shared memory of each.
 template <typename T>
-__host__ __device__ inline Layout layout(int nb, int N, int dk, int cols, int slots, int stage_rows) {
+__host__ __device__ constexpr int resident(int MT, int NT) { return Parts<T>::q == 1 && MT * NT <= 4 ? 3 : 2; }
+template <typename T>
+__host__ __device__ constexpr int room(int MT, int NT) { return resident<T>(MT, NT) == 3 ? 72 * 1024 : 111 * 1024; }
+
+// Shared memory of decode_tree_kernel, bytes from a multiple of 1024. The sums take the place of q and k at the end.
+struct Layout {
+    int q, k;      // kTma: panels of 64 columns, rows of 128 bytes, swizzled; else parts of rows of row_bytes
+    int panel_q, panel_k;
+    int ring, stage, stages;
+    int v, lam, p, far, up, total;
+};
+__host__ __device__ inline int up1024(int x) { return (x + 1023) / 1024 * 1024; }
+// nodes of a block, all nodes, columns of a block, slots; rows of a stage (0: no ring); its stages
+template <typename T>
+__host__ __device__ inline Layout layout(int nb, int N, int dk, int cols, int slots, int stage_rows, int stages) {
     Layout s;
-    const int parts = Parts<T>::q, rb = row_bytes(dk), rows = parts * (nb + N) * rb, sums = nb * (cols + 4) * 4;
+    const int parts = Parts<T>::q, rb = row_bytes(dk), panels = (dk + 63) / 64, sums = nb * (cols + 4) * 4;
+    const bool tma = parts == 1 && stage_rows > 0;
+    s.panel_q = nb * 128;
+    s.panel_k = (N + 7) / 8 * 1024;
     s.q = 0;
-    s.k = s.q + parts * nb * rb;
-    s.v = rows > sums ? rows : sums;
-    s.lam = s.v + N * cols * static_cast<int>(sizeof(T));
+    s.k = tma ? panels * s.panel_q : parts * nb * rb;
+    const int rows = s.k + (tma ? panels * s.panel_k : parts * N * rb);
+    s.ring = up1024(rows > sums ? rows : sums);
+    s.stage = stage_rows * cols * 4;
+    s.stages = stages;
+    s.v = s.ring + stages * s.stage;
+    s.lam = s.v + (N + 7) / 8 * 8 * cols * static_cast<int>(sizeof(T));
     s.p = s.lam + nb * slots * 4;
     s.far = s.p + nb * (N + 1) * 4;
-    s.ring = s.far + nb * slots * 4;
-    s.stage = stage_rows * cols * 4;
+    s.up = s.far + nb * slots * 4;
+    s.total = s.up + nb * N + 1024;  // and what aligns the start
     return s;
 }
 
@@ -106,18 +134,18 @@ template <int kBytes>
 __device__ __forceinline__ void copy_async(void* to, const void* from) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(smem_u32(to)), "l"(from), "n"(kBytes) : "memory");
 }
-__device__ __forceinline__ void copies_done() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+__device__ __forceinline__ void copies_group() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int kLeft>
+__device__ __forceinline__ void copies_done() { asm volatile("cp.async.wait_group %0;" ::"n"(kLeft) : "memory"); }
 
 // Rows of q or k into shared memory as bf16 parts, zeros behind dk and behind the valid rows.
 template <typename T, int kThreads>
-__device__ __forceinline__ void stage(char* to, const T* from, int rows, int valid, int dk, int dkp) {
+__device__ __forceinline__ void stage_rows(char* to, const T* from, int rows, int valid, int dk, int dkp) {
     constexpr int kParts = Parts<T>::q;
     const int rb = row_bytes(dk);
     if (dk % 8 == 0) {  // rows of whole 16-byte pieces: eight values at a time
-        const int per = dkp / 8;
-        const float inv = 1.f / static_cast<float>(per);
-        for (int e = threadIdx.x; e < rows * per; e += kThreads) {
-            const int i = static_cast<int>((static_cast<float>(e) + 0.5f) * inv), c = (e - i * per) * 8;  // e < 2^12
+        const int per = dkp / 8, step = kThreads / per, first = threadIdx.x / per, c = (threadIdx.x - first * per) * 8;
+        for (int i = first < step ? first : rows; i < rows; i += step) {
             char* at = to + i * rb + c * 2;
             const T* src = from + static_cast<int64_t>(i) * dk + c;
             const bool in = i < valid && c < dk;
@@ -170,197 +198,281 @@ __device__ __forceinline__ void mma_parts(float (&d)[4], const uint32_t (&a)[kQ]
         }
 }
 
-// Four 8 x 8 pieces of a staged matrix of bf16 rows: rows r0 .. r0 + 15 (lanes 0-15 name them) and summed indexes 16 ks ..
-// + 15, as the A operand takes them.
-__device__ __forceinline__ uint32_t piece_at(const char* m, int rb, int r0, int ks, int lane) {
-    return smem_u32(m + (r0 + (lane & 15)) * rb + ks * 32 + (lane >> 4) * 16);
-}
+// Maps of the tensors that come by TMA, each [heads (states: slots)][rows][columns].
+struct Maps {
+    CUtensorMap states, q, k, v;
+};
 
-// Grid: (heads of all sequences, blocks of 16 MT NG nodes, column blocks of 32 CU). The warps are CU column pieces of 32
-// times NG groups of 16 MT nodes times KS shares of the 16-row units. kStageRows: state rows of a
-// stage of the ring, or 0 where it is not used (rows that are no multiples of 16 bytes, or less than 128).
-template <typename T, int MT, int NG, int CU, int kStageRows>
-__global__ void __launch_bounds__(256, 2) decode_tree_kernel(const TreeCall c, const __grid_constant__ CUtensorMap map, const int stages) {
-    constexpr int kWarps = 8, kThreads = kWarps * 32, kNb = 16 * MT * NG, kCols = 32 * CU, KS = kWarps / (CU * NG);
-    constexpr int kQ = Parts<T>::q, kS = Parts<T>::s;
+// Grid: (heads of all sequences times blocks of 16 MT NG nodes, column blocks of 8 CW NT). The warps are CW column pieces of
+// 8 NT times NG groups of 16 MT nodes times KS shares of the 16-row units. kStageRows: state rows of a stage of the ring, or
+// 0 for loads by the lanes themselves (rows that are no multiples of 16 bytes).
+//
+// Four warps walk the tree and form the weights while the other four multiply queries and keys; most of a short block's
+// time is latency. With one tree after another (a first version): 10000 cycles before the first slot, now 5000.
+template <typename T, int MT, int NG, int CW, int NT, int kStageRows>
+__global__ void __launch_bounds__(256, resident<T>(MT, NT))
+    decode_tree_kernel(const TreeCall c, const __grid_constant__ Maps maps, const int stages) {
+    constexpr int kWarps = 8, kThreads = kWarps * 32, kNb = 16 * MT * NG, kCols = 8 * CW * NT, KS = kWarps / (CW * NG);
+    constexpr int kQ = Parts<T>::q, kS = Parts<T>::s, CU = kCols / 32;
+    constexpr bool kRing = kStageRows > 0, kTma = kRing && kQ == 1;
     constexpr int kUnits = kStageRows / 16;  // of a stage
-    constexpr bool kRing = kStageRows > 0;
-    extern __shared__ __align__(16) char smem[];
+    constexpr int kWalkers = 128;            // threads that form the weights
+    extern __shared__ __align__(16) char smem_any[];
     __shared__ int par[kMaxTree], dep[kMaxTree], slot_of[kSlots];
     __shared__ float la[kMaxTree];
     __shared__ int64_t slot_at[kSlots];
-    __shared__ __align__(8) uint64_t full[kMaxStages], empty[kMaxStages];
+    __shared__ __align__(8) uint64_t full[kMaxStages], empty[kMaxStages], inputs;
+    char* smem = smem_any + (-smem_u32(smem_any) & 1023u);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, cc = lane & 3;
-    const int64_t bh = blockIdx.x;
+    const int blocks = (c.N - 1) / kNb + 1;  // of nodes: those of one head run side by side, so that its states come once
+    const int64_t bh = blockIdx.x / blocks;
     const int b = static_cast<int>(bh / c.H), h = static_cast<int>(bh - static_cast<int64_t>(b) * c.H);
     const int N = c.N, dk = c.dk, dv = c.dv, dkp = (dk + 15) / 16 * 16, rb = row_bytes(dk), ksteps = dkp / 16;
-    const int i0 = blockIdx.y * kNb, col0 = blockIdx.z * kCols, live = N - i0 < kNb ? N - i0 : kNb;
+    const int i0 = static_cast<int>(blockIdx.x % blocks) * kNb, col0 = blockIdx.y * kCols, live = N - i0 < kNb ? N - i0 : kNb;
     const bool linear = c.t == nullptr;
-    const int64_t t = linear ? 1 : c.t[b];
-    const Layout s = layout<T>(kNb, N, dk, kCols, c.Lmax, kStageRows);
-    char *qs = smem + s.q, *ks = smem + s.k;
-    T* vs = reinterpret_cast<T*>(smem + s.v);             // [N][kCols]
-    float* lam = reinterpret_cast<float*>(smem + s.lam);  // [kNb][Lmax]
-    float* P = reinterpret_cast<float*>(smem + s.p);      // [kNb][N + 1]
-    float* far = reinterpret_cast<float*>(smem + s.far);  // [slots][kNb]
-    float* acc = reinterpret_cast<float*>(smem);          // [kNb][kCols + 4], once q and k are done with
+    const Layout s = layout<T>(kNb, N, dk, kCols, c.Lmax, kStageRows, stages);
+    char *qs = smem + s.q, *ks = smem + s.k, *ring = smem + s.ring;
+    T* vs = reinterpret_cast<T*>(smem + s.v);               // [N][kCols]
+    float* lam = reinterpret_cast<float*>(smem + s.lam);    // [kNb][Lmax]
+    float* P = reinterpret_cast<float*>(smem + s.p);        // [kNb][N + 1]: weights, then scores times weights
+    float* far = reinterpret_cast<float*>(smem + s.far);    // [slots][kNb]
+    uint8_t* up = reinterpret_cast<uint8_t*>(smem + s.up);  // [kNb][N]: a node and those above it, upwards
+    float* acc = reinterpret_cast<float*>(smem);            // [kNb][kCols + 4], once q and k are done with
+    const int wide = dv - col0 < kCols ? dv - col0 : kCols; // columns of the block
 
-    // the held slots of t - 1, in pieces of kStageRows rows
-    const bool there = t > 0 && (linear || t < (int64_t(1) << (c.Lmax - 1)));  // else there are none, or the call is bad
-    const int slots = !there ? 0 : linear ? 1 : 1 + __popcll(static_cast<unsigned long long>(t - 1));
-    const int pieces = kRing ? (dk - 1) / (kRing ? kStageRows : 1) + 1 : 1, rounds = slots * pieces;
-    const int64_t msz = static_cast<int64_t>(dk) * dv;
-    const float* S = c.states + bh * c.Lmax * msz + col0;
-    const int wide = dv - col0 < kCols ? dv - col0 : kCols;  // columns of the block
-    char* ring = smem + s.ring + (-smem_u32(smem + s.ring) & 1023u);  // boxes begin at multiples of 1024 bytes
-    constexpr int kBox = kStageRows * 128;                            // bytes of a stage's 32 columns
-    auto copy = [&](int at, int slot, int piece) {                    // into stage `at`, by one thread
+    // The held slots of t - 1, in pieces of kStageRows rows (dk <= 128).
+    const int pieces = !kRing || kStageRows >= 128 ? 1 : (dk - 1) / (kRing ? kStageRows : 1) + 1;
+    constexpr int kBox = kStageRows * 128;          // bytes of a stage's 32 columns
+    auto copy = [&](int at, int slot, int piece) {  // into stage `at`, by one thread
         uint64_t* bar = &full[at];
         mbar_expect_tx(bar, CU * kBox);
-        const int y = static_cast<int>((bh * c.Lmax + slot) * dk) + piece * kStageRows;
-        for (int u = 0; u < CU; u++) tma_load_2d(ring + at * s.stage + u * kBox, &map, bar, col0 + u * 32, y);
+        for (int u = 0; u < CU; u++)
+            tma_load_3d(ring + at * s.stage + u * kBox, &maps.states, bar, col0 + u * 32, piece * kStageRows,
+                        static_cast<int>(bh * c.Lmax + slot));
     };
+    auto held = [&](int64_t t) {  // none where there are none, or the call is bad
+        const bool there = t > 0 && (linear || t < (int64_t(1) << (c.Lmax - 1)));
+        return !there ? 0 : linear ? 1 : 1 + __popcll(static_cast<unsigned long long>(t - 1));
+    };
+
+    // Everything that the block reads is on its way before the first wait.
     if (warp == kWarps - 1) {
-        for (int l = lane; l < kSlots && there; l += 32)
+        if (lane == 0) {
+            for (int i = 0; i < kMaxStages; i++) {
+                mbar_init(&full[i], 1);
+                mbar_init(&empty[i], kWarps);
+            }
+            mbar_init(&inputs, 1);
+            fence_mbar_init();
+            if constexpr (kTma) {
+                const int panels = (dk + 63) / 64;
+                mbar_expect_tx(&inputs, panels * (s.panel_q + s.panel_k) + (N + 7) / 8 * 8 * kCols * 2);
+                for (int y = 0; y < panels; y++) {
+                    tma_load_3d(qs + y * s.panel_q, &maps.q, &inputs, y * 64, i0, static_cast<int>(bh));
+                    tma_load_3d(ks + y * s.panel_k, &maps.k, &inputs, y * 64, 0, static_cast<int>(bh));
+                }
+                tma_load_3d(vs, &maps.v, &inputs, col0, 0, static_cast<int>(bh));
+            }
+        }
+        const int64_t t = linear ? 1 : c.t[b];
+        const int rounds = held(t) * pieces;
+        for (int l = lane; l < kSlots && rounds > 0; l += 32)
             if (l == 0 || (!linear && ((t - 1) >> (l - 1) & 1))) {
                 const int64_t below = l == 0 ? 0 : (int64_t(1) << (l - 1)) - 1;
                 const int at = l == 0 ? 0 : 1 + __popcll(static_cast<unsigned long long>((t - 1) & below));
                 slot_of[at] = l;
                 slot_at[at] = ((t - 1) >> l) << l;
             }
-        if (kRing) {
-            if (lane < stages) {
-                mbar_init(&full[lane], 1);
-                mbar_init(&empty[lane], kWarps);
-                fence_mbar_init();
-            }
-            __syncwarp();
+        __syncwarp();
+        if (kRing)
             for (int r = 0; r < stages && r < rounds && lane == 0; r++) copy(r, slot_of[r / pieces], r % pieces);
-        }
     }
-
-    // everything else that the block reads is on its way before the first wait
-    for (int i = tid; i < N; i += kThreads) {
-        copy_async<4>(&par[i], c.parent + (c.BP > 1 ? static_cast<int64_t>(b) * N : 0) + i);
-        if (!linear) copy_async<4>(&la[i], c.log_a + bh * N + i);
-    }
-    stage<T, kThreads>(qs, static_cast<const T*>(c.q) + (bh * N + i0) * dk, kNb, live, dk, dkp);
-    stage<T, kThreads>(ks, static_cast<const T*>(c.k) + bh * N * dk, N, N, dk, dkp);
-    const T* vg = static_cast<const T*>(c.v) + bh * N * dv + col0;
-    constexpr int kE = 16 / sizeof(T);
-    if (dv % kE == 0) {
-        for (int e = tid; e < N * (kCols / kE); e += kThreads) {
-            const int j = e / (kCols / kE), x = (e - j * (kCols / kE)) * kE;
-            if (col0 + x < dv) copy_async<16>(vs + j * kCols + x, vg + static_cast<int64_t>(j) * dv + x);
+    if (tid < kWalkers) {
+        for (int i = tid; i < N; i += kWalkers) {
+            copy_async<4>(&par[i], c.parent + (c.BP > 1 ? static_cast<int64_t>(b) * N : 0) + i);
+            if (!linear) copy_async<4>(&la[i], c.log_a + bh * N + i);
         }
-    } else {
+        if (!linear)
+            for (int e = tid; e < live * c.Lmax; e += kWalkers) copy_async<4>(&lam[e], c.lambda + (bh * N + i0) * c.Lmax + e);
+        copies_group();
+    }
+    const int64_t t = linear ? 1 : c.t[b];
+    const int slots = held(t), rounds = slots * pieces;
+    if constexpr (!kTma) {
+        stage_rows<T, kThreads>(qs, static_cast<const T*>(c.q) + (bh * N + i0) * dk, kNb, live, dk, dkp);
+        stage_rows<T, kThreads>(ks, static_cast<const T*>(c.k) + bh * N * dk, N, N, dk, dkp);
+        const T* vg = static_cast<const T*>(c.v) + bh * N * dv + col0;
         for (int e = tid; e < N * kCols; e += kThreads) {
             const int j = e / kCols, x = e - j * kCols;
-            if (col0 + x < dv) vs[e] = vg[static_cast<int64_t>(j) * dv + x];
+            if (x < wide) vs[e] = vg[static_cast<int64_t>(j) * dv + x];
         }
+        copies_group();
+        copies_done<0>();
     }
-    if (!linear)
-        for (int e = tid; e < live * c.Lmax; e += kThreads) copy_async<4>(&lam[e], c.lambda + (bh * N + i0) * c.Lmax + e);
-    copies_done();
-    __syncthreads();
+    __syncthreads();  // barriers and slots are there (not kTma: everything is)
 
-    // scores: 16 x 8 pieces dealt to the warps
-    {
-        const int mts = (live + 15) / 16, nts = (N + 7) / 8;
-        for (int u = warp; u < mts * nts; u += kWarps) {
-            const int mt = u % mts, nt = u / mts;
-            float d[4] = {0.f, 0.f, 0.f, 0.f};
-            const int j = nt * 8 + g < N ? nt * 8 + g : N - 1;  // columns behind the last are not kept
-            for (int kk = 0; kk < ksteps; kk++) {
-                uint32_t a[kQ][4], b0[kQ], b1[kQ];
+    // Operands of 16 queries (from row r0, summed indexes 16 kk ..), and of 8 keys (from row j0, 16 kk .. + 31).
+    auto load_q = [&](uint32_t (&a)[kQ][4], int r0, int kk) {
+        if constexpr (kTma) {
+            ldmatrix4(a[0], smem_u32(qs) + (kk >> 2) * s.panel_q + (r0 + (lane & 15)) * 128 +
+                                ((((kk & 3) * 2 + (lane >> 4)) ^ (lane & 7)) << 4));
+        } else {
+#pragma unroll
+            for (int w = 0; w < kQ; w++)
+                ldmatrix4(a[w], smem_u32(qs) + (w * kNb + r0 + (lane & 15)) * rb + kk * 32 + (lane >> 4) * 16);
+        }
+    };
+    auto load_k = [&](uint32_t (&z)[kQ][4], int j0, int kk) {
+        if constexpr (kTma) {
+            ldmatrix4(z[0], smem_u32(ks) + (kk >> 2) * s.panel_k + (j0 + (lane & 7)) * 128 +
+                                ((((kk & 3) * 2 + (lane >> 3)) ^ (lane & 7)) << 4));
+        } else {
+            const int j = j0 + (lane & 7) < N ? j0 + (lane & 7) : N - 1;  // behind the last key: that one, not kept
+#pragma unroll
+            for (int w = 0; w < kQ; w++)
+                ldmatrix4(z[w], smem_u32(ks) + (w * N + j) * rb + kk * 32 + (lane >> 3) * 16);
+        }
+    };
+    // scores: units of `many` 16 x 8 pieces side by side
+    const int mts = (live + 15) / 16, nts = (N + 7) / 8;
+    const int many = mts * nts > 8 ? 4 : mts * nts > 4 ? 2 : 1, groups = (nts + many - 1) / many;
+    auto score = [&](float (&d)[4][4], int u) {
+        const int mt = u % mts, nt0 = u / mts * many;
+#pragma unroll
+        for (int y = 0; y < 4; y++)
+#pragma unroll
+            for (int r = 0; r < 4; r++) d[y][r] = 0.f;
+        for (int kk = 0; kk < ksteps; kk += 2) {
+            uint32_t a[kQ][4], a1[kQ][4];
+            load_q(a, mt * 16, kk);
+            if (kk + 1 < ksteps) load_q(a1, mt * 16, kk + 1);
+#pragma unroll
+            for (int y = 0; y < 4; y++) {
+                if (y >= many || nt0 + y >= nts) break;
+                uint32_t z[kQ][4], b0[kQ], b1[kQ];
+                load_k(z, (nt0 + y) * 8, kk);
 #pragma unroll
                 for (int w = 0; w < kQ; w++) {
-                    ldmatrix4(a[w], piece_at(qs + w * kNb * rb, rb, mt * 16, kk, lane));
-                    const char* at = ks + (w * N + j) * rb + (kk * 16 + cc * 2) * 2;
-                    b0[w] = *reinterpret_cast<const uint32_t*>(at);
-                    b1[w] = *reinterpret_cast<const uint32_t*>(at + 16);
+                    b0[w] = z[w][0];
+                    b1[w] = z[w][1];
                 }
-                mma_parts<false>(d, a, b0, b1);
+                mma_parts<false>(d[y], a, b0, b1);
+                if (kk + 1 == ksteps) continue;
+#pragma unroll
+                for (int w = 0; w < kQ; w++) {
+                    b0[w] = z[w][2];
+                    b1[w] = z[w][3];
+                }
+                mma_parts<false>(d[y], a1, b0, b1);
             }
+        }
+    };
+    auto onto_weights = [&](const float (&d)[4][4], int u) {
+        const int mt = u % mts, nt0 = u / mts * many;
+#pragma unroll
+        for (int y = 0; y < 4; y++) {
+            if (y >= many) break;
 #pragma unroll
             for (int r = 0; r < 4; r++) {
-                const int i = mt * 16 + g + (r >> 1) * 8, x = nt * 8 + cc * 2 + (r & 1);
-                if (x < N) P[i * (N + 1) + x] = d[r];
+                const int i = mt * 16 + g + (r >> 1) * 8, x = (nt0 + y) * 8 + cc * 2 + (r & 1);
+                if (x < N) P[i * (N + 1) + x] *= d[y][r];
             }
         }
-    }
-    // depths; a walk up only goes to smaller indexes, so it ends in a bad tree too
-    bool bad = t < 0;
-    for (int i = tid; i < N; i += kThreads) {
-        int d = -1;
-        for (int j = i; j >= 0; d++) {
-            const int up = par[j];
-            if (up >= j || up < -2 || (up == -2 && j != i)) {
-                bad = true;
-                break;
+    };
+
+    bool bad = t < 0, in_time = true;
+    float held_scores[2][4][4];
+    const int scorer = warp - kWalkers / 32;
+    if (tid < kWalkers) {
+        // Depths and weights. A walk up only goes to smaller indexes, so it ends in a bad tree too.
+        copies_done<0>();
+        asm volatile("bar.sync 1, 128;" ::: "memory");
+        auto depth = [&](int i, uint8_t* list) {
+            int d = -1;
+            for (int j = i; j >= 0; d++) {
+                const int p = par[j];
+                if (list) list[d + 1] = static_cast<uint8_t>(j);
+                if (p >= j || p < -2 || (p == -2 && j != i)) {
+                    bad = true;
+                    return d;
+                }
+                j = p;
             }
-            j = up;
+            if (!linear && t + d >= (int64_t(1) << (c.Lmax - 1))) bad = true;
+            return d;
+        };
+        // kEach threads to a node, each with every so many of its steps and of the held slots
+        constexpr int kEach = kWalkers / kNb;
+        const int i = tid % kNb, first = tid / kNb;
+        if (i < live) {
+            const float lg = linear ? c.log_a[h] : 0.f;
+            const int d = depth(i0 + i, first == 0 ? up + i * N : nullptr);
+            if (first == 0) dep[i] = d;
+            if (!bad && par[i0 + i] != -2) {
+                float D = 0.f;
+                int turn = first, n = 0;
+                for (int j = i0 + i; j >= 0; j = par[j], n++) {
+                    if (turn-- == 0) {
+                        turn = kEach - 1;
+                        P[i * (N + 1) + j] =
+                            linear ? (n == 0 ? 1.f : expf(lg * static_cast<float>(n)))
+                                   : lam[i * c.Lmax + 64 - __clzll(static_cast<long long>((t + d) ^ (t + d - n)))] * expf(D);
+                    }
+                    if (!linear) D += la[j];
+                }
+                const float whole = linear ? expf(lg * static_cast<float>(d + 1)) : expf(D);
+                for (int m = first; m < slots; m += kEach)
+                    far[m * kNb + i] =
+                        linear ? whole
+                               : whole * lam[i * c.Lmax + 64 - __clzll(static_cast<long long>((t + d) ^ slot_at[m]))];
+            }
         }
-        dep[i] = d;
-        if (!linear && t + d >= (int64_t(1) << (c.Lmax - 1))) bad = true;
+        for (int j = tid; j < N; j += kWalkers)  // the other blocks' nodes
+            if (j < i0 || j >= i0 + live) depth(j, nullptr);
+    } else {
+        if (kTma) in_time = mbar_try_wait(&inputs, 0) || mbar_wait(&inputs, 0);
+#pragma unroll
+        for (int y = 0; y < 2; y++)
+            if (scorer + 4 * y < mts * groups) score(held_scores[y], scorer + 4 * y);
     }
     bad = __syncthreads_or(bad);
     if (bad && tid == 0) record_error(c.err, kDevBadInput);
-
-    // weights of the nodes above, onto their scores, and of the held slots: kThreads / kNb threads walk up from each node,
-    // each with every so many of the steps
-    if (!bad) {
-        constexpr int kEach = kThreads / kNb;
-        const int i = tid % kNb, first = tid / kNb;
-        if (i < live && par[i0 + i] != -2) {
-            const int d = dep[i0 + i];
-            const float lg = linear ? c.log_a[h] : 0.f;
-            float D = 0.f;
-            int turn = first, n = 0;
-            for (int j = i0 + i; j >= 0; j = par[j], n++) {
-                if (turn-- == 0) {
-                    turn = kEach - 1;
-                    P[i * (N + 1) + j] *=
-                        linear ? (n == 0 ? 1.f : expf(lg * static_cast<float>(n)))
-                               : lam[i * c.Lmax + 64 - __clzll(static_cast<long long>((t + d) ^ (t + d - n)))] * expf(D);
-                }
-                if (!linear) D += la[j];
-            }
-            const float whole = linear ? expf(lg * static_cast<float>(d + 1)) : expf(D);
-            for (int m = first; m < slots; m += kEach)
-                far[m * kNb + i] =
-                    linear ? whole
-                           : whole * lam[i * c.Lmax + 64 - __clzll(static_cast<long long>((t + d) ^ slot_at[m]))];
-        }
+    if (tid >= kWalkers) {
+#pragma unroll
+        for (int y = 0; y < 2; y++)
+            if (scorer + 4 * y < mts * groups) onto_weights(held_scores[y], scorer + 4 * y);
+    } else if (kTma) {
+        in_time = mbar_try_wait(&inputs, 0) || mbar_wait(&inputs, 0);
     }
-    __syncthreads();
+    for (int u = 8 + warp; u < mts * groups; u += kWarps) {
+        score(held_scores[0], u);
+        onto_weights(held_scores[0], u);
+    }
 
     // the states' part: a slot's units of 16 rows summed, then weighted
-    const int cu = warp % CU, ng = warp / CU % NG, share = warp / (CU * NG);
-    const int colw = cu * 32 + g * 4;  // of the lane's pieces
-    float out[MT][4][4], d[MT][4][4];
+    const int cw = warp % CW, ng = warp / CW % NG, share = warp / (CW * NG);
+    const int colw = cw * 8 * NT + g * NT;  // of the lane's pieces
+    float out[MT][NT][4], d[MT][NT][4];
 #pragma unroll
     for (int mt = 0; mt < MT; mt++)
 #pragma unroll
-        for (int n = 0; n < 4; n++)
+        for (int n = 0; n < NT; n++)
 #pragma unroll
-            for (int r = 0; r < 4; r++) out[mt][n][r] = d[mt][n][r] = 0.f;
-    // one unit's products; f: rows 2 cc, 2 cc + 1, 2 cc + 8, 2 cc + 9 and the lane's four columns
-    auto multiply = [&](const float (&f)[4][4], int kk) {
-        uint32_t b0[4][kS], b1[4][kS];
+            for (int r = 0; r < 4; r++) out[mt][n][r] = 0.f;
+    // one unit's products; f: rows 2 cc, 2 cc + 1, 2 cc + 8, 2 cc + 9 and the lane's NT columns
+    auto multiply = [&](const float (&f)[4][NT], int kk, auto first) {  // first: onto zeros
+        uint32_t b0[NT][kS], b1[NT][kS];
 #pragma unroll
-        for (int n = 0; n < 4; n++) {
+        for (int n = 0; n < NT; n++) {
             cut<kS>(f[0][n], f[1][n], b0[n]);
             cut<kS>(f[2][n], f[3][n], b1[n]);
         }
 #pragma unroll
         for (int mt = 0; mt < MT; mt++) {
             uint32_t a[kQ][4];
+            load_q(a, (ng * MT + mt) * 16, kk);
 #pragma unroll
-            for (int w = 0; w < kQ; w++)
-                ldmatrix4(a[w], piece_at(qs + w * kNb * rb, rb, (ng * MT + mt) * 16, kk, lane));
-#pragma unroll
-            for (int n = 0; n < 4; n++) mma_parts<false>(d[mt][n], a, b0[n], b1[n]);
+            for (int n = 0; n < NT; n++) mma_parts<decltype(first)::value>(d[mt][n], a, b0[n], b1[n]);
         }
     };
     auto weigh = [&](int m) {
@@ -369,44 +481,47 @@ __global__ void __launch_bounds__(256, 2) decode_tree_kernel(const TreeCall c, c
             const int row = (ng * MT + mt) * 16 + g;
             const float w0 = far[m * kNb + row], w1 = far[m * kNb + row + 8];
 #pragma unroll
-            for (int n = 0; n < 4; n++) {
+            for (int n = 0; n < NT; n++) {
 #pragma unroll
-                for (int r = 0; r < 4; r++) {
-                    out[mt][n][r] = fmaf(r < 2 ? w0 : w1, d[mt][n][r], out[mt][n][r]);
-                    d[mt][n][r] = 0.f;
+                for (int r = 0; r < 4; r += 2) {
+                    const float w = r == 0 ? w0 : w1;
+                    const float2 y = split2(fma2(pair2(w, w), pair2(d[mt][n][r], d[mt][n][r + 1]),
+                                                 pair2(out[mt][n][r], out[mt][n][r + 1])));
+                    out[mt][n][r] = y.x;
+                    out[mt][n][r + 1] = y.y;
                 }
             }
         }
     };
+    using yes = std::true_type;
+    using no = std::false_type;
     constexpr int kRow[4] = {0, 1, 8, 9};
     if constexpr (kRing) {
-        bool in_time = true;
         int m = 0, piece = 0, slot_ahead = stages / pieces, piece_ahead = stages % pieces, at = 0, issued = -1;
         uint32_t parity = 0;
+        // places of the lane's pieces in a unit's swizzled rows 2 cc and 2 cc + 1; those 8 rows on lie alike
+        const int chunk = colw % 32 / 4, rest = colw % 4 * 4;
+        const int even = cc * 256 + ((chunk ^ (cc * 2)) << 4) + rest, odd = cc * 256 + 128 + ((chunk ^ (cc * 2 + 1)) << 4) + rest;
+        const bool mine = share < ksteps;  // whether any unit of a slot is this warp's
         for (int round = 0; round < rounds; round++) {
             if (in_time && !mbar_try_wait(&full[at], parity)) in_time = mbar_wait(&full[at], parity);
-            const char* st = ring + at * s.stage + cu * kBox;
-            const int left = dk - piece * kStageRows;  // rows of the stage that are the slot's
+            const char* st = ring + at * s.stage + colw / 32 * kBox;
+            const int left = dk - piece * kStageRows;  // rows of the stage that are the slot's; zeros lie behind them
             constexpr int kTimes = (kUnits + KS - 1) / KS;
-            float f[kTimes][4][4];
+            float f[kTimes][4][NT];
 #pragma unroll
             for (int k = 0; k < kTimes; k++) {
                 const int u = share + k * KS;
                 if (u * 16 >= left || u >= kUnits) break;
 #pragma unroll
-                for (int r = 0; r < 4; r++) {
-                    const int row = u * 16 + cc * 2 + kRow[r];
-                    load4(reinterpret_cast<const float*>(st + row * 128 + ((g ^ (row & 7)) << 4)), f[k][r]);
-                    if (u * 16 + 16 > left && row >= left) {  // the next slot's
-#pragma unroll
-                        for (int v = 0; v < 4; v++) f[k][r][v] = 0.f;
-                    }
-                }
+                for (int r = 0; r < 4; r++)
+                    load_nt(reinterpret_cast<const float*>(st + u * 2048 + (r & 1 ? odd : even) + (r >> 1) * 1024), f[k][r]);
                 if (k + 1 == kTimes || (u + KS) * 16 >= left || u + KS >= kUnits) {  // read to the end
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&empty[at]);
                 }
-                multiply(f[k], piece * kUnits + u);
+                if (k == 0 && piece == 0) multiply(f[k], piece * kUnits + u, yes());
+                else multiply(f[k], piece * kUnits + u, no());
             }
             if (share * 16 >= left || share >= kUnits) {  // nothing here for this warp
                 __syncwarp();
@@ -425,7 +540,7 @@ __global__ void __launch_bounds__(256, 2) decode_tree_kernel(const TreeCall c, c
                 slot_ahead++;
             }
             if (++piece == pieces) {
-                weigh(m);
+                if (mine) weigh(m);
                 piece = 0;
                 m++;
             }
@@ -439,121 +554,169 @@ __global__ void __launch_bounds__(256, 2) decode_tree_kernel(const TreeCall c, c
             if (issued >= 0) mbar_wait(&full[issued % stages], (issued / stages) & 1);
             if (warp == kWarps - 1)
                 for (int r = 0; r < stages && r < rounds; r++) mbar_wait(&full[r], 0);
+            if (kTma && warp == kWarps - 1) mbar_wait(&inputs, 0);
         }
     } else {
         // the lane's own loads, a unit ahead
-        auto fetch = [&](float (&f)[4][4], int m, int kk) {
+        const int64_t msz = static_cast<int64_t>(dk) * dv;
+        const float* S = c.states + bh * c.Lmax * msz + col0;
+        auto fetch = [&](float (&f)[4][NT], int m, int kk) {
 #pragma unroll
             for (int r = 0; r < 4; r++) {
                 const int row = kk * 16 + cc * 2 + kRow[r];
                 const float* from = S + slot_of[m] * msz + static_cast<int64_t>(row) * dv + colw;
 #pragma unroll
-                for (int v = 0; v < 4; v++) f[r][v] = row < dk && colw + v < wide ? __ldcs(from + v) : 0.f;
+                for (int v = 0; v < NT; v++) f[r][v] = row < dk && colw + v < wide ? __ldcs(from + v) : 0.f;
             }
         };
-        float f[4][4], next[4][4];
+        float f[4][NT], next[4][NT];
         if (slots > 0 && share < ksteps) fetch(f, 0, share);
         for (int m = 0; m < slots; m++) {
             for (int kk = share; kk < ksteps; kk += KS) {
                 const bool more = kk + KS < ksteps;
                 if (more || m + 1 < slots) fetch(next, more ? m : m + 1, more ? kk + KS : share);
-                multiply(f, kk);
+                if (kk == share) multiply(f, kk, yes());
+                else multiply(f, kk, no());
 #pragma unroll
                 for (int r = 0; r < 4; r++)
 #pragma unroll
-                    for (int v = 0; v < 4; v++) f[r][v] = next[r][v];
+                    for (int v = 0; v < NT; v++) f[r][v] = next[r][v];
             }
-            weigh(m);
+            if (share < ksteps) weigh(m);
         }
     }
     if (bad) return;
     __syncthreads();  // q is not read any more
-    // the shares are added in order; a lane holds columns 8 cc + {0..3, 4..7} of its rows
+    // the shares are added in order; a lane holds 2 NT neighbouring columns of its rows
     for (int sh = 0; sh < KS; sh++) {
         if (share == sh) {
 #pragma unroll
             for (int mt = 0; mt < MT; mt++)
 #pragma unroll
-                for (int r = 0; r < 4; r++) {
-                    float4* at = reinterpret_cast<float4*>(acc + ((ng * MT + mt) * 16 + g + (r >> 1) * 8) * (kCols + 4) +
-                                                           cu * 32 + cc * 8 + (r & 1) * 4);
-                    float4 x = make_float4(out[mt][0][r], out[mt][1][r], out[mt][2][r], out[mt][3][r]);
-                    if (sh > 0) {
-                        const float4 y = *at;
-                        x.x += y.x; x.y += y.y; x.z += y.z; x.w += y.w;
+                for (int r = 0; r < 4; r += 2) {
+                    float* at = acc + ((ng * MT + mt) * 16 + g + r * 4) * (kCols + 4) + cw * 8 * NT + cc * 2 * NT;
+#pragma unroll
+                    for (int x = 0; x < 2 * NT; x += 4) {
+                        float4 y;
+                        y.x = out[mt][x % NT][r + x / NT];
+                        y.y = out[mt][(x + 1) % NT][r + (x + 1) / NT];
+                        y.z = out[mt][(x + 2) % NT][r + (x + 2) / NT];
+                        y.w = out[mt][(x + 3) % NT][r + (x + 3) / NT];
+                        if (sh > 0) {
+                            const float4 z = *reinterpret_cast<const float4*>(at + x);
+                            y.x += z.x; y.y += z.y; y.z += z.z; y.w += z.w;
+                        }
+                        *reinterpret_cast<float4*>(at + x) = y;
                     }
-                    *at = x;
                 }
         }
         __syncthreads();
     }
-    // the nodes above, in fp32, and the result; four columns of a node to a thread
+    // the nodes above, in fp32, and the result; eight columns of a node to a thread
     T* og = static_cast<T*>(c.out) + (bh * N + i0) * dv + col0;
-    for (int e = tid; e < live * (kCols / 4); e += kThreads) {
-        const int i = e / (kCols / 4), x = (e - i * (kCols / 4)) * 4;
+    for (int e = tid; e < live * (kCols / 8); e += kThreads) {
+        const int i = e / (kCols / 8), x = (e - i * (kCols / 8)) * 8;
         if (par[i0 + i] == -2 || x >= wide) continue;
-        float o[4] = {0.f, 0.f, 0.f, 0.f};
-        for (int j = i0 + i; j >= 0; j = par[j]) {
+        f32x2 o[4];
+        {
+            const float4* sum = reinterpret_cast<const float4*>(acc + i * (kCols + 4) + x);
+            const float4 y = sum[0], z = sum[1];
+            o[0] = pair2(y.x, y.y); o[1] = pair2(y.z, y.w); o[2] = pair2(z.x, z.y); o[3] = pair2(z.z, z.w);
+        }
+        const int d = dep[i];
+#pragma unroll 2
+        for (int n = 0; n <= d; n++) {
+            const int j = up[i * N + n];
             const float p = P[i * (N + 1) + j];
-            float f[4];
-            load4(vs + j * kCols + x, f);
-#pragma unroll
-            for (int v = 0; v < 4; v++) o[v] = fmaf(p, f[v], o[v]);
+            const f32x2 pp = pair2(p, p);
+            float f[4], h[4];
+            load8(vs + j * kCols + x, f, h);
+            o[0] = fma2(pp, pair2(f[0], f[1]), o[0]);
+            o[1] = fma2(pp, pair2(f[2], f[3]), o[1]);
+            o[2] = fma2(pp, pair2(h[0], h[1]), o[2]);
+            o[3] = fma2(pp, pair2(h[2], h[3]), o[3]);
         }
         T* to = og + static_cast<int64_t>(i) * dv + x;
-        float sum[4];
-        load4(acc + i * (kCols + 4) + x, sum);
+        float y[8];
 #pragma unroll
         for (int v = 0; v < 4; v++) {
-            o[v] += sum[v];
-            if (!kRing && x + v < wide) store_f(to + v, o[v]);
+            const float2 z = split2(o[v]);
+            y[2 * v] = z.x;
+            y[2 * v + 1] = z.y;
         }
-        if constexpr (kRing) {
-            if constexpr (sizeof(T) == 4) *reinterpret_cast<float4*>(to) = make_float4(o[0], o[1], o[2], o[3]);
-            else *reinterpret_cast<uint2*>(to) = make_uint2(pack(o[0], o[1]), pack(o[2], o[3]));
+        if (kRing && x + 8 <= wide) {  // rows of multiples of four values at least
+            if constexpr (sizeof(T) == 4) {
+                *reinterpret_cast<float4*>(to) = make_float4(y[0], y[1], y[2], y[3]);
+                *reinterpret_cast<float4*>(to + 4) = make_float4(y[4], y[5], y[6], y[7]);
+            } else {
+                *reinterpret_cast<uint2*>(to) = make_uint2(pack(y[0], y[1]), pack(y[2], y[3]));
+                *reinterpret_cast<uint2*>(to + 4) = make_uint2(pack(y[4], y[5]), pack(y[6], y[7]));
+            }
+        } else {
+#pragma unroll
+            for (int v = 0; v < 8; v++)
+                if (x + v < wide) store_f(to + v, y[v]);
         }
     }
 }
 
-template <typename T, int MT, int NG, int CU, int kStageRows>
-cudaError_t launch_tree(const TreeCall& c, cudaStream_t stream) {
-    constexpr int kNb = 16 * MT * NG;
-    constexpr bool ring = kStageRows > 0;
-    const Layout s = layout<T>(kNb, c.N, c.dk, 32 * CU, c.Lmax, kStageRows);
-    const dim3 grid(static_cast<unsigned>(c.B) * c.H, (c.N - 1) / kNb + 1, (c.dv - 1) / (32 * CU) + 1);
-    // stages of the ring: four, or as many as leave room for two blocks on an SM, two at least
-    const int64_t rows = static_cast<int64_t>(c.B) * c.H * c.Lmax * c.dk;
-    int stages = 0;
-    CUtensorMap map = {};
-    if (ring) {
-        if (!make_map_box(&map, c.states, true, static_cast<uint64_t>(rows), static_cast<uint64_t>(c.dv), 32, kStageRows))
+// Map of a tensor [z][rows][cols]; parts of a box outside a matrix read as zeros.
+bool map_3d(CUtensorMap* m, const void* base, bool f32, int64_t z, int rows, int cols, int box_cols, int box_rows, bool swizzle) {
+    auto fn = encode_fn();
+    if (!fn) return false;
+    const cuuint64_t e = f32 ? 4 : 2, row = static_cast<cuuint64_t>(cols) * e;
+    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows), static_cast<cuuint64_t>(z)};
+    const cuuint64_t strides[2] = {row, row * rows};
+    const cuuint32_t box[3] = {static_cast<cuuint32_t>(box_cols), static_cast<cuuint32_t>(box_rows), 1}, one[3] = {1, 1, 1};
+    return fn(m, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims,
+              strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              swizzle ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <typename T, int MT, int NG, int CW, int NT, int kStageRows>
+cudaError_t launch_tree(const TreeCall& c, int stages, cudaStream_t stream) {
+    constexpr int kNb = 16 * MT * NG, kCols = 8 * CW * NT;
+    const int64_t heads = static_cast<int64_t>(c.B) * c.H;
+    Maps maps = {};
+    if (kStageRows > 0) {
+        if (!map_3d(&maps.states, c.states, true, heads * c.Lmax, c.dk, c.dv, 32, kStageRows, true)) return cudaErrorInvalidValue;
+        const int keys = (c.N + 7) / 8 * 8;
+        if (Parts<T>::q == 1 &&
+            (!map_3d(&maps.q, c.q, false, heads, c.N, c.dk, 64, kNb, true) ||
+             !map_3d(&maps.k, c.k, false, heads, c.N, c.dk, 64, keys, true) ||
+             !map_3d(&maps.v, c.v, false, heads, c.N, c.dv, kCols, keys, false)))
             return cudaErrorInvalidValue;
-        const int most = c.Lmax * ((c.dk - 1) / (ring ? kStageRows : 1) + 1);
-        stages = (kHalfSm - s.ring - 1024) / s.stage;
-        stages = stages > kMaxStages ? kMaxStages : stages < 2 ? 2 : stages;
-        if (stages > most) stages = most;
     }
-    const int smem = s.ring + stages * s.stage + (ring ? 1024 : 0);
-    auto go = [&](auto kern) {
-        cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-        if (e != cudaSuccess) return e;
-        kern<<<grid, 256, smem, stream>>>(c, map, stages);
-        note_launch(stream, "decode_tree");
-        return cudaGetLastError();
-    };
-    return go(decode_tree_kernel<T, MT, NG, CU, kStageRows>);
+    const Layout s = layout<T>(kNb, c.N, c.dk, kCols, c.Lmax, kStageRows, stages);
+    auto kern = decode_tree_kernel<T, MT, NG, CW, NT, kStageRows>;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, s.total);
+    if (e != cudaSuccess) return e;
+    const dim3 grid(static_cast<unsigned>(heads * ((c.N - 1) / kNb + 1)), (c.dv - 1) / kCols + 1);
+    kern<<<grid, 256, s.total, stream>>>(c, maps, stages);
+    note_launch(stream, "decode_tree");
+    return cudaGetLastError();
 }
 
-// The stage's size: a whole slot's columns where two of them and another block fit on an SM, else half of its rows.
-template <typename T, int MT, int NG, int CU>
+// The ring: stages of a whole slot's columns, or of part of its rows, the largest of which two fit beside the other blocks of
+// an SM (one, where there is one slot); up to four of them.
+template <typename T, int MT, int NG, int CW, int NT>
 cudaError_t pick_stage(const TreeCall& c, cudaStream_t stream) {
-    constexpr int most = 8 / (CU * NG) * 16 > 64 ? 8 / (CU * NG) * 16 : 64;  // every warp has a unit of a stage
-    if (c.dv % 4 != 0 || c.dv < 32 || static_cast<int64_t>(c.B) * c.H * c.Lmax * c.dk >= (int64_t(1) << 31))
-        return launch_tree<T, MT, NG, CU, 0>(c, stream);
-    const Layout s = layout<T>(16 * MT * NG, c.N, c.dk, 32 * CU, c.Lmax, 128);
+    constexpr int KS = 8 / (CW * NG), least = KS * 16 > 32 ? KS * 16 : 32;  // every warp has a unit of a stage
+    constexpr int middle = least > 64 ? least : 64;
+    const bool tma = Parts<T>::q == 3 || (c.dk % 8 == 0 && c.dv % 8 == 0);  // rows of whole 16-byte pieces
+    const int64_t heads = static_cast<int64_t>(c.B) * c.H;
+    if (c.dv % 4 != 0 || !tma || heads * c.Lmax >= (int64_t(1) << 31)) return launch_tree<T, MT, NG, CW, NT, 0>(c, 0, stream);
+    auto fit = [&](int rows) {
+        const Layout s = layout<T>(16 * MT * NG, c.N, c.dk, 8 * CW * NT, c.Lmax, rows, 0);
+        const int most = c.Lmax * ((c.dk - 1) / rows + 1), n = (room<T>(MT, NT) - s.total) / s.stage;
+        return n < most ? (n < kMaxStages ? n : kMaxStages) : (most < kMaxStages ? most : kMaxStages);
+    };
     const int want = c.Lmax > 1 ? 2 : 1;
-    if (c.dk > 64 && s.ring + want * s.stage + 1024 <= kHalfSm) return launch_tree<T, MT, NG, CU, 128>(c, stream);
-    return launch_tree<T, MT, NG, CU, most>(c, stream);
+    if ((c.dk > 64 || middle == 128) && fit(128) >= want) return launch_tree<T, MT, NG, CW, NT, 128>(c, fit(128), stream);
+    if ((c.dk > 32 || least == middle) && fit(middle) >= want) return launch_tree<T, MT, NG, CW, NT, middle>(c, fit(middle), stream);
+    const int n = fit(least);
+    return launch_tree<T, MT, NG, CW, NT, least>(c, n < want ? want : n, stream);
 }
 
 // ---- commit
@@ -715,15 +878,16 @@ cudaError_t launch_commit(const CommitCall& c, cudaStream_t stream) {
 }  // namespace
 
 cudaError_t decode_tree(int dtype, const TreeCall& c, cudaStream_t stream) {
-    const bool wide = c.dv > 32;
+    // 64 columns to a block, or 32 where that leaves SMs without one
+    const bool wide = c.dv > 32 && static_cast<int64_t>(c.B) * c.H * ((c.dv - 1) / 64 + 1) > 76;
     if (dtype == 1) {
-        if (c.N <= 16) return wide ? pick_stage<float, 1, 1, 2>(c, stream) : pick_stage<float, 1, 1, 1>(c, stream);
-        return wide ? pick_stage<float, 1, 2, 2>(c, stream) : pick_stage<float, 1, 2, 1>(c, stream);
+        if (c.N <= 16) return wide ? pick_stage<float, 1, 1, 2, 4>(c, stream) : pick_stage<float, 1, 1, 1, 4>(c, stream);
+        return wide ? pick_stage<float, 1, 2, 2, 4>(c, stream) : pick_stage<float, 1, 2, 1, 4>(c, stream);
     }
     using T = __nv_bfloat16;
-    if (c.N <= 16) return wide ? pick_stage<T, 1, 1, 2>(c, stream) : pick_stage<T, 1, 1, 1>(c, stream);
-    if (c.N <= 32) return wide ? pick_stage<T, 2, 1, 2>(c, stream) : pick_stage<T, 2, 1, 1>(c, stream);
-    return wide ? pick_stage<T, 2, 2, 2>(c, stream) : pick_stage<T, 2, 2, 1>(c, stream);
+    if (c.N <= 16) return wide ? pick_stage<T, 1, 1, 2, 4>(c, stream) : pick_stage<T, 1, 1, 1, 4>(c, stream);
+    if (c.N <= 32) return wide ? pick_stage<T, 2, 1, 2, 4>(c, stream) : pick_stage<T, 2, 1, 1, 4>(c, stream);
+    return wide ? pick_stage<T, 4, 1, 4, 2>(c, stream) : pick_stage<T, 4, 1, 2, 2>(c, stream);
 }
 
 cudaError_t decode_commit(int dtype, const CommitCall& c, cudaStream_t stream) {
