@@ -97,9 +97,10 @@ template <> struct Parts<float> { static constexpr int q = 3, s = 3; };
 template <typename T>
 __host__ __device__ constexpr int resident(int MT, int NT) { return Parts<T>::q == 1 && MT * NT <= 4 ? 3 : 2; }
 template <typename T>
-__host__ __device__ constexpr int room(int MT, int NT) { return resident<T>(MT, NT) == 3 ? 72 * 1024 : 111 * 1024; }
+__host__ __device__ constexpr int room(int MT, int NT) { return resident<T>(MT, NT) == 3 ? 69 * 1024 : 107 * 1024; }
 
-// Shared memory of decode_tree_kernel, bytes from a multiple of 1024. The sums take the place of q and k at the end.
+// Shared memory of decode_tree_kernel, bytes from a multiple of 1024. The shares' sums take the place
+// of q, k and the ring at the end.
 struct Layout {
     int q, k;      // kTma: panels of 64 columns, rows of 128 bytes, swizzled; else parts of rows of row_bytes
     int panel_q, panel_k;
@@ -107,21 +108,21 @@ struct Layout {
     int v, lam, p, far, up, total;
 };
 __host__ __device__ inline int up1024(int x) { return (x + 1023) / 1024 * 1024; }
-// nodes of a block, all nodes, columns of a block, slots; rows of a stage (0: no ring); its stages
+// nodes of a block, all nodes, columns of a block, slots; rows of a stage (0: no ring); its stages; shares of the warps
 template <typename T>
-__host__ __device__ inline Layout layout(int nb, int N, int dk, int cols, int slots, int stage_rows, int stages) {
+__host__ __device__ inline Layout layout(int nb, int N, int dk, int cols, int slots, int stage_rows, int stages, int shares) {
     Layout s;
-    const int parts = Parts<T>::q, rb = row_bytes(dk), panels = (dk + 63) / 64, sums = nb * (cols + 4) * 4;
+    const int parts = Parts<T>::q, rb = row_bytes(dk), panels = (dk + 63) / 64, sums = shares * nb * (cols + 4) * 4;
     const bool tma = parts == 1 && stage_rows > 0;
     s.panel_q = nb * 128;
     s.panel_k = (N + 7) / 8 * 1024;
     s.q = 0;
     s.k = tma ? panels * s.panel_q : parts * nb * rb;
     const int rows = s.k + (tma ? panels * s.panel_k : parts * N * rb);
-    s.ring = up1024(rows > sums ? rows : sums);
+    s.ring = up1024(rows);
     s.stage = stage_rows * cols * 4;
     s.stages = stages;
-    s.v = s.ring + stages * s.stage;
+    s.v = s.ring + stages * s.stage > sums ? s.ring + stages * s.stage : up1024(sums);
     s.lam = s.v + (N + 7) / 8 * 8 * cols * static_cast<int>(sizeof(T));
     s.p = s.lam + nb * slots * 4;
     s.far = s.p + nb * (N + 1) * 4;
@@ -198,6 +199,28 @@ __device__ __forceinline__ void mma_parts(float (&d)[4], const uint32_t (&a)[kQ]
         }
 }
 
+// What lies between a node and the one that its jump leads to (-1: past the root): steps, sum of the finite log decays of
+// the nodes from it up to there, and how many are -inf. At the end jumps lead past the root everywhere.
+struct __align__(16) Link {
+    int jump, steps;
+    float decay;
+    int zeros;
+};
+__device__ __forceinline__ void scorers_meet() { asm volatile("bar.sync 2, 128;" ::: "memory"); }
+// Walkers' barrier; any(x): whether one of them has x.
+__device__ __forceinline__ void walkers_meet() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+__device__ __forceinline__ bool walkers_any(bool x) {
+    int r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.s32 p, %1, 0;\n\t"
+        "bar.red.or.pred q, 1, 128, p;\n\t"
+        "selp.s32 %0, 1, 0, q;\n\t}"
+        : "=r"(r)
+        : "r"(static_cast<int>(x))
+        : "memory");
+    return r != 0;
+}
 // Maps of the tensors that come by TMA, each [heads (states: slots)][rows][columns].
 struct Maps {
     CUtensorMap states, q, k, v;
@@ -218,9 +241,10 @@ __global__ void __launch_bounds__(256, resident<T>(MT, NT))
     constexpr int kUnits = kStageRows / 16;  // of a stage
     constexpr int kWalkers = 128;            // threads that form the weights
     extern __shared__ __align__(16) char smem_any[];
-    __shared__ int par[kMaxTree], dep[kMaxTree], slot_of[kSlots];
+    __shared__ int par[kMaxTree], slot_of[kSlots];
     __shared__ float la[kMaxTree];
-    __shared__ int64_t slot_at[kSlots];
+    __shared__ Link link[kMaxTree];
+    __shared__ uint4 above[kMaxTree];
     __shared__ __align__(8) uint64_t full[kMaxStages], empty[kMaxStages], inputs;
     char* smem = smem_any + (-smem_u32(smem_any) & 1023u);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, cc = lane & 3;
@@ -230,14 +254,14 @@ __global__ void __launch_bounds__(256, resident<T>(MT, NT))
     const int N = c.N, dk = c.dk, dv = c.dv, dkp = (dk + 15) / 16 * 16, rb = row_bytes(dk), ksteps = dkp / 16;
     const int i0 = static_cast<int>(blockIdx.x % blocks) * kNb, col0 = blockIdx.y * kCols, live = N - i0 < kNb ? N - i0 : kNb;
     const bool linear = c.t == nullptr;
-    const Layout s = layout<T>(kNb, N, dk, kCols, c.Lmax, kStageRows, stages);
+    const Layout s = layout<T>(kNb, N, dk, kCols, c.Lmax, kStageRows, stages, KS);
     char *qs = smem + s.q, *ks = smem + s.k, *ring = smem + s.ring;
     T* vs = reinterpret_cast<T*>(smem + s.v);               // [N][kCols]
     float* lam = reinterpret_cast<float*>(smem + s.lam);    // [kNb][Lmax]
     float* P = reinterpret_cast<float*>(smem + s.p);        // [kNb][N + 1]: weights, then scores times weights
     float* far = reinterpret_cast<float*>(smem + s.far);    // [slots][kNb]
     uint8_t* up = reinterpret_cast<uint8_t*>(smem + s.up);  // [kNb][N]: a node and those above it, upwards
-    float* acc = reinterpret_cast<float*>(smem);            // [kNb][kCols + 4], once q and k are done with
+    float* acc = reinterpret_cast<float*>(smem);            // [KS][kNb][kCols + 4], once q, k and the ring are done with
     const int wide = dv - col0 < kCols ? dv - col0 : kCols; // columns of the block
 
     // The held slots of t - 1, in pieces of kStageRows rows (dk <= 128).
@@ -274,6 +298,8 @@ __global__ void __launch_bounds__(256, resident<T>(MT, NT))
                 tma_load_3d(vs, &maps.v, &inputs, col0, 0, static_cast<int>(bh));
             }
         }
+        __syncwarp();
+        if (kTma) scorers_meet();
         const int64_t t = linear ? 1 : c.t[b];
         const int rounds = held(t) * pieces;
         for (int l = lane; l < kSlots && rounds > 0; l += 32)
@@ -281,7 +307,6 @@ __global__ void __launch_bounds__(256, resident<T>(MT, NT))
                 const int64_t below = l == 0 ? 0 : (int64_t(1) << (l - 1)) - 1;
                 const int at = l == 0 ? 0 : 1 + __popcll(static_cast<unsigned long long>((t - 1) & below));
                 slot_of[at] = l;
-                slot_at[at] = ((t - 1) >> l) << l;
             }
         __syncwarp();
         if (kRing)
@@ -308,8 +333,10 @@ __global__ void __launch_bounds__(256, resident<T>(MT, NT))
         }
         copies_group();
         copies_done<0>();
+        __syncthreads();
+    } else if (warp >= kWalkers / 32 && warp < kWarps - 1) {
+        scorers_meet();  // the barriers are set up
     }
-    __syncthreads();  // barriers and slots are there (not kTma: everything is)
 
     // Operands of 16 queries (from row r0, summed indexes 16 kk ..), and of 8 keys (from row j0, 16 kk .. + 31).
     auto load_q = [&](uint32_t (&a)[kQ][4], int r0, int kk) {
@@ -384,51 +411,85 @@ __global__ void __launch_bounds__(256, resident<T>(MT, NT))
     float held_scores[2][4][4];
     const int scorer = warp - kWalkers / 32;
     if (tid < kWalkers) {
-        // Depths and weights. A walk up only goes to smaller indexes, so it ends in a bad tree too.
+        // Depths, sums of log decays and the nodes above each node, by jumps that double in length: log2 of the depth
+        // rounds. A thread to a node (N <= 128).
+        static_assert(kMaxTree == kWalkers);
         copies_done<0>();
-        asm volatile("bar.sync 1, 128;" ::: "memory");
-        auto depth = [&](int i, uint8_t* list) {
-            int d = -1;
-            for (int j = i; j >= 0; d++) {
-                const int p = par[j];
-                if (list) list[d + 1] = static_cast<uint8_t>(j);
-                if (p >= j || p < -2 || (p == -2 && j != i)) {
-                    bad = true;
-                    return d;
-                }
-                j = p;
+        walkers_meet();
+        const int p = tid < N ? par[tid] : -2;
+        Link me = {p, p >= 0 ? 1 : 0, 0.f, 0};
+        uint4 mask = make_uint4(0u, 0u, 0u, 0u);
+        if (tid < N) {
+            if (p >= tid || p < -2 || (p >= 0 && par[p] == -2)) {
+                bad = true;
+                me.jump = -1;
             }
-            if (!linear && t + d >= (int64_t(1) << (c.Lmax - 1))) bad = true;
-            return d;
-        };
-        // kEach threads to a node, each with every so many of its steps and of the held slots
+            const float x = linear ? 0.f : la[tid];
+            me.zeros = x == -INFINITY;
+            me.decay = me.zeros ? 0.f : x;
+            const uint32_t bit = 1u << (tid & 31);
+            (tid < 32 ? mask.x : tid < 64 ? mask.y : tid < 96 ? mask.z : mask.w) = bit;
+        }
+        for (;;) {
+            link[tid] = me;
+            above[tid] = mask;
+            walkers_meet();
+            if (me.jump >= 0) {
+                const Link to = link[me.jump];
+                const uint4 m = above[me.jump];
+                me.jump = to.jump;
+                me.steps += to.steps;
+                me.decay += to.decay;
+                me.zeros += to.zeros;
+                mask = make_uint4(mask.x | m.x, mask.y | m.y, mask.z | m.z, mask.w | m.w);
+            }
+            if (!walkers_any(me.jump >= 0)) break;
+        }
+        if (!linear && tid < N && t + me.steps >= (int64_t(1) << (c.Lmax - 1))) bad = true;
+        link[tid] = me;
+        above[tid] = mask;
+        walkers_meet();
+        // weights: kEach threads to a node, each with every so many of the nodes above it and of the held slots
         constexpr int kEach = kWalkers / kNb;
-        const int i = tid % kNb, first = tid / kNb;
-        if (i < live) {
+        const int i = tid % kNb, first = tid / kNb, node = i0 + i;
+        if (i < live && par[node] != -2 && (linear || (t >= 0 && t < (int64_t(1) << (c.Lmax - 1))))) {
             const float lg = linear ? c.log_a[h] : 0.f;
-            const int d = depth(i0 + i, first == 0 ? up + i * N : nullptr);
-            if (first == 0) dep[i] = d;
-            if (!bad && par[i0 + i] != -2) {
-                float D = 0.f;
-                int turn = first, n = 0;
-                for (int j = i0 + i; j >= 0; j = par[j], n++) {
-                    if (turn-- == 0) {
-                        turn = kEach - 1;
-                        P[i * (N + 1) + j] =
-                            linear ? (n == 0 ? 1.f : expf(lg * static_cast<float>(n)))
-                                   : lam[i * c.Lmax + 64 - __clzll(static_cast<long long>((t + d) ^ (t + d - n)))] * expf(D);
-                    }
-                    if (!linear) D += la[j];
+            const Link at = link[node];
+            const uint4 line = above[node];
+            const int64_t pos = t + at.steps;
+            const float* lam_i = lam + i * c.Lmax;
+            int turn = first;
+#pragma unroll
+            for (int y = 0; y < kMaxTree / 32; y++) {
+                if (y * 32 > node) break;
+                for (uint32_t bits = y == 0 ? line.x : y == 1 ? line.y : y == 2 ? line.z : line.w; bits; bits &= bits - 1) {
+                    if (turn-- != 0) continue;
+                    turn = kEach - 1;
+                    const int j = y * 32 + __ffs(static_cast<int>(bits)) - 1;
+                    const Link other = link[j];
+                    const int n = at.steps - other.steps;
+                    up[i * N + n] = static_cast<uint8_t>(j);
+                    float w;
+                    if (linear) w = n == 0 ? 1.f : expf(lg * static_cast<float>(n));
+                    else
+                        w = at.zeros > other.zeros ? 0.f
+                                                   : lam_i[64 - __clzll(static_cast<long long>(pos ^ (pos - n)))] *
+                                                         expf(at.decay - other.decay);
+                    P[i * (N + 1) + j] = w;
                 }
-                const float whole = linear ? expf(lg * static_cast<float>(d + 1)) : expf(D);
-                for (int m = first; m < slots; m += kEach)
-                    far[m * kNb + i] =
-                        linear ? whole
-                               : whole * lam[i * c.Lmax + 64 - __clzll(static_cast<long long>((t + d) ^ slot_at[m]))];
+            }
+            const float whole = linear ? expf(lg * static_cast<float>(at.steps + 1)) : at.zeros ? 0.f : expf(at.decay);
+            // the blocks of the walk of t - 1 begin at t - 1 and where its set bits are cleared one by one
+            if (linear) {
+                if (first == 0) far[i] = whole;
+            } else {
+                int64_t begin = t - 1;
+                for (int m = 0; m < slots; m++, begin &= begin - 1) {
+                    if (m % kEach != first) continue;
+                    far[m * kNb + i] = whole * lam_i[64 - __clzll(static_cast<long long>(pos ^ begin))];
+                }
             }
         }
-        for (int j = tid; j < N; j += kWalkers)  // the other blocks' nodes
-            if (j < i0 || j >= i0 + live) depth(j, nullptr);
     } else {
         if (kTma) in_time = mbar_try_wait(&inputs, 0) || mbar_wait(&inputs, 0);
 #pragma unroll
@@ -587,43 +648,35 @@ __global__ void __launch_bounds__(256, resident<T>(MT, NT))
     }
     if (bad) return;
     __syncthreads();  // q is not read any more
-    // the shares are added in order; a lane holds 2 NT neighbouring columns of its rows
-    for (int sh = 0; sh < KS; sh++) {
-        if (share == sh) {
+    // the shares' sums; a lane holds 2 NT neighbouring columns of its rows
+    constexpr int kSums = kNb * (kCols + 4);
 #pragma unroll
-            for (int mt = 0; mt < MT; mt++)
+    for (int mt = 0; mt < MT; mt++)
 #pragma unroll
-                for (int r = 0; r < 4; r += 2) {
-                    float* at = acc + ((ng * MT + mt) * 16 + g + r * 4) * (kCols + 4) + cw * 8 * NT + cc * 2 * NT;
+        for (int r = 0; r < 4; r += 2) {
+            float* at = acc + share * kSums + ((ng * MT + mt) * 16 + g + r * 4) * (kCols + 4) + cw * 8 * NT + cc * 2 * NT;
 #pragma unroll
-                    for (int x = 0; x < 2 * NT; x += 4) {
-                        float4 y;
-                        y.x = out[mt][x % NT][r + x / NT];
-                        y.y = out[mt][(x + 1) % NT][r + (x + 1) / NT];
-                        y.z = out[mt][(x + 2) % NT][r + (x + 2) / NT];
-                        y.w = out[mt][(x + 3) % NT][r + (x + 3) / NT];
-                        if (sh > 0) {
-                            const float4 z = *reinterpret_cast<const float4*>(at + x);
-                            y.x += z.x; y.y += z.y; y.z += z.z; y.w += z.w;
-                        }
-                        *reinterpret_cast<float4*>(at + x) = y;
-                    }
-                }
+            for (int x = 0; x < 2 * NT; x += 4)
+                *reinterpret_cast<float4*>(at + x) =
+                    make_float4(out[mt][x % NT][r + x / NT], out[mt][(x + 1) % NT][r + (x + 1) / NT],
+                                out[mt][(x + 2) % NT][r + (x + 2) / NT], out[mt][(x + 3) % NT][r + (x + 3) / NT]);
         }
-        __syncthreads();
-    }
+    __syncthreads();
     // the nodes above, in fp32, and the result; eight columns of a node to a thread
     T* og = static_cast<T*>(c.out) + (bh * N + i0) * dv + col0;
     for (int e = tid; e < live * (kCols / 8); e += kThreads) {
         const int i = e / (kCols / 8), x = (e - i * (kCols / 8)) * 8;
         if (par[i0 + i] == -2 || x >= wide) continue;
         f32x2 o[4];
-        {
-            const float4* sum = reinterpret_cast<const float4*>(acc + i * (kCols + 4) + x);
+#pragma unroll
+        for (int sh = 0; sh < KS; sh++) {  // in order
+            const float4* sum = reinterpret_cast<const float4*>(acc + sh * kSums + i * (kCols + 4) + x);
             const float4 y = sum[0], z = sum[1];
-            o[0] = pair2(y.x, y.y); o[1] = pair2(y.z, y.w); o[2] = pair2(z.x, z.y); o[3] = pair2(z.z, z.w);
+            const f32x2 add[4] = {pair2(y.x, y.y), pair2(y.z, y.w), pair2(z.x, z.y), pair2(z.z, z.w)};
+#pragma unroll
+            for (int v = 0; v < 4; v++) o[v] = sh == 0 ? add[v] : add2(o[v], add[v]);
         }
-        const int d = dep[i];
+        const int d = link[i0 + i].steps;
 #pragma unroll 2
         for (int n = 0; n <= d; n++) {
             const int j = up[i * N + n];
@@ -688,7 +741,7 @@ cudaError_t launch_tree(const TreeCall& c, int stages, cudaStream_t stream) {
              !map_3d(&maps.v, c.v, false, heads, c.N, c.dv, kCols, keys, false)))
             return cudaErrorInvalidValue;
     }
-    const Layout s = layout<T>(kNb, c.N, c.dk, kCols, c.Lmax, kStageRows, stages);
+    const Layout s = layout<T>(kNb, c.N, c.dk, kCols, c.Lmax, kStageRows, stages, 8 / (CW * NG));
     auto kern = decode_tree_kernel<T, MT, NG, CW, NT, kStageRows>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, s.total);
     if (e != cudaSuccess) return e;
@@ -708,8 +761,8 @@ cudaError_t pick_stage(const TreeCall& c, cudaStream_t stream) {
     const int64_t heads = static_cast<int64_t>(c.B) * c.H;
     if (c.dv % 4 != 0 || !tma || heads * c.Lmax >= (int64_t(1) << 31)) return launch_tree<T, MT, NG, CW, NT, 0>(c, 0, stream);
     auto fit = [&](int rows) {
-        const Layout s = layout<T>(16 * MT * NG, c.N, c.dk, 8 * CW * NT, c.Lmax, rows, 0);
-        const int most = c.Lmax * ((c.dk - 1) / rows + 1), n = (room<T>(MT, NT) - s.total) / s.stage;
+        const Layout s = layout<T>(16 * MT * NG, c.N, c.dk, 8 * CW * NT, c.Lmax, rows, 0, KS);
+        const int most = c.Lmax * ((c.dk - 1) / rows + 1), n = (room<T>(MT, NT) - (s.total - s.v) - s.ring) / s.stage;
         return n < most ? (n < kMaxStages ? n : kMaxStages) : (most < kMaxStages ? most : kMaxStages);
     };
     const int want = c.Lmax > 1 ? 2 : 1;

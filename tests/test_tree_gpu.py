@@ -60,8 +60,9 @@ def draft(r, B, H, N, dk, dv, dtype, Lmax, t, one_tree=False, chain=0.4, live=No
 
 
 def gate_units(log_a, n):
-    """What a branch's weight may be off by, in units of 2^-24 (see tree_check)."""
-    return n * (np.abs(log_a).max() * n + 1)
+    """What a branch's weight may be off by, in units of 2^-24 (see tree_check): the exponent is the difference of two sums
+    of up to n log decays, each of whose additions rounds."""
+    return 2 * n * (np.abs(log_a).max() * n + 1)
 
 
 CASES = [  # B, H, N, dk, dv, Lmax, t
