@@ -102,18 +102,18 @@ __host__ __device__ constexpr int room(int MT, int NT) { return resident<T>(MT, 
 // Shared memory of decode_tree_kernel, bytes from a multiple of 1024. The shares' sums take the place
 // of q, k and the ring at the end.
 struct Layout {
-    int q, k;      // kTma: panels of 64 columns, rows of 128 bytes, swizzled; else parts of rows of row_bytes
+    int q, k;      // kAll: panels of 64 columns, rows of 128 bytes, swizzled; else parts of rows of row_bytes
     int panel_q, panel_k;
     int ring, stage, stages;
     int v, lam, p, far, up, total;
 };
 __host__ __device__ inline int up1024(int x) { return (x + 1023) / 1024 * 1024; }
-// nodes of a block, all nodes, columns of a block, slots; rows of a stage (0: no ring); its stages; shares of the warps
+// nodes of a block, all nodes, columns of a block, slots; rows of a stage; its stages; shares of the warps
 template <typename T>
-__host__ __device__ inline Layout layout(int nb, int N, int dk, int cols, int slots, int stage_rows, int stages, int shares) {
+__host__ __device__ inline Layout layout(int nb, int N, int dk, int cols, int slots, int stage_rows, int stages, int shares,
+                                         bool tma) {
     Layout s;
     const int parts = Parts<T>::q, rb = row_bytes(dk), panels = (dk + 63) / 64, sums = shares * nb * (cols + 4) * 4;
-    const bool tma = parts == 1 && stage_rows > 0;
     s.panel_q = nb * 128;
     s.panel_k = (N + 7) / 8 * 1024;
     s.q = 0;
@@ -139,6 +139,12 @@ __device__ __forceinline__ void copies_group() { asm volatile("cp.async.commit_g
 template <int kLeft>
 __device__ __forceinline__ void copies_done() { asm volatile("cp.async.wait_group %0;" ::"n"(kLeft) : "memory"); }
 
+// Loads that may run ahead of stores.
+__device__ __forceinline__ float load_nc(const float* p) { return __ldg(p); }
+__device__ __forceinline__ float load_nc(const __nv_bfloat16* p) {
+    return __uint_as_float(static_cast<uint32_t>(__ldg(reinterpret_cast<const unsigned short*>(p))) << 16);
+}
+
 // Rows of q or k into shared memory as bf16 parts, zeros behind dk and behind the valid rows.
 template <typename T, int kThreads>
 __device__ __forceinline__ void stage_rows(char* to, const T* from, int rows, int valid, int dk, int dkp) {
@@ -146,6 +152,7 @@ __device__ __forceinline__ void stage_rows(char* to, const T* from, int rows, in
     const int rb = row_bytes(dk);
     if (dk % 8 == 0) {  // rows of whole 16-byte pieces: eight values at a time
         const int per = dkp / 8, step = kThreads / per, first = threadIdx.x / per, c = (threadIdx.x - first * per) * 8;
+#pragma unroll 4
         for (int i = first < step ? first : rows; i < rows; i += step) {
             char* at = to + i * rb + c * 2;
             const T* src = from + static_cast<int64_t>(i) * dk + c;
@@ -172,10 +179,11 @@ __device__ __forceinline__ void stage_rows(char* to, const T* from, int rows, in
         return;
     }
     const int pairs = dkp / 2;
+#pragma unroll 4
     for (int e = threadIdx.x; e < rows * pairs; e += kThreads) {
         const int i = e / pairs, c = (e - i * pairs) * 2;
         const T* src = from + static_cast<int64_t>(i) * dk + c;
-        const float x = i < valid && c < dk ? load_f(src) : 0.f, y = i < valid && c + 1 < dk ? load_f(src + 1) : 0.f;
+        const float x = i < valid && c < dk ? load_nc(src) : 0.f, y = i < valid && c + 1 < dk ? load_nc(src + 1) : 0.f;
         uint32_t p[kParts];
         cut<kParts>(x, y, p);
 #pragma unroll
@@ -221,23 +229,26 @@ __device__ __forceinline__ bool walkers_any(bool x) {
         : "memory");
     return r != 0;
 }
+enum Mode { kNone, kStates, kAll };
+
 // Maps of the tensors that come by TMA, each [heads (states: slots)][rows][columns].
 struct Maps {
     CUtensorMap states, q, k, v;
 };
 
 // Grid: (heads of all sequences times blocks of 16 MT NG nodes, column blocks of 8 CW NT). The warps are CW column pieces of
-// 8 NT times NG groups of 16 MT nodes times KS shares of the 16-row units. kStageRows: state rows of a stage of the ring, or
-// 0 for loads by the lanes themselves (rows that are no multiples of 16 bytes).
+// 8 NT times NG groups of 16 MT nodes times KS shares of the 16-row units. kStageRows: state rows of a stage of the ring.
+// kMode: what comes by TMA, as rows of multiples of 16 bytes can; the states' ring is else filled by 4-byte copies of every
+// thread, in two stages.
 //
 // Four warps walk the tree and form the weights while the other four multiply queries and keys; most of a short block's
 // time is latency. With one tree after another (a first version): 10000 cycles before the first slot, now 5000.
-template <typename T, int MT, int NG, int CW, int NT, int kStageRows>
+template <typename T, int MT, int NG, int CW, int NT, int kStageRows, int kMode>
 __global__ void __launch_bounds__(256, resident<T>(MT, NT))
     decode_tree_kernel(const TreeCall c, const __grid_constant__ Maps maps, const int stages) {
     constexpr int kWarps = 8, kThreads = kWarps * 32, kNb = 16 * MT * NG, kCols = 8 * CW * NT, KS = kWarps / (CW * NG);
     constexpr int kQ = Parts<T>::q, kS = Parts<T>::s, CU = kCols / 32;
-    constexpr bool kRing = kStageRows > 0, kTma = kRing && kQ == 1;
+    constexpr bool kTma = kMode >= kStates, kTmaIn = kMode == kAll;
     constexpr int kUnits = kStageRows / 16;  // of a stage
     constexpr int kWalkers = 128;            // threads that form the weights
     extern __shared__ __align__(16) char smem_any[];
@@ -254,7 +265,7 @@ __global__ void __launch_bounds__(256, resident<T>(MT, NT))
     const int N = c.N, dk = c.dk, dv = c.dv, dkp = (dk + 15) / 16 * 16, rb = row_bytes(dk), ksteps = dkp / 16;
     const int i0 = static_cast<int>(blockIdx.x % blocks) * kNb, col0 = blockIdx.y * kCols, live = N - i0 < kNb ? N - i0 : kNb;
     const bool linear = c.t == nullptr;
-    const Layout s = layout<T>(kNb, N, dk, kCols, c.Lmax, kStageRows, stages, KS);
+    const Layout s = layout<T>(kNb, N, dk, kCols, c.Lmax, kStageRows, stages, KS, kTmaIn);
     char *qs = smem + s.q, *ks = smem + s.k, *ring = smem + s.ring;
     T* vs = reinterpret_cast<T*>(smem + s.v);               // [N][kCols]
     float* lam = reinterpret_cast<float*>(smem + s.lam);    // [kNb][Lmax]
@@ -265,7 +276,7 @@ __global__ void __launch_bounds__(256, resident<T>(MT, NT))
     const int wide = dv - col0 < kCols ? dv - col0 : kCols; // columns of the block
 
     // The held slots of t - 1, in pieces of kStageRows rows (dk <= 128).
-    const int pieces = !kRing || kStageRows >= 128 ? 1 : (dk - 1) / (kRing ? kStageRows : 1) + 1;
+    const int pieces = kStageRows >= 128 ? 1 : (dk - 1) / kStageRows + 1;
     constexpr int kBox = kStageRows * 128;          // bytes of a stage's 32 columns
     auto copy = [&](int at, int slot, int piece) {  // into stage `at`, by one thread
         uint64_t* bar = &full[at];
@@ -288,7 +299,7 @@ __global__ void __launch_bounds__(256, resident<T>(MT, NT))
             }
             mbar_init(&inputs, 1);
             fence_mbar_init();
-            if constexpr (kTma) {
+            if constexpr (kTmaIn) {
                 const int panels = (dk + 63) / 64;
                 mbar_expect_tx(&inputs, panels * (s.panel_q + s.panel_k) + (N + 7) / 8 * 8 * kCols * 2);
                 for (int y = 0; y < panels; y++) {
@@ -299,7 +310,7 @@ __global__ void __launch_bounds__(256, resident<T>(MT, NT))
             }
         }
         __syncwarp();
-        if (kTma) scorers_meet();
+        if (kTmaIn) scorers_meet();
         const int64_t t = linear ? 1 : c.t[b];
         const int rounds = held(t) * pieces;
         for (int l = lane; l < kSlots && rounds > 0; l += 32)
@@ -309,7 +320,7 @@ __global__ void __launch_bounds__(256, resident<T>(MT, NT))
                 slot_of[at] = l;
             }
         __syncwarp();
-        if (kRing)
+        if (kTma)
             for (int r = 0; r < stages && r < rounds && lane == 0; r++) copy(r, slot_of[r / pieces], r % pieces);
     }
     if (tid < kWalkers) {
@@ -323,13 +334,37 @@ __global__ void __launch_bounds__(256, resident<T>(MT, NT))
     }
     const int64_t t = linear ? 1 : c.t[b];
     const int slots = held(t), rounds = slots * pieces;
+    // A round's rows into stage `at` as TMA lays them, by all threads, zeros behind them; columns behind the last stay zero.
+    auto fill = [&](int at, int slot, int piece) {
+        const int r0 = piece * kStageRows, rows = dk - r0 < kStageRows ? dk - r0 : kStageRows;
+        const float* from = c.states + ((bh * c.Lmax + slot) * dk + r0) * dv + col0;
+        char* to = ring + at * s.stage;
+        const int down = kThreads / wide, right = kThreads - down * wide;
+        int r = tid / wide, x = tid - r * wide;
+        while (r < (rows + 15) / 16 * 16) {
+            char* place = to + x / 32 * kBox + r * 128 + ((x % 32 / 4 ^ (r & 7)) << 4) + x % 4 * 4;
+            if (r < rows) copy_async<4>(place, from + static_cast<int64_t>(r) * dv + x);
+            else *reinterpret_cast<float*>(place) = 0.f;
+            r += down;
+            x += right;
+            if (x >= wide) {
+                x -= wide;
+                r++;
+            }
+        }
+        copies_group();
+    };
     if constexpr (!kTma) {
+        for (int e = tid; e < stages * s.stage / 16; e += kThreads) reinterpret_cast<uint4*>(ring)[e] = make_uint4(0u, 0u, 0u, 0u);
+    }
+    if constexpr (!kTmaIn) {
         stage_rows<T, kThreads>(qs, static_cast<const T*>(c.q) + (bh * N + i0) * dk, kNb, live, dk, dkp);
         stage_rows<T, kThreads>(ks, static_cast<const T*>(c.k) + bh * N * dk, N, N, dk, dkp);
         const T* vg = static_cast<const T*>(c.v) + bh * N * dv + col0;
+#pragma unroll 4
         for (int e = tid; e < N * kCols; e += kThreads) {
             const int j = e / kCols, x = e - j * kCols;
-            if (x < wide) vs[e] = vg[static_cast<int64_t>(j) * dv + x];
+            if (x < wide) store_f(vs + e, load_nc(vg + static_cast<int64_t>(j) * dv + x));
         }
         copies_group();
         copies_done<0>();
@@ -340,7 +375,7 @@ __global__ void __launch_bounds__(256, resident<T>(MT, NT))
 
     // Operands of 16 queries (from row r0, summed indexes 16 kk ..), and of 8 keys (from row j0, 16 kk .. + 31).
     auto load_q = [&](uint32_t (&a)[kQ][4], int r0, int kk) {
-        if constexpr (kTma) {
+        if constexpr (kTmaIn) {
             ldmatrix4(a[0], smem_u32(qs) + (kk >> 2) * s.panel_q + (r0 + (lane & 15)) * 128 +
                                 ((((kk & 3) * 2 + (lane >> 4)) ^ (lane & 7)) << 4));
         } else {
@@ -350,7 +385,7 @@ __global__ void __launch_bounds__(256, resident<T>(MT, NT))
         }
     };
     auto load_k = [&](uint32_t (&z)[kQ][4], int j0, int kk) {
-        if constexpr (kTma) {
+        if constexpr (kTmaIn) {
             ldmatrix4(z[0], smem_u32(ks) + (kk >> 2) * s.panel_k + (j0 + (lane & 7)) * 128 +
                                 ((((kk & 3) * 2 + (lane >> 3)) ^ (lane & 7)) << 4));
         } else {
@@ -491,7 +526,7 @@ __global__ void __launch_bounds__(256, resident<T>(MT, NT))
             }
         }
     } else {
-        if (kTma) in_time = mbar_try_wait(&inputs, 0) || mbar_wait(&inputs, 0);
+        if (kTmaIn) in_time = mbar_try_wait(&inputs, 0) || mbar_wait(&inputs, 0);
 #pragma unroll
         for (int y = 0; y < 2; y++)
             if (scorer + 4 * y < mts * groups) score(held_scores[y], scorer + 4 * y);
@@ -502,7 +537,7 @@ __global__ void __launch_bounds__(256, resident<T>(MT, NT))
 #pragma unroll
         for (int y = 0; y < 2; y++)
             if (scorer + 4 * y < mts * groups) onto_weights(held_scores[y], scorer + 4 * y);
-    } else if (kTma) {
+    } else if (kTmaIn) {
         in_time = mbar_try_wait(&inputs, 0) || mbar_wait(&inputs, 0);
     }
     for (int u = 8 + warp; u < mts * groups; u += kWarps) {
@@ -556,38 +591,39 @@ __global__ void __launch_bounds__(256, resident<T>(MT, NT))
     };
     using yes = std::true_type;
     using no = std::false_type;
-    constexpr int kRow[4] = {0, 1, 8, 9};
-    if constexpr (kRing) {
-        int m = 0, piece = 0, slot_ahead = stages / pieces, piece_ahead = stages % pieces, at = 0, issued = -1;
+    // places of the lane's pieces in a unit's swizzled rows 2 cc and 2 cc + 1; those 8 rows on lie alike
+    const int chunk = colw % 32 / 4, rest = colw % 4 * 4;
+    const int even = cc * 256 + ((chunk ^ (cc * 2)) << 4) + rest, odd = cc * 256 + 128 + ((chunk ^ (cc * 2 + 1)) << 4) + rest;
+    const bool mine = share < ksteps;  // whether any unit of a slot is this warp's
+    // a stage's units; read(): once the last of them is in registers
+    auto consume = [&](int at, int piece, auto read) {
+        const char* st = ring + at * s.stage + colw / 32 * kBox;
+        const int left = dk - piece * kStageRows;  // rows of the stage that are the slot's; zeros lie behind them
+        constexpr int kTimes = (kUnits + KS - 1) / KS;
+        float f[kTimes][4][NT];
+#pragma unroll
+        for (int k = 0; k < kTimes; k++) {
+            const int u = share + k * KS;
+            if (u * 16 >= left || u >= kUnits) break;
+#pragma unroll
+            for (int r = 0; r < 4; r++)
+                load_nt(reinterpret_cast<const float*>(st + u * 2048 + (r & 1 ? odd : even) + (r >> 1) * 1024), f[k][r]);
+            if (k + 1 == kTimes || (u + KS) * 16 >= left || u + KS >= kUnits) read();
+            if (k == 0 && piece == 0) multiply(f[k], piece * kUnits + u, yes());
+            else multiply(f[k], piece * kUnits + u, no());
+        }
+        if (share * 16 >= left || share >= kUnits) read();  // nothing here for this warp
+    };
+    int m = 0, piece = 0;
+    if constexpr (kTma) {
+        int slot_ahead = stages / pieces, piece_ahead = stages % pieces, at = 0, issued = -1;
         uint32_t parity = 0;
-        // places of the lane's pieces in a unit's swizzled rows 2 cc and 2 cc + 1; those 8 rows on lie alike
-        const int chunk = colw % 32 / 4, rest = colw % 4 * 4;
-        const int even = cc * 256 + ((chunk ^ (cc * 2)) << 4) + rest, odd = cc * 256 + 128 + ((chunk ^ (cc * 2 + 1)) << 4) + rest;
-        const bool mine = share < ksteps;  // whether any unit of a slot is this warp's
         for (int round = 0; round < rounds; round++) {
             if (in_time && !mbar_try_wait(&full[at], parity)) in_time = mbar_wait(&full[at], parity);
-            const char* st = ring + at * s.stage + colw / 32 * kBox;
-            const int left = dk - piece * kStageRows;  // rows of the stage that are the slot's; zeros lie behind them
-            constexpr int kTimes = (kUnits + KS - 1) / KS;
-            float f[kTimes][4][NT];
-#pragma unroll
-            for (int k = 0; k < kTimes; k++) {
-                const int u = share + k * KS;
-                if (u * 16 >= left || u >= kUnits) break;
-#pragma unroll
-                for (int r = 0; r < 4; r++)
-                    load_nt(reinterpret_cast<const float*>(st + u * 2048 + (r & 1 ? odd : even) + (r >> 1) * 1024), f[k][r]);
-                if (k + 1 == kTimes || (u + KS) * 16 >= left || u + KS >= kUnits) {  // read to the end
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&empty[at]);
-                }
-                if (k == 0 && piece == 0) multiply(f[k], piece * kUnits + u, yes());
-                else multiply(f[k], piece * kUnits + u, no());
-            }
-            if (share * 16 >= left || share >= kUnits) {  // nothing here for this warp
+            consume(at, piece, [&] {
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&empty[at]);
-            }
+            });
             if (warp == (round & (kWarps - 1)) && round + stages < rounds) {  // the stage's next rows, by one warp in turn
                 if (in_time && !mbar_try_wait(&empty[at], parity)) in_time = mbar_wait(&empty[at], parity);
                 in_time = __all_sync(0xffffffffu, in_time);
@@ -615,35 +651,20 @@ __global__ void __launch_bounds__(256, resident<T>(MT, NT))
             if (issued >= 0) mbar_wait(&full[issued % stages], (issued / stages) & 1);
             if (warp == kWarps - 1)
                 for (int r = 0; r < stages && r < rounds; r++) mbar_wait(&full[r], 0);
-            if (kTma && warp == kWarps - 1) mbar_wait(&inputs, 0);
+            if (kTmaIn && warp == kWarps - 1) mbar_wait(&inputs, 0);
         }
     } else {
-        // the lane's own loads, a unit ahead
-        const int64_t msz = static_cast<int64_t>(dk) * dv;
-        const float* S = c.states + bh * c.Lmax * msz + col0;
-        auto fetch = [&](float (&f)[4][NT], int m, int kk) {
-#pragma unroll
-            for (int r = 0; r < 4; r++) {
-                const int row = kk * 16 + cc * 2 + kRow[r];
-                const float* from = S + slot_of[m] * msz + static_cast<int64_t>(row) * dv + colw;
-#pragma unroll
-                for (int v = 0; v < NT; v++) f[r][v] = row < dk && colw + v < wide ? __ldcs(from + v) : 0.f;
+        if (rounds > 0) fill(0, slot_of[0], 0);
+        for (int round = 0; round < rounds; round++) {
+            copies_done<0>();
+            __syncthreads();  // this round's rows are there, and the other stage's have been read
+            if (round + 1 < rounds) fill((round + 1) & 1, slot_of[(round + 1) / pieces], (round + 1) % pieces);
+            consume(round & 1, piece, [] {});
+            if (++piece == pieces) {
+                if (mine) weigh(m);
+                piece = 0;
+                m++;
             }
-        };
-        float f[4][NT], next[4][NT];
-        if (slots > 0 && share < ksteps) fetch(f, 0, share);
-        for (int m = 0; m < slots; m++) {
-            for (int kk = share; kk < ksteps; kk += KS) {
-                const bool more = kk + KS < ksteps;
-                if (more || m + 1 < slots) fetch(next, more ? m : m + 1, more ? kk + KS : share);
-                if (kk == share) multiply(f, kk, yes());
-                else multiply(f, kk, no());
-#pragma unroll
-                for (int r = 0; r < 4; r++)
-#pragma unroll
-                    for (int v = 0; v < NT; v++) f[r][v] = next[r][v];
-            }
-            if (share < ksteps) weigh(m);
         }
     }
     if (bad) return;
@@ -697,7 +718,7 @@ __global__ void __launch_bounds__(256, resident<T>(MT, NT))
             y[2 * v] = z.x;
             y[2 * v + 1] = z.y;
         }
-        if (kRing && x + 8 <= wide) {  // rows of multiples of four values at least
+        if (kTma && x + 8 <= wide) {  // rows of multiples of four values at least
             if constexpr (sizeof(T) == 4) {
                 *reinterpret_cast<float4*>(to) = make_float4(y[0], y[1], y[2], y[3]);
                 *reinterpret_cast<float4*>(to + 4) = make_float4(y[4], y[5], y[6], y[7]);
@@ -727,22 +748,22 @@ bool map_3d(CUtensorMap* m, const void* base, bool f32, int64_t z, int rows, int
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <typename T, int MT, int NG, int CW, int NT, int kStageRows>
+template <typename T, int MT, int NG, int CW, int NT, int kStageRows, int kMode>
 cudaError_t launch_tree(const TreeCall& c, int stages, cudaStream_t stream) {
     constexpr int kNb = 16 * MT * NG, kCols = 8 * CW * NT;
     const int64_t heads = static_cast<int64_t>(c.B) * c.H;
     Maps maps = {};
-    if (kStageRows > 0) {
+    if (kMode >= kStates) {
         if (!map_3d(&maps.states, c.states, true, heads * c.Lmax, c.dk, c.dv, 32, kStageRows, true)) return cudaErrorInvalidValue;
         const int keys = (c.N + 7) / 8 * 8;
-        if (Parts<T>::q == 1 &&
+        if (kMode == kAll &&
             (!map_3d(&maps.q, c.q, false, heads, c.N, c.dk, 64, kNb, true) ||
              !map_3d(&maps.k, c.k, false, heads, c.N, c.dk, 64, keys, true) ||
              !map_3d(&maps.v, c.v, false, heads, c.N, c.dv, kCols, keys, false)))
             return cudaErrorInvalidValue;
     }
-    const Layout s = layout<T>(kNb, c.N, c.dk, kCols, c.Lmax, kStageRows, stages, 8 / (CW * NG));
-    auto kern = decode_tree_kernel<T, MT, NG, CW, NT, kStageRows>;
+    const Layout s = layout<T>(kNb, c.N, c.dk, kCols, c.Lmax, kStageRows, stages, 8 / (CW * NG), kMode == kAll);
+    auto kern = decode_tree_kernel<T, MT, NG, CW, NT, kStageRows, kMode>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, s.total);
     if (e != cudaSuccess) return e;
     const dim3 grid(static_cast<unsigned>(heads * ((c.N - 1) / kNb + 1)), (c.dv - 1) / kCols + 1);
@@ -752,24 +773,33 @@ cudaError_t launch_tree(const TreeCall& c, int stages, cudaStream_t stream) {
 }
 
 // The ring: stages of a whole slot's columns, or of part of its rows, the largest of which two fit beside the other blocks of
-// an SM (one, where there is one slot); up to four of them.
-template <typename T, int MT, int NG, int CW, int NT>
+// an SM (one, where there is one slot); by TMA up to four of them.
+template <typename T, int MT, int NG, int CW, int NT, int kMode>
 cudaError_t pick_stage(const TreeCall& c, cudaStream_t stream) {
     constexpr int KS = 8 / (CW * NG), least = KS * 16 > 32 ? KS * 16 : 32;  // every warp has a unit of a stage
     constexpr int middle = least > 64 ? least : 64;
-    const bool tma = Parts<T>::q == 3 || (c.dk % 8 == 0 && c.dv % 8 == 0);  // rows of whole 16-byte pieces
-    const int64_t heads = static_cast<int64_t>(c.B) * c.H;
-    if (c.dv % 4 != 0 || !tma || heads * c.Lmax >= (int64_t(1) << 31)) return launch_tree<T, MT, NG, CW, NT, 0>(c, 0, stream);
+    if constexpr (kMode == kNone) return launch_tree<T, MT, NG, CW, NT, least, kMode>(c, 2, stream);
     auto fit = [&](int rows) {
-        const Layout s = layout<T>(16 * MT * NG, c.N, c.dk, 8 * CW * NT, c.Lmax, rows, 0, KS);
-        const int most = c.Lmax * ((c.dk - 1) / rows + 1), n = (room<T>(MT, NT) - (s.total - s.v) - s.ring) / s.stage;
-        return n < most ? (n < kMaxStages ? n : kMaxStages) : (most < kMaxStages ? most : kMaxStages);
+        const Layout s = layout<T>(16 * MT * NG, c.N, c.dk, 8 * CW * NT, c.Lmax, rows, 0, KS, kMode == kAll);
+        const int all = c.Lmax * ((c.dk - 1) / rows + 1), most = all < kMaxStages ? all : kMaxStages;
+        const int n = (room<T>(MT, NT) - (s.total - s.v) - s.ring) / s.stage;
+        return n < most ? n : most;
     };
     const int want = c.Lmax > 1 ? 2 : 1;
-    if ((c.dk > 64 || middle == 128) && fit(128) >= want) return launch_tree<T, MT, NG, CW, NT, 128>(c, fit(128), stream);
-    if ((c.dk > 32 || least == middle) && fit(middle) >= want) return launch_tree<T, MT, NG, CW, NT, middle>(c, fit(middle), stream);
+    if ((c.dk > 64 || middle == 128) && fit(128) >= want) return launch_tree<T, MT, NG, CW, NT, 128, kMode>(c, fit(128), stream);
+    if ((c.dk > 32 || least == middle) && fit(middle) >= want)
+        return launch_tree<T, MT, NG, CW, NT, middle, kMode>(c, fit(middle), stream);
     const int n = fit(least);
-    return launch_tree<T, MT, NG, CW, NT, least>(c, n < want ? want : n, stream);
+    return launch_tree<T, MT, NG, CW, NT, least, kMode>(c, n < want ? want : n, stream);
+}
+
+template <typename T, int MT, int NG, int CW, int NT>
+cudaError_t pick_copies(const TreeCall& c, cudaStream_t stream) {
+    if (c.dv % 4 != 0 || static_cast<int64_t>(c.B) * c.H * c.Lmax >= (int64_t(1) << 31))
+        return pick_stage<T, MT, NG, CW, NT, kNone>(c, stream);
+    if constexpr (Parts<T>::q == 1)  // fp32 queries and keys are cut on their way
+        if (c.dk % 8 == 0 && c.dv % 8 == 0) return pick_stage<T, MT, NG, CW, NT, kAll>(c, stream);
+    return pick_stage<T, MT, NG, CW, NT, kStates>(c, stream);
 }
 
 // ---- commit
@@ -934,13 +964,13 @@ cudaError_t decode_tree(int dtype, const TreeCall& c, cudaStream_t stream) {
     // 64 columns to a block, or 32 where that leaves SMs without one
     const bool wide = c.dv > 32 && static_cast<int64_t>(c.B) * c.H * ((c.dv - 1) / 64 + 1) > 76;
     if (dtype == 1) {
-        if (c.N <= 16) return wide ? pick_stage<float, 1, 1, 2, 4>(c, stream) : pick_stage<float, 1, 1, 1, 4>(c, stream);
-        return wide ? pick_stage<float, 1, 2, 2, 4>(c, stream) : pick_stage<float, 1, 2, 1, 4>(c, stream);
+        if (c.N <= 16) return wide ? pick_copies<float, 1, 1, 2, 4>(c, stream) : pick_copies<float, 1, 1, 1, 4>(c, stream);
+        return wide ? pick_copies<float, 1, 2, 2, 4>(c, stream) : pick_copies<float, 1, 2, 1, 4>(c, stream);
     }
     using T = __nv_bfloat16;
-    if (c.N <= 16) return wide ? pick_stage<T, 1, 1, 2, 4>(c, stream) : pick_stage<T, 1, 1, 1, 4>(c, stream);
-    if (c.N <= 32) return wide ? pick_stage<T, 2, 1, 2, 4>(c, stream) : pick_stage<T, 2, 1, 1, 4>(c, stream);
-    return wide ? pick_stage<T, 4, 1, 4, 2>(c, stream) : pick_stage<T, 4, 1, 2, 2>(c, stream);
+    if (c.N <= 16) return wide ? pick_copies<T, 1, 1, 2, 4>(c, stream) : pick_copies<T, 1, 1, 1, 4>(c, stream);
+    if (c.N <= 32) return wide ? pick_copies<T, 2, 1, 2, 4>(c, stream) : pick_copies<T, 2, 1, 1, 4>(c, stream);
+    return wide ? pick_copies<T, 4, 1, 4, 2>(c, stream) : pick_copies<T, 4, 1, 2, 2>(c, stream);
 }
 
 cudaError_t decode_commit(int dtype, const CommitCall& c, cudaStream_t stream) {
