@@ -709,11 +709,12 @@ def _want(t_, name, dtype, shape, device):
 def _gated_inputs(x, log_a, *like, dims, name="x"):
     """(device index, dtype code, gate's dtype code) of a gated call: x, log_a of one shape, the gate fp32 or of x's type."""
     torch = _torch()
-    _check(x, name)
+    if type(x) is not torch.Tensor or not (x.is_cuda and x.is_contiguous()):
+        _check(x, name)
     code = _dtype_code(x)
     if x.dim() != dims:
         raise ValueError(f"{name} must have {dims} dimensions, got {list(x.shape)}")
-    gate = torch.float32 if isinstance(log_a, torch.Tensor) and log_a.dtype == torch.float32 else x.dtype
+    gate = torch.float32 if isinstance(log_a, torch.Tensor) and log_a.dtype is torch.float32 else x.dtype
     index = x.get_device()
     if not _fits(log_a, gate, x.shape, index):
         _want(log_a, "log_a", gate, x.shape, x.device)
@@ -889,24 +890,18 @@ def gated_decode_commit(x, log_a, state, count, path=None, stream=None):
     return state
 
 
-def _nodes(k, v, log_a, gates, q=None):
-    """(B, H, N, dk, dv, device index) of a tree's or a commit's tokens: q, k [B,H,N,dk], v [B,H,N,dv] of one dtype,
-    log_a fp32 of the shape ``gates(B, H, N)``."""
-    torch = _torch()
-    _check(k, "k")
-    _check(v, "v", k.device)
-    if k.dim() != 4 or v.dim() != 4:
-        raise ValueError("k must be [B,H,N,dk] and v [B,H,N,dv]")
-    B, H, N, dk = k.shape
-    dv, index, dtype = v.shape[3], k.get_device(), k.dtype
-    if q is not None and not _fits(q, dtype, k.shape, index):
-        _want(q, "q", dtype, k.shape, k.device)
-    if v.dtype != dtype or v.shape != (B, H, N, dv):
-        _want(v, "v", dtype, (B, H, N, dv), k.device)
-    shape = gates(B, H, N)
-    if not _fits(log_a, torch.float32, shape, index):
-        _want(log_a, "log_a", torch.float32, shape, k.device)
-    return B, H, N, dk, dv, index
+def _nodes(names, tokens, log_a, gates):
+    """Says what is wrong with a tree's or a commit's tokens: q, k [B,H,N,dk], v [B,H,N,dv] of one dtype, log_a fp32."""
+    v = tokens[-1]
+    for n, t_ in zip(names, tokens):
+        _check(t_, n, v.device if isinstance(v, _torch().Tensor) and v.is_cuda else None)
+        if t_.dim() != 4:
+            raise ValueError(f"{n} must have 4 dimensions, got {list(t_.shape)}")
+    k = tokens[-2]
+    for n, t_ in zip(names, tokens):
+        _want(t_, n, k.dtype, tuple(k.shape[:3]) + (v.shape[3],) if n == "v" else k.shape, k.device)
+    shape = gates(*k.shape[:3])
+    _want(log_a, "log_a", _torch_module.float32, shape, k.device)
 
 
 def _one_gate(B, H, N):
@@ -915,6 +910,11 @@ def _one_gate(B, H, N):
 
 def _node_gates(B, H, N):
     return (B, H, N)
+
+
+def _places(where, written, *arrays):
+    """Small arrays at the library's alignment (see _small)."""
+    return [None if a is None else _small(a, where, written) for a in arrays]
 
 
 def decode_tree(q, k, v, log_a, lam, states, t, parent, out=None, stream=None):
@@ -926,25 +926,33 @@ def decode_tree(q, k, v, log_a, lam, states, t, parent, out=None, stream=None):
     batch) or [B,N] on the device: the node that a node goes on from, before it in the list, -1 for the last token of
     the states, -2 for no node (its row of ``out`` is left as it was; uninitialised in a new ``out``). Returns out
     [B,H,N,dv]."""
-    B, H, N, dk, dv, index = _nodes(k, v, log_a, _node_gates, q)
-    if stream is not None or index != _current_device():
-        return _elsewhere(q.device, stream, decode_tree, q, k, v, log_a, lam, states, t, parent, out)
-    torch = _torch_module
-    if states is None or states.dim() != 5:
+    torch = _torch()
+    if not (type(q) is type(k) is type(v) is type(log_a) is torch.Tensor and q.dim() == v.dim() == 4):
+        _nodes(("q", "k", "v"), (q, k, v), log_a, _node_gates)
+    B, H, N, dk = q.shape
+    dv, dtype, index = v.shape[3], q.dtype, q.get_device()
+    if type(states) is not torch.Tensor or states.dim() != 5:
         raise ValueError("states must be float32 [B,H,Lmax,dk,dv]")
     L = states.shape[2]
-    if not (_fits(states, torch.float32, (B, H, L, dk, dv), index) and _fits(lam, torch.float32, (B, H, N, L), index)
+    if not (index >= 0 and k.dtype is dtype and v.dtype is dtype and k.shape == q.shape and v.shape == (B, H, N, dv)
+            and log_a.dtype is torch.float32 and log_a.shape == (B, H, N) and q.is_contiguous() and k.is_contiguous()
+            and v.is_contiguous() and log_a.is_contiguous()
+            and k.get_device() == v.get_device() == log_a.get_device() == index
+            and _fits(states, torch.float32, (B, H, L, dk, dv), index) and _fits(lam, torch.float32, (B, H, N, L), index)
             and _fits(t, torch.int64, (B,), index)):
+        _nodes(("q", "k", "v"), (q, k, v), log_a, _node_gates)
         _want(states, "states", torch.float32, (B, H, L, dk, dv), q.device)
         _want(lam, "lambda", torch.float32, (B, H, N, L), q.device)
         _want(t, "t", torch.int64, (B,), q.device)
+    if stream is not None or index != _current_device():
+        return _elsewhere(q.device, stream, decode_tree, q, k, v, log_a, lam, states, t, parent, out)
     trees = _parent(parent, B, N, index, q.device)
     o = torch.empty_like(v) if out is None else _given(out, v)
-    where = "lla_decode_tree"
-    log_a, lam, t, parent = _small(log_a, where, o), _small(lam, where, o), _small(t, where, o), _small(parent, where, o)
+    if (log_a.data_ptr() | lam.data_ptr() | t.data_ptr() | parent.data_ptr()) & 15:
+        log_a, lam, t, parent = _places("lla_decode_tree", o, log_a, lam, t, parent)
     _call(load().lla_decode_tree(q.data_ptr(), k.data_ptr(), v.data_ptr(), log_a.data_ptr(), lam.data_ptr(),
                                  states.data_ptr(), t.data_ptr(), parent.data_ptr(), o.data_ptr(), _raw_stream(index), B,
-                                 trees, H, N, dk, dv, L, _dtype_code(q)), where)
+                                 trees, H, N, dk, dv, L, _dtype_code(q)), "lla_decode_tree")
     return o
 
 
@@ -955,57 +963,81 @@ def decode_commit(k, v, log_a, states, t, count, path=None, stream=None):
 
     ``count`` int32 [B]: accepted tokens of each sequence (0: left as it is); ``path`` int32 [B,M]: their nodes in order
     (entries past count are not read); without it tokens 0..count-1."""
-    B, H, N, dk, dv, index = _nodes(k, v, log_a, _node_gates)
-    if stream is not None or index != _current_device():
-        return _elsewhere(k.device, stream, decode_commit, k, v, log_a, states, t, count, path)
-    torch = _torch_module
-    if states is None or states.dim() != 5:
+    torch = _torch()
+    if not (type(k) is type(v) is type(log_a) is torch.Tensor and k.dim() == v.dim() == 4):
+        _nodes(("k", "v"), (k, v), log_a, _node_gates)
+    B, H, N, dk = k.shape
+    dv, dtype, index = v.shape[3], k.dtype, k.get_device()
+    if type(states) is not torch.Tensor or states.dim() != 5:
         raise ValueError("states must be float32 [B,H,Lmax,dk,dv]")
     L = states.shape[2]
-    if not (_fits(states, torch.float32, (B, H, L, dk, dv), index) and _fits(t, torch.int64, (B,), index)):
+    if not (index >= 0 and v.dtype is dtype and v.shape == (B, H, N, dv) and log_a.dtype is torch.float32
+            and log_a.shape == (B, H, N) and k.is_contiguous() and v.is_contiguous() and log_a.is_contiguous()
+            and v.get_device() == log_a.get_device() == index and _fits(states, torch.float32, (B, H, L, dk, dv), index)
+            and _fits(t, torch.int64, (B,), index)):
+        _nodes(("k", "v"), (k, v), log_a, _node_gates)
         _want(states, "states", torch.float32, (B, H, L, dk, dv), k.device)
         _want(t, "t", torch.int64, (B,), k.device)
+    if stream is not None or index != _current_device():
+        return _elsewhere(k.device, stream, decode_commit, k, v, log_a, states, t, count, path)
     M = _accepted(count, path, B, index, k.device)
-    where = "lla_decode_commit"
-    log_a, t, count = _small(log_a, where, states), _small(t, where, states), _small(count, where, states)
-    path = None if path is None else _small(path, where, states)
+    at = 0 if path is None else path.data_ptr()
+    if (log_a.data_ptr() | t.data_ptr() | count.data_ptr() | at) & 15:
+        log_a, t, count, path = _places("lla_decode_commit", states, log_a, t, count, path)
     _call(load().lla_decode_commit(k.data_ptr(), v.data_ptr(), log_a.data_ptr(), states.data_ptr(), t.data_ptr(),
                                    count.data_ptr(), None if path is None else path.data_ptr(), _raw_stream(index), B, H,
-                                   N, M, dk, dv, L, _dtype_code(k)), where)
+                                   N, M, dk, dv, L, _dtype_code(k)), "lla_decode_commit")
     return states
 
 
 def linear_decode_tree(q, k, v, log_a, state, parent, out=None, stream=None):
     """Outputs of a tree of drafted tokens over the state of linear_decode_step, lla_linear_decode_tree (see
     decode_tree). log_a [H] fp32; ``state`` [B,H,dk,dv] fp32 is read. Returns out [B,H,N,dv]."""
-    B, H, N, dk, dv, index = _nodes(k, v, log_a, _one_gate, q)
+    torch = _torch()
+    if not (type(q) is type(k) is type(v) is type(log_a) is torch.Tensor and q.dim() == v.dim() == 4):
+        _nodes(("q", "k", "v"), (q, k, v), log_a, _one_gate)
+    B, H, N, dk = q.shape
+    dv, dtype, index = v.shape[3], q.dtype, q.get_device()
+    if not (index >= 0 and k.dtype is dtype and v.dtype is dtype and k.shape == q.shape and v.shape == (B, H, N, dv)
+            and log_a.dtype is torch.float32 and log_a.shape == (H,) and q.is_contiguous() and k.is_contiguous()
+            and v.is_contiguous() and log_a.is_contiguous()
+            and k.get_device() == v.get_device() == log_a.get_device() == index
+            and _fits(state, torch.float32, (B, H, dk, dv), index)):
+        _nodes(("q", "k", "v"), (q, k, v), log_a, _one_gate)
+        _want(state, "state", torch.float32, (B, H, dk, dv), q.device)
     if stream is not None or index != _current_device():
         return _elsewhere(q.device, stream, linear_decode_tree, q, k, v, log_a, state, parent, out)
-    if not _fits(state, _torch_module.float32, (B, H, dk, dv), index):
-        _want(state, "state", _torch_module.float32, (B, H, dk, dv), q.device)
     trees = _parent(parent, B, N, index, q.device)
-    o = _torch_module.empty_like(v) if out is None else _given(out, v)
-    where = "lla_linear_decode_tree"
-    log_a, parent = _small(log_a, where, o), _small(parent, where, o)
+    o = torch.empty_like(v) if out is None else _given(out, v)
+    if (log_a.data_ptr() | parent.data_ptr()) & 15:
+        log_a, parent = _places("lla_linear_decode_tree", o, log_a, parent)
     _call(load().lla_linear_decode_tree(q.data_ptr(), k.data_ptr(), v.data_ptr(), log_a.data_ptr(), state.data_ptr(),
                                         parent.data_ptr(), o.data_ptr(), _raw_stream(index), B, trees, H, N, dk, dv,
-                                        _dtype_code(q)), where)
+                                        _dtype_code(q)), "lla_linear_decode_tree")
     return o
 
 
 def linear_decode_commit(k, v, log_a, state, count, path=None, stream=None):
     """Accepted tokens into the state of linear_decode_step, lla_linear_decode_commit (see decode_commit). log_a [H]
     fp32; ``state`` [B,H,dk,dv] fp32 is updated in place and returned."""
-    B, H, N, dk, dv, index = _nodes(k, v, log_a, _one_gate)
+    torch = _torch()
+    if not (type(k) is type(v) is type(log_a) is torch.Tensor and k.dim() == v.dim() == 4):
+        _nodes(("k", "v"), (k, v), log_a, _one_gate)
+    B, H, N, dk = k.shape
+    dv, dtype, index = v.shape[3], k.dtype, k.get_device()
+    if not (index >= 0 and v.dtype is dtype and v.shape == (B, H, N, dv) and log_a.dtype is torch.float32
+            and log_a.shape == (H,) and k.is_contiguous() and v.is_contiguous() and log_a.is_contiguous()
+            and v.get_device() == log_a.get_device() == index and _fits(state, torch.float32, (B, H, dk, dv), index)):
+        _nodes(("k", "v"), (k, v), log_a, _one_gate)
+        _want(state, "state", torch.float32, (B, H, dk, dv), k.device)
     if stream is not None or index != _current_device():
         return _elsewhere(k.device, stream, linear_decode_commit, k, v, log_a, state, count, path)
-    if not _fits(state, _torch_module.float32, (B, H, dk, dv), index):
-        _want(state, "state", _torch_module.float32, (B, H, dk, dv), k.device)
     M = _accepted(count, path, B, index, k.device)
-    where = "lla_linear_decode_commit"
-    log_a, count = _small(log_a, where, state), _small(count, where, state)
-    path = None if path is None else _small(path, where, state)
+    at = 0 if path is None else path.data_ptr()
+    if (log_a.data_ptr() | count.data_ptr() | at) & 15:
+        log_a, count, path = _places("lla_linear_decode_commit", state, log_a, count, path)
     _call(load().lla_linear_decode_commit(k.data_ptr(), v.data_ptr(), log_a.data_ptr(), state.data_ptr(),
                                           count.data_ptr(), None if path is None else path.data_ptr(),
-                                          _raw_stream(index), B, H, N, M, dk, dv, _dtype_code(k)), where)
+                                          _raw_stream(index), B, H, N, M, dk, dv, _dtype_code(k)),
+          "lla_linear_decode_commit")
     return state

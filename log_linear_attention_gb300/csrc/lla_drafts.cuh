@@ -2,6 +2,8 @@
 // drafted tokens over recurrent states (lla_tree.cu).
 #pragma once
 
+#include <atomic>
+
 #include "lla_internal.cuh"
 
 namespace lla {
@@ -55,16 +57,17 @@ struct CommitCall {
 cudaError_t decode_commit(int dtype, const CommitCall& c, cudaStream_t stream);
 
 namespace {
-// Whether a tree's parents are as they should be, by every thread of the block together: par[i] (shared memory) < i, not
-// below -2, and not a place without a node.
-__device__ __forceinline__ bool tree_is_bad(const int* par, int N) {
-    bool bad = false;
-    for (int i = threadIdx.x; i < N; i += blockDim.x) {
-        const int p = par[i];
-        if (p >= i || p < -2) bad = true;
-        else if (p >= 0 && par[p] == -2) bad = true;
-    }
-    return __syncthreads_or(bad);
+// Allows the kernel `bytes` of dynamic shared memory on the current device, once for each (asking costs about a microsecond).
+template <typename Kernel>
+cudaError_t allow_shared(Kernel* kern, int bytes, std::atomic<uint64_t>& done) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = uint64_t(1) << (dev & 63);
+    if (dev < 64 && (done.load(std::memory_order_relaxed) & bit)) return cudaSuccess;
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess && dev < 64) done.fetch_or(bit, std::memory_order_relaxed);
+    return e;
 }
 }  // namespace
 

@@ -675,7 +675,8 @@ cudaError_t launch_scan(Args& a, cudaStream_t stream) {
     }
     const int64_t walks = static_cast<int64_t>(a.cols) * a.spans;
     const int smem = kPath == kTma ? C::stage_bytes * (pieces <= a.cluster ? 1 : C::kStages) : 0;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    static std::atomic<uint64_t> allowed{0};
+    cudaError_t e = smem > 0 ? allow_shared(kern, C::stage_bytes * C::kStages, allowed) : cudaSuccess;
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(a.cluster * walks));
@@ -745,6 +746,18 @@ __global__ void __launch_bounds__(kThreads) gated_step(const T* __restrict__ x, 
 // ---- trees: a thread per channel walks the nodes in order; parents come before their children, whose states it keeps in
 // shared memory.
 constexpr int kTreeThreads = 64;
+
+// Whether a tree's parents are not as they should be, by every thread of the block together: par[i] (shared memory) < i, not
+// below -2, and not a place without a node.
+__device__ __forceinline__ bool tree_is_bad(const int* par, int N) {
+    bool bad = false;
+    for (int i = threadIdx.x; i < N; i += blockDim.x) {
+        const int p = par[i];
+        if (p >= i || p < -2) bad = true;
+        else if (p >= 0 && par[p] == -2) bad = true;
+    }
+    return __syncthreads_or(bad);
+}
 
 template <typename T, typename G>
 __global__ void __launch_bounds__(kTreeThreads) gated_tree(const T* __restrict__ x, const G* __restrict__ log_a,

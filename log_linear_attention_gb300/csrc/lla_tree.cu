@@ -26,6 +26,7 @@ namespace {
 
 constexpr int kSlots = 40;
 constexpr int kMaxStages = 4;
+constexpr int kMostShared = 220 * 1024;  // dynamic; static and reserved shared memory fit beside it in the SM's 228 KB
 
 // bf16 halves of two floats, the first in the low half
 __device__ __forceinline__ uint32_t pack(float lo, float hi) {
@@ -764,8 +765,10 @@ cudaError_t launch_tree(const TreeCall& c, int stages, cudaStream_t stream) {
     }
     const Layout s = layout<T>(kNb, c.N, c.dk, kCols, c.Lmax, kStageRows, stages, 8 / (CW * NG), kMode == kAll);
     auto kern = decode_tree_kernel<T, MT, NG, CW, NT, kStageRows, kMode>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, s.total);
+    static std::atomic<uint64_t> allowed{0};
+    cudaError_t e = allow_shared(kern, kMostShared, allowed);
     if (e != cudaSuccess) return e;
+    if (s.total > kMostShared) return cudaErrorInvalidValue;
     const dim3 grid(static_cast<unsigned>(heads * ((c.N - 1) / kNb + 1)), (c.dv - 1) / kCols + 1);
     kern<<<grid, 256, s.total, stream>>>(c, maps, stages);
     note_launch(stream, "decode_tree");
@@ -817,7 +820,7 @@ template <typename T, int kW, int kU>  // kW columns of a thread, kU of its elem
 __global__ void __launch_bounds__(kThreads) decode_commit_kernel(const CommitCall c, int share) {
     extern __shared__ float tok[];  // [n][dk] weighted keys, [n][dv] values
     __shared__ int node[kMaxTree], first[kSlots + 1];
-    __shared__ float w[kMaxTree];
+    __shared__ float w[kMaxTree], la[kMaxTree];
     __shared__ unsigned long long from[kSlots];
     __shared__ float whole_s;
     const int tid = threadIdx.x, dk = c.dk, dv = c.dv;
@@ -839,18 +842,19 @@ __global__ void __launch_bounds__(kThreads) decode_commit_kernel(const CommitCal
         return;
     }
     if (n == 0) return;
-    if (tid == 0) {
-        if (linear) {
-            const float g = c.log_a[h];
-            for (int i = 0; i < n; i++) w[i] = i == n - 1 ? 1.f : expf(g * static_cast<float>(n - 1 - i));
-            whole_s = expf(g * static_cast<float>(n));
-        } else {
+    // weights: what the tokens after one make of it; of the old slots (thread n): what all make of them
+    if (linear) {
+        const float g = c.log_a[h];
+        if (tid < n) w[tid] = tid == n - 1 ? 1.f : expf(g * static_cast<float>(n - 1 - tid));
+        if (tid == n) whole_s = expf(g * static_cast<float>(n));
+    } else {
+        if (tid < n) la[tid] = c.log_a[bh * c.N + node[tid]];
+        __syncthreads();
+        if (tid <= n) {
+            const int stop = tid < n ? tid : -1;
             float D = 0.f;
-            for (int i = n - 1; i >= 0; i--) {
-                w[i] = expf(D);
-                D += c.log_a[bh * c.N + node[i]];
-            }
-            whole_s = expf(D);
+            for (int i = n - 1; i > stop; i--) D += la[i];
+            (tid < n ? w[tid] : whole_s) = expf(D);
         }
     }
     // old slots that go into slot l, and its first token (tokens of slot l: first[l] .. the first of the next lower held one)
@@ -944,18 +948,21 @@ cudaError_t launch_commit(const CommitCall& c, cudaStream_t stream) {
     const size_t smem = static_cast<size_t>(c.M) * (c.dk + c.dv) * sizeof(float);
     const int64_t heads = static_cast<int64_t>(c.B) * c.H;
     const int width = c.dv % 4 == 0 ? 4 : 1, items = c.dk * (c.dv / width), most = (items - 1) / kThreads + 1;
+    // Blocks for a few waves (64 x 16 heads of 128 x 64: 97 us as one block a head, 94 as two, 108 as four, which leave a
+    // thread fewer rows in flight).
     int parts = 1;
-    while (parts < most && heads * parts < 600) parts *= 2;
+    while (parts < most && heads * parts < 2000) parts *= 2;
     const int share = (items - 1) / parts + 1;
-    auto go = [&](auto kern) {
-        cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    auto go = [&](auto kern, std::atomic<uint64_t>& allowed) {
+        cudaError_t e = smem > 48 * 1024 ? allow_shared(kern, kMaxTree * 256 * 4, allowed) : cudaSuccess;
         if (e != cudaSuccess) return e;
         kern<<<dim3(static_cast<unsigned>(heads), parts), kThreads, smem, stream>>>(c, share);
         note_launch(stream, "decode_commit");
         return cudaGetLastError();
     };
-    if (width == 1) return go(decode_commit_kernel<T, 1, 4>);
-    return share > kThreads ? go(decode_commit_kernel<T, 4, 4>) : go(decode_commit_kernel<T, 4, 1>);
+    static std::atomic<uint64_t> allowed[3];
+    if (width == 1) return go(decode_commit_kernel<T, 1, 4>, allowed[0]);
+    return share > kThreads ? go(decode_commit_kernel<T, 4, 4>, allowed[1]) : go(decode_commit_kernel<T, 4, 1>, allowed[2]);
 }
 
 }  // namespace
