@@ -396,55 +396,51 @@ __global__ void __launch_bounds__(256, resident<T>(MT, NT))
                 ldmatrix4(z[w], smem_u32(ks) + (w * N + j) * rb + kk * 32 + (lane >> 3) * 16);
         }
     };
-    // scores: units of `many` 16 x 8 pieces side by side
-    const int mts = (live + 15) / 16, nts = (N + 7) / 8;
-    const int many = mts * nts > 8 ? 4 : mts * nts > 4 ? 2 : 1, groups = (nts + many - 1) / many;
-    auto score = [&](float (&d)[4][4], int u) {
-        const int mt = u % mts, nt0 = u / mts * many;
+    // scores: units of kMany 16 x 8 pieces side by side (those behind the last key are not kept)
+    constexpr int kMany = kNb / 16;
+    const int mts = (live + 15) / 16, nts = (N + 7) / 8, groups = (nts + kMany - 1) / kMany;
+    auto score = [&](float (&d)[kMany][4], int u) {
+        const int mt = u % mts, nt0 = u / mts * kMany;
 #pragma unroll
-        for (int y = 0; y < 4; y++)
+        for (int y = 0; y < kMany; y++)
 #pragma unroll
             for (int r = 0; r < 4; r++) d[y][r] = 0.f;
         for (int kk = 0; kk < ksteps; kk += 2) {
-            uint32_t a[kQ][4], a1[kQ][4];
-            load_q(a, mt * 16, kk);
-            if (kk + 1 < ksteps) load_q(a1, mt * 16, kk + 1);
+            uint32_t a[2][kQ][4], z[kMany][kQ][4];
+            const bool two = kk + 1 < ksteps;
+            load_q(a[0], mt * 16, kk);
+            if (two) load_q(a[1], mt * 16, kk + 1);
 #pragma unroll
-            for (int y = 0; y < 4; y++) {
-                if (y >= many || nt0 + y >= nts) break;
-                uint32_t z[kQ][4], b0[kQ], b1[kQ];
-                load_k(z, (nt0 + y) * 8, kk);
+            for (int y = 0; y < kMany; y++) load_k(z[y], (nt0 + y) * 8, kk);
 #pragma unroll
-                for (int w = 0; w < kQ; w++) {
-                    b0[w] = z[w][0];
-                    b1[w] = z[w][1];
+            for (int half = 0; half < 2; half++) {
+                if (half == 1 && !two) break;
+#pragma unroll
+                for (int y = 0; y < kMany; y++) {
+                    uint32_t b0[kQ], b1[kQ];
+#pragma unroll
+                    for (int w = 0; w < kQ; w++) {
+                        b0[w] = z[y][w][half * 2];
+                        b1[w] = z[y][w][half * 2 + 1];
+                    }
+                    mma_parts<false>(d[y], a[half], b0, b1);
                 }
-                mma_parts<false>(d[y], a, b0, b1);
-                if (kk + 1 == ksteps) continue;
-#pragma unroll
-                for (int w = 0; w < kQ; w++) {
-                    b0[w] = z[w][2];
-                    b1[w] = z[w][3];
-                }
-                mma_parts<false>(d[y], a1, b0, b1);
             }
         }
     };
-    auto onto_weights = [&](const float (&d)[4][4], int u) {
-        const int mt = u % mts, nt0 = u / mts * many;
+    auto onto_weights = [&](const float (&d)[kMany][4], int u) {
+        const int mt = u % mts, nt0 = u / mts * kMany;
 #pragma unroll
-        for (int y = 0; y < 4; y++) {
-            if (y >= many) break;
+        for (int y = 0; y < kMany; y++)
 #pragma unroll
             for (int r = 0; r < 4; r++) {
                 const int i = mt * 16 + g + (r >> 1) * 8, x = (nt0 + y) * 8 + cc * 2 + (r & 1);
                 if (x < N) P[i * (N + 1) + x] *= d[y][r];
             }
-        }
     };
 
     bool bad = t < 0, in_time = true;
-    float held_scores[2][4][4];
+    float held_scores[2][kMany][4];
     const int scorer = warp - kWalkers / 32;
     if (tid < kWalkers) {
         // Depths, sums of log decays and the nodes above each node, by jumps that double in length: log2 of the depth
@@ -699,7 +695,7 @@ __global__ void __launch_bounds__(256, resident<T>(MT, NT))
             for (int v = 0; v < 4; v++) o[v] = sh == 0 ? add[v] : add2(o[v], add[v]);
         }
         const int d = link[i0 + i].steps;
-#pragma unroll 2
+#pragma unroll 4
         for (int n = 0; n <= d; n++) {
             const int j = up[i * N + n];
             const float p = P[i * (N + 1) + j];
