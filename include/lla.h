@@ -418,7 +418,8 @@ int lla_decode_step_shared(const void* q, const void* k, const void* v, const fl
  *   x, out    [B,T,D]   dtype       any T, D >= 1. Layers with heads: [B,H,T,d] is [B H,T,d], and
  *                                   [B,T,H,d] is [B,T,H d]; to the recurrence all channels are alike.
  *   log_a     [B,T,D]   gate_dtype  log of the gate (<= 0 expected; -inf, a gate of 0, is valid; positive
- *                                   values are computed as given). gate_dtype: LLA_F32, or dtype.
+ *                                   values are computed as given, but where the product of some rows'
+ *                                   gates overflows fp32 a NaN may come out). gate_dtype: LLA_F32, or dtype.
  *   state0    [B0,D]    fp32        h_{-1}: B0 = 0 (state0 NULL: zeros), 1 (one for the whole batch) or B.
  *   state_out [B,D]     fp32        written: h_{T-1} before its rounding to dtype. NULL: not wanted.
  * The recurrence is computed in fp32, sums in a fixed order: repeated calls give identical bits. Channels
@@ -443,7 +444,7 @@ int lla_decode_step_shared(const void* q, const void* k, const void* v, const fl
  * lla_gated_decode_step: one token of every sequence; x, log_a, out [B,D], state [B,D] fp32 read and written
  *   in place (h_{t-1} on entry, h_t on return; what the prompt left in state_out).
  *
- * Limits: rows x D up to 2^40; T (packed: total_T) up to 2^31 - 2^16. Workspace: only for dstate0 with B0 = 1
+ * Limits: rows x D up to 2^40, D up to 2^30; T (packed: total_T) up to 2^31 - 2^16. Workspace: only for dstate0 with B0 = 1
  * (B D floats, the library's pool). A bounded wait that runs out is reported by lla_device_error as
  * LLA_ERR_TIMEOUT. Fastest where rows of x and log_a are multiples of 16 bytes (copied by TMA); then where D is
  * a multiple of 4.
@@ -491,7 +492,7 @@ int lla_gated_decode_step(const void* x, const void* log_a, float* state, void* 
  *   state [B,H,dk,dv] fp32.
  *   dk, dv 1..128; Lmax 1..40. Products with the states run on tensor cores: bf16 queries as they are, states
  *   in two bf16 parts (2^-16 of each element), fp32 calls in three parts of both; sums in fp32 in a fixed order
- *   (repeated calls give identical bits). An infinity in the states may come out as NaN; one in a node reaches
+ *   (repeated calls give identical bits; a call of fewer heads may cut its sums otherwise). An infinity in the states may come out as NaN; one in a node reaches
  *   only that node's and its descendants' outputs.
  * lla_gated_decode_tree, lla_gated_decode_commit: the same for lla_gated_decode_step; x, log_a, out [B,N,D],
  *   state [B,D] fp32; B up to 65535. (h of a node: exp(log_a_i) h_parent(i) + x_i.)

@@ -994,7 +994,7 @@ int validate_gated(int dtype, int gate_dtype, int64_t rows, int D) {
     if (dtype != LLA_BF16 && dtype != LLA_F32) return LLA_ERR_INVALID_ARG;
     if (gate_dtype != LLA_F32 && gate_dtype != dtype) return LLA_ERR_INVALID_ARG;
     if (rows < 1 || D < 1) return LLA_ERR_INVALID_ARG;
-    if (rows > ((int64_t)1 << 40) / D) return LLA_ERR_UNSUPPORTED;
+    if (rows > ((int64_t)1 << 40) / D || D > (1 << 30)) return LLA_ERR_UNSUPPORTED;
     return LLA_OK;
 }
 
@@ -1048,7 +1048,7 @@ int tree_call(lla::TreeCall c, bool linear, void* stream, int dtype) {
     if (c.B < 1 || c.H < 1 || c.N < 1 || c.dk < 1 || c.dv < 1 || c.Lmax < 1 || c.Lmax > 40) return LLA_ERR_INVALID_ARG;
     if (c.BP != 1 && c.BP != c.B) return LLA_ERR_INVALID_ARG;
     if (c.N > lla::kMaxTree || c.dk > 128 || c.dv > 128) return LLA_ERR_UNSUPPORTED;
-    if ((int64_t)c.B * c.H > 0x7fffffff) return LLA_ERR_UNSUPPORTED;
+    if ((int64_t)c.B * c.H > 0x7fffffff / 8) return LLA_ERR_UNSUPPORTED;  // up to 8 blocks a head
     const size_t heads = (size_t)c.B * c.H, row = heads * c.N * type_bytes(dtype), f = sizeof(float);
     if (clash({{c.out, row * c.dv}},
               {{c.q, row * c.dk}, {c.k, row * c.dk}, {c.v, row * c.dv}, {c.log_a, (linear ? c.H : heads * c.N) * f},

@@ -439,7 +439,8 @@ __global__ void __launch_bounds__(256, resident<T>(MT, NT))
             }
     };
 
-    bool bad = t < 0, in_time = true;
+    const int64_t limit = linear ? 2 : int64_t(1) << (c.Lmax - 1);  // of positions
+    bool bad = t < 0 || t >= limit, in_time = true;
     float held_scores[2][kMany][4];
     const int scorer = warp - kWalkers / 32;
     if (tid < kWalkers) {
@@ -477,14 +478,14 @@ __global__ void __launch_bounds__(256, resident<T>(MT, NT))
             }
             if (!walkers_any(me.jump >= 0)) break;
         }
-        if (!linear && tid < N && t + me.steps >= (int64_t(1) << (c.Lmax - 1))) bad = true;
+        if (!linear && tid < N && t < limit && t + me.steps >= limit) bad = true;
         link[tid] = me;
         above[tid] = mask;
         walkers_meet();
         // weights: kEach threads to a node, each with every so many of the nodes above it and of the held slots
         constexpr int kEach = kWalkers / kNb;
         const int i = tid % kNb, first = tid / kNb, node = i0 + i;
-        if (i < live && par[node] != -2 && (linear || (t >= 0 && t < (int64_t(1) << (c.Lmax - 1))))) {
+        if (i < live && par[node] != -2 && t >= 0 && t < limit) {
             const float lg = linear ? c.log_a[h] : 0.f;
             const Link at = link[node];
             const uint4 line = above[node];
@@ -826,7 +827,7 @@ __global__ void __launch_bounds__(kThreads) decode_commit_kernel(const CommitCal
     const int64_t t = linear ? 0 : c.t[b];
     const int n = c.count[b];
     const int64_t e = t + n - 1;
-    bool bad = n < 0 || n > c.M || t < 0 || (!linear && e >= (int64_t(1) << (c.Lmax - 1)));
+    bool bad = n < 0 || n > c.M || t < 0 || (!linear && t > (int64_t(1) << (c.Lmax - 1)) - n);
     if (!bad)
         for (int i = tid; i < n; i += kThreads) {
             const int at = c.path ? c.path[static_cast<int64_t>(b) * c.M + i] : i;

@@ -30,6 +30,7 @@ def lib():
     (dict(B=0), BAD), (dict(T=0), BAD), (dict(D=0), BAD), (dict(dtype=2), BAD), (dict(gate=2), BAD),
     (dict(dtype=1, gate=0), BAD),                        # 16-bit gates of fp32 inputs
     (dict(B=2 ** 20, T=2 ** 20, D=2), UNS), (dict(T=2 ** 31 - 1), UNS), (dict(B=2 ** 28, T=1), UNS),
+    (dict(B=1, T=1, D=2 ** 30 + 1), UNS),
 ])
 def test_gated_forward_refuses(lib, over, expect):
     a = dict(x=A, log_a=A, state0=None, out=Z, state_out=None, B=3, B0=0, T=5, D=16, dtype=0, gate=1)

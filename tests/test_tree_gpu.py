@@ -214,6 +214,24 @@ def test_bad_sequences_are_skipped(lla):
         assert torch.equal(one[b], was[b]) == (b in (2, 5, 6, 7, 8)), b
 
 
+def test_positions_that_overflow_are_refused(lla):
+    B, H, N, d, Lmax = 3, 1, 2, 16, 40
+    q, k, v = torch.randn(3, B, H, N, d, device="cuda").unbind()
+    la, lam = -torch.rand(B, H, N, device="cuda"), torch.rand(B, H, N, Lmax, device="cuda")
+    states, out = torch.randn(B, H, Lmax, d, d, device="cuda"), torch.full((B, H, N, d), 7.0, device="cuda")
+    t = ints([2 ** 63 - 1, -2 ** 63, 2 ** 39], torch.int64)
+    lla.decode_tree(q.contiguous(), k.contiguous(), v.contiguous(), la, lam, states, t, ints([-1, 0]), out=out)
+    assert lla.device_error() == lla.LLA_ERR_DEVICE and bool((out == 7).all())
+    was = states.clone()
+    lla.decode_commit(k.contiguous(), v.contiguous(), la, states, t, ints([2, 2, 1]))
+    assert lla.device_error() == lla.LLA_ERR_DEVICE and torch.equal(states, was)
+    # the last position that there is
+    t = ints([2 ** 39 - 1] * B, torch.int64)
+    lla.decode_commit(k.contiguous(), v.contiguous(), la, states, t, ints([2, 1, 0]))
+    assert lla.device_error() == lla.LLA_ERR_DEVICE
+    assert [torch.equal(states[b], was[b]) for b in range(B)] == [True, False, True]
+
+
 def test_values_that_are_not_finite_stay_on_their_branch(lla):
     B, H, N, dk, dv, Lmax = 1, 2, 20, 64, 48, 9
     r = np.random.default_rng(8)
