@@ -188,6 +188,92 @@ def test_packed(lla, lens, lead, tail, D, dtype, gt):
             R.gated_check(np64(dsg[0]), sum_s, sum_size, "f32", "dstate0 of all", factors=0)
 
 
+@pytest.mark.parametrize("dtype,gt", TYPES)
+@pytest.mark.parametrize("B,T,D", [(4, 1100, 96), (40, 1100, 64), (3, 530, 24), (160, 140, 72), (1, 9000, 32)])
+def test_every_cut_of_the_channels(lla, B, T, D, dtype, gt):
+    """Columns of 64, 32 and 16 channels, clusters of one to eight blocks, several steps, rows of whole 16-byte pieces."""
+    r = np.random.default_rng(B + T + D)
+    (x, xt), (a, at), (do, dot) = normal(r, (B, T, D), dtype), gate(r, (B, T, D), gt), normal(r, (B, T, D), dtype)
+    (s0, s0t), (ds, dst) = normal(r, (B, D), "f32"), normal(r, (B, D), "f32")
+    end = torch.empty(B, D, device="cuda")
+    out = lla.gated_forward(xt, at, state0=s0t, state_out=end)
+    dx, da, dsg = lla.gated_backward(at, xt, dot, state0=s0t, dstate_out=dst)
+    # all sequences at once, row by row
+    e, h, g, w = np.exp(a), s0.copy(), ds.copy(), np.abs(ds)
+    sizes, k = np.abs(s0), np.abs(s0)
+    want, size = np.empty_like(x), np.empty_like(x)
+    for t in range(T):
+        h = e[:, t] * h + x[:, t]
+        sizes = e[:, t] * sizes + np.abs(x[:, t])
+        k = e[:, t] * k + sizes
+        want[:, t], size[:, t] = h, k
+    R.gated_check(np64(out), want, size, dtype, "out")
+    R.gated_check(np64(end), h, k, "f32", "state")
+    rx, ra, back = np.empty_like(x), np.empty_like(x), np.empty_like(x)
+    k = w.copy()
+    for t in reversed(range(T)):
+        g = g + do[:, t]
+        w = w + np.abs(do[:, t])
+        k = k + w
+        rx[:, t], back[:, t] = g, k
+        ra[:, t] = g * e[:, t] * (x[:, t - 1] if t else s0)
+        g, w, k = g * e[:, t], w * e[:, t], k * e[:, t]
+    R.gated_check(np64(dx), rx, back, dtype, "dx")
+    before = np.abs(np.concatenate([s0[:, None], x[:, :-1]], 1))
+    R.gated_check(np64(da), ra, back * e * before, gt, "dlog_a", factors=3)
+    R.gated_check(np64(dsg), g, k, "f32", "dstate0")
+
+
+@pytest.mark.parametrize("D", [8, 40, 264])
+@pytest.mark.parametrize("lens,lead,tail", PACKS + [([700, 0, 1, 900, 33, 0, 0, 5] * 3, 3, 2)])
+def test_packed_rows_of_16_bytes(lla, lens, lead, tail, D):
+    """Packed rows that come by TMA, in bf16 with gates of both types."""
+    for gt in ("f32", "bf16"):
+        r = np.random.default_rng(sum(lens) + D)
+        n, total = len(lens), max(1, lead + sum(lens) + tail)
+        at_ = np.concatenate([[lead], lead + np.cumsum(lens)])
+        cu = torch.from_numpy(at_.astype(np.int32)).cuda()
+        (x, xt), (a, at), (do, dot) = normal(r, (total, D), "bf16"), gate(r, (total, D), gt), normal(r, (total, D), "bf16")
+        (s0, s0t), (ds, dst) = normal(r, (n, D), "f32"), normal(r, (n, D), "f32")
+        end, out = torch.full((n, D), float("nan"), device="cuda"), torch.full((total, D), 7.0, device="cuda").bfloat16()
+        lla.gated_forward_varlen(xt, at, cu, state0=s0t, state_out=end, out=out)
+        dx, da, dsg = lla.gated_backward_varlen(at, xt, dot, cu, state0=s0t, dstate_out=dst)
+        for b in range(n):
+            w = slice(int(at_[b]), int(at_[b + 1]))
+            s, d = s0[b], ds[b]
+            if lens[b] == 0:
+                assert np.array_equal(np64(end[b]), s) and np.array_equal(np64(dsg[b]), d)
+                continue
+            ref, last = one(x[w], a[w], s)
+            size, end_size = R.gated_size(x[w], a[w], s)
+            R.gated_check(np64(out[w]), ref, size, "bf16", ("out", b))
+            R.gated_check(np64(end[b]), last, end_size, "f32", ("state", b))
+            rx, ra, rs = one_back(a[w], x[w], do[w], s, d)
+            size, s_size = back_size(a[w], do[w], d)
+            R.gated_check(np64(dx[w]), rx, size, "bf16", ("dx", b))
+            before = np.abs(np.concatenate([s[None], x[w][:-1]]))
+            R.gated_check(np64(da[w]), ra, size * np.exp(a[w]) * before, gt, ("dlog_a", b), factors=3)
+            R.gated_check(np64(dsg[b]), rs, s_size, "f32", ("dstate0", b))
+
+
+def test_two_streams_at_once(lla):
+    """Calls side by side on two streams, of clusters that fill the GPU together: as alone."""
+    x = torch.randn(4, 4096, 512, device="cuda").bfloat16()
+    a = -torch.rand(4, 4096, 512, device="cuda")
+    s0 = torch.randn(1, 512, device="cuda")
+    want = lla.gated_forward(x, a, state0=s0)
+    grads = lla.gated_backward(a, want, x, state0=s0)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream(priority=-1)]
+    got = []
+    for i in range(6):
+        s = streams[i % 2]
+        got.append((lla.gated_forward(x, a, state0=s0, stream=s), lla.gated_backward(a, want, x, state0=s0, stream=s)))
+    torch.cuda.synchronize()
+    for out, g in got:
+        assert torch.equal(out, want) and all(torch.equal(p, q) for p, q in zip(g, grads))
+
+
 def test_values_that_are_not_finite_stay_where_they_belong(lla):
     T, D = 700, 8
     r = np.random.default_rng(1)

@@ -317,6 +317,40 @@ def test_graphs_streams_and_given_outputs(lla):
         lla.decode_tree(*args, out=g["v"])
 
 
+def test_two_streams_at_once(lla):
+    B, H, N, dk, dv, Lmax = 32, 8, 30, 128, 64, 14
+    r = np.random.default_rng(13)
+    d = draft(r, B, H, N, dk, dv, "bf16", Lmax, [int(x) for x in r.integers(0, 8000, B)])
+    g = {n: x[1] for n, x in d.items()}
+    args = [g[n] for n in ("q", "k", "v", "log_a", "lam", "states", "t", "parent")]
+    want = lla.decode_tree(*args, out=torch.zeros_like(g["v"]))
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream(priority=-1)]
+    outs = [torch.zeros_like(g["v"]) for _ in range(6)]
+    torch.cuda.synchronize()
+    for i, o in enumerate(outs):
+        lla.decode_tree(*args, out=o, stream=streams[i % 2])
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, want) for o in outs)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("dk,dv", [(104, 64), (100, 64), (64, 20), (128, 100), (40, 33), (8, 8), (72, 128)])
+def test_every_way_of_copying(lla, dk, dv, dtype):
+    """Rows of whole 16-byte pieces or not, of states and of tokens; a chain, whose nodes all count."""
+    B, H, N, Lmax, t = 2, 2, 37, 13, [3000, 17]
+    r = np.random.default_rng(dk + dv)
+    d = draft(r, B, H, N, dk, dv, dtype, Lmax, t, chain=0.9, live=N)
+    g = {n: x[1] for n, x in d.items()}
+    out = lla.decode_tree(g["q"], g["k"], g["v"], g["log_a"], g["lam"], g["states"], g["t"], g["parent"])
+    for b in range(B):
+        deep = max(len(R.branch(d["parent"][0][b], i)) for i in range(N))
+        for h in range(H):
+            a = [d[n][0][b, h] for n in ("q", "k", "v", "log_a", "lam", "states")]
+            ref, size = R.tree(*a, t[b], d["parent"][0][b])
+            R.tree_check(np64(out[b, h]), ref, size, dtype, dk * (Lmax + deep), gate_units(a[3], deep + 1), (b, h))
+
+
 def test_states_behind_element_2_31(lla):
     B, H, N, dk, dv, Lmax = 480, 16, 9, 128, 128, 18
     r = np.random.default_rng(11)
