@@ -492,8 +492,8 @@ int lla_gated_decode_step(const void* x, const void* log_a, float* state, void* 
  *   state [B,H,dk,dv] fp32.
  *   dk, dv 1..128; Lmax 1..40. Products with the states run on tensor cores: bf16 queries as they are, states
  *   in two bf16 parts (2^-16 of each element), fp32 calls in three parts of both; sums in fp32 in a fixed order
- *   (repeated calls give identical bits; a call of fewer heads may cut its sums otherwise). An infinity in the states may come out as NaN; one in a node reaches
- *   only that node's and its descendants' outputs.
+ *   (repeated calls give identical bits; a call of fewer heads may cut its sums otherwise). An infinity in the
+ *   states may come out as NaN; one in a node reaches only that node's and its descendants' outputs.
  * lla_gated_decode_tree, lla_gated_decode_commit: the same for lla_gated_decode_step; x, log_a, out [B,N,D],
  *   state [B,D] fp32; B up to 65535. (h of a node: exp(log_a_i) h_parent(i) + x_i.)
  *

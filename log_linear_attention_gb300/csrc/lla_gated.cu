@@ -718,7 +718,7 @@ cudaError_t run_t(Args& a, bool back, cudaStream_t stream) {
     return back ? go(yes(), no()) : go(no(), no());
 }
 
-// ---- single tokens
+// ---- single tokens: one pass of 16-byte accesses over state, inputs and outputs
 
 template <typename T, typename G>
 __global__ void __launch_bounds__(kThreads) gated_step(const T* __restrict__ x, const G* __restrict__ log_a,
@@ -744,7 +744,8 @@ __global__ void __launch_bounds__(kThreads) gated_step(const T* __restrict__ x, 
 }
 
 // ---- trees: a thread per channel walks the nodes in order; parents come before their children, whose states it keeps in
-// shared memory.
+// shared memory. 64 x 1024 channels, 32 nodes: 8.7 us for 14 MB, bound by latency: two batches of 16 nodes' loads and the
+// chain of 32 states behind them (node by node 34 us; 32 nodes' loads at once 12.9, as registers leave fewer threads).
 constexpr int kTreeThreads = 64;
 
 // Whether a tree's parents are not as they should be, by every thread of the block together: par[i] (shared memory) < i, not
@@ -798,6 +799,7 @@ __global__ void __launch_bounds__(kTreeThreads) gated_tree(const T* __restrict__
     }
 }
 
+// Commits: the same chain over the accepted tokens, 2.8 us for 64 x 1024 channels with 6 tokens at most, about a launch.
 template <typename T, typename G>
 __global__ void __launch_bounds__(kTreeThreads) gated_commit(const T* __restrict__ x, const G* __restrict__ log_a,
                                                              float* __restrict__ state,

@@ -18,6 +18,13 @@
 // each slot by itself and weighted in fp32, so queries are never rounded with their weights. The states' rows come to a
 // ring in shared memory by TMA, in swizzled boxes of 32 columns, from which a lane reads the four rows' pieces of four
 // columns of its MMA operands without bank conflicts and cuts them itself.
+//
+// Measured (calls in a CUDA graph, inputs larger than L2): 64 sequences x 16 heads of 128 x 64 at t up to 65536, 32 nodes,
+// bf16: 62 us for 328 MB (78% of the copy rate); 16 nodes 58 us (81%), 64 nodes 100 us, fp32 with 32 nodes 129 us. One state
+// a head (linear) and 64 nodes: 33 us for 84 MB. What a block does before and after its states bounds it: of 26 thousand
+// cycles (two blocks on an SM) the first slot is taken at 8.4, a slot of 32 KB every 1.7, the rest is 1.9; fp32 is bound
+// by the six products. Steps: the lanes' own loads of states 85 us, row by row with untiled bulk copies 226 (their issue),
+// the ring of boxes 75, walkers beside scorers 62.
 #include "lla_drafts.cuh"
 #include "lla_linear_tc.cuh"
 
@@ -76,7 +83,7 @@ __device__ __forceinline__ void load4(const float* p, float (&f)[4]) {
     f[0] = y.x; f[1] = y.y; f[2] = y.z; f[3] = y.w;
 }
 __device__ __forceinline__ void load_nt(const float* p, float (&f)[4]) { load4(p, f); }
-[[maybe_unused]] __device__ __forceinline__ void load_nt(const float* p, float (&f)[2]) {
+__device__ __forceinline__ void load_nt(const float* p, float (&f)[2]) {
     const float2 y = *reinterpret_cast<const float2*>(p);
     f[0] = y.x; f[1] = y.y;
 }
@@ -94,7 +101,8 @@ template <typename T> struct Parts;  // of queries and keys; of states
 template <> struct Parts<__nv_bfloat16> { static constexpr int q = 1, s = 2; };
 template <> struct Parts<float> { static constexpr int q = 3, s = 3; };
 
-// Blocks of an SM by their registers, and the shared memory of each.
+// Blocks of an SM by their registers, and the shared memory of each. (32 nodes in pieces of 16 columns a warp leave room for
+// three blocks, but take every query twice as often: 76 us against 69 at that point.)
 template <typename T>
 __host__ __device__ constexpr int resident(int MT, int NT) { return Parts<T>::q == 1 && MT * NT <= 4 ? 3 : 2; }
 template <typename T>
@@ -105,7 +113,7 @@ __host__ __device__ constexpr int room(int MT, int NT) { return resident<T>(MT, 
 struct Layout {
     int q, k;      // kAll: panels of 64 columns, rows of 128 bytes, swizzled; else parts of rows of row_bytes
     int panel_q, panel_k;
-    int ring, stage, stages;
+    int ring, stage;
     int v, lam, p, far, up, total;
 };
 __host__ __device__ inline int up1024(int x) { return (x + 1023) / 1024 * 1024; }
@@ -122,7 +130,6 @@ __host__ __device__ inline Layout layout(int nb, int N, int dk, int cols, int sl
     const int rows = s.k + (tma ? panels * s.panel_k : parts * N * rb);
     s.ring = up1024(rows);
     s.stage = stage_rows * cols * 4;
-    s.stages = stages;
     s.v = s.ring + stages * s.stage > sums ? s.ring + stages * s.stage : up1024(sums);
     s.lam = s.v + (N + 7) / 8 * 8 * cols * static_cast<int>(sizeof(T));
     s.p = s.lam + nb * slots * 4;
@@ -242,8 +249,8 @@ struct Maps {
 // kMode: what comes by TMA, as rows of multiples of 16 bytes can; the states' ring is else filled by 4-byte copies of every
 // thread, in two stages.
 //
-// Four warps walk the tree and form the weights while the other four multiply queries and keys; most of a short block's
-// time is latency. With one tree after another (a first version): 10000 cycles before the first slot, now 5000.
+// Four warps walk the tree and form the weights while the other four multiply queries and keys, as most of what comes before
+// the first slot is latency: 75 us as one after the other, 62 side by side (32 nodes, the batch above).
 template <typename T, int MT, int NG, int CW, int NT, int kStageRows, int kMode>
 __global__ void __launch_bounds__(256, resident<T>(MT, NT))
     decode_tree_kernel(const TreeCall c, const __grid_constant__ Maps maps, const int stages) {
@@ -261,8 +268,9 @@ __global__ void __launch_bounds__(256, resident<T>(MT, NT))
     char* smem = smem_any + (-smem_u32(smem_any) & 1023u);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, cc = lane & 3;
     const int blocks = (c.N - 1) / kNb + 1;  // of nodes: those of one head run side by side, so that its states come once
-    const int64_t bh = blockIdx.x / blocks;
-    const int b = static_cast<int>(bh / c.H), h = static_cast<int>(bh - static_cast<int64_t>(b) * c.H);
+    const unsigned head = blockIdx.x / blocks;
+    const int b = static_cast<int>(head / c.H), h = static_cast<int>(head - b * static_cast<unsigned>(c.H));
+    const int64_t bh = head;
     const int N = c.N, dk = c.dk, dv = c.dv, dkp = (dk + 15) / 16 * 16, rb = row_bytes(dk), ksteps = dkp / 16;
     const int i0 = static_cast<int>(blockIdx.x % blocks) * kNb, col0 = blockIdx.y * kCols, live = N - i0 < kNb ? N - i0 : kNb;
     const bool linear = c.t == nullptr;
@@ -333,6 +341,7 @@ __global__ void __launch_bounds__(256, resident<T>(MT, NT))
             for (int e = tid; e < live * c.Lmax; e += kWalkers) copy_async<4>(&lam[e], c.lambda + (bh * N + i0) * c.Lmax + e);
         copies_group();
     }
+    const float lg = linear && tid < kWalkers ? c.log_a[h] : 0.f;
     const int64_t t = linear ? 1 : c.t[b];
     const int slots = held(t), rounds = slots * pieces;
     // A round's rows into stage `at` as TMA lays them, by all threads, zeros behind them; columns behind the last stay zero.
@@ -486,31 +495,45 @@ __global__ void __launch_bounds__(256, resident<T>(MT, NT))
         constexpr int kEach = kWalkers / kNb;
         const int i = tid % kNb, first = tid / kNb, node = i0 + i;
         if (i < live && par[node] != -2 && t >= 0 && t < limit) {
-            const float lg = linear ? c.log_a[h] : 0.f;
             const Link at = link[node];
             const uint4 line = above[node];
             const int64_t pos = t + at.steps;
             const float* lam_i = lam + i * c.Lmax;
-            int turn = first;
+            // nodes j of j % kEach == first, four at a time, so that their links are read side by side
+            constexpr unsigned long long kMine = ~0ull / ((1ull << kEach) - 1);
+            unsigned long long lo = (line.x | static_cast<unsigned long long>(line.y) << 32) & kMine << first;
+            unsigned long long hi = (line.z | static_cast<unsigned long long>(line.w) << 32) & kMine << first;
+            int base = 0, j[4];
+            do {
+                Link other[4];
 #pragma unroll
-            for (int y = 0; y < kMaxTree / 32; y++) {
-                if (y * 32 > node) break;
-                for (uint32_t bits = y == 0 ? line.x : y == 1 ? line.y : y == 2 ? line.z : line.w; bits; bits &= bits - 1) {
-                    if (turn-- != 0) continue;
-                    turn = kEach - 1;
-                    const int j = y * 32 + __ffs(static_cast<int>(bits)) - 1;
-                    const Link other = link[j];
-                    const int n = at.steps - other.steps;
-                    up[i * N + n] = static_cast<uint8_t>(j);
-                    float w;
-                    if (linear) w = n == 0 ? 1.f : expf(lg * static_cast<float>(n));
-                    else
-                        w = at.zeros > other.zeros ? 0.f
-                                                   : lam_i[64 - __clzll(static_cast<long long>(pos ^ (pos - n)))] *
-                                                         expf(at.decay - other.decay);
-                    P[i * (N + 1) + j] = w;
+                for (int y = 0; y < 4; y++) {
+                    if (lo == 0) {
+                        lo = hi;
+                        hi = 0;
+                        base = 64;
+                    }
+                    j[y] = lo == 0 ? -1 : base + __ffsll(static_cast<long long>(lo)) - 1;
+                    lo &= lo - 1;
+                    other[y] = link[j[y] < 0 ? node : j[y]];
                 }
-            }
+                float w[4];
+#pragma unroll
+                for (int y = 0; y < 4; y++) {
+                    const int n = at.steps - other[y].steps;
+                    if (linear) w[y] = n == 0 ? 1.f : expf(lg * static_cast<float>(n));
+                    else
+                        w[y] = at.zeros > other[y].zeros ? 0.f
+                                                         : lam_i[64 - __clzll(static_cast<long long>(pos ^ (pos - n)))] *
+                                                               expf(at.decay - other[y].decay);
+                }
+#pragma unroll
+                for (int y = 0; y < 4; y++)
+                    if (j[y] >= 0) {
+                        up[i * N + at.steps - other[y].steps] = static_cast<uint8_t>(j[y]);
+                        P[i * (N + 1) + j[y]] = w[y];
+                    }
+            } while (j[3] >= 0);
             const float whole = linear ? expf(lg * static_cast<float>(at.steps + 1)) : at.zeros ? 0.f : expf(at.decay);
             // the blocks of the walk of t - 1 begin at t - 1 and where its set bits are cleared one by one
             if (linear) {
@@ -773,7 +796,8 @@ cudaError_t launch_tree(const TreeCall& c, int stages, cudaStream_t stream) {
 }
 
 // The ring: stages of a whole slot's columns, or of part of its rows, the largest of which two fit beside the other blocks of
-// an SM (one, where there is one slot); by TMA up to four of them.
+// an SM (one, where there is one slot); by TMA up to four of them. (Two stages of 128 rows against four of 64: 62 us and
+// 66 for 32 nodes, alike for 16.)
 template <typename T, int MT, int NG, int CW, int NT, int kMode>
 cudaError_t pick_stage(const TreeCall& c, cudaStream_t stream) {
     constexpr int KS = 8 / (CW * NG), least = KS * 16 > 32 ? KS * 16 : 32;  // every warp has a unit of a stage
@@ -812,7 +836,8 @@ __device__ __forceinline__ int slot_in_walk(int64_t e, int64_t s) { return 64 - 
 // Every held slot of the last accepted position e = t + n - 1 from the old slots and the new tokens inside it. Each old
 // slot lies inside one new slot of its own number or above, so a thread, which takes its elements through all slots, goes
 // from the highest slot down and never reads what it has written. Elements are independent: grid (heads of all sequences,
-// shares of a state's elements).
+// shares of a state's elements). Bound by HBM: 64 x 16 heads of 128 x 64 with 6 tokens at most, 95 us for 531 MB read and
+// written (83% of the copy rate), four elements of a thread at a time (two 107 us, eight 151).
 template <typename T, int kW, int kU>  // kW columns of a thread, kU of its elements at a time
 __global__ void __launch_bounds__(kThreads) decode_commit_kernel(const CommitCall c, int share) {
     extern __shared__ float tok[];  // [n][dk] weighted keys, [n][dv] values
@@ -965,7 +990,9 @@ cudaError_t launch_commit(const CommitCall& c, cudaStream_t stream) {
 }  // namespace
 
 cudaError_t decode_tree(int dtype, const TreeCall& c, cudaStream_t stream) {
-    // 64 columns to a block, or 32 where that leaves SMs without one
+    // 64 columns to a block, or 32 where that leaves half of the SMs without one (4 x 16 heads of 128 x 64, 8 nodes: 9.8 us
+    // against 16). More than 32 nodes: blocks of 64 nodes with 16 columns a warp (64 nodes at that point: 113 us; two groups
+    // of warps of 32 nodes 119, two blocks of 32 nodes 147). fp32: two groups, whose three parts of a query fit registers.
     const bool wide = c.dv > 32 && static_cast<int64_t>(c.B) * c.H * ((c.dv - 1) / 64 + 1) > 76;
     if (dtype == 1) {
         if (c.N <= 16) return wide ? pick_copies<float, 1, 1, 2, 4>(c, stream) : pick_copies<float, 1, 1, 1, 4>(c, stream);
