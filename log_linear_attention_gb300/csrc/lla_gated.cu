@@ -14,8 +14,8 @@
 // them. Blocks of a cluster are resident together, so nothing waits for a block that may not run yet, and neither flags
 // nor workspace are needed. Maps are composed in one fixed order: repeated calls give identical bits.
 //
-// Bound by HBM: 4 x 8192 x 1024, bf16 with fp32 gates, 43 us for 268 MB (92% of the copy rate), gradients 76 us for 470 MB
-// (91%); 65536 x 1024 with bf16 gates 68 us for 403 MB (88%; a step's latency, about 2 us with the exchange, shows). What
+// Bound by HBM: 4 x 8192 x 1024, bf16 with fp32 gates, 43 us for 268 MB (92% of the copy rate), gradients 74 us for 470 MB
+// (93%); 65536 x 1024 with bf16 gates 68 us for 403 MB (88%; a step's latency, about 2 us with the exchange, shows). What
 // got it there: tiles by TMA two steps ahead (69 us with per-thread asynchronous copies, which cost a quarter of all
 // instructions and pass through L1), the exchange by stores that signal a barrier (a cluster barrier waits for the step's
 // stores to global memory besides: 0.7 us a step), steps without questions asked of a row, two channels to an instruction.
@@ -46,7 +46,9 @@ struct Cut {
     static constexpr int kL = kPath == kTma ? 8 : 4;  // kTma with 4 and three stages: 49 us against 43 (4 x 8192 x 1024)
     static constexpr int kStages = 2;
     static constexpr int stage_bytes = row_bytes * kL * kThreads;
-    static constexpr int kResident = kPath == kTma && stage_bytes * kStages > 110000 ? 1 : 2;  // blocks of an SM
+    // Blocks of an SM. Where shared memory holds one, its threads have all registers (fp32 gradients of 16 packed documents
+    // of 100 to 4000 rows of 512 channels: 54 us, with registers for two blocks 83).
+    static constexpr int kResident = kPath == kTma && stage_bytes * kStages > 110000 ? 1 : 2;
 };
 
 struct Args {
@@ -204,6 +206,12 @@ __device__ __forceinline__ float apply(float A, float s, float h) {
 
 // What a row of a packed call is: its sequence, and whether that one's walk begins or ends there. -1: no sequence's.
 constexpr int kBegins = 1 << 30, kEnds = 1 << 29, kSeq = kEnds - 1;
+// Of a row between an entry of cu, `here`, and the next one
+template <bool kBack>
+__device__ __forceinline__ int row_flags(int entry, int here, int next, int n, int row) {
+    const bool first = row == here, last = row == next - 1;
+    return entry < 0 || entry >= n ? -1 : entry | ((kBack ? last : first) ? kBegins : 0) | ((kBack ? first : last) ? kEnds : 0);
+}
 // The last entry of cu that is not behind the row is at `lo` or above, below `hi`; at(i) is entry i, and one in front of the
 // table (i = -1) is in front of every row.
 template <bool kBack, typename At>
@@ -214,10 +222,10 @@ __device__ __forceinline__ int row_info(At at, int lo, int hi, int n, int row) {
         else hi = mid;
     }
     if (lo < 0 || lo >= n) return -1;
-    const bool first = row == at(lo), last = row == at(lo + 1) - 1;
-    return lo | ((kBack ? last : first) ? kBegins : 0) | ((kBack ? first : last) ? kEnds : 0);
+    return row_flags<kBack>(lo, at(lo), at(lo + 1), n, row);
 }
 constexpr int kWindow = 32;  // entries of cu around a block's rows
+constexpr int kFew = 8;      // of them that are compared side by side, where the next one lies behind the rows
 
 // Four channels of a row as they lie in memory, loaded before they are needed.
 template <typename T, bool kVec>
@@ -245,7 +253,7 @@ struct Ahead<T, false> {
 };
 
 template <typename T, typename G, bool kBack, bool kPacked, int kPath, int kLanes>
-__global__ void __launch_bounds__(kThreads, 2) gated_scan(const __grid_constant__ Args a) {
+__global__ void __launch_bounds__(kThreads, Cut<T, G, kBack, kPath>::kResident) gated_scan(const __grid_constant__ Args a) {
     using C = Cut<T, G, kBack, kPath>;
     constexpr bool kVec = kPath != kSingles;
     using Ch = Chan<kVec, kLanes>;
@@ -403,14 +411,31 @@ __global__ void __launch_bounds__(kThreads, 2) gated_scan(const __grid_constant_
             plain &= plain_of[buf] != 0;
             if (!plain) {
                 const int base = near[buf];  // entry of window[buf][0]
-                const bool enough = window[buf][kWindow - 1] > (kBack ? hi - block0 : lo + block0 + kRows);
+                const int last = kBack ? hi - 1 - block0 : lo + block0 + kRows - 1;
+                const bool few = window[buf][kFew] > last, enough = window[buf][kWindow - 1] > last;
+                int w[kFew];
+#pragma unroll
+                for (int e = 0; e < kFew; e++) w[e] = window[buf][e];
                 for (int i = tid; i < kRows; i += kThreads) {
                     const int u = block0 + i, row = kBack ? hi - 1 - u : lo + u;
                     int inf = -1;
-                    if (u < len && enough)
+                    if (u < len && few) {  // side by side
+                        int at = 0, here = w[0], next = window[buf][kFew];
+#pragma unroll
+                        for (int e = 1; e < kFew; e++)
+                            if (w[e] <= row) {
+                                at = e;
+                                here = w[e];
+                            }
+#pragma unroll
+                        for (int e = kFew - 1; e > 0; e--)
+                            if (w[e] > row) next = w[e];
+                        inf = row_flags<kBack>(base + at, here, next, p.n, row);
+                    } else if (u < len && enough) {
                         inf = row_info<kBack>([&](int e) { return window[buf][e - base]; }, base, base + kWindow - 1, p.n, row);
-                    else if (u < len)
+                    } else if (u < len) {
                         inf = row_info<kBack>([&](int e) { return e < 0 ? -1 : p.cu[e]; }, base, p.n + 1, p.n, row);
+                    }
                     info[buf][i] = inf;
                 }
                 __syncthreads();
@@ -457,6 +482,7 @@ __global__ void __launch_bounds__(kThreads, 2) gated_scan(const __grid_constant_
             split(pa, A);
             split(ps, s);
         } else {
+            bool begun = false;
 #pragma unroll
             for (int v = 0; v < 4; v++) {
                 A[v] = 1.f;
@@ -465,18 +491,21 @@ __global__ void __launch_bounds__(kThreads, 2) gated_scan(const __grid_constant_
 #pragma unroll
             for (int j = 0; j < kL; j++) {
                 const int inf = kPacked ? info[buf][seg * kL + j] : 0;
+                const bool in = kPacked ? inf >= 0 : u0 + j < len, begins = kPacked && in && (inf & kBegins);
                 float gf[4] = {0.f, 0.f, 0.f, 0.f}, xf[4] = {0.f, 0.f, 0.f, 0.f};
-                if (u0 + j < len && (!kPacked || inf >= 0)) {
+                if (kPacked || in) {
                     gates_of(j, gf);
                     inputs_of(j, xf);
-                    if (kPacked && (inf & kBegins)) {
+                }
+                if (kPacked) {  // selects; a branch only where a state enters
 #pragma unroll
-                        for (int v = 0; v < 4; v++) {
-                            A[v] = -1.f;
-                            s[v] = 0.f;
-                        }
-                        if (enter) ch.load(enters(inf & kSeq), s);
+                    for (int v = 0; v < 4; v++) {
+                        gf[v] = in ? gf[v] : 0.f;
+                        xf[v] = in ? xf[v] : 0.f;
+                        s[v] = begins ? 0.f : s[v];
                     }
+                    if (enter && begins) ch.load(enters(inf & kSeq), s);
+                    begun |= begins;
                 }
                 g[j] = gate(quad(gf));
                 x[j] = quad(xf);
@@ -484,8 +513,12 @@ __global__ void __launch_bounds__(kThreads, 2) gated_scan(const __grid_constant_
 #pragma unroll
                 for (int v = 0; v < 4; v++) {
                     s[v] = kBack ? fmaf(gf[v], s[v], gf[v] * xf[v]) : fmaf(gf[v], s[v], xf[v]);
-                    if (!kPacked || A[v] >= 0.f) A[v] *= gf[v];
+                    A[v] *= gf[v];
                 }
+            }
+            if (begun) {
+#pragma unroll
+                for (int v = 0; v < 4; v++) A[v] = -1.f;
             }
         }
         if (kPath != kTma) prefetch(st + 1);
@@ -582,41 +615,49 @@ __global__ void __launch_bounds__(kThreads, 2) gated_scan(const __grid_constant_
             for (int j = 0; j < kL; j++) {
                 const int u = u0 + j, row = kBack ? hi - 1 - u : lo + u;
                 const int inf = kPacked ? info[buf][seg * kL + j] : 0;
-                if (u >= len) continue;
-                if (kPacked && inf < 0) {
-                    if (kBack) {  // rows of no sequence take no part in the sum that is differentiated
-                        const float z[4] = {0.f, 0.f, 0.f, 0.f};
-                        ch.store(op + static_cast<int64_t>(row) * D, z);
-                        ch.store(ap + static_cast<int64_t>(row) * D, z);
-                    }
-                    continue;
-                }
-                if (kPacked && (inf & kBegins)) {
+                if (!kPacked && u >= len) continue;
+                const bool in = inf >= 0, begins = kPacked && in && (inf & kBegins);
+                const bool ends = kPacked ? in && (inf & kEnds) : row == 0;
+                const int64_t off = static_cast<int64_t>(row) * D;
+                if (kPacked) {
 #pragma unroll
-                    for (int v = 0; v < 4; v++) h[v] = 0.f;
-                    if (enter) ch.load(enters(inf & kSeq), h);
+                    for (int v = 0; v < 4; v++) h[v] = begins ? 0.f : h[v];
+                    if (enter && begins) ch.load(enters(inf & kSeq), h);
                 }
                 float gf[4], xf[4];
                 split(g[j], gf);
                 split(x[j], xf);
                 if constexpr (kBack) {
                     float before[4] = {0.f, 0.f, 0.f, 0.f}, d[4], da[4];
-                    if (!(kPacked ? (inf & kEnds) != 0 : row == 0)) hp[j].get(before);
-                    else if (p.state0) ch.load(first_state(kPacked ? inf & kSeq : b), before);
+                    if constexpr (kPacked) {
+                        hp[j].get(before);
+#pragma unroll
+                        for (int v = 0; v < 4; v++) before[v] = ends ? 0.f : before[v];
+                        if (ends && p.state0) ch.load(first_state(inf & kSeq), before);
+                    } else {
+                        if (!ends) hp[j].get(before);
+                        else if (p.state0) ch.load(first_state(b), before);
+                    }
 #pragma unroll
                     for (int v = 0; v < 4; v++) {
                         d[v] = xf[v] + h[v];
                         h[v] = gf[v] * d[v];
                         da[v] = h[v] * before[v];
+                        if constexpr (kPacked) {  // rows of no sequence take no part in the sum that is differentiated
+                            d[v] = in ? d[v] : 0.f;
+                            da[v] = in ? da[v] : 0.f;
+                        }
                     }
-                    ch.store(op + static_cast<int64_t>(row) * D, d);
-                    ch.store(ap + static_cast<int64_t>(row) * D, da);
+                    if (!kPacked || u < len) {
+                        ch.store(op + off, d);
+                        ch.store(ap + off, da);
+                    }
                 } else {
 #pragma unroll
                     for (int v = 0; v < 4; v++) h[v] = fmaf(gf[v], h[v], xf[v]);
-                    ch.store(op + static_cast<int64_t>(row) * D, h);
+                    if (!kPacked || in) ch.store(op + off, h);
                 }
-                if (kPacked && (inf & kEnds) && p.leave) ch.store(p.leave + static_cast<int64_t>(inf & kSeq) * D, h);
+                if (kPacked && p.leave && ends) ch.store(p.leave + static_cast<int64_t>(inf & kSeq) * D, h);
             }
         }
     }
