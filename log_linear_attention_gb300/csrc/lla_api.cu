@@ -1031,7 +1031,7 @@ int gated_pass(bool back, const void* x, const void* log_a, const float* state0,
     float* parts = reinterpret_cast<float*>(ws.p);
     const lla::GatedPass p = {log_a, x, dout, out, dlog_a, state0, dstate_out, sum ? parts : leave, cu, n, n0, T, D};
     cudaError_t e = lla::gated_run(p, back, dtype, gate_dtype, err, s);
-    if (e == cudaSuccess && sum) e = lla::linear_sum_batch(parts, leave, n, D, s);
+    if (e == cudaSuccess && sum) e = lla::gated_sum_shared(parts, leave, cu, n, T, D, s);
     return ws.give(e);
 }
 

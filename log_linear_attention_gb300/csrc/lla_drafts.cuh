@@ -24,6 +24,8 @@ struct GatedPass {
     int T, D;                 // rows of a sequence (packed: of all); channels
 };
 cudaError_t gated_run(const GatedPass& p, bool backward, int dtype, int gate_dtype, int* err, cudaStream_t stream);
+// The gradient of one shared state: out [D] from the sequences' parts [n][D] (GatedPass::leave), in order.
+cudaError_t gated_sum_shared(const float* parts, float* out, const int32_t* cu, int n, int T, int D, cudaStream_t stream);
 cudaError_t gated_decode_step(int dtype, int gate_dtype, const void* x, const void* log_a, float* state, void* out,
                               int64_t size, cudaStream_t stream);
 cudaError_t gated_decode_tree(int dtype, int gate_dtype, const void* x, const void* log_a, const float* state,

@@ -293,10 +293,16 @@ __global__ void __launch_bounds__(kThreads, Cut<T, G, kBack, kPath>::kResident) 
             if (x < cut1) upto++;
             else if (x < next) next = x;
         }
-        atomicMin(&bounds[0], first);
-        atomicMin(&bounds[1], next);
-        atomicAdd(&bounds[2], before);
-        atomicAdd(&bounds[3], upto);
+        first = __reduce_min_sync(0xffffffffu, first);
+        next = __reduce_min_sync(0xffffffffu, next);
+        before = __reduce_add_sync(0xffffffffu, before);
+        upto = __reduce_add_sync(0xffffffffu, upto);
+        if ((tid & 31) == 0) {
+            atomicMin(&bounds[0], first);
+            atomicMin(&bounds[1], next);
+            atomicAdd(&bounds[2], before);
+            atomicAdd(&bounds[3], upto);
+        }
         if (__syncthreads_or(bad)) {  // every block finds the same
             if (blockIdx.x == 0 && tid == 0) record_error(a.err, kDevBadInput);
             return;
@@ -670,6 +676,26 @@ __global__ void __launch_bounds__(kThreads, Cut<T, G, kBack, kPath>::kResident) 
     if (cs > 1) cluster_meet<false>();
 }
 
+// The gradient of a state that n sequences share: their parts summed in order. Launched while the scan ends (its results are
+// read behind the wait); it writes nothing either where cu is bad.
+__global__ void __launch_bounds__(kThreads) gated_sum(const float* parts, float* out, const int32_t* __restrict__ cu, int n,
+                                                      int T, int D) {
+    bool bad = false;
+    if (cu)
+        for (int i = threadIdx.x; i <= n; i += kThreads) {
+            const int x = cu[i];
+            bad |= x < 0 || x > T || (i > 0 && x < cu[i - 1]);
+        }
+    bad = __syncthreads_or(bad);
+    grid_dep_wait();
+    const int64_t c = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
+    if (bad || c >= D) return;
+    float s = 0.f;
+#pragma unroll 8
+    for (int b = 0; b < n; b++) s += parts[static_cast<int64_t>(b) * D + c];
+    out[c] = s;
+}
+
 // Tile map of a tensor [rows, D]
 bool tile_map(CUtensorMap* m, const void* base, bool f32, int64_t rows, int D, int cols, int box_rows) {
     auto fn = encode_fn();
@@ -884,6 +910,21 @@ cudaError_t gated_run(const GatedPass& p, bool backward, int dtype, int gate_dty
     a.p = p;
     a.err = err;
     return by_types(dtype, gate_dtype, [&](auto t, auto g) { return run_t<decltype(t), decltype(g)>(a, backward, stream); });
+}
+
+cudaError_t gated_sum_shared(const float* parts, float* out, const int32_t* cu, int n, int T, int D, cudaStream_t stream) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((D - 1) / kThreads + 1);
+    cfg.blockDim = dim3(kThreads);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    cudaError_t e = cudaLaunchKernelEx(&cfg, gated_sum, parts, out, cu, n, T, D);
+    note_launch(stream, "gated_sum");
+    return e;
 }
 
 cudaError_t gated_decode_step(int dtype, int gate_dtype, const void* x, const void* log_a, float* state, void* out,

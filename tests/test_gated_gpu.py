@@ -330,6 +330,21 @@ def test_bad_bounds_write_nothing(lla, cu):
     assert lla.device_error() == lla.LLA_ERR_DEVICE
 
 
+@pytest.mark.parametrize("cu", [[0, 9, 5, 20], [-1, 3, 9, 20], [0, 3, 9, 21]])
+def test_bad_bounds_leave_the_shared_gradient(lla, cu):
+    """The gradient of one shared state is a sum over the sequences, in a launch of its own."""
+    x, a = torch.ones(20, 24, device="cuda"), torch.zeros(20, 24, device="cuda")
+    s0, c = torch.zeros(1, 24, device="cuda"), torch.tensor(cu, dtype=torch.int32, device="cuda")
+    dx, da, ds = torch.full_like(x, 7.0), torch.full_like(x, 7.0), torch.full_like(s0, 7.0)
+    stream = torch.cuda.current_stream().cuda_stream
+    status = lla.load().lla_gated_backward_varlen(
+        a.data_ptr(), x.data_ptr(), s0.data_ptr(), x.data_ptr(), None, dx.data_ptr(), da.data_ptr(), ds.data_ptr(),
+        c.data_ptr(), 3, 1, 20, 24, stream, lla.LLA_F32, lla.LLA_F32)
+    assert status == lla.LLA_OK
+    assert lla.device_error() == lla.LLA_ERR_DEVICE
+    assert all(bool((t == 7.0).all()) for t in (dx, da, ds))
+
+
 def test_prompts_go_on_from_states(lla):
     r = np.random.default_rng(3)
     for dtype, gt in TYPES:
