@@ -46,9 +46,7 @@ struct Cut {
     static constexpr int kL = kPath == kTma ? 8 : 4;  // kTma with 4 and three stages: 49 us against 43 (4 x 8192 x 1024)
     static constexpr int kStages = 2;
     static constexpr int stage_bytes = row_bytes * kL * kThreads;
-    // Blocks of an SM. Where shared memory holds one, its threads have all registers (fp32 gradients of 16 packed documents
-    // of 100 to 4000 rows of 512 channels: 54 us, with registers for two blocks 83).
-    static constexpr int kResident = kPath == kTma && stage_bytes * kStages > 110000 ? 1 : 2;
+    static constexpr int kResident = kPath == kTma && stage_bytes * kStages > 110000 ? 1 : 2;  // blocks of an SM
 };
 
 struct Args {
@@ -252,8 +250,14 @@ struct Ahead<T, false> {
     }
 };
 
+// Registers: where shared memory holds one block of an SM, its threads have all of them (fp32 gradients of 16 packed documents of
+// 100 to 4000 rows of 512 channels: 54 us, with registers for two blocks 83), but for dense fp32, where the loads that the
+// compiler then moves together cost more than they save (gradients of 4 x 8192 x 1024: 107 us for two blocks, 117).
+template <typename T, typename G, bool kBack, bool kPacked, int kPath>
+constexpr int kBlocks = kPacked || sizeof(T) == 2 ? Cut<T, G, kBack, kPath>::kResident : 2;
+
 template <typename T, typename G, bool kBack, bool kPacked, int kPath, int kLanes>
-__global__ void __launch_bounds__(kThreads, Cut<T, G, kBack, kPath>::kResident) gated_scan(const __grid_constant__ Args a) {
+__global__ void __launch_bounds__(kThreads, (kBlocks<T, G, kBack, kPacked, kPath>)) gated_scan(const __grid_constant__ Args a) {
     using C = Cut<T, G, kBack, kPath>;
     constexpr bool kVec = kPath != kSingles;
     using Ch = Chan<kVec, kLanes>;
