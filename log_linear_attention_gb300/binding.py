@@ -693,7 +693,7 @@ def decode_step_shared(q, k, v, log_a, lam, prefix_states, prefix_len: int, pref
 
 
 def _fits(t_, dtype, shape, index):
-    return (type(t_) is _torch_module.Tensor and t_.dtype is dtype and t_.shape == shape and t_.get_device() == index
+    return (isinstance(t_, _torch_module.Tensor) and t_.dtype is dtype and t_.shape == shape and t_.get_device() == index
             and t_.is_contiguous())
 
 
@@ -931,7 +931,7 @@ def decode_tree(q, k, v, log_a, lam, states, t, parent, out=None, stream=None):
         _nodes(("q", "k", "v"), (q, k, v), log_a, _node_gates)
     B, H, N, dk = q.shape
     dv, dtype, index = v.shape[3], q.dtype, q.get_device()
-    if type(states) is not torch.Tensor or states.dim() != 5:
+    if not isinstance(states, torch.Tensor) or states.dim() != 5:
         raise ValueError("states must be float32 [B,H,Lmax,dk,dv]")
     L = states.shape[2]
     if not (index >= 0 and k.dtype is dtype and v.dtype is dtype and k.shape == q.shape and v.shape == (B, H, N, dv)
@@ -968,7 +968,7 @@ def decode_commit(k, v, log_a, states, t, count, path=None, stream=None):
         _nodes(("k", "v"), (k, v), log_a, _node_gates)
     B, H, N, dk = k.shape
     dv, dtype, index = v.shape[3], k.dtype, k.get_device()
-    if type(states) is not torch.Tensor or states.dim() != 5:
+    if not isinstance(states, torch.Tensor) or states.dim() != 5:
         raise ValueError("states must be float32 [B,H,Lmax,dk,dv]")
     L = states.shape[2]
     if not (index >= 0 and v.dtype is dtype and v.shape == (B, H, N, dv) and log_a.dtype is torch.float32

@@ -317,6 +317,25 @@ def test_graphs_streams_and_given_outputs(lla):
         lla.decode_tree(*args, out=g["v"])
 
 
+def test_parameters_are_tensors(lla):
+    """What a module holds (torch.nn.Parameter) is taken like any other tensor."""
+    P = lambda x: torch.nn.Parameter(x, requires_grad=False)
+    r = np.random.default_rng(14)
+    d = draft(r, 2, 2, 5, 64, 64, "bf16", 9, [100, 3], live=5)
+    g = {n: x[1] for n, x in d.items()}
+    args = [g[n] for n in ("q", "k", "v", "log_a", "lam", "states", "t", "parent")]
+    ref = lla.decode_tree(*args)
+    assert torch.equal(lla.decode_tree(*(P(x) for x in args)), ref)
+    count = ints([2, 1])
+    one, two = g["states"].clone(), P(g["states"].clone())
+    lla.decode_commit(g["k"], g["v"], g["log_a"], one, g["t"], count)
+    lla.decode_commit(P(g["k"]), P(g["v"]), P(g["log_a"]), two, g["t"], P(count))
+    assert torch.equal(one.view(torch.int32), two.detach().view(torch.int32))  # slots that hold nothing are NaN
+    decay, state = torch.full((2,), -0.1, device="cuda"), g["states"][:, :, 0].contiguous()
+    ref = lla.linear_decode_tree(*args[:3], decay, state, args[7])
+    assert torch.equal(lla.linear_decode_tree(*args[:3], P(decay), P(state), args[7]), ref)
+
+
 def test_two_streams_at_once(lla):
     B, H, N, dk, dv, Lmax = 32, 8, 30, 128, 64, 14
     r = np.random.default_rng(13)
