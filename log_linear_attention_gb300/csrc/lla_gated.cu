@@ -815,8 +815,10 @@ __global__ void __launch_bounds__(kThreads) gated_step(const T* __restrict__ x, 
 }
 
 // ---- trees: a thread per channel walks the nodes in order; parents come before their children, whose states it keeps in
-// shared memory. 64 x 1024 channels, 32 nodes: 8.7 us for 14 MB, bound by latency: two batches of 16 nodes' loads and the
-// chain of 32 states behind them (node by node 34 us; 32 nodes' loads at once 12.9, as registers leave fewer threads).
+// shared memory. 64 x 1024 channels, 32 nodes: 6.7 us for 14 MB, bound by latency: the loads of 16 nodes at a time, the next
+// ones on their way meanwhile, and the chain of 32 states. (Node by node 34 us; a batch after the other, behind the look at the
+// tree, 8.7; each place filled again as it is used 14; 32 nodes' loads at once 12.9; a chain's states passed on in a
+// register, behind a branch, 7.5.)
 constexpr int kTreeThreads = 64;
 
 // Whether a tree's parents are not as they should be, by every thread of the block together: par[i] (shared memory) < i, not
@@ -837,36 +839,52 @@ __global__ void __launch_bounds__(kTreeThreads) gated_tree(const T* __restrict__
                                                            const int32_t* __restrict__ parent, T* __restrict__ out,
                                                            int BP, int N, int D, int* err) {
     __shared__ int par[kMaxTree];
-    extern __shared__ float hs[];  // [N][kTreeThreads]
+    extern __shared__ float hs[];  // [1 + N][kTreeThreads]: the entering state, the nodes'
     const int tid = threadIdx.x, b = blockIdx.y, c = blockIdx.x * kTreeThreads + tid;
+    const bool mine = c < D;
+    hs[tid] = mine ? state[static_cast<int64_t>(b) * D + c] : 0.f;
+    const int64_t at = static_cast<int64_t>(b) * N * D + c;
+    constexpr int kAhead = 16;  // nodes whose inputs are loaded together, while those before them are walked
+    struct Nodes {
+        T x[kAhead];
+        G g[kAhead];
+    };
+    auto load = [&](Nodes& n, int i0) {
+        if (i0 >= N || !mine) return;
+#pragma unroll
+        for (int j = 0; j < kAhead; j++) {
+            const int64_t off = at + static_cast<int64_t>(i0 + j < N ? i0 + j : N - 1) * D;
+            n.x[j] = x[off];
+            n.g[j] = log_a[off];
+        }
+    };
+    auto walk = [&](const Nodes& n, int i0) {
+        int at_node[kAhead];
+#pragma unroll
+        for (int j = 0; j < kAhead; j++) at_node[j] = par[i0 + j < kMaxTree ? i0 + j : 0];
+#pragma unroll
+        for (int j = 0; j < kAhead; j++) {
+            if (i0 + j >= N) break;
+            const int up = at_node[j] < 0 ? 0 : at_node[j] + 1;  // places without a node go along, but are not stored
+            const float h = fmaf(expf(load_f(&n.g[j])), hs[up * kTreeThreads + tid], load_f(&n.x[j]));
+            hs[(i0 + j + 1) * kTreeThreads + tid] = h;
+            if (at_node[j] != -2) store_f(out + at + static_cast<int64_t>(i0 + j) * D, h);
+        }
+    };
+    Nodes even, odd;
+    load(even, 0);
     for (int i = tid; i < N; i += kTreeThreads) par[i] = parent[(BP > 1 ? static_cast<int64_t>(b) * N : 0) + i];
     __syncthreads();
     if (tree_is_bad(par, N)) {
         if (tid == 0) record_error(err, kDevBadInput);
         return;
     }
-    if (c >= D) return;
-    const float h0 = state[static_cast<int64_t>(b) * D + c];
-    const int64_t at = static_cast<int64_t>(b) * N * D + c;
-    constexpr int kAhead = 16;  // nodes whose inputs are loaded together
-    for (int i0 = 0; i0 < N; i0 += kAhead) {
-        T xi[kAhead];
-        G gi[kAhead];
-#pragma unroll
-        for (int j = 0; j < kAhead; j++) {
-            const int64_t off = at + static_cast<int64_t>(i0 + j < N ? i0 + j : N - 1) * D;
-            xi[j] = x[off];
-            gi[j] = log_a[off];
-        }
-#pragma unroll
-        for (int j = 0; j < kAhead; j++) {
-            if (i0 + j >= N) break;
-            const int pi = par[i0 + j];
-            if (pi == -2) continue;
-            const float h = fmaf(expf(load_f(&gi[j])), pi < 0 ? h0 : hs[pi * kTreeThreads + tid], load_f(&xi[j]));
-            hs[(i0 + j) * kTreeThreads + tid] = h;
-            store_f(out + at + static_cast<int64_t>(i0 + j) * D, h);
-        }
+    if (!mine) return;
+    for (int i0 = 0; i0 < N; i0 += 2 * kAhead) {
+        load(odd, i0 + kAhead);
+        walk(even, i0);
+        load(even, i0 + 2 * kAhead);
+        walk(odd, i0 + kAhead);
     }
 }
 
@@ -949,7 +967,7 @@ cudaError_t gated_decode_tree(int dtype, int gate_dtype, const void* x, const vo
     return by_types(dtype, gate_dtype, [&](auto t, auto g) {
         using T = decltype(t);
         using G = decltype(g);
-        gated_tree<T, G><<<dim3((D - 1) / kTreeThreads + 1, B), kTreeThreads, N * kTreeThreads * sizeof(float), stream>>>(
+        gated_tree<T, G><<<dim3((D - 1) / kTreeThreads + 1, B), kTreeThreads, (N + 1) * kTreeThreads * sizeof(float), stream>>>(
             static_cast<const T*>(x), static_cast<const G*>(log_a), state, parent, static_cast<T*>(out), BP, N, D, err);
         note_launch(stream, "gated_tree");
         return cudaGetLastError();
