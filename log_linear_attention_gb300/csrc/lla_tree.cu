@@ -246,8 +246,8 @@ struct Maps {
 
 // Grid: (heads of all sequences times blocks of 16 MT NG nodes, column blocks of 8 CW NT). The warps are CW column pieces of
 // 8 NT times NG groups of 16 MT nodes times KS shares of the 16-row units. kStageRows: state rows of a stage of the ring.
-// kMode: what comes by TMA, as rows of multiples of 16 bytes can; the states' ring is else filled by 4-byte copies of every
-// thread, in two stages.
+// kMode: what comes by TMA, as rows of multiples of 16 bytes can; the states' ring is else filled by copies of every thread,
+// of 4 bytes (8 where dv is even), in two stages.
 //
 // Four warps walk the tree and form the weights while the other four multiply queries and keys, as most of what comes before
 // the first slot is latency: 75 us as one after the other, 62 side by side (32 nodes, the batch above).
@@ -345,24 +345,31 @@ __global__ void __launch_bounds__(256, resident<T>(MT, NT))
     const int64_t t = linear ? 1 : c.t[b];
     const int slots = held(t), rounds = slots * pieces;
     // A round's rows into stage `at` as TMA lays them, by all threads, zeros behind them; columns behind the last stay zero.
-    auto fill = [&](int at, int slot, int piece) {
+    // A warp to every eighth row, whose places differ by a constant (64 x 16 heads of 128 x 50, 12 nodes: 92 us, with every
+    // element's place worked out 178; four stages instead of two: no change).
+    auto fill_by = [&](int at, int slot, int piece, auto width) {
+        constexpr int kW = decltype(width)::value;  // columns of a copy
         const int r0 = piece * kStageRows, rows = dk - r0 < kStageRows ? dk - r0 : kStageRows;
         const float* from = c.states + ((bh * c.Lmax + slot) * dk + r0) * dv + col0;
-        char* to = ring + at * s.stage;
-        const int down = kThreads / wide, right = kThreads - down * wide;
-        int r = tid / wide, x = tid - r * wide;
-        while (r < (rows + 15) / 16 * 16) {
-            char* place = to + x / 32 * kBox + r * 128 + ((x % 32 / 4 ^ (r & 7)) << 4) + x % 4 * 4;
-            if (r < rows) copy_async<4>(place, from + static_cast<int64_t>(r) * dv + x);
-            else *reinterpret_cast<float*>(place) = 0.f;
-            r += down;
-            x += right;
-            if (x >= wide) {
-                x -= wide;
-                r++;
+        static_assert(kWarps == 8);  // a warp's rows lie alike in their swizzled lines
+        for (int x = lane * kW; x < wide; x += 32 * kW) {
+            char* place = ring + at * s.stage + x / 32 * kBox + warp * 128 + ((x % 32 / 4 ^ warp) << 4) + x % 4 * 4;
+            const float* src = from + static_cast<int64_t>(warp) * dv + x;
+#pragma unroll 4
+            for (int r = warp; r < (rows + 15) / 16 * 16; r += 8, place += 1024, src += 8 * dv) {
+                if (r < rows) {
+                    copy_async<4 * kW>(place, src);
+                } else {
+#pragma unroll
+                    for (int v = 0; v < kW; v++) reinterpret_cast<float*>(place)[v] = 0.f;
+                }
             }
         }
         copies_group();
+    };
+    auto fill = [&](int at, int slot, int piece) {
+        if (dv % 2 == 0) fill_by(at, slot, piece, std::integral_constant<int, 2>());
+        else fill_by(at, slot, piece, std::integral_constant<int, 1>());
     };
     if constexpr (!kTma) {
         for (int e = tid; e < stages * s.stage / 16; e += kThreads) reinterpret_cast<uint4*>(ring)[e] = make_uint4(0u, 0u, 0u, 0u);
@@ -802,14 +809,13 @@ template <typename T, int MT, int NG, int CW, int NT, int kMode>
 cudaError_t pick_stage(const TreeCall& c, cudaStream_t stream) {
     constexpr int KS = 8 / (CW * NG), least = KS * 16 > 32 ? KS * 16 : 32;  // every warp has a unit of a stage
     constexpr int middle = least > 64 ? least : 64;
-    if constexpr (kMode == kNone) return launch_tree<T, MT, NG, CW, NT, least, kMode>(c, 2, stream);
     auto fit = [&](int rows) {
         const Layout s = layout<T>(16 * MT * NG, c.N, c.dk, 8 * CW * NT, c.Lmax, rows, 0, KS, kMode == kAll);
         const int all = c.Lmax * ((c.dk - 1) / rows + 1), most = all < kMaxStages ? all : kMaxStages;
         const int n = (room<T>(MT, NT) - (s.total - s.v) - s.ring) / s.stage;
-        return n < most ? n : most;
+        return kMode == kNone ? n < 2 ? n : 2 : n < most ? n : most;
     };
-    const int want = c.Lmax > 1 ? 2 : 1;
+    const int want = c.Lmax > 1 || kMode == kNone ? 2 : 1;
     if ((c.dk > 64 || middle == 128) && fit(128) >= want) return launch_tree<T, MT, NG, CW, NT, 128, kMode>(c, fit(128), stream);
     if ((c.dk > 32 || least == middle) && fit(middle) >= want)
         return launch_tree<T, MT, NG, CW, NT, middle, kMode>(c, fit(middle), stream);
