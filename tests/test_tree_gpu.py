@@ -354,7 +354,8 @@ def test_two_streams_at_once(lla):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
-@pytest.mark.parametrize("dk,dv", [(104, 64), (100, 64), (64, 20), (128, 100), (40, 33), (8, 8), (72, 128)])
+@pytest.mark.parametrize("dk,dv", [(104, 64), (100, 64), (64, 20), (128, 100), (40, 33), (8, 8), (72, 128),
+                                   (128, 126), (100, 50), (24, 2), (33, 1), (17, 66)])
 def test_every_way_of_copying(lla, dk, dv, dtype):
     """Rows of whole 16-byte pieces or not, of states and of tokens; a chain, whose nodes all count."""
     B, H, N, Lmax, t = 2, 2, 37, 13, [3000, 17]
