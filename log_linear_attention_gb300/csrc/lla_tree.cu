@@ -215,13 +215,27 @@ __device__ __forceinline__ void mma_parts(float (&d)[4], const uint32_t (&a)[kQ]
         }
 }
 
-// What lies between a node and the one that its jump leads to (-1: past the root): steps, sum of the finite log decays of
-// the nodes from it up to there, and how many are -inf. At the end jumps lead past the root everywhere.
+// What lies between a node and the one that its jump leads to (-1: past the root). At the end jumps lead past the root
+// everywhere, and what lies between a node and one above it is the difference of the two, so the sum of log decays carries what
+// its additions round away in a second float: behind gates of -100 each, a difference of plain fp32 sums has lost 2^-10 of the
+// weight. A gate that is 0 in fp32 forgets whatever it is (-inf, -1e9), and one that is infinite or NaN spoils the weight; both
+// are counted instead of summed.
 struct __align__(16) Link {
-    int jump, steps;
-    float decay;
-    int zeros;
+    int jump;
+    unsigned counts;  // steps, gates of zero << 8, gates that are not finite << 16: 128 of each at most
+    float decay, rest;
+    __device__ __forceinline__ int steps() const { return static_cast<int>(counts & 255u); }
 };
+constexpr unsigned kZero = 1u << 8, kOdd = 1u << 16;
+__device__ __forceinline__ void add_decays(Link& a, const Link& b) {  // the first sum's rounding error is exact
+    const float s = a.decay + b.decay, part = s - a.decay;
+    a.rest += b.rest + ((a.decay - (s - part)) + (b.decay - part));
+    a.decay = s;
+}
+// e^(sum of log decays) between a node and one above it, or past the root: `counts` and sums are differences
+__device__ __forceinline__ float weight(unsigned counts, float decay, float rest) {
+    return counts < kZero ? expf(decay + rest) : counts < kOdd ? 0.f : __int_as_float(0x7fffffff);
+}
 __device__ __forceinline__ void scorers_meet() { asm volatile("bar.sync 2, 128;" ::: "memory"); }
 // Walkers' barrier; any(x): whether one of them has x.
 __device__ __forceinline__ void walkers_meet() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
@@ -466,16 +480,17 @@ __global__ void __launch_bounds__(256, resident<T>(MT, NT))
         copies_done<0>();
         walkers_meet();
         const int p = tid < N ? par[tid] : -2;
-        Link me = {p, p >= 0 ? 1 : 0, 0.f, 0};
+        Link me = {p, p >= 0 ? 1u : 0u, 0.f, 0.f};
         uint4 mask = make_uint4(0u, 0u, 0u, 0u);
         if (tid < N) {
             if (p >= tid || p < -2 || (p >= 0 && par[p] == -2)) {
                 bad = true;
                 me.jump = -1;
             }
-            const float x = linear ? 0.f : la[tid];
-            me.zeros = x == -INFINITY;
-            me.decay = me.zeros ? 0.f : x;
+            const float x = linear ? 0.f : la[tid], gate = expf(x);
+            if (gate == 0.f) me.counts += kZero;
+            else if (!(gate < INFINITY)) me.counts += kOdd;
+            else me.decay = x;
             const uint32_t bit = 1u << (tid & 31);
             (tid < 32 ? mask.x : tid < 64 ? mask.y : tid < 96 ? mask.z : mask.w) = bit;
         }
@@ -487,14 +502,13 @@ __global__ void __launch_bounds__(256, resident<T>(MT, NT))
                 const Link to = link[me.jump];
                 const uint4 m = above[me.jump];
                 me.jump = to.jump;
-                me.steps += to.steps;
-                me.decay += to.decay;
-                me.zeros += to.zeros;
+                me.counts += to.counts;
+                add_decays(me, to);
                 mask = make_uint4(mask.x | m.x, mask.y | m.y, mask.z | m.z, mask.w | m.w);
             }
             if (!walkers_any(me.jump >= 0)) break;
         }
-        if (!linear && tid < N && t < limit && t + me.steps >= limit) bad = true;
+        if (!linear && tid < N && t < limit && t + me.steps() >= limit) bad = true;
         link[tid] = me;
         above[tid] = mask;
         walkers_meet();
@@ -504,7 +518,7 @@ __global__ void __launch_bounds__(256, resident<T>(MT, NT))
         if (i < live && par[node] != -2 && t >= 0 && t < limit) {
             const Link at = link[node];
             const uint4 line = above[node];
-            const int64_t pos = t + at.steps;
+            const int64_t pos = t + at.steps();
             const float* lam_i = lam + i * c.Lmax;
             // nodes j of j % kEach == first, four at a time, so that their links are read side by side
             constexpr unsigned long long kMine = ~0ull / ((1ull << kEach) - 1);
@@ -527,21 +541,20 @@ __global__ void __launch_bounds__(256, resident<T>(MT, NT))
                 float w[4];
 #pragma unroll
                 for (int y = 0; y < 4; y++) {
-                    const int n = at.steps - other[y].steps;
+                    const int n = at.steps() - other[y].steps();
                     if (linear) w[y] = n == 0 ? 1.f : expf(lg * static_cast<float>(n));
                     else
-                        w[y] = at.zeros > other[y].zeros ? 0.f
-                                                         : lam_i[64 - __clzll(static_cast<long long>(pos ^ (pos - n)))] *
-                                                               expf(at.decay - other[y].decay);
+                        w[y] = lam_i[64 - __clzll(static_cast<long long>(pos ^ (pos - n)))] *
+                               weight(at.counts - other[y].counts, at.decay - other[y].decay, at.rest - other[y].rest);
                 }
 #pragma unroll
                 for (int y = 0; y < 4; y++)
                     if (j[y] >= 0) {
-                        up[i * N + at.steps - other[y].steps] = static_cast<uint8_t>(j[y]);
+                        up[i * N + at.steps() - other[y].steps()] = static_cast<uint8_t>(j[y]);
                         P[i * (N + 1) + j[y]] = w[y];
                     }
             } while (j[3] >= 0);
-            const float whole = linear ? expf(lg * static_cast<float>(at.steps + 1)) : at.zeros ? 0.f : expf(at.decay);
+            const float whole = linear ? expf(lg * static_cast<float>(at.steps() + 1)) : weight(at.counts, at.decay, at.rest);
             // the blocks of the walk of t - 1 begin at t - 1 and where its set bits are cleared one by one
             if (linear) {
                 if (first == 0) far[i] = whole;
@@ -725,7 +738,7 @@ __global__ void __launch_bounds__(256, resident<T>(MT, NT))
 #pragma unroll
             for (int v = 0; v < 4; v++) o[v] = sh == 0 ? add[v] : add2(o[v], add[v]);
         }
-        const int d = link[i0 + i].steps;
+        const int d = link[i0 + i].steps();
 #pragma unroll 4
         for (int n = 0; n <= d; n++) {
             const int j = up[i * N + n];
