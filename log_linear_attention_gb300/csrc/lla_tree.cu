@@ -995,7 +995,8 @@ cudaError_t launch_commit(const CommitCall& c, cudaStream_t stream) {
     while (parts < most && heads * parts < 2000) parts *= 2;
     const int share = (items - 1) / parts + 1;
     auto go = [&](auto kern, std::atomic<uint64_t>& allowed) {
-        cudaError_t e = smem > 48 * 1024 ? allow_shared(kern, kMaxTree * 256 * 4, allowed) : cudaSuccess;
+        // always: the kernel's static memory counts to what a launch has without asking
+        cudaError_t e = allow_shared(kern, kMaxTree * 256 * 4, allowed);
         if (e != cudaSuccess) return e;
         kern<<<dim3(static_cast<unsigned>(heads), parts), kThreads, smem, stream>>>(c, share);
         note_launch(stream, "decode_commit");
