@@ -959,10 +959,12 @@ __global__ void __launch_bounds__(kThreads) decode_commit_kernel(const CommitCal
                     for (int r = 0; r < kU; r++) a[r][0] += at[r][off];
                 }
             }
+            if (from[l] != 0) {  // a slot of new tokens alone stays clear of gates that are not finite before them
 #pragma unroll
-            for (int r = 0; r < kU; r++)
+                for (int r = 0; r < kU; r++)
 #pragma unroll
-                for (int v = 0; v < kW; v++) a[r][v] *= whole;
+                    for (int v = 0; v < kW; v++) a[r][v] *= whole;
+            }
             // this slot's tokens end where the next lower held slot's begin
             const int stop = l == 0 ? n : first[l - 1];
             for (int s = first[l]; s < stop; s++) {
