@@ -422,7 +422,9 @@ int lla_decode_step_shared(const void* q, const void* k, const void* v, const fl
  *                                   gates overflows fp32 a NaN may come out). gate_dtype: LLA_F32, or dtype.
  *   state0    [B0,D]    fp32        h_{-1}: B0 = 0 (state0 NULL: zeros), 1 (one for the whole batch) or B.
  *   state_out [B,D]     fp32        written: h_{T-1} before its rounding to dtype. NULL: not wanted.
- * The recurrence is computed in fp32, sums in a fixed order: repeated calls give identical bits. Channels
+ * The recurrence is computed in fp32, sums in a fixed order: repeated calls give identical bits. Gates are
+ * expf(log_a); those of lla_gated_forward(_varlen) with 16-bit log_a are within (|log_a| + 2) 2^-24 of
+ * themselves instead (log_a's own step is 2^-8 of it), and 0 below fp32's normal numbers. Channels
  * never mix; within one, an infinity or NaN reaches every later row of its sequence (gradients: every
  * earlier one) and no row of another.
  * Nothing that is written may overlap another argument (refused: LLA_ERR_INVALID_ARG).

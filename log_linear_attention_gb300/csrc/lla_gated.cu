@@ -14,8 +14,8 @@
 // them. Blocks of a cluster are resident together, so nothing waits for a block that may not run yet, and neither flags
 // nor workspace are needed. Maps are composed in one fixed order: repeated calls give identical bits.
 //
-// Bound by HBM: 4 x 8192 x 1024, bf16 with fp32 gates, 43 us for 268 MB (92% of the copy rate), gradients 74 us for 470 MB
-// (93%); 65536 x 1024 with bf16 gates 68 us for 403 MB (88%; a step's latency, about 2 us with the exchange, shows). What
+// Bound by HBM: 4 x 8192 x 1024, bf16 with fp32 gates, 43 us for 268 MB (91% of the copy rate), gradients 76 us for 470 MB
+// (91%); 65536 x 1024 with bf16 gates 67 us for 403 MB (88%; a step's latency, about 2 us with the exchange, shows). What
 // got it there: tiles by TMA two steps ahead (69 us with per-thread asynchronous copies, which cost a quarter of all
 // instructions and pass through L1), the exchange by stores that signal a barrier (a cluster barrier waits for the step's
 // stores to global memory besides: 0.7 us a step), steps without questions asked of a row, two channels to an instruction.
@@ -71,17 +71,28 @@ __device__ __forceinline__ Quad mul(const Quad& a, const Quad& b) { return {mul2
 __device__ __forceinline__ Quad fma(const Quad& a, const Quad& b, const Quad& c) {
     return {fma2(a.lo, b.lo, c.lo), fma2(a.hi, b.hi, c.hi)};
 }
+// exp. kFine: by expf (within 2.5 x 2^-24 of the value wherever measured), as single tokens, trees and commits form their gates.
+// Else by the exponential of a rounded product with log2 e: within (|log_a| + 2) x 2^-24, and 0 for gates below fp32's normal
+// numbers. That is what a prompt's gates of 16 bits get, whose own step is 2^15 times as wide as what the product rounds away:
+// 65536 x 1024 take 67 us so, 78 by expf, whose instructions lie on the step's chain. Other passes are not bound by them:
+// prompts of 4 x 8192 x 1024 with fp32 gates take 43.0 and 43.5 us, their gradients 74.6 and 76.7, those with gates of 16
+// bits 66 and 58.
 __device__ __forceinline__ float power2(float x) {
     float r;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
     return r;
 }
-__device__ __forceinline__ Quad gate(const Quad& log_a) {  // exp
-    const f32x2 k = pair2(kLog2e, kLog2e);
+template <bool kFine>
+__device__ __forceinline__ Quad gate(const Quad& log_a) {
     float f[4];
-    split({mul2(log_a.lo, k), mul2(log_a.hi, k)}, f);
+    if constexpr (kFine) {
+        split(log_a, f);
+    } else {
+        const f32x2 k = pair2(kLog2e, kLog2e);
+        split({mul2(log_a.lo, k), mul2(log_a.hi, k)}, f);
+    }
 #pragma unroll
-    for (int v = 0; v < 4; v++) f[v] = power2(f[v]);
+    for (int v = 0; v < 4; v++) f[v] = kFine ? expf(f[v]) : power2(f[v]);
     return quad(f);
 }
 
@@ -259,7 +270,7 @@ constexpr int kBlocks = kPacked || sizeof(T) == 2 ? Cut<T, G, kBack, kPath>::kRe
 template <typename T, typename G, bool kBack, bool kPacked, int kPath, int kLanes>
 __global__ void __launch_bounds__(kThreads, (kBlocks<T, G, kBack, kPacked, kPath>)) gated_scan(const __grid_constant__ Args a) {
     using C = Cut<T, G, kBack, kPath>;
-    constexpr bool kVec = kPath != kSingles;
+    constexpr bool kVec = kPath != kSingles, kFine = kBack || sizeof(G) == 4;
     using Ch = Chan<kVec, kLanes>;
     constexpr int kCols = kLanes * 4;               // channels of a block
     constexpr int kL = C::kL, kStages = C::kStages;
@@ -482,7 +493,7 @@ __global__ void __launch_bounds__(kThreads, (kBlocks<T, G, kBack, kPacked, kPath
             for (int j = 0; j < kL; j++) {
                 float f[4];
                 gates_of(j, f);
-                g[j] = gate(quad(f));
+                g[j] = gate<kFine>(quad(f));
                 inputs_of(j, f);
                 x[j] = quad(f);
                 const Quad in = kBack ? mul(g[j], x[j]) : x[j];
@@ -517,7 +528,7 @@ __global__ void __launch_bounds__(kThreads, (kBlocks<T, G, kBack, kPacked, kPath
                     if (enter && begins) ch.load(enters(inf & kSeq), s);
                     begun |= begins;
                 }
-                g[j] = gate(quad(gf));
+                g[j] = gate<kFine>(quad(gf));
                 x[j] = quad(xf);
                 split(g[j], gf);
 #pragma unroll
