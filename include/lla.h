@@ -521,7 +521,8 @@ int lla_gated_decode_commit(const void* x, const void* log_a, float* state, cons
  * Test hook for the failure path of the bounded waits (no counterpart on the
  * pages; not for production use). On the current device, for the tensor-core
  * prefill output kernel of dv = 64, the tensor-core kernels of linear
- * attention and the passes of the gated recurrence: limit_cycles > 0 bounds each of its pipeline
+ * attention, the passes of the gated recurrence and the tree kernels whose states come by TMA (dv a
+ * multiple of 4): limit_cycles > 0 bounds each of its pipeline
  * waits to that many SM cycles (<= 0 restores the default, about 2 s at the
  * maximum clock); hold != 0 makes its epilogue (where only states are formed,
  * the warps that hold the state) first wait on a barrier that nothing arrives

@@ -267,7 +267,7 @@ struct Maps {
 // the first slot is latency: 75 us as one after the other, 62 side by side (32 nodes, the batch above).
 template <typename T, int MT, int NG, int CW, int NT, int kStageRows, int kMode>
 __global__ void __launch_bounds__(256, resident<T>(MT, NT))
-    decode_tree_kernel(const TreeCall c, const __grid_constant__ Maps maps, const int stages) {
+    decode_tree_kernel(const TreeCall c, const __grid_constant__ Maps maps, const int stages, const LinWaits waits) {
     constexpr int kWarps = 8, kThreads = kWarps * 32, kNb = 16 * MT * NG, kCols = 8 * CW * NT, KS = kWarps / (CW * NG);
     constexpr int kQ = Parts<T>::q, kS = Parts<T>::s, CU = kCols / 32;
     constexpr bool kTma = kMode >= kStates, kTmaIn = kMode == kAll;
@@ -278,7 +278,7 @@ __global__ void __launch_bounds__(256, resident<T>(MT, NT))
     __shared__ float la[kMaxTree];
     __shared__ Link link[kMaxTree];
     __shared__ uint4 above[kMaxTree];
-    __shared__ __align__(8) uint64_t full[kMaxStages], empty[kMaxStages], inputs;
+    __shared__ __align__(8) uint64_t full[kMaxStages], empty[kMaxStages], inputs, never;
     char* smem = smem_any + (-smem_u32(smem_any) & 1023u);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, cc = lane & 3;
     const int blocks = (c.N - 1) / kNb + 1;  // of nodes: those of one head run side by side, so that its states come once
@@ -321,6 +321,7 @@ __global__ void __launch_bounds__(256, resident<T>(MT, NT))
                 mbar_init(&empty[i], kWarps);
             }
             mbar_init(&inputs, 1);
+            mbar_init(&never, 1);
             fence_mbar_init();
             if constexpr (kTmaIn) {
                 const int panels = (dk + 63) / 64;
@@ -567,7 +568,7 @@ __global__ void __launch_bounds__(256, resident<T>(MT, NT))
             }
         }
     } else {
-        if (kTmaIn) in_time = mbar_try_wait(&inputs, 0) || mbar_wait(&inputs, 0);
+        if (kTmaIn) in_time = mbar_try_wait(&inputs, 0) || mbar_wait(&inputs, 0, waits.cycles);
 #pragma unroll
         for (int y = 0; y < 2; y++)
             if (scorer + 4 * y < mts * groups) score(held_scores[y], scorer + 4 * y);
@@ -579,7 +580,7 @@ __global__ void __launch_bounds__(256, resident<T>(MT, NT))
         for (int y = 0; y < 2; y++)
             if (scorer + 4 * y < mts * groups) onto_weights(held_scores[y], scorer + 4 * y);
     } else if (kTmaIn) {
-        in_time = mbar_try_wait(&inputs, 0) || mbar_wait(&inputs, 0);
+        in_time = mbar_try_wait(&inputs, 0) || mbar_wait(&inputs, 0, waits.cycles);
     }
     for (int u = 8 + warp; u < mts * groups; u += kWarps) {
         score(held_scores[0], u);
@@ -657,16 +658,17 @@ __global__ void __launch_bounds__(256, resident<T>(MT, NT))
     };
     int m = 0, piece = 0;
     if constexpr (kTma) {
+        if (waits.hold && in_time) in_time = mbar_wait(&never, 0, waits.cycles);
         int slot_ahead = stages / pieces, piece_ahead = stages % pieces, at = 0, issued = -1;
         uint32_t parity = 0;
         for (int round = 0; round < rounds; round++) {
-            if (in_time && !mbar_try_wait(&full[at], parity)) in_time = mbar_wait(&full[at], parity);
+            if (in_time && !mbar_try_wait(&full[at], parity)) in_time = mbar_wait(&full[at], parity, waits.cycles);
             consume(at, piece, [&] {
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&empty[at]);
             });
             if (warp == (round & (kWarps - 1)) && round + stages < rounds) {  // the stage's next rows, by one warp in turn
-                if (in_time && !mbar_try_wait(&empty[at], parity)) in_time = mbar_wait(&empty[at], parity);
+                if (in_time && !mbar_try_wait(&empty[at], parity)) in_time = mbar_wait(&empty[at], parity, waits.cycles);
                 in_time = __all_sync(0xffffffffu, in_time);
                 if (in_time) {
                     if (lane == 0) copy(at, slot_of[slot_ahead], piece_ahead);
@@ -810,7 +812,7 @@ cudaError_t launch_tree(const TreeCall& c, int stages, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
     if (s.total > kMostShared) return cudaErrorInvalidValue;
     const dim3 grid(static_cast<unsigned>(heads * ((c.N - 1) / kNb + 1)), (c.dv - 1) / kCols + 1);
-    kern<<<grid, 256, s.total, stream>>>(c, maps, stages);
+    kern<<<grid, 256, s.total, stream>>>(c, maps, stages, linear_waits());
     note_launch(stream, "decode_tree");
     return cudaGetLastError();
 }
