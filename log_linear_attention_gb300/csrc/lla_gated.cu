@@ -185,13 +185,14 @@ __device__ __forceinline__ bool arrived(uint64_t* bar, uint32_t parity) {
     return ok != 0;
 }
 
-// Bounded wait for a phase of a barrier; what ran out is recorded.
-__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, long long limit, int* err) {
+// Bounded wait for a phase of a barrier; what ran out is recorded, for the block in `late`.
+__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, long long limit, int* err, int* late) {
     if (arrived(bar, parity)) return true;
     const long long start = clock64();
     while (!arrived(bar, parity))
         if (clock64() - start > limit) {
             record_error(err, kDevTimeout);
+            *late = 1;
             return false;
         }
     return true;
@@ -281,7 +282,7 @@ __global__ void __launch_bounds__(kThreads, (kBlocks<T, G, kBack, kPacked, kPath
     __shared__ __align__(16) float2 part[2][kMaxCluster][kCols];
     __shared__ __align__(16) float carry[2][kCols];
     __shared__ int info[2][kPacked ? kRows : 1];
-    __shared__ int bounds[4], plain_of[2], near[2], window[2][kPacked ? kWindow : 1];
+    __shared__ int late, bounds[4], plain_of[2], near[2], window[2][kPacked ? kWindow : 1];
     __shared__ __align__(8) uint64_t come[2], full[kStages], never;
     extern __shared__ __align__(128) char staged[];
     const GatedPass& p = a.p;
@@ -330,6 +331,7 @@ __global__ void __launch_bounds__(kThreads, (kBlocks<T, G, kBack, kPacked, kPath
         mbar_init(&come[0], 1);
         mbar_init(&come[1], 1);
         mbar_init(&never, 1);
+        late = 0;
         for (int i = 0; i < kStages; i++) mbar_init(&full[i], 1);
         fence_mbar_init();
     }
@@ -421,7 +423,7 @@ __global__ void __launch_bounds__(kThreads, (kBlocks<T, G, kBack, kPacked, kPath
     }
 
     // After a wait that ran out a walk goes on to its end without waiting, sending or copying, its values undefined.
-    bool in_time = !a.waits.hold || wait(&never, 0, a.waits.cycles, a.err);
+    bool in_time = !a.waits.hold || wait(&never, 0, a.waits.cycles, a.err, &late);
     for (int st = 0; st < steps; st++) {
         const int buf = st & 1;
         const int block0 = (st * cs + rank) * kRows, u0 = block0 + seg * kL;
@@ -479,7 +481,7 @@ __global__ void __launch_bounds__(kThreads, (kBlocks<T, G, kBack, kPacked, kPath
         Quad g[kL], x[kL];
         Ahead<T, kVec> hp[kBack ? kL : 1];
         float A[4], s[4];
-        if (kPath == kTma && in_time) in_time = wait(&full[st % kStages], (st / kStages) & 1, a.waits.cycles, a.err);
+        if (kPath == kTma && in_time) in_time = wait(&full[st % kStages], (st / kStages) & 1, a.waits.cycles, a.err, &late);
         if (kBack) {
 #pragma unroll
             for (int j = 0; j < kL; j++) {
@@ -586,7 +588,7 @@ __global__ void __launch_bounds__(kThreads, (kBlocks<T, G, kBack, kPacked, kPath
                     if (tid == 0) mbar_expect_tx(&come[buf], static_cast<uint32_t>(cs) * kCols * sizeof(float2));
                     const uint32_t to = smem_u32(&part[buf][rank][tid]), sign = smem_u32(&come[buf]);
                     for (int r = 0; r < cs; r++) send(to, sign, r, own_a, own_s);
-                    in_time = wait(&come[buf], (st >> 1) & 1, a.waits.cycles, a.err);
+                    in_time = wait(&come[buf], (st >> 1) & 1, a.waits.cycles, a.err, &late);
                 }
                 for (int r = 0; r < cs; r++) {
                     if (r == rank) carry[buf][tid] = state;
@@ -687,8 +689,13 @@ __global__ void __launch_bounds__(kThreads, (kBlocks<T, G, kBack, kPacked, kPath
     // no block leaves while its own copies are under way, or while another may still write to it
     if (kPath == kTma && tid == 0)
         for (int st = issued < kStages ? 0 : issued - kStages; st < issued; st++)
-            wait(&full[st % kStages], (st / kStages) & 1, kWaitCycles, a.err);
-    if (cs > 1) cluster_meet<false>();
+            wait(&full[st % kStages], (st / kStages) & 1, kWaitCycles, a.err, &late);
+    if (cs > 1) {
+        cluster_meet<false>();
+        // The block's own waits took in all that others sent it. One that ran out did not: a block that came late may have sent
+        // its maps just before it got here, so stay for another bound (those stores take microseconds).
+        if (late) wait(&never, 0, a.waits.cycles, a.err, &late);
+    }
 }
 
 // The gradient of a state that n sequences share: their parts summed in order. Launched while the scan ends (its results are
