@@ -728,7 +728,7 @@ def _gated_state(t_, name, n, D, device):
     """(rows, address) of an entering state [n,D] or [1,D], or (0, NULL)."""
     if t_ is None:
         return 0, None
-    one = t_.dim() == 2 and t_.shape[0] == 1
+    one = isinstance(t_, _torch_module.Tensor) and t_.dim() == 2 and t_.shape[0] == 1
     return (1 if one else n), _state(t_, name, (1 if one else n, D), device)
 
 
@@ -848,6 +848,8 @@ def _accepted(count, path, B, index, device):
         _want(count, "count", torch.int32, (B,), device)
     if path is None:
         return 0
+    if not isinstance(path, torch.Tensor):
+        _check(path, "path")
     if path.dim() != 2 or path.shape[0] != B or path.shape[1] < 1:
         raise ValueError(f"path must be int32 [{B},M], got {list(path.shape)}")
     if not _fits(path, torch.int32, path.shape, index):
