@@ -423,8 +423,8 @@ int lla_decode_step_shared(const void* q, const void* k, const void* v, const fl
  *   state0    [B0,D]    fp32        h_{-1}: B0 = 0 (state0 NULL: zeros), 1 (one for the whole batch) or B.
  *   state_out [B,D]     fp32        written: h_{T-1} before its rounding to dtype. NULL: not wanted.
  * The recurrence is computed in fp32, sums in a fixed order: repeated calls give identical bits. Gates are
- * expf(log_a); those of lla_gated_forward(_varlen) with 16-bit log_a are within (|log_a| + 2) 2^-24 of
- * themselves instead (log_a's own step is 2^-8 of it), and 0 below fp32's normal numbers. Channels
+ * expf(log_a); those of lla_gated_forward(_varlen) with 16-bit log_a may be off by (1.3 |log_a| + 4) 2^-24 of
+ * themselves (log_a's own step is 2^-8 of it), and are 0 below fp32's normal numbers. Channels
  * never mix; within one, an infinity or NaN reaches every later row of its sequence (gradients: every
  * earlier one) and no row of another.
  * Nothing that is written may overlap another argument (refused: LLA_ERR_INVALID_ARG).
@@ -495,7 +495,8 @@ int lla_gated_decode_step(const void* x, const void* log_a, float* state, void* 
  *   dk, dv 1..128; Lmax 1..40. Products with the states run on tensor cores: bf16 queries as they are, states
  *   in two bf16 parts (2^-16 of each element), fp32 calls in three parts of both; sums in fp32 in a fixed order
  *   (repeated calls give identical bits; a call of fewer heads may cut its sums otherwise). An infinity in the
- *   states may come out as NaN; one in a node reaches only that node's and its descendants' outputs.
+ *   states, or a gate that is infinite in fp32, may come out as NaN; one in a node reaches only that node's and its
+ *   descendants' outputs.
  * lla_gated_decode_tree, lla_gated_decode_commit: the same for lla_gated_decode_step; x, log_a, out [B,N,D],
  *   state [B,D] fp32; B up to 65535. (h of a node: exp(log_a_i) h_parent(i) + x_i.)
  *

@@ -72,11 +72,11 @@ __device__ __forceinline__ Quad fma(const Quad& a, const Quad& b, const Quad& c)
     return {fma2(a.lo, b.lo, c.lo), fma2(a.hi, b.hi, c.hi)};
 }
 // exp. kFine: by expf (within 2.5 x 2^-24 of the value wherever measured), as single tokens, trees and commits form their gates.
-// Else by the exponential of a rounded product with log2 e: within (|log_a| + 2) x 2^-24, and 0 for gates below fp32's normal
-// numbers. That is what a prompt's gates of 16 bits get, whose own step is 2^15 times as wide as what the product rounds away:
-// 65536 x 1024 take 67 us so, 78 by expf, whose instructions lie on the step's chain. Other passes are not bound by them:
-// prompts of 4 x 8192 x 1024 with fp32 gates take 43.0 and 43.5 us, their gradients 74.6 and 76.7, those with gates of 16
-// bits 66 and 58.
+// Else by the power of two of a rounded product with log2 e: within (|log_a| + 2) x 2^-24 wherever measured, and 0 for gates
+// below fp32's normal numbers. That is what a prompt's gates of 16 bits get, whose own step is 2^15 times as wide as what the product rounds away:
+// 65536 x 1024 take 67 us so, 78 by expf, whose instructions lie on the step's chain. Other passes feel them less: prompts of
+// 4 x 8192 x 1024 with fp32 gates take 43.0 and 43.4 us, their gradients 74.6 and 76, those in fp32 108 and 114, those with
+// gates of 16 bits 66 and 58.
 __device__ __forceinline__ float power2(float x) {
     float r;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
@@ -263,8 +263,8 @@ struct Ahead<T, false> {
 };
 
 // Registers: where shared memory holds one block of an SM, its threads have all of them (fp32 gradients of 16 packed documents of
-// 100 to 4000 rows of 512 channels: 54 us, with registers for two blocks 83), but for dense fp32, where the loads that the
-// compiler then moves together cost more than they save (gradients of 4 x 8192 x 1024: 107 us for two blocks, 117).
+// 100 to 4000 rows of 512 channels: 55 us, with registers for two blocks 78), but for dense fp32, where the loads that the
+// compiler then moves together cost more than they save (gradients of 4 x 8192 x 1024: 114 us for two blocks, 118).
 template <typename T, typename G, bool kBack, bool kPacked, int kPath>
 constexpr int kBlocks = kPacked || sizeof(T) == 2 ? Cut<T, G, kBack, kPath>::kResident : 2;
 
@@ -739,9 +739,9 @@ cudaError_t launch_scan(Args& a, cudaStream_t stream) {
     const int pieces = (a.p.T - 1) / kRows + 1;
     a.spans = kPacked ? 1 : a.p.n;
     // The smallest cluster that gives every SM a block: an exchange costs about as much as a step of 1 us (4 x 8192 x 1024:
-    // clusters of 1, 2, 4, 8 take 60, 44, 43, 48 us; one sequence of 65536 x 1024 in 32 columns 258, 164, 86, 68).
+    // clusters of 1, 2, 4, 8 take 70, 46, 44, 49 us; one sequence of 65536 x 1024 in 32 columns 258, 164, 86, 67).
     // Packed sequences are cut into spans besides, for what a few waves' blocks leave to chance when lengths differ: 32
-    // sequences of 256 to 8192 rows of 1024 channels take 176 us as 2 spans of clusters of 4, 183 as one of 8, 186 as
+    // sequences of 256 to 8192 rows of 1024 channels take 152 us as 2 spans of clusters of 4, 168 as one of 8, 183 as
     // 8 spans of single blocks.
     a.cluster = 1;
     const int most = kPacked && a.p.n > 1 ? 4 : kMaxCluster;
@@ -788,9 +788,9 @@ cudaError_t run_t(Args& a, bool back, cudaStream_t stream) {
     const bool tma = static_cast<int64_t>(a.p.D) * sizeof(T) % 16 == 0 && static_cast<int64_t>(a.p.D) * sizeof(G) % 16 == 0 &&
                      static_cast<int64_t>(a.p.T) * (a.p.cu ? 1 : a.p.n) < (int64_t(1) << 31);
     // Columns of 64 channels, whose rows are the longest stretches of memory, where clusters of up to four of them fill the
-    // GPU; else of 32, with longer steps of fewer channels (one sequence of 65536 x 1024: 68 us against 111), and of 16
-    // where even those leave more than half of it idle (65536 x 64: 36 us against 55; but 74 against 94 the other way for
-    // gradients of 65536 x 256). Packed: 32 (the mix above: 176 us against 203 with 64).
+    // GPU; else of 32, with longer steps of fewer channels (one sequence of 65536 x 1024: 67 us against 110), and of 16
+    // where even those leave more than half of it idle (65536 x 64: 30 us against 47; but 73 against 90 the other way for
+    // gradients of 65536 x 256). Packed: 32 (the sequences of 256 to 8192 rows: 152 us against 206 with 64).
     const int64_t walks = a.p.cu ? 1 : a.p.n, wide = ((a.p.D - 1) / 64 + 1) * walks, half = ((a.p.D - 1) / 32 + 1) * walks;
     const int lanes = a.p.cu ? 8 : wide * 4 >= kFill ? 16 : half * 8 >= 64 ? 8 : 4;
     auto go = [&](auto kback, auto kpacked) {

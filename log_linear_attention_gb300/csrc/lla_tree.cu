@@ -20,11 +20,12 @@
 // columns of its MMA operands without bank conflicts and cuts them itself.
 //
 // Measured (calls in a CUDA graph, inputs larger than L2): 64 sequences x 16 heads of 128 x 64 at t up to 65536, 32 nodes,
-// bf16: 62 us for 328 MB (78% of the copy rate); 16 nodes 58 us (81%), 64 nodes 100 us, fp32 with 32 nodes 129 us. One state
+// bf16: 63 us for 328 MB (77% of the copy rate); 16 nodes 59 us (80%), 64 nodes 100 us, fp32 with 32 nodes 130 us. One state
 // a head (linear) and 64 nodes: 33 us for 84 MB. What a block does before and after its states bounds it: of 26 thousand
-// cycles (two blocks on an SM) the first slot is taken at 8.4, a slot of 32 KB every 1.7, the rest is 1.9; fp32 is bound
-// by the six products. Steps: the lanes' own loads of states 85 us, row by row with untiled bulk copies 226 (their issue),
-// the ring of boxes 75, walkers beside scorers 62.
+// cycles (two blocks on an SM) the first slot is taken at 8.4, a slot of 32 KB every 1.7, the rest is 1.9. fp32 fills no pipe
+// either (tensor 38%, issue slots 42%, shared memory 29%): six products and two groups of warps that cut the same states stand
+// in a chain that 16 warps of an SM do not hide. Steps: the lanes' own loads of states 85 us, row by row with untiled bulk
+// copies 226 (their issue), the ring of boxes 75, walkers beside scorers 62.
 #include "lla_drafts.cuh"
 #include "lla_linear_tc.cuh"
 
@@ -857,8 +858,8 @@ __device__ __forceinline__ int slot_in_walk(int64_t e, int64_t s) { return 64 - 
 // Every held slot of the last accepted position e = t + n - 1 from the old slots and the new tokens inside it. Each old
 // slot lies inside one new slot of its own number or above, so a thread, which takes its elements through all slots, goes
 // from the highest slot down and never reads what it has written. Elements are independent: grid (heads of all sequences,
-// shares of a state's elements). Bound by HBM: 64 x 16 heads of 128 x 64 with 6 tokens at most, 95 us for 531 MB read and
-// written (83% of the copy rate), four elements of a thread at a time (two 107 us, eight 151).
+// shares of a state's elements). Bound by HBM: 64 x 16 heads of 128 x 64 with 6 tokens at most, 96 us for 531 MB read and
+// written (82% of the copy rate), four elements of a thread at a time (two 107 us, eight 151).
 template <typename T, int kW, int kU>  // kW columns of a thread, kU of its elements at a time
 __global__ void __launch_bounds__(kThreads) decode_commit_kernel(const CommitCall c, int share) {
     extern __shared__ float tok[];  // [n][dk] weighted keys, [n][dv] values
