@@ -73,10 +73,10 @@ __device__ __forceinline__ Quad fma(const Quad& a, const Quad& b, const Quad& c)
 }
 // exp. kFine: by expf (within 2.5 x 2^-24 of the value wherever measured), as single tokens, trees and commits form their gates.
 // Else by the power of two of a rounded product with log2 e: within (|log_a| + 2) x 2^-24 wherever measured, and 0 for gates
-// below fp32's normal numbers. That is what a prompt's gates of 16 bits get, whose own step is 2^15 times as wide as what the product rounds away:
-// 65536 x 1024 take 67 us so, 78 by expf, whose instructions lie on the step's chain. Other passes feel them less: prompts of
-// 4 x 8192 x 1024 with fp32 gates take 43.0 and 43.4 us, their gradients 74.6 and 76, those in fp32 108 and 114, those with
-// gates of 16 bits 66 and 58.
+// below fp32's normal numbers. That is what a prompt's gates of 16 bits get, whose own step is 2^15 times as wide as what the
+// product rounds away: 65536 x 1024 take 67 us so, 78 by expf, whose instructions lie on the step's chain. Other passes feel
+// them less: prompts of 4 x 8192 x 1024 with fp32 gates take 43.0 and 43.4 us, their gradients 74.6 and 76, those in fp32 108
+// and 114, those with gates of 16 bits 66 and 58.
 __device__ __forceinline__ float power2(float x) {
     float r;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
@@ -693,8 +693,8 @@ __global__ void __launch_bounds__(kThreads, (kBlocks<T, G, kBack, kPacked, kPath
     if (cs > 1) {
         cluster_meet<false>();
         // The block's own waits took in all that others sent it. One that ran out did not: a block that came late may have sent
-        // its maps just before it got here, so stay for another bound (those stores take microseconds).
-        if (late) wait(&never, 0, a.waits.cycles, a.err, &late);
+        // its maps just before it got here, so stay for half a millisecond, whatever the bound is (those stores take microseconds).
+        if (late) wait(&never, 0, 1 << 20, a.err, &late);
     }
 }
 

@@ -76,13 +76,13 @@ def close(got, w, D, dtype, what, steps=0):
 
 GATES = {  # what some gates of a draft are, the others lie between 0 and -2
     "strong": [-30.0], "underflow": [-90.0, -103.0, -105.0], "1e4": [-1e4], "1e9": [-1e9], "lowest": [-3.4e38],
-    "-inf": [-np.inf], "review": None, "many": [-20.0, -33.0, -60.0],
+    "-inf": [-np.inf], "order": None, "many": [-20.0, -33.0, -60.0],
     "all": [-30.0, -200.0, -1e4, -1e6, -1e9, -3.4e38, -np.inf],
 }
 
 
 def gates(r, name, N):
-    if name == "review":
+    if name == "order":
         la = np.array([-1e9, -33, -0.5, -33, -0.5, -0.5, -20, -0.1] * (N // 8 + 1))[:N]
     else:
         la = -2 * r.random(N)
